@@ -27,7 +27,11 @@ EXPORTS = ("conv_plan_create", "conv_plan_output_shape", "conv_plan_info", "conv
            "conv_plan_launch_info", "conv_forward_affine", "conv_block_plan_create",
            "conv_block_plan_output_shape", "conv_block_forward", "conv_block_plan_launch_info",
            "conv_block_plan_destroy", "conv_measure_mma_rate", "conv_check_wait_timeout",
-           "conv_plan_gemm_config", "conv_plan_device_status", "conv_block_plan_device_status")
+           "conv_plan_gemm_config", "conv_plan_device_status", "conv_block_plan_device_status",
+           "conv_group_norm_plan_create", "conv_group_norm_workspace", "conv_group_norm_forward",
+           "conv_group_norm_forward_int8", "conv_group_norm_backward", "conv_group_norm_plan_destroy",
+           "conv_int8_plan_create", "conv_int8_forward", "conv_int8_workspace", "conv_int8_forward_quantize",
+           "conv_int8_plan_device_status", "conv_int8_plan_destroy", "conv_quantize_rows")
 CONV_BLOCK_DW_RELU, CONV_BLOCK_PW_RELU = 1, 2
 
 _lock = threading.Lock()
@@ -98,6 +102,23 @@ def lib():
             L.conv_measure_mma_rate.restype = c_int
             L.conv_check_wait_timeout.argtypes = [ctypes.c_ulonglong, vp, vp]
             L.conv_check_wait_timeout.restype = c_int
+            c_ull = ctypes.c_ulonglong
+            L.conv_group_norm_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 5 + [ctypes.c_float, c_int, c_int]
+            L.conv_group_norm_workspace.argtypes = [vp, ctypes.POINTER(c_ull)]
+            L.conv_group_norm_forward.argtypes = [vp] * 8
+            L.conv_group_norm_forward_int8.argtypes = [vp] * 9
+            L.conv_group_norm_backward.argtypes = [vp] * 11
+            L.conv_group_norm_plan_destroy.argtypes = [vp]
+            L.conv_int8_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 5
+            L.conv_int8_forward.argtypes = [vp] * 8
+            L.conv_int8_workspace.argtypes = [vp, ctypes.POINTER(c_ull)]
+            L.conv_int8_forward_quantize.argtypes = [vp, vp, c_int] + [vp] * 6
+            L.conv_int8_plan_device_status.argtypes = [vp, vp, ctypes.POINTER(c_int)]
+            L.conv_int8_plan_destroy.argtypes = [vp]
+            L.conv_quantize_rows.argtypes = [vp, c_int, c_int, c_int, vp, vp, vp]
+            for name in EXPORTS:
+                if name.startswith(("conv_group_norm", "conv_int8", "conv_quantize")):
+                    getattr(L, name).restype = c_int
             _lib = L
         return _lib
 

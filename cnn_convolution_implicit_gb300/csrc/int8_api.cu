@@ -1,0 +1,163 @@
+// int8_api.cu -- C ABI of the 8-bit product and of the row quantiser
+// (conv_int8_*, conv_quantize_rows in include/conv.h): checks, launch
+// configuration and the calls.
+#include <new>
+
+#include "../../include/conv.h"
+#include "int8_internal.h"
+#include "status_slots.h"
+
+using namespace convgb;
+
+struct conv_int8_plan {
+    Int8Params ip;
+    int device;
+    int num_sms;
+    int status_slot;  // index of the plan's own status word, -1: the library-wide word
+};
+
+namespace {
+
+constexpr int kMaxK = 131071;  // 128 * 128 * K stays below 2^31
+
+bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+
+conv_status check_device(const conv_int8_plan* pl) {
+    if (pl->device < 0) return CONV_ERR_CUDA;  // host-only plan
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess) {
+        cudaGetLastError();
+        return CONV_ERR_CUDA;
+    }
+    return cur == pl->device ? CONV_OK : CONV_ERR_INVALID_ARG;
+}
+
+// The 8-bit rows of a call that quantises: [M][K] integers, rounded up to 16 bytes, then [M] scales.
+size_t rows_bytes(const Int8Params& p) { return (static_cast<size_t>(p.M) * p.K + 15) & ~static_cast<size_t>(15); }
+
+conv_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return CONV_OK;
+    cudaGetLastError();
+    return CONV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+conv_status conv_int8_plan_create(conv_int8_plan** out, int M, int N, int K, conv_dtype out_dtype, conv_act act) {
+    if (out == nullptr) return CONV_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (M <= 0 || N <= 0 || K <= 0) return CONV_ERR_INVALID_ARG;
+    if (out_dtype != CONV_F32 && out_dtype != CONV_BF16) return CONV_ERR_INVALID_ARG;
+    if (act != CONV_ACT_NONE && act != CONV_ACT_RELU && act != CONV_ACT_SILU) return CONV_ERR_INVALID_ARG;
+    const long long most = 1LL << 40;
+    if (K > kMaxK || static_cast<long long>(M) * K > most || static_cast<long long>(N) * K > most ||
+        static_cast<long long>(M) * N > most)
+        return CONV_ERR_UNSUPPORTED;
+    conv_int8_plan* pl = new (std::nothrow) conv_int8_plan();
+    if (pl == nullptr) return CONV_ERR_NO_MEMORY;
+    Int8Params& p = pl->ip;
+    p = Int8Params();
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out_bf16 = out_dtype == CONV_BF16;
+    p.act = act;
+    pl->status_slot = -1;
+    int ndev = 0;
+    if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
+        cudaGetLastError();
+        pl->device = -1;
+        pl->num_sms = 152;
+    } else if (cudaGetDevice(&pl->device) != cudaSuccess ||
+               cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess ||
+               acquire_status_word(pl->device, &p.status, &pl->status_slot) != cudaSuccess) {
+        cudaGetLastError();
+        delete pl;
+        return CONV_ERR_CUDA;
+    }
+    *out = pl;
+    return CONV_OK;
+}
+
+conv_status conv_int8_forward(conv_int8_plan* pl, const void* x, const float* x_scale, const void* w,
+                              const float* w_scale, const float* bias, void* y, void* stream) {
+    if (pl == nullptr || x == nullptr || x_scale == nullptr || w == nullptr || w_scale == nullptr || y == nullptr)
+        return CONV_ERR_INVALID_ARG;
+    for (const void* ptr : {x, static_cast<const void*>(x_scale), w, static_cast<const void*>(w_scale),
+                            static_cast<const void*>(bias), static_cast<const void*>(y)})
+        if (ptr != nullptr && !aligned16(ptr)) return CONV_ERR_MISALIGNED;
+    const conv_status s = check_device(pl);
+    if (s != CONV_OK) return s;
+    Int8Params p = pl->ip;
+    p.x = static_cast<const int8_t*>(x);
+    p.x_scale = x_scale;
+    p.w = static_cast<const int8_t*>(w);
+    p.w_scale = w_scale;
+    p.bias = bias;
+    p.y = y;
+    return launched(launch_int8_product(p, pl->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+conv_status conv_int8_workspace(const conv_int8_plan* p, unsigned long long* bytes) {
+    if (p == nullptr || bytes == nullptr) return CONV_ERR_INVALID_ARG;
+    *bytes = rows_bytes(p->ip) + static_cast<size_t>(p->ip.M) * sizeof(float);
+    return CONV_OK;
+}
+
+conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_dtype x_dtype, const void* w,
+                                       const float* w_scale, const float* bias, void* y, void* workspace,
+                                       void* stream) {
+    if (pl == nullptr || x == nullptr || w == nullptr || w_scale == nullptr || y == nullptr || workspace == nullptr)
+        return CONV_ERR_INVALID_ARG;
+    if (x_dtype != CONV_F32 && x_dtype != CONV_BF16) return CONV_ERR_INVALID_ARG;
+    for (const void* ptr : {x, w, static_cast<const void*>(w_scale), static_cast<const void*>(bias),
+                            static_cast<const void*>(y), static_cast<const void*>(workspace)})
+        if (ptr != nullptr && !aligned16(ptr)) return CONV_ERR_MISALIGNED;
+    const conv_status s = check_device(pl);
+    if (s != CONV_OK) return s;
+    Int8Params p = pl->ip;
+    int8_t* q = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(q + rows_bytes(p));
+    p.x = q;
+    p.x_scale = scale;
+    p.w = static_cast<const int8_t*>(w);
+    p.w_scale = w_scale;
+    p.bias = bias;
+    p.y = y;
+    const cudaError_t e = launch_quantize_rows(x, x_dtype == CONV_BF16, p.M, p.K, q, scale, pl->num_sms,
+                                               static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return launched(e);
+    return launched(launch_int8_product(p, pl->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+conv_status conv_int8_plan_device_status(const conv_int8_plan* p, void* stream, int* code) {
+    if (p == nullptr || code == nullptr) return CONV_ERR_INVALID_ARG;
+    *code = 0;
+    if (p->device < 0) return CONV_ERR_CUDA;  // host-only plan
+    return read_status_word(p->device, p->ip.status, stream, code);
+}
+
+conv_status conv_int8_plan_destroy(conv_int8_plan* p) {
+    if (p != nullptr) release_status_word(p->device, p->status_slot);
+    delete p;
+    return CONV_OK;
+}
+
+conv_status conv_quantize_rows(const void* x, conv_dtype dtype, int M, int K, void* q, float* scale, void* stream) {
+    if (x == nullptr || q == nullptr || scale == nullptr || M <= 0 || K <= 0) return CONV_ERR_INVALID_ARG;
+    if (dtype != CONV_F32 && dtype != CONV_BF16) return CONV_ERR_INVALID_ARG;
+    if (static_cast<long long>(M) * K > (1LL << 40)) return CONV_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return CONV_ERR_MISALIGNED;
+    int dev = -1, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return CONV_ERR_CUDA;
+    }
+    return launched(launch_quantize_rows(x, dtype == CONV_BF16, M, K, static_cast<int8_t*>(q), scale, sms,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

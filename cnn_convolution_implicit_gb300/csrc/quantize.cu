@@ -1,0 +1,71 @@
+// quantize.cu -- rows of FP32 or BF16 values to 8-bit integers with one scale
+// per row: scale = amax / 127, q = rint(x * (127 / amax)).
+//
+// One warp per row, two sweeps (the row's largest magnitude, then the values); the
+// second finds a row of ordinary length in L1.  Bound by the bytes of x read and q
+// written.
+#include "int8_internal.h"
+#include "pointwise_math.cuh"
+
+namespace convgb {
+
+namespace {
+
+constexpr int kQuantThreads = 256;
+
+// VEC = 16 bytes of T (rows that all start on 16 bytes) or 1.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* x, int M, int K, int8_t* q,
+                                                                      float* scale) {
+    const int lane = threadIdx.x & 31;
+    const int vecs = K / VEC;
+    using Io = VecIo<T, VEC>;
+    for (long long row = static_cast<long long>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); row < M;
+         row += static_cast<long long>(gridDim.x) * (kQuantThreads / 32)) {
+        const auto* src = reinterpret_cast<const typename Io::Raw*>(x) + row * vecs;
+        uint32_t amax = 0;
+        for (int v = lane; v < vecs; v += 32) {
+            float f[VEC];
+            Io::unpack(src[v], f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) amax = max(amax, magnitude_bits(f[i]));
+        }
+        const RowScale rs = row_scale(warp_max(amax));
+        if (lane == 0) scale[row] = rs.scale;
+        int8_t* dst = q + row * K;
+        for (int v = lane; v < vecs; v += 32) {
+            float f[VEC];
+            Io::unpack(src[v], f);
+            int o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = quantise(f[i], rs.inv);
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint2*>(dst + v * 8) =
+                    make_uint2(pack_int8x4(o[0], o[1], o[2], o[3]), pack_int8x4(o[4], o[5], o[6], o[7]));
+            else if constexpr (VEC == 4)
+                *reinterpret_cast<uint32_t*>(dst + v * 4) = pack_int8x4(o[0], o[1], o[2], o[3]);
+            else
+                dst[v] = static_cast<int8_t>(o[0]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, bool bf16, int M, int K, int8_t* q, float* scale, int num_sms,
+                                 cudaStream_t stream) {
+    const long long need = (static_cast<long long>(M) + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+    const unsigned grid = static_cast<unsigned>(need < 8LL * num_sms ? need : 8LL * num_sms);
+    if (bf16) {
+        const auto* b = static_cast<const __nv_bfloat16*>(x);
+        if (K % 8 == 0) quantize_rows_kernel<__nv_bfloat16, 8><<<grid, kQuantThreads, 0, stream>>>(b, M, K, q, scale);
+        else quantize_rows_kernel<__nv_bfloat16, 1><<<grid, kQuantThreads, 0, stream>>>(b, M, K, q, scale);
+    } else {
+        const auto* f = static_cast<const float*>(x);
+        if (K % 4 == 0) quantize_rows_kernel<float, 4><<<grid, kQuantThreads, 0, stream>>>(f, M, K, q, scale);
+        else quantize_rows_kernel<float, 1><<<grid, kQuantThreads, 0, stream>>>(f, M, K, q, scale);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace convgb

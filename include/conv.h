@@ -353,6 +353,152 @@ conv_status conv_block_plan_device_status(const conv_block_plan *p, void *stream
 /* Free the block plan: the same contract as conv_plan_destroy.  NULL is accepted. */
 conv_status conv_block_plan_destroy(conv_block_plan *p);
 
+/* Activations of the operators below. */
+typedef enum {
+    CONV_ACT_NONE = 0,
+    CONV_ACT_RELU = 1,   /* max(z, 0)                                                 */
+    CONV_ACT_SILU = 2    /* z / (1 + exp(-z))                                         */
+} conv_act;
+
+/* ------------------------------------------------------------------------
+ * Group norm with an activation over an NHWC feature map, forward and backward.
+ *
+ *   S = (image n, group g): the P = H * W pixels of C / groups neighbouring channels
+ *   mean = sum_S x / |S|,  rstd = 1 / sqrt(sum_S (x - mean)^2 / |S| + eps)
+ *   y[n][h][w][c] = act( (x - mean) * rstd * gamma[c] + beta[c] )
+ *
+ * groups = 1 normalises an image as a whole, groups = C each channel of it.
+ * Sums, statistics and the arithmetic are FP32; the result is rounded once.  A
+ * NaN or Inf in a group makes that group NaN and no other.
+ *
+ * Layouts (dense, caller-owned device memory, 16-byte aligned):
+ *   x, y, dy, dx   [N][H][W][C]   FP32 (CONV_F32) or BF16 (CONV_BF16)
+ *   gamma, beta    [C]            FP32, each may be NULL (1 and 0)
+ *   stats          [2][N][groups] FP32: the means, then the rstds
+ *   dgamma, dbeta  [C]            FP32
+ *   q              [N][H][W][C]   8-bit integers
+ *   q_scale        [N][H][W]      FP32
+ *   workspace      conv_group_norm_workspace bytes, contents of no account before
+ *                  and after a call; calls that may run at the same time take one each
+ * ------------------------------------------------------------------------ */
+typedef struct conv_group_norm_plan conv_group_norm_plan; /* opaque, host-owned */
+
+/*
+ * Check the shape and choose the kernels.  *plan gets a new plan, or NULL on
+ * error.  Returns CONV_ERR_INVALID_ARG for non-positive sizes, C % groups != 0, an
+ * eps that is negative or not finite, or an unknown dtype or act; CONV_ERR_UNSUPPORTED
+ * above 2^30 pixels an image, 2^40 elements or 2^24 (image, group) pairs;
+ * CONV_ERR_CUDA if the device cannot be queried.  Tied to the device current at
+ * creation; without a device a host-only plan is made (shape checks only), whose calls
+ * return CONV_ERR_CUDA.
+ */
+conv_status conv_group_norm_plan_create(conv_group_norm_plan **plan, int N, int C, int H, int W, int groups,
+                                        float eps, conv_dtype dtype, conv_act act);
+
+/* Bytes of device workspace that each call of this plan takes. */
+conv_status conv_group_norm_workspace(const conv_group_norm_plan *p, unsigned long long *bytes);
+
+/*
+ * y = act(norm(x)).  stats (may be NULL) receives what the backward pass reads.
+ * y must not overlap the inputs.  Asynchronous on `stream`; CONV_ERR_INVALID_ARG
+ * for a NULL plan, x, y or workspace or another current device, CONV_ERR_MISALIGNED
+ * for a pointer that is not 16-byte aligned, CONV_ERR_CUDA if a launch fails.
+ */
+conv_status conv_group_norm_forward(conv_group_norm_plan *p, const void *x, const float *gamma, const float *beta,
+                                    void *y, float *stats, void *workspace, void *stream);
+
+/*
+ * The forward pass with its result in 8 bits, one scale for each pixel (all C
+ * channels): q = rint(y * (127 / amax)), q_scale = amax / 127 with amax the pixel's
+ * largest |y|, taken from the FP32 values.  The rules of conv_quantize_rows.
+ */
+conv_status conv_group_norm_forward_int8(conv_group_norm_plan *p, const void *x, const float *gamma,
+                                         const float *beta, void *q, float *q_scale, float *stats,
+                                         void *workspace, void *stream);
+
+/*
+ * Gradients, from the forward pass's input and stats: with u = dy * act'(z) and
+ * h = (x - mean) * rstd,
+ *   dbeta[c] = sum u, dgamma[c] = sum u * h   (over n, h, w)
+ *   dx = rstd * (u * gamma - mean_S(u * gamma) - h * mean_S(u * gamma * h)).
+ * The derivative of ReLU at 0 is 0.  dgamma and dbeta are written, not added to, and
+ * both or neither may be NULL.  Every sum has one fixed order: the same inputs give
+ * the same bits.
+ */
+conv_status conv_group_norm_backward(conv_group_norm_plan *p, const void *dy, const void *x, const float *stats,
+                                     const float *gamma, const float *beta, void *dx, float *dgamma, float *dbeta,
+                                     void *workspace, void *stream);
+
+/* Free the plan.  NULL is accepted. */
+conv_status conv_group_norm_plan_destroy(conv_group_norm_plan *p);
+
+/* ------------------------------------------------------------------------
+ * 8-bit integer product with scales: a linear layer, or the pointwise (1x1)
+ * convolution, of rows (tokens, pixels) and weights held in 8 bits.
+ *
+ *   y[m][n] = act( x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k] + bias[n] )
+ *
+ * Layouts (dense, row-major, caller-owned device memory, 16-byte aligned bases; a
+ * row may start anywhere, K and N may be odd):
+ *   x        [M][K]  8-bit integers (-128 .. 127)
+ *   x_scale  [M]     FP32
+ *   w        [N][K]  8-bit integers
+ *   w_scale  [N]     FP32
+ *   bias     [N]     FP32, may be NULL (0)
+ *   y        [M][N]  BF16 or FP32
+ * The sum is exact while it stays within 2^24 in magnitude (always for K <= 1024);
+ * beyond that it carries FP32 rounding.  Scales, bias and activation are FP32, the
+ * result is rounded once.  A row or channel whose scale is NaN or Inf gives NaN or Inf
+ * in its own outputs only.
+ * ------------------------------------------------------------------------ */
+typedef struct conv_int8_plan conv_int8_plan; /* opaque, host-owned */
+
+/*
+ * Check the shape and choose the kernel.  *plan gets a new plan, or NULL on error.
+ * Returns CONV_ERR_INVALID_ARG for non-positive sizes or an unknown dtype or act,
+ * CONV_ERR_UNSUPPORTED for K > 131071 (the sum would pass 32 bits) or above 2^40
+ * elements of x, w or y, CONV_ERR_CUDA if the device cannot be queried.  Tied to the
+ * device current at creation; without a device a host-only plan is made, whose calls
+ * return CONV_ERR_CUDA.  out_dtype is y's type.
+ */
+conv_status conv_int8_plan_create(conv_int8_plan **plan, int M, int N, int K, conv_dtype out_dtype, conv_act act);
+
+/* The product.  Asynchronous on `stream`; y must not overlap the inputs.
+ * CONV_ERR_INVALID_ARG for a NULL plan or a NULL required pointer or another current
+ * device, CONV_ERR_MISALIGNED for a base that is not 16-byte aligned, CONV_ERR_CUDA if a
+ * launch fails. */
+conv_status conv_int8_forward(conv_int8_plan *p, const void *x, const float *x_scale, const void *w,
+                              const float *w_scale, const float *bias, void *y, void *stream);
+
+/* Bytes of device workspace that conv_int8_forward_quantize takes (may be 0; pass NULL then). */
+conv_status conv_int8_workspace(const conv_int8_plan *p, unsigned long long *bytes);
+
+/* The product from x [M][K] in FP32 or BF16 (x_dtype): its rows are brought to 8 bits in
+ * the call, by the rules of conv_quantize_rows.  workspace: conv_int8_workspace bytes,
+ * contents of no account before and after; calls that may run at the same time take one
+ * each. */
+conv_status conv_int8_forward_quantize(conv_int8_plan *p, const void *x, conv_dtype x_dtype, const void *w,
+                                       const float *w_scale, const float *bias, void *y, void *workspace,
+                                       void *stream);
+
+/* Status word of the plan (waits that gave up): the contract of conv_plan_device_status. */
+conv_status conv_int8_plan_device_status(const conv_int8_plan *p, void *stream, int *code);
+
+/* Free the plan: the contract of conv_plan_destroy.  NULL is accepted. */
+conv_status conv_int8_plan_destroy(conv_int8_plan *p);
+
+/*
+ * Rows to 8 bits: for each row of x [M][K] (FP32 or BF16), amax = max |x|,
+ *   scale = amax / 127,  q = rint(x * (127 / amax))      (ties to even),
+ * each operation rounded once in FP32.  A row whose amax is below 2^-100 gets scale 0 and
+ * q = 0; a row with a NaN or an Inf gets scale NaN and q = 0, so that its products are NaN.
+ * q [M][K] 8-bit integers, scale [M] FP32.  Asynchronous on `stream`.
+ * CONV_ERR_INVALID_ARG for NULL pointers, non-positive sizes or an unknown dtype,
+ * CONV_ERR_UNSUPPORTED above 2^40 elements, CONV_ERR_MISALIGNED for a base that is not
+ * 16-byte aligned, CONV_ERR_CUDA if the launch fails.
+ */
+conv_status conv_quantize_rows(const void *x, conv_dtype dtype, int M, int K, void *q, float *scale, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
