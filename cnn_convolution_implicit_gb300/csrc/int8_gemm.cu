@@ -1,0 +1,516 @@
+// int8_gemm.cu -- the 8-bit product on tcgen05 tensor cores:
+//
+//   y[m][n] = act( x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k] + bias[n] )
+//
+// An 8-bit integer is exact in FP16 (11 significand bits), a product of two of them
+// stays below 2^15 and the FP32 accumulator holds every partial sum below 2^24
+// exactly, so the FP16 MMA gives the integer sum (always for K <= 1024).  This part's
+// 8-bit integer tensor rate is a small fraction of its FP16 rate.
+//
+// The operands stay 8-bit in memory; converter warps bring them to FP16 on their way
+// into shared memory:
+//   x ^ 0x80 = x + 128 as an unsigned byte u; the FP16 bit pattern 0x6400 | u is
+//   1024 + u; subtracting 1152 leaves x.  One exclusive-or, two byte permutes and two
+//   packed subtractions for four values.
+//
+// Warp roles (544 threads, one CTA per SM, persistent over tiles):
+//   warps 0..7    converters: 16-byte loads of x and w rows one K-step ahead, in registers,
+//                 FP16 values into the 128-byte-swizzle operand tiles of a stage
+//   warps 8..15   epilogue: two warps per 32-row quarter of tensor memory, half of the
+//                 columns each: scales, bias, activation, rounding, stores from registers
+//   warp 16       tensor memory; one lane issues tcgen05.mma and commits
+// A stage holds K = 128 of both operands as two K = 64 blocks of 128-byte rows.  Tensor
+// memory holds two accumulators, so the epilogue of one tile overlaps the next one's MMAs.
+//
+// PAIR: two SMs share a 256 x BN tile (tcgen05.mma.cta_group::2): each converts its own
+// 128 rows of x and BN / 2 rows of w.  Shared memory bounds this kernel (written by the
+// converters, read by the MMA), and a pair halves the traffic of w.
+//
+// Rows past M or N are neither loaded nor written: their outputs are never stored, and
+// one row's operand does not reach another row's result.  Past K both operands are 0.
+#include "int8_internal.h"
+#include "pointwise_math.cuh"
+#include "ptx.cuh"
+
+namespace convgb {
+
+namespace {
+
+constexpr int kConverterWarps = 8;
+constexpr int kEpilogueWarps = 8;
+constexpr int kMmaWarp = kConverterWarps + kEpilogueWarps;
+constexpr int kGemmThreads = 32 * (kMmaWarp + 1);
+constexpr int kStepK = 128;      // K of one stage
+constexpr int kRowBytes = 128;   // one operand row of a K = 64 block
+
+template <bool PAIR, int BN>
+struct Shape {
+    static constexpr int kRowsB = PAIR ? BN / 2 : BN;
+    static constexpr int kBlockA = 128 * kRowBytes;      // one K = 64 block
+    static constexpr int kBlockB = kRowsB * kRowBytes;
+    static constexpr int kStage = 2 * (kBlockA + kBlockB);
+    static constexpr int kStages = kStage >= 65536 ? 3 : (kStage >= 49152 ? 4 : 5);
+    static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
+    static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int kSmem = kStages * kStage + 1024 + 256;
+};
+
+struct Bars {
+    uint64_t* full;
+    uint64_t* empty;
+    uint64_t* tfull;
+    uint64_t* tempty;
+    uint64_t* drain;
+    uint32_t* tmem_slot;
+    int* abort;
+};
+
+// Four 8-bit integers to FP16.
+__device__ __forceinline__ uint2 to_half4(uint32_t v) {
+    const uint32_t u = v ^ 0x80808080u;
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);  // bytes 0, 1 below 0x64
+    uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));  // 1152
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+    return make_uint2(lo, hi);
+}
+
+// 16 bytes of a row from byte `at` of a matrix of `total` bytes, zero from `len` on (1..16 bytes
+// are wanted).  Rows that start on 16 bytes take one load (len a multiple of 16).  Others
+// take the one or two aligned granules that hold the bytes and shift; a granule that the matrix
+// ends in is read byte by byte, so nothing past its last byte is touched.
+__device__ __forceinline__ uint4 granule(const int8_t* base, long long g, long long total) {
+    const long long at = g << 4;
+    if (at + 16 <= total) return __ldg(reinterpret_cast<const uint4*>(base + at));
+    uint32_t v[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 16; ++i)
+        if (at + i < total) v[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(base[at + i])) << (8 * (i & 3));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load_item(const int8_t* base, long long at, int len, long long total) {
+    if constexpr (ALIGNED) {
+        return __ldg(reinterpret_cast<const uint4*>(base + at));
+    } else {
+        const long long g = at >> 4;
+        const int off = static_cast<int>(at & 15);
+        const uint4 a = granule(base, g, total);
+        const uint4 b = off + len > 16 ? granule(base, g + 1, total) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int word = off >> 2, shift = (off & 3) * 8;
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // word is 0..3: a select per word keeps w in registers
+                lo = word == j ? w[i + j] : lo;
+                hi = word == j ? w[i + j + 1] : hi;
+            }
+            const int left = len - 4 * i;
+            const uint32_t v = __funnelshift_r(lo, hi, shift);
+            r[i] = left >= 4 ? v : (left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u));
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
+__device__ __forceinline__ void store_v8(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Where a converter stands: its tile and K-step.
+struct Walk {
+    int u, k0;
+    int m0, n0;  // first row of x and of w that this CTA converts
+};
+
+template <bool PAIR, int BN>
+__device__ __forceinline__ void place(Walk& w, int n_tiles, uint32_t rank) {
+    const int mu = w.u / n_tiles;
+    const int nt = w.u - mu * n_tiles;
+    w.m0 = PAIR ? mu * 256 + static_cast<int>(rank) * 128 : mu * 128;
+    w.n0 = nt * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
+}
+
+template <bool PAIR, int BN, bool ALIGNED>
+__device__ __forceinline__ void load_stage(const Int8Params& p, const Walk& w, int r0, int c, uint4 (&item)[Shape<PAIR, BN>::kItems]) {
+    const int k = w.k0 + 16 * c;
+    const int len = p.K - k;
+    const long long total_x = static_cast<long long>(p.M) * p.K, total_w = static_cast<long long>(p.N) * p.K;
+#pragma unroll
+    for (int i = 0; i < Shape<PAIR, BN>::kItems; ++i) {
+        item[i] = make_uint4(0, 0, 0, 0);
+        if (len <= 0) continue;
+        const int n_len = len < 16 ? len : 16;
+        if (i < 4) {
+            const int row = w.m0 + r0 + 32 * i;
+            if (row < p.M) item[i] = load_item<ALIGNED>(p.x, static_cast<long long>(row) * p.K + k, n_len, total_x);
+        } else {
+            const int row = w.n0 + r0 + 32 * (i - 4);
+            if (row < p.N) item[i] = load_item<ALIGNED>(p.w, static_cast<long long>(row) * p.K + k, n_len, total_w);
+        }
+    }
+}
+
+template <bool PAIR, int BN>
+__device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c, const uint4 (&item)[Shape<PAIR, BN>::kItems],
+                                            uint8_t* stage) {
+    using S = Shape<PAIR, BN>;
+    const int kb = c >> 2;
+    const int first = (c & 3) * 2;  // the item's two 16-byte chunks of the FP16 row
+    const int swap = kb;            // a warp's lanes 4..7 (of 8) write their upper half first: 8 lanes, 8 bank groups
+#pragma unroll
+    for (int i = 0; i < S::kItems; ++i) {
+        const int row = r0 + 32 * (i < 4 ? i : i - 4);
+        if (i < 4 ? w.m0 + row >= p.M : w.n0 + row >= p.N) continue;
+        const uint2 a = to_half4(item[i].x), b = to_half4(item[i].y), d = to_half4(item[i].z), e = to_half4(item[i].w);
+        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+        uint8_t* dst = stage + (i < 4 ? kb * S::kBlockA : 2 * S::kBlockA + kb * S::kBlockB) + row * kRowBytes;
+        const int sw = row & 7;
+        *reinterpret_cast<uint4*>(dst + (((first + swap) ^ sw) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + (((first + 1 - swap) ^ sw) << 4)) = swap ? lo : hi;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void finish_chunk(const Int8Params& p, const uint32_t (&v)[32], float xs, int n, float (&f)[32]) {
+    if (n + 32 <= p.N) {
+        const float4* ws = reinterpret_cast<const float4*>(p.w_scale + n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 s = __ldg(ws + i);
+            f[4 * i + 0] = __uint_as_float(v[4 * i + 0]) * xs * s.x;
+            f[4 * i + 1] = __uint_as_float(v[4 * i + 1]) * xs * s.y;
+            f[4 * i + 2] = __uint_as_float(v[4 * i + 2]) * xs * s.z;
+            f[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * xs * s.w;
+        }
+        if (p.bias) {
+            const float4* b4 = reinterpret_cast<const float4*>(p.bias + n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 b = __ldg(b4 + i);
+                f[4 * i + 0] += b.x;
+                f[4 * i + 1] += b.y;
+                f[4 * i + 2] += b.z;
+                f[4 * i + 3] += b.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const bool on = n + i < p.N;
+            f[i] = __uint_as_float(v[i]) * xs * (on ? __ldg(p.w_scale + n + i) : 0.0f);
+            if (p.bias && on) f[i] += __ldg(p.bias + n + i);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
+}
+
+// 32 outputs of one row, in the widest stores that the row's start allows (wide: 32 or 16
+// bytes; 0: one by one).
+__device__ __forceinline__ void store_chunk(const Int8Params& p, const float (&f)[32], long long row, int n, int wide) {
+    const long long at = row * p.N + n;
+    if (n + 32 <= p.N && wide != 0) {
+        if (p.out_bf16) {
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
+            if (wide == 32) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t q[8] = {h[8 * j], h[8 * j + 1], h[8 * j + 2], h[8 * j + 3],
+                                           h[8 * j + 4], h[8 * j + 5], h[8 * j + 6], h[8 * j + 7]};
+                    store_v8(y + 16 * j, q);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<uint4*>(y)[j] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+            }
+        } else {
+            float* y = static_cast<float*>(p.y) + at;
+            if (wide == 32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t q[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(f[8 * j + i]);
+                    store_v8(y + 8 * j, q);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    reinterpret_cast<float4*>(y)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            }
+        }
+        return;
+    }
+    if (p.out_bf16) {
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (n + i < p.N) y[i] = __float2bfloat16_rn(f[i]);
+    } else {
+        float* y = static_cast<float*>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (n + i < p.N) y[i] = f[i];
+    }
+}
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as idesc_bf16_f32 with FP16 operands (type 0)
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <bool PAIR, int BN, bool ALIGNED>
+__global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Params p) {
+    using S = Shape<PAIR, BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars b;
+    b.full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage);
+    b.empty = b.full + S::kStages;
+    b.tfull = b.empty + S::kStages;
+    b.tempty = b.tfull + 2;
+    b.drain = b.tempty + 2;
+    b.tmem_slot = reinterpret_cast<uint32_t*>(b.drain + 1);
+    b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
+    volatile int* abort = b.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    constexpr int kCtas = PAIR ? 2 : 1;
+
+    const int n_tiles = (p.N + BN - 1) / BN;
+    const int units = ((p.M + 128 * kCtas - 1) / (128 * kCtas)) * n_tiles;
+    const int unit0 = static_cast<int>(blockIdx.x) / kCtas, unit_step = static_cast<int>(gridDim.x) / kCtas;
+    const int ksteps = (p.K + kStepK - 1) / kStepK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&b.full[s], kCtas * kConverterWarps);
+            mbar_init(&b.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.tfull[i], 1);
+            mbar_init(&b.tempty[i], kCtas * kEpilogueWarps);
+        }
+        mbar_init(b.drain, 1);
+        *b.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(b.tmem_slot, S::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(b.tmem_slot, S::kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // the peer's barriers exist before anything signals them
+    tc_fence_after();
+    const uint32_t tmem = *b.tmem_slot;
+
+    if (warp < kConverterWarps) {
+        // ------------------------------------------------------------ converters
+        const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+        Walk w{unit0, 0, 0, 0};
+        if (w.u < units) {
+            place<PAIR, BN>(w, n_tiles, rank);
+            uint4 cur[S::kItems];
+            load_stage<PAIR, BN, ALIGNED>(p, w, r0, c, cur);
+            int st = 0;
+            uint32_t ph = 0;
+            while (true) {
+                Walk nw = w;
+                nw.k0 += kStepK;
+                if (nw.k0 >= p.K) {
+                    nw.k0 = 0;
+                    nw.u += unit_step;
+                    if (nw.u < units) place<PAIR, BN>(nw, n_tiles, rank);
+                }
+                const bool more = nw.u < units;
+                uint4 nxt[S::kItems];
+                if (more) load_stage<PAIR, BN, ALIGNED>(p, nw, r0, c, nxt);  // in flight while this step converts
+                if (!mbar_wait(&b.empty[st], ph ^ 1u, abort)) {
+                    record_status(p.status, kStatusTimeoutTransform, abort);
+                    break;
+                }
+                store_stage<PAIR, BN>(p, w, r0, c, cur, smem + st * S::kStage);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.full[st]), 0));
+                    else mbar_arrive(&b.full[st]);
+                }
+                if (++st == S::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+                if (!more) break;
+                w = nw;
+#pragma unroll
+                for (int i = 0; i < S::kItems; ++i) cur[i] = nxt[i];
+            }
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3;
+        const int half = (warp - kConverterWarps) >> 2;
+        constexpr int kHalfCols = BN >= 64 ? BN / 2 : BN;
+        const bool mine = BN >= 64 || half == 0;  // 32 columns: one warp a quarter drains them
+        const int es = p.out_bf16 ? 2 : 4;
+        const long long row_bytes = static_cast<long long>(p.N) * es;
+        const uintptr_t y0 = reinterpret_cast<uintptr_t>(p.y);
+        const int wide = row_bytes % 32 == 0 && y0 % 32 == 0 ? 32 : (row_bytes % 16 == 0 ? 16 : 0);
+        int local = 0;
+        for (int u = unit0; u < units; u += unit_step, ++local) {
+            const int buf = local & 1;
+            const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
+            const int mu = u / n_tiles, nt = u - mu * n_tiles;
+            const long long row = static_cast<long long>(mu) * 128 * kCtas + rank * 128 + quarter * 32 + lane;
+            const float xs = row < p.M ? __ldg(p.x_scale + row) : 0.0f;
+            if (!mbar_wait_cluster(&b.tfull[buf], use, abort)) {
+                record_status(p.status, kStatusTimeoutEpilogue, abort);
+                break;
+            }
+            tc_fence_after();
+            if (mine) {
+#pragma unroll 1
+                for (int cc = 0; cc < kHalfCols; cc += 32) {
+                    const int col = half * kHalfCols + cc;
+                    const int n = nt * BN + col;
+                    if (n >= p.N) break;
+                    uint32_t v[32];
+                    tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + col, v);
+                    tmem_ld_wait(v);
+                    float f[32];
+                    if (p.act == CONV_ACT_RELU) finish_chunk<CONV_ACT_RELU>(p, v, xs, n, f);
+                    else if (p.act == CONV_ACT_SILU) finish_chunk<CONV_ACT_SILU>(p, v, xs, n, f);
+                    else finish_chunk<CONV_ACT_NONE>(p, v, xs, n, f);
+                    if (row < p.M) store_chunk(p, f, row, n, wide);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.tempty[buf]), 0));
+                else mbar_arrive(&b.tempty[buf]);
+            }
+        }
+    } else if (lane == 0 && leader) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t idesc = idesc_f16_f32(128 * kCtas, BN);
+        int st = 0, local = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+            const int buf = local & 1;
+            const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
+            if (!mbar_wait_cluster(&b.tempty[buf], use ^ 1u, abort)) {
+                record_status(p.status, kStatusTimeoutMma, abort);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + buf * BN;
+            for (int ks = 0; ks < ksteps; ++ks) {
+                if (!mbar_wait_cluster(&b.full[st], ph, abort)) {
+                    record_status(p.status, kStatusTimeoutMma, abort);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = smem_addr(smem + st * S::kStage);
+                const int left = (p.K - ks * kStepK + 15) >> 4;
+                const int mmas = left < 8 ? left : 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= mmas) break;
+                    const uint64_t da = sdesc_sw128(base + (j >> 2) * S::kBlockA) + (j & 3) * 2;
+                    const uint64_t db = sdesc_sw128(base + 2 * S::kBlockA + (j >> 2) * S::kBlockB) + (j & 3) * 2;
+                    const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
+                    if constexpr (PAIR) mma_bf16_pair(d, da, db, idesc, acc);  // kind::f16; idesc names the type
+                    else mma_bf16(d, da, db, idesc, acc);
+                }
+                if constexpr (PAIR) mma_commit_pair(&b.empty[st], 3);
+                else mma_commit(&b.empty[st]);
+                if (++st == S::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if constexpr (PAIR) mma_commit_pair(&b.tfull[buf], 3);
+            else mma_commit(&b.tfull[buf]);
+        }
+        if constexpr (PAIR) mma_commit_pair(b.drain, 1);
+        else mma_commit(b.drain);
+        if (!mbar_wait_cluster(b.drain, 0, nullptr)) record_status(p.status, kStatusTimeoutDrain, abort);
+    }
+    __syncwarp();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // no CTA leaves while its peer may still signal it
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, S::kTmemCols);
+        else tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+template <bool PAIR, int BN, bool ALIGNED>
+cudaError_t launch_variant(const Int8Params& p, int num_sms, cudaStream_t stream) {
+    using S = Shape<PAIR, BN>;
+    static SmemLimitCache limits;
+    auto* fn = int8_gemm_kernel<PAIR, BN, ALIGNED>;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), S::kSmem, limits);
+    if (e != cudaSuccess) return e;
+    constexpr int ctas = PAIR ? 2 : 1;
+    const long long units = (static_cast<long long>(p.M) + 128 * ctas - 1) / (128 * ctas) * ((p.N + BN - 1) / BN);
+    const int slots = num_sms / ctas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((units < slots ? units : slots) * ctas));
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <bool PAIR, int BN>
+cudaError_t launch_aligned(const Int8Params& p, int num_sms, cudaStream_t stream) {
+    if (p.K % 16 == 0) return launch_variant<PAIR, BN, true>(p, num_sms, stream);
+    return launch_variant<PAIR, BN, false>(p, num_sms, stream);
+}
+
+}  // namespace
+
+bool int8_gemm_fits(const Int8Params& p) {  // tile counts and row indexes in 32 bits
+    return (static_cast<long long>(p.M) + 127) / 128 * ((p.N + 31) / 32) < (1LL << 30) && p.M < (1 << 30) && p.N < (1 << 30);
+}
+
+cudaError_t launch_int8_gemm(const Int8Params& p, int num_sms, cudaStream_t stream) {
+    const long long m128 = (static_cast<long long>(p.M) + 127) / 128, m256 = (m128 + 1) / 2;
+    const auto tiles = [&](int bn) { return (p.N + bn - 1) / bn; };
+    if (m128 > 1 && m256 * tiles(256) >= num_sms / 4) return launch_aligned<true, 256>(p, num_sms, stream);
+    if (m128 * tiles(128) >= num_sms / 2) return launch_aligned<false, 128>(p, num_sms, stream);
+    if (m128 * tiles(64) >= num_sms / 2) return launch_aligned<false, 64>(p, num_sms, stream);
+    return launch_aligned<false, 32>(p, num_sms, stream);
+}
+
+}  // namespace convgb

@@ -22,6 +22,9 @@ struct Int8Params {
     void* y;
     unsigned* status;
 };
+// Tensor-core kernel (int8_gemm.cu); whether its tile counts stay within 32 bits.
+bool int8_gemm_fits(const Int8Params& p);
+cudaError_t launch_int8_gemm(const Int8Params& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_product(const Int8Params& p, int num_sms, cudaStream_t stream);
 
 // Rows of x (BF16 or FP32) to 8 bits with one scale each.

@@ -30,7 +30,7 @@ __global__ void int8_plain_kernel(const Int8Params p) {
 }  // namespace
 
 cudaError_t launch_int8_product(const Int8Params& p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
+    if (p.M > 8 && int8_gemm_fits(p)) return launch_int8_gemm(p, num_sms, stream);
     const int rows = (p.M + 7) / 8;
     const dim3 grid((p.N + 31) / 32, rows < 65535 ? rows : 65535), block(32, 8);
     if (p.act == CONV_ACT_RELU) int8_plain_kernel<CONV_ACT_RELU><<<grid, block, 0, stream>>>(p);
