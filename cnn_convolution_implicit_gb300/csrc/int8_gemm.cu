@@ -13,12 +13,18 @@
 //   1024 + u; subtracting 1152 leaves x.  One exclusive-or, two byte permutes and two
 //   packed subtractions for four values.
 //
-// Warp roles (544 threads, one CTA per SM, persistent over tiles):
-//   warps 0..7    converters: 16-byte loads of x and w rows one K-step ahead, in registers,
-//                 FP16 values into the 128-byte-swizzle operand tiles of a stage
-//   warps 8..15   epilogue: two warps per 32-row quarter of tensor memory, half of the
-//                 columns each: scales, bias, activation, rounding, stores from registers
-//   warp 16       tensor memory; one lane issues tcgen05.mma and commits
+// Warp roles (448 threads, one CTA per SM, persistent over tiles):
+//   warps 0..7    converters: 8-bit rows from the raw ring to FP16 values in the 128-byte-swizzle
+//                 operand tiles of a stage
+//   warps 8..11   epilogue: one warp per 32-row quarter of tensor memory: scales, bias,
+//                 activation, rounding, stores from registers
+//   warp 12       tensor memory; one lane issues tcgen05.mma and commits
+//   warp 13       one lane fills the raw ring by TMA: K = 128 of both operands, 8-bit, per slot
+// Rows that do not start on 16 bytes (K % 16) are beyond the TMA: there the converters load
+// them straight from memory, one step ahead in registers (ALIGNED = false).  That form is
+// slower on any K: the fence that publishes a stage also waits for the loads under way, so
+// their latency is not hidden (8192 x 4096 x 4096: 413 us against the ring's in the launch
+// code's comment).
 // A stage holds K = 128 of both operands as two K = 64 blocks of 128-byte rows.  Tensor
 // memory holds two accumulators, so the epilogue of one tile overlaps the next one's MMAs.
 //
@@ -37,25 +43,30 @@ namespace convgb {
 namespace {
 
 constexpr int kConverterWarps = 8;
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 4;
 constexpr int kMmaWarp = kConverterWarps + kEpilogueWarps;
-constexpr int kGemmThreads = 32 * (kMmaWarp + 1);
+constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kGemmThreads = 32 * (kLoadWarp + 1);
 constexpr int kStepK = 128;      // K of one stage
 constexpr int kRowBytes = 128;   // one operand row of a K = 64 block
 
-template <bool PAIR, int BN>
+template <bool PAIR, int BN, bool ALIGNED>
 struct Shape {
     static constexpr int kRowsB = PAIR ? BN / 2 : BN;
     static constexpr int kBlockA = 128 * kRowBytes;      // one K = 64 block
     static constexpr int kBlockB = kRowsB * kRowBytes;
     static constexpr int kStage = 2 * (kBlockA + kBlockB);
-    static constexpr int kStages = kStage >= 65536 ? 3 : (kStage >= 49152 ? 4 : 5);
+    static constexpr int kRaw = ALIGNED ? (128 + kRowsB) * kStepK : 0;  // one slot of the raw ring
+    static constexpr int kStages = ALIGNED ? 2 : (kStage >= 65536 ? 3 : 4);
+    static constexpr int kRawSlots = ALIGNED ? (kStage >= 65536 ? 3 : 5) : 0;
     static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int kSmem = kStages * kStage + 1024 + 256;
+    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 1024 + 256;
 };
 
 struct Bars {
+    uint64_t* rfull;
+    uint64_t* rempty;
     uint64_t* full;
     uint64_t* empty;
     uint64_t* tfull;
@@ -76,9 +87,8 @@ __device__ __forceinline__ uint2 to_half4(uint32_t v) {
 }
 
 // 16 bytes of a row from byte `at` of a matrix of `total` bytes, zero from `len` on (1..16 bytes
-// are wanted).  Rows that start on 16 bytes take one load (len a multiple of 16).  Others
-// take the one or two aligned granules that hold the bytes and shift; a granule that the matrix
-// ends in is read byte by byte, so nothing past its last byte is touched.
+// are wanted): the one or two aligned granules that hold the bytes, shifted.  A granule that
+// the matrix ends in is read byte by byte, so nothing past its last byte is touched.
 __device__ __forceinline__ uint4 granule(const int8_t* base, long long g, long long total) {
     const long long at = g << 4;
     if (at + 16 <= total) return __ldg(reinterpret_cast<const uint4*>(base + at));
@@ -88,32 +98,27 @@ __device__ __forceinline__ uint4 granule(const int8_t* base, long long g, long l
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-template <bool ALIGNED>
 __device__ __forceinline__ uint4 load_item(const int8_t* base, long long at, int len, long long total) {
-    if constexpr (ALIGNED) {
-        return __ldg(reinterpret_cast<const uint4*>(base + at));
-    } else {
-        const long long g = at >> 4;
-        const int off = static_cast<int>(at & 15);
-        const uint4 a = granule(base, g, total);
-        const uint4 b = off + len > 16 ? granule(base, g + 1, total) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const int word = off >> 2, shift = (off & 3) * 8;
-        uint32_t r[4];
+    const long long g = at >> 4;
+    const int off = static_cast<int>(at & 15);
+    const uint4 a = granule(base, g, total);
+    const uint4 b = off + len > 16 ? granule(base, g + 1, total) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int word = off >> 2, shift = (off & 3) * 8;
+    uint32_t r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t lo = 0, hi = 0;
+    for (int i = 0; i < 4; ++i) {
+        uint32_t lo = 0, hi = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // word is 0..3: a select per word keeps w in registers
-                lo = word == j ? w[i + j] : lo;
-                hi = word == j ? w[i + j + 1] : hi;
-            }
-            const int left = len - 4 * i;
-            const uint32_t v = __funnelshift_r(lo, hi, shift);
-            r[i] = left >= 4 ? v : (left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u));
+        for (int j = 0; j < 4; ++j) {  // word is 0..3: a select per word keeps w in registers
+            lo = word == j ? w[i + j] : lo;
+            hi = word == j ? w[i + j + 1] : hi;
         }
-        return make_uint4(r[0], r[1], r[2], r[3]);
+        const int left = len - 4 * i;
+        const uint32_t v = __funnelshift_r(lo, hi, shift);
+        r[i] = left >= 4 ? v : (left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u));
     }
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 __device__ __forceinline__ void store_v8(void* p, const uint32_t (&v)[8]) {
@@ -136,30 +141,41 @@ __device__ __forceinline__ void place(Walk& w, int n_tiles, uint32_t rank) {
     w.n0 = nt * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
 }
 
-template <bool PAIR, int BN, bool ALIGNED>
-__device__ __forceinline__ void load_stage(const Int8Params& p, const Walk& w, int r0, int c, uint4 (&item)[Shape<PAIR, BN>::kItems]) {
+template <bool PAIR, int BN>
+__device__ __forceinline__ void advance(const Int8Params& p, Walk& w, int n_tiles, int units, int unit_step, uint32_t rank) {
+    w.k0 += kStepK;
+    if (w.k0 >= p.K) {
+        w.k0 = 0;
+        w.u += unit_step;
+        if (w.u < units) place<PAIR, BN>(w, n_tiles, rank);
+    }
+}
+
+template <bool PAIR, int BN>
+__device__ __forceinline__ void load_stage(const Int8Params& p, const Walk& w, int r0, int c,
+                                           uint4 (&item)[Shape<PAIR, BN, false>::kItems]) {
     const int k = w.k0 + 16 * c;
     const int len = p.K - k;
     const long long total_x = static_cast<long long>(p.M) * p.K, total_w = static_cast<long long>(p.N) * p.K;
 #pragma unroll
-    for (int i = 0; i < Shape<PAIR, BN>::kItems; ++i) {
+    for (int i = 0; i < Shape<PAIR, BN, false>::kItems; ++i) {
         item[i] = make_uint4(0, 0, 0, 0);
         if (len <= 0) continue;
         const int n_len = len < 16 ? len : 16;
         if (i < 4) {
             const int row = w.m0 + r0 + 32 * i;
-            if (row < p.M) item[i] = load_item<ALIGNED>(p.x, static_cast<long long>(row) * p.K + k, n_len, total_x);
+            if (row < p.M) item[i] = load_item(p.x, static_cast<long long>(row) * p.K + k, n_len, total_x);
         } else {
             const int row = w.n0 + r0 + 32 * (i - 4);
-            if (row < p.N) item[i] = load_item<ALIGNED>(p.w, static_cast<long long>(row) * p.K + k, n_len, total_w);
+            if (row < p.N) item[i] = load_item(p.w, static_cast<long long>(row) * p.K + k, n_len, total_w);
         }
     }
 }
 
 template <bool PAIR, int BN>
-__device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c, const uint4 (&item)[Shape<PAIR, BN>::kItems],
-                                            uint8_t* stage) {
-    using S = Shape<PAIR, BN>;
+__device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c,
+                                            const uint4 (&item)[Shape<PAIR, BN, false>::kItems], uint8_t* stage) {
+    using S = Shape<PAIR, BN, false>;
     const int kb = c >> 2;
     const int first = (c & 3) * 2;  // the item's two 16-byte chunks of the FP16 row
     const int swap = kb;            // a warp's lanes 4..7 (of 8) write their upper half first: 8 lanes, 8 bank groups
@@ -269,12 +285,17 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as ides
 }
 
 template <bool PAIR, int BN, bool ALIGNED>
-__global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Params p) {
-    using S = Shape<PAIR, BN>;
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    int8_gemm_kernel(const Int8Params p, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_w) {
+    using S = Shape<PAIR, BN, ALIGNED>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars b;
-    b.full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStage);
+    uint8_t* raw = smem + S::kStages * S::kStage;
+    b.rfull = reinterpret_cast<uint64_t*>(raw + S::kRawSlots * S::kRaw);
+    b.rempty = b.rfull + S::kRawSlots;
+    b.full = b.rempty + S::kRawSlots;
     b.empty = b.full + S::kStages;
     b.tfull = b.empty + S::kStages;
     b.tempty = b.tfull + 2;
@@ -293,6 +314,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Pa
     const int ksteps = (p.K + kStepK - 1) / kStepK;
 
     if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kRawSlots; ++s) {
+            mbar_init(&b.rfull[s], 1);
+            mbar_init(&b.rempty[s], kConverterWarps);
+        }
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&b.full[s], kCtas * kConverterWarps);
             mbar_init(&b.empty[s], 1);
@@ -326,26 +351,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Pa
         Walk w{unit0, 0, 0, 0};
         if (w.u < units) {
             place<PAIR, BN>(w, n_tiles, rank);
-            uint4 cur[S::kItems];
-            load_stage<PAIR, BN, ALIGNED>(p, w, r0, c, cur);
             int st = 0;
             uint32_t ph = 0;
-            while (true) {
-                Walk nw = w;
-                nw.k0 += kStepK;
-                if (nw.k0 >= p.K) {
-                    nw.k0 = 0;
-                    nw.u += unit_step;
-                    if (nw.u < units) place<PAIR, BN>(nw, n_tiles, rank);
-                }
-                const bool more = nw.u < units;
-                uint4 nxt[S::kItems];
-                if (more) load_stage<PAIR, BN, ALIGNED>(p, nw, r0, c, nxt);  // in flight while this step converts
+            const auto publish = [&](const uint4(&item)[S::kItems]) {  // one stage
                 if (!mbar_wait(&b.empty[st], ph ^ 1u, abort)) {
                     record_status(p.status, kStatusTimeoutTransform, abort);
-                    break;
+                    return false;
                 }
-                store_stage<PAIR, BN>(p, w, r0, c, cur, smem + st * S::kStage);
+                store_stage<PAIR, BN>(p, w, r0, c, item, smem + st * S::kStage);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -356,18 +369,49 @@ __global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Pa
                     st = 0;
                     ph ^= 1u;
                 }
-                if (!more) break;
-                w = nw;
+                return true;
+            };
+            if constexpr (ALIGNED) {
+                int rs = 0;
+                uint32_t rph = 0;
+                while (w.u < units) {
+                    if (!mbar_wait(&b.rfull[rs], rph, abort)) {
+                        record_status(p.status, kStatusTimeoutTransform, abort);
+                        break;
+                    }
+                    uint4 item[S::kItems];
+                    const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + threadIdx.x;
 #pragma unroll
-                for (int i = 0; i < S::kItems; ++i) cur[i] = nxt[i];
+                    for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 256];  // rows r0 + 32 i of x, then of w
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.rempty[rs]);
+                    if (!publish(item)) break;
+                    if (++rs == S::kRawSlots) {
+                        rs = 0;
+                        rph ^= 1u;
+                    }
+                    advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+                }
+            } else {
+                uint4 set0[S::kItems], set1[S::kItems];
+                load_stage<PAIR, BN>(p, w, r0, c, set0);
+                // Converts `cur`; `nxt` is in flight meanwhile.  Returns whether another step follows.
+                const auto step = [&](const uint4(&cur)[S::kItems], uint4(&nxt)[S::kItems]) {
+                    Walk nw = w;
+                    advance<PAIR, BN>(p, nw, n_tiles, units, unit_step, rank);
+                    const bool more = nw.u < units;
+                    if (more) load_stage<PAIR, BN>(p, nw, r0, c, nxt);
+                    if (!publish(cur)) return false;
+                    w = nw;
+                    return more;
+                };
+                while (step(set0, set1) && step(set1, set0)) {
+                }
             }
         }
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3;
-        const int half = (warp - kConverterWarps) >> 2;
-        constexpr int kHalfCols = BN >= 64 ? BN / 2 : BN;
-        const bool mine = BN >= 64 || half == 0;  // 32 columns: one warp a quarter drains them
         const int es = p.out_bf16 ? 2 : 4;
         const long long row_bytes = static_cast<long long>(p.N) * es;
         const uintptr_t y0 = reinterpret_cast<uintptr_t>(p.y);
@@ -384,27 +428,56 @@ __global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Pa
                 break;
             }
             tc_fence_after();
-            if (mine) {
 #pragma unroll 1
-                for (int cc = 0; cc < kHalfCols; cc += 32) {
-                    const int col = half * kHalfCols + cc;
-                    const int n = nt * BN + col;
-                    if (n >= p.N) break;
-                    uint32_t v[32];
-                    tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + col, v);
-                    tmem_ld_wait(v);
-                    float f[32];
-                    if (p.act == CONV_ACT_RELU) finish_chunk<CONV_ACT_RELU>(p, v, xs, n, f);
-                    else if (p.act == CONV_ACT_SILU) finish_chunk<CONV_ACT_SILU>(p, v, xs, n, f);
-                    else finish_chunk<CONV_ACT_NONE>(p, v, xs, n, f);
-                    if (row < p.M) store_chunk(p, f, row, n, wide);
-                }
+            for (int col = 0; col < BN; col += 32) {
+                const int n = nt * BN + col;
+                if (n >= p.N) break;
+                uint32_t v[32];
+                tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + col, v);
+                tmem_ld_wait(v);
+                float f[32];
+                if (p.act == CONV_ACT_RELU) finish_chunk<CONV_ACT_RELU>(p, v, xs, n, f);
+                else if (p.act == CONV_ACT_SILU) finish_chunk<CONV_ACT_SILU>(p, v, xs, n, f);
+                else finish_chunk<CONV_ACT_NONE>(p, v, xs, n, f);
+                if (row < p.M) store_chunk(p, f, row, n, wide);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.tempty[buf]), 0));
                 else mbar_arrive(&b.tempty[buf]);
+            }
+        }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ raw ring
+        if constexpr (ALIGNED) {
+            Walk w{unit0, 0, 0, 0};
+            if (lane == 0 && w.u < units) {
+                place<PAIR, BN>(w, n_tiles, rank);
+                long long issued = 0;
+                int rs = 0;
+                uint32_t ph = 0;
+                while (w.u < units) {
+                    if (!mbar_wait(&b.rempty[rs], ph ^ 1u, abort)) {
+                        record_status(p.status, kStatusTimeoutProducer, abort);
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&b.rfull[rs], S::kRaw);
+                    uint8_t* slot = raw + rs * S::kRaw;
+                    tma_load_2d(slot, &map_x, &b.rfull[rs], w.k0, w.m0);  // past the matrix: zeros
+                    tma_load_2d(slot + 128 * kStepK, &map_w, &b.rfull[rs], w.k0, w.n0);
+                    ++issued;
+                    if (++rs == S::kRawSlots) {
+                        rs = 0;
+                        ph ^= 1u;
+                    }
+                    advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+                }
+                for (int s = 0; s < S::kRawSlots; ++s) {  // no copy in flight when the CTA leaves
+                    const long long fills = issued / S::kRawSlots + (s < issued % S::kRawSlots ? 1 : 0);
+                    if (fills && !mbar_wait(&b.rfull[s], static_cast<uint32_t>((fills - 1) & 1), nullptr))
+                        record_status(p.status, kStatusTimeoutDrain, abort);
+                }
             }
         }
     } else if (lane == 0 && leader) {
@@ -467,9 +540,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) int8_gemm_kernel(const Int8Pa
     }
 }
 
+// [rows][K] 8-bit matrix in boxes of `box_rows` rows x 128 bytes.
+bool encode_rows(CUtensorMap* map, const int8_t* base, int rows, int K, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+    const cuuint32_t box[2] = {kStepK, static_cast<cuuint32_t>(box_rows)};
+    return tensor_map_encoder_ready() &&
+           encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_NONE) == CUDA_SUCCESS;
+}
+
 template <bool PAIR, int BN, bool ALIGNED>
 cudaError_t launch_variant(const Int8Params& p, int num_sms, cudaStream_t stream) {
-    using S = Shape<PAIR, BN>;
+    using S = Shape<PAIR, BN, ALIGNED>;
     static SmemLimitCache limits;
     auto* fn = int8_gemm_kernel<PAIR, BN, ALIGNED>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), S::kSmem, limits);
@@ -489,7 +572,10 @@ cudaError_t launch_variant(const Int8Params& p, int num_sms, cudaStream_t stream
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, p);
+    CUtensorMap map_x = {}, map_w = {};
+    if (ALIGNED && (!encode_rows(&map_x, p.x, p.M, p.K, 128) || !encode_rows(&map_w, p.w, p.N, p.K, S::kRowsB)))
+        return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, fn, p, map_x, map_w);
 }
 
 template <bool PAIR, int BN>
