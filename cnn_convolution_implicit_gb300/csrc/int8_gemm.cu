@@ -13,18 +13,18 @@
 //   1024 + u; subtracting 1152 leaves x.  One exclusive-or, two byte permutes and two
 //   packed subtractions for four values.
 //
-// Warp roles (448 threads, one CTA per SM, persistent over tiles):
-//   warps 0..7    converters: 8-bit rows from the raw ring to FP16 values in the 128-byte-swizzle
-//                 operand tiles of a stage
-//   warps 8..11   epilogue: one warp per 32-row quarter of tensor memory: scales, bias,
+// Warp roles (704 threads, one CTA per SM, persistent over tiles):
+//   warps 0..15   converters, two groups that take turns by stage, so one loads or waits while
+//                 the other converts: 8-bit rows from the raw ring to FP16 values in the
+//                 128-byte-swizzle operand tiles of a stage
+//   warps 16..19  epilogue: one warp per 32-row quarter of tensor memory: scales, bias,
 //                 activation, rounding, stores from registers
-//   warp 12       tensor memory; one lane issues tcgen05.mma and commits
-//   warp 13       one lane fills the raw ring by TMA: K = 128 of both operands, 8-bit, per slot
+//   warp 20       tensor memory; one lane issues tcgen05.mma and commits
+//   warp 21       one lane fills the raw ring by TMA: K = 128 of both operands, 8-bit, per slot
 // Rows that do not start on 16 bytes (K % 16) are beyond the TMA: there the converters load
-// them straight from memory, one step ahead in registers (ALIGNED = false).  That form is
-// slower on any K: the fence that publishes a stage also waits for the loads under way, so
-// their latency is not hidden (8192 x 4096 x 4096: 413 us against the ring's in the launch
-// code's comment).
+// them straight from memory (ALIGNED = false).  Loading a step ahead in registers does not
+// replace the ring: the fence that publishes a stage also waits for the loads under way
+// (8192 x 4096 x 4096 measured 413 us that way and 325 us with the ring).
 // A stage holds K = 128 of both operands as two K = 64 blocks of 128-byte rows.  Tensor
 // memory holds two accumulators, so the epilogue of one tile overlaps the next one's MMAs.
 //
@@ -42,7 +42,9 @@ namespace convgb {
 
 namespace {
 
-constexpr int kConverterWarps = 8;
+constexpr int kGroups = 2;       // converter groups
+constexpr int kGroupWarps = 8;
+constexpr int kConverterWarps = kGroups * kGroupWarps;
 constexpr int kEpilogueWarps = 4;
 constexpr int kMmaWarp = kConverterWarps + kEpilogueWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
@@ -57,11 +59,11 @@ struct Shape {
     static constexpr int kBlockB = kRowsB * kRowBytes;
     static constexpr int kStage = 2 * (kBlockA + kBlockB);
     static constexpr int kRaw = ALIGNED ? (128 + kRowsB) * kStepK : 0;  // one slot of the raw ring
-    static constexpr int kStages = ALIGNED ? 2 : (kStage >= 65536 ? 3 : 4);
+    static constexpr int kStages = 2;  // one for each converter group
     static constexpr int kRawSlots = ALIGNED ? (kStage >= 65536 ? 3 : 5) : 0;
     static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 1024 + 256;
+    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 2 * 256 * 4 + 256;
 };
 
 struct Bars {
@@ -72,6 +74,7 @@ struct Bars {
     uint64_t* tfull;
     uint64_t* tempty;
     uint64_t* drain;
+    uint64_t* esync;
     uint32_t* tmem_slot;
     int* abort;
 };
@@ -127,6 +130,25 @@ __device__ __forceinline__ void store_v8(void* p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
+// A bounded wait whose answer is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
+}
+
+// The epilogue warps among themselves: an mbarrier instead of a CTA barrier, so that this wait
+// is bounded like every other.
+__device__ __forceinline__ bool epilogue_sync(uint64_t* bar, uint32_t& phase, volatile int* abort) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    const bool ok = warp_wait(bar, phase, abort);
+    phase ^= 1u;
+    return ok;
+}
+
 // Where a converter stands: its tile and K-step.
 struct Walk {
     int u, k0;
@@ -149,6 +171,12 @@ __device__ __forceinline__ void advance(const Int8Params& p, Walk& w, int n_tile
         w.u += unit_step;
         if (w.u < units) place<PAIR, BN>(w, n_tiles, rank);
     }
+}
+
+template <bool PAIR, int BN>
+__device__ __forceinline__ void advance2(const Int8Params& p, Walk& w, int n_tiles, int units, int unit_step, uint32_t rank) {
+    advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+    if (w.u < units) advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
 }
 
 template <bool PAIR, int BN>
@@ -192,50 +220,30 @@ __device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, 
     }
 }
 
+// Scales, bias and activation of 32 columns of one row, in place.
 template <int ACT>
-__device__ __forceinline__ void finish_chunk(const Int8Params& p, const uint32_t (&v)[32], float xs, int n, float (&f)[32]) {
-    if (n + 32 <= p.N) {
-        const float4* ws = reinterpret_cast<const float4*>(p.w_scale + n);
+__device__ __forceinline__ void finish_chunk(uint32_t (&v)[32], float xs, const float* col_scale, const float* col_bias) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 s = __ldg(ws + i);
-            f[4 * i + 0] = __uint_as_float(v[4 * i + 0]) * xs * s.x;
-            f[4 * i + 1] = __uint_as_float(v[4 * i + 1]) * xs * s.y;
-            f[4 * i + 2] = __uint_as_float(v[4 * i + 2]) * xs * s.z;
-            f[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * xs * s.w;
-        }
-        if (p.bias) {
-            const float4* b4 = reinterpret_cast<const float4*>(p.bias + n);
+    for (int i = 0; i < 8; ++i) {
+        const float4 s = reinterpret_cast<const float4*>(col_scale)[i];
+        const float4 b = reinterpret_cast<const float4*>(col_bias)[i];
+        const float sv[4] = {s.x, s.y, s.z, s.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 b = __ldg(b4 + i);
-                f[4 * i + 0] += b.x;
-                f[4 * i + 1] += b.y;
-                f[4 * i + 2] += b.z;
-                f[4 * i + 3] += b.w;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const bool on = n + i < p.N;
-            f[i] = __uint_as_float(v[i]) * xs * (on ? __ldg(p.w_scale + n + i) : 0.0f);
-            if (p.bias && on) f[i] += __ldg(p.bias + n + i);
-        }
+        for (int j = 0; j < 4; ++j)
+            v[4 * i + j] = __float_as_uint(activate<ACT>(fmaf(__uint_as_float(v[4 * i + j]) * xs, sv[j], bv[j])));
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = activate<ACT>(f[i]);
 }
 
 // 32 outputs of one row, in the widest stores that the row's start allows (wide: 32 or 16
 // bytes; 0: one by one).
-__device__ __forceinline__ void store_chunk(const Int8Params& p, const float (&f)[32], long long row, int n, int wide) {
+__device__ __forceinline__ void store_chunk(const Int8Params& p, const uint32_t (&v)[32], long long row, int n, int wide) {
+    const auto f = [&](int i) { return __uint_as_float(v[i]); };
     const long long at = row * p.N + n;
     if (n + 32 <= p.N && wide != 0) {
         if (p.out_bf16) {
             uint32_t h[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+            for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(f(2 * i), f(2 * i + 1));
             __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
             if (wide == 32) {
 #pragma unroll
@@ -256,13 +264,13 @@ __device__ __forceinline__ void store_chunk(const Int8Params& p, const float (&f
                 for (int j = 0; j < 4; ++j) {
                     uint32_t q[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(f[8 * j + i]);
+                    for (int i = 0; i < 8; ++i) q[i] = v[8 * j + i];
                     store_v8(y + 8 * j, q);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    reinterpret_cast<float4*>(y)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                    reinterpret_cast<float4*>(y)[j] = make_float4(f(4 * j), f(4 * j + 1), f(4 * j + 2), f(4 * j + 3));
             }
         }
         return;
@@ -271,12 +279,12 @@ __device__ __forceinline__ void store_chunk(const Int8Params& p, const float (&f
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (n + i < p.N) y[i] = __float2bfloat16_rn(f[i]);
+            if (n + i < p.N) y[i] = __float2bfloat16_rn(f(i));
     } else {
         float* y = static_cast<float*>(p.y) + at;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (n + i < p.N) y[i] = f[i];
+            if (n + i < p.N) y[i] = f(i);
     }
 }
 
@@ -289,18 +297,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int8_gemm_kernel(const Int8Params p, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w) {
     using S = Shape<PAIR, BN, ALIGNED>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_addr(smem) & 1023u) {  // the swizzle's atoms; uniform, so no CTA waits for another
+        record_status(p.status, kStatusTimeoutMma, nullptr);
+        return;
+    }
     Bars b;
     uint8_t* raw = smem + S::kStages * S::kStage;
-    b.rfull = reinterpret_cast<uint64_t*>(raw + S::kRawSlots * S::kRaw);
+    float* col_scale = reinterpret_cast<float*>(raw + S::kRawSlots * S::kRaw);  // of the tile in the epilogue
+    float* col_bias = col_scale + 256;
+    b.rfull = reinterpret_cast<uint64_t*>(col_bias + 256);
     b.rempty = b.rfull + S::kRawSlots;
     b.full = b.rempty + S::kRawSlots;
     b.empty = b.full + S::kStages;
     b.tfull = b.empty + S::kStages;
     b.tempty = b.tfull + 2;
     b.drain = b.tempty + 2;
-    b.tmem_slot = reinterpret_cast<uint32_t*>(b.drain + 1);
+    b.esync = b.drain + 1;
+    b.tmem_slot = reinterpret_cast<uint32_t*>(b.esync + 1);
     b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
     volatile int* abort = b.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -316,10 +330,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kRawSlots; ++s) {
             mbar_init(&b.rfull[s], 1);
-            mbar_init(&b.rempty[s], kConverterWarps);
+            mbar_init(&b.rempty[s], kGroupWarps);
         }
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(&b.full[s], kCtas * kConverterWarps);
+            mbar_init(&b.full[s], kCtas * kGroupWarps);
             mbar_init(&b.empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -327,6 +341,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_init(&b.tempty[i], kCtas * kEpilogueWarps);
         }
         mbar_init(b.drain, 1);
+        mbar_init(b.esync, kEpilogueWarps);
         *b.abort = 0;
         fence_barrier_init();
     }
@@ -347,65 +362,57 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     if (warp < kConverterWarps) {
         // ------------------------------------------------------------ converters
-        const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+        const int group = warp / kGroupWarps;  // converts steps group, group + 2, ... into stage `group`
+        const int t = threadIdx.x & (32 * kGroupWarps - 1);
+        const int c = t & 7, r0 = t >> 3;
         Walk w{unit0, 0, 0, 0};
+        if (w.u < units) place<PAIR, BN>(w, n_tiles, rank);
+        if (group && w.u < units) advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
         if (w.u < units) {
-            place<PAIR, BN>(w, n_tiles, rank);
-            int st = 0;
             uint32_t ph = 0;
-            const auto publish = [&](const uint4(&item)[S::kItems]) {  // one stage
-                if (!mbar_wait(&b.empty[st], ph ^ 1u, abort)) {
+            uint8_t* stage = smem + group * S::kStage;
+            const auto publish = [&](const uint4(&item)[S::kItems]) {
+                if (!warp_wait(&b.empty[group], ph ^ 1u, abort)) {
                     record_status(p.status, kStatusTimeoutTransform, abort);
                     return false;
                 }
-                store_stage<PAIR, BN>(p, w, r0, c, item, smem + st * S::kStage);
+                store_stage<PAIR, BN>(p, w, r0, c, item, stage);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.full[st]), 0));
-                    else mbar_arrive(&b.full[st]);
+                    if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.full[group]), 0));
+                    else mbar_arrive(&b.full[group]);
                 }
-                if (++st == S::kStages) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                ph ^= 1u;
                 return true;
             };
             if constexpr (ALIGNED) {
-                int rs = 0;
+                int rs = group;
                 uint32_t rph = 0;
                 while (w.u < units) {
-                    if (!mbar_wait(&b.rfull[rs], rph, abort)) {
+                    if (!warp_wait(&b.rfull[rs], rph, abort)) {
                         record_status(p.status, kStatusTimeoutTransform, abort);
                         break;
                     }
                     uint4 item[S::kItems];
-                    const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + threadIdx.x;
+                    const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + t;
 #pragma unroll
                     for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 256];  // rows r0 + 32 i of x, then of w
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.rempty[rs]);
                     if (!publish(item)) break;
-                    if (++rs == S::kRawSlots) {
-                        rs = 0;
+                    if ((rs += kGroups) >= S::kRawSlots) {  // 3 or 5 slots: one wrap a turn at most
+                        rs -= S::kRawSlots;
                         rph ^= 1u;
                     }
-                    advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+                    advance2<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
                 }
             } else {
-                uint4 set0[S::kItems], set1[S::kItems];
-                load_stage<PAIR, BN>(p, w, r0, c, set0);
-                // Converts `cur`; `nxt` is in flight meanwhile.  Returns whether another step follows.
-                const auto step = [&](const uint4(&cur)[S::kItems], uint4(&nxt)[S::kItems]) {
-                    Walk nw = w;
-                    advance<PAIR, BN>(p, nw, n_tiles, units, unit_step, rank);
-                    const bool more = nw.u < units;
-                    if (more) load_stage<PAIR, BN>(p, nw, r0, c, nxt);
-                    if (!publish(cur)) return false;
-                    w = nw;
-                    return more;
-                };
-                while (step(set0, set1) && step(set1, set0)) {
+                while (w.u < units) {
+                    uint4 item[S::kItems];
+                    load_stage<PAIR, BN>(p, w, r0, c, item);
+                    if (!publish(item)) break;
+                    advance2<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
                 }
             }
         }
@@ -417,17 +424,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uintptr_t y0 = reinterpret_cast<uintptr_t>(p.y);
         const int wide = row_bytes % 32 == 0 && y0 % 32 == 0 ? 32 : (row_bytes % 16 == 0 ? 16 : 0);
         int local = 0;
+        uint32_t eph = 0;
         for (int u = unit0; u < units; u += unit_step, ++local) {
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
             const int mu = u / n_tiles, nt = u - mu * n_tiles;
             const long long row = static_cast<long long>(mu) * 128 * kCtas + rank * 128 + quarter * 32 + lane;
             const float xs = row < p.M ? __ldg(p.x_scale + row) : 0.0f;
-            if (!mbar_wait_cluster(&b.tfull[buf], use, abort)) {
+            float cs[2], cb[2];  // two columns a thread, in flight while the MMAs finish
+            const int et = threadIdx.x - 32 * kConverterWarps;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = nt * BN + et + 128 * i;
+                const bool on = et + 128 * i < BN && n < p.N;
+                cs[i] = on ? __ldg(p.w_scale + n) : 0.0f;
+                cb[i] = on && p.bias ? __ldg(p.bias + n) : 0.0f;
+            }
+            if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 break;
             }
             tc_fence_after();
+            bool in_step = epilogue_sync(b.esync, eph, abort);  // every warp is past the last tile's columns
+            if (in_step) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    col_scale[et + 128 * i] = cs[i];
+                    col_bias[et + 128 * i] = cb[i];
+                }
+                in_step = epilogue_sync(b.esync, eph, abort);
+            }
+            if (!in_step) {
+                record_status(p.status, kStatusTimeoutEpilogue, abort);
+                break;
+            }
 #pragma unroll 1
             for (int col = 0; col < BN; col += 32) {
                 const int n = nt * BN + col;
@@ -435,11 +465,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 uint32_t v[32];
                 tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + col, v);
                 tmem_ld_wait(v);
-                float f[32];
-                if (p.act == CONV_ACT_RELU) finish_chunk<CONV_ACT_RELU>(p, v, xs, n, f);
-                else if (p.act == CONV_ACT_SILU) finish_chunk<CONV_ACT_SILU>(p, v, xs, n, f);
-                else finish_chunk<CONV_ACT_NONE>(p, v, xs, n, f);
-                if (row < p.M) store_chunk(p, f, row, n, wide);
+                if (p.act == CONV_ACT_RELU) finish_chunk<CONV_ACT_RELU>(v, xs, col_scale + col, col_bias + col);
+                else if (p.act == CONV_ACT_SILU) finish_chunk<CONV_ACT_SILU>(v, xs, col_scale + col, col_bias + col);
+                else finish_chunk<CONV_ACT_NONE>(v, xs, col_scale + col, col_bias + col);
+                if (row < p.M) store_chunk(p, v, row, n, wide);
             }
             tc_fence_before();
             __syncwarp();
