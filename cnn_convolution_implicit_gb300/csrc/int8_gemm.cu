@@ -13,20 +13,27 @@
 //   1024 + u; subtracting 1152 leaves x.  One exclusive-or, two byte permutes and two
 //   packed subtractions for four values.
 //
-// Warp roles (704 threads, one CTA per SM, persistent over tiles):
-//   warps 0..15   converters, two groups that take turns by stage, so one loads or waits while
-//                 the other converts: 8-bit rows from the raw ring to FP16 values in the
-//                 128-byte-swizzle operand tiles of a stage
-//   warps 16..19  epilogue: one warp per 32-row quarter of tensor memory: scales, bias,
-//                 activation, rounding, stores from registers
-//   warp 20       tensor memory; one lane issues tcgen05.mma and commits
-//   warp 21       one lane fills the raw ring by TMA: K = 128 of both operands, 8-bit, per slot
+// Warp roles (832 threads, one CTA per SM, persistent over tiles):
+//   warps 0..15   converters, four groups that take turns by stage, so one loads, converts,
+//                 publishes or waits while the others do: 8-bit rows from the raw ring to FP16
+//                 values in the 128-byte-swizzle operand tiles of a stage
+//   warps 16..23  epilogue: two warps per 32-row quarter of tensor memory, half of the columns
+//                 each: scales, bias, activation, rounding, stores from registers
+//   warp 24       tensor memory; one lane issues tcgen05.mma and commits
+//   warp 25       one lane fills the raw ring by TMA: K = 64 of both operands, 8-bit, per slot
 // Rows that do not start on 16 bytes (K % 16) are beyond the TMA: there the converters load
 // them straight from memory (ALIGNED = false).  Loading a step ahead in registers does not
 // replace the ring: the fence that publishes a stage also waits for the loads under way
 // (8192 x 4096 x 4096 measured 413 us that way and 325 us with the ring).
-// A stage holds K = 128 of both operands as two K = 64 blocks of 128-byte rows.  Tensor
-// memory holds two accumulators, so the epilogue of one tile overlaps the next one's MMAs.
+// A stage holds K = 64 of both operands, one 128-byte FP16 row each.  Tensor memory holds two
+// accumulators, so the epilogue of one tile overlaps the next one's MMAs.
+//
+// Columns: a lane of the epilogue reads accumulator columns 8 j + 2 q + {0, 1} of two rows
+// (q = lane % 4, j = 0..7: the 16 x 256-bit shape).  The converters put weight row
+// 16 q + 2 j + {0, 1} of each 64 there, so a lane holds 16 neighbouring outputs of a row, four
+// lanes a 128-byte line of BF16, and a store instruction covers 8 whole lines.  (One row a
+// lane, 32 lines touched per instruction, cost 38 us of 133 at 200704 x 256 -> 512; its 16-byte
+// broadcast reads of the scales, four times as many as here, another 34.)
 //
 // PAIR: two SMs share a 256 x BN tile (tcgen05.mma.cta_group::2): each converts its own
 // 128 rows of x and BN / 2 rows of w.  Shared memory bounds this kernel (written by the
@@ -42,25 +49,24 @@ namespace convgb {
 
 namespace {
 
-constexpr int kGroups = 2;       // converter groups
-constexpr int kGroupWarps = 8;
+constexpr int kGroups = 4;       // converter groups
+constexpr int kGroupWarps = 4;
 constexpr int kConverterWarps = kGroups * kGroupWarps;
-constexpr int kEpilogueWarps = 4;
+constexpr int kEpilogueWarps = 8;
 constexpr int kMmaWarp = kConverterWarps + kEpilogueWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
 constexpr int kGemmThreads = 32 * (kLoadWarp + 1);
-constexpr int kStepK = 128;      // K of one stage
-constexpr int kRowBytes = 128;   // one operand row of a K = 64 block
+constexpr int kStepK = 64;       // K of one stage
+constexpr int kRowBytes = 128;   // one FP16 operand row of a stage
 
 template <bool PAIR, int BN, bool ALIGNED>
 struct Shape {
     static constexpr int kRowsB = PAIR ? BN / 2 : BN;
-    static constexpr int kBlockA = 128 * kRowBytes;      // one K = 64 block
-    static constexpr int kBlockB = kRowsB * kRowBytes;
-    static constexpr int kStage = 2 * (kBlockA + kBlockB);
+    static constexpr int kTileA = 128 * kRowBytes;
+    static constexpr int kStage = kTileA + kRowsB * kRowBytes;
+    static constexpr int kStages = kGroups;              // one for each converter group
     static constexpr int kRaw = ALIGNED ? (128 + kRowsB) * kStepK : 0;  // one slot of the raw ring
-    static constexpr int kStages = 2;  // one for each converter group
-    static constexpr int kRawSlots = ALIGNED ? (kStage >= 65536 ? 3 : 5) : 0;
+    static constexpr int kRawSlots = ALIGNED ? (kRowsB >= 128 ? 6 : 8) : 0;  // in 227 KB beside the stages
     static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 2 * 256 * 4 + 256;
@@ -124,9 +130,10 @@ __device__ __forceinline__ uint4 load_item(const int8_t* base, long long at, int
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-__device__ __forceinline__ void store_v8(void* p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+__device__ __forceinline__ void store_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                         uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+                 "r"(e), "r"(f), "r"(g), "r"(h)
                  : "memory");
 }
 
@@ -152,31 +159,53 @@ __device__ __forceinline__ bool epilogue_sync(uint64_t* bar, uint32_t& phase, vo
 // Where a converter stands: its tile and K-step.
 struct Walk {
     int u, k0;
+    int mu, nt;
     int m0, n0;  // first row of x and of w that this CTA converts
 };
 
+// The tiles of a launch, and this CTA's way through them (no division per tile).
+struct Tiles {
+    int n_tiles, units, step, step_m, step_n;
+    uint32_t rank;
+};
+
 template <bool PAIR, int BN>
-__device__ __forceinline__ void place(Walk& w, int n_tiles, uint32_t rank) {
-    const int mu = w.u / n_tiles;
-    const int nt = w.u - mu * n_tiles;
-    w.m0 = PAIR ? mu * 256 + static_cast<int>(rank) * 128 : mu * 128;
-    w.n0 = nt * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
+__device__ __forceinline__ void place(const Tiles& t, Walk& w) {
+    w.m0 = PAIR ? w.mu * 256 + static_cast<int>(t.rank) * 128 : w.mu * 128;
+    w.n0 = w.nt * BN + (PAIR ? static_cast<int>(t.rank) * (BN / 2) : 0);
 }
 
 template <bool PAIR, int BN>
-__device__ __forceinline__ void advance(const Int8Params& p, Walk& w, int n_tiles, int units, int unit_step, uint32_t rank) {
-    w.k0 += kStepK;
-    if (w.k0 >= p.K) {
-        w.k0 = 0;
-        w.u += unit_step;
-        if (w.u < units) place<PAIR, BN>(w, n_tiles, rank);
+__device__ __forceinline__ Walk walk_from(const Tiles& t, int unit0) {
+    Walk w;
+    w.u = unit0;
+    w.k0 = 0;
+    w.mu = unit0 / t.n_tiles;
+    w.nt = unit0 - w.mu * t.n_tiles;
+    place<PAIR, BN>(t, w);
+    return w;
+}
+
+__device__ __forceinline__ void next_unit(const Tiles& t, Walk& w) {
+    w.u += t.step;
+    w.mu += t.step_m;
+    w.nt += t.step_n;
+    if (w.nt >= t.n_tiles) {
+        w.nt -= t.n_tiles;
+        ++w.mu;
     }
 }
 
 template <bool PAIR, int BN>
-__device__ __forceinline__ void advance2(const Int8Params& p, Walk& w, int n_tiles, int units, int unit_step, uint32_t rank) {
-    advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
-    if (w.u < units) advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+__device__ __forceinline__ void advance(const Int8Params& p, const Tiles& t, Walk& w, int steps) {
+    for (int i = 0; i < steps && w.u < t.units; ++i) {
+        w.k0 += kStepK;
+        if (w.k0 >= p.K) {
+            w.k0 = 0;
+            next_unit(t, w);
+            place<PAIR, BN>(t, w);
+        }
+    }
 }
 
 template <bool PAIR, int BN>
@@ -200,91 +229,134 @@ __device__ __forceinline__ void load_stage(const Int8Params& p, const Walk& w, i
     }
 }
 
+// The stage's row (accumulator column) of weight row n: columns 16 q + 2 j + e of each 64 sit at
+// 8 j + 2 q + e.  Tiles of 32 columns: the same with 8 neighbours a lane, j = 0..3.
+template <int BN>
+__device__ __forceinline__ int column_of(int n) {
+    if constexpr (BN >= 64) return (n & ~63) | ((n & 14) << 2) | ((n & 48) >> 3) | (n & 1);
+    else return ((n & 6) << 2) | ((n & 24) >> 2) | (n & 1);
+}
+
 template <bool PAIR, int BN>
 __device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c,
                                             const uint4 (&item)[Shape<PAIR, BN, false>::kItems], uint8_t* stage) {
     using S = Shape<PAIR, BN, false>;
-    const int kb = c >> 2;
-    const int first = (c & 3) * 2;  // the item's two 16-byte chunks of the FP16 row
-    const int swap = kb;            // a warp's lanes 4..7 (of 8) write their upper half first: 8 lanes, 8 bank groups
 #pragma unroll
     for (int i = 0; i < S::kItems; ++i) {
-        const int row = r0 + 32 * (i < 4 ? i : i - 4);
+        int row = r0 + 32 * (i < 4 ? i : i - 4);
         if (i < 4 ? w.m0 + row >= p.M : w.n0 + row >= p.N) continue;
         const uint2 a = to_half4(item[i].x), b = to_half4(item[i].y), d = to_half4(item[i].z), e = to_half4(item[i].w);
-        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
-        uint8_t* dst = stage + (i < 4 ? kb * S::kBlockA : 2 * S::kBlockA + kb * S::kBlockB) + row * kRowBytes;
-        const int sw = row & 7;
-        *reinterpret_cast<uint4*>(dst + (((first + swap) ^ sw) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + (((first + 1 - swap) ^ sw) << 4)) = swap ? lo : hi;
+        if (i >= 4) row = column_of<BN>(row);
+        uint8_t* dst = stage + (i < 4 ? 0 : S::kTileA) + row * kRowBytes;
+        const int sw = row & 7;  // eight lanes: four chunks of two rows, eight bank groups
+        *reinterpret_cast<uint4*>(dst + (((2 * c) ^ sw) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ sw) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
     }
 }
 
-// Scales, bias and activation of 32 columns of one row, in place.
+// 16 lanes (rows) x 64 columns of tensor memory: register 4 j + 2 h + e of a lane is row
+// lane / 4 + 8 h, column 8 j + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// The same with 32 columns, in the first 16 registers.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 16; i < 32; ++i) r[i] = 0;
+}
+
+// Scale, bias and activation of two neighbouring columns of one row, in place, as packed FP32.
 template <int ACT>
-__device__ __forceinline__ void finish_chunk(uint32_t (&v)[32], float xs, const float* col_scale, const float* col_bias) {
+__device__ __forceinline__ void finish_two(uint32_t& lo, uint32_t& hi, uint64_t xs2, uint64_t ws2, uint64_t bias2) {
+    asm("{\n\t.reg .b64 t;\n\t"
+        "mov.b64 t, {%0, %1};\n\t"
+        "mul.rn.f32x2 t, t, %2;\n\t"
+        "fma.rn.f32x2 t, t, %3, %4;\n\t"
+        "mov.b64 {%0, %1}, t;\n\t}"
+        : "+r"(lo), "+r"(hi)
+        : "l"(xs2), "l"(ws2), "l"(bias2));
+    lo = __float_as_uint(activate<ACT>(__uint_as_float(lo)));
+    hi = __float_as_uint(activate<ACT>(__uint_as_float(hi)));
+}
+
+// A lane's part of 16 rows x 64 columns: 16 neighbouring columns of two rows (J = 8), or 8 of them
+// where a tile has 32 columns (J = 4).
+template <int ACT, int J>
+__device__ __forceinline__ void finish_block(uint32_t (&v)[32], float xs_lo, float xs_hi, const float* scale,
+                                             const float* bias) {
+    uint64_t lo2, hi2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(lo2) : "f"(xs_lo));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(hi2) : "f"(xs_hi));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 s = reinterpret_cast<const float4*>(col_scale)[i];
-        const float4 b = reinterpret_cast<const float4*>(col_bias)[i];
-        const float sv[4] = {s.x, s.y, s.z, s.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[4 * i + j] = __float_as_uint(activate<ACT>(fmaf(__uint_as_float(v[4 * i + j]) * xs, sv[j], bv[j])));
+    for (int j = 0; j < J; j += 2) {
+        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(scale + 2 * j);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bias + 2 * j);
+        finish_two<ACT>(v[4 * j], v[4 * j + 1], lo2, s.x, b.x);
+        finish_two<ACT>(v[4 * j + 2], v[4 * j + 3], hi2, s.x, b.x);
+        finish_two<ACT>(v[4 * j + 4], v[4 * j + 5], lo2, s.y, b.y);
+        finish_two<ACT>(v[4 * j + 6], v[4 * j + 7], hi2, s.y, b.y);
     }
 }
 
-// 32 outputs of one row, in the widest stores that the row's start allows (wide: 32 or 16
-// bytes; 0: one by one).
-__device__ __forceinline__ void store_chunk(const Int8Params& p, const uint32_t (&v)[32], long long row, int n, int wide) {
-    const auto f = [&](int i) { return __uint_as_float(v[i]); };
-    const long long at = row * p.N + n;
-    if (n + 32 <= p.N && wide != 0) {
+// 2 J neighbouring outputs of row h of a lane's two, in the widest stores that every row's start
+// allows (wide: 32 or 16 bytes; 0: one by one).
+template <int J>
+__device__ __forceinline__ void store_row(const Int8Params& p, const uint32_t (&v)[32], int h, long long row, int n, int wide) {
+    const auto at = [&](int i) { return v[4 * (i >> 1) + 2 * h + (i & 1)]; };  // column n + i
+    const long long o = row * p.N + n;
+    if (n + 2 * J <= p.N && wide != 0) {
         if (p.out_bf16) {
-            uint32_t h[16];
+            uint32_t q[J];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(f(2 * i), f(2 * i + 1));
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
-            if (wide == 32) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t q[8] = {h[8 * j], h[8 * j + 1], h[8 * j + 2], h[8 * j + 3],
-                                           h[8 * j + 4], h[8 * j + 5], h[8 * j + 6], h[8 * j + 7]};
-                    store_v8(y + 16 * j, q);
-                }
+            for (int i = 0; i < J; ++i) q[i] = pack_bf16x2(__uint_as_float(at(2 * i)), __uint_as_float(at(2 * i + 1)));
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
+            if (J == 8 && wide == 32) {
+                store_v8(y, q[0], q[1], q[2], q[3], q[4 % J], q[5 % J], q[6 % J], q[7 % J]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<uint4*>(y)[j] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+                for (int i = 0; i < J / 4; ++i)
+                    reinterpret_cast<uint4*>(y)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
             }
         } else {
-            float* y = static_cast<float*>(p.y) + at;
+            float* y = static_cast<float*>(p.y) + o;
             if (wide == 32) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t q[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) q[i] = v[8 * j + i];
-                    store_v8(y + 8 * j, q);
-                }
+                for (int i = 0; i < 2 * J; i += 8)
+                    store_v8(y + i, at(i), at(i + 1), at(i + 2), at(i + 3), at(i + 4), at(i + 5), at(i + 6), at(i + 7));
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    reinterpret_cast<float4*>(y)[j] = make_float4(f(4 * j), f(4 * j + 1), f(4 * j + 2), f(4 * j + 3));
+                for (int i = 0; i < 2 * J; i += 4)
+                    *reinterpret_cast<uint4*>(y + i) = make_uint4(at(i), at(i + 1), at(i + 2), at(i + 3));
             }
         }
         return;
     }
     if (p.out_bf16) {
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + at;
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (n + i < p.N) y[i] = __float2bfloat16_rn(f(i));
+        for (int i = 0; i < 2 * J; ++i)
+            if (n + i < p.N) y[i] = __float2bfloat16_rn(__uint_as_float(at(i)));
     } else {
-        float* y = static_cast<float*>(p.y) + at;
+        float* y = static_cast<float*>(p.y) + o;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (n + i < p.N) y[i] = f(i);
+        for (int i = 0; i < 2 * J; ++i)
+            if (n + i < p.N) y[i] = __uint_as_float(at(i));
     }
 }
 
@@ -322,9 +394,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool leader = rank == 0;
     constexpr int kCtas = PAIR ? 2 : 1;
 
-    const int n_tiles = (p.N + BN - 1) / BN;
-    const int units = ((p.M + 128 * kCtas - 1) / (128 * kCtas)) * n_tiles;
-    const int unit0 = static_cast<int>(blockIdx.x) / kCtas, unit_step = static_cast<int>(gridDim.x) / kCtas;
+    Tiles tiles;
+    tiles.n_tiles = (p.N + BN - 1) / BN;
+    tiles.units = ((p.M + 128 * kCtas - 1) / (128 * kCtas)) * tiles.n_tiles;
+    tiles.step = static_cast<int>(gridDim.x) / kCtas;
+    tiles.step_m = tiles.step / tiles.n_tiles;
+    tiles.step_n = tiles.step - tiles.step_m * tiles.n_tiles;
+    tiles.rank = rank;
+    const int unit0 = static_cast<int>(blockIdx.x) / kCtas, units = tiles.units, unit_step = tiles.step;
     const int ksteps = (p.K + kStepK - 1) / kStepK;
 
     if (threadIdx.x == 0) {
@@ -362,16 +439,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     if (warp < kConverterWarps) {
         // ------------------------------------------------------------ converters
-        const int group = warp / kGroupWarps;  // converts steps group, group + 2, ... into stage `group`
+        const int group = warp / kGroupWarps;  // converts steps group, group + kGroups, ... into stage `group`
         const int t = threadIdx.x & (32 * kGroupWarps - 1);
-        const int c = t & 7, r0 = t >> 3;
-        Walk w{unit0, 0, 0, 0};
-        if (w.u < units) place<PAIR, BN>(w, n_tiles, rank);
-        if (group && w.u < units) advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+        const int c = t & 3, r0 = t >> 2;
+        Walk w = walk_from<PAIR, BN>(tiles, unit0);
+        advance<PAIR, BN>(p, tiles, w, group);
         if (w.u < units) {
             uint32_t ph = 0;
             uint8_t* stage = smem + group * S::kStage;
-            const auto publish = [&](const uint4(&item)[S::kItems]) {
+            const auto publish = [&](uint4(&item)[S::kItems]) {
                 if (!warp_wait(&b.empty[group], ph ^ 1u, abort)) {
                     record_status(p.status, kStatusTimeoutTransform, abort);
                     return false;
@@ -397,49 +473,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     uint4 item[S::kItems];
                     const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + t;
 #pragma unroll
-                    for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 256];  // rows r0 + 32 i of x, then of w
+                    for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 128];  // rows r0 + 32 i of x, then of w
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.rempty[rs]);
                     if (!publish(item)) break;
-                    if ((rs += kGroups) >= S::kRawSlots) {  // 3 or 5 slots: one wrap a turn at most
+                    if ((rs += kGroups) >= S::kRawSlots) {  // more slots than groups: one wrap a turn at most
                         rs -= S::kRawSlots;
                         rph ^= 1u;
                     }
-                    advance2<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+                    advance<PAIR, BN>(p, tiles, w, kGroups);
                 }
             } else {
                 while (w.u < units) {
                     uint4 item[S::kItems];
                     load_stage<PAIR, BN>(p, w, r0, c, item);
                     if (!publish(item)) break;
-                    advance2<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+                    advance<PAIR, BN>(p, tiles, w, kGroups);
                 }
             }
         }
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3;
+        const int half = (warp - kConverterWarps) >> 2;
         const int es = p.out_bf16 ? 2 : 4;
         const long long row_bytes = static_cast<long long>(p.N) * es;
         const uintptr_t y0 = reinterpret_cast<uintptr_t>(p.y);
         const int wide = row_bytes % 32 == 0 && y0 % 32 == 0 ? 32 : (row_bytes % 16 == 0 ? 16 : 0);
         int local = 0;
         uint32_t eph = 0;
-        for (int u = unit0; u < units; u += unit_step, ++local) {
+        constexpr int J = BN >= 64 ? 8 : 4;        // pairs of columns a lane holds of a row
+        constexpr int kCols = BN >= 128 ? BN / 2 : BN;  // columns of a warp; narrow tiles: 16 of its quarter's 32 rows
+        const int col0 = BN >= 128 ? half * kCols : 0;
+        for (Walk w = walk_from<PAIR, BN>(tiles, unit0); w.u < units; next_unit(tiles, w), ++local) {
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
-            const int mu = u / n_tiles, nt = u - mu * n_tiles;
-            const long long row = static_cast<long long>(mu) * 128 * kCtas + rank * 128 + quarter * 32 + lane;
-            const float xs = row < p.M ? __ldg(p.x_scale + row) : 0.0f;
-            float cs[2], cb[2];  // two columns a thread, in flight while the MMAs finish
-            const int et = threadIdx.x - 32 * kConverterWarps;
+            const int nt = w.nt;
+            const long long row0 = static_cast<long long>(w.mu) * 128 * kCtas + rank * 128 + quarter * 32 + (lane >> 2);
+            float xs[4];  // rows row0, + 8, + 16, + 24
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = nt * BN + et + 128 * i;
-                const bool on = et + 128 * i < BN && n < p.N;
-                cs[i] = on ? __ldg(p.w_scale + n) : 0.0f;
-                cb[i] = on && p.bias ? __ldg(p.bias + n) : 0.0f;
-            }
+            for (int i = 0; i < 4; ++i) xs[i] = row0 + 8 * i < p.M ? __ldg(p.x_scale + row0 + 8 * i) : 0.0f;
+            const int et = threadIdx.x - 32 * kConverterWarps;  // a column a thread, in flight while the MMAs finish
+            const bool on = et < BN && nt * BN + et < p.N;
+            const float cs = on ? __ldg(p.w_scale + nt * BN + et) : 0.0f;
+            const float cb = on && p.bias ? __ldg(p.bias + nt * BN + et) : 0.0f;
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 break;
@@ -447,28 +524,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tc_fence_after();
             bool in_step = epilogue_sync(b.esync, eph, abort);  // every warp is past the last tile's columns
             if (in_step) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    col_scale[et + 128 * i] = cs[i];
-                    col_bias[et + 128 * i] = cb[i];
-                }
+                col_scale[et] = cs;
+                col_bias[et] = cb;
                 in_step = epilogue_sync(b.esync, eph, abort);
             }
             if (!in_step) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 break;
             }
+            const int mine = (lane & 3) * 2 * J;  // this lane's first column of a block
 #pragma unroll 1
-            for (int col = 0; col < BN; col += 32) {
-                const int n = nt * BN + col;
-                if (n >= p.N) break;
-                uint32_t v[32];
-                tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + col, v);
-                tmem_ld_wait(v);
-                if (p.act == CONV_ACT_RELU) finish_chunk<CONV_ACT_RELU>(v, xs, col_scale + col, col_bias + col);
-                else if (p.act == CONV_ACT_SILU) finish_chunk<CONV_ACT_SILU>(v, xs, col_scale + col, col_bias + col);
-                else finish_chunk<CONV_ACT_NONE>(v, xs, col_scale + col, col_bias + col);
-                if (row < p.M) store_chunk(p, v, row, n, wide);
+            for (int col = col0; col < col0 + kCols; col += 8 * J) {
+                if (nt * BN + col >= p.N) break;
+                const int n = nt * BN + col + mine;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {  // 16 rows at a time
+                    if (BN < 128 && g != half) continue;
+                    uint32_t v[32];
+                    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32 + 16 * g) << 16) + buf * BN + col;
+                    if constexpr (J == 8) tmem_ld_16x64(at, v);
+                    else tmem_ld_16x32(at, v);
+                    tmem_ld_wait(v);
+                    const float* sc = col_scale + col + mine;
+                    const float* bi = col_bias + col + mine;
+                    if (p.act == CONV_ACT_RELU) finish_block<CONV_ACT_RELU, J>(v, xs[2 * g], xs[2 * g + 1], sc, bi);
+                    else if (p.act == CONV_ACT_SILU) finish_block<CONV_ACT_SILU, J>(v, xs[2 * g], xs[2 * g + 1], sc, bi);
+                    else finish_block<CONV_ACT_NONE, J>(v, xs[2 * g], xs[2 * g + 1], sc, bi);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const long long row = row0 + 16 * g + 8 * h;
+                        if (row < p.M && n < p.N) store_row<J>(p, v, h, row, n, wide);
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -480,9 +567,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ raw ring
         if constexpr (ALIGNED) {
-            Walk w{unit0, 0, 0, 0};
+            Walk w = walk_from<PAIR, BN>(tiles, unit0);
             if (lane == 0 && w.u < units) {
-                place<PAIR, BN>(w, n_tiles, rank);
                 long long issued = 0;
                 int rs = 0;
                 uint32_t ph = 0;
@@ -500,7 +586,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         rs = 0;
                         ph ^= 1u;
                     }
-                    advance<PAIR, BN>(p, w, n_tiles, units, unit_step, rank);
+                    advance<PAIR, BN>(p, tiles, w, 1);
                 }
                 for (int s = 0; s < S::kRawSlots; ++s) {  // no copy in flight when the CTA leaves
                     const long long fills = issued / S::kRawSlots + (s < issued % S::kRawSlots ? 1 : 0);
@@ -533,12 +619,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_fence_after();
                 const uint32_t base = smem_addr(smem + st * S::kStage);
                 const int left = (p.K - ks * kStepK + 15) >> 4;
-                const int mmas = left < 8 ? left : 8;
+                const int mmas = left < 4 ? left : 4;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     if (j >= mmas) break;
-                    const uint64_t da = sdesc_sw128(base + (j >> 2) * S::kBlockA) + (j & 3) * 2;
-                    const uint64_t db = sdesc_sw128(base + 2 * S::kBlockA + (j >> 2) * S::kBlockB) + (j & 3) * 2;
+                    const uint64_t da = sdesc_sw128(base) + 2 * j;
+                    const uint64_t db = sdesc_sw128(base + S::kTileA) + 2 * j;
                     const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
                     if constexpr (PAIR) mma_bf16_pair(d, da, db, idesc, acc);  // kind::f16; idesc names the type
                     else mma_bf16(d, da, db, idesc, acc);
