@@ -32,26 +32,8 @@ conv_status check_device(const conv_int8_plan* pl) {
     return cur == pl->device ? CONV_OK : CONV_ERR_INVALID_ARG;
 }
 
-size_t up(size_t v, size_t to) { return (v + to - 1) / to * to; }
-
-// Workspace: FP16 weights, then x with rows on 16 bytes (both for the tensor-core form only), then
-// the 8-bit rows and scales of a call that quantises (rows on 16 bytes too for that form).
-struct Workspace {
-    size_t weights, x_rows, rows, scales;  // offsets
-    size_t forward, quantize;              // bytes of either call
-};
-
-Workspace workspace_of(const Int8Params& p) {
-    const bool gemm = int8_use_gemm(p);
-    Workspace w;
-    w.weights = 0;
-    w.x_rows = gemm ? up(up(p.N, 64) * p.pitch * 2, 256) : 0;
-    w.rows = w.x_rows;
-    w.forward = w.x_rows + (gemm && p.K % 16 != 0 ? up(static_cast<size_t>(p.M) * p.pitch, 256) : 0);
-    w.scales = w.rows + up(static_cast<size_t>(p.M) * (gemm ? p.pitch : p.K), 256);
-    w.quantize = w.scales + static_cast<size_t>(p.M) * sizeof(float);
-    return w;
-}
+// The 8-bit rows of a call that quantises: [M][K] integers, rounded up to 16 bytes, then [M] scales.
+size_t rows_bytes(const Int8Params& p) { return (static_cast<size_t>(p.M) * p.K + 15) & ~static_cast<size_t>(15); }
 
 conv_status launched(cudaError_t e) {
     if (e == cudaSuccess) return CONV_OK;
@@ -82,7 +64,6 @@ conv_status conv_int8_plan_create(conv_int8_plan** out, int M, int N, int K, con
     p.K = K;
     p.out_bf16 = out_dtype == CONV_BF16;
     p.act = act;
-    p.pitch = (K + 15) & ~15;
     pl->status_slot = -1;
     int ndev = 0;
     if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
@@ -101,38 +82,27 @@ conv_status conv_int8_plan_create(conv_int8_plan** out, int M, int N, int K, con
 }
 
 conv_status conv_int8_forward(conv_int8_plan* pl, const void* x, const float* x_scale, const void* w,
-                              const float* w_scale, const float* bias, void* y, void* workspace, void* stream) {
+                              const float* w_scale, const float* bias, void* y, void* stream) {
     if (pl == nullptr || x == nullptr || x_scale == nullptr || w == nullptr || w_scale == nullptr || y == nullptr)
         return CONV_ERR_INVALID_ARG;
-    const Workspace ws = workspace_of(pl->ip);
-    if (ws.forward != 0 && workspace == nullptr) return CONV_ERR_INVALID_ARG;
     for (const void* ptr : {x, static_cast<const void*>(x_scale), w, static_cast<const void*>(w_scale),
-                            static_cast<const void*>(bias), static_cast<const void*>(y),
-                            static_cast<const void*>(workspace)})
+                            static_cast<const void*>(bias), static_cast<const void*>(y)})
         if (ptr != nullptr && !aligned16(ptr)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
     Int8Params p = pl->ip;
     p.x = static_cast<const int8_t*>(x);
-    p.x_pitch = p.K;
     p.x_scale = x_scale;
     p.w = static_cast<const int8_t*>(w);
     p.w_scale = w_scale;
     p.bias = bias;
     p.y = y;
-    if (ws.forward != 0) {
-        uint8_t* base = static_cast<uint8_t*>(workspace);
-        p.w_rows = reinterpret_cast<uint16_t*>(base + ws.weights);
-        p.x_rows = p.K % 16 != 0 ? reinterpret_cast<int8_t*>(base + ws.x_rows) : nullptr;
-    }
     return launched(launch_int8_product(p, pl->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
-conv_status conv_int8_workspace(const conv_int8_plan* p, unsigned long long* forward, unsigned long long* quantize) {
-    if (p == nullptr) return CONV_ERR_INVALID_ARG;
-    const Workspace ws = workspace_of(p->ip);
-    if (forward) *forward = ws.forward;
-    if (quantize) *quantize = ws.quantize;
+conv_status conv_int8_workspace(const conv_int8_plan* p, unsigned long long* bytes) {
+    if (p == nullptr || bytes == nullptr) return CONV_ERR_INVALID_ARG;
+    *bytes = rows_bytes(p->ip) + static_cast<size_t>(p->ip.M) * sizeof(float);
     return CONV_OK;
 }
 
@@ -148,20 +118,15 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
     Int8Params p = pl->ip;
-    const Workspace ws = workspace_of(p);
-    uint8_t* base = static_cast<uint8_t*>(workspace);
-    int8_t* q = reinterpret_cast<int8_t*>(base + ws.rows);
-    float* scale = reinterpret_cast<float*>(base + ws.scales);
-    const int pitch = int8_use_gemm(p) ? p.pitch : p.K;
+    int8_t* q = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(q + rows_bytes(p));
     p.x = q;
     p.x_scale = scale;
-    p.x_pitch = pitch;
-    p.w_rows = reinterpret_cast<uint16_t*>(base + ws.weights);
     p.w = static_cast<const int8_t*>(w);
     p.w_scale = w_scale;
     p.bias = bias;
     p.y = y;
-    const cudaError_t e = launch_quantize_rows(x, x_dtype == CONV_BF16, p.M, p.K, pitch, q, scale, pl->num_sms,
+    const cudaError_t e = launch_quantize_rows(x, x_dtype == CONV_BF16, p.M, p.K, q, scale, pl->num_sms,
                                                static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return launched(e);
     return launched(launch_int8_product(p, pl->num_sms, static_cast<cudaStream_t>(stream)));
@@ -191,7 +156,7 @@ conv_status conv_quantize_rows(const void* x, conv_dtype dtype, int M, int K, vo
         cudaGetLastError();
         return CONV_ERR_CUDA;
     }
-    return launched(launch_quantize_rows(x, dtype == CONV_BF16, M, K, K, static_cast<int8_t*>(q), scale, sms,
+    return launched(launch_quantize_rows(x, dtype == CONV_BF16, M, K, static_cast<int8_t*>(q), scale, sms,
                                          static_cast<cudaStream_t>(stream)));
 }
 

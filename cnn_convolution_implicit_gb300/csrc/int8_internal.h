@@ -14,29 +14,21 @@ struct Int8Params {
     int M, N, K;
     int out_bf16;  // y BF16 (else FP32)
     int act;       // conv_act
-    const int8_t* x;  // rows x_pitch bytes apart
-    int x_pitch;
+    const int8_t* x;
     const float* x_scale;
     const int8_t* w;
     const float* w_scale;
     const float* bias;  // nullptr: 0
     void* y;
-    // tensor-core form: operands laid out in the workspace
-    uint16_t* w_rows;  // FP16 weights [N rounded up to 64][pitch]
-    int8_t* x_rows;    // x with rows on 16 bytes [M][pitch], nullptr where x has them itself
-    int pitch;         // K rounded up to 16
     unsigned* status;
 };
-// Whether a product runs on the tensor cores (else on the CUDA cores, without a workspace).
-bool int8_use_gemm(const Int8Params& p);
-cudaError_t launch_int8_layout(const Int8Params& p, int num_sms, cudaStream_t stream);
 // Tensor-core kernel (int8_gemm.cu); whether its tile counts stay within 32 bits.
 bool int8_gemm_fits(const Int8Params& p);
 cudaError_t launch_int8_gemm(const Int8Params& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_int8_product(const Int8Params& p, int num_sms, cudaStream_t stream);
 
-// Rows of x (BF16 or FP32) to 8 bits with one scale each; rows of q `pitch` bytes apart.
-cudaError_t launch_quantize_rows(const void* x, bool bf16, int M, int K, int pitch, int8_t* q, float* scale, int num_sms,
+// Rows of x (BF16 or FP32) to 8 bits with one scale each.
+cudaError_t launch_quantize_rows(const void* x, bool bf16, int M, int K, int8_t* q, float* scale, int num_sms,
                                  cudaStream_t stream);
 
 }  // namespace convgb

@@ -14,7 +14,7 @@ __global__ void int8_plain_kernel(const Int8Params p) {
     const int n = blockIdx.x * 32 + threadIdx.x;
     for (long long m = static_cast<long long>(blockIdx.y) * 8 + threadIdx.y; m < p.M; m += gridDim.y * 8LL) {
         if (n >= p.N) return;
-        const int8_t* x = p.x + m * p.x_pitch;
+        const int8_t* x = p.x + m * p.K;
         const int8_t* w = p.w + static_cast<long long>(n) * p.K;
         int acc = 0;
         for (int k = 0; k < p.K; ++k) acc += static_cast<int>(x[k]) * static_cast<int>(w[k]);
@@ -29,13 +29,8 @@ __global__ void int8_plain_kernel(const Int8Params p) {
 
 }  // namespace
 
-bool int8_use_gemm(const Int8Params& p) { return p.M > 8 && int8_gemm_fits(p); }
-
 cudaError_t launch_int8_product(const Int8Params& p, int num_sms, cudaStream_t stream) {
-    if (int8_use_gemm(p)) {
-        const cudaError_t e = launch_int8_layout(p, num_sms, stream);
-        return e != cudaSuccess ? e : launch_int8_gemm(p, num_sms, stream);
-    }
+    if (p.M > 8 && int8_gemm_fits(p)) return launch_int8_gemm(p, num_sms, stream);
     const int rows = (p.M + 7) / 8;
     const dim3 grid((p.N + 31) / 32, rows < 65535 ? rows : 65535), block(32, 8);
     if (p.act == CONV_ACT_RELU) int8_plain_kernel<CONV_ACT_RELU><<<grid, block, 0, stream>>>(p);

@@ -55,11 +55,6 @@ def _handle(stream, device):
     return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
-def _workspace(nbytes, device):
-    import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
 def _check(status, what):
     if status != 0:
         raise ConvError(status, what)
@@ -108,6 +103,10 @@ class GroupNormPlan:
         if stats is not None:
             _need(stats, "stats", self.stats_shape, torch.float32, x.device)
 
+    def _workspace(self, device):
+        import torch
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+
     def forward(self, x, gamma=None, beta=None, y=None, stats=None, stream=None):
         """act(norm(x)); ``stats`` (empty_stats()) receives what backward() reads."""
         import torch
@@ -118,7 +117,7 @@ class GroupNormPlan:
                 y = torch.empty_like(x)
             else:
                 _need(y, "y", self.shape, self.torch_dtype, x.device)
-            ws = _workspace(self.workspace_bytes, x.device)
+            ws = self._workspace(x.device)
             _check(lib().conv_group_norm_forward(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(),
                                                  _ptr(stats), ws.data_ptr(), _handle(stream, x.device)),
                    "conv_group_norm_forward")
@@ -141,7 +140,7 @@ class GroupNormPlan:
                 scale = torch.empty(N * H * W, dtype=torch.float32, device=x.device)
             else:
                 _need(scale, "scale", (N * H * W,), torch.float32, x.device)
-            ws = _workspace(self.workspace_bytes, x.device)
+            ws = self._workspace(x.device)
             _check(lib().conv_group_norm_forward_int8(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), q.data_ptr(),
                                                       scale.data_ptr(), _ptr(stats), ws.data_ptr(),
                                                       _handle(stream, x.device)),
@@ -168,7 +167,7 @@ class GroupNormPlan:
                 else:
                     _need(t, name, (self.C,), torch.float32, x.device)
                 grads.append(t)
-            ws = _workspace(self.workspace_bytes, x.device)
+            ws = self._workspace(x.device)
             _check(lib().conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(),
                                                   _ptr(gamma), _ptr(beta), dx.data_ptr(), grads[0].data_ptr(),
                                                   grads[1].data_ptr(), ws.data_ptr(), _handle(stream, x.device)),
@@ -194,9 +193,9 @@ class Int8MatmulPlan:
         self._plan = h
         self.M, self.N, self.K, self.out, self.act = M, N, K, out, act
         self.torch_dtype = _torch_dtypes()[out]
-        a, b = ctypes.c_ulonglong(), ctypes.c_ulonglong()
-        _check(L.conv_int8_workspace(h, ctypes.byref(a), ctypes.byref(b)), "conv_int8_workspace")
-        self.workspace_bytes, self.workspace_bytes_quantize = a.value, b.value
+        b = ctypes.c_ulonglong()
+        _check(L.conv_int8_workspace(h, ctypes.byref(b)), "conv_int8_workspace")
+        self.workspace_bytes = b.value
 
     def close(self):
         if self._plan is not None and binding._lib is not None:
@@ -233,10 +232,8 @@ class Int8MatmulPlan:
         stream, scope = _on(stream)
         with scope:
             y = self._output(y, x.device)
-            ws = _workspace(self.workspace_bytes, x.device)
             _check(lib().conv_int8_forward(self._plan, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
-                                           w_scale.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(ws),
-                                           _handle(stream, x.device)),
+                                           w_scale.data_ptr(), _ptr(bias), y.data_ptr(), _handle(stream, x.device)),
                    "conv_int8_forward")
         return y
 
@@ -251,7 +248,7 @@ class Int8MatmulPlan:
         stream, scope = _on(stream)
         with scope:
             y = self._output(y, x.device)
-            ws = _workspace(self.workspace_bytes_quantize, x.device)
+            ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=x.device) if self.workspace_bytes else None
             _check(lib().conv_int8_forward_quantize(self._plan, x.data_ptr(),
                                                     CONV_BF16 if x.dtype == torch.bfloat16 else CONV_F32,
                                                     w.data_ptr(), w_scale.data_ptr(), _ptr(bias), y.data_ptr(),
