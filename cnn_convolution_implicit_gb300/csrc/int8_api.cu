@@ -64,6 +64,10 @@ conv_status conv_int8_plan_create(conv_int8_plan** out, int M, int N, int K, con
     p.K = K;
     p.out_bf16 = out_dtype == CONV_BF16;
     p.act = act;
+    if (int8_use_gemm(p) && !int8_gemm_fits(p)) {
+        delete pl;
+        return CONV_ERR_UNSUPPORTED;
+    }
     pl->status_slot = -1;
     int ndev = 0;
     if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
@@ -102,14 +106,15 @@ conv_status conv_int8_forward(conv_int8_plan* pl, const void* x, const float* x_
 
 conv_status conv_int8_workspace(const conv_int8_plan* p, unsigned long long* bytes) {
     if (p == nullptr || bytes == nullptr) return CONV_ERR_INVALID_ARG;
-    *bytes = rows_bytes(p->ip) + static_cast<size_t>(p->ip.M) * sizeof(float);
+    *bytes = int8_use_gemm(p->ip) ? rows_bytes(p->ip) + static_cast<size_t>(p->ip.M) * sizeof(float) : 0;
     return CONV_OK;
 }
 
 conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_dtype x_dtype, const void* w,
                                        const float* w_scale, const float* bias, void* y, void* workspace,
                                        void* stream) {
-    if (pl == nullptr || x == nullptr || w == nullptr || w_scale == nullptr || y == nullptr || workspace == nullptr)
+    if (pl == nullptr || x == nullptr || w == nullptr || w_scale == nullptr || y == nullptr ||
+        (workspace == nullptr && int8_use_gemm(pl->ip)))
         return CONV_ERR_INVALID_ARG;
     if (x_dtype != CONV_F32 && x_dtype != CONV_BF16) return CONV_ERR_INVALID_ARG;
     for (const void* ptr : {x, w, static_cast<const void*>(w_scale), static_cast<const void*>(bias),
@@ -118,14 +123,16 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
     Int8Params p = pl->ip;
-    int8_t* q = static_cast<int8_t*>(workspace);
-    float* scale = reinterpret_cast<float*>(q + rows_bytes(p));
-    p.x = q;
-    p.x_scale = scale;
     p.w = static_cast<const int8_t*>(w);
     p.w_scale = w_scale;
     p.bias = bias;
     p.y = y;
+    if (!int8_use_gemm(p))
+        return launched(launch_int8_few_quantize(p, x, x_dtype == CONV_BF16, static_cast<cudaStream_t>(stream)));
+    int8_t* q = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(q + rows_bytes(p));
+    p.x = q;
+    p.x_scale = scale;
     const cudaError_t e = launch_quantize_rows(x, x_dtype == CONV_BF16, p.M, p.K, q, scale, pl->num_sms,
                                                static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return launched(e);

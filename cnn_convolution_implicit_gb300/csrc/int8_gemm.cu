@@ -29,11 +29,11 @@
 // accumulators, so the epilogue of one tile overlaps the next one's MMAs.
 //
 // Columns: a lane of the epilogue reads accumulator columns 8 j + 2 q + {0, 1} of two rows
-// (q = lane % 4, j = 0..7: the 16 x 256-bit shape).  The converters put weight row
-// 16 q + 2 j + {0, 1} of each 64 there, so a lane holds 16 neighbouring outputs of a row, four
-// lanes a 128-byte line of BF16, and a store instruction covers 8 whole lines.  (One row a
-// lane, 32 lines touched per instruction, cost 38 us of 133 at 200704 x 256 -> 512; its 16-byte
-// broadcast reads of the scales, four times as many as here, another 34.)
+// (q = lane % 4, j = 0..3: the 16 x 256-bit shape).  The converters put weight row
+// 8 q + 2 j + {0, 1} of each 32 there, so a lane holds 8 neighbouring outputs of a row, four
+// lanes 64 bytes of BF16, and a store instruction touches 8 lines.  (One row a lane, 32 lines
+// touched per instruction, cost 38 us of 133 at 200704 x 256 -> 512; scales read through shared
+// memory, which the operands keep busy, another 34.)
 //
 // PAIR: two SMs share a 256 x BN tile (tcgen05.mma.cta_group::2): each converts its own
 // 128 rows of x and BN / 2 rows of w.  Shared memory bounds this kernel (written by the
@@ -42,6 +42,7 @@
 // Rows past M or N are neither loaded nor written: their outputs are never stored, and
 // one row's operand does not reach another row's result.  Past K both operands are 0.
 #include "int8_internal.h"
+#include "int8_rows.cuh"
 #include "pointwise_math.cuh"
 #include "ptx.cuh"
 
@@ -69,7 +70,7 @@ struct Shape {
     static constexpr int kRawSlots = ALIGNED ? (kRowsB >= 128 ? 6 : 8) : 0;  // in 227 KB beside the stages
     static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 2 * 256 * 4 + 256;
+    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 256;
 };
 
 struct Bars {
@@ -80,7 +81,6 @@ struct Bars {
     uint64_t* tfull;
     uint64_t* tempty;
     uint64_t* drain;
-    uint64_t* esync;
     uint32_t* tmem_slot;
     int* abort;
 };
@@ -95,46 +95,12 @@ __device__ __forceinline__ uint2 to_half4(uint32_t v) {
     return make_uint2(lo, hi);
 }
 
-// 16 bytes of a row from byte `at` of a matrix of `total` bytes, zero from `len` on (1..16 bytes
-// are wanted): the one or two aligned granules that hold the bytes, shifted.  A granule that
-// the matrix ends in is read byte by byte, so nothing past its last byte is touched.
-__device__ __forceinline__ uint4 granule(const int8_t* base, long long g, long long total) {
-    const long long at = g << 4;
-    if (at + 16 <= total) return __ldg(reinterpret_cast<const uint4*>(base + at));
-    uint32_t v[4] = {0, 0, 0, 0};
-    for (int i = 0; i < 16; ++i)
-        if (at + i < total) v[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(base[at + i])) << (8 * (i & 3));
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-__device__ __forceinline__ uint4 load_item(const int8_t* base, long long at, int len, long long total) {
-    const long long g = at >> 4;
-    const int off = static_cast<int>(at & 15);
-    const uint4 a = granule(base, g, total);
-    const uint4 b = off + len > 16 ? granule(base, g + 1, total) : make_uint4(0, 0, 0, 0);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const int word = off >> 2, shift = (off & 3) * 8;
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // word is 0..3: a select per word keeps w in registers
-            lo = word == j ? w[i + j] : lo;
-            hi = word == j ? w[i + j + 1] : hi;
-        }
-        const int left = len - 4 * i;
-        const uint32_t v = __funnelshift_r(lo, hi, shift);
-        r[i] = left >= 4 ? v : (left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u));
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
-__device__ __forceinline__ void store_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
-                                         uint32_t g, uint32_t h) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
-                 "r"(e), "r"(f), "r"(g), "r"(h)
-                 : "memory");
+// Arrive on the pair leader's barrier.  What it announces is ordered by other means: operand
+// tiles by the proxy fence before it, tensor memory by tcgen05's own fences; it orders no memory
+// of its own.  With release at cluster scope it held its warp for ~1,800 clocks, three and a half
+// times a stage's MMAs (8192 x 4096 x 4096: 246 us, and 217 us as it is).
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_addr(bar), 0)) : "memory");
 }
 
 // A bounded wait whose answer is the same in every lane.
@@ -144,16 +110,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
-}
-
-// The epilogue warps among themselves: an mbarrier instead of a CTA barrier, so that this wait
-// is bounded like every other.
-__device__ __forceinline__ bool epilogue_sync(uint64_t* bar, uint32_t& phase, volatile int* abort) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    const bool ok = warp_wait(bar, phase, abort);
-    phase ^= 1u;
-    return ok;
 }
 
 // Where a converter stands: its tile and K-step.
@@ -229,13 +185,9 @@ __device__ __forceinline__ void load_stage(const Int8Params& p, const Walk& w, i
     }
 }
 
-// The stage's row (accumulator column) of weight row n: columns 16 q + 2 j + e of each 64 sit at
-// 8 j + 2 q + e.  Tiles of 32 columns: the same with 8 neighbours a lane, j = 0..3.
-template <int BN>
-__device__ __forceinline__ int column_of(int n) {
-    if constexpr (BN >= 64) return (n & ~63) | ((n & 14) << 2) | ((n & 48) >> 3) | (n & 1);
-    else return ((n & 6) << 2) | ((n & 24) >> 2) | (n & 1);
-}
+// The stage's row (accumulator column) of weight row n: columns 8 q + 2 j + e of each 32 sit at
+// 8 j + 2 q + e.
+__device__ __forceinline__ int column_of(int n) { return (n & ~31) | ((n & 6) << 2) | ((n & 24) >> 2) | (n & 1); }
 
 template <bool PAIR, int BN>
 __device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c,
@@ -246,7 +198,7 @@ __device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, 
         int row = r0 + 32 * (i < 4 ? i : i - 4);
         if (i < 4 ? w.m0 + row >= p.M : w.n0 + row >= p.N) continue;
         const uint2 a = to_half4(item[i].x), b = to_half4(item[i].y), d = to_half4(item[i].z), e = to_half4(item[i].w);
-        if (i >= 4) row = column_of<BN>(row);
+        if (i >= 4) row = column_of(row);
         uint8_t* dst = stage + (i < 4 ? 0 : S::kTileA) + row * kRowBytes;
         const int sw = row & 7;  // eight lanes: four chunks of two rows, eight bank groups
         *reinterpret_cast<uint4*>(dst + (((2 * c) ^ sw) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
@@ -254,31 +206,47 @@ __device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, 
     }
 }
 
-// 16 lanes (rows) x 64 columns of tensor memory: register 4 j + 2 h + e of a lane is row
+// 16 lanes (rows) x 32 columns of tensor memory: register 4 j + 2 h + e of a lane is row
 // lane / 4 + 8 h, column 8 j + 2 (lane % 4) + e.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-          "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
-// The same with 32 columns, in the first 16 registers.
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+}
+
+// Waits for this thread's tcgen05.ld, tied to the registers so that no use moves before it.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// Eight neighbouring FP32 values from element n of v (n a multiple of 8), zero past N or without v,
+// as four packed pairs.
+template <bool WHOLE>
+__device__ __forceinline__ void load_pairs(const float* v, int n, int N, uint64_t (&pair)[4]) {
+    if constexpr (WHOLE) {
+        pair[0] = pair[1] = pair[2] = pair[3] = 0;
+        if (v == nullptr) return;
+        const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(v + n));
+        const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(v + n + 4));
+        pair[0] = a.x;
+        pair[1] = a.y;
+        pair[2] = b.x;
+        pair[3] = b.y;
+    } else {
 #pragma unroll
-    for (int i = 16; i < 32; ++i) r[i] = 0;
+        for (int j = 0; j < 4; ++j) {
+            const float lo = v != nullptr && n + 2 * j < N ? __ldg(v + n + 2 * j) : 0.0f;
+            const float hi = v != nullptr && n + 2 * j + 1 < N ? __ldg(v + n + 2 * j + 1) : 0.0f;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(pair[j]) : "f"(lo), "f"(hi));
+        }
+    }
 }
 
 // Scale, bias and activation of two neighbouring columns of one row, in place, as packed FP32.
@@ -295,69 +263,82 @@ __device__ __forceinline__ void finish_two(uint32_t& lo, uint32_t& hi, uint64_t 
     hi = __float_as_uint(activate<ACT>(__uint_as_float(hi)));
 }
 
-// A lane's part of 16 rows x 64 columns: 16 neighbouring columns of two rows (J = 8), or 8 of them
-// where a tile has 32 columns (J = 4).
-template <int ACT, int J>
-__device__ __forceinline__ void finish_block(uint32_t (&v)[32], float xs_lo, float xs_hi, const float* scale,
-                                             const float* bias) {
+// A lane's part of 16 rows x 32 columns: 8 neighbouring columns of two rows.
+template <int ACT>
+__device__ __forceinline__ void finish_block(uint32_t (&v)[16], float xs_lo, float xs_hi, const uint64_t (&ws)[4],
+                                             const uint64_t (&bias)[4]) {
     uint64_t lo2, hi2;
     asm("mov.b64 %0, {%1, %1};" : "=l"(lo2) : "f"(xs_lo));
     asm("mov.b64 %0, {%1, %1};" : "=l"(hi2) : "f"(xs_hi));
 #pragma unroll
-    for (int j = 0; j < J; j += 2) {
-        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(scale + 2 * j);
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bias + 2 * j);
-        finish_two<ACT>(v[4 * j], v[4 * j + 1], lo2, s.x, b.x);
-        finish_two<ACT>(v[4 * j + 2], v[4 * j + 3], hi2, s.x, b.x);
-        finish_two<ACT>(v[4 * j + 4], v[4 * j + 5], lo2, s.y, b.y);
-        finish_two<ACT>(v[4 * j + 6], v[4 * j + 7], hi2, s.y, b.y);
+    for (int j = 0; j < 4; ++j) {
+        finish_two<ACT>(v[4 * j], v[4 * j + 1], lo2, ws[j], bias[j]);
+        finish_two<ACT>(v[4 * j + 2], v[4 * j + 3], hi2, ws[j], bias[j]);
     }
 }
 
-// 2 J neighbouring outputs of row h of a lane's two, in the widest stores that every row's start
-// allows (wide: 32 or 16 bytes; 0: one by one).
-template <int J>
-__device__ __forceinline__ void store_row(const Int8Params& p, const uint32_t (&v)[32], int h, long long row, int n, int wide) {
+// 8 neighbouring outputs of row h of a lane's two to y.  Whole blocks go in 16-byte stores (every
+// row of y starts on 16 bytes then); others one by one, `left` of them.
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void store_row(uint8_t* y, const uint32_t (&v)[16], int h, int left) {
     const auto at = [&](int i) { return v[4 * (i >> 1) + 2 * h + (i & 1)]; };  // column n + i
-    const long long o = row * p.N + n;
-    if (n + 2 * J <= p.N && wide != 0) {
-        if (p.out_bf16) {
-            uint32_t q[J];
+    if constexpr (WHOLE && BF16) {
+        uint32_t q[4];
 #pragma unroll
-            for (int i = 0; i < J; ++i) q[i] = pack_bf16x2(__uint_as_float(at(2 * i)), __uint_as_float(at(2 * i + 1)));
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
-            if (J == 8 && wide == 32) {
-                store_v8(y, q[0], q[1], q[2], q[3], q[4 % J], q[5 % J], q[6 % J], q[7 % J]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < J / 4; ++i)
-                    reinterpret_cast<uint4*>(y)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
-            }
-        } else {
-            float* y = static_cast<float*>(p.y) + o;
-            if (wide == 32) {
-#pragma unroll
-                for (int i = 0; i < 2 * J; i += 8)
-                    store_v8(y + i, at(i), at(i + 1), at(i + 2), at(i + 3), at(i + 4), at(i + 5), at(i + 6), at(i + 7));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * J; i += 4)
-                    *reinterpret_cast<uint4*>(y + i) = make_uint4(at(i), at(i + 1), at(i + 2), at(i + 3));
-            }
-        }
-        return;
-    }
-    if (p.out_bf16) {
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
-#pragma unroll
-        for (int i = 0; i < 2 * J; ++i)
-            if (n + i < p.N) y[i] = __float2bfloat16_rn(__uint_as_float(at(i)));
+        for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(__uint_as_float(at(2 * i)), __uint_as_float(at(2 * i + 1)));
+        *reinterpret_cast<uint4*>(y) = make_uint4(q[0], q[1], q[2], q[3]);
+    } else if constexpr (WHOLE) {
+        reinterpret_cast<uint4*>(y)[0] = make_uint4(at(0), at(1), at(2), at(3));
+        reinterpret_cast<uint4*>(y)[1] = make_uint4(at(4), at(5), at(6), at(7));
     } else {
-        float* y = static_cast<float*>(p.y) + o;
 #pragma unroll
-        for (int i = 0; i < 2 * J; ++i)
-            if (n + i < p.N) y[i] = __uint_as_float(at(i));
+        for (int i = 0; i < 8; ++i) {
+            if (i >= left) break;
+            if constexpr (BF16) reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(__uint_as_float(at(i)));
+            else reinterpret_cast<uint32_t*>(y)[i] = at(i);
+        }
     }
+}
+
+// What an epilogue warp drains of a tile: its columns in blocks of 32, 16 or 32 rows of them.
+struct Drain {
+    uint32_t at;     // tensor memory of its first row and column
+    int n;           // this lane's first column
+    int rows;        // which of the lane's rows, 8 apart, exist (bits)
+    uint8_t* y;      // its first row and column
+    long long row8;  // bytes of 8 rows of y
+    float xs[4];
+};
+
+// G: 16-row groups of the quarter that this warp drains.
+template <int ACT, bool BF16, bool WHOLE, int G>
+__device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d) {
+    uint32_t v[G][16];
+#pragma unroll
+    for (int g = 0; g < G; ++g) tmem_ld_16x32(d.at + (static_cast<uint32_t>(16 * g) << 16), v[g]);
+    uint64_t ws[4], bias[4];
+    load_pairs<WHOLE>(p.w_scale, d.n, p.N, ws);
+    load_pairs<WHOLE>(p.bias, d.n, p.N, bias);
+#pragma unroll
+    for (int g = 0; g < G; ++g) tmem_ld_wait16(v[g]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        finish_block<ACT>(v[g], d.xs[2 * g], d.xs[2 * g + 1], ws, bias);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (d.rows >> (2 * g + h) & 1) store_row<BF16, WHOLE>(d.y + (2 * g + h) * d.row8, v[g], h, p.N - d.n);
+    }
+}
+
+// The columns of a warp, `whole` of its blocks of 32 in wide accesses.
+template <int ACT, bool BF16, int G>
+__device__ __forceinline__ void drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
+    constexpr int es = BF16 ? 2 : 4;
+    int i = 0;
+#pragma unroll 1
+    for (; i < whole; ++i, d.at += 32, d.n += 32, d.y += 32 * es) drain_block<ACT, BF16, true, G>(p, d);
+#pragma unroll 1
+    for (; i < blocks; ++i, d.at += 32, d.n += 32, d.y += 32 * es) drain_block<ACT, BF16, false, G>(p, d);
 }
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as idesc_bf16_f32 with FP16 operands (type 0)
@@ -376,17 +357,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     Bars b;
     uint8_t* raw = smem + S::kStages * S::kStage;
-    float* col_scale = reinterpret_cast<float*>(raw + S::kRawSlots * S::kRaw);  // of the tile in the epilogue
-    float* col_bias = col_scale + 256;
-    b.rfull = reinterpret_cast<uint64_t*>(col_bias + 256);
+    b.rfull = reinterpret_cast<uint64_t*>(raw + S::kRawSlots * S::kRaw);
     b.rempty = b.rfull + S::kRawSlots;
     b.full = b.rempty + S::kRawSlots;
     b.empty = b.full + S::kStages;
     b.tfull = b.empty + S::kStages;
     b.tempty = b.tfull + 2;
     b.drain = b.tempty + 2;
-    b.esync = b.drain + 1;
-    b.tmem_slot = reinterpret_cast<uint32_t*>(b.esync + 1);
+    b.tmem_slot = reinterpret_cast<uint32_t*>(b.drain + 1);
     b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
     volatile int* abort = b.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -418,7 +396,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_init(&b.tempty[i], kCtas * kEpilogueWarps);
         }
         mbar_init(b.drain, 1);
-        mbar_init(b.esync, kEpilogueWarps);
         *b.abort = 0;
         fence_barrier_init();
     }
@@ -456,7 +433,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.full[group]), 0));
+                    if constexpr (PAIR) arrive_leader(&b.full[group]);
                     else mbar_arrive(&b.full[group]);
                 }
                 ph ^= 1u;
@@ -498,69 +475,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int half = (warp - kConverterWarps) >> 2;
         const int es = p.out_bf16 ? 2 : 4;
         const long long row_bytes = static_cast<long long>(p.N) * es;
-        const uintptr_t y0 = reinterpret_cast<uintptr_t>(p.y);
-        const int wide = row_bytes % 32 == 0 && y0 % 32 == 0 ? 32 : (row_bytes % 16 == 0 ? 16 : 0);
+        const bool wide = row_bytes % 16 == 0;  // y itself starts on 16 bytes
         int local = 0;
-        uint32_t eph = 0;
-        constexpr int J = BN >= 64 ? 8 : 4;        // pairs of columns a lane holds of a row
-        constexpr int kCols = BN >= 128 ? BN / 2 : BN;  // columns of a warp; narrow tiles: 16 of its quarter's 32 rows
-        const int col0 = BN >= 128 ? half * kCols : 0;
+        // A warp drains half of the columns of its quarter's 32 rows; of a tile of 32 columns, 16 rows.
+        constexpr int kCols = BN >= 64 ? BN / 2 : BN;
+        const int col0 = BN >= 64 ? half * kCols : 0;
+        constexpr int G = BN >= 64 ? 2 : 1;
+        const int lane0 = quarter * 32 + (BN >= 64 ? 0 : 16 * half);  // its first row of the tile
         for (Walk w = walk_from<PAIR, BN>(tiles, unit0); w.u < units; next_unit(tiles, w), ++local) {
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
-            const int nt = w.nt;
-            const long long row0 = static_cast<long long>(w.mu) * 128 * kCtas + rank * 128 + quarter * 32 + (lane >> 2);
-            float xs[4];  // rows row0, + 8, + 16, + 24
+            const long long row0 = static_cast<long long>(w.mu) * 128 * kCtas + rank * 128 + lane0 + (lane >> 2);
+            const int first = w.nt * BN + col0, left = p.N - first;
+            Drain d;
+            d.at = tmem + (static_cast<uint32_t>(lane0) << 16) + buf * BN + col0;
+            d.n = first + (lane & 3) * 8;
+            d.y = static_cast<uint8_t*>(p.y) + row0 * row_bytes + static_cast<long long>(d.n) * es;
+            d.row8 = 8 * row_bytes;
+            d.rows = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xs[i] = row0 + 8 * i < p.M ? __ldg(p.x_scale + row0 + 8 * i) : 0.0f;
-            const int et = threadIdx.x - 32 * kConverterWarps;  // a column a thread, in flight while the MMAs finish
-            const bool on = et < BN && nt * BN + et < p.N;
-            const float cs = on ? __ldg(p.w_scale + nt * BN + et) : 0.0f;
-            const float cb = on && p.bias ? __ldg(p.bias + nt * BN + et) : 0.0f;
+            for (int i = 0; i < 2 * G; ++i) {
+                const bool on = row0 + 8 * i < p.M;
+                d.rows |= on ? 1 << i : 0;
+                d.xs[i] = on ? __ldg(p.x_scale + row0 + 8 * i) : 0.0f;
+            }
+            const int blocks = left <= 0 ? 0 : (left >= kCols ? kCols / 32 : (left + 31) / 32);
+            const int whole = wide && left > 0 ? (left >= kCols ? kCols / 32 : left / 32) : 0;
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 break;
             }
             tc_fence_after();
-            bool in_step = epilogue_sync(b.esync, eph, abort);  // every warp is past the last tile's columns
-            if (in_step) {
-                col_scale[et] = cs;
-                col_bias[et] = cb;
-                in_step = epilogue_sync(b.esync, eph, abort);
-            }
-            if (!in_step) {
-                record_status(p.status, kStatusTimeoutEpilogue, abort);
-                break;
-            }
-            const int mine = (lane & 3) * 2 * J;  // this lane's first column of a block
-#pragma unroll 1
-            for (int col = col0; col < col0 + kCols; col += 8 * J) {
-                if (nt * BN + col >= p.N) break;
-                const int n = nt * BN + col + mine;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {  // 16 rows at a time
-                    if (BN < 128 && g != half) continue;
-                    uint32_t v[32];
-                    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32 + 16 * g) << 16) + buf * BN + col;
-                    if constexpr (J == 8) tmem_ld_16x64(at, v);
-                    else tmem_ld_16x32(at, v);
-                    tmem_ld_wait(v);
-                    const float* sc = col_scale + col + mine;
-                    const float* bi = col_bias + col + mine;
-                    if (p.act == CONV_ACT_RELU) finish_block<CONV_ACT_RELU, J>(v, xs[2 * g], xs[2 * g + 1], sc, bi);
-                    else if (p.act == CONV_ACT_SILU) finish_block<CONV_ACT_SILU, J>(v, xs[2 * g], xs[2 * g + 1], sc, bi);
-                    else finish_block<CONV_ACT_NONE, J>(v, xs[2 * g], xs[2 * g + 1], sc, bi);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const long long row = row0 + 16 * g + 8 * h;
-                        if (row < p.M && n < p.N) store_row<J>(p, v, h, row, n, wide);
-                    }
-                }
+            if (p.out_bf16) {
+                if (p.act == CONV_ACT_RELU) drain_columns<CONV_ACT_RELU, true, G>(p, d, blocks, whole);
+                else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, true, G>(p, d, blocks, whole);
+                else drain_columns<CONV_ACT_NONE, true, G>(p, d, blocks, whole);
+            } else {
+                if (p.act == CONV_ACT_RELU) drain_columns<CONV_ACT_RELU, false, G>(p, d, blocks, whole);
+                else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, false, G>(p, d, blocks, whole);
+                else drain_columns<CONV_ACT_NONE, false, G>(p, d, blocks, whole);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_addr(&b.tempty[buf]), 0));
+                if constexpr (PAIR) arrive_leader(&b.tempty[buf]);
                 else mbar_arrive(&b.tempty[buf]);
             }
         }

@@ -456,8 +456,8 @@ typedef struct conv_int8_plan conv_int8_plan; /* opaque, host-owned */
 /*
  * Check the shape and choose the kernel.  *plan gets a new plan, or NULL on error.
  * Returns CONV_ERR_INVALID_ARG for non-positive sizes or an unknown dtype or act,
- * CONV_ERR_UNSUPPORTED for K > 131071 (the sum would pass 32 bits) or above 2^40
- * elements of x, w or y, CONV_ERR_CUDA if the device cannot be queried.  Tied to the
+ * CONV_ERR_UNSUPPORTED for K > 131071 (the sum would pass 32 bits), from 2^30 rows or
+ * channels on, or above 2^40 elements of x, w or y, CONV_ERR_CUDA if the device cannot be queried.  Tied to the
  * device current at creation; without a device a host-only plan is made, whose calls
  * return CONV_ERR_CUDA.  out_dtype is y's type.
  */

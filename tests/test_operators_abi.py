@@ -81,6 +81,9 @@ def test_null_and_misaligned_pointers():
     assert f(p._plan, A, A, A, A, A + 4, A, None) == 3
     assert g(p._plan, None, 1, A, A, None, A, A, None) == 1
     assert g(p._plan, A, 7, A, A, None, A, A, None) == 1
+    assert p.workspace_bytes == 0                                                # few rows need none
+    big = cg.Int8MatmulPlan(400, 8, 16)
+    assert big.workspace_bytes > 0 and g(big._plan, A, 1, A, A, None, A, None, None) == 1
     assert g(p._plan, A + 2, 1, A, A, None, A, A, None) == 3
     quant = L.conv_quantize_rows
     assert quant(None, 1, 4, 4, A, A, None) == 1 and quant(A, 1, 0, 4, A, A, None) == 1
