@@ -19,7 +19,7 @@ namespace convgb {
 
 namespace {
 
-constexpr int kFewThreads = 128;
+constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewRowsW = 2;           // rows of w a warp takes
 constexpr int kFewLoads = 8;           // 16-byte loads a lane has under way per row of w
@@ -42,74 +42,75 @@ __device__ __forceinline__ void load_w(const Int8Params& p, int n, int k0, int l
 
 __device__ __forceinline__ float few_load(const float* x, long long i) { return x[i]; }
 __device__ __forceinline__ float few_load(const __nv_bfloat16* x, long long i) { return __bfloat162float(x[i]); }
-__device__ __forceinline__ float few_load(const int8_t*, long long) { return 0.0f; }
 
-__device__ __forceinline__ void few_load4(const float* x, float (&f)[4]) {
-    VecIo<float, 4>::unpack(__ldg(reinterpret_cast<const uint4*>(x)), f);
-}
-__device__ __forceinline__ void few_load4(const __nv_bfloat16* x, float (&f)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(x));
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-
-// Largest magnitude (bits) of row m of x, over the CTA.
-template <typename T>
-__device__ __forceinline__ uint32_t few_amax(const T* x, int K, bool vec, uint32_t* scratch) {
-    uint32_t a = 0;
+// Largest magnitudes (bits) of the rows of x, over the CTA: every row at once, kFewWarps / M warps
+// (one at least) to a row.  One barrier.
+template <typename T, int M>
+__device__ __forceinline__ void few_amax(const Int8Params& p, const T* x, uint32_t* top) {
     constexpr int V = 16 / sizeof(T);
-    if (vec) {
-        using Io = VecIo<T, V>;
-        for (int i = threadIdx.x; i < K / V; i += kFewThreads) {
-            float f[V];
-            Io::unpack(__ldg(reinterpret_cast<const uint4*>(x) + i), f);
+    constexpr int kSegs = kFewWarps / M;  // M is 1, 2, 4 or 8
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m = warp / kSegs, seg = warp - m * kSegs;
+    uint32_t a = 0;
+    if (m < p.M) {
+        const T* row = x + static_cast<long long>(m) * p.K;
+        if (p.K % V == 0) {  // every row starts on 16 bytes
+            using Io = VecIo<T, V>;
+#pragma unroll 8
+            for (int i = seg * 32 + lane; i < p.K / V; i += 32 * kSegs) {
+                float f[V];
+                Io::unpack(__ldg(reinterpret_cast<const uint4*>(row) + i), f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) a = max(a, magnitude_bits(f[j]));
+                for (int j = 0; j < V; ++j) a = max(a, magnitude_bits(f[j]));
+            }
+        } else {
+            for (int i = seg * 32 + lane; i < p.K; i += 32 * kSegs) a = max(a, magnitude_bits(few_load(row, i)));
         }
-    } else {
-        for (int i = threadIdx.x; i < K; i += kFewThreads) a = max(a, magnitude_bits(few_load(x, i)));
     }
     a = warp_max(a);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = a;
+    if (lane == 0) top[warp] = a;
     __syncthreads();
-    a = 0;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) a = max(a, scratch[w]);
-    __syncthreads();
-    return a;
 }
 
-// Chunk [k0, k0 + kFewChunk) of M rows of x to shared memory as 8-bit values, zero past K.
+// Chunk [k0, k0 + kFewChunk) of the rows of x to shared memory as 8-bit values, zero from K up to
+// the next multiple of 16.
 template <typename T, int M>
-__device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int rows, int k0, const float (&inv)[M],
-                                          uint8_t* sx) {
-    const int words = min(kFewChunk, (p.K - k0 + 15) & ~15) / 4;
-    for (int m = 0; m < rows; ++m) {
-        const long long row = static_cast<long long>(m) * p.K + k0;
-        for (int i = threadIdx.x; i < words; i += kFewThreads) {
-            uint32_t v = 0;
-            const int k = k0 + 4 * i;
-            if constexpr (sizeof(T) == 1) {
-                if (k + 4 <= p.K && ((row + 4 * i) & 3) == 0) v = *reinterpret_cast<const uint32_t*>(x + row + 4 * i);
-                else
-                    for (int j = 0; j < 4; ++j)
-                        if (k + j < p.K) v |= static_cast<uint32_t>(static_cast<uint8_t>(x[row + 4 * i + j])) << (8 * j);
+__device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int k0, const float (&inv)[M], uint8_t* sx) {
+    const int len = min(kFewChunk, p.K - k0);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        if (m >= p.M) break;
+        const T* row = x + static_cast<long long>(m) * p.K + k0;
+        uint8_t* dst = sx + m * kFewChunk;
+        if constexpr (sizeof(T) == 1) {
+            if (p.K % 16 == 0) {
+#pragma unroll
+                for (int i = threadIdx.x; i < kFewChunk / 16; i += kFewThreads)
+                    if (i < len / 16) reinterpret_cast<uint4*>(dst)[i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
             } else {
-                float f[4];
-                if (p.K % 4 == 0 && k < p.K) {  // every row starts on four elements
-                    few_load4(x + row + 4 * i, f);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) f[j] = k + j < p.K ? few_load(x, row + 4 * i + j) : 0.0f;
-                }
-                int q[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = quantise(f[j], inv[m]);
-                v = pack_int8x4(q[0], q[1], q[2], q[3]);
+                for (int i = threadIdx.x; i < ((len + 15) & ~15); i += kFewThreads)
+                    dst[i] = i < len ? static_cast<uint8_t>(row[i]) : 0;
             }
-            reinterpret_cast<uint32_t*>(sx + m * kFewChunk)[i] = v;
+        } else {
+            constexpr int V = 16 / sizeof(T);
+            if (p.K % V == 0) {
+                using Io = VecIo<T, V>;
+#pragma unroll
+                for (int i = threadIdx.x; i < kFewChunk / V; i += kFewThreads) {
+                    if (i >= len / V) break;
+                    float f[V];
+                    Io::unpack(__ldg(reinterpret_cast<const uint4*>(row) + i), f);
+#pragma unroll
+                    for (int j = 0; j < V; j += 4)
+                        reinterpret_cast<uint32_t*>(dst)[(i * V + j) / 4] =
+                            pack_int8x4(quantise(f[j], inv[m]), quantise(f[j + 1], inv[m]), quantise(f[j + 2], inv[m]),
+                                        quantise(f[j + 3], inv[m]));
+                }
+                if (threadIdx.x < 16 && (len & 15) > 0 && threadIdx.x >= (len & 15)) dst[(len & ~15) + threadIdx.x] = 0;
+            } else {
+                for (int i = threadIdx.x; i < ((len + 15) & ~15); i += kFewThreads)
+                    dst[i] = i < len ? static_cast<uint8_t>(quantise(few_load(row, i), inv[m])) : 0;
+            }
         }
     }
 }
@@ -119,7 +120,7 @@ __device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int r
 template <typename T, int M, bool ALIGNED>
 __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Params p, const T* x) {
     extern __shared__ __align__(16) uint8_t sx[];  // [M][kFewChunk]
-    __shared__ uint32_t scratch[kFewWarps];
+    __shared__ uint32_t top[kFewWarps];
     const int lane = threadIdx.x & 31;
     const int n0 = (blockIdx.x * kFewWarps + (threadIdx.x >> 5)) * kFewRowsW;
     uint4 w[kFewRowsW][kFewLoads];
@@ -127,15 +128,17 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
     for (int r = 0; r < kFewRowsW; ++r) load_w<ALIGNED>(p, n0 + r, 0, lane, w[r]);
 
     float inv[M], scale[M];
+    if constexpr (sizeof(T) > 1) few_amax<T, M>(p, x, top);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         inv[m] = scale[m] = 0.0f;
-        if (m >= p.M) continue;
         if constexpr (sizeof(T) == 1) {
-            scale[m] = __ldg(p.x_scale + m);
+            if (m < p.M) scale[m] = __ldg(p.x_scale + m);
         } else {
-            const bool vec = p.K % (16 / sizeof(T)) == 0;
-            const RowScale rs = row_scale(few_amax(x + static_cast<long long>(m) * p.K, p.K, vec, scratch));
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < kFewWarps / M; ++i) a = max(a, top[m * (kFewWarps / M) + i]);
+            const RowScale rs = row_scale(a);
             inv[m] = rs.inv;
             scale[m] = rs.scale;
         }
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
 #pragma unroll
             for (int r = 0; r < kFewRowsW; ++r) load_w<ALIGNED>(p, n0 + r, k0, lane, w[r]);
         }
-        few_stage<T, M>(p, x, p.M, k0, inv, sx);
+        few_stage<T, M>(p, x, k0, inv, sx);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kFewLoads; ++i) {
