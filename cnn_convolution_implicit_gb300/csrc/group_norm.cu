@@ -10,13 +10,20 @@
 //   a = sum_S u * gamma / |S|,  b = sum_S u * gamma * h / |S|
 //   dx = rstd * (u * gamma - a - h * b)
 //
-// Both directions compute h and z in the same order of rounded operations, so
-// the backward pass takes ReLU's kink where the forward pass had it.
+// The forward pass takes z as a difference and one fused multiply-add, (x - mean) * (rstd *
+// gamma) + beta (a flat group gives beta itself); the backward pass, which needs h, rounds
+// each operation as written, so that ReLU's kink lies where the formula in FP32 puts it.
 //
 // Sums are FP32.  The variance never comes from a difference of large sums: each
 // thread sums the distances to its own first value, and partial (count, mean,
 // sum of squares) triples join as
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + n_i (mean_i - mean)^2.
+//
+// Resident form (where a 16-CTA cluster's shared memory holds the map of some whole groups):
+// each CTA copies its pixels of `chunk` channels into shared memory once (cp.async, each
+// thread reads back only what it copied), the cluster joins the statistics through
+// distributed shared memory, and the values are written from there: every byte of x (and
+// dy) crosses the memory bus once.  Two CTAs an SM, so one loads while the other stores.
 //
 // Streaming form (any shape): one pass that leaves per-channel partials of pixel
 // ranges in the workspace, a small kernel that joins them per group, and a
@@ -73,6 +80,42 @@ __device__ __forceinline__ void column_sums(float (&val)[VEC], const Lanes& l, f
         for (int i = 0; i < VEC; ++i) val[i] = scratch[col * VEC + i];
 }
 
+// Sums of distances to the thread's first value, then its mean and sum of squares about it.
+template <int VEC>
+struct Moments {
+    static constexpr int H = (VEC + 1) / 2;
+    f2 minus_pivot[H], sum[H], sq[H];
+    int cnt;
+    __device__ __forceinline__ Moments() : cnt(0) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) minus_pivot[i] = sum[i] = sq[i] = 0;
+    }
+    __device__ __forceinline__ void add(const f2 (&v)[H]) {
+        if (cnt == 0)
+#pragma unroll
+            for (int i = 0; i < H; ++i) minus_pivot[i] = f2_make(-f2_lo(v[i]), -f2_hi(v[i]));
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const f2 d = f2_add(v[i], minus_pivot[i]);
+            sum[i] = f2_add(sum[i], d);
+            sq[i] = f2_fma(d, d, sq[i]);
+        }
+        ++cnt;
+    }
+    __device__ __forceinline__ void finish(float (&mean)[VEC], float (&m2)[VEC]) const {
+        const float n = static_cast<float>(cnt);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float pv = i & 1 ? f2_hi(minus_pivot[i / 2]) : f2_lo(minus_pivot[i / 2]);
+            const float s = i & 1 ? f2_hi(sum[i / 2]) : f2_lo(sum[i / 2]);
+            const float q = i & 1 ? f2_hi(sq[i / 2]) : f2_lo(sq[i / 2]);
+            const float d = cnt ? s / n : 0.0f;
+            mean[i] = d - pv;
+            m2[i] = fmaxf(q - d * s, q * 0.0f);  // not below 0; NaN stays
+        }
+    }
+};
+
 // Per-channel (mean, M2) of one pixel range.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_moments_kernel(const NormParams p) {
@@ -84,40 +127,26 @@ __global__ void __launch_bounds__(kNormThreads) norm_moments_kernel(const NormPa
     split_range(p.P, p.splits, s, p0, p1);
     using Io = VecIo<T, VEC>;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + static_cast<long long>(n) * p.P * vecs + l.v;
-    float pivot[VEC], sum[VEC], sq[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) pivot[i] = sum[i] = sq[i] = 0.0f;
-    int cnt = 0;
+    Moments<VEC> mo;
     if (l.on) {
-        for (int px = p0 + l.r; px < p1; px += l.rows, ++cnt) {
-            float v[VEC];
+#pragma unroll 4
+        for (int px = p0 + l.r; px < p1; px += l.rows) {
+            f2 v[Moments<VEC>::H];
             Io::unpack(x[static_cast<long long>(px) * vecs], v);
-            if (cnt == 0)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) pivot[i] = v[i];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float d = v[i] - pivot[i];
-                sum[i] += d;
-                sq[i] = fmaf(d, d, sq[i]);
-            }
+            mo.add(v);
         }
     }
-    const float total = static_cast<float>(p1 - p0), n_t = static_cast<float>(cnt);
+    const float total = static_cast<float>(p1 - p0), n_t = static_cast<float>(mo.cnt);
     float mean[VEC], m2[VEC], joint[VEC];
+    mo.finish(mean, m2);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const float d = cnt ? sum[i] / n_t : 0.0f;
-        mean[i] = pivot[i] + d;
-        m2[i] = fmaxf(sq[i] - d * sum[i], sq[i] * 0.0f);  // not below 0; NaN stays
-        joint[i] = n_t * mean[i];
-    }
+    for (int i = 0; i < VEC; ++i) joint[i] = n_t * mean[i];
     column_sums<VEC>(joint, l, scratch);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         joint[i] /= total;
         const float d = mean[i] - joint[i];
-        if (cnt) m2[i] = fmaf(n_t * d, d, m2[i]);
+        if (mo.cnt) m2[i] = fmaf(n_t * d, d, m2[i]);
     }
     column_sums<VEC>(m2, l, scratch);
     if (l.on && l.r == 0)
@@ -168,18 +197,109 @@ __global__ void __launch_bounds__(128) norm_join_kernel(const NormParams p) {
     }
 }
 
-// What a channel needs to apply the norm.
-struct Channel {
-    float mean, rstd, gamma, beta;
+// What the channels of a vector need: the forward pass's z = (x - mean) * a + beta.
+template <int VEC>
+struct Affine {
+    static constexpr int H = (VEC + 1) / 2;
+    f2 minus_mean[H], a[H], b[H];
+    template <typename F>
+    __device__ __forceinline__ void set(const NormParams& p, int c, F&& stats) {  // stats(channel): (mean, rstd)
+        float mv[2 * H], av[2 * H], bv[2 * H];
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i) {
+            mv[i] = av[i] = bv[i] = 0.0f;
+            if (i < VEC) {
+                const float2 st = stats(c + i);
+                mv[i] = -st.x;
+                av[i] = st.y * (p.gamma ? __ldg(p.gamma + c + i) : 1.0f);
+                bv[i] = p.beta ? __ldg(p.beta + c + i) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            minus_mean[i] = f2_make(mv[2 * i], mv[2 * i + 1]);
+            a[i] = f2_make(av[2 * i], av[2 * i + 1]);
+            b[i] = f2_make(bv[2 * i], bv[2 * i + 1]);
+        }
+    }
+    template <int ACT>
+    __device__ __forceinline__ void apply(f2 (&v)[H]) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) v[i] = activate2<ACT>(f2_fma(f2_add(v[i], minus_mean[i]), a[i], b[i]));
+    }
 };
 
-__device__ __forceinline__ Channel channel_of(const NormParams& p, int n, int c) {
-    const int s = n * p.G + c / p.cpg;
-    return {p.mean[s], p.rstd[s], p.gamma ? p.gamma[c] : 1.0f, p.beta ? p.beta[c] : 0.0f};
-}
+// The backward pass: h and z as written, u, and the sums or dx.
+template <int VEC>
+struct Grad {
+    static constexpr int H = (VEC + 1) / 2;
+    f2 minus_mean[H], rstd[H], gamma[H], beta[H];
+    template <typename F>
+    __device__ __forceinline__ void set(const NormParams& p, int c, F&& stats) {
+        float m[2 * H], r[2 * H], g[2 * H], be[2 * H];
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i) {
+            m[i] = r[i] = g[i] = be[i] = 0.0f;
+            if (i < VEC) {
+                const float2 st = stats(c + i);
+                m[i] = -st.x;
+                r[i] = st.y;
+                g[i] = p.gamma ? __ldg(p.gamma + c + i) : 1.0f;
+                be[i] = p.beta ? __ldg(p.beta + c + i) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            minus_mean[i] = f2_make(m[2 * i], m[2 * i + 1]);
+            rstd[i] = f2_make(r[2 * i], r[2 * i + 1]);
+            gamma[i] = f2_make(g[2 * i], g[2 * i + 1]);
+            beta[i] = f2_make(be[2 * i], be[2 * i + 1]);
+        }
+    }
+    // x -> h, dy -> u
+    template <int ACT>
+    __device__ __forceinline__ void apply(f2 (&x)[H], f2 (&dy)[H]) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            x[i] = f2_mul(f2_add(x[i], minus_mean[i]), rstd[i]);
+            dy[i] = activate_grad2<ACT>(f2_add_rounded(f2_mul(x[i], gamma[i]), beta[i]), dy[i]);
+        }
+    }
+};
 
-__device__ __forceinline__ float norm_h(float x, float mean, float rstd) { return __fmul_rn(__fsub_rn(x, mean), rstd); }
-__device__ __forceinline__ float norm_z(float h, float gamma, float beta) { return __fadd_rn(__fmul_rn(h, gamma), beta); }
+// (a, b) of a vector's groups, for dx = rstd * (u * gamma - a - h * b).
+template <int VEC>
+struct GroupMeans {
+    static constexpr int H = (VEC + 1) / 2;
+    f2 minus_a[H], minus_b[H];
+    template <typename F>
+    __device__ __forceinline__ void set(int c, F&& means) {
+        float a[2 * H], b[2 * H];
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i) {
+            a[i] = b[i] = 0.0f;
+            if (i < VEC) {
+                const float2 m = means(c + i);
+                a[i] = -m.x;
+                b[i] = -m.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            minus_a[i] = f2_make(a[2 * i], a[2 * i + 1]);
+            minus_b[i] = f2_make(b[2 * i], b[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void dx(f2 (&h)[H], const f2 (&u)[H], const Grad<VEC>& g) const {
+#pragma unroll
+        for (int i = 0; i < H; ++i) h[i] = f2_mul(g.rstd[i], f2_fma(h[i], minus_b[i], f2_fma(u[i], g.gamma[i], minus_a[i])));
+    }
+};
+
+__device__ __forceinline__ float2 stats_of(const NormParams& p, int n, int c) {
+    const int s = n * p.G + c / p.cpg;
+    return make_float2(__ldg(p.mean + s), __ldg(p.rstd + s));
+}
 
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const NormParams p) {
@@ -193,15 +313,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const NormPara
     const long long base = static_cast<long long>(n) * p.P * vecs + l.v;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
     auto* y = reinterpret_cast<typename Io::Raw*>(p.y) + base;
-    Channel ch[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) ch[i] = channel_of(p, n, l.v * VEC + i);
+    Affine<VEC> f;
+    f.set(p, l.v * VEC, [&](int c) { return stats_of(p, n, c); });
+#pragma unroll 4
     for (int px = p0 + l.r; px < p1; px += l.rows) {
-        float v[VEC];
+        f2 v[Affine<VEC>::H];
         Io::unpack(x[static_cast<long long>(px) * vecs], v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] = activate<ACT>(norm_z(norm_h(v[i], ch[i].mean, ch[i].rstd), ch[i].gamma, ch[i].beta));
+        f.template apply<ACT>(v);
         y[static_cast<long long>(px) * vecs] = Io::pack(v);
     }
 }
@@ -218,35 +336,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_int8_kernel(const Nor
          row += static_cast<long long>(gridDim.x) * (kNormThreads / 32)) {
         const int n = static_cast<int>(row / p.P);
         const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + row * vecs;
-        uint32_t amax = 0;
-        for (int v = lane; v < vecs; v += 32) {
-            float f[VEC];
+        const auto value = [&](int v, f2 (&f)[Affine<VEC>::H]) {
+            Affine<VEC> af;
+            af.set(p, v * VEC, [&](int c) { return stats_of(p, n, c); });
             Io::unpack(x[v], f);
+            af.template apply<ACT>(f);
+        };
+        float top = 0.0f;
+        for (int v = lane; v < vecs; v += 32) {
+            f2 f[Affine<VEC>::H];
+            value(v, f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const Channel ch = channel_of(p, n, v * VEC + i);
-                amax = max(amax, magnitude_bits(activate<ACT>(norm_z(norm_h(f[i], ch.mean, ch.rstd), ch.gamma, ch.beta))));
-            }
+            for (int i = 0; i < Affine<VEC>::H; ++i) top = magnitude(top, f[i]);
         }
-        const RowScale rs = row_scale(warp_max(amax));
+        const RowScale rs = row_scale(warp_max(magnitude_bits(top)));
         if (lane == 0) p.scale[row] = rs.scale;
-        int8_t* q = p.q + row * p.C;
         for (int v = lane; v < vecs; v += 32) {
-            float f[VEC];
-            Io::unpack(x[v], f);
-            int o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const Channel ch = channel_of(p, n, v * VEC + i);
-                o[i] = quantise(activate<ACT>(norm_z(norm_h(f[i], ch.mean, ch.rstd), ch.gamma, ch.beta)), rs.inv);
-            }
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint2*>(q + v * 8) =
-                    make_uint2(pack_int8x4(o[0], o[1], o[2], o[3]), pack_int8x4(o[4], o[5], o[6], o[7]));
-            else if constexpr (VEC == 4)
-                *reinterpret_cast<uint32_t*>(q + v * 4) = pack_int8x4(o[0], o[1], o[2], o[3]);
-            else
-                q[v] = static_cast<int8_t>(o[0]);
+            f2 f[Affine<VEC>::H];
+            value(v, f);
+            quantise_store<VEC>(p.q + row * p.C + v * VEC, f, rs);
         }
     }
 }
@@ -265,25 +373,31 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_sums_kernel(const Norm
     const long long base = static_cast<long long>(n) * p.P * vecs + l.v;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
     const auto* dy = reinterpret_cast<const typename Io::Raw*>(p.dy) + base;
-    float su[VEC], suh[VEC];
+    constexpr int H = Grad<VEC>::H;
+    f2 s1[H], s2[H];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) su[i] = suh[i] = 0.0f;
+    for (int i = 0; i < H; ++i) s1[i] = s2[i] = 0;
     if (l.on) {
-        Channel ch[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) ch[i] = channel_of(p, n, l.v * VEC + i);
+        Grad<VEC> g;
+        g.set(p, l.v * VEC, [&](int c) { return stats_of(p, n, c); });
+#pragma unroll 2
         for (int px = p0 + l.r; px < p1; px += l.rows) {
-            float v[VEC], d[VEC];
+            f2 v[H], d[H];
             Io::unpack(x[static_cast<long long>(px) * vecs], v);
             Io::unpack(dy[static_cast<long long>(px) * vecs], d);
+            g.template apply<ACT>(v, d);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float h = norm_h(v[i], ch[i].mean, ch[i].rstd);
-                const float u = activate_grad<ACT>(norm_z(h, ch[i].gamma, ch[i].beta), d[i]);
-                su[i] += u;
-                suh[i] = fmaf(u, h, suh[i]);
+            for (int i = 0; i < H; ++i) {
+                s1[i] = f2_add(s1[i], d[i]);
+                s2[i] = f2_fma(d[i], v[i], s2[i]);
             }
         }
+    }
+    float su[VEC], suh[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        su[i] = i & 1 ? f2_hi(s1[i / 2]) : f2_lo(s1[i / 2]);
+        suh[i] = i & 1 ? f2_hi(s2[i / 2]) : f2_lo(s2[i / 2]);
     }
     column_sums<VEC>(su, l, scratch);
     column_sums<VEC>(suh, l, scratch);
@@ -313,22 +427,29 @@ __global__ void __launch_bounds__(128) norm_grad_join_kernel(const NormParams p)
     if (threadIdx.x == 0) p.ab[blockIdx.x] = make_float2(a, b);
 }
 
-// One CTA per channel: dgamma and dbeta over every image and range.
-__global__ void __launch_bounds__(128) norm_grad_channels_kernel(const NormParams p) {
-    __shared__ float scratch[4];
-    const int c = blockIdx.x;
+// dgamma and dbeta over every image and range: 32 channels a CTA, 16 rows of partials at a time.
+__global__ void __launch_bounds__(512) norm_grad_channels_kernel(const NormParams p) {
+    __shared__ float2 scratch[16][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
     const long long entries = static_cast<long long>(p.N) * p.splits;
-    float s = 0.0f, h = 0.0f;
-    for (long long e = threadIdx.x; e < entries; e += blockDim.x) {
-        const float2 v = p.part[e * p.C + c];
-        s += v.x;
-        h += v.y;
-    }
-    s = block_sum(s, scratch);
-    h = block_sum(h, scratch);
-    if (threadIdx.x == 0) {
-        p.dbeta[c] = s;
-        p.dgamma[c] = h;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (c < p.C)
+#pragma unroll 4
+        for (long long e = r; e < entries; e += 16) {
+            const float2 v = p.part[e * p.C + c];
+            s.x += v.x;
+            s.y += v.y;
+        }
+    scratch[r][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (r == 0 && c < p.C) {
+        for (int k = 1; k < 16; ++k) {
+            const float2 v = scratch[k][threadIdx.x];
+            s.x += v.x;
+            s.y += v.y;
+        }
+        p.dbeta[c] = s.x;
+        p.dgamma[c] = s.y;
     }
 }
 
@@ -345,25 +466,364 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_apply_kernel(const Nor
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
     const auto* dy = reinterpret_cast<const typename Io::Raw*>(p.dy) + base;
     auto* dx = reinterpret_cast<typename Io::Raw*>(p.y) + base;
-    Channel ch[VEC];
-    float2 ab[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        ch[i] = channel_of(p, n, l.v * VEC + i);
-        ab[i] = p.ab[n * p.G + (l.v * VEC + i) / p.cpg];
-    }
+    Grad<VEC> g;
+    GroupMeans<VEC> gm;
+    g.set(p, l.v * VEC, [&](int c) { return stats_of(p, n, c); });
+    gm.set(l.v * VEC, [&](int c) { return p.ab[n * p.G + c / p.cpg]; });
+#pragma unroll 2
     for (int px = p0 + l.r; px < p1; px += l.rows) {
-        float v[VEC], d[VEC];
+        f2 v[Grad<VEC>::H], d[Grad<VEC>::H];
         Io::unpack(x[static_cast<long long>(px) * vecs], v);
         Io::unpack(dy[static_cast<long long>(px) * vecs], d);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float h = norm_h(v[i], ch[i].mean, ch[i].rstd);
-            const float u = activate_grad<ACT>(norm_z(h, ch[i].gamma, ch[i].beta), d[i]);
-            v[i] = ch[i].rstd * (fmaf(u, ch[i].gamma, -ab[i].x) - h * ab[i].y);
-        }
+        g.template apply<ACT>(v, d);
+        gm.dx(v, d, g);
         dx[static_cast<long long>(px) * vecs] = Io::pack(v);
     }
+}
+
+// ---------------------------------------------------------------- resident form
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+__device__ __forceinline__ uint32_t res_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void res_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void res_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Two floats at the same shared-memory place of cluster CTA `rank`.
+__device__ __forceinline__ float2 res_peer(const float2* p, uint32_t rank) {
+    uint32_t a;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sums over the CTA's pixel rows of a value per (row, channel), one fixed order: scratch
+// [rows][width], summed in two levels.  out[2 c] receives channel c's sum.  Every thread calls it.
+template <int VEC>
+__device__ __forceinline__ void res_column_sums(const float (&a)[VEC], int r, int rows, int v, int width, float* scratch,
+                                                float* out) {
+    if (r < rows)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) scratch[r * width + v * VEC + i] = a[i];
+    __syncthreads();
+    const int parts = width < kResThreads ? kResThreads / width : 1;
+    for (int t = threadIdx.x; t < parts * width; t += kResThreads) {
+        const int part = t / width, c = t - part * width;
+        float s = 0.0f;
+        for (int k = part; k < rows; k += parts) s += scratch[k * width + c];
+        if (part < rows) scratch[part * width + c] = s;  // its old value was read above by this thread alone
+    }
+    __syncthreads();
+    const int last = parts < rows ? parts : rows;
+    for (int c = threadIdx.x; c < width; c += kResThreads) {
+        float s = 0.0f;
+        for (int k = 0; k < last; ++k) s += scratch[k * width + c];
+        out[2 * c] = s;
+    }
+    __syncthreads();
+}
+
+// Shared memory of a resident CTA: the items of x (and dy), the scratch of the column sums,
+// per-channel sums, per-group results, and a magnitude a pixel (8-bit output).
+struct ResSmem {
+    uint4* x;
+    uint4* dy;
+    float* scratch;    // [kResThreads * VEC]
+    float2* channel;   // [chunk]
+    float2* group;     // [chunk / cpg], read by the cluster
+    float2* result;    // [chunk / cpg]
+    uint32_t* top;     // [pixels of the CTA]
+};
+
+__host__ __device__ inline int res_groups(const NormParams& p) { return p.chunk / p.cpg; }
+__host__ __device__ inline int res_pixels(const NormParams& p) { return (p.P + p.splits - 1) / p.splits; }
+
+template <int MODE>
+__host__ __device__ inline size_t res_smem_bytes(const NormParams& p) {
+    return static_cast<size_t>(MODE == kNormBackward ? 2 : 1) * p.items * kResThreads * 16 +
+           static_cast<size_t>(kResThreads) * p.vec * 4 + static_cast<size_t>(p.chunk) * 8 +
+           static_cast<size_t>(res_groups(p)) * 16 + (MODE == kNormInt8 ? static_cast<size_t>(res_pixels(p)) * 4 : 0);
+}
+
+template <int MODE>
+__device__ __forceinline__ ResSmem res_carve(uint8_t* raw, const NormParams& p) {
+    ResSmem s;
+    s.x = reinterpret_cast<uint4*>(raw);
+    s.dy = s.x + static_cast<size_t>(p.items) * kResThreads;
+    s.scratch = reinterpret_cast<float*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * kResThreads : s.dy);
+    s.channel = reinterpret_cast<float2*>(s.scratch + kResThreads * p.vec);
+    s.group = s.channel + p.chunk;
+    s.result = s.group + res_groups(p);
+    s.top = reinterpret_cast<uint32_t*>(s.result + res_groups(p));
+    return s;
+}
+
+constexpr int kResBatches = 4;  // commit groups: sums start when a quarter has landed
+
+template <typename T, int MODE, int ACT>
+__global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const NormParams p) {
+    constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+    using Io = VecIo<T, VEC>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const ResSmem sm = res_carve<MODE>(smem_raw, p);
+    const int rank = p.splits > 1 ? static_cast<int>(res_rank()) : 0;
+    const int unit = blockIdx.x / p.splits;
+    const int chunks = p.C / p.chunk;
+    const int n = unit / chunks;
+    const int c0 = (unit - n * chunks) * p.chunk;
+    const int vpr = p.chunk / VEC;           // vectors of a pixel
+    const int rows = kResThreads / vpr;
+    const int r = threadIdx.x / vpr, v = threadIdx.x - r * vpr;
+    int p0, p1;
+    split_range(p.P, p.splits, rank, p0, p1);
+    const int mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;  // this thread's items
+    const long long step = static_cast<long long>(rows) * p.C;
+    const long long base = (static_cast<long long>(n) * p.P + p0 + r) * p.C + c0 + v * VEC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int batch = (p.items + kResBatches - 1) / kResBatches;
+    const uint4* items = sm.x + threadIdx.x;
+    const uint4* items_dy = sm.dy + threadIdx.x;
+
+    {
+        const T* x = static_cast<const T*>(p.x) + base;
+        const T* dy = static_cast<const T*>(p.dy) + base;
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(items));
+        const uint32_t dst2 = static_cast<uint32_t>(__cvta_generic_to_shared(items_dy));
+#pragma unroll
+        for (int b = 0; b < kResBatches; ++b) {
+            const int end = min((b + 1) * batch, mine);
+#pragma unroll 2
+            for (int i = b * batch; i < end; ++i) {
+                copy_async16(dst + i * (kResThreads * 16), x + i * step);
+                if constexpr (MODE == kNormBackward) copy_async16(dst2 + i * (kResThreads * 16), dy + i * step);
+            }
+            copy_commit();
+        }
+    }
+
+    const int groups = res_groups(p);
+    const int my_c = c0 + (r < rows ? v : 0) * VEC;
+    float* sums = reinterpret_cast<float*>(sm.channel);
+    Grad<VEC> grad;
+    // `sweep` over the items as their copies land
+    const auto sweep_all = [&](auto&& sweep) {
+        copy_wait<3>();
+        sweep(0, min(batch, mine));
+        copy_wait<2>();
+        sweep(batch, min(2 * batch, mine));
+        copy_wait<1>();
+        sweep(2 * batch, min(3 * batch, mine));
+        copy_wait<0>();
+        sweep(3 * batch, mine);
+    };
+
+    if constexpr (MODE != kNormBackward) {
+        const float pixels = static_cast<float>(p1 - p0);
+        Moments<VEC> mo;
+        sweep_all([&](int from, int to) {
+#pragma unroll 2
+            for (int i = from; i < to; ++i) {
+                f2 f[H];
+                Io::unpack(items[i * kResThreads], f);
+                mo.add(f);
+            }
+        });
+        // The thread's own mean and sum of squares about it; then, through the channel's mean in
+        // this CTA, sums that add up.
+        const float cnt = static_cast<float>(mine);
+        float mean[VEC], m2[VEC], joint[VEC];
+        mo.finish(mean, m2);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) joint[j] = cnt * mean[j];
+        res_column_sums<VEC>(joint, r, rows, v, p.chunk, sm.scratch, sums);
+        if (mine)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float d = mean[j] - sm.channel[v * VEC + j].x / pixels;
+                m2[j] = fmaf(cnt * d, d, m2[j]);
+            }
+        res_column_sums<VEC>(m2, r, rows, v, p.chunk, sm.scratch, sums + 1);
+        // Groups of this CTA: (mean, M2) of pixels * cpg values.
+        for (int g = warp; g < groups; g += kResThreads / 32) {
+            float m = 0.0f;
+            for (int c = lane; c < p.cpg; c += 32) m += sm.channel[g * p.cpg + c].x;
+            m = p1 > p0 ? warp_sum(m) / (pixels * static_cast<float>(p.cpg)) : 0.0f;
+            float q = 0.0f;
+            if (p1 > p0)
+                for (int c = lane; c < p.cpg; c += 32) {
+                    const float2 ch = sm.channel[g * p.cpg + c];
+                    const float d = ch.x / pixels - m;
+                    q += fmaf(pixels * d, d, ch.y);
+                }
+            q = warp_sum(q);
+            if (lane == 0) sm.group[g] = make_float2(m, q);
+        }
+    } else {
+        grad.set(p, my_c, [&](int c) { return stats_of(p, n, c); });
+        f2 s1[H], s2[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) s1[i] = s2[i] = 0;
+        sweep_all([&](int from, int to) {
+            for (int i = from; i < to; ++i) {
+                f2 f[H], d[H];
+                Io::unpack(items[i * kResThreads], f);
+                Io::unpack(items_dy[i * kResThreads], d);
+                grad.template apply<ACT>(f, d);
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    s1[j] = f2_add(s1[j], d[j]);
+                    s2[j] = f2_fma(d[j], f[j], s2[j]);
+                }
+            }
+        });
+        float a[VEC], b[VEC];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            f2_split(s1[j], a[2 * j], a[2 * j + 1]);
+            f2_split(s2[j], b[2 * j], b[2 * j + 1]);
+        }
+        res_column_sums<VEC>(a, r, rows, v, p.chunk, sm.scratch, sums);
+        res_column_sums<VEC>(b, r, rows, v, p.chunk, sm.scratch, sums + 1);
+        if (p.dgamma != nullptr)
+            for (int c = threadIdx.x; c < p.chunk; c += kResThreads)
+                p.part[(static_cast<long long>(n) * p.splits + rank) * p.C + c0 + c] = sm.channel[c];
+        for (int g = warp; g < groups; g += kResThreads / 32) {
+            float ga = 0.0f, gb = 0.0f;
+            for (int c = lane; c < p.cpg; c += 32) {
+                const float2 ch = sm.channel[g * p.cpg + c];
+                const float gm = p.gamma ? __ldg(p.gamma + c0 + g * p.cpg + c) : 1.0f;
+                ga = fmaf(gm, ch.x, ga);
+                gb = fmaf(gm, ch.y, gb);
+            }
+            ga = warp_sum(ga);
+            gb = warp_sum(gb);
+            if (lane == 0) sm.group[g] = make_float2(ga, gb);
+        }
+    }
+
+    // The cluster's groups, every CTA for itself in the same order.
+    if (p.splits > 1) {
+        res_cluster_arrive();
+        res_cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    const float total = static_cast<float>(p.P) * static_cast<float>(p.cpg);
+    for (int g = warp; g < groups; g += kResThreads / 32) {
+        float2 o = make_float2(0.0f, 0.0f);
+        float cnt = 0.0f;
+        if (lane < p.splits) {
+            o = p.splits > 1 ? res_peer(sm.group + g, lane) : sm.group[g];
+            int a, b;
+            split_range(p.P, p.splits, lane, a, b);
+            cnt = static_cast<float>(b - a) * static_cast<float>(p.cpg);
+        }
+        float2 res;
+        if constexpr (MODE != kNormBackward) {
+            const float m = warp_sum(cnt * o.x) / total;
+            const float d = o.x - m;
+            const float var = warp_sum(cnt > 0.0f ? fmaf(cnt * d, d, o.y) : 0.0f) / total;
+            res = make_float2(m, __fdiv_rn(1.0f, __fsqrt_rn(var + p.eps)));
+            if (rank == 0 && lane == 0 && p.mean != nullptr) {
+                const int s = n * p.G + c0 / p.cpg + g;
+                p.mean[s] = res.x;
+                p.rstd[s] = res.y;
+            }
+        } else {
+            res = make_float2(warp_sum(o.x) / total, warp_sum(o.y) / total);
+        }
+        if (lane == 0) sm.result[g] = res;
+    }
+    if constexpr (MODE == kNormInt8)
+        for (int i = threadIdx.x; i < p1 - p0; i += kResThreads) sm.top[i] = 0;
+    __syncthreads();
+    if (p.splits > 1) res_cluster_arrive();  // done with the peers' shared memory
+
+    const auto result = [&](int c) { return sm.result[(c - c0) / p.cpg]; };
+    if constexpr (MODE == kNormForward) {
+        Affine<VEC> af;
+        af.set(p, my_c, result);
+        T* y = static_cast<T*>(p.y) + base;
+#pragma unroll 2
+        for (int i = 0; i < mine; ++i) {
+            f2 f[H];
+            Io::unpack(items[i * kResThreads], f);
+            af.template apply<ACT>(f);
+            *reinterpret_cast<uint4*>(y + i * step) = Io::pack(f);
+        }
+    } else if constexpr (MODE == kNormBackward) {
+        GroupMeans<VEC> gm;
+        gm.set(my_c, result);
+        T* dx = static_cast<T*>(p.y) + base;
+        for (int i = 0; i < mine; ++i) {
+            f2 f[H], d[H];
+            Io::unpack(items[i * kResThreads], f);
+            Io::unpack(items_dy[i * kResThreads], d);
+            grad.template apply<ACT>(f, d);
+            gm.dx(f, d, grad);
+            *reinterpret_cast<uint4*>(dx + i * step) = Io::pack(f);
+        }
+    } else {
+        // 8-bit output (chunk = C: whole pixels here).  A pixel on 1, 2, 4, ... 32 neighbouring lanes
+        // finds its largest magnitude by shuffles; any other width through shared memory.
+        Affine<VEC> af;
+        af.set(p, my_c, result);
+        float* scales = p.scale + static_cast<long long>(n) * p.P + p0 + r;
+        int8_t* q = p.q + base;
+        const auto value = [&](int i, f2 (&f)[H]) {
+            Io::unpack(items[i * kResThreads], f);
+            af.template apply<ACT>(f);
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < H; ++j) top = magnitude(top, f[j]);
+            return magnitude_bits(top);
+        };
+        if ((vpr & (vpr - 1)) == 0 && vpr <= 32) {
+            const int turns = (p1 - p0 + rows - 1) / rows;
+            for (int i = 0; i < turns; ++i) {  // every lane of the warp takes part in the shuffles
+                f2 f[H];
+                uint32_t a = 0;
+                if (i < mine) a = value(i, f);
+                if (vpr == 32) a = warp_max(a);
+                else
+                    for (int o = 1; o < vpr; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+                if (i < mine) {
+                    const RowScale rs = row_scale(a);
+                    quantise_store<VEC>(q + i * step, f, rs);
+                    if (v == 0) scales[i * rows] = rs.scale;
+                }
+            }
+        } else {
+            for (int i = 0; i < mine; ++i) {
+                f2 f[H];
+                atomicMax(sm.top + r + i * rows, value(i, f));
+            }
+            __syncthreads();
+            for (int i = 0; i < mine; ++i) {
+                f2 f[H];
+                value(i, f);
+                const RowScale rs = row_scale(sm.top[r + i * rows]);
+                quantise_store<VEC>(q + i * step, f, rs);
+                if (v == 0) scales[i * rows] = rs.scale;
+            }
+        }
+    }
+    if (p.splits > 1) res_cluster_wait();  // no CTA leaves while a peer may still read it
 }
 
 // ---------------------------------------------------------------- launch
@@ -393,12 +853,125 @@ dim3 stream_grid(const NormParams& p) {
 
 }  // namespace
 
-size_t norm_workspace_bytes(const NormParams& p) {
+namespace {
+
+template <typename F>
+void with_resident(const NormParams& p, int mode, F&& f) {
+    with_act(p.act, [&](auto act) {
+        const auto with_mode = [&](auto t) {
+            using T = decltype(t);
+            if (mode == kNormForward) f(norm_resident_kernel<T, kNormForward, act.value>);
+            else if (mode == kNormInt8) f(norm_resident_kernel<T, kNormInt8, act.value>);
+            else f(norm_resident_kernel<T, kNormBackward, act.value>);
+        };
+        if (p.bf16) with_mode(__nv_bfloat16());
+        else with_mode(float());
+    });
+}
+
+size_t resident_smem(const NormParams& p, int mode) {
+    return mode == kNormForward ? res_smem_bytes<kNormForward>(p)
+                                : (mode == kNormInt8 ? res_smem_bytes<kNormInt8>(p) : res_smem_bytes<kNormBackward>(p));
+}
+
+template <typename K>
+cudaError_t resident_config(K* fn, const NormParams& p, cudaStream_t stream, cudaLaunchConfig_t& cfg,
+                            cudaLaunchAttribute (&attr)[1]) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem_bytes);
+    if (e == cudaSuccess && p.splits > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cfg = cudaLaunchConfig_t();
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.N) * (p.C / p.chunk) * p.splits));
+    cfg.blockDim = dim3(kResThreads);
+    cfg.dynamicSmemBytes = p.smem_bytes;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    return e;
+}
+
+cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    with_resident(p, mode, [&](auto* fn) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[1];
+        e = resident_config(fn, p, stream, cfg, attr);
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, p);
+    });
+    return e;
+}
+
+}  // namespace
+
+// Channels a unit takes and CTAs that share it: the widest chunk of whole groups up to 128 bytes
+// a pixel (whole lines; the 8-bit output needs whole pixels), then the fewest CTAs that hold it two
+// to an SM, then one to an SM; more CTAs while there are fewer than SMs.
+void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
+    const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
+    p.chunk = 0;
+    if (p.vec == 1) return;
+    int chunk = 0;
+    if (mode == kNormInt8) {
+        chunk = p.C;
+    } else {
+        for (int g = 1; g <= p.G; ++g) {  // whole groups that divide the channels and make whole vectors
+            const int c = g * p.cpg;
+            if (p.G % g != 0 || c % p.vec != 0) continue;
+            if (chunk == 0 || c * es <= 128) chunk = c;
+            if (c * es >= 128) break;
+        }
+    }
+    if (chunk == 0 || chunk / p.vec > kResThreads) return;
+    const int rows = kResThreads / (chunk / p.vec);
+    const long long units = static_cast<long long>(p.N) * (p.C / chunk);
+    NormParams t = p;
+    t.chunk = chunk;
+    const auto fits = [&](int cluster, int limit) {
+        t.splits = cluster;
+        const int pixels = res_pixels(t);
+        t.items = (pixels + rows - 1) / rows;
+        if (static_cast<double>(t.items) * tensors * kResThreads * 16 > limit) return false;
+        t.smem_bytes = static_cast<int>(resident_smem(t, mode));
+        return t.smem_bytes <= limit;
+    };
+    int best = 0;
+    for (int limit : {smem_optin / 2 - 1024, smem_optin}) {
+        for (int cluster = 1; cluster <= kResMaxCluster && best == 0; cluster *= 2)
+            if (fits(cluster, limit)) best = cluster;
+        if (best != 0) break;
+    }
+    if (best == 0 || units * best > 0x7fffffffLL) return;
+    while (best < kResMaxCluster && units * best * 2 <= num_sms && p.P >= 2 * best * rows) best *= 2;
+    fits(best, smem_optin);
+    p = t;
+}
+
+bool norm_resident_runs(const NormParams& p, int mode) {
+    int clusters = 0;
+    with_resident(p, mode, [&](auto* fn) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[1];
+        if (resident_config(fn, p, nullptr, cfg, attr) != cudaSuccess ||
+            (p.splits > 1 && cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) != cudaSuccess)) {
+            cudaGetLastError();
+            clusters = 0;
+        } else if (p.splits == 1) {
+            clusters = 1;
+        }
+    });
+    return clusters > 0;
+}
+
+size_t norm_workspace_bytes(const NormParams& p) {  // of the streaming form, or the backward partials
     return (static_cast<size_t>(p.N) * p.splits * p.C + static_cast<size_t>(p.N) * p.G) * sizeof(float2) +
            2 * static_cast<size_t>(p.N) * p.G * sizeof(float);
 }
 
 cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t stream) {
+    if (p.chunk != 0) return launch_resident(p, p.q != nullptr ? kNormInt8 : kNormForward, stream);
     const dim3 grid = stream_grid(p);
     with_types(p, [&](auto t, auto vec) {
         norm_moments_kernel<decltype(t), vec.value><<<grid, kNormThreads, 0, stream>>>(p);
@@ -420,12 +993,18 @@ cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t s
 
 cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream) {
     (void)num_sms;
+    if (p.chunk != 0) {
+        const cudaError_t e = launch_resident(p, kNormBackward, stream);
+        if (e != cudaSuccess) return e;
+        if (p.dgamma != nullptr) norm_grad_channels_kernel<<<(p.C + 31) / 32, 512, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     const dim3 grid = stream_grid(p);
     with_types(p, [&](auto t, auto vec) {
         with_act(p.act, [&](auto act) {
             norm_grad_sums_kernel<decltype(t), vec.value, act.value><<<grid, kNormThreads, 0, stream>>>(p);
             norm_grad_join_kernel<<<p.N * p.G, 128, 0, stream>>>(p);
-            if (p.dgamma != nullptr) norm_grad_channels_kernel<<<p.C, 128, 0, stream>>>(p);
+            if (p.dgamma != nullptr) norm_grad_channels_kernel<<<(p.C + 31) / 32, 512, 0, stream>>>(p);
             norm_grad_apply_kernel<decltype(t), vec.value, act.value><<<grid, kNormThreads, 0, stream>>>(p);
         });
     });

@@ -51,31 +51,31 @@ __device__ __forceinline__ void few_amax(const Int8Params& p, const T* x, uint32
     constexpr int kSegs = kFewWarps / M;  // M is 1, 2, 4 or 8
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m = warp / kSegs, seg = warp - m * kSegs;
-    uint32_t a = 0;
+    float a = 0.0f;
     if (m < p.M) {
         const T* row = x + static_cast<long long>(m) * p.K;
         if (p.K % V == 0) {  // every row starts on 16 bytes
             using Io = VecIo<T, V>;
 #pragma unroll 8
             for (int i = seg * 32 + lane; i < p.K / V; i += 32 * kSegs) {
-                float f[V];
+                f2 f[V / 2];
                 Io::unpack(__ldg(reinterpret_cast<const uint4*>(row) + i), f);
 #pragma unroll
-                for (int j = 0; j < V; ++j) a = max(a, magnitude_bits(f[j]));
+                for (int j = 0; j < V / 2; ++j) a = magnitude(a, f[j]);
             }
         } else {
-            for (int i = seg * 32 + lane; i < p.K; i += 32 * kSegs) a = max(a, magnitude_bits(few_load(row, i)));
+            for (int i = seg * 32 + lane; i < p.K; i += 32 * kSegs) a = max_nan(a, fabsf(few_load(row, i)));
         }
     }
-    a = warp_max(a);
-    if (lane == 0) top[warp] = a;
+    const uint32_t bits = warp_max(magnitude_bits(a));
+    if (lane == 0) top[warp] = bits;
     __syncthreads();
 }
 
 // Chunk [k0, k0 + kFewChunk) of the rows of x to shared memory as 8-bit values, zero from K up to
 // the next multiple of 16.
 template <typename T, int M>
-__device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int k0, const float (&inv)[M], uint8_t* sx) {
+__device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int k0, const RowScale (&rs)[M], uint8_t* sx) {
     const int len = min(kFewChunk, p.K - k0);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -98,18 +98,14 @@ __device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int k
 #pragma unroll
                 for (int i = threadIdx.x; i < kFewChunk / V; i += kFewThreads) {
                     if (i >= len / V) break;
-                    float f[V];
+                    f2 f[V / 2];
                     Io::unpack(__ldg(reinterpret_cast<const uint4*>(row) + i), f);
-#pragma unroll
-                    for (int j = 0; j < V; j += 4)
-                        reinterpret_cast<uint32_t*>(dst)[(i * V + j) / 4] =
-                            pack_int8x4(quantise(f[j], inv[m]), quantise(f[j + 1], inv[m]), quantise(f[j + 2], inv[m]),
-                                        quantise(f[j + 3], inv[m]));
+                    quantise_store<V>(reinterpret_cast<int8_t*>(dst) + i * V, f, rs[m]);
                 }
                 if (threadIdx.x < 16 && (len & 15) > 0 && threadIdx.x >= (len & 15)) dst[(len & ~15) + threadIdx.x] = 0;
             } else {
                 for (int i = threadIdx.x; i < ((len + 15) & ~15); i += kFewThreads)
-                    dst[i] = i < len ? static_cast<uint8_t>(quantise(few_load(row, i), inv[m])) : 0;
+                    dst[i] = i < len ? static_cast<uint8_t>(quantise1(few_load(row, i), rs[m])) : 0;
             }
         }
     }
@@ -127,20 +123,17 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
 #pragma unroll
     for (int r = 0; r < kFewRowsW; ++r) load_w<ALIGNED>(p, n0 + r, 0, lane, w[r]);
 
-    float inv[M], scale[M];
+    RowScale rs[M];
     if constexpr (sizeof(T) > 1) few_amax<T, M>(p, x, top);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-        inv[m] = scale[m] = 0.0f;
         if constexpr (sizeof(T) == 1) {
-            if (m < p.M) scale[m] = __ldg(p.x_scale + m);
+            rs[m] = {m < p.M ? __ldg(p.x_scale + m) : 0.0f, 0.0f, 0u};
         } else {
             uint32_t a = 0;
 #pragma unroll
             for (int i = 0; i < kFewWarps / M; ++i) a = max(a, top[m * (kFewWarps / M) + i]);
-            const RowScale rs = row_scale(a);
-            inv[m] = rs.inv;
-            scale[m] = rs.scale;
+            rs[m] = row_scale(a);
         }
     }
     int acc[kFewRowsW][M];
@@ -155,7 +148,7 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
 #pragma unroll
             for (int r = 0; r < kFewRowsW; ++r) load_w<ALIGNED>(p, n0 + r, k0, lane, w[r]);
         }
-        few_stage<T, M>(p, x, k0, inv, sx);
+        few_stage<T, M>(p, x, k0, rs, sx);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kFewLoads; ++i) {
@@ -182,7 +175,7 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
             const int sum = __reduce_add_sync(0xffffffffu, acc[r][m]);
             const int n = n0 + r;
             if (lane == m && m < p.M && n < p.N) {
-                float v = fmaf(static_cast<float>(sum) * scale[m], __ldg(p.w_scale + n), p.bias ? __ldg(p.bias + n) : 0.0f);
+                float v = fmaf(static_cast<float>(sum) * rs[m].scale, __ldg(p.w_scale + n), p.bias ? __ldg(p.bias + n) : 0.0f);
                 if (p.act == CONV_ACT_RELU) v = activate<CONV_ACT_RELU>(v);
                 else if (p.act == CONV_ACT_SILU) v = activate<CONV_ACT_SILU>(v);
                 const long long o = static_cast<long long>(m) * p.N + n;

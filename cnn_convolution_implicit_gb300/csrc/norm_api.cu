@@ -9,7 +9,7 @@
 using namespace convgb;
 
 struct conv_group_norm_plan {
-    NormParams np;
+    NormParams np[3];  // by NormMode
     int device;
     int num_sms;
 };
@@ -20,6 +20,7 @@ bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u
 
 // Workspace: per-channel partials, then (a, b) per group, then statistics nobody asked for.
 void carve_workspace(NormParams& p, void* workspace) {
+    if (p.chunk != 0 && p.dy == nullptr) return;  // resident forward passes need none
     p.part = static_cast<float2*>(workspace);
     p.ab = p.part + static_cast<size_t>(p.N) * p.splits * p.C;
     if (p.mean == nullptr) {
@@ -47,7 +48,7 @@ conv_status forward(conv_group_norm_plan* pl, const void* x, const float* gamma,
         if (ptr != nullptr && !aligned16(ptr)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
-    NormParams p = pl->np;
+    NormParams p = pl->np[q != nullptr ? kNormInt8 : kNormForward];
     p.x = x;
     p.gamma = gamma;
     p.beta = beta;
@@ -83,19 +84,20 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
 
     conv_group_norm_plan* pl = new (std::nothrow) conv_group_norm_plan();
     if (pl == nullptr) return CONV_ERR_NO_MEMORY;
-    int ndev = 0;
+    int ndev = 0, smem_optin = 232448;
     if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
         cudaGetLastError();
         pl->device = -1;
         pl->num_sms = 152;
     } else if (cudaGetDevice(&pl->device) != cudaSuccess ||
-               cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess) {
+               cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess ||
+               cudaDeviceGetAttribute(&smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, pl->device) !=
+                   cudaSuccess) {
         cudaGetLastError();
         delete pl;
         return CONV_ERR_CUDA;
     }
-    NormParams& p = pl->np;
-    p = NormParams();
+    NormParams p = NormParams();
     p.N = N;
     p.P = static_cast<int>(P);
     p.C = C;
@@ -113,13 +115,21 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
     long long splits = (8LL * pl->num_sms + blocks - 1) / blocks;
     if (splits > P / least) splits = P / least;
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    for (int mode = 0; mode < 3; ++mode) {
+        NormParams& m = pl->np[mode];
+        m = p;
+        norm_pick_resident(m, mode, pl->num_sms, smem_optin);
+        if (m.chunk != 0 && pl->device >= 0 && !norm_resident_runs(m, mode)) m = p;
+    }
     *out = pl;
     return CONV_OK;
 }
 
 conv_status conv_group_norm_workspace(const conv_group_norm_plan* p, unsigned long long* bytes) {
     if (p == nullptr || bytes == nullptr) return CONV_ERR_INVALID_ARG;
-    *bytes = norm_workspace_bytes(p->np);
+    *bytes = 0;
+    for (const NormParams& m : p->np)
+        if (norm_workspace_bytes(m) > *bytes) *bytes = norm_workspace_bytes(m);
     return CONV_OK;
 }
 
@@ -150,7 +160,7 @@ conv_status conv_group_norm_backward(conv_group_norm_plan* pl, const void* dy, c
         if (ptr != nullptr && !aligned16(ptr)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
-    NormParams p = pl->np;
+    NormParams p = pl->np[kNormBackward];
     p.x = x;
     p.dy = dy;
     p.gamma = gamma;

@@ -19,7 +19,11 @@ struct NormParams {
     int act;      // conv_act
     int bf16;     // element type of x, y, dy, dx (else FP32)
     int vec;      // elements per access: 16 bytes where every pixel starts on 16 bytes, else 1
-    int splits;   // pixel ranges per image of the streaming sums
+    int splits;   // pixel ranges per image: of the streaming sums, or the CTAs of a resident cluster
+    // resident form (0 chunk: streaming): a cluster of `splits` CTAs holds `chunk` channels of an image
+    int chunk;
+    int items;       // 16-byte vectors a thread holds of each tensor
+    int smem_bytes;
     const void* x;
     const void* dy;
     const float* gamma;  // nullptr: 1
@@ -35,7 +39,16 @@ struct NormParams {
     float2* ab;          // workspace [N][G] (backward)
 };
 
+constexpr int kResThreads = 256;     // of a resident CTA
+constexpr int kResMaxCluster = 16;
+
+enum NormMode { kNormForward = 0, kNormInt8 = 1, kNormBackward = 2 };
+
 size_t norm_workspace_bytes(const NormParams& p);
+// Fills the resident form's fields for a mode, or leaves chunk 0 where it does not fit.
+void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin);
+// Whether the device runs a cluster of that shape (called once per plan, with its device current).
+bool norm_resident_runs(const NormParams& p, int mode);
 cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream);
 

@@ -23,29 +23,23 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* x
     for (long long row = static_cast<long long>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); row < M;
          row += static_cast<long long>(gridDim.x) * (kQuantThreads / 32)) {
         const auto* src = reinterpret_cast<const typename Io::Raw*>(x) + row * vecs;
-        uint32_t amax = 0;
+        constexpr int H = (VEC + 1) / 2;
+        float top = 0.0f;
+#pragma unroll 4
         for (int v = lane; v < vecs; v += 32) {
-            float f[VEC];
+            f2 f[H];
             Io::unpack(src[v], f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) amax = max(amax, magnitude_bits(f[i]));
+            for (int i = 0; i < H; ++i) top = magnitude(top, f[i]);
         }
-        const RowScale rs = row_scale(warp_max(amax));
+        const RowScale rs = row_scale(warp_max(magnitude_bits(top)));
         if (lane == 0) scale[row] = rs.scale;
         int8_t* dst = q + row * K;
+#pragma unroll 4
         for (int v = lane; v < vecs; v += 32) {
-            float f[VEC];
+            f2 f[H];
             Io::unpack(src[v], f);
-            int o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = quantise(f[i], rs.inv);
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint2*>(dst + v * 8) =
-                    make_uint2(pack_int8x4(o[0], o[1], o[2], o[3]), pack_int8x4(o[4], o[5], o[6], o[7]));
-            else if constexpr (VEC == 4)
-                *reinterpret_cast<uint32_t*>(dst + v * 4) = pack_int8x4(o[0], o[1], o[2], o[3]);
-            else
-                dst[v] = static_cast<int8_t>(o[0]);
+            quantise_store<VEC>(dst + v * VEC, f, rs);
         }
     }
 }
