@@ -21,9 +21,11 @@
 //
 // Resident form (where a 16-CTA cluster's shared memory holds the map of some whole groups):
 // each CTA copies its pixels of `chunk` channels into shared memory once (cp.async, each
-// thread reads back only what it copied), the cluster joins the statistics through
-// distributed shared memory, and the values are written from there: every byte of x (and
-// dy) crosses the memory bus once.  Two CTAs an SM, so one loads while the other stores.
+// thread reads back only what it copied), pushes its groups' sums into the shared memory of
+// its cluster, and after one cluster barrier writes the values from there: every byte of x
+// (and dy) crosses the memory bus once.  Two CTAs an SM, so one loads while the other stores;
+// with 200 KB an SM in flight the rate is those bytes over a CTA's life, so what lies
+// between its last load and its first store counts: one CTA barrier, one cluster barrier.
 //
 // Streaming form (any shape): one pass that leaves per-channel partials of pixel
 // ranges in the workspace, a small kernel that joins them per group, and a
@@ -85,31 +87,30 @@ template <int VEC>
 struct Moments {
     static constexpr int H = (VEC + 1) / 2;
     f2 minus_pivot[H], sum[H], sq[H];
-    int cnt;
-    __device__ __forceinline__ Moments() : cnt(0) {
+    __device__ __forceinline__ Moments() {
 #pragma unroll
         for (int i = 0; i < H; ++i) minus_pivot[i] = sum[i] = sq[i] = 0;
     }
-    __device__ __forceinline__ void add(const f2 (&v)[H]) {
-        if (cnt == 0)
+    __device__ __forceinline__ void start(const f2 (&v)[H]) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) minus_pivot[i] = f2_make(-f2_lo(v[i]), -f2_hi(v[i]));
+        for (int i = 0; i < H; ++i) minus_pivot[i] = f2_make(-f2_lo(v[i]), -f2_hi(v[i]));
+    }
+    __device__ __forceinline__ void add(const f2 (&v)[H]) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const f2 d = f2_add(v[i], minus_pivot[i]);
             sum[i] = f2_add(sum[i], d);
             sq[i] = f2_fma(d, d, sq[i]);
         }
-        ++cnt;
     }
-    __device__ __forceinline__ void finish(float (&mean)[VEC], float (&m2)[VEC]) const {
-        const float n = static_cast<float>(cnt);
+    __device__ __forceinline__ void finish(int cnt, float (&mean)[VEC], float (&m2)[VEC]) const {
+        const float over_n = cnt ? __frcp_rn(static_cast<float>(cnt)) : 0.0f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const float pv = i & 1 ? f2_hi(minus_pivot[i / 2]) : f2_lo(minus_pivot[i / 2]);
             const float s = i & 1 ? f2_hi(sum[i / 2]) : f2_lo(sum[i / 2]);
             const float q = i & 1 ? f2_hi(sq[i / 2]) : f2_lo(sq[i / 2]);
-            const float d = cnt ? s / n : 0.0f;
+            const float d = s * over_n;
             mean[i] = d - pv;
             m2[i] = fmaxf(q - d * s, q * 0.0f);  // not below 0; NaN stays
         }
@@ -128,17 +129,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_moments_kernel(const NormPa
     using Io = VecIo<T, VEC>;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + static_cast<long long>(n) * p.P * vecs + l.v;
     Moments<VEC> mo;
-    if (l.on) {
+    const int cnt = l.on && p0 + l.r < p1 ? (p1 - p0 - l.r + l.rows - 1) / l.rows : 0;
+    if (cnt) {
+        x += static_cast<long long>(p0 + l.r) * vecs;
+        const long long step = static_cast<long long>(l.rows) * vecs;
+        f2 v[Moments<VEC>::H];
+        Io::unpack(x[0], v);
+        mo.start(v);
 #pragma unroll 4
-        for (int px = p0 + l.r; px < p1; px += l.rows) {
-            f2 v[Moments<VEC>::H];
-            Io::unpack(x[static_cast<long long>(px) * vecs], v);
+        for (int i = 0; i < cnt; ++i) {
+            Io::unpack(x[i * step], v);
             mo.add(v);
         }
     }
-    const float total = static_cast<float>(p1 - p0), n_t = static_cast<float>(mo.cnt);
+    const float total = static_cast<float>(p1 - p0), n_t = static_cast<float>(cnt);
     float mean[VEC], m2[VEC], joint[VEC];
-    mo.finish(mean, m2);
+    mo.finish(cnt, mean, m2);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) joint[i] = n_t * mean[i];
     column_sums<VEC>(joint, l, scratch);
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_moments_kernel(const NormPa
     for (int i = 0; i < VEC; ++i) {
         joint[i] /= total;
         const float d = mean[i] - joint[i];
-        if (mo.cnt) m2[i] = fmaf(n_t * d, d, m2[i]);
+        if (cnt) m2[i] = fmaf(n_t * d, d, m2[i]);
     }
     column_sums<VEC>(m2, l, scratch);
     if (l.on && l.r == 0)
@@ -197,29 +203,32 @@ __global__ void __launch_bounds__(128) norm_join_kernel(const NormParams p) {
     }
 }
 
-// What the channels of a vector need: the forward pass's z = (x - mean) * a + beta.
+// What the channels of a vector need: the forward pass's z = (x - mean) * a + beta.  load() takes
+// gamma and beta, set() the statistics.
 template <int VEC>
 struct Affine {
     static constexpr int H = (VEC + 1) / 2;
     f2 minus_mean[H], a[H], b[H];
-    template <typename F>
-    __device__ __forceinline__ void set(const NormParams& p, int c, F&& stats) {  // stats(channel): (mean, rstd)
-        float mv[2 * H], av[2 * H], bv[2 * H];
+    __device__ __forceinline__ void load(const NormParams& p, int c) {
+        float av[2 * H], bv[2 * H];
 #pragma unroll
         for (int i = 0; i < 2 * H; ++i) {
-            mv[i] = av[i] = bv[i] = 0.0f;
-            if (i < VEC) {
-                const float2 st = stats(c + i);
-                mv[i] = -st.x;
-                av[i] = st.y * (p.gamma ? __ldg(p.gamma + c + i) : 1.0f);
-                bv[i] = p.beta ? __ldg(p.beta + c + i) : 0.0f;
-            }
+            av[i] = i < VEC && p.gamma ? __ldg(p.gamma + c + i) : 1.0f;
+            bv[i] = i < VEC && p.beta ? __ldg(p.beta + c + i) : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            minus_mean[i] = f2_make(mv[2 * i], mv[2 * i + 1]);
             a[i] = f2_make(av[2 * i], av[2 * i + 1]);
             b[i] = f2_make(bv[2 * i], bv[2 * i + 1]);
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void set(int c, F&& stats) {  // stats(channel): (mean, rstd)
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 lo = stats(c + 2 * i), hi = 2 * i + 1 < VEC ? stats(c + 2 * i + 1) : make_float2(0.0f, 0.0f);
+            minus_mean[i] = f2_make(-lo.x, -hi.x);
+            a[i] = f2_mul(a[i], f2_make(lo.y, hi.y));
         }
     }
     template <int ACT>
@@ -314,7 +323,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const NormPara
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
     auto* y = reinterpret_cast<typename Io::Raw*>(p.y) + base;
     Affine<VEC> f;
-    f.set(p, l.v * VEC, [&](int c) { return stats_of(p, n, c); });
+    f.load(p, l.v * VEC);
+    f.set(l.v * VEC, [&](int c) { return stats_of(p, n, c); });
 #pragma unroll 4
     for (int px = p0 + l.r; px < p1; px += l.rows) {
         f2 v[Affine<VEC>::H];
@@ -338,7 +348,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_int8_kernel(const Nor
         const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + row * vecs;
         const auto value = [&](int v, f2 (&f)[Affine<VEC>::H]) {
             Affine<VEC> af;
-            af.set(p, v * VEC, [&](int c) { return stats_of(p, n, c); });
+            af.load(p, v * VEC);
+            af.set(v * VEC, [&](int c) { return stats_of(p, n, c); });
             Io::unpack(x[v], f);
             af.template apply<ACT>(f);
         };
@@ -497,13 +508,11 @@ __device__ __forceinline__ uint32_t res_rank() {
 __device__ __forceinline__ void res_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void res_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Two floats at the same shared-memory place of cluster CTA `rank`.
-__device__ __forceinline__ float2 res_peer(const float2* p, uint32_t rank) {
+// Two floats to the same shared-memory place of cluster CTA `rank`.
+__device__ __forceinline__ void res_push(float2* p, uint32_t rank, float2 v) {
     uint32_t a;
-    float2 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -512,52 +521,43 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sums over the CTA's pixel rows of a value per (row, channel), one fixed order: scratch
-// [rows][width], summed in two levels.  out[2 c] receives channel c's sum.  Every thread calls it.
-template <int VEC>
-__device__ __forceinline__ void res_column_sums(const float (&a)[VEC], int r, int rows, int v, int width, float* scratch,
-                                                float* out) {
-    if (r < rows)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) scratch[r * width + v * VEC + i] = a[i];
-    __syncthreads();
-    const int parts = width < kResThreads ? kResThreads / width : 1;
-    for (int t = threadIdx.x; t < parts * width; t += kResThreads) {
-        const int part = t / width, c = t - part * width;
-        float s = 0.0f;
-        for (int k = part; k < rows; k += parts) s += scratch[k * width + c];
-        if (part < rows) scratch[part * width + c] = s;  // its old value was read above by this thread alone
-    }
-    __syncthreads();
-    const int last = parts < rows ? parts : rows;
-    for (int c = threadIdx.x; c < width; c += kResThreads) {
-        float s = 0.0f;
-        for (int k = 0; k < last; ++k) s += scratch[k * width + c];
-        out[2 * c] = s;
-    }
-    __syncthreads();
+// Lanes of a vector that share a group, always: the largest power of two that divides cpg, at most
+// a vector.  A thread's statistics are joined over them before they leave it.
+__host__ __device__ inline int res_lump(const NormParams& p) {
+    int l = 1;
+    while (l < p.vec && p.cpg % (2 * l) == 0) l *= 2;
+    return l;
 }
 
-// Shared memory of a resident CTA: the items of x (and dy), the scratch of the column sums,
-// per-channel sums, per-group results, and a magnitude a pixel (8-bit output).
-struct ResSmem {
-    uint4* x;
-    uint4* dy;
-    float* scratch;    // [kResThreads * VEC]
-    float2* channel;   // [chunk]
-    float2* group;     // [chunk / cpg], read by the cluster
-    float2* result;    // [chunk / cpg]
-    uint32_t* top;     // [pixels of the CTA]
-};
+// Rows of backward partials a CTA keeps: one a warp where neighbouring lanes hold several rows of
+// a channel and add them up first (2, 4, .. 16 vectors to a pixel), else one a pixel row.
+__host__ __device__ inline bool res_warp_rows(int vpr) { return vpr < 32 && (vpr & (vpr - 1)) == 0; }
 
 __host__ __device__ inline int res_groups(const NormParams& p) { return p.chunk / p.cpg; }
 __host__ __device__ inline int res_pixels(const NormParams& p) { return (p.P + p.splits - 1) / p.splits; }
 
+// Shared memory of a resident CTA.
+struct ResSmem {
+    uint4* x;        // the items [items][kResThreads]
+    uint4* dy;       // backward: those of dy
+    float2* part;    // forward: (mean, M2) [rows][vectors * lumps]; backward: (sum u, sum u h) [rows][chunk]
+    float2* recv;    // per group and cluster CTA [groups][kResMaxCluster]
+    float2* result;  // per group
+    uint32_t* top;   // 8-bit output: a magnitude a pixel
+};
+
+template <int MODE>
+__host__ __device__ inline int res_part_entries(const NormParams& p) {
+    const int vpr = p.chunk / p.vec, rows = kResThreads / vpr;
+    if (MODE == kNormBackward) return (res_warp_rows(vpr) ? kResThreads / 32 : rows) * p.chunk;
+    return rows * vpr * (p.vec / res_lump(p));
+}
+
 template <int MODE>
 __host__ __device__ inline size_t res_smem_bytes(const NormParams& p) {
     return static_cast<size_t>(MODE == kNormBackward ? 2 : 1) * p.items * kResThreads * 16 +
-           static_cast<size_t>(kResThreads) * p.vec * 4 + static_cast<size_t>(p.chunk) * 8 +
-           static_cast<size_t>(res_groups(p)) * 16 + (MODE == kNormInt8 ? static_cast<size_t>(res_pixels(p)) * 4 : 0);
+           static_cast<size_t>(res_part_entries<MODE>(p)) * 8 + static_cast<size_t>(res_groups(p)) * (kResMaxCluster + 1) * 8 +
+           (MODE == kNormInt8 ? static_cast<size_t>(res_pixels(p)) * 4 : 0);
 }
 
 template <int MODE>
@@ -565,12 +565,32 @@ __device__ __forceinline__ ResSmem res_carve(uint8_t* raw, const NormParams& p) 
     ResSmem s;
     s.x = reinterpret_cast<uint4*>(raw);
     s.dy = s.x + static_cast<size_t>(p.items) * kResThreads;
-    s.scratch = reinterpret_cast<float*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * kResThreads : s.dy);
-    s.channel = reinterpret_cast<float2*>(s.scratch + kResThreads * p.vec);
-    s.group = s.channel + p.chunk;
-    s.result = s.group + res_groups(p);
+    s.part = reinterpret_cast<float2*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * kResThreads : s.dy);
+    s.recv = s.part + res_part_entries<MODE>(p);
+    s.result = s.recv + res_groups(p) * kResMaxCluster;
     s.top = reinterpret_cast<uint32_t*>(s.result + res_groups(p));
     return s;
+}
+
+// A thread's VEC lanes, (mean, M2) of `cnt` values each, joined in lumps of L and stored.
+template <int VEC, int L>
+__device__ __forceinline__ void res_store_lumps(int cnt, const float (&mean)[VEC], const float (&m2)[VEC], float2* to) {
+    if constexpr (L <= VEC) {
+        const float n = static_cast<float>(cnt);
+#pragma unroll
+        for (int k = 0; k < VEC / L; ++k) {
+            float m = 0.0f, q = 0.0f;
+#pragma unroll
+            for (int i = 0; i < L; ++i) m += mean[k * L + i];
+            m *= 1.0f / L;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const float d = mean[k * L + i] - m;
+                q += fmaf(n * d, d, m2[k * L + i]);
+            }
+            to[k] = make_float2(m, cnt ? q : 0.0f);
+        }
+    }
 }
 
 constexpr int kResBatches = 4;  // commit groups: sums start when a quarter has landed
@@ -596,6 +616,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     const long long base = (static_cast<long long>(n) * p.P + p0 + r) * p.C + c0 + v * VEC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int batch = (p.items + kResBatches - 1) / kResBatches;
+    if (p.splits > 1) res_cluster_arrive();  // this CTA runs: its peers may write to it after their wait below
     const uint4* items = sm.x + threadIdx.x;
     const uint4* items_dy = sm.dy + threadIdx.x;
 
@@ -618,8 +639,10 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
 
     const int groups = res_groups(p);
     const int my_c = c0 + (r < rows ? v : 0) * VEC;
-    float* sums = reinterpret_cast<float*>(sm.channel);
     Grad<VEC> grad;
+    Affine<VEC> af;
+    if constexpr (MODE == kNormBackward) grad.set(p, my_c, [&](int c) { return stats_of(p, n, c); });
+    else af.load(p, my_c);
     // `sweep` over the items as their copies land
     const auto sweep_all = [&](auto&& sweep) {
         copy_wait<3>();
@@ -631,50 +654,62 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         copy_wait<0>();
         sweep(3 * batch, mine);
     };
+    const auto push = [&](int g, float2 val) {  // this CTA's sums of group g, to every CTA of the cluster
+        if (lane < p.splits) {
+            float2* slot = sm.recv + g * kResMaxCluster + rank;
+            if (p.splits > 1) res_push(slot, lane, val);
+            else *slot = val;
+        }
+    };
 
     if constexpr (MODE != kNormBackward) {
-        const float pixels = static_cast<float>(p1 - p0);
         Moments<VEC> mo;
         sweep_all([&](int from, int to) {
+            f2 f[H];
+            if (from == 0 && to > 0) {
+                Io::unpack(items[0], f);
+                mo.start(f);
+            }
 #pragma unroll 2
             for (int i = from; i < to; ++i) {
-                f2 f[H];
                 Io::unpack(items[i * kResThreads], f);
                 mo.add(f);
             }
         });
-        // The thread's own mean and sum of squares about it; then, through the channel's mean in
-        // this CTA, sums that add up.
-        const float cnt = static_cast<float>(mine);
-        float mean[VEC], m2[VEC], joint[VEC];
-        mo.finish(mean, m2);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) joint[j] = cnt * mean[j];
-        res_column_sums<VEC>(joint, r, rows, v, p.chunk, sm.scratch, sums);
-        if (mine)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float d = mean[j] - sm.channel[v * VEC + j].x / pixels;
-                m2[j] = fmaf(cnt * d, d, m2[j]);
-            }
-        res_column_sums<VEC>(m2, r, rows, v, p.chunk, sm.scratch, sums + 1);
-        // Groups of this CTA: (mean, M2) of pixels * cpg values.
+        float mean[VEC], m2[VEC];
+        mo.finish(mine, mean, m2);
+        const int lump = res_lump(p), width = vpr * (VEC / lump);
+        if (r < rows) {
+            float2* to = sm.part + r * width + v * (VEC / lump);
+            if (lump == 8) res_store_lumps<VEC, 8>(mine, mean, m2, to);
+            else if (lump == 4) res_store_lumps<VEC, 4>(mine, mean, m2, to);
+            else if (lump == 2) res_store_lumps<VEC, 2>(mine, mean, m2, to);
+            else res_store_lumps<VEC, 1>(mine, mean, m2, to);
+        }
+        __syncthreads();
+        if (p.splits > 1) res_cluster_wait();  // every CTA of the cluster runs
+        // A warp a group: the CTA's (mean, M2) of it.
+        const int per_row = p.cpg / lump, entries = rows * per_row;
+        const int whole = (p1 - p0) / rows, more = (p1 - p0) - whole * rows;  // items of a row: whole, one more in the first `more`
+        const float cta = static_cast<float>(p1 - p0) * static_cast<float>(p.cpg);
+        const float over = cta > 0.0f ? __frcp_rn(cta) : 0.0f;
         for (int g = warp; g < groups; g += kResThreads / 32) {
-            float m = 0.0f;
-            for (int c = lane; c < p.cpg; c += 32) m += sm.channel[g * p.cpg + c].x;
-            m = p1 > p0 ? warp_sum(m) / (pixels * static_cast<float>(p.cpg)) : 0.0f;
-            float q = 0.0f;
-            if (p1 > p0)
-                for (int c = lane; c < p.cpg; c += 32) {
-                    const float2 ch = sm.channel[g * p.cpg + c];
-                    const float d = ch.x / pixels - m;
-                    q += fmaf(pixels * d, d, ch.y);
-                }
-            q = warp_sum(q);
-            if (lane == 0) sm.group[g] = make_float2(m, q);
+            const float2* part = sm.part + g * per_row;
+            float m = 0.0f, q = 0.0f;
+            for (int e = lane; e < entries; e += 32) {
+                const int er = e / per_row;
+                m = fmaf(static_cast<float>((whole + (er < more)) * lump), part[er * width + (e - er * per_row)].x, m);
+            }
+            m = warp_sum(m) * over;
+            for (int e = lane; e < entries; e += 32) {
+                const int er = e / per_row;
+                const float2 o = part[er * width + (e - er * per_row)];
+                const float d = o.x - m, cnt = static_cast<float>((whole + (er < more)) * lump);
+                if (cnt > 0.0f) q += fmaf(cnt * d, d, o.y);
+            }
+            push(g, make_float2(m, warp_sum(q)));
         }
     } else {
-        grad.set(p, my_c, [&](int c) { return stats_of(p, n, c); });
         f2 s1[H], s2[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) s1[i] = s2[i] = 0;
@@ -691,53 +726,71 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
                 }
             }
         });
-        float a[VEC], b[VEC];
+        const bool by_warp = res_warp_rows(vpr);
+        if (by_warp) {  // the warp's rows of a channel
+            for (int o = vpr; o < 32; o <<= 1)
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            f2_split(s1[j], a[2 * j], a[2 * j + 1]);
-            f2_split(s2[j], b[2 * j], b[2 * j + 1]);
+                for (int j = 0; j < H; ++j) {
+                    s1[j] = f2_add(s1[j], __shfl_xor_sync(0xffffffffu, s1[j], o));
+                    s2[j] = f2_add(s2[j], __shfl_xor_sync(0xffffffffu, s2[j], o));
+                }
         }
-        res_column_sums<VEC>(a, r, rows, v, p.chunk, sm.scratch, sums);
-        res_column_sums<VEC>(b, r, rows, v, p.chunk, sm.scratch, sums + 1);
-        if (p.dgamma != nullptr)
-            for (int c = threadIdx.x; c < p.chunk; c += kResThreads)
-                p.part[(static_cast<long long>(n) * p.splits + rank) * p.C + c0 + c] = sm.channel[c];
+        const int part_rows = by_warp ? kResThreads / 32 : rows;
+        if (by_warp ? lane < vpr : r < rows) {
+            float4* to = reinterpret_cast<float4*>(sm.part + (by_warp ? warp : r) * p.chunk + v * VEC);
+#pragma unroll
+            for (int j = 0; j < H; ++j) to[j] = make_float4(f2_lo(s1[j]), f2_lo(s2[j]), f2_hi(s1[j]), f2_hi(s2[j]));
+        }
+        __syncthreads();
+        if (p.splits > 1) res_cluster_wait();  // every CTA of the cluster runs
+        // A warp a group: channel sums (they are dgamma's and dbeta's partials), then the group's.
+        float2* out = p.part + (static_cast<long long>(n) * p.splits + rank) * p.C + c0;
         for (int g = warp; g < groups; g += kResThreads / 32) {
             float ga = 0.0f, gb = 0.0f;
-            for (int c = lane; c < p.cpg; c += 32) {
-                const float2 ch = sm.channel[g * p.cpg + c];
-                const float gm = p.gamma ? __ldg(p.gamma + c0 + g * p.cpg + c) : 1.0f;
-                ga = fmaf(gm, ch.x, ga);
-                gb = fmaf(gm, ch.y, gb);
+            for (int i = lane; i < p.cpg; i += 32) {
+                const int c = g * p.cpg + i;
+                float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+                for (int k = 0; k < part_rows; ++k) {
+                    const float2 o = sm.part[k * p.chunk + c];
+                    t.x += o.x;
+                    t.y += o.y;
+                }
+                if (p.dgamma != nullptr) out[c] = t;
+                const float gm = p.gamma ? __ldg(p.gamma + c0 + c) : 1.0f;
+                ga = fmaf(gm, t.x, ga);
+                gb = fmaf(gm, t.y, gb);
             }
             ga = warp_sum(ga);
             gb = warp_sum(gb);
-            if (lane == 0) sm.group[g] = make_float2(ga, gb);
+            push(g, make_float2(ga, gb));
         }
     }
 
     // The cluster's groups, every CTA for itself in the same order.
+    if constexpr (MODE == kNormInt8)
+        for (int i = threadIdx.x; i < p1 - p0; i += kResThreads) sm.top[i] = 0;
     if (p.splits > 1) {
         res_cluster_arrive();
         res_cluster_wait();
     } else {
-        __syncthreads();
+        __syncwarp();  // a warp reads back what it wrote
     }
-    const float total = static_cast<float>(p.P) * static_cast<float>(p.cpg);
+    const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
     for (int g = warp; g < groups; g += kResThreads / 32) {
         float2 o = make_float2(0.0f, 0.0f);
         float cnt = 0.0f;
         if (lane < p.splits) {
-            o = p.splits > 1 ? res_peer(sm.group + g, lane) : sm.group[g];
+            o = sm.recv[g * kResMaxCluster + lane];
             int a, b;
             split_range(p.P, p.splits, lane, a, b);
             cnt = static_cast<float>(b - a) * static_cast<float>(p.cpg);
         }
         float2 res;
         if constexpr (MODE != kNormBackward) {
-            const float m = warp_sum(cnt * o.x) / total;
+            const float m = warp_sum(cnt * o.x) * over_total;
             const float d = o.x - m;
-            const float var = warp_sum(cnt > 0.0f ? fmaf(cnt * d, d, o.y) : 0.0f) / total;
+            const float var = warp_sum(cnt > 0.0f ? fmaf(cnt * d, d, o.y) : 0.0f) * over_total;
             res = make_float2(m, __fdiv_rn(1.0f, __fsqrt_rn(var + p.eps)));
             if (rank == 0 && lane == 0 && p.mean != nullptr) {
                 const int s = n * p.G + c0 / p.cpg + g;
@@ -745,19 +798,15 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
                 p.rstd[s] = res.y;
             }
         } else {
-            res = make_float2(warp_sum(o.x) / total, warp_sum(o.y) / total);
+            res = make_float2(warp_sum(o.x) * over_total, warp_sum(o.y) * over_total);
         }
         if (lane == 0) sm.result[g] = res;
     }
-    if constexpr (MODE == kNormInt8)
-        for (int i = threadIdx.x; i < p1 - p0; i += kResThreads) sm.top[i] = 0;
     __syncthreads();
-    if (p.splits > 1) res_cluster_arrive();  // done with the peers' shared memory
 
     const auto result = [&](int c) { return sm.result[(c - c0) / p.cpg]; };
     if constexpr (MODE == kNormForward) {
-        Affine<VEC> af;
-        af.set(p, my_c, result);
+        af.set(my_c, result);
         T* y = static_cast<T*>(p.y) + base;
 #pragma unroll 2
         for (int i = 0; i < mine; ++i) {
@@ -781,8 +830,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     } else {
         // 8-bit output (chunk = C: whole pixels here).  A pixel on 1, 2, 4, ... 32 neighbouring lanes
         // finds its largest magnitude by shuffles; any other width through shared memory.
-        Affine<VEC> af;
-        af.set(p, my_c, result);
+        af.set(my_c, result);
         float* scales = p.scale + static_cast<long long>(n) * p.P + p0 + r;
         int8_t* q = p.q + base;
         const auto value = [&](int i, f2 (&f)[H]) {
@@ -823,7 +871,6 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
             }
         }
     }
-    if (p.splits > 1) res_cluster_wait();  // no CTA leaves while a peer may still read it
 }
 
 // ---------------------------------------------------------------- launch
