@@ -529,6 +529,12 @@ __host__ __device__ inline int res_lump(const NormParams& p) {
     return l;
 }
 
+// Pixels of CTA k of a cluster: pix_base, one more in the first pix_more.
+__device__ __forceinline__ void res_range(const NormParams& p, int k, int& p0, int& p1) {
+    p0 = k * p.pix_base + min(k, p.pix_more);
+    p1 = p0 + p.pix_base + (k < p.pix_more);
+}
+
 // Rows of backward partials a CTA keeps: one a warp where neighbouring lanes hold several rows of
 // a channel and add them up first (2, 4, .. 16 vectors to a pixel), else one a pixel row.
 __host__ __device__ inline bool res_warp_rows(int vpr) { return vpr < 32 && (vpr & (vpr - 1)) == 0; }
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     const int rows = kResThreads / vpr;
     const int r = threadIdx.x / vpr, v = threadIdx.x - r * vpr;
     int p0, p1;
-    split_range(p.P, p.splits, rank, p0, p1);
+    res_range(p, rank, p0, p1);
     const int mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;  // this thread's items
     const long long step = static_cast<long long>(rows) * p.C;
     const long long base = (static_cast<long long>(n) * p.P + p0 + r) * p.C + c0 + v * VEC;
@@ -690,22 +696,37 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         if (p.splits > 1) res_cluster_wait();  // every CTA of the cluster runs
         // A warp a group: the CTA's (mean, M2) of it.
         const int per_row = p.cpg / lump, entries = rows * per_row;
+        const int first_r = per_row == 1 ? lane : lane / per_row, first_k = lane - first_r * per_row;
+        const int step_r = per_row == 1 ? 32 : 32 / per_row, step_k = 32 - step_r * per_row;
         const int whole = (p1 - p0) / rows, more = (p1 - p0) - whole * rows;  // items of a row: whole, one more in the first `more`
         const float cta = static_cast<float>(p1 - p0) * static_cast<float>(p.cpg);
         const float over = cta > 0.0f ? __frcp_rn(cta) : 0.0f;
         for (int g = warp; g < groups; g += kResThreads / 32) {
             const float2* part = sm.part + g * per_row;
             float m = 0.0f, q = 0.0f;
+            int er = first_r, ek = first_k;  // entry lane: its row and lump
             for (int e = lane; e < entries; e += 32) {
-                const int er = e / per_row;
-                m = fmaf(static_cast<float>((whole + (er < more)) * lump), part[er * width + (e - er * per_row)].x, m);
+                m = fmaf(static_cast<float>((whole + (er < more)) * lump), part[er * width + ek].x, m);
+                er += step_r;
+                ek += step_k;
+                if (ek >= per_row) {
+                    ek -= per_row;
+                    ++er;
+                }
             }
             m = warp_sum(m) * over;
+            er = first_r;
+            ek = first_k;
             for (int e = lane; e < entries; e += 32) {
-                const int er = e / per_row;
-                const float2 o = part[er * width + (e - er * per_row)];
+                const float2 o = part[er * width + ek];
                 const float d = o.x - m, cnt = static_cast<float>((whole + (er < more)) * lump);
                 if (cnt > 0.0f) q += fmaf(cnt * d, d, o.y);
+                er += step_r;
+                ek += step_k;
+                if (ek >= per_row) {
+                    ek -= per_row;
+                    ++er;
+                }
             }
             push(g, make_float2(m, warp_sum(q)));
         }
@@ -782,9 +803,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         float cnt = 0.0f;
         if (lane < p.splits) {
             o = sm.recv[g * kResMaxCluster + lane];
-            int a, b;
-            split_range(p.P, p.splits, lane, a, b);
-            cnt = static_cast<float>(b - a) * static_cast<float>(p.cpg);
+            cnt = static_cast<float>(p.pix_base + (lane < p.pix_more)) * static_cast<float>(p.cpg);
         }
         float2 res;
         if constexpr (MODE != kNormBackward) {
@@ -953,8 +972,9 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
 
 }  // namespace
 
-// Channels a unit takes and CTAs that share it: the widest chunk of whole groups up to 128 bytes
-// a pixel (whole lines; the 8-bit output needs whole pixels), then the fewest CTAs that hold it two
+// Channels a unit takes and CTAs that share it: the widest chunk of whole groups up to 64 bytes
+// a pixel (the 8-bit output needs whole pixels; 128 bytes make clusters of 16, of which a GPC
+// holds fewer: 32 x 112 x 112 x 256 BF16 113 us against 97, 32 bytes 122), then the fewest CTAs that hold it two
 // to an SM, then one to an SM; more CTAs while there are fewer than SMs.
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
@@ -967,8 +987,8 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
         for (int g = 1; g <= p.G; ++g) {  // whole groups that divide the channels and make whole vectors
             const int c = g * p.cpg;
             if (p.G % g != 0 || c % p.vec != 0) continue;
-            if (chunk == 0 || c * es <= 128) chunk = c;
-            if (c * es >= 128) break;
+            if (chunk == 0 || c * es <= 64) chunk = c;
+            if (c * es >= 64) break;
         }
     }
     if (chunk == 0 || chunk / p.vec > kResThreads) return;
@@ -986,13 +1006,15 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     };
     int best = 0;
     for (int limit : {smem_optin / 2 - 1024, smem_optin}) {
-        for (int cluster = 1; cluster <= kResMaxCluster && best == 0; cluster *= 2)
+        for (int cluster = 1; cluster <= kResMaxCluster && best == 0; ++cluster)
             if (fits(cluster, limit)) best = cluster;
         if (best != 0) break;
     }
     if (best == 0 || units * best > 0x7fffffffLL) return;
-    while (best < kResMaxCluster && units * best * 2 <= num_sms && p.P >= 2 * best * rows) best *= 2;
+    while (2 * best <= kResMaxCluster && units * best * 2 <= num_sms && p.P >= 2 * best * rows) best *= 2;
     fits(best, smem_optin);
+    t.pix_base = t.P / best;
+    t.pix_more = t.P % best;
     p = t;
 }
 

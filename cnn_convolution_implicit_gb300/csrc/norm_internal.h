@@ -24,6 +24,7 @@ struct NormParams {
     int chunk;
     int items;       // 16-byte vectors a thread holds of each tensor
     int smem_bytes;
+    int pix_base, pix_more;  // pixels of a CTA of the cluster, and how many CTAs have one more
     const void* x;
     const void* dy;
     const float* gamma;  // nullptr: 1
