@@ -19,17 +19,17 @@
 // sum of squares) triples join as
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + n_i (mean_i - mean)^2.
 //
-// Resident form (where a 16-CTA cluster's shared memory holds the map of some whole groups):
-// each CTA copies its pixels of `chunk` channels into shared memory once (cp.async, each
-// thread reads back only what it copied), pushes its groups' sums into the shared memory of
-// its cluster, and after one cluster barrier writes the values from there: every byte of x
-// (and dy) crosses the memory bus once.  Two CTAs an SM, so one loads while the other stores;
-// with 200 KB an SM in flight the rate is those bytes over a CTA's life, so what lies
-// between its last load and its first store counts: one CTA barrier, one cluster barrier.
-//
-// Streaming form (any shape): one pass that leaves per-channel partials of pixel
-// ranges in the workspace, a small kernel that joins them per group, and a
-// second pass that applies them.
+// Three forms.
+//   Resident (small maps; FORM_RULE): each CTA copies its pixels of `chunk` channels into
+//   shared memory once (cp.async, each thread reads back only what it copied), pushes its
+//   groups' sums into the shared memory of its cluster, and after one cluster barrier
+//   writes the values from there.  One launch.
+//   Two passes (any other map whose pixels start on 16 bytes): one kernel leaves each pixel range's
+//   group sums, the next joins them in its prologue and writes the values, walking its range
+//   backwards and storing past the caches, so that what the first pass left in the 129 MB L2
+//   is read from there.  The second is launched early and waits for the first.
+//   By channel (odd channel counts, over 256 vectors a pixel): as two passes, the sums kept per
+//   channel and joined by a kernel of their own.
 #include "norm_internal.h"
 #include "pointwise_math.cuh"
 
@@ -515,11 +515,14 @@ __device__ __forceinline__ void res_push(float2* p, uint32_t rank, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sum over segments of `width` lanes (a power of two), every lane of the warp calling it.
+__device__ __forceinline__ float segment_sum(float v, int width) {
+    for (int o = width >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+
+// The smallest power of two that is at least n, at most a warp.
+__device__ __forceinline__ int segment_width(int n) { return n >= 32 ? 32 : (n <= 1 ? 1 : 1 << (32 - __clz(n - 1))); }
 
 // Lanes of a vector that share a group, always: the largest power of two that divides cpg, at most
 // a vector.  A thread's statistics are joined over them before they leave it.
@@ -601,6 +604,109 @@ __device__ __forceinline__ void res_store_lumps(int cnt, const float (&mean)[VEC
 
 constexpr int kResBatches = 4;  // commit groups: sums start when a quarter has landed
 
+// (mean, M2) of a CTA's groups from its threads' lanes, a segment of lanes to each group;
+// emit(group, value, lanes of the segment).  between() runs after the CTA barrier.
+template <int VEC, typename B, typename E>
+__device__ __forceinline__ void cta_group_moments(const NormParams& p, int pixels, int vpr, int rows, int r, int v, int mine,
+                                                  const float (&mean)[VEC], const float (&m2)[VEC], int groups,
+                                                  float2* part, B&& between, E&& emit) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int lump = res_lump(p), width = vpr * (VEC / lump);
+    if (r < rows) {
+        float2* to = part + r * width + v * (VEC / lump);
+        if (lump == 8) res_store_lumps<VEC, 8>(mine, mean, m2, to);
+        else if (lump == 4) res_store_lumps<VEC, 4>(mine, mean, m2, to);
+        else if (lump == 2) res_store_lumps<VEC, 2>(mine, mean, m2, to);
+        else res_store_lumps<VEC, 1>(mine, mean, m2, to);
+    }
+    __syncthreads();
+    between();
+    const int per_row = p.cpg / lump, entries = rows * per_row;
+    const int wide = segment_width(entries), e0 = lane & (wide - 1);
+    const int first_r = per_row == 1 ? e0 : e0 / per_row, first_k = e0 - first_r * per_row;
+    const int step_r = per_row == 1 ? wide : wide / per_row, step_k = wide - step_r * per_row;
+    const int whole = pixels / rows, more = pixels - whole * rows;  // items of a row: whole, one more in the first `more`
+    const float cta = static_cast<float>(pixels) * static_cast<float>(p.cpg);
+    const float over = cta > 0.0f ? __frcp_rn(cta) : 0.0f;
+    const int at_once = 32 / wide;
+    for (int gb = warp * at_once; gb < groups; gb += warps * at_once) {
+        const int g = gb + lane / wide;
+        const float2* from = part + g * per_row;
+        const int end = g < groups ? entries : 0;
+        float m = 0.0f, q = 0.0f;
+        int er = first_r, ek = first_k;  // an entry's row and lump
+        const auto next = [&] {
+            er += step_r;
+            ek += step_k;
+            if (ek >= per_row) {
+                ek -= per_row;
+                ++er;
+            }
+        };
+        for (int e = e0; e < end; e += wide, next())
+            m = fmaf(static_cast<float>((whole + (er < more)) * lump), from[er * width + ek].x, m);
+        m = segment_sum(m, wide) * over;
+        er = first_r;
+        ek = first_k;
+        for (int e = e0; e < end; e += wide, next()) {
+            const float2 o = from[er * width + ek];
+            const float d = o.x - m, cnt = static_cast<float>((whole + (er < more)) * lump);
+            if (cnt > 0.0f) q += fmaf(cnt * d, d, o.y);
+        }
+        q = segment_sum(q, wide);
+        if (g < groups) emit(g, make_float2(m, q), wide);
+    }
+}
+
+// The backward pass's: channel sums (written to `out`, dgamma's and dbeta's partials), then their
+// groups' (sum u gamma, sum u h gamma).
+template <int VEC, typename B, typename E>
+__device__ __forceinline__ void cta_group_grads(const NormParams& p, int vpr, int rows, int r, int v, f2 (&s1)[VEC / 2],
+                                                f2 (&s2)[VEC / 2], int groups, int channels, const float* gamma, float2* out,
+                                                float2* part, B&& between, E&& emit) {
+    constexpr int H = VEC / 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool by_warp = res_warp_rows(vpr);
+    if (by_warp) {  // the warp's rows of a channel
+        for (int o = vpr; o < 32; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                s1[j] = f2_add(s1[j], __shfl_xor_sync(0xffffffffu, s1[j], o));
+                s2[j] = f2_add(s2[j], __shfl_xor_sync(0xffffffffu, s2[j], o));
+            }
+    }
+    const int part_rows = by_warp ? warps : rows;
+    if (by_warp ? lane < vpr : r < rows) {
+        float4* to = reinterpret_cast<float4*>(part + (by_warp ? warp : r) * channels + v * VEC);
+#pragma unroll
+        for (int j = 0; j < H; ++j) to[j] = make_float4(f2_lo(s1[j]), f2_lo(s2[j]), f2_hi(s1[j]), f2_hi(s2[j]));
+    }
+    __syncthreads();
+    between();
+    const int wide = segment_width(p.cpg), at_once = 32 / wide;
+    for (int gfirst = warp * at_once; gfirst < groups; gfirst += warps * at_once) {
+        const int g = gfirst + lane / wide;
+        float ga = 0.0f, gb = 0.0f;
+        for (int i = lane & (wide - 1); i < p.cpg && g < groups; i += wide) {
+            const int c = g * p.cpg + i;
+            float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+            for (int k = 0; k < part_rows; ++k) {
+                const float2 o = part[k * channels + c];
+                t.x += o.x;
+                t.y += o.y;
+            }
+            if (out != nullptr) out[c] = t;
+            const float gm = gamma ? __ldg(gamma + c) : 1.0f;
+            ga = fmaf(gm, t.x, ga);
+            gb = fmaf(gm, t.y, gb);
+        }
+        ga = segment_sum(ga, wide);
+        gb = segment_sum(gb, wide);
+        if (g < groups) emit(g, make_float2(ga, gb), wide);
+    }
+}
+
 template <typename T, int MODE, int ACT>
 __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const NormParams p) {
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
@@ -660,12 +766,17 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         copy_wait<0>();
         sweep(3 * batch, mine);
     };
-    const auto push = [&](int g, float2 val) {  // this CTA's sums of group g, to every CTA of the cluster
-        if (lane < p.splits) {
+    // This CTA's sums of group g, to every CTA of the cluster: by the `width` lanes that hold them.
+    const auto push = [&](int g, float2 val, int width) {
+        for (int k = lane & (width - 1); k < p.splits; k += width) {
             float2* slot = sm.recv + g * kResMaxCluster + rank;
-            if (p.splits > 1) res_push(slot, lane, val);
+            if (p.splits > 1) res_push(slot, k, val);
             else *slot = val;
         }
+    };
+
+    const auto running = [&] {
+        if (p.splits > 1) res_cluster_wait();  // every CTA of the cluster runs
     };
 
     if constexpr (MODE != kNormBackward) {
@@ -676,7 +787,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
                 Io::unpack(items[0], f);
                 mo.start(f);
             }
-#pragma unroll 2
+#pragma unroll 4
             for (int i = from; i < to; ++i) {
                 Io::unpack(items[i * kResThreads], f);
                 mo.add(f);
@@ -684,52 +795,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         });
         float mean[VEC], m2[VEC];
         mo.finish(mine, mean, m2);
-        const int lump = res_lump(p), width = vpr * (VEC / lump);
-        if (r < rows) {
-            float2* to = sm.part + r * width + v * (VEC / lump);
-            if (lump == 8) res_store_lumps<VEC, 8>(mine, mean, m2, to);
-            else if (lump == 4) res_store_lumps<VEC, 4>(mine, mean, m2, to);
-            else if (lump == 2) res_store_lumps<VEC, 2>(mine, mean, m2, to);
-            else res_store_lumps<VEC, 1>(mine, mean, m2, to);
-        }
-        __syncthreads();
-        if (p.splits > 1) res_cluster_wait();  // every CTA of the cluster runs
-        // A warp a group: the CTA's (mean, M2) of it.
-        const int per_row = p.cpg / lump, entries = rows * per_row;
-        const int first_r = per_row == 1 ? lane : lane / per_row, first_k = lane - first_r * per_row;
-        const int step_r = per_row == 1 ? 32 : 32 / per_row, step_k = 32 - step_r * per_row;
-        const int whole = (p1 - p0) / rows, more = (p1 - p0) - whole * rows;  // items of a row: whole, one more in the first `more`
-        const float cta = static_cast<float>(p1 - p0) * static_cast<float>(p.cpg);
-        const float over = cta > 0.0f ? __frcp_rn(cta) : 0.0f;
-        for (int g = warp; g < groups; g += kResThreads / 32) {
-            const float2* part = sm.part + g * per_row;
-            float m = 0.0f, q = 0.0f;
-            int er = first_r, ek = first_k;  // entry lane: its row and lump
-            for (int e = lane; e < entries; e += 32) {
-                m = fmaf(static_cast<float>((whole + (er < more)) * lump), part[er * width + ek].x, m);
-                er += step_r;
-                ek += step_k;
-                if (ek >= per_row) {
-                    ek -= per_row;
-                    ++er;
-                }
-            }
-            m = warp_sum(m) * over;
-            er = first_r;
-            ek = first_k;
-            for (int e = lane; e < entries; e += 32) {
-                const float2 o = part[er * width + ek];
-                const float d = o.x - m, cnt = static_cast<float>((whole + (er < more)) * lump);
-                if (cnt > 0.0f) q += fmaf(cnt * d, d, o.y);
-                er += step_r;
-                ek += step_k;
-                if (ek >= per_row) {
-                    ek -= per_row;
-                    ++er;
-                }
-            }
-            push(g, make_float2(m, warp_sum(q)));
-        }
+        cta_group_moments<VEC>(p, p1 - p0, vpr, rows, r, v, mine, mean, m2, groups, sm.part, running, push);
     } else {
         f2 s1[H], s2[H];
 #pragma unroll
@@ -747,45 +813,9 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
                 }
             }
         });
-        const bool by_warp = res_warp_rows(vpr);
-        if (by_warp) {  // the warp's rows of a channel
-            for (int o = vpr; o < 32; o <<= 1)
-#pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    s1[j] = f2_add(s1[j], __shfl_xor_sync(0xffffffffu, s1[j], o));
-                    s2[j] = f2_add(s2[j], __shfl_xor_sync(0xffffffffu, s2[j], o));
-                }
-        }
-        const int part_rows = by_warp ? kResThreads / 32 : rows;
-        if (by_warp ? lane < vpr : r < rows) {
-            float4* to = reinterpret_cast<float4*>(sm.part + (by_warp ? warp : r) * p.chunk + v * VEC);
-#pragma unroll
-            for (int j = 0; j < H; ++j) to[j] = make_float4(f2_lo(s1[j]), f2_lo(s2[j]), f2_hi(s1[j]), f2_hi(s2[j]));
-        }
-        __syncthreads();
-        if (p.splits > 1) res_cluster_wait();  // every CTA of the cluster runs
-        // A warp a group: channel sums (they are dgamma's and dbeta's partials), then the group's.
         float2* out = p.part + (static_cast<long long>(n) * p.splits + rank) * p.C + c0;
-        for (int g = warp; g < groups; g += kResThreads / 32) {
-            float ga = 0.0f, gb = 0.0f;
-            for (int i = lane; i < p.cpg; i += 32) {
-                const int c = g * p.cpg + i;
-                float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-                for (int k = 0; k < part_rows; ++k) {
-                    const float2 o = sm.part[k * p.chunk + c];
-                    t.x += o.x;
-                    t.y += o.y;
-                }
-                if (p.dgamma != nullptr) out[c] = t;
-                const float gm = p.gamma ? __ldg(p.gamma + c0 + c) : 1.0f;
-                ga = fmaf(gm, t.x, ga);
-                gb = fmaf(gm, t.y, gb);
-            }
-            ga = warp_sum(ga);
-            gb = warp_sum(gb);
-            push(g, make_float2(ga, gb));
-        }
+        cta_group_grads<VEC>(p, vpr, rows, r, v, s1, s2, groups, p.chunk, p.gamma ? p.gamma + c0 : nullptr,
+                             p.dgamma != nullptr ? out : nullptr, sm.part, running, push);
     }
 
     // The cluster's groups, every CTA for itself in the same order.
@@ -795,31 +825,29 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         res_cluster_arrive();
         res_cluster_wait();
     } else {
-        __syncwarp();  // a warp reads back what it wrote
+        __syncthreads();
     }
     const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
-    for (int g = warp; g < groups; g += kResThreads / 32) {
-        float2 o = make_float2(0.0f, 0.0f);
-        float cnt = 0.0f;
-        if (lane < p.splits) {
-            o = sm.recv[g * kResMaxCluster + lane];
-            cnt = static_cast<float>(p.pix_base + (lane < p.pix_more)) * static_cast<float>(p.cpg);
-        }
+    const int wide = segment_width(p.splits), at_once = 32 / wide, k = lane & (wide - 1);
+    const float cnt = k < p.splits ? static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg) : 0.0f;
+    for (int gfirst = warp * at_once; gfirst < groups; gfirst += kResThreads / 32 * at_once) {
+        const int g = gfirst + lane / wide;
+        const float2 o = g < groups && k < p.splits ? sm.recv[g * kResMaxCluster + k] : make_float2(0.0f, 0.0f);
         float2 res;
         if constexpr (MODE != kNormBackward) {
-            const float m = warp_sum(cnt * o.x) * over_total;
+            const float m = segment_sum(cnt * o.x, wide) * over_total;
             const float d = o.x - m;
-            const float var = warp_sum(cnt > 0.0f ? fmaf(cnt * d, d, o.y) : 0.0f) * over_total;
+            const float var = segment_sum(cnt > 0.0f ? fmaf(cnt * d, d, o.y) : 0.0f, wide) * over_total;
             res = make_float2(m, __fdiv_rn(1.0f, __fsqrt_rn(var + p.eps)));
-            if (rank == 0 && lane == 0 && p.mean != nullptr) {
+            if (rank == 0 && k == 0 && g < groups && p.mean != nullptr) {
                 const int s = n * p.G + c0 / p.cpg + g;
                 p.mean[s] = res.x;
                 p.rstd[s] = res.y;
             }
         } else {
-            res = make_float2(warp_sum(o.x) * over_total, warp_sum(o.y) * over_total);
+            res = make_float2(segment_sum(o.x, wide) * over_total, segment_sum(o.y, wide) * over_total);
         }
-        if (lane == 0) sm.result[g] = res;
+        if (k == 0 && g < groups) sm.result[g] = res;
     }
     __syncthreads();
 
@@ -827,7 +855,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     if constexpr (MODE == kNormForward) {
         af.set(my_c, result);
         T* y = static_cast<T*>(p.y) + base;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < mine; ++i) {
             f2 f[H];
             Io::unpack(items[i * kResThreads], f);
@@ -862,18 +890,29 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
         };
         if ((vpr & (vpr - 1)) == 0 && vpr <= 32) {
             const int turns = (p1 - p0 + rows - 1) / rows;
-            for (int i = 0; i < turns; ++i) {  // every lane of the warp takes part in the shuffles
-                f2 f[H];
-                uint32_t a = 0;
-                if (i < mine) a = value(i, f);
-                if (vpr == 32) a = warp_max(a);
-                else
-                    for (int o = 1; o < vpr; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-                if (i < mine) {
-                    const RowScale rs = row_scale(a);
-                    quantise_store<VEC>(q + i * step, f, rs);
-                    if (v == 0) scales[i * rows] = rs.scale;
+            constexpr int U = 4;  // pixels under way at a time: their shuffles and divisions overlap
+            for (int i0 = 0; i0 < turns; i0 += U) {  // every lane of the warp takes part in the shuffles
+                f2 f[U][H];
+                uint32_t a[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) a[u] = i0 + u < mine ? value(i0 + u, f[u]) : 0u;
+                if (vpr == 32) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) a[u] = warp_max(a[u]);
+                } else {
+                    for (int o = 1; o < vpr; o <<= 1)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
                 }
+                RowScale rs[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u < mine) {
+                        quantise_store<VEC>(q + (i0 + u) * step, f[u], rs[u]);
+                        if (v == 0) scales[(i0 + u) * rows] = rs[u].scale;
+                    }
             }
         } else {
             for (int i = 0; i < mine; ++i) {
@@ -888,6 +927,302 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
                 quantise_store<VEC>(q + i * step, f, rs);
                 if (v == 0) scales[i * rows] = rs.scale;
             }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- two passes
+constexpr int kTwoBatch = 8;  // 16-byte loads a thread has under way
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 load_last(const uint4* p) { return __ldcs(p); }  // not needed again
+__device__ __forceinline__ void store_past(uint4* p, uint4 v) { __stcs(p, v); }
+
+// Where a CTA of either pass stands: pixel range `s` of image n, all channels.
+struct TwoRange {
+    int n, s, vpr, rows, r, v, p0, p1, mine;
+    long long base, step;  // in vectors
+    __device__ __forceinline__ TwoRange(const NormParams& p, int block, int VEC) {
+        n = block / p.splits;
+        s = block - n * p.splits;
+        vpr = p.C / VEC;
+        rows = kNormThreads / vpr;
+        r = threadIdx.x / vpr;
+        v = threadIdx.x - r * vpr;
+        res_range(p, s, p0, p1);
+        mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;
+        base = (static_cast<long long>(n) * p.P + p0 + r) * vpr + v;
+        step = static_cast<long long>(rows) * vpr;
+    }
+};
+
+// First pass.  Forward: (mean, M2) of the range's groups; backward: (sum u gamma, sum u h gamma) of
+// them and the channels' (sum u, sum u h).
+template <typename T, int MODE, int ACT>
+__global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) norm_range_sums_kernel(const NormParams p) {
+    constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+    using Io = VecIo<T, VEC>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    float2* part = reinterpret_cast<float2*>(smem_raw);
+    const TwoRange t(p, blockIdx.x, VEC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint4* x = static_cast<const uint4*>(p.x) + t.base;
+    launch_dependents();
+    if constexpr (MODE != kNormBackward) {
+        Moments<VEC> mo;
+        f2 f[H];
+        if (t.mine) {
+            Io::unpack(__ldg(x), f);
+            mo.start(f);
+        }
+        int i = 0;
+        for (; i + kTwoBatch <= t.mine; i += kTwoBatch) {
+            uint4 raw[kTwoBatch];
+#pragma unroll
+            for (int k = 0; k < kTwoBatch; ++k) raw[k] = __ldg(x + (i + k) * t.step);
+#pragma unroll
+            for (int k = 0; k < kTwoBatch; ++k) {
+                Io::unpack(raw[k], f);
+                mo.add(f);
+            }
+        }
+        for (; i < t.mine; ++i) {
+            Io::unpack(__ldg(x + i * t.step), f);
+            mo.add(f);
+        }
+        float mean[VEC], m2[VEC];
+        mo.finish(t.mine, mean, m2);
+        const auto store = [&](int g, float2 val, int wide) {
+            if ((lane & (wide - 1)) == 0) p.part[(static_cast<long long>(t.n) * p.G + g) * p.splits + t.s] = val;
+        };
+        cta_group_moments<VEC>(p, t.p1 - t.p0, t.vpr, t.rows, t.r, t.v, t.mine, mean, m2, p.G, part, [] {}, store);
+    } else {
+        const uint4* dy = static_cast<const uint4*>(p.dy) + t.base;
+        Grad<VEC> grad;
+        grad.set(p, (t.r < t.rows ? t.v : 0) * VEC, [&](int c) { return stats_of(p, t.n, c); });
+        f2 s1[H], s2[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) s1[j] = s2[j] = 0;
+        const auto take = [&](const uint4& a, const uint4& b) {
+            f2 f[H], d[H];
+            Io::unpack(a, f);
+            Io::unpack(b, d);
+            grad.template apply<ACT>(f, d);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                s1[j] = f2_add(s1[j], d[j]);
+                s2[j] = f2_fma(d[j], f[j], s2[j]);
+            }
+        };
+        constexpr int B = 4;
+        int i = 0;
+        for (; i + B <= t.mine; i += B) {
+            uint4 a[B], b[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                a[k] = __ldg(x + (i + k) * t.step);
+                b[k] = __ldg(dy + (i + k) * t.step);
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) take(a[k], b[k]);
+        }
+        for (; i < t.mine; ++i) take(__ldg(x + i * t.step), __ldg(dy + i * t.step));
+        float2* out = p.part + (static_cast<long long>(t.n) * p.splits + t.s) * p.C;
+        const auto store = [&](int g, float2 val, int wide) {
+            if ((lane & (wide - 1)) == 0) p.ab[(static_cast<long long>(t.n) * p.G + g) * p.splits + t.s] = val;
+        };
+        cta_group_grads<VEC>(p, t.vpr, t.rows, t.r, t.v, s1, s2, p.G, p.C, p.gamma, p.dgamma != nullptr ? out : nullptr,
+                             part, [] {}, store);
+    }
+    (void)warp;
+}
+
+// Second pass.  Joins the ranges of the image's groups, then writes the range backwards.  Backward:
+// the first `extra` CTAs write dgamma and dbeta instead, 32 channels each.
+template <typename T, int MODE, int ACT>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_range_apply_kernel(const NormParams p, int extra) {
+    constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+    using Io = VecIo<T, VEC>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    float2* joined = reinterpret_cast<float2*>(smem_raw);  // [G]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (MODE == kNormBackward && static_cast<int>(blockIdx.x) < extra) {
+        wait_for_previous();
+        const int c = blockIdx.x * 32 + lane;
+        const long long entries = static_cast<long long>(p.N) * p.splits;
+        float2 sum = make_float2(0.0f, 0.0f);
+        if (c < p.C)
+#pragma unroll 8
+            for (long long e = warp; e < entries; e += kNormThreads / 32) {
+                const float2 o = p.part[e * p.C + c];
+                sum.x += o.x;
+                sum.y += o.y;
+            }
+        joined[warp * 32 + lane] = sum;
+        __syncthreads();
+        if (warp == 0 && c < p.C) {
+            for (int k = 1; k < kNormThreads / 32; ++k) {
+                sum.x += joined[k * 32 + lane].x;
+                sum.y += joined[k * 32 + lane].y;
+            }
+            p.dbeta[c] = sum.x;
+            p.dgamma[c] = sum.y;
+        }
+        return;
+    }
+    const TwoRange t(p, blockIdx.x - (MODE == kNormBackward ? extra : 0), VEC);
+    const int my_c = (t.r < t.rows ? t.v : 0) * VEC;
+    const uint4* x = static_cast<const uint4*>(p.x) + t.base;
+    Affine<VEC> af;
+    Grad<VEC> grad;
+    if constexpr (MODE == kNormBackward) grad.set(p, my_c, [&](int c) { return stats_of(p, t.n, c); });
+    else af.load(p, my_c);
+    wait_for_previous();
+    {
+        const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
+        const int wide = segment_width(p.splits), at_once = 32 / wide;
+        for (int gfirst = warp * at_once; gfirst < p.G; gfirst += kNormThreads / 32 * at_once) {
+            const int g = gfirst + lane / wide;
+            const float2* from = (MODE == kNormBackward ? p.ab : p.part) + (static_cast<long long>(t.n) * p.G + g) * p.splits;
+            const int end = g < p.G ? p.splits : 0;
+            float2 res;
+            if constexpr (MODE != kNormBackward) {
+                float m = 0.0f, q = 0.0f;
+                for (int k = lane & (wide - 1); k < end; k += wide)
+                    m = fmaf(static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg), from[k].x, m);
+                m = segment_sum(m, wide) * over_total;
+                for (int k = lane & (wide - 1); k < end; k += wide) {
+                    const float cnt = static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg);
+                    const float2 o = from[k];
+                    const float d = o.x - m;
+                    q += fmaf(cnt * d, d, o.y);
+                }
+                const float var = segment_sum(q, wide) * over_total;
+                res = make_float2(m, __fdiv_rn(1.0f, __fsqrt_rn(var + p.eps)));
+                if (t.s == 0 && (lane & (wide - 1)) == 0 && g < p.G && p.mean != nullptr) {
+                    p.mean[t.n * p.G + g] = res.x;
+                    p.rstd[t.n * p.G + g] = res.y;
+                }
+            } else {
+                float a = 0.0f, b = 0.0f;
+                for (int k = lane & (wide - 1); k < end; k += wide) {
+                    a += from[k].x;
+                    b += from[k].y;
+                }
+                res = make_float2(segment_sum(a, wide) * over_total, segment_sum(b, wide) * over_total);
+            }
+            if ((lane & (wide - 1)) == 0 && g < p.G) joined[g] = res;
+        }
+    }
+    __syncthreads();
+    const auto result = [&](int c) { return joined[c / p.cpg]; };
+    if constexpr (MODE == kNormForward) {
+        af.set(my_c, result);
+        uint4* y = static_cast<uint4*>(p.y) + t.base;
+        const auto put = [&](const uint4& raw, int i) {
+            f2 f[H];
+            Io::unpack(raw, f);
+            af.template apply<ACT>(f);
+            store_past(y + i * t.step, Io::pack(f));
+        };
+        int i = t.mine;
+        for (; i >= kTwoBatch; i -= kTwoBatch) {
+            uint4 raw[kTwoBatch];
+#pragma unroll
+            for (int k = 0; k < kTwoBatch; ++k) raw[k] = load_last(x + (i - 1 - k) * t.step);
+#pragma unroll
+            for (int k = 0; k < kTwoBatch; ++k) put(raw[k], i - 1 - k);
+        }
+        for (; i > 0; --i) put(load_last(x + (i - 1) * t.step), i - 1);
+    } else if constexpr (MODE == kNormBackward) {
+        GroupMeans<VEC> gm;
+        gm.set(my_c, result);
+        const uint4* dy = static_cast<const uint4*>(p.dy) + t.base;
+        uint4* dx = static_cast<uint4*>(p.y) + t.base;
+        const auto put = [&](const uint4& a, const uint4& b, int i) {
+            f2 f[H], d[H];
+            Io::unpack(a, f);
+            Io::unpack(b, d);
+            grad.template apply<ACT>(f, d);
+            gm.dx(f, d, grad);
+            store_past(dx + i * t.step, Io::pack(f));
+        };
+        constexpr int B = 4;
+        int i = t.mine;
+        for (; i >= B; i -= B) {
+            uint4 a[B], b[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                a[k] = load_last(x + (i - 1 - k) * t.step);
+                b[k] = load_last(dy + (i - 1 - k) * t.step);
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) put(a[k], b[k], i - 1 - k);
+        }
+        for (; i > 0; --i) put(load_last(x + (i - 1) * t.step), load_last(dy + (i - 1) * t.step), i - 1);
+    } else {
+        // A pixel on 1, 2, 4, ... 32 neighbouring lanes finds its largest magnitude by shuffles, any
+        // other width through shared memory; four pixels under way at a time.
+        af.set(my_c, result);
+        constexpr int U = 4;
+        float* scales = p.scale + static_cast<long long>(t.n) * p.P + t.p0 + t.r;
+        const bool by_lanes = (t.vpr & (t.vpr - 1)) == 0 && t.vpr <= 32;
+        uint32_t* top = reinterpret_cast<uint32_t*>(joined + p.G);  // [2][U][rows]
+        if (!by_lanes) {
+            for (int i = threadIdx.x; i < 2 * U * t.rows; i += kNormThreads) top[i] = 0;
+            __syncthreads();
+        }
+        const int turns = (t.p1 - t.p0 + t.rows - 1) / t.rows;
+        int buf = 0;
+        for (int i0 = ((turns - 1) / U) * U; i0 >= 0; i0 -= U, buf ^= 1) {
+            uint4 raw[U];
+            f2 f[U][H];
+            uint32_t a[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < t.mine) raw[u] = load_last(x + (i0 + u) * t.step);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                a[u] = 0;
+                if (i0 + u >= t.mine) continue;
+                Io::unpack(raw[u], f[u]);
+                af.template apply<ACT>(f[u]);
+                float m = 0.0f;
+#pragma unroll
+                for (int j = 0; j < H; ++j) m = magnitude(m, f[u][j]);
+                a[u] = magnitude_bits(m);
+            }
+            if (!by_lanes) {
+                uint32_t* row = top + buf * U * t.rows + t.r;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u < t.mine) atomicMax(row + u * t.rows, a[u]);
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u < t.mine) a[u] = row[u * t.rows];
+                // the other buffer was read before this barrier: clear it for the next turn
+                for (int i = threadIdx.x; i < U * t.rows; i += kNormThreads) top[(buf ^ 1) * U * t.rows + i] = 0;
+                __syncthreads();
+            } else if (t.vpr == 32) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) a[u] = warp_max(a[u]);
+            } else {
+                for (int o = 1; o < t.vpr; o <<= 1)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
+            }
+            RowScale rs[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < t.mine) {
+                    quantise_store<VEC>(p.q + (t.base + (i0 + u) * t.step) * VEC, f[u], rs[u]);
+                    if (t.v == 0) scales[(i0 + u) * t.rows] = rs[u].scale;
+                }
         }
     }
 }
@@ -1018,6 +1353,20 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     p = t;
 }
 
+// Two passes: pixel ranges that fill the SMs once, four CTAs to each (three backward).
+void norm_pick_two_pass(NormParams& p, int mode, int num_sms) {
+    const int vecs = p.C / p.vec;
+    if (p.vec == 1 || vecs > kNormThreads) return;
+    const int rows = kNormThreads / vecs;
+    long long splits = static_cast<long long>(num_sms) * (mode == kNormBackward ? 3 : 4) / p.N;
+    const long long most = p.P / (2LL * rows);  // two pixels a thread at least
+    if (splits > most) splits = most;
+    p.two_pass = 1;
+    p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    p.pix_base = p.P / p.splits;
+    p.pix_more = p.P % p.splits;
+}
+
 bool norm_resident_runs(const NormParams& p, int mode) {
     int clusters = 0;
     with_resident(p, mode, [&](auto* fn) {
@@ -1034,13 +1383,65 @@ bool norm_resident_runs(const NormParams& p, int mode) {
     return clusters > 0;
 }
 
-size_t norm_workspace_bytes(const NormParams& p) {  // of the streaming form, or the backward partials
-    return (static_cast<size_t>(p.N) * p.splits * p.C + static_cast<size_t>(p.N) * p.G) * sizeof(float2) +
+// Partials of channels (or, forward in two passes, of groups), then per group and range, then the
+// statistics of the form that joins them in a kernel of its own.
+size_t norm_workspace_bytes(const NormParams& p) {
+    return norm_part_entries(p) * sizeof(float2) + norm_ab_entries(p) * sizeof(float2) +
            2 * static_cast<size_t>(p.N) * p.G * sizeof(float);
 }
 
+size_t norm_part_entries(const NormParams& p) { return static_cast<size_t>(p.N) * p.splits * p.C; }
+size_t norm_ab_entries(const NormParams& p) { return static_cast<size_t>(p.N) * p.G * (p.two_pass ? p.splits : 1); }
+
+namespace {
+
+template <int MODE>
+int range_sums_smem(const NormParams& p) {
+    const int vpr = p.C / p.vec, rows = kNormThreads / vpr;
+    const int entries = MODE == kNormBackward ? (res_warp_rows(vpr) ? kNormThreads / 32 : rows) * p.C
+                                              : rows * vpr * (p.vec / res_lump(p));
+    return entries * 8;  // 16 KB at most
+}
+
+template <int MODE>
+cudaError_t launch_two_pass(const NormParams& p, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    const unsigned grid = static_cast<unsigned>(p.N) * p.splits;
+    const int extra = MODE == kNormBackward && p.dgamma != nullptr ? (p.C + 31) / 32 : 0;
+    const int vpr = p.C / p.vec, rows = kNormThreads / vpr;
+    const int joined = p.G * 8 + (MODE == kNormInt8 ? 2 * 4 * rows * 4 : 0);
+    const int apply_smem = joined > kNormThreads * 8 ? joined : kNormThreads * 8;
+    const auto run = [&](auto* sums, auto* apply) {
+        sums<<<grid, kNormThreads, range_sums_smem<MODE>(p), stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid + extra);
+        cfg.blockDim = dim3(kNormThreads);
+        cfg.dynamicSmemBytes = apply_smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, apply, p, extra);
+    };
+    with_act(p.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        constexpr int SA = MODE == kNormBackward ? A : static_cast<int>(CONV_ACT_NONE);  // forward sums need no activation
+        constexpr int SM = MODE == kNormBackward ? kNormBackward : kNormForward;
+        if (p.bf16) run(norm_range_sums_kernel<__nv_bfloat16, SM, SA>, norm_range_apply_kernel<__nv_bfloat16, MODE, A>);
+        else run(norm_range_sums_kernel<float, SM, SA>, norm_range_apply_kernel<float, MODE, A>);
+    });
+    return e;
+}
+
+}  // namespace
+
 cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t stream) {
     if (p.chunk != 0) return launch_resident(p, p.q != nullptr ? kNormInt8 : kNormForward, stream);
+    if (p.two_pass) return p.q != nullptr ? launch_two_pass<kNormInt8>(p, stream) : launch_two_pass<kNormForward>(p, stream);
     const dim3 grid = stream_grid(p);
     with_types(p, [&](auto t, auto vec) {
         norm_moments_kernel<decltype(t), vec.value><<<grid, kNormThreads, 0, stream>>>(p);
@@ -1068,6 +1469,7 @@ cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t 
         if (p.dgamma != nullptr) norm_grad_channels_kernel<<<(p.C + 31) / 32, 512, 0, stream>>>(p);
         return cudaGetLastError();
     }
+    if (p.two_pass) return launch_two_pass<kNormBackward>(p, stream);
     const dim3 grid = stream_grid(p);
     with_types(p, [&](auto t, auto vec) {
         with_act(p.act, [&](auto act) {

@@ -22,9 +22,9 @@ bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u
 void carve_workspace(NormParams& p, void* workspace) {
     if (p.chunk != 0 && p.dy == nullptr) return;  // resident forward passes need none
     p.part = static_cast<float2*>(workspace);
-    p.ab = p.part + static_cast<size_t>(p.N) * p.splits * p.C;
-    if (p.mean == nullptr) {
-        p.mean = reinterpret_cast<float*>(p.ab + static_cast<size_t>(p.N) * p.G);
+    p.ab = p.part + norm_part_entries(p);
+    if (p.mean == nullptr && !p.two_pass) {
+        p.mean = reinterpret_cast<float*>(p.ab + norm_ab_entries(p));
         p.rstd = p.mean + static_cast<size_t>(p.N) * p.G;
     }
 }
@@ -120,6 +120,7 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
         m = p;
         norm_pick_resident(m, mode, pl->num_sms, smem_optin);
         if (m.chunk != 0 && pl->device >= 0 && !norm_resident_runs(m, mode)) m = p;
+        if (m.chunk == 0) norm_pick_two_pass(m, mode, pl->num_sms);
     }
     *out = pl;
     return CONV_OK;

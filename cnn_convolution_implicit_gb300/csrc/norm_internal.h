@@ -19,12 +19,13 @@ struct NormParams {
     int act;      // conv_act
     int bf16;     // element type of x, y, dy, dx (else FP32)
     int vec;      // elements per access: 16 bytes where every pixel starts on 16 bytes, else 1
-    int splits;   // pixel ranges per image: of the streaming sums, or the CTAs of a resident cluster
-    // resident form (0 chunk: streaming): a cluster of `splits` CTAs holds `chunk` channels of an image
+    int splits;   // pixel ranges per image, or the CTAs of a resident cluster
+    int two_pass; // two passes over pixel ranges (else, without a chunk, by channel)
+    // resident form (0 chunk: another): a cluster of `splits` CTAs holds `chunk` channels of an image
     int chunk;
     int items;       // 16-byte vectors a thread holds of each tensor
     int smem_bytes;
-    int pix_base, pix_more;  // pixels of a CTA of the cluster, and how many CTAs have one more
+    int pix_base, pix_more;  // pixels of a CTA of the cluster or of a range, and how many have one more
     const void* x;
     const void* dy;
     const float* gamma;  // nullptr: 1
@@ -37,7 +38,7 @@ struct NormParams {
     float* dgamma;       // [C]
     float* dbeta;        // [C]
     float2* part;        // workspace [N][splits][C]
-    float2* ab;          // workspace [N][G] (backward)
+    float2* ab;          // workspace [N][G] or, in two passes, [N][G][splits] (backward)
 };
 
 constexpr int kResThreads = 256;     // of a resident CTA
@@ -46,6 +47,9 @@ constexpr int kResMaxCluster = 16;
 enum NormMode { kNormForward = 0, kNormInt8 = 1, kNormBackward = 2 };
 
 size_t norm_workspace_bytes(const NormParams& p);
+size_t norm_part_entries(const NormParams& p);
+size_t norm_ab_entries(const NormParams& p);
+void norm_pick_two_pass(NormParams& p, int mode, int num_sms);
 // Fills the resident form's fields for a mode, or leaves chunk 0 where it does not fit.
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin);
 // Whether the device runs a cluster of that shape (called once per plan, with its device current).
