@@ -223,7 +223,16 @@ struct Affine {
         }
     }
     template <typename F>
-    __device__ __forceinline__ void set(int c, F&& stats) {  // stats(channel): (mean, rstd)
+    __device__ __forceinline__ void set(int c, int cpg, F&& stats) {  // stats(channel): (mean, rstd)
+        if (cpg % VEC == 0) {  // the vector lies in one group
+            const float2 st = stats(c);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                minus_mean[i] = f2_dup(-st.x);
+                a[i] = f2_mul(a[i], f2_dup(st.y));
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const float2 lo = stats(c + 2 * i), hi = 2 * i + 1 < VEC ? stats(c + 2 * i + 1) : make_float2(0.0f, 0.0f);
@@ -246,11 +255,13 @@ struct Grad {
     template <typename F>
     __device__ __forceinline__ void set(const NormParams& p, int c, F&& stats) {
         float m[2 * H], r[2 * H], g[2 * H], be[2 * H];
+        const bool one = p.cpg % VEC == 0;  // the vector lies in one group
+        const float2 first = stats(c);
 #pragma unroll
         for (int i = 0; i < 2 * H; ++i) {
             m[i] = r[i] = g[i] = be[i] = 0.0f;
             if (i < VEC) {
-                const float2 st = stats(c + i);
+                const float2 st = one ? first : stats(c + i);
                 m[i] = -st.x;
                 r[i] = st.y;
                 g[i] = p.gamma ? __ldg(p.gamma + c + i) : 1.0f;
@@ -282,13 +293,15 @@ struct GroupMeans {
     static constexpr int H = (VEC + 1) / 2;
     f2 minus_a[H], minus_b[H];
     template <typename F>
-    __device__ __forceinline__ void set(int c, F&& means) {
+    __device__ __forceinline__ void set(int c, int cpg, F&& means) {
         float a[2 * H], b[2 * H];
+        const bool one = cpg % VEC == 0;
+        const float2 first = means(c);
 #pragma unroll
         for (int i = 0; i < 2 * H; ++i) {
             a[i] = b[i] = 0.0f;
             if (i < VEC) {
-                const float2 m = means(c + i);
+                const float2 m = one ? first : means(c + i);
                 a[i] = -m.x;
                 b[i] = -m.y;
             }
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const NormPara
     auto* y = reinterpret_cast<typename Io::Raw*>(p.y) + base;
     Affine<VEC> f;
     f.load(p, l.v * VEC);
-    f.set(l.v * VEC, [&](int c) { return stats_of(p, n, c); });
+    f.set(l.v * VEC, p.cpg, [&](int c) { return stats_of(p, n, c); });
 #pragma unroll 4
     for (int px = p0 + l.r; px < p1; px += l.rows) {
         f2 v[Affine<VEC>::H];
@@ -349,7 +362,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_int8_kernel(const Nor
         const auto value = [&](int v, f2 (&f)[Affine<VEC>::H]) {
             Affine<VEC> af;
             af.load(p, v * VEC);
-            af.set(v * VEC, [&](int c) { return stats_of(p, n, c); });
+            af.set(v * VEC, p.cpg, [&](int c) { return stats_of(p, n, c); });
             Io::unpack(x[v], f);
             af.template apply<ACT>(f);
         };
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_apply_kernel(const Nor
     Grad<VEC> g;
     GroupMeans<VEC> gm;
     g.set(p, l.v * VEC, [&](int c) { return stats_of(p, n, c); });
-    gm.set(l.v * VEC, [&](int c) { return p.ab[n * p.G + c / p.cpg]; });
+    gm.set(l.v * VEC, p.cpg, [&](int c) { return p.ab[n * p.G + c / p.cpg]; });
 #pragma unroll 2
     for (int px = p0 + l.r; px < p1; px += l.rows) {
         f2 v[Grad<VEC>::H], d[Grad<VEC>::H];
@@ -547,7 +560,7 @@ __host__ __device__ inline int res_pixels(const NormParams& p) { return (p.P + p
 
 // Shared memory of a resident CTA.
 struct ResSmem {
-    uint4* x;        // the items [items][kResThreads]
+    uint4* x;        // the items [items][threads]
     uint4* dy;       // backward: those of dy
     float2* part;    // forward: (mean, M2) [rows][vectors * lumps]; backward: (sum u, sum u h) [rows][chunk]
     float2* recv;    // per group and cluster CTA [groups][kResMaxCluster]
@@ -557,14 +570,14 @@ struct ResSmem {
 
 template <int MODE>
 __host__ __device__ inline int res_part_entries(const NormParams& p) {
-    const int vpr = p.chunk / p.vec, rows = kResThreads / vpr;
-    if (MODE == kNormBackward) return (res_warp_rows(vpr) ? kResThreads / 32 : rows) * p.chunk;
+    const int vpr = p.chunk / p.vec, rows = res_threads(MODE) / vpr;
+    if (MODE == kNormBackward) return (res_warp_rows(vpr) ? res_threads(MODE) / 32 : rows) * p.chunk;
     return rows * vpr * (p.vec / res_lump(p));
 }
 
 template <int MODE>
 __host__ __device__ inline size_t res_smem_bytes(const NormParams& p) {
-    return static_cast<size_t>(MODE == kNormBackward ? 2 : 1) * p.items * kResThreads * 16 +
+    return static_cast<size_t>(MODE == kNormBackward ? 2 : 1) * p.items * res_threads(MODE) * 16 +
            static_cast<size_t>(res_part_entries<MODE>(p)) * 8 + static_cast<size_t>(res_groups(p)) * (kResMaxCluster + 1) * 8 +
            (MODE == kNormInt8 ? static_cast<size_t>(res_pixels(p)) * 4 : 0);
 }
@@ -573,8 +586,8 @@ template <int MODE>
 __device__ __forceinline__ ResSmem res_carve(uint8_t* raw, const NormParams& p) {
     ResSmem s;
     s.x = reinterpret_cast<uint4*>(raw);
-    s.dy = s.x + static_cast<size_t>(p.items) * kResThreads;
-    s.part = reinterpret_cast<float2*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * kResThreads : s.dy);
+    s.dy = s.x + static_cast<size_t>(p.items) * res_threads(MODE);
+    s.part = reinterpret_cast<float2*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * res_threads(MODE) : s.dy);
     s.recv = s.part + res_part_entries<MODE>(p);
     s.result = s.recv + res_groups(p) * kResMaxCluster;
     s.top = reinterpret_cast<uint32_t*>(s.result + res_groups(p));
@@ -708,8 +721,9 @@ __device__ __forceinline__ void cta_group_grads(const NormParams& p, int vpr, in
 }
 
 template <typename T, int MODE, int ACT>
-__global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const NormParams p) {
+__global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(const NormParams p) {
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+    constexpr int kThreads = res_threads(MODE);
     using Io = VecIo<T, VEC>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const ResSmem sm = res_carve<MODE>(smem_raw, p);
@@ -719,7 +733,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     const int n = unit / chunks;
     const int c0 = (unit - n * chunks) * p.chunk;
     const int vpr = p.chunk / VEC;           // vectors of a pixel
-    const int rows = kResThreads / vpr;
+    const int rows = kThreads / vpr;
     const int r = threadIdx.x / vpr, v = threadIdx.x - r * vpr;
     int p0, p1;
     res_range(p, rank, p0, p1);
@@ -742,8 +756,8 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
             const int end = min((b + 1) * batch, mine);
 #pragma unroll 2
             for (int i = b * batch; i < end; ++i) {
-                copy_async16(dst + i * (kResThreads * 16), x + i * step);
-                if constexpr (MODE == kNormBackward) copy_async16(dst2 + i * (kResThreads * 16), dy + i * step);
+                copy_async16(dst + i * (kThreads * 16), x + i * step);
+                if constexpr (MODE == kNormBackward) copy_async16(dst2 + i * (kThreads * 16), dy + i * step);
             }
             copy_commit();
         }
@@ -789,7 +803,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
             }
 #pragma unroll 4
             for (int i = from; i < to; ++i) {
-                Io::unpack(items[i * kResThreads], f);
+                Io::unpack(items[i * kThreads], f);
                 mo.add(f);
             }
         });
@@ -801,10 +815,11 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
 #pragma unroll
         for (int i = 0; i < H; ++i) s1[i] = s2[i] = 0;
         sweep_all([&](int from, int to) {
+#pragma unroll 2
             for (int i = from; i < to; ++i) {
                 f2 f[H], d[H];
-                Io::unpack(items[i * kResThreads], f);
-                Io::unpack(items_dy[i * kResThreads], d);
+                Io::unpack(items[i * kThreads], f);
+                Io::unpack(items_dy[i * kThreads], d);
                 grad.template apply<ACT>(f, d);
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
@@ -820,7 +835,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
 
     // The cluster's groups, every CTA for itself in the same order.
     if constexpr (MODE == kNormInt8)
-        for (int i = threadIdx.x; i < p1 - p0; i += kResThreads) sm.top[i] = 0;
+        for (int i = threadIdx.x; i < p1 - p0; i += kThreads) sm.top[i] = 0;
     if (p.splits > 1) {
         res_cluster_arrive();
         res_cluster_wait();
@@ -830,7 +845,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
     const int wide = segment_width(p.splits), at_once = 32 / wide, k = lane & (wide - 1);
     const float cnt = k < p.splits ? static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg) : 0.0f;
-    for (int gfirst = warp * at_once; gfirst < groups; gfirst += kResThreads / 32 * at_once) {
+    for (int gfirst = warp * at_once; gfirst < groups; gfirst += kThreads / 32 * at_once) {
         const int g = gfirst + lane / wide;
         const float2 o = g < groups && k < p.splits ? sm.recv[g * kResMaxCluster + k] : make_float2(0.0f, 0.0f);
         float2 res;
@@ -853,23 +868,24 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
 
     const auto result = [&](int c) { return sm.result[(c - c0) / p.cpg]; };
     if constexpr (MODE == kNormForward) {
-        af.set(my_c, result);
+        af.set(my_c, p.cpg, result);
         T* y = static_cast<T*>(p.y) + base;
 #pragma unroll 4
         for (int i = 0; i < mine; ++i) {
             f2 f[H];
-            Io::unpack(items[i * kResThreads], f);
+            Io::unpack(items[i * kThreads], f);
             af.template apply<ACT>(f);
             *reinterpret_cast<uint4*>(y + i * step) = Io::pack(f);
         }
     } else if constexpr (MODE == kNormBackward) {
         GroupMeans<VEC> gm;
-        gm.set(my_c, result);
+        gm.set(my_c, p.cpg, result);
         T* dx = static_cast<T*>(p.y) + base;
+#pragma unroll 2
         for (int i = 0; i < mine; ++i) {
             f2 f[H], d[H];
-            Io::unpack(items[i * kResThreads], f);
-            Io::unpack(items_dy[i * kResThreads], d);
+            Io::unpack(items[i * kThreads], f);
+            Io::unpack(items_dy[i * kThreads], d);
             grad.template apply<ACT>(f, d);
             gm.dx(f, d, grad);
             *reinterpret_cast<uint4*>(dx + i * step) = Io::pack(f);
@@ -877,11 +893,11 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
     } else {
         // 8-bit output (chunk = C: whole pixels here).  A pixel on 1, 2, 4, ... 32 neighbouring lanes
         // finds its largest magnitude by shuffles; any other width through shared memory.
-        af.set(my_c, result);
+        af.set(my_c, p.cpg, result);
         float* scales = p.scale + static_cast<long long>(n) * p.P + p0 + r;
         int8_t* q = p.q + base;
         const auto value = [&](int i, f2 (&f)[H]) {
-            Io::unpack(items[i * kResThreads], f);
+            Io::unpack(items[i * kThreads], f);
             af.template apply<ACT>(f);
             float top = 0.0f;
 #pragma unroll
@@ -932,7 +948,7 @@ __global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const Nor
 }
 
 // ---------------------------------------------------------------- two passes
-constexpr int kTwoBatch = 8;  // 16-byte loads a thread has under way
+constexpr int kTwoBatch = 4;  // vectors a thread has under way (of each tensor)
 
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -977,20 +993,18 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
             Io::unpack(__ldg(x), f);
             mo.start(f);
         }
-        int i = 0;
-        for (; i + kTwoBatch <= t.mine; i += kTwoBatch) {
-            uint4 raw[kTwoBatch];
+        constexpr int B = 2 * kTwoBatch;
+        for (int i = 0; i < t.mine; i += B) {
+            uint4 raw[B];
 #pragma unroll
-            for (int k = 0; k < kTwoBatch; ++k) raw[k] = __ldg(x + (i + k) * t.step);
+            for (int k = 0; k < B; ++k)
+                if (i + k < t.mine) raw[k] = __ldg(x + (i + k) * t.step);
 #pragma unroll
-            for (int k = 0; k < kTwoBatch; ++k) {
-                Io::unpack(raw[k], f);
-                mo.add(f);
-            }
-        }
-        for (; i < t.mine; ++i) {
-            Io::unpack(__ldg(x + i * t.step), f);
-            mo.add(f);
+            for (int k = 0; k < B; ++k)
+                if (i + k < t.mine) {
+                    Io::unpack(raw[k], f);
+                    mo.add(f);
+                }
         }
         float mean[VEC], m2[VEC];
         mo.finish(t.mine, mean, m2);
@@ -1016,19 +1030,19 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
                 s2[j] = f2_fma(d[j], f[j], s2[j]);
             }
         };
-        constexpr int B = 4;
-        int i = 0;
-        for (; i + B <= t.mine; i += B) {
+        constexpr int B = kTwoBatch;
+        for (int i = 0; i < t.mine; i += B) {
             uint4 a[B], b[B];
 #pragma unroll
-            for (int k = 0; k < B; ++k) {
-                a[k] = __ldg(x + (i + k) * t.step);
-                b[k] = __ldg(dy + (i + k) * t.step);
-            }
+            for (int k = 0; k < B; ++k)
+                if (i + k < t.mine) {
+                    a[k] = __ldg(x + (i + k) * t.step);
+                    b[k] = __ldg(dy + (i + k) * t.step);
+                }
 #pragma unroll
-            for (int k = 0; k < B; ++k) take(a[k], b[k]);
+            for (int k = 0; k < B; ++k)
+                if (i + k < t.mine) take(a[k], b[k]);
         }
-        for (; i < t.mine; ++i) take(__ldg(x + i * t.step), __ldg(dy + i * t.step));
         float2* out = p.part + (static_cast<long long>(t.n) * p.splits + t.s) * p.C;
         const auto store = [&](int g, float2 val, int wide) {
             if ((lane & (wide - 1)) == 0) p.ab[(static_cast<long long>(t.n) * p.G + g) * p.splits + t.s] = val;
@@ -1042,7 +1056,7 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
 // Second pass.  Joins the ranges of the image's groups, then writes the range backwards.  Backward:
 // the first `extra` CTAs write dgamma and dbeta instead, 32 channels each.
 template <typename T, int MODE, int ACT>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_range_apply_kernel(const NormParams p, int extra) {
+__global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) norm_range_apply_kernel(const NormParams p, int extra) {
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
     using Io = VecIo<T, VEC>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -1119,7 +1133,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_range_apply_kernel(const
     __syncthreads();
     const auto result = [&](int c) { return joined[c / p.cpg]; };
     if constexpr (MODE == kNormForward) {
-        af.set(my_c, result);
+        af.set(my_c, p.cpg, result);
         uint4* y = static_cast<uint4*>(p.y) + t.base;
         const auto put = [&](const uint4& raw, int i) {
             f2 f[H];
@@ -1127,18 +1141,19 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_range_apply_kernel(const
             af.template apply<ACT>(f);
             store_past(y + i * t.step, Io::pack(f));
         };
-        int i = t.mine;
-        for (; i >= kTwoBatch; i -= kTwoBatch) {
-            uint4 raw[kTwoBatch];
+        constexpr int B = kTwoBatch;
+        for (int i = t.mine; i > 0; i -= B) {
+            uint4 raw[B];
 #pragma unroll
-            for (int k = 0; k < kTwoBatch; ++k) raw[k] = load_last(x + (i - 1 - k) * t.step);
+            for (int k = 0; k < B; ++k)
+                if (i > k) raw[k] = load_last(x + (i - 1 - k) * t.step);
 #pragma unroll
-            for (int k = 0; k < kTwoBatch; ++k) put(raw[k], i - 1 - k);
+            for (int k = 0; k < B; ++k)
+                if (i > k) put(raw[k], i - 1 - k);
         }
-        for (; i > 0; --i) put(load_last(x + (i - 1) * t.step), i - 1);
     } else if constexpr (MODE == kNormBackward) {
         GroupMeans<VEC> gm;
-        gm.set(my_c, result);
+        gm.set(my_c, p.cpg, result);
         const uint4* dy = static_cast<const uint4*>(p.dy) + t.base;
         uint4* dx = static_cast<uint4*>(p.y) + t.base;
         const auto put = [&](const uint4& a, const uint4& b, int i) {
@@ -1149,24 +1164,24 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_range_apply_kernel(const
             gm.dx(f, d, grad);
             store_past(dx + i * t.step, Io::pack(f));
         };
-        constexpr int B = 4;
-        int i = t.mine;
-        for (; i >= B; i -= B) {
+        constexpr int B = kTwoBatch / 2;
+        for (int i = t.mine; i > 0; i -= B) {
             uint4 a[B], b[B];
 #pragma unroll
-            for (int k = 0; k < B; ++k) {
-                a[k] = load_last(x + (i - 1 - k) * t.step);
-                b[k] = load_last(dy + (i - 1 - k) * t.step);
-            }
+            for (int k = 0; k < B; ++k)
+                if (i > k) {
+                    a[k] = load_last(x + (i - 1 - k) * t.step);
+                    b[k] = load_last(dy + (i - 1 - k) * t.step);
+                }
 #pragma unroll
-            for (int k = 0; k < B; ++k) put(a[k], b[k], i - 1 - k);
+            for (int k = 0; k < B; ++k)
+                if (i > k) put(a[k], b[k], i - 1 - k);
         }
-        for (; i > 0; --i) put(load_last(x + (i - 1) * t.step), load_last(dy + (i - 1) * t.step), i - 1);
     } else {
         // A pixel on 1, 2, 4, ... 32 neighbouring lanes finds its largest magnitude by shuffles, any
-        // other width through shared memory; four pixels under way at a time.
-        af.set(my_c, result);
-        constexpr int U = 4;
+        // other width through shared memory; two pixels under way at a time.
+        af.set(my_c, p.cpg, result);
+        constexpr int U = 2;
         float* scales = p.scale + static_cast<long long>(t.n) * p.P + t.p0 + t.r;
         const bool by_lanes = (t.vpr & (t.vpr - 1)) == 0 && t.vpr <= 32;
         uint32_t* top = reinterpret_cast<uint32_t*>(joined + p.G);  // [2][U][rows]
@@ -1277,12 +1292,12 @@ size_t resident_smem(const NormParams& p, int mode) {
 
 template <typename K>
 cudaError_t resident_config(K* fn, const NormParams& p, cudaStream_t stream, cudaLaunchConfig_t& cfg,
-                            cudaLaunchAttribute (&attr)[1]) {
+                            int mode, cudaLaunchAttribute (&attr)[1]) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem_bytes);
     if (e == cudaSuccess && p.splits > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     cfg = cudaLaunchConfig_t();
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.N) * (p.C / p.chunk) * p.splits));
-    cfg.blockDim = dim3(kResThreads);
+    cfg.blockDim = dim3(res_threads(mode));
     cfg.dynamicSmemBytes = p.smem_bytes;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1299,7 +1314,7 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
     with_resident(p, mode, [&](auto* fn) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[1];
-        e = resident_config(fn, p, stream, cfg, attr);
+        e = resident_config(fn, p, stream, cfg, mode, attr);
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, p);
     });
     return e;
@@ -1326,8 +1341,9 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
             if (c * es >= 64) break;
         }
     }
-    if (chunk == 0 || chunk / p.vec > kResThreads) return;
-    const int rows = kResThreads / (chunk / p.vec);
+    const int threads = res_threads(mode);
+    if (chunk == 0 || chunk / p.vec > threads) return;
+    const int rows = threads / (chunk / p.vec);
     const long long units = static_cast<long long>(p.N) * (p.C / chunk);
     NormParams t = p;
     t.chunk = chunk;
@@ -1335,7 +1351,7 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
         t.splits = cluster;
         const int pixels = res_pixels(t);
         t.items = (pixels + rows - 1) / rows;
-        if (static_cast<double>(t.items) * tensors * kResThreads * 16 > limit) return false;
+        if (static_cast<double>(t.items) * tensors * threads * 16 > limit) return false;
         t.smem_bytes = static_cast<int>(resident_smem(t, mode));
         return t.smem_bytes <= limit;
     };
@@ -1372,7 +1388,7 @@ bool norm_resident_runs(const NormParams& p, int mode) {
     with_resident(p, mode, [&](auto* fn) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[1];
-        if (resident_config(fn, p, nullptr, cfg, attr) != cudaSuccess ||
+        if (resident_config(fn, p, nullptr, cfg, mode, attr) != cudaSuccess ||
             (p.splits > 1 && cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) != cudaSuccess)) {
             cudaGetLastError();
             clusters = 0;
@@ -1409,7 +1425,7 @@ cudaError_t launch_two_pass(const NormParams& p, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>(p.N) * p.splits;
     const int extra = MODE == kNormBackward && p.dgamma != nullptr ? (p.C + 31) / 32 : 0;
     const int vpr = p.C / p.vec, rows = kNormThreads / vpr;
-    const int joined = p.G * 8 + (MODE == kNormInt8 ? 2 * 4 * rows * 4 : 0);
+    const int joined = p.G * 8 + (MODE == kNormInt8 ? 2 * 2 * rows * 4 : 0);
     const int apply_smem = joined > kNormThreads * 8 ? joined : kNormThreads * 8;
     const auto run = [&](auto* sums, auto* apply) {
         sums<<<grid, kNormThreads, range_sums_smem<MODE>(p), stream>>>(p);

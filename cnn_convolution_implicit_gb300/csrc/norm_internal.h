@@ -41,10 +41,12 @@ struct NormParams {
     float2* ab;          // workspace [N][G] or, in two passes, [N][G][splits] (backward)
 };
 
-constexpr int kResThreads = 256;     // of a resident CTA
 constexpr int kResMaxCluster = 16;
 
 enum NormMode { kNormForward = 0, kNormInt8 = 1, kNormBackward = 2 };
+
+// Threads of a resident CTA, two to an SM: what 64 or 80 registers leave room for.
+__host__ __device__ constexpr int res_threads(int mode) { return mode == kNormBackward ? 256 : 256; }
 
 size_t norm_workspace_bytes(const NormParams& p);
 size_t norm_part_entries(const NormParams& p);
