@@ -104,7 +104,7 @@ def lib():
             L.conv_check_wait_timeout.restype = c_int
             c_ull = ctypes.c_ulonglong
             L.conv_group_norm_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 5 + [ctypes.c_float, c_int, c_int]
-            L.conv_group_norm_workspace.argtypes = [vp, ctypes.POINTER(c_ull)]
+            L.conv_group_norm_workspace.argtypes = [vp] + [ctypes.POINTER(c_ull)] * 3
             L.conv_group_norm_forward.argtypes = [vp] * 8
             L.conv_group_norm_forward_int8.argtypes = [vp] * 9
             L.conv_group_norm_backward.argtypes = [vp] * 11

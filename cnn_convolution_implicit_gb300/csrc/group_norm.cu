@@ -1271,14 +1271,22 @@ dim3 stream_grid(const NormParams& p) {
 
 namespace {
 
+// Each kernel with its own record of the shared memory it was given.
+template <typename T, int MODE, int ACT, typename F>
+void with_limits(F&& f) {
+    static SmemLimitCache limits;
+    f(norm_resident_kernel<T, MODE, ACT>, limits);
+}
+
 template <typename F>
 void with_resident(const NormParams& p, int mode, F&& f) {
     with_act(p.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
         const auto with_mode = [&](auto t) {
             using T = decltype(t);
-            if (mode == kNormForward) f(norm_resident_kernel<T, kNormForward, act.value>);
-            else if (mode == kNormInt8) f(norm_resident_kernel<T, kNormInt8, act.value>);
-            else f(norm_resident_kernel<T, kNormBackward, act.value>);
+            if (mode == kNormForward) with_limits<T, kNormForward, A>(f);
+            else if (mode == kNormInt8) with_limits<T, kNormInt8, A>(f);
+            else with_limits<T, kNormBackward, A>(f);
         };
         if (p.bf16) with_mode(__nv_bfloat16());
         else with_mode(float());
@@ -1291,10 +1299,9 @@ size_t resident_smem(const NormParams& p, int mode) {
 }
 
 template <typename K>
-cudaError_t resident_config(K* fn, const NormParams& p, cudaStream_t stream, cudaLaunchConfig_t& cfg,
-                            int mode, cudaLaunchAttribute (&attr)[1]) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem_bytes);
-    if (e == cudaSuccess && p.splits > 8) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t resident_config(K* fn, SmemLimitCache& limits, const NormParams& p, int mode, cudaStream_t stream,
+                            cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[1]) {
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), p.smem_bytes, limits);
     cfg = cudaLaunchConfig_t();
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.N) * (p.C / p.chunk) * p.splits));
     cfg.blockDim = dim3(res_threads(mode));
@@ -1311,10 +1318,10 @@ cudaError_t resident_config(K* fn, const NormParams& p, cudaStream_t stream, cud
 
 cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
-    with_resident(p, mode, [&](auto* fn) {
+    with_resident(p, mode, [&](auto* fn, SmemLimitCache& limits) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[1];
-        e = resident_config(fn, p, stream, cfg, mode, attr);
+        e = resident_config(fn, limits, p, mode, stream, cfg, attr);
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, p);
     });
     return e;
@@ -1385,10 +1392,11 @@ void norm_pick_two_pass(NormParams& p, int mode, int num_sms) {
 
 bool norm_resident_runs(const NormParams& p, int mode) {
     int clusters = 0;
-    with_resident(p, mode, [&](auto* fn) {
+    with_resident(p, mode, [&](auto* fn, SmemLimitCache& limits) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[1];
-        if (resident_config(fn, p, nullptr, cfg, mode, attr) != cudaSuccess ||
+        if (resident_config(fn, limits, p, mode, nullptr, cfg, attr) != cudaSuccess ||
+            cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
             (p.splits > 1 && cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) != cudaSuccess)) {
             cudaGetLastError();
             clusters = 0;

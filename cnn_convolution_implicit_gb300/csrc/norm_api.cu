@@ -29,6 +29,11 @@ void carve_workspace(NormParams& p, void* workspace) {
     }
 }
 
+size_t workspace_bytes(const conv_group_norm_plan* pl, int mode) {
+    const NormParams& p = pl->np[mode];
+    return p.chunk != 0 && mode != kNormBackward ? 0 : norm_workspace_bytes(p);  // resident forward passes need none
+}
+
 conv_status check_device(const conv_group_norm_plan* pl) {
     if (pl->device < 0) return CONV_ERR_CUDA;  // host-only plan
     int cur = -1;
@@ -126,24 +131,27 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
     return CONV_OK;
 }
 
-conv_status conv_group_norm_workspace(const conv_group_norm_plan* p, unsigned long long* bytes) {
-    if (p == nullptr || bytes == nullptr) return CONV_ERR_INVALID_ARG;
-    *bytes = 0;
-    for (const NormParams& m : p->np)
-        if (norm_workspace_bytes(m) > *bytes) *bytes = norm_workspace_bytes(m);
+conv_status conv_group_norm_workspace(const conv_group_norm_plan* p, unsigned long long* forward,
+                                      unsigned long long* forward_int8, unsigned long long* backward) {
+    if (p == nullptr) return CONV_ERR_INVALID_ARG;
+    unsigned long long* to[3] = {forward, forward_int8, backward};
+    for (int mode = 0; mode < 3; ++mode)
+        if (to[mode] != nullptr) *to[mode] = workspace_bytes(p, mode);
     return CONV_OK;
 }
 
 conv_status conv_group_norm_forward(conv_group_norm_plan* p, const void* x, const float* gamma, const float* beta,
                                     void* y, float* stats, void* workspace, void* stream) {
-    if (p == nullptr || x == nullptr || y == nullptr || workspace == nullptr) return CONV_ERR_INVALID_ARG;
+    if (p == nullptr || x == nullptr || y == nullptr || (workspace == nullptr && workspace_bytes(p, kNormForward) != 0))
+        return CONV_ERR_INVALID_ARG;
     return forward(p, x, gamma, beta, y, nullptr, nullptr, stats, workspace, stream);
 }
 
 conv_status conv_group_norm_forward_int8(conv_group_norm_plan* p, const void* x, const float* gamma,
                                          const float* beta, void* q, float* q_scale, float* stats, void* workspace,
                                          void* stream) {
-    if (p == nullptr || x == nullptr || q == nullptr || q_scale == nullptr || workspace == nullptr)
+    if (p == nullptr || x == nullptr || q == nullptr || q_scale == nullptr ||
+        (workspace == nullptr && workspace_bytes(p, kNormInt8) != 0))
         return CONV_ERR_INVALID_ARG;
     return forward(p, x, gamma, beta, nullptr, q, q_scale, stats, workspace, stream);
 }

@@ -7,7 +7,6 @@ allocated on that stream, so torch's allocator reuses them in its order.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 from . import binding
@@ -16,10 +15,23 @@ from .binding import CONV_BF16, CONV_F32, ConvError, _plan_status, lib
 ACTS = {"none": 0, "relu": 1, "silu": 2}
 _DTYPES = {"f32": CONV_F32, "bf16": CONV_BF16}
 
+# torch, imported with the first plan or call (as in binding.py, importing the package needs no
+# torch), and what every call takes from it.
+_t = None
+_raw_stream = None
+
+
+def _torch():
+    global _t, _raw_stream
+    if _t is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _t = torch
+    return _t
+
 
 def _torch_dtypes():
-    import torch
-    return {"f32": torch.float32, "bf16": torch.bfloat16}
+    return {"f32": _torch().float32, "bf16": _torch().bfloat16}
 
 
 def _choice(value, table, name):
@@ -28,9 +40,10 @@ def _choice(value, table, name):
     return table[value]
 
 
-def _need(t, name, shape, dtype, device):
-    if t is None or t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, tuple(shape), device))
+def _need(t, name, shape, dtype, dev):
+    """A contiguous tensor of that shape and type on CUDA device ``dev``."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d" % (name, dtype, tuple(shape), dev))
 
 
 def _need_any(t, name, dtypes):
@@ -42,17 +55,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream):
-    """(the stream to launch on, a context that allocates on it)."""
-    import torch
+def _on(stream, dev, run):
+    """run(raw stream): on torch's current stream, or on ``stream`` with allocations made on it."""
     if stream is None:
-        return None, contextlib.nullcontext()
-    return stream, torch.cuda.stream(stream)
+        return run(_raw_stream(dev))
+    with _t.cuda.stream(stream):
+        return run(stream.cuda_stream)
 
 
-def _handle(stream, device):
-    import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _workspace(nbytes, dev):
+    return _t.empty(nbytes, dtype=_t.uint8, device=dev) if nbytes else None
 
 
 def _check(status, what):
@@ -74,12 +86,14 @@ class GroupNormPlan:
                                              _choice(dtype, _DTYPES, "dtype"), _choice(act, ACTS, "act")),
                "conv_group_norm_plan_create")
         self._plan = h
-        self.shape, self.C, self.groups = (N, H, W, C), C, groups
+        self._L = L
+        torch = _torch()
+        self.shape, self.C, self.groups = torch.Size((N, H, W, C)), C, groups
         self.dtype, self.torch_dtype, self.eps, self.act = dtype, _torch_dtypes()[dtype], eps, act
-        self.stats_shape = (2, N, groups)
-        b = ctypes.c_ulonglong()
-        _check(L.conv_group_norm_workspace(h, ctypes.byref(b)), "conv_group_norm_workspace")
-        self.workspace_bytes = b.value
+        self.stats_shape, self._channels, self._pixels = torch.Size((2, N, groups)), torch.Size((C,)), torch.Size((N * H * W,))
+        b = [ctypes.c_ulonglong() for _ in range(3)]
+        _check(L.conv_group_norm_workspace(h, *[ctypes.byref(v) for v in b]), "conv_group_norm_workspace")
+        self.workspace_bytes = dict(zip(("forward", "forward_int8", "backward"), [v.value for v in b]))
 
     def close(self):
         if self._plan is not None and binding._lib is not None:
@@ -93,90 +107,81 @@ class GroupNormPlan:
             pass
 
     def _inputs(self, x, gamma, beta, stats):
-        import torch
-        if not x.is_cuda:
+        """Checks them; returns x's device."""
+        dev = x.get_device()
+        if dev < 0:
             raise ValueError("x must be a CUDA tensor")
-        _need(x, "x", self.shape, self.torch_dtype, x.device)
-        for t, name in ((gamma, "gamma"), (beta, "beta")):
-            if t is not None:
-                _need(t, name, (self.C,), torch.float32, x.device)
+        _need(x, "x", self.shape, self.torch_dtype, dev)
+        if gamma is not None:
+            _need(gamma, "gamma", self._channels, _t.float32, dev)
+        if beta is not None:
+            _need(beta, "beta", self._channels, _t.float32, dev)
         if stats is not None:
-            _need(stats, "stats", self.stats_shape, torch.float32, x.device)
-
-    def _workspace(self, device):
-        import torch
-        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+            _need(stats, "stats", self.stats_shape, _t.float32, dev)
+        return dev
 
     def forward(self, x, gamma=None, beta=None, y=None, stats=None, stream=None):
         """act(norm(x)); ``stats`` (empty_stats()) receives what backward() reads."""
-        import torch
-        self._inputs(x, gamma, beta, stats)
-        stream, scope = _on(stream)
-        with scope:
-            if y is None:
-                y = torch.empty_like(x)
-            else:
-                _need(y, "y", self.shape, self.torch_dtype, x.device)
-            ws = self._workspace(x.device)
-            _check(lib().conv_group_norm_forward(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(),
-                                                 _ptr(stats), ws.data_ptr(), _handle(stream, x.device)),
-                   "conv_group_norm_forward")
-        return y
+        dev = self._inputs(x, gamma, beta, stats)
+
+        def run(raw):
+            out = _t.empty_like(x) if y is None else y
+            ws = _workspace(self.workspace_bytes["forward"], dev)
+            _check(self._L.conv_group_norm_forward(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(),
+                                                   _ptr(stats), _ptr(ws), raw), "conv_group_norm_forward")
+            return out
+
+        if y is not None:
+            _need(y, "y", self.shape, self.torch_dtype, dev)
+        return _on(stream, dev, run)
 
     __call__ = forward
 
     def forward_int8(self, x, gamma=None, beta=None, q=None, scale=None, stats=None, stream=None):
         """(q, scale): act(norm(x)) as int8 [N][H][W][C] with one FP32 scale per pixel [N*H*W]."""
-        import torch
-        self._inputs(x, gamma, beta, stats)
-        N, H, W, _ = self.shape
-        stream, scope = _on(stream)
-        with scope:
-            if q is None:
-                q = torch.empty(self.shape, dtype=torch.int8, device=x.device)
-            else:
-                _need(q, "q", self.shape, torch.int8, x.device)
-            if scale is None:
-                scale = torch.empty(N * H * W, dtype=torch.float32, device=x.device)
-            else:
-                _need(scale, "scale", (N * H * W,), torch.float32, x.device)
-            ws = self._workspace(x.device)
-            _check(lib().conv_group_norm_forward_int8(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), q.data_ptr(),
-                                                      scale.data_ptr(), _ptr(stats), ws.data_ptr(),
-                                                      _handle(stream, x.device)),
+        dev = self._inputs(x, gamma, beta, stats)
+        if q is not None:
+            _need(q, "q", self.shape, _t.int8, dev)
+        if scale is not None:
+            _need(scale, "scale", self._pixels, _t.float32, dev)
+
+        def run(raw):
+            qo = _t.empty(self.shape, dtype=_t.int8, device=dev) if q is None else q
+            so = _t.empty(self._pixels, dtype=_t.float32, device=dev) if scale is None else scale
+            ws = _workspace(self.workspace_bytes["forward_int8"], dev)
+            _check(self._L.conv_group_norm_forward_int8(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta),
+                                                        qo.data_ptr(), so.data_ptr(), _ptr(stats), _ptr(ws), raw),
                    "conv_group_norm_forward_int8")
-        return q, scale
+            return qo, so
+
+        return _on(stream, dev, run)
 
     def backward(self, dy, x, stats, gamma=None, beta=None, dx=None, dgamma=None, dbeta=None, stream=None):
         """(dx, dgamma, dbeta) from the forward pass's x and stats."""
-        import torch
         if stats is None:
             raise ValueError("stats must be what forward(stats=...) wrote")
-        self._inputs(x, gamma, beta, stats)
-        _need(dy, "dy", self.shape, self.torch_dtype, x.device)
-        stream, scope = _on(stream)
-        with scope:
-            if dx is None:
-                dx = torch.empty_like(x)
-            else:
-                _need(dx, "dx", self.shape, self.torch_dtype, x.device)
-            grads = []
-            for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
-                if t is None:
-                    t = torch.empty(self.C, dtype=torch.float32, device=x.device)
-                else:
-                    _need(t, name, (self.C,), torch.float32, x.device)
-                grads.append(t)
-            ws = self._workspace(x.device)
-            _check(lib().conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(),
-                                                  _ptr(gamma), _ptr(beta), dx.data_ptr(), grads[0].data_ptr(),
-                                                  grads[1].data_ptr(), ws.data_ptr(), _handle(stream, x.device)),
-                   "conv_group_norm_backward")
-        return dx, grads[0], grads[1]
+        dev = self._inputs(x, gamma, beta, stats)
+        _need(dy, "dy", self.shape, self.torch_dtype, dev)
+        if dx is not None:
+            _need(dx, "dx", self.shape, self.torch_dtype, dev)
+        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+            if t is not None:
+                _need(t, name, self._channels, _t.float32, dev)
+
+        def run(raw):
+            out = _t.empty_like(x) if dx is None else dx
+            dg = _t.empty(self._channels, dtype=_t.float32, device=dev) if dgamma is None else dgamma
+            db = _t.empty(self._channels, dtype=_t.float32, device=dev) if dbeta is None else dbeta
+            ws = _workspace(self.workspace_bytes["backward"], dev)
+            _check(self._L.conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(),
+                                                    _ptr(gamma), _ptr(beta), out.data_ptr(), dg.data_ptr(),
+                                                    db.data_ptr(), _ptr(ws), raw), "conv_group_norm_backward")
+            return out, dg, db
+
+        return _on(stream, dev, run)
 
     def empty_stats(self, device="cuda"):
-        import torch
-        return torch.empty(self.stats_shape, dtype=torch.float32, device=device)
+        return _t.empty(self.stats_shape, dtype=_t.float32, device=device)
 
 
 class Int8MatmulPlan:
@@ -191,8 +196,12 @@ class Int8MatmulPlan:
         _check(L.conv_int8_plan_create(ctypes.byref(h), M, N, K, _choice(out, _DTYPES, "out"),
                                        _choice(act, ACTS, "act")), "conv_int8_plan_create")
         self._plan = h
+        self._L = L
+        torch = _torch()
         self.M, self.N, self.K, self.out, self.act = M, N, K, out, act
         self.torch_dtype = _torch_dtypes()[out]
+        self._x, self._w, self._y = torch.Size((M, K)), torch.Size((N, K)), torch.Size((M, N))
+        self._rows, self._cols = torch.Size((M,)), torch.Size((N,))
         b = ctypes.c_ulonglong()
         _check(L.conv_int8_workspace(h, ctypes.byref(b)), "conv_int8_workspace")
         self.workspace_bytes = b.value
@@ -208,53 +217,53 @@ class Int8MatmulPlan:
         except Exception:
             pass
 
-    def _weights(self, w, w_scale, bias, device):
-        import torch
-        _need(w, "w", (self.N, self.K), torch.int8, device)
-        _need(w_scale, "w_scale", (self.N,), torch.float32, device)
+    def _operands(self, x, w, w_scale, bias, y):
+        """Checks all but x's type; returns x's device."""
+        dev = x.get_device()
+        if dev < 0:
+            raise ValueError("x must be a CUDA tensor")
+        _need(x, "x", self._x, x.dtype, dev)
+        _need(w, "w", self._w, _t.int8, dev)
+        _need(w_scale, "w_scale", self._cols, _t.float32, dev)
         if bias is not None:
-            _need(bias, "bias", (self.N,), torch.float32, device)
-
-    def _output(self, y, device):
-        import torch
-        if y is None:
-            return torch.empty((self.M, self.N), dtype=self.torch_dtype, device=device)
-        _need(y, "y", (self.M, self.N), self.torch_dtype, device)
-        return y
+            _need(bias, "bias", self._cols, _t.float32, dev)
+        if y is not None:
+            _need(y, "y", self._y, self.torch_dtype, dev)
+        return dev
 
     def forward(self, x, x_scale, w, w_scale, bias=None, y=None, stream=None):
         """The product of int8 rows x [M][K] with their scales [M]."""
-        import torch
-        _need_any(x, "x", (torch.int8,))
-        _need(x, "x", (self.M, self.K), torch.int8, x.device)
-        _need(x_scale, "x_scale", (self.M,), torch.float32, x.device)
-        self._weights(w, w_scale, bias, x.device)
-        stream, scope = _on(stream)
-        with scope:
-            y = self._output(y, x.device)
-            _check(lib().conv_int8_forward(self._plan, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
-                                           w_scale.data_ptr(), _ptr(bias), y.data_ptr(), _handle(stream, x.device)),
-                   "conv_int8_forward")
-        return y
+        if x.dtype is not _t.int8:
+            raise ValueError("x must be int8")
+        dev = self._operands(x, w, w_scale, bias, y)
+        _need(x_scale, "x_scale", self._rows, _t.float32, dev)
+
+        def run(raw):
+            out = _t.empty(self._y, dtype=self.torch_dtype, device=dev) if y is None else y
+            _check(self._L.conv_int8_forward(self._plan, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
+                                             w_scale.data_ptr(), _ptr(bias), out.data_ptr(), raw), "conv_int8_forward")
+            return out
+
+        return _on(stream, dev, run)
 
     __call__ = forward
 
     def forward_quantize(self, x, w, w_scale, bias=None, y=None, stream=None):
         """The product of BF16 or FP32 rows, brought to 8 bits (quantize_rows) in the call."""
-        import torch
-        _need_any(x, "x", (torch.bfloat16, torch.float32))
-        _need(x, "x", (self.M, self.K), x.dtype, x.device)
-        self._weights(w, w_scale, bias, x.device)
-        stream, scope = _on(stream)
-        with scope:
-            y = self._output(y, x.device)
-            ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=x.device) if self.workspace_bytes else None
-            _check(lib().conv_int8_forward_quantize(self._plan, x.data_ptr(),
-                                                    CONV_BF16 if x.dtype == torch.bfloat16 else CONV_F32,
-                                                    w.data_ptr(), w_scale.data_ptr(), _ptr(bias), y.data_ptr(),
-                                                    _ptr(ws), _handle(stream, x.device)),
+        if x.dtype is not _t.bfloat16 and x.dtype is not _t.float32:
+            raise ValueError("x must be bfloat16 or float32")
+        dev = self._operands(x, w, w_scale, bias, y)
+
+        def run(raw):
+            out = _t.empty(self._y, dtype=self.torch_dtype, device=dev) if y is None else y
+            ws = _workspace(self.workspace_bytes, dev)
+            _check(self._L.conv_int8_forward_quantize(self._plan, x.data_ptr(),
+                                                      CONV_BF16 if x.dtype is _t.bfloat16 else CONV_F32, w.data_ptr(),
+                                                      w_scale.data_ptr(), _ptr(bias), out.data_ptr(), _ptr(ws), raw),
                    "conv_int8_forward_quantize")
-        return y
+            return out
+
+        return _on(stream, dev, run)
 
     def device_status(self, stream=None) -> int:
         """Read and clear the plan's own status word, as ConvPlan.device_status."""
@@ -267,13 +276,13 @@ _int8_plans = {}
 
 
 def _norm_plan(x, groups, eps, act):
-    import torch
-    _need_any(x, "x", (torch.bfloat16, torch.float32))
-    if x.dim() != 4:
-        raise ValueError("x must be an NHWC tensor [N][H][W][C]")
-    key = (x.device.index, x.shape, x.dtype, groups, eps, act)
+    key = (x.shape, x.dtype, x.get_device(), groups, eps, act)
     plan = _norm_plans.get(key)
     if plan is None:
+        torch = _torch()
+        _need_any(x, "x", (torch.bfloat16, torch.float32))
+        if x.dim() != 4:
+            raise ValueError("x must be an NHWC tensor [N][H][W][C]")
         N, H, W, C = x.shape
         plan = _norm_plans[key] = GroupNormPlan(N, C, H, W, groups, "bf16" if x.dtype == torch.bfloat16 else "f32",
                                                 eps, act)
@@ -296,19 +305,24 @@ def group_norm_backward(dy, x, stats, groups, gamma=None, beta=None, eps=1e-5, a
 
 
 def _int8_plan(x, w, act, out):
-    if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
-        raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
-    N, K = w.shape
-    M = x.numel() // K if K else 0
-    key = (x.device.index, M, N, K, out, act)
+    key = (x.shape, w.shape, x.get_device(), out, act)
     plan = _int8_plans.get(key)
     if plan is None:
-        plan = _int8_plans[key] = Int8MatmulPlan(M, N, K, out, act)
+        if not x.is_cuda:
+            raise ValueError("x must be a CUDA tensor")
+        if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
+            raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
+        N, K = w.shape
+        plan = _int8_plans[key] = Int8MatmulPlan(x.numel() // K if K else 0, N, K, out, act)
     return plan
 
 
 def _as_rows(x, plan):
-    return x if x.dim() == 2 else x.view(plan.M, plan.K)
+    if x.dim() == 2:
+        return x
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    return x.view(plan.M, plan.K)
 
 
 def _as_given(y, x):
@@ -318,33 +332,33 @@ def _as_given(y, x):
 def int8_matmul(x, x_scale, w, w_scale, bias=None, act="none", out="bf16", stream=None):
     """x int8 [..., K] (rows or NHWC pixels) with x_scale, one FP32 scale per row in row order,
     times w int8 [N][K] with w_scale [N]: [..., N] in ``out`` ("bf16" or "f32")."""
-    import torch
-    _need_any(x, "x", (torch.int8,))
     plan = _int8_plan(x, w, act, out)
-    return _as_given(plan.forward(_as_rows(x, plan), x_scale.view(-1), w, w_scale, bias, stream=stream), x)
+    if x_scale.dim() != 1:
+        x_scale = x_scale.reshape(-1)
+    return _as_given(plan.forward(_as_rows(x, plan), x_scale, w, w_scale, bias, stream=stream), x)
 
 
 def int8_linear(x, w, w_scale, bias=None, act="none", out="bf16", stream=None):
     """x BF16 or FP32 [..., K], its rows brought to 8 bits in the call, times w int8 [N][K]."""
-    import torch
-    _need_any(x, "x", (torch.bfloat16, torch.float32))
     plan = _int8_plan(x, w, act, out)
     return _as_given(plan.forward_quantize(_as_rows(x, plan), w, w_scale, bias, stream=stream), x)
 
 
 def quantize_rows(x, stream=None):
     """(q, scale): rows of x [..., K] (BF16 or FP32) as int8 with one FP32 scale each, flat."""
-    import torch
+    torch = _torch()
     _need_any(x, "x", (torch.bfloat16, torch.float32))
     if x.dim() < 2 or not x.numel():
         raise ValueError("x must be [..., K] with at least one row and one column")
     K = x.shape[-1]
     M = x.numel() // K
-    stream, scope = _on(stream)
-    with scope:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-        _check(lib().conv_quantize_rows(x.data_ptr(), CONV_BF16 if x.dtype == torch.bfloat16 else CONV_F32, M, K,
-                                        q.data_ptr(), scale.data_ptr(), _handle(stream, x.device)),
-               "conv_quantize_rows")
-    return q, scale
+    dev = x.get_device()
+
+    def run(raw):
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        _check(lib().conv_quantize_rows(x.data_ptr(), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, M, K,
+                                        q.data_ptr(), scale.data_ptr(), raw), "conv_quantize_rows")
+        return q, scale
+
+    return _on(stream, dev, run)

@@ -395,13 +395,15 @@ typedef struct conv_group_norm_plan conv_group_norm_plan; /* opaque, host-owned 
 conv_status conv_group_norm_plan_create(conv_group_norm_plan **plan, int N, int C, int H, int W, int groups,
                                         float eps, conv_dtype dtype, conv_act act);
 
-/* Bytes of device workspace that each call of this plan takes. */
-conv_status conv_group_norm_workspace(const conv_group_norm_plan *p, unsigned long long *bytes);
+/* Bytes of device workspace that each call of this plan takes (any may be 0, then NULL will do;
+ * any pointer may be NULL). */
+conv_status conv_group_norm_workspace(const conv_group_norm_plan *p, unsigned long long *forward,
+                                      unsigned long long *forward_int8, unsigned long long *backward);
 
 /*
  * y = act(norm(x)).  stats (may be NULL) receives what the backward pass reads.
  * y must not overlap the inputs.  Asynchronous on `stream`; CONV_ERR_INVALID_ARG
- * for a NULL plan, x, y or workspace or another current device, CONV_ERR_MISALIGNED
+ * for a NULL plan, x or y, a NULL workspace where one is needed, or another current device, CONV_ERR_MISALIGNED
  * for a pointer that is not 16-byte aligned, CONV_ERR_CUDA if a launch fails.
  */
 conv_status conv_group_norm_forward(conv_group_norm_plan *p, const void *x, const float *gamma, const float *beta,

@@ -55,7 +55,7 @@ def test_null_and_misaligned_pointers():
     assert L.conv_group_norm_plan_create(None, 1, 32, 4, 4, 4, 1e-5, 1, 0) == 1
     assert L.conv_int8_plan_create(None, 1, 8, 8, 1, 0) == 1
     assert L.conv_group_norm_plan_destroy(None) == 0 and L.conv_int8_plan_destroy(None) == 0
-    assert L.conv_group_norm_workspace(None, None) == 1 and L.conv_int8_workspace(None, None) == 1
+    assert L.conv_group_norm_workspace(None, None, None, None) == 1 and L.conv_int8_workspace(None, None) == 1
     assert L.conv_int8_plan_device_status(None, None, None) == 1
     n = cg.GroupNormPlan(1, 32, 4, 4, 4)
     A = 256
@@ -63,7 +63,8 @@ def test_null_and_misaligned_pointers():
     assert fwd(None, A, None, None, A, None, A, None) == 1
     assert fwd(n._plan, None, None, None, A, None, A, None) == 1
     assert fwd(n._plan, A, None, None, None, None, A, None) == 1
-    assert fwd(n._plan, A, None, None, A, None, None, None) == 1
+    wide = cg.GroupNormPlan(1, 7, 4, 4, 7)     # odd channels: sums by channel, in a workspace
+    assert wide.workspace_bytes["forward"] > 0 and fwd(wide._plan, A, None, None, A, None, None, None) == 1
     assert fwd(n._plan, A + 2, None, None, A, None, A, None) == 3
     assert fwd(n._plan, A, A + 4, None, A, None, A, None) == 3
     assert fwd(n._plan, A, None, None, A, A + 8, A, None) == 3
