@@ -2,8 +2,8 @@
 conv_quantize_rows (include/conv.h).
 
 Argument checks and marshalling only, as in binding.py: every step runs in the library's
-CUDA kernels, on the given stream or torch's current one.  Results and workspaces are
-allocated on that stream, so torch's allocator reuses them in its order.
+CUDA kernels, on torch's current stream or, with ``stream``, as if that were it: results and
+workspaces are allocated on it, so torch's allocator reuses them in its order.
 """
 from __future__ import annotations
 
@@ -53,14 +53,6 @@ def _need_any(t, name, dtypes):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _on(stream, dev, run):
-    """run(raw stream): on torch's current stream, or on ``stream`` with allocations made on it."""
-    if stream is None:
-        return run(_raw_stream(dev))
-    with _t.cuda.stream(stream):
-        return run(stream.cuda_stream)
 
 
 def _workspace(nbytes, dev):
@@ -122,63 +114,67 @@ class GroupNormPlan:
 
     def forward(self, x, gamma=None, beta=None, y=None, stats=None, stream=None):
         """act(norm(x)); ``stats`` (empty_stats()) receives what backward() reads."""
+        if stream is not None:
+            with _t.cuda.stream(stream):
+                return self.forward(x, gamma, beta, y, stats)
         dev = self._inputs(x, gamma, beta, stats)
-
-        def run(raw):
-            out = _t.empty_like(x) if y is None else y
-            ws = _workspace(self.workspace_bytes["forward"], dev)
-            _check(self._L.conv_group_norm_forward(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(),
-                                                   _ptr(stats), _ptr(ws), raw), "conv_group_norm_forward")
-            return out
-
-        if y is not None:
+        if y is None:
+            y = _t.empty_like(x)
+        else:
             _need(y, "y", self.shape, self.torch_dtype, dev)
-        return _on(stream, dev, run)
+        ws = _workspace(self.workspace_bytes["forward"], dev)
+        _check(self._L.conv_group_norm_forward(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(),
+                                               _ptr(stats), _ptr(ws), _raw_stream(dev)), "conv_group_norm_forward")
+        return y
 
     __call__ = forward
 
     def forward_int8(self, x, gamma=None, beta=None, q=None, scale=None, stats=None, stream=None):
         """(q, scale): act(norm(x)) as int8 [N][H][W][C] with one FP32 scale per pixel [N*H*W]."""
+        if stream is not None:
+            with _t.cuda.stream(stream):
+                return self.forward_int8(x, gamma, beta, q, scale, stats)
         dev = self._inputs(x, gamma, beta, stats)
-        if q is not None:
+        if q is None:
+            q = _t.empty(self.shape, dtype=_t.int8, device=dev)
+        else:
             _need(q, "q", self.shape, _t.int8, dev)
-        if scale is not None:
+        if scale is None:
+            scale = _t.empty(self._pixels, dtype=_t.float32, device=dev)
+        else:
             _need(scale, "scale", self._pixels, _t.float32, dev)
-
-        def run(raw):
-            qo = _t.empty(self.shape, dtype=_t.int8, device=dev) if q is None else q
-            so = _t.empty(self._pixels, dtype=_t.float32, device=dev) if scale is None else scale
-            ws = _workspace(self.workspace_bytes["forward_int8"], dev)
-            _check(self._L.conv_group_norm_forward_int8(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta),
-                                                        qo.data_ptr(), so.data_ptr(), _ptr(stats), _ptr(ws), raw),
-                   "conv_group_norm_forward_int8")
-            return qo, so
-
-        return _on(stream, dev, run)
+        ws = _workspace(self.workspace_bytes["forward_int8"], dev)
+        _check(self._L.conv_group_norm_forward_int8(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), q.data_ptr(),
+                                                    scale.data_ptr(), _ptr(stats), _ptr(ws), _raw_stream(dev)),
+               "conv_group_norm_forward_int8")
+        return q, scale
 
     def backward(self, dy, x, stats, gamma=None, beta=None, dx=None, dgamma=None, dbeta=None, stream=None):
         """(dx, dgamma, dbeta) from the forward pass's x and stats."""
+        if stream is not None:
+            with _t.cuda.stream(stream):
+                return self.backward(dy, x, stats, gamma, beta, dx, dgamma, dbeta)
         if stats is None:
             raise ValueError("stats must be what forward(stats=...) wrote")
         dev = self._inputs(x, gamma, beta, stats)
         _need(dy, "dy", self.shape, self.torch_dtype, dev)
-        if dx is not None:
+        if dx is None:
+            dx = _t.empty_like(x)
+        else:
             _need(dx, "dx", self.shape, self.torch_dtype, dev)
-        for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
-            if t is not None:
-                _need(t, name, self._channels, _t.float32, dev)
-
-        def run(raw):
-            out = _t.empty_like(x) if dx is None else dx
-            dg = _t.empty(self._channels, dtype=_t.float32, device=dev) if dgamma is None else dgamma
-            db = _t.empty(self._channels, dtype=_t.float32, device=dev) if dbeta is None else dbeta
-            ws = _workspace(self.workspace_bytes["backward"], dev)
-            _check(self._L.conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(),
-                                                    _ptr(gamma), _ptr(beta), out.data_ptr(), dg.data_ptr(),
-                                                    db.data_ptr(), _ptr(ws), raw), "conv_group_norm_backward")
-            return out, dg, db
-
-        return _on(stream, dev, run)
+        if dgamma is None:
+            dgamma = _t.empty(self._channels, dtype=_t.float32, device=dev)
+        else:
+            _need(dgamma, "dgamma", self._channels, _t.float32, dev)
+        if dbeta is None:
+            dbeta = _t.empty(self._channels, dtype=_t.float32, device=dev)
+        else:
+            _need(dbeta, "dbeta", self._channels, _t.float32, dev)
+        ws = _workspace(self.workspace_bytes["backward"], dev)
+        _check(self._L.conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(gamma),
+                                                _ptr(beta), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+                                                _ptr(ws), _raw_stream(dev)), "conv_group_norm_backward")
+        return dx, dgamma, dbeta
 
     def empty_stats(self, device="cuda"):
         return _t.empty(self.stats_shape, dtype=_t.float32, device=device)
@@ -233,37 +229,37 @@ class Int8MatmulPlan:
 
     def forward(self, x, x_scale, w, w_scale, bias=None, y=None, stream=None):
         """The product of int8 rows x [M][K] with their scales [M]."""
+        if stream is not None:
+            with _t.cuda.stream(stream):
+                return self.forward(x, x_scale, w, w_scale, bias, y)
         if x.dtype is not _t.int8:
             raise ValueError("x must be int8")
         dev = self._operands(x, w, w_scale, bias, y)
         _need(x_scale, "x_scale", self._rows, _t.float32, dev)
-
-        def run(raw):
-            out = _t.empty(self._y, dtype=self.torch_dtype, device=dev) if y is None else y
-            _check(self._L.conv_int8_forward(self._plan, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
-                                             w_scale.data_ptr(), _ptr(bias), out.data_ptr(), raw), "conv_int8_forward")
-            return out
-
-        return _on(stream, dev, run)
+        if y is None:
+            y = _t.empty(self._y, dtype=self.torch_dtype, device=dev)
+        _check(self._L.conv_int8_forward(self._plan, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                                         _ptr(bias), y.data_ptr(), _raw_stream(dev)), "conv_int8_forward")
+        return y
 
     __call__ = forward
 
     def forward_quantize(self, x, w, w_scale, bias=None, y=None, stream=None):
         """The product of BF16 or FP32 rows, brought to 8 bits (quantize_rows) in the call."""
-        if x.dtype is not _t.bfloat16 and x.dtype is not _t.float32:
+        if stream is not None:
+            with _t.cuda.stream(stream):
+                return self.forward_quantize(x, w, w_scale, bias, y)
+        bf16 = x.dtype is _t.bfloat16
+        if not bf16 and x.dtype is not _t.float32:
             raise ValueError("x must be bfloat16 or float32")
         dev = self._operands(x, w, w_scale, bias, y)
-
-        def run(raw):
-            out = _t.empty(self._y, dtype=self.torch_dtype, device=dev) if y is None else y
-            ws = _workspace(self.workspace_bytes, dev)
-            _check(self._L.conv_int8_forward_quantize(self._plan, x.data_ptr(),
-                                                      CONV_BF16 if x.dtype is _t.bfloat16 else CONV_F32, w.data_ptr(),
-                                                      w_scale.data_ptr(), _ptr(bias), out.data_ptr(), _ptr(ws), raw),
-                   "conv_int8_forward_quantize")
-            return out
-
-        return _on(stream, dev, run)
+        if y is None:
+            y = _t.empty(self._y, dtype=self.torch_dtype, device=dev)
+        ws = _workspace(self.workspace_bytes, dev)
+        _check(self._L.conv_int8_forward_quantize(self._plan, x.data_ptr(), CONV_BF16 if bf16 else CONV_F32, w.data_ptr(),
+                                                  w_scale.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(ws),
+                                                  _raw_stream(dev)), "conv_int8_forward_quantize")
+        return y
 
     def device_status(self, stream=None) -> int:
         """Read and clear the plan's own status word, as ConvPlan.device_status."""
@@ -352,13 +348,12 @@ def quantize_rows(x, stream=None):
         raise ValueError("x must be [..., K] with at least one row and one column")
     K = x.shape[-1]
     M = x.numel() // K
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_rows(x)
     dev = x.get_device()
-
-    def run(raw):
-        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
-        scale = torch.empty(M, dtype=torch.float32, device=dev)
-        _check(lib().conv_quantize_rows(x.data_ptr(), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, M, K,
-                                        q.data_ptr(), scale.data_ptr(), raw), "conv_quantize_rows")
-        return q, scale
-
-    return _on(stream, dev, run)
+    q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    scale = torch.empty(M, dtype=torch.float32, device=dev)
+    _check(lib().conv_quantize_rows(x.data_ptr(), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, M, K,
+                                    q.data_ptr(), scale.data_ptr(), _raw_stream(dev)), "conv_quantize_rows")
+    return q, scale
