@@ -461,11 +461,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     advance<PAIR, BN>(p, tiles, w, kGroups);
                 }
             } else {
-                while (w.u < units) {
-                    uint4 item[S::kItems];
-                    load_stage<PAIR, BN>(p, w, r0, c, item);
-                    if (!publish(item)) break;
-                    advance<PAIR, BN>(p, tiles, w, kGroups);
+                // The next turn's loads are under way while this one's items are converted.
+                uint4 item[S::kItems], next[S::kItems];
+                load_stage<PAIR, BN>(p, w, r0, c, item);
+                while (true) {
+                    Walk nw = w;
+                    advance<PAIR, BN>(p, tiles, nw, kGroups);
+                    const bool more = nw.u < units;
+                    if (more) load_stage<PAIR, BN>(p, nw, r0, c, next);
+                    if (!publish(item) || !more) break;
+                    w = nw;
+#pragma unroll
+                    for (int i = 0; i < S::kItems; ++i) item[i] = next[i];
                 }
             }
         }

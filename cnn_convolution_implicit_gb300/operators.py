@@ -183,9 +183,10 @@ class GroupNormPlan:
 class Int8MatmulPlan:
     """8-bit product of one shape (include/conv.h, conv_int8_*):
     y[m][n] = act(x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k] + bias[n]), x int8 [M][K], w
-    int8 [N][K], FP32 scales and bias, y BF16 ("bf16") or FP32 ("f32")."""
+    int8 [N][K], FP32 scales and bias, y BF16 ("bf16") or FP32 ("f32").  ``x_shape`` [..., K] with M rows
+    in all: x has that shape instead, and y [..., N]."""
 
-    def __init__(self, M, N, K, out="bf16", act="none"):
+    def __init__(self, M, N, K, out="bf16", act="none", x_shape=None):
         L = lib()
         self._plan = None
         h = ctypes.c_void_p()
@@ -196,7 +197,10 @@ class Int8MatmulPlan:
         torch = _torch()
         self.M, self.N, self.K, self.out, self.act = M, N, K, out, act
         self.torch_dtype = _torch_dtypes()[out]
-        self._x, self._w, self._y = torch.Size((M, K)), torch.Size((N, K)), torch.Size((M, N))
+        self._x = torch.Size((M, K) if x_shape is None else x_shape)
+        if self._x.numel() != M * K or self._x[-1] != K:
+            raise ValueError("x_shape must hold %d rows of %d" % (M, K))
+        self._w, self._y = torch.Size((N, K)), torch.Size(self._x[:-1] + (N,))
         self._rows, self._cols = torch.Size((M,)), torch.Size((N,))
         b = ctypes.c_ulonglong()
         _check(L.conv_int8_workspace(h, ctypes.byref(b)), "conv_int8_workspace")
@@ -309,35 +313,21 @@ def _int8_plan(x, w, act, out):
         if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
             raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
         N, K = w.shape
-        plan = _int8_plans[key] = Int8MatmulPlan(x.numel() // K if K else 0, N, K, out, act)
+        plan = _int8_plans[key] = Int8MatmulPlan(x.numel() // K if K else 0, N, K, out, act, x.shape)
     return plan
-
-
-def _as_rows(x, plan):
-    if x.dim() == 2:
-        return x
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
-    return x.view(plan.M, plan.K)
-
-
-def _as_given(y, x):
-    return y if x.dim() == 2 else y.view(*x.shape[:-1], y.shape[1])
 
 
 def int8_matmul(x, x_scale, w, w_scale, bias=None, act="none", out="bf16", stream=None):
     """x int8 [..., K] (rows or NHWC pixels) with x_scale, one FP32 scale per row in row order,
     times w int8 [N][K] with w_scale [N]: [..., N] in ``out`` ("bf16" or "f32")."""
-    plan = _int8_plan(x, w, act, out)
     if x_scale.dim() != 1:
         x_scale = x_scale.reshape(-1)
-    return _as_given(plan.forward(_as_rows(x, plan), x_scale, w, w_scale, bias, stream=stream), x)
+    return _int8_plan(x, w, act, out).forward(x, x_scale, w, w_scale, bias, stream=stream)
 
 
 def int8_linear(x, w, w_scale, bias=None, act="none", out="bf16", stream=None):
     """x BF16 or FP32 [..., K], its rows brought to 8 bits in the call, times w int8 [N][K]."""
-    plan = _int8_plan(x, w, act, out)
-    return _as_given(plan.forward_quantize(_as_rows(x, plan), w, w_scale, bias, stream=stream), x)
+    return _int8_plan(x, w, act, out).forward_quantize(x, w, w_scale, bias, stream=stream)
 
 
 def quantize_rows(x, stream=None):
