@@ -110,8 +110,8 @@ def lib():
             L.conv_group_norm_backward.argtypes = [vp] * 11
             L.conv_group_norm_plan_destroy.argtypes = [vp]
             L.conv_int8_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 5
-            L.conv_int8_forward.argtypes = [vp] * 8
-            L.conv_int8_workspace.argtypes = [vp, ctypes.POINTER(c_ull)]
+            L.conv_int8_forward.argtypes = [vp] * 9
+            L.conv_int8_workspace.argtypes = [vp, ctypes.POINTER(c_ull), ctypes.POINTER(c_ull)]
             L.conv_int8_forward_quantize.argtypes = [vp, vp, c_int] + [vp] * 6
             L.conv_int8_plan_device_status.argtypes = [vp, vp, ctypes.POINTER(c_int)]
             L.conv_int8_plan_destroy.argtypes = [vp]

@@ -32,8 +32,28 @@ conv_status check_device(const conv_int8_plan* pl) {
     return cur == pl->device ? CONV_OK : CONV_ERR_INVALID_ARG;
 }
 
-// The 8-bit rows of a call that quantises: [M][K] integers, rounded up to 16 bytes, then [M] scales.
-size_t rows_bytes(const Int8Params& p) { return (static_cast<size_t>(p.M) * p.K + 15) & ~static_cast<size_t>(15); }
+size_t up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+// Workspace of the tensor-core form: rows of x that it quantises, or that do not start on 16 bytes
+// as they are; rows of w that do not; the scales of quantised rows.
+struct Workspace {
+    int pitch;                // bytes between rows
+    size_t x, w, scales;      // offsets
+    size_t forward, quantize; // bytes of either call
+};
+
+Workspace workspace_of(const Int8Params& p) {
+    Workspace ws = {};
+    if (!int8_use_gemm(p)) return ws;
+    ws.pitch = static_cast<int>(up(p.K, 16));
+    const size_t x = up(static_cast<size_t>(p.M) * ws.pitch, 256);
+    const size_t w = p.K % 16 != 0 ? up(static_cast<size_t>(p.N) * ws.pitch, 256) : 0;
+    ws.w = x;
+    ws.scales = x + w;
+    ws.forward = w != 0 ? x + w : 0;
+    ws.quantize = ws.scales + static_cast<size_t>(p.M) * sizeof(float);
+    return ws;
+}
 
 conv_status launched(cudaError_t e) {
     if (e == cudaSuccess) return CONV_OK;
@@ -86,11 +106,14 @@ conv_status conv_int8_plan_create(conv_int8_plan** out, int M, int N, int K, con
 }
 
 conv_status conv_int8_forward(conv_int8_plan* pl, const void* x, const float* x_scale, const void* w,
-                              const float* w_scale, const float* bias, void* y, void* stream) {
+                              const float* w_scale, const float* bias, void* y, void* workspace, void* stream) {
     if (pl == nullptr || x == nullptr || x_scale == nullptr || w == nullptr || w_scale == nullptr || y == nullptr)
         return CONV_ERR_INVALID_ARG;
+    const Workspace ws = workspace_of(pl->ip);
+    if (workspace == nullptr && ws.forward != 0) return CONV_ERR_INVALID_ARG;
     for (const void* ptr : {x, static_cast<const void*>(x_scale), w, static_cast<const void*>(w_scale),
-                            static_cast<const void*>(bias), static_cast<const void*>(y)})
+                            static_cast<const void*>(bias), static_cast<const void*>(y),
+                            static_cast<const void*>(workspace)})
         if (ptr != nullptr && !aligned16(ptr)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
@@ -101,12 +124,25 @@ conv_status conv_int8_forward(conv_int8_plan* pl, const void* x, const float* x_
     p.w_scale = w_scale;
     p.bias = bias;
     p.y = y;
-    return launched(launch_int8_product(p, pl->num_sms, static_cast<cudaStream_t>(stream)));
+    p.x_pitch = p.w_pitch = p.K;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!int8_use_gemm(p)) return launched(launch_int8_few(p, st));
+    if (ws.forward != 0) {
+        int8_t* base = static_cast<int8_t*>(workspace);
+        const cudaError_t e = launch_int8_layout(p.x, base + ws.x, p.M, p.w, base + ws.w, p.N, p.K, ws.pitch, pl->num_sms, st);
+        if (e != cudaSuccess) return launched(e);
+        p.x = base + ws.x;
+        p.w = base + ws.w;
+        p.x_pitch = p.w_pitch = ws.pitch;
+    }
+    return launched(launch_int8_gemm(p, pl->num_sms, ws.forward != 0, st));
 }
 
-conv_status conv_int8_workspace(const conv_int8_plan* p, unsigned long long* bytes) {
-    if (p == nullptr || bytes == nullptr) return CONV_ERR_INVALID_ARG;
-    *bytes = int8_use_gemm(p->ip) ? rows_bytes(p->ip) + static_cast<size_t>(p->ip.M) * sizeof(float) : 0;
+conv_status conv_int8_workspace(const conv_int8_plan* p, unsigned long long* forward, unsigned long long* quantize) {
+    if (p == nullptr) return CONV_ERR_INVALID_ARG;
+    const Workspace ws = workspace_of(p->ip);
+    if (forward) *forward = ws.forward;
+    if (quantize) *quantize = ws.quantize;
     return CONV_OK;
 }
 
@@ -129,14 +165,24 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     p.y = y;
     if (!int8_use_gemm(p))
         return launched(launch_int8_few_quantize(p, x, x_dtype == CONV_BF16, static_cast<cudaStream_t>(stream)));
-    int8_t* q = static_cast<int8_t*>(workspace);
-    float* scale = reinterpret_cast<float*>(q + rows_bytes(p));
-    p.x = q;
-    p.x_scale = scale;
-    const cudaError_t e = launch_quantize_rows(x, x_dtype == CONV_BF16, p.M, p.K, q, scale, pl->num_sms,
-                                               static_cast<cudaStream_t>(stream));
+    const Workspace ws = workspace_of(p);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int8_t* base = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(base + ws.scales);
+    p.w_pitch = p.K;
+    cudaError_t e = cudaSuccess;
+    if (p.K % 16 != 0) {
+        e = launch_int8_layout(nullptr, nullptr, 0, p.w, base + ws.w, p.N, p.K, ws.pitch, pl->num_sms, st);
+        p.w = base + ws.w;
+        p.w_pitch = ws.pitch;
+    }
+    if (e == cudaSuccess)
+        e = launch_quantize_rows(x, x_dtype == CONV_BF16, p.M, p.K, ws.pitch, base + ws.x, scale, pl->num_sms, st);
     if (e != cudaSuccess) return launched(e);
-    return launched(launch_int8_product(p, pl->num_sms, static_cast<cudaStream_t>(stream)));
+    p.x = base + ws.x;
+    p.x_pitch = ws.pitch;
+    p.x_scale = scale;
+    return launched(launch_int8_gemm(p, pl->num_sms, true, st));
 }
 
 conv_status conv_int8_plan_device_status(const conv_int8_plan* p, void* stream, int* code) {
@@ -163,7 +209,7 @@ conv_status conv_quantize_rows(const void* x, conv_dtype dtype, int M, int K, vo
         cudaGetLastError();
         return CONV_ERR_CUDA;
     }
-    return launched(launch_quantize_rows(x, dtype == CONV_BF16, M, K, static_cast<int8_t*>(q), scale, sms,
+    return launched(launch_quantize_rows(x, dtype == CONV_BF16, M, K, K, static_cast<int8_t*>(q), scale, sms,
                                          static_cast<cudaStream_t>(stream)));
 }
 

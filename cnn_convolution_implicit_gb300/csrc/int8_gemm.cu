@@ -21,10 +21,8 @@
 //                 each: scales, bias, activation, rounding, stores from registers
 //   warp 24       tensor memory; one lane issues tcgen05.mma and commits
 //   warp 25       one lane fills the raw ring by TMA: K = 64 of both operands, 8-bit, per slot
-// Rows that do not start on 16 bytes (K % 16) are beyond the TMA: there the converters load
-// them straight from memory (ALIGNED = false).  Loading a step ahead in registers does not
-// replace the ring: the fence that publishes a stage also waits for the loads under way
-// (8192 x 4096 x 4096 measured 413 us that way and 325 us with the ring).
+// Rows that do not start on 16 bytes (K % 16) are beyond the TMA: a kernel of its own copies
+// them to rows that do, in the workspace, first.
 // A stage holds K = 64 of both operands, one 128-byte FP16 row each.  Tensor memory holds two
 // accumulators, so the epilogue of one tile overlaps the next one's MMAs.
 //
@@ -38,6 +36,10 @@
 // PAIR: two SMs share a 256 x BN tile (tcgen05.mma.cta_group::2): each converts its own
 // 128 rows of x and BN / 2 rows of w.  Shared memory bounds this kernel (written by the
 // converters, read by the MMA), and a pair halves the traffic of w.
+//
+// Few tiles: a cluster of up to 8 CTAs splits the K of one tile (p.splits).  Each leaves its sums in
+// its shared memory; after a cluster barrier each finishes its share of the rows, adding the
+// parts in one order.
 //
 // Rows past M or N are neither loaded nor written: their outputs are never stored, and
 // one row's operand does not reach another row's result.  Past K both operands are 0.
@@ -60,14 +62,15 @@ constexpr int kGemmThreads = 32 * (kLoadWarp + 1);
 constexpr int kStepK = 64;       // K of one stage
 constexpr int kRowBytes = 128;   // one FP16 operand row of a stage
 
-template <bool PAIR, int BN, bool ALIGNED>
+template <bool PAIR, int BN>
 struct Shape {
     static constexpr int kRowsB = PAIR ? BN / 2 : BN;
     static constexpr int kTileA = 128 * kRowBytes;
     static constexpr int kStage = kTileA + kRowsB * kRowBytes;
     static constexpr int kStages = kGroups;              // one for each converter group
-    static constexpr int kRaw = ALIGNED ? (128 + kRowsB) * kStepK : 0;  // one slot of the raw ring
-    static constexpr int kRawSlots = ALIGNED ? (kRowsB >= 128 ? 6 : 8) : 0;  // in 227 KB beside the stages
+    static constexpr int kRaw = (128 + kRowsB) * kStepK;  // one slot of the raw ring
+    static constexpr int kRawSlots = kRowsB >= 128 ? 6 : 8;  // in 227 KB beside the stages
+    static constexpr int kPartRow = BN + 8;              // floats of a row of partial sums (K split over a cluster)
     static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 256;
@@ -122,7 +125,8 @@ struct Walk {
 // The tiles of a launch, and this CTA's way through them (no division per tile).
 struct Tiles {
     int n_tiles, units, step, step_m, step_n;
-    uint32_t rank;
+    int k_begin, k_end;  // the CTA's part of K
+    uint32_t rank;       // of a pair
 };
 
 template <bool PAIR, int BN>
@@ -135,7 +139,7 @@ template <bool PAIR, int BN>
 __device__ __forceinline__ Walk walk_from(const Tiles& t, int unit0) {
     Walk w;
     w.u = unit0;
-    w.k0 = 0;
+    w.k0 = t.k_begin;
     w.mu = unit0 / t.n_tiles;
     w.nt = unit0 - w.mu * t.n_tiles;
     place<PAIR, BN>(t, w);
@@ -153,34 +157,13 @@ __device__ __forceinline__ void next_unit(const Tiles& t, Walk& w) {
 }
 
 template <bool PAIR, int BN>
-__device__ __forceinline__ void advance(const Int8Params& p, const Tiles& t, Walk& w, int steps) {
+__device__ __forceinline__ void advance(const Tiles& t, Walk& w, int steps) {
     for (int i = 0; i < steps && w.u < t.units; ++i) {
         w.k0 += kStepK;
-        if (w.k0 >= p.K) {
-            w.k0 = 0;
+        if (w.k0 >= t.k_end) {
+            w.k0 = t.k_begin;
             next_unit(t, w);
             place<PAIR, BN>(t, w);
-        }
-    }
-}
-
-template <bool PAIR, int BN>
-__device__ __forceinline__ void load_stage(const Int8Params& p, const Walk& w, int r0, int c,
-                                           uint4 (&item)[Shape<PAIR, BN, false>::kItems]) {
-    const int k = w.k0 + 16 * c;
-    const int len = p.K - k;
-    const long long total_x = static_cast<long long>(p.M) * p.K, total_w = static_cast<long long>(p.N) * p.K;
-#pragma unroll
-    for (int i = 0; i < Shape<PAIR, BN, false>::kItems; ++i) {
-        item[i] = make_uint4(0, 0, 0, 0);
-        if (len <= 0) continue;
-        const int n_len = len < 16 ? len : 16;
-        if (i < 4) {
-            const int row = w.m0 + r0 + 32 * i;
-            if (row < p.M) item[i] = load_item(p.x, static_cast<long long>(row) * p.K + k, n_len, total_x);
-        } else {
-            const int row = w.n0 + r0 + 32 * (i - 4);
-            if (row < p.N) item[i] = load_item(p.w, static_cast<long long>(row) * p.K + k, n_len, total_w);
         }
     }
 }
@@ -191,8 +174,8 @@ __device__ __forceinline__ int column_of(int n) { return (n & ~31) | ((n & 6) <<
 
 template <bool PAIR, int BN>
 __device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c,
-                                            const uint4 (&item)[Shape<PAIR, BN, false>::kItems], uint8_t* stage) {
-    using S = Shape<PAIR, BN, false>;
+                                            const uint4 (&item)[Shape<PAIR, BN>::kItems], uint8_t* stage) {
+    using S = Shape<PAIR, BN>;
 #pragma unroll
     for (int i = 0; i < S::kItems; ++i) {
         int row = r0 + 32 * (i < 4 ? i : i - 4);
@@ -330,6 +313,71 @@ __device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d)
     }
 }
 
+// The sums of such a block to shared memory as they are (K split over a cluster): every operand tile
+// of this CTA has been read by then.
+template <int G>
+__device__ __forceinline__ void leave_block(uint32_t at, float* part, int row_floats) {
+    uint32_t v[G][16];
+#pragma unroll
+    for (int g = 0; g < G; ++g) tmem_ld_16x32(at + (static_cast<uint32_t>(16 * g) << 16), v[g]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) tmem_ld_wait16(v[g]);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const auto at8 = [&](int i) { return v[g][4 * (i >> 1) + 2 * h + (i & 1)]; };
+            uint4* to = reinterpret_cast<uint4*>(part + (16 * g + 8 * h) * row_floats);
+            to[0] = make_uint4(at8(0), at8(1), at8(2), at8(3));
+            to[1] = make_uint4(at8(4), at8(5), at8(6), at8(7));
+        }
+}
+
+__device__ __forceinline__ float4 peer_float4(const float* p, uint32_t cta) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(mapa_shared(smem_addr(p), cta))
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float finish_one(const Int8Params& p, float sum, float xs, int n) {
+    const float v = fmaf(sum * xs, __ldg(p.w_scale + n), p.bias ? __ldg(p.bias + n) : 0.0f);
+    if (p.act == CONV_ACT_RELU) return activate<CONV_ACT_RELU>(v);
+    if (p.act == CONV_ACT_SILU) return activate<CONV_ACT_SILU>(v);
+    return v;
+}
+
+// This CTA's rows of the cluster's tile from the parts of all its CTAs, four columns a thread.
+template <int BN>
+__device__ __forceinline__ void join_parts(const Int8Params& p, const float* part, int m0, int n0, uint32_t cta, int splits) {
+    constexpr int kRow = BN + 8, kQuads = BN / 4;
+    const int rows = 128 / splits, first = static_cast<int>(cta) * rows;
+    for (int i = threadIdx.x; i < rows * kQuads; i += kGemmThreads) {
+        const int row = first + i / kQuads, q = i % kQuads, n = n0 + 4 * q;
+        if (m0 + row >= p.M || n >= p.N) continue;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < splits; ++k) {
+            const float4 v = peer_float4(part + row * kRow + 4 * q, k);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+        const float xs = __ldg(p.x_scale + m0 + row);
+        const float in[4] = {sum.x, sum.y, sum.z, sum.w};
+        const long long o = static_cast<long long>(m0 + row) * p.N + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n + j >= p.N) break;
+            const float v = finish_one(p, in[j], xs, n + j);
+            if (p.out_bf16) static_cast<__nv_bfloat16*>(p.y)[o + j] = __float2bfloat16_rn(v);
+            else static_cast<float*>(p.y)[o + j] = v;
+        }
+    }
+}
+
 // The columns of a warp, `whole` of its blocks of 32 in wide accesses.
 template <int ACT, bool BF16, int G>
 __device__ __forceinline__ void drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
@@ -345,11 +393,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as ides
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <bool PAIR, int BN, bool ALIGNED>
+template <bool PAIR, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     int8_gemm_kernel(const Int8Params p, const __grid_constant__ CUtensorMap map_x,
                      const __grid_constant__ CUtensorMap map_w) {
-    using S = Shape<PAIR, BN, ALIGNED>;
+    using S = Shape<PAIR, BN>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_addr(smem) & 1023u) {  // the swizzle's atoms; uniform, so no CTA waits for another
         record_status(p.status, kStatusTimeoutMma, nullptr);
@@ -368,9 +416,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
     volatile int* abort = b.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const uint32_t cta = cluster_ctarank();  // 0 without a cluster
+    const uint32_t rank = PAIR ? cta : 0u;
     const bool leader = rank == 0;
     constexpr int kCtas = PAIR ? 2 : 1;
+    const int splits = PAIR ? 1 : p.splits;
 
     Tiles tiles;
     tiles.n_tiles = (p.N + BN - 1) / BN;
@@ -379,8 +429,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tiles.step_m = tiles.step / tiles.n_tiles;
     tiles.step_n = tiles.step - tiles.step_m * tiles.n_tiles;
     tiles.rank = rank;
-    const int unit0 = static_cast<int>(blockIdx.x) / kCtas, units = tiles.units, unit_step = tiles.step;
-    const int ksteps = (p.K + kStepK - 1) / kStepK;
+    int unit0 = static_cast<int>(blockIdx.x) / kCtas;
+    const int units = tiles.units;
+    int kfirst = 0, ksteps = (p.K + kStepK - 1) / kStepK;
+    if (splits > 1) {  // one tile a cluster
+        unit0 = static_cast<int>(blockIdx.x) / splits;
+        tiles.step = units;
+        const int all = ksteps;
+        kfirst = static_cast<int>(cta) * all / splits;
+        ksteps = (static_cast<int>(cta) + 1) * all / splits - kfirst;
+    }
+    tiles.k_begin = kfirst * kStepK;
+    tiles.k_end = min(p.K, (kfirst + ksteps) * kStepK);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kRawSlots; ++s) {
@@ -413,6 +473,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if constexpr (PAIR) cluster_sync_all();  // the peer's barriers exist before anything signals them
     tc_fence_after();
     const uint32_t tmem = *b.tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // rows laid out by the kernel before this one
 
     if (warp < kConverterWarps) {
         // ------------------------------------------------------------ converters
@@ -420,7 +481,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int t = threadIdx.x & (32 * kGroupWarps - 1);
         const int c = t & 3, r0 = t >> 2;
         Walk w = walk_from<PAIR, BN>(tiles, unit0);
-        advance<PAIR, BN>(p, tiles, w, group);
+        advance<PAIR, BN>(tiles, w, group);
         if (w.u < units) {
             uint32_t ph = 0;
             uint8_t* stage = smem + group * S::kStage;
@@ -439,41 +500,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ph ^= 1u;
                 return true;
             };
-            if constexpr (ALIGNED) {
-                int rs = group;
-                uint32_t rph = 0;
-                while (w.u < units) {
-                    if (!warp_wait(&b.rfull[rs], rph, abort)) {
-                        record_status(p.status, kStatusTimeoutTransform, abort);
-                        break;
-                    }
-                    uint4 item[S::kItems];
-                    const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + t;
-#pragma unroll
-                    for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 128];  // rows r0 + 32 i of x, then of w
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b.rempty[rs]);
-                    if (!publish(item)) break;
-                    if ((rs += kGroups) >= S::kRawSlots) {  // more slots than groups: one wrap a turn at most
-                        rs -= S::kRawSlots;
-                        rph ^= 1u;
-                    }
-                    advance<PAIR, BN>(p, tiles, w, kGroups);
+            int rs = group;
+            uint32_t rph = 0;
+            while (w.u < units) {
+                if (!warp_wait(&b.rfull[rs], rph, abort)) {
+                    record_status(p.status, kStatusTimeoutTransform, abort);
+                    break;
                 }
-            } else {
-                // The next turn's loads are under way while this one's items are converted.
-                uint4 item[S::kItems], next[S::kItems];
-                load_stage<PAIR, BN>(p, w, r0, c, item);
-                while (true) {
-                    Walk nw = w;
-                    advance<PAIR, BN>(p, tiles, nw, kGroups);
-                    const bool more = nw.u < units;
-                    if (more) load_stage<PAIR, BN>(p, nw, r0, c, next);
-                    if (!publish(item) || !more) break;
-                    w = nw;
+                uint4 item[S::kItems];
+                const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + t;
 #pragma unroll
-                    for (int i = 0; i < S::kItems; ++i) item[i] = next[i];
+                for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 128];  // rows r0 + 32 i of x, then of w
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.rempty[rs]);
+                if (!publish(item)) break;
+                if ((rs += kGroups) >= S::kRawSlots) {  // more slots than groups: one wrap a turn at most
+                    rs -= S::kRawSlots;
+                    rph ^= 1u;
                 }
+                advance<PAIR, BN>(tiles, w, kGroups);
             }
         }
     } else if (warp < kMmaWarp) {
@@ -513,7 +558,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 break;
             }
             tc_fence_after();
-            if (p.out_bf16) {
+            if (splits > 1) {
+                float* part = reinterpret_cast<float*>(smem) + static_cast<size_t>(lane0 + (lane >> 2)) * S::kPartRow + (lane & 3) * 8;
+                for (int c = col0; c < col0 + kCols; c += 32)
+                    leave_block<G>(d.at + (c - col0), part + c, S::kPartRow);
+            } else if (p.out_bf16) {
                 if (p.act == CONV_ACT_RELU) drain_columns<CONV_ACT_RELU, true, G>(p, d, blocks, whole);
                 else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, true, G>(p, d, blocks, whole);
                 else drain_columns<CONV_ACT_NONE, true, G>(p, d, blocks, whole);
@@ -531,33 +580,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ raw ring
-        if constexpr (ALIGNED) {
-            Walk w = walk_from<PAIR, BN>(tiles, unit0);
-            if (lane == 0 && w.u < units) {
-                long long issued = 0;
-                int rs = 0;
-                uint32_t ph = 0;
-                while (w.u < units) {
-                    if (!mbar_wait(&b.rempty[rs], ph ^ 1u, abort)) {
-                        record_status(p.status, kStatusTimeoutProducer, abort);
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&b.rfull[rs], S::kRaw);
-                    uint8_t* slot = raw + rs * S::kRaw;
-                    tma_load_2d(slot, &map_x, &b.rfull[rs], w.k0, w.m0);  // past the matrix: zeros
-                    tma_load_2d(slot + 128 * kStepK, &map_w, &b.rfull[rs], w.k0, w.n0);
-                    ++issued;
-                    if (++rs == S::kRawSlots) {
-                        rs = 0;
-                        ph ^= 1u;
-                    }
-                    advance<PAIR, BN>(p, tiles, w, 1);
+        Walk w = walk_from<PAIR, BN>(tiles, unit0);
+        if (lane == 0 && w.u < units) {
+            long long issued = 0;
+            int rs = 0;
+            uint32_t ph = 0;
+            while (w.u < units) {
+                if (!mbar_wait(&b.rempty[rs], ph ^ 1u, abort)) {
+                    record_status(p.status, kStatusTimeoutProducer, abort);
+                    break;
                 }
-                for (int s = 0; s < S::kRawSlots; ++s) {  // no copy in flight when the CTA leaves
-                    const long long fills = issued / S::kRawSlots + (s < issued % S::kRawSlots ? 1 : 0);
-                    if (fills && !mbar_wait(&b.rfull[s], static_cast<uint32_t>((fills - 1) & 1), nullptr))
-                        record_status(p.status, kStatusTimeoutDrain, abort);
+                mbar_arrive_expect_tx(&b.rfull[rs], S::kRaw);
+                uint8_t* slot = raw + rs * S::kRaw;
+                tma_load_2d(slot, &map_x, &b.rfull[rs], w.k0, w.m0);  // past the matrix: zeros
+                tma_load_2d(slot + 128 * kStepK, &map_w, &b.rfull[rs], w.k0, w.n0);
+                ++issued;
+                if (++rs == S::kRawSlots) {
+                    rs = 0;
+                    ph ^= 1u;
                 }
+                advance<PAIR, BN>(tiles, w, 1);
+            }
+            for (int s = 0; s < S::kRawSlots; ++s) {  // no copy in flight when the CTA leaves
+                const long long fills = issued / S::kRawSlots + (s < issued % S::kRawSlots ? 1 : 0);
+                if (fills && !mbar_wait(&b.rfull[s], static_cast<uint32_t>((fills - 1) & 1), nullptr))
+                    record_status(p.status, kStatusTimeoutDrain, abort);
             }
         }
     } else if (lane == 0 && leader) {
@@ -566,7 +613,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int st = 0, local = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+        for (int u = unit0; u < units && ok; u += tiles.step, ++local) {
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
             if (!mbar_wait_cluster(&b.tempty[buf], use ^ 1u, abort)) {
@@ -583,7 +630,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t base = smem_addr(smem + st * S::kStage);
-                const int left = (p.K - ks * kStepK + 15) >> 4;
+                const int left = (p.K - (kfirst + ks) * kStepK + 15) >> 4;
                 const int mmas = left < 4 ? left : 4;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -612,6 +659,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncwarp();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();  // no CTA leaves while its peer may still signal it
+    if (!PAIR && splits > 1) {
+        cluster_sync_all();  // every part is in place
+        const Walk w = walk_from<PAIR, BN>(tiles, unit0);
+        join_parts<BN>(p, reinterpret_cast<const float*>(smem), w.m0, w.n0, cta, splits);
+        cluster_sync_all();  // no CTA leaves while another may still read its part
+    }
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
@@ -620,48 +673,70 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
 }
 
-// [rows][K] 8-bit matrix in boxes of `box_rows` rows x 128 bytes.
-bool encode_rows(CUtensorMap* map, const int8_t* base, int rows, int K, int box_rows) {
+// [rows][K] 8-bit matrix, rows `pitch` bytes apart, in boxes of `box_rows` rows x 64 bytes.
+bool encode_rows(CUtensorMap* map, const int8_t* base, int rows, int K, int pitch, int box_rows) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
     const cuuint32_t box[2] = {kStepK, static_cast<cuuint32_t>(box_rows)};
     return tensor_map_encoder_ready() &&
            encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, box,
                         CU_TENSOR_MAP_SWIZZLE_NONE) == CUDA_SUCCESS;
 }
 
-template <bool PAIR, int BN, bool ALIGNED>
-cudaError_t launch_variant(const Int8Params& p, int num_sms, cudaStream_t stream) {
-    using S = Shape<PAIR, BN, ALIGNED>;
+template <bool PAIR, int BN>
+cudaError_t launch_variant(const Int8Params& p, int num_sms, bool after_layout, cudaStream_t stream) {
+    using S = Shape<PAIR, BN>;
     static SmemLimitCache limits;
-    auto* fn = int8_gemm_kernel<PAIR, BN, ALIGNED>;
+    auto* fn = int8_gemm_kernel<PAIR, BN>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), S::kSmem, limits);
     if (e != cudaSuccess) return e;
     constexpr int ctas = PAIR ? 2 : 1;
     const long long units = (static_cast<long long>(p.M) + 128 * ctas - 1) / (128 * ctas) * ((p.N + BN - 1) / BN);
     const int slots = num_sms / ctas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((units < slots ? units : slots) * ctas));
+    cfg.gridDim = dim3(p.splits > 1 ? static_cast<unsigned>(units * p.splits)
+                                    : static_cast<unsigned>((units < slots ? units : slots) * ctas));
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (PAIR || p.splits > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = PAIR ? 2 : p.splits;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (after_layout) {  // its set-up overlaps the kernel before it
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    CUtensorMap map_x = {}, map_w = {};
-    if (ALIGNED && (!encode_rows(&map_x, p.x, p.M, p.K, 128) || !encode_rows(&map_w, p.w, p.N, p.K, S::kRowsB)))
+    cfg.numAttrs = n;
+    CUtensorMap map_x, map_w;
+    if (!encode_rows(&map_x, p.x, p.M, p.K, p.x_pitch, 128) || !encode_rows(&map_w, p.w, p.N, p.K, p.w_pitch, S::kRowsB))
         return cudaErrorInvalidValue;
     return cudaLaunchKernelEx(&cfg, fn, p, map_x, map_w);
 }
 
-template <bool PAIR, int BN>
-cudaError_t launch_aligned(const Int8Params& p, int num_sms, cudaStream_t stream) {
-    if (p.K % 16 == 0) return launch_variant<PAIR, BN, true>(p, num_sms, stream);
-    return launch_variant<PAIR, BN, false>(p, num_sms, stream);
+// Rows of K bytes to rows `pitch` apart (pitch a multiple of 16, at least K), 16 bytes a thread; the
+// bytes that only pad are 0.
+__global__ void __launch_bounds__(256) int8_layout_kernel(const int8_t* x, int8_t* xr, long long x_rows, const int8_t* w, int8_t* wr,
+                                                          long long w_rows, int K, int pitch) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int chunks = pitch >> 4;
+    const long long x_items = x_rows * chunks, items = x_items + w_rows * chunks;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < items; i += gridDim.x * 256LL) {
+        const bool is_x = i < x_items;
+        const long long at = is_x ? i : i - x_items;
+        const long long row = at / chunks;
+        const int k = static_cast<int>(at - row * chunks) * 16;
+        const int len = K - k < 16 ? K - k : 16;
+        const uint4 v = load_item(is_x ? x : w, row * K + k, len, (is_x ? x_rows : w_rows) * K);
+        *reinterpret_cast<uint4*>((is_x ? xr : wr) + row * pitch + k) = v;
+    }
 }
 
 }  // namespace
@@ -670,13 +745,27 @@ bool int8_gemm_fits(const Int8Params& p) {  // tile counts and row indexes in 32
     return (static_cast<long long>(p.M) + 127) / 128 * ((p.N + 31) / 32) < (1LL << 30) && p.M < (1 << 30) && p.N < (1 << 30);
 }
 
-cudaError_t launch_int8_gemm(const Int8Params& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_int8_layout(const int8_t* x, int8_t* xr, long long x_rows, const int8_t* w, int8_t* wr, long long w_rows,
+                               int K, int pitch, int num_sms, cudaStream_t stream) {
+    const long long blocks = ((x_rows + w_rows) * (pitch / 16) + 255) / 256;
+    int8_layout_kernel<<<static_cast<unsigned>(blocks < 8LL * num_sms ? blocks : 8LL * num_sms), 256, 0, stream>>>(
+        x, xr, x_rows, w, wr, w_rows, K, pitch);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_layout, cudaStream_t stream) {
+    Int8Params p = given;
     const long long m128 = (static_cast<long long>(p.M) + 127) / 128, m256 = (m128 + 1) / 2;
     const auto tiles = [&](int bn) { return (p.N + bn - 1) / bn; };
-    if (m128 > 1 && m256 * tiles(256) >= num_sms / 4) return launch_aligned<true, 256>(p, num_sms, stream);
-    if (m128 * tiles(128) >= num_sms / 2) return launch_aligned<false, 128>(p, num_sms, stream);
-    if (m128 * tiles(64) >= num_sms / 2) return launch_aligned<false, 64>(p, num_sms, stream);
-    return launch_aligned<false, 32>(p, num_sms, stream);
+    p.splits = 1;
+    if (m128 > 1 && m256 * tiles(256) >= num_sms / 4) return launch_variant<true, 256>(p, num_sms, after_layout, stream);
+    if (m128 * tiles(128) >= num_sms / 2) return launch_variant<false, 128>(p, num_sms, after_layout, stream);
+    // RULE
+    const int steps = (p.K + kStepK - 1) / kStepK;
+    int bn = m128 * tiles(64) >= num_sms / 2 ? 64 : 32;
+    while (p.splits < 8 && m128 * tiles(bn) * p.splits * 2 <= num_sms && steps / (2 * p.splits) >= 2) p.splits *= 2;
+    if (bn == 64) return launch_variant<false, 64>(p, num_sms, after_layout, stream);
+    return launch_variant<false, 32>(p, num_sms, after_layout, stream);
 }
 
 }  // namespace convgb

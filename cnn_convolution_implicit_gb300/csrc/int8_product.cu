@@ -206,10 +206,7 @@ cudaError_t launch_few(const Int8Params& p, const T* x, cudaStream_t stream) {
 
 bool int8_use_gemm(const Int8Params& p) { return p.M > 8; }
 
-cudaError_t launch_int8_product(const Int8Params& p, int num_sms, cudaStream_t stream) {
-    if (int8_use_gemm(p)) return launch_int8_gemm(p, num_sms, stream);
-    return launch_few<int8_t>(p, p.x, stream);
-}
+cudaError_t launch_int8_few(const Int8Params& p, cudaStream_t stream) { return launch_few<int8_t>(p, p.x, stream); }
 
 cudaError_t launch_int8_few_quantize(const Int8Params& p, const void* x, bool bf16, cudaStream_t stream) {
     if (bf16) return launch_few<__nv_bfloat16>(p, static_cast<const __nv_bfloat16*>(x), stream);

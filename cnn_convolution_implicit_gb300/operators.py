@@ -202,9 +202,9 @@ class Int8MatmulPlan:
             raise ValueError("x_shape must hold %d rows of %d" % (M, K))
         self._w, self._y = torch.Size((N, K)), torch.Size(self._x[:-1] + (N,))
         self._rows, self._cols = torch.Size((M,)), torch.Size((N,))
-        b = ctypes.c_ulonglong()
-        _check(L.conv_int8_workspace(h, ctypes.byref(b)), "conv_int8_workspace")
-        self.workspace_bytes = b.value
+        a, b = ctypes.c_ulonglong(), ctypes.c_ulonglong()
+        _check(L.conv_int8_workspace(h, ctypes.byref(a), ctypes.byref(b)), "conv_int8_workspace")
+        self.workspace_bytes = {"forward": a.value, "forward_quantize": b.value}
 
     def close(self):
         if self._plan is not None and binding._lib is not None:
@@ -242,8 +242,9 @@ class Int8MatmulPlan:
         _need(x_scale, "x_scale", self._rows, _t.float32, dev)
         if y is None:
             y = _t.empty(self._y, dtype=self.torch_dtype, device=dev)
+        ws = _workspace(self.workspace_bytes["forward"], dev)
         _check(self._L.conv_int8_forward(self._plan, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                                         _ptr(bias), y.data_ptr(), _raw_stream(dev)), "conv_int8_forward")
+                                         _ptr(bias), y.data_ptr(), _ptr(ws), _raw_stream(dev)), "conv_int8_forward")
         return y
 
     __call__ = forward
@@ -259,7 +260,7 @@ class Int8MatmulPlan:
         dev = self._operands(x, w, w_scale, bias, y)
         if y is None:
             y = _t.empty(self._y, dtype=self.torch_dtype, device=dev)
-        ws = _workspace(self.workspace_bytes, dev)
+        ws = _workspace(self.workspace_bytes["forward_quantize"], dev)
         _check(self._L.conv_int8_forward_quantize(self._plan, x.data_ptr(), CONV_BF16 if bf16 else CONV_F32, w.data_ptr(),
                                                   w_scale.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(ws),
                                                   _raw_stream(dev)), "conv_int8_forward_quantize")

@@ -465,20 +465,19 @@ typedef struct conv_int8_plan conv_int8_plan; /* opaque, host-owned */
  */
 conv_status conv_int8_plan_create(conv_int8_plan **plan, int M, int N, int K, conv_dtype out_dtype, conv_act act);
 
-/* The product.  Asynchronous on `stream`; y must not overlap the inputs.
- * CONV_ERR_INVALID_ARG for a NULL plan or a NULL required pointer or another current
- * device, CONV_ERR_MISALIGNED for a base that is not 16-byte aligned, CONV_ERR_CUDA if a
- * launch fails. */
-conv_status conv_int8_forward(conv_int8_plan *p, const void *x, const float *x_scale, const void *w,
-                              const float *w_scale, const float *bias, void *y, void *stream);
+/* Bytes of device workspace that conv_int8_forward and conv_int8_forward_quantize take (either
+ * may be 0, then NULL will do; either pointer may be NULL).  Its contents are of no account
+ * before and after a call; calls that may run at the same time take one each. */
+conv_status conv_int8_workspace(const conv_int8_plan *p, unsigned long long *forward, unsigned long long *quantize);
 
-/* Bytes of device workspace that conv_int8_forward_quantize takes (may be 0; pass NULL then). */
-conv_status conv_int8_workspace(const conv_int8_plan *p, unsigned long long *bytes);
+/* The product.  Asynchronous on `stream`; y must not overlap the inputs.
+ * CONV_ERR_INVALID_ARG for a NULL plan, a NULL required pointer or another current device,
+ * CONV_ERR_MISALIGNED for a base that is not 16-byte aligned, CONV_ERR_CUDA if a launch fails. */
+conv_status conv_int8_forward(conv_int8_plan *p, const void *x, const float *x_scale, const void *w,
+                              const float *w_scale, const float *bias, void *y, void *workspace, void *stream);
 
 /* The product from x [M][K] in FP32 or BF16 (x_dtype): its rows are brought to 8 bits in
- * the call, by the rules of conv_quantize_rows.  workspace: conv_int8_workspace bytes,
- * contents of no account before and after; calls that may run at the same time take one
- * each. */
+ * the call, by the rules of conv_quantize_rows.  Errors as above. */
 conv_status conv_int8_forward_quantize(conv_int8_plan *p, const void *x, conv_dtype x_dtype, const void *w,
                                        const float *w_scale, const float *bias, void *y, void *workspace,
                                        void *stream);

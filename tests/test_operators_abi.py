@@ -55,7 +55,7 @@ def test_null_and_misaligned_pointers():
     assert L.conv_group_norm_plan_create(None, 1, 32, 4, 4, 4, 1e-5, 1, 0) == 1
     assert L.conv_int8_plan_create(None, 1, 8, 8, 1, 0) == 1
     assert L.conv_group_norm_plan_destroy(None) == 0 and L.conv_int8_plan_destroy(None) == 0
-    assert L.conv_group_norm_workspace(None, None, None, None) == 1 and L.conv_int8_workspace(None, None) == 1
+    assert L.conv_group_norm_workspace(None, None, None, None) == 1 and L.conv_int8_workspace(None, None, None) == 1
     assert L.conv_int8_plan_device_status(None, None, None) == 1
     n = cg.GroupNormPlan(1, 32, 4, 4, 4)
     A = 256
@@ -75,16 +75,19 @@ def test_null_and_misaligned_pointers():
     assert bwd(n._plan, A, A, A, None, None, A + 8, A, A, A, None) == 3
     p = cg.Int8MatmulPlan(4, 8, 16)
     f, g = L.conv_int8_forward, L.conv_int8_forward_quantize
-    assert f(None, A, A, A, A, None, A, None) == 1
-    assert f(p._plan, A, None, A, A, None, A, None) == 1
-    assert f(p._plan, A, A, A, A, None, None, None) == 1
-    assert f(p._plan, A + 1, A, A, A, None, A, None) == 3
-    assert f(p._plan, A, A, A, A, A + 4, A, None) == 3
+    assert f(None, A, A, A, A, None, A, A, None) == 1
+    assert f(p._plan, A, None, A, A, None, A, A, None) == 1
+    assert f(p._plan, A, A, A, A, None, None, A, None) == 1
+    assert f(p._plan, A + 1, A, A, A, None, A, A, None) == 3
+    assert f(p._plan, A, A, A, A, A + 4, A, A, None) == 3
+    assert f(p._plan, A, A, A, A, None, A, A + 8, None) == 3
+    odd = cg.Int8MatmulPlan(400, 8, 20)
+    assert odd.workspace_bytes["forward"] > 0 and f(odd._plan, A, A, A, A, None, A, None, None) == 1  # rows to lay out
     assert g(p._plan, None, 1, A, A, None, A, A, None) == 1
     assert g(p._plan, A, 7, A, A, None, A, A, None) == 1
-    assert p.workspace_bytes == 0                                                # few rows need none
+    assert p.workspace_bytes == {"forward": 0, "forward_quantize": 0}            # few rows need none
     big = cg.Int8MatmulPlan(400, 8, 16)
-    assert big.workspace_bytes > 0 and g(big._plan, A, 1, A, A, None, A, None, None) == 1
+    assert big.workspace_bytes["forward"] == 0 and g(big._plan, A, 1, A, A, None, A, None, None) == 1
     assert g(p._plan, A + 2, 1, A, A, None, A, A, None) == 3
     quant = L.conv_quantize_rows
     assert quant(None, 1, 4, 4, A, A, None) == 1 and quant(A, 1, 0, 4, A, A, None) == 1
@@ -99,7 +102,7 @@ def test_without_a_device_calls_fail_loudly():
     assert L.conv_group_norm_forward(n._plan, A, None, None, A, None, A, None) == 4
     assert L.conv_group_norm_forward_int8(n._plan, A, None, None, A, A, None, A, None) == 4
     assert L.conv_group_norm_backward(n._plan, A, A, A, None, None, A, A, A, A, None) == 4
-    assert L.conv_int8_forward(p._plan, A, A, A, A, None, A, None) == 4
+    assert L.conv_int8_forward(p._plan, A, A, A, A, None, A, A, None) == 4
     assert L.conv_int8_forward_quantize(p._plan, A, 1, A, A, None, A, A, None) == 4
     assert L.conv_quantize_rows(A, 1, 4, 4, A, A, None) == 4
     code = ctypes.c_int(5)
