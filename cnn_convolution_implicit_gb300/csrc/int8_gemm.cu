@@ -753,18 +753,53 @@ cudaError_t launch_int8_layout(const int8_t* x, int8_t* xr, long long x_rows, co
     return cudaGetLastError();
 }
 
+namespace {
+
+// Tile shapes and what they cost, in microseconds on a 152-SM part at ~1.9 GHz (repeated launches
+// in a graph, 8-bit input, BF16 output): a K = 64 step, the least a tile takes (its epilogue), and
+// what joining the parts adds where a cluster splits K.  From 16 x 4096 x 4096 (64 steps): 29.4 us as
+// 128 tiles of 32 columns, 18.8 as 64 tiles of 64 split in two, 14.2 as 32 tiles of 128 split
+// in four; from 1000 x 4096 x 4096: 66 us in tiles of 128 x 128 and 37 on pairs; from
+// 100 x 512 x 512 in two steps: 7.2 / 7.5 / 9.3 us with 32 / 64 / 128 columns.
+struct Tile {
+    int rows, columns;
+    double step, least, join;
+};
+constexpr Tile kTiles[4] = {{128, 32, 0.38, 0.6, 1.9}, {128, 64, 0.42, 1.0, 2.4}, {128, 128, 0.55, 2.0, 3.8}, {256, 256, 0.50, 4.0, 0.0}};
+
+// Clusters of this kernel's CTAs (one an SM) that the part holds at a time, by CTAs in a cluster: a
+// 152-SM part holds 76 of 2, 36 of 4 and 15 of 8.
+int clusters_at_a_time(int num_sms, int ctas) {
+    return ctas == 1 ? num_sms : (ctas == 2 ? num_sms / 2 : (ctas == 4 ? num_sms * 36 / 152 : num_sms * 15 / 152));
+}
+
+}  // namespace
+
+// The tile shape and split of K that cost least by those figures.
 cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_layout, cudaStream_t stream) {
     Int8Params p = given;
-    const long long m128 = (static_cast<long long>(p.M) + 127) / 128, m256 = (m128 + 1) / 2;
-    const auto tiles = [&](int bn) { return (p.N + bn - 1) / bn; };
-    p.splits = 1;
-    if (m128 > 1 && m256 * tiles(256) >= num_sms / 4) return launch_variant<true, 256>(p, num_sms, after_layout, stream);
-    if (m128 * tiles(128) >= num_sms / 2) return launch_variant<false, 128>(p, num_sms, after_layout, stream);
-    // RULE
-    const int steps = (p.K + kStepK - 1) / kStepK;
-    int bn = m128 * tiles(64) >= num_sms / 2 ? 64 : 32;
-    while (p.splits < 8 && m128 * tiles(bn) * p.splits * 2 <= num_sms && steps / (2 * p.splits) >= 2) p.splits *= 2;
-    if (bn == 64) return launch_variant<false, 64>(p, num_sms, after_layout, stream);
+    const long long steps = (p.K + kStepK - 1) / kStepK;
+    double best = 0.0;
+    int tile = -1;
+    for (int i = 0; i < 4; ++i) {
+        const Tile& t = kTiles[i];
+        const long long units = (static_cast<long long>(p.M) + t.rows - 1) / t.rows * ((p.N + t.columns - 1) / t.columns);
+        for (int splits = 1; splits <= (i < 3 ? 8 : 1); splits *= 2) {
+            const long long at_a_time = clusters_at_a_time(num_sms, i == 3 ? 2 : splits);
+            if (splits > 1 && (units > at_a_time || steps < 2 * splits)) break;
+            const double each = static_cast<double>((steps + splits - 1) / splits) * t.step;
+            const double cost = static_cast<double>((units + at_a_time - 1) / at_a_time) * (each > t.least ? each : t.least) +
+                                (splits > 1 ? t.join : 0.0);
+            if (tile < 0 || cost < best) {
+                best = cost;
+                tile = i;
+                p.splits = splits;
+            }
+        }
+    }
+    if (tile == 3) return launch_variant<true, 256>(p, num_sms, after_layout, stream);
+    if (tile == 2) return launch_variant<false, 128>(p, num_sms, after_layout, stream);
+    if (tile == 1) return launch_variant<false, 64>(p, num_sms, after_layout, stream);
     return launch_variant<false, 32>(p, num_sms, after_layout, stream);
 }
 
