@@ -921,8 +921,12 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
                         for (int u = 0; u < U; ++u) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
                 }
                 RowScale rs[U];
+                if (vpr >= U) {
+                    row_scales<U>(a, v, vpr, rs);
+                } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+                    for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (i0 + u < mine) {
@@ -1230,8 +1234,12 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
                     for (int u = 0; u < U; ++u) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
             }
             RowScale rs[U];
+            if (by_lanes && t.vpr >= U) {
+                row_scales<U>(a, t.v, t.vpr, rs);
+            } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+                for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (i0 + u < t.mine) {

@@ -183,6 +183,23 @@ __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
     return {__fdiv_rn(amax, 127.0f), __fdiv_rn(127.0f, amax), ~0u};
 }
 
+// Scales of R rows whose magnitudes every lane of a segment holds: lane r of it works out row r's (the
+// two divisions once for all rows) and hands it round.  lane: within the segment, of `width` lanes
+// (a power of two, R at least).
+template <int R>
+__device__ __forceinline__ void row_scales(const uint32_t (&top)[R], int lane, int width, RowScale (&rs)[R]) {
+    uint32_t mine = top[0];
+#pragma unroll
+    for (int r = 1; r < R; ++r) mine = lane == r ? top[r] : mine;
+    const RowScale own = row_scale(mine);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        rs[r].scale = __shfl_sync(0xffffffffu, own.scale, r, width);
+        rs[r].inv = __shfl_sync(0xffffffffu, own.inv, r, width);
+        rs[r].keep = __shfl_sync(0xffffffffu, own.keep, r, width);
+    }
+}
+
 // Four values to four bytes, the first in the low one.  |x * inv| <= 127 up to one rounding; adding
 // 1.5 * 2^23 rounds it to an integer (ties to even), whose low byte is then the sum's.
 __device__ __forceinline__ uint32_t quantise4(f2 a, f2 b, const RowScale& r) {
