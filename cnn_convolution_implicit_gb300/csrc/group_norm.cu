@@ -1057,6 +1057,58 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
     (void)warp;
 }
 
+// One group of an image from its ranges, by `width` threads of which this is the k-th: (mean, rstd),
+// or the backward pass's (a, b).  sum() adds over those threads.
+template <int MODE, typename F>
+__device__ __forceinline__ float2 join_ranges(const NormParams& p, int n, int g, int k0, int width, F&& sum) {
+    const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
+    const float2* from = (MODE == kNormBackward ? p.ab : p.part) + (static_cast<long long>(n) * p.G + g) * p.splits;
+    const int end = g < p.G ? p.splits : 0;
+    if constexpr (MODE == kNormBackward) {
+        float a = 0.0f, b = 0.0f;
+        for (int k = k0; k < end; k += width) {
+            a += from[k].x;
+            b += from[k].y;
+        }
+        a = sum(a);
+        return make_float2(a * over_total, sum(b) * over_total);
+    } else {
+        const float each = static_cast<float>(p.pix_base) * static_cast<float>(p.cpg);
+        const float one_more = static_cast<float>(p.pix_base + 1) * static_cast<float>(p.cpg);
+        float m = 0.0f, q = 0.0f;
+        for (int k = k0; k < end; k += width) m = fmaf(k < p.pix_more ? one_more : each, from[k].x, m);
+        m = sum(m) * over_total;
+        for (int k = k0; k < end; k += width) {
+            const float2 o = from[k];
+            const float d = o.x - m;
+            q += fmaf((k < p.pix_more ? one_more : each) * d, d, o.y);
+        }
+        const float var = sum(q) * over_total;
+        return make_float2(m, __fdiv_rn(1.0f, __fsqrt_rn(var + p.eps)));
+    }
+}
+
+__device__ __forceinline__ long long norm_ab_of(const NormParams& p) { return static_cast<long long>(p.N) * p.G * p.splits; }
+
+// Many ranges an image (few images): joined once, a CTA to each group, instead of by every CTA of the
+// second pass (608 ranges of 1 x 512 x 512 x 128: 94 MB of partials read again, 48 us of 70).
+template <int MODE>
+__global__ void __launch_bounds__(128) norm_range_join_kernel(const NormParams p) {
+    __shared__ float scratch[4];
+    launch_dependents();
+    wait_for_previous();
+    const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
+    const float2 res = join_ranges<MODE>(p, n, g, threadIdx.x, 128, [&](float v) { return block_sum(v, scratch); });
+    if (threadIdx.x == 0) {
+        if constexpr (MODE == kNormBackward) {
+            p.ab[norm_ab_of(p) + blockIdx.x] = res;
+        } else {
+            p.mean[blockIdx.x] = res.x;
+            p.rstd[blockIdx.x] = res.y;
+        }
+    }
+}
+
 // Second pass.  Joins the ranges of the image's groups, then writes the range backwards.  Backward:
 // the first `extra` CTAs write dgamma and dbeta instead, 32 channels each.
 template <typename T, int MODE, int ACT>
@@ -1098,40 +1150,22 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
     if constexpr (MODE == kNormBackward) grad.set(p, my_c, [&](int c) { return stats_of(p, t.n, c); });
     else af.load(p, my_c);
     wait_for_previous();
-    {
-        const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
+    if (p.joined) {
+        for (int g = threadIdx.x; g < p.G; g += kNormThreads)
+            joined[g] = MODE == kNormBackward ? p.ab[norm_ab_of(p) + t.n * p.G + g]
+                                              : make_float2(p.mean[t.n * p.G + g], p.rstd[t.n * p.G + g]);
+    } else {
         const int wide = segment_width(p.splits), at_once = 32 / wide;
         for (int gfirst = warp * at_once; gfirst < p.G; gfirst += kNormThreads / 32 * at_once) {
             const int g = gfirst + lane / wide;
-            const float2* from = (MODE == kNormBackward ? p.ab : p.part) + (static_cast<long long>(t.n) * p.G + g) * p.splits;
-            const int end = g < p.G ? p.splits : 0;
-            float2 res;
-            if constexpr (MODE != kNormBackward) {
-                float m = 0.0f, q = 0.0f;
-                for (int k = lane & (wide - 1); k < end; k += wide)
-                    m = fmaf(static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg), from[k].x, m);
-                m = segment_sum(m, wide) * over_total;
-                for (int k = lane & (wide - 1); k < end; k += wide) {
-                    const float cnt = static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg);
-                    const float2 o = from[k];
-                    const float d = o.x - m;
-                    q += fmaf(cnt * d, d, o.y);
-                }
-                const float var = segment_sum(q, wide) * over_total;
-                res = make_float2(m, __fdiv_rn(1.0f, __fsqrt_rn(var + p.eps)));
-                if (t.s == 0 && (lane & (wide - 1)) == 0 && g < p.G && p.mean != nullptr) {
+            const float2 res = join_ranges<MODE>(p, t.n, g, lane & (wide - 1), wide, [&](float v) { return segment_sum(v, wide); });
+            if ((lane & (wide - 1)) == 0 && g < p.G) {
+                joined[g] = res;
+                if (MODE != kNormBackward && t.s == 0 && p.mean != nullptr) {
                     p.mean[t.n * p.G + g] = res.x;
                     p.rstd[t.n * p.G + g] = res.y;
                 }
-            } else {
-                float a = 0.0f, b = 0.0f;
-                for (int k = lane & (wide - 1); k < end; k += wide) {
-                    a += from[k].x;
-                    b += from[k].y;
-                }
-                res = make_float2(segment_sum(a, wide) * over_total, segment_sum(b, wide) * over_total);
             }
-            if ((lane & (wide - 1)) == 0 && g < p.G) joined[g] = res;
         }
     }
     __syncthreads();
@@ -1377,6 +1411,9 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
         if (best != 0) break;
     }
     if (best == 0 || units * best > 0x7fffffffLL) return;
+    // 8-bit output in more than one round of CTAs: the pixel-wide units make large clusters and long
+    // CTAs (64 x 56 x 56 x 256 BF16: 92 us, in two passes 79; 2 x 16 x 16 x 128: 10 us against 13).
+    if (mode == kNormInt8 && units * best > 2LL * num_sms) return;
     while (2 * best <= kResMaxCluster && units * best * 2 <= num_sms && p.P >= 2 * best * rows) best *= 2;
     fits(best, smem_optin);
     t.pix_base = t.P / best;
@@ -1394,6 +1431,7 @@ void norm_pick_two_pass(NormParams& p, int mode, int num_sms) {
     if (splits > most) splits = most;
     p.two_pass = 1;
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    p.joined = p.splits > 64;
     p.pix_base = p.P / p.splits;
     p.pix_more = p.P % p.splits;
 }
@@ -1423,7 +1461,7 @@ size_t norm_workspace_bytes(const NormParams& p) {
 }
 
 size_t norm_part_entries(const NormParams& p) { return static_cast<size_t>(p.N) * p.splits * p.C; }
-size_t norm_ab_entries(const NormParams& p) { return static_cast<size_t>(p.N) * p.G * (p.two_pass ? p.splits : 1); }
+size_t norm_ab_entries(const NormParams& p) { return static_cast<size_t>(p.N) * p.G * (p.two_pass ? p.splits + p.joined : 1); }
 
 namespace {
 
@@ -1448,15 +1486,21 @@ cudaError_t launch_two_pass(const NormParams& p, cudaStream_t stream) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(grid + extra);
-        cfg.blockDim = dim3(kNormThreads);
-        cfg.dynamicSmemBytes = apply_smem;
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
+        if (p.joined) {
+            cfg.gridDim = dim3(static_cast<unsigned>(p.N) * p.G);
+            cfg.blockDim = dim3(128);
+            e = cudaLaunchKernelEx(&cfg, norm_range_join_kernel<MODE == kNormBackward ? kNormBackward : kNormForward>, p);
+            if (e != cudaSuccess) return;
+        }
+        cfg.gridDim = dim3(grid + extra);
+        cfg.blockDim = dim3(kNormThreads);
+        cfg.dynamicSmemBytes = apply_smem;
         e = cudaLaunchKernelEx(&cfg, apply, p, extra);
     };
     with_act(p.act, [&](auto act) {

@@ -23,7 +23,7 @@ void carve_workspace(NormParams& p, void* workspace) {
     if (p.chunk != 0 && p.dy == nullptr) return;  // resident forward passes need none
     p.part = static_cast<float2*>(workspace);
     p.ab = p.part + norm_part_entries(p);
-    if (p.mean == nullptr && !p.two_pass) {
+    if (p.mean == nullptr && (!p.two_pass || p.joined)) {
         p.mean = reinterpret_cast<float*>(p.ab + norm_ab_entries(p));
         p.rstd = p.mean + static_cast<size_t>(p.N) * p.G;
     }

@@ -21,6 +21,7 @@ struct NormParams {
     int vec;      // elements per access: 16 bytes where every pixel starts on 16 bytes, else 1
     int splits;   // pixel ranges per image, or the CTAs of a resident cluster
     int two_pass; // two passes over pixel ranges (else, without a chunk, by channel)
+    int joined;   // two passes: a kernel between them joins the ranges
     // resident form (0 chunk: another): a cluster of `splits` CTAs holds `chunk` channels of an image
     int chunk;
     int items;       // 16-byte vectors a thread holds of each tensor

@@ -1,10 +1,10 @@
 // quantize.cu -- rows of FP32 or BF16 values to 8-bit integers with one scale
 // per row: scale = amax / 127, q = rint(x * (127 / amax)).
 //
-// Bound by the bytes of x read and q written.  One warp per row: a row of at most two 16-byte
-// vectors a lane (1 KB) stays in registers, and a warp takes several such rows at a time, so
-// that their loads are under way together (200704 rows of 256 BF16: 33 us one at a time, see
-// the figure at the launch).  Longer rows take two sweeps, the largest magnitude, then the
+// Bound by the bytes of x read and q written.  One warp per row: a row of at most sixteen 16-byte
+// vectors a lane (8 KB) stays in registers, and a warp takes several short ones at a time, so
+// that a lane has about four loads or more under way (200704 rows of 256 BF16: 40 us one row at
+// a time, 27 us four; the divisions of a row's scale are shared out too).  Longer rows take two sweeps, the largest magnitude, then the
 // values; the second finds a row of ordinary length in L1.
 #include "int8_internal.h"
 #include "pointwise_math.cuh"
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* x
 
 // Rows of at most 32 P vectors, in registers, R at a time.
 template <typename T, int P, int R>
-__global__ void __launch_bounds__(kQuantThreads, 4) quantize_short_rows_kernel(const T* x, int M, int K, int pitch, int8_t* q,
+__global__ void __launch_bounds__(kQuantThreads, P >= 16 ? 2 : (P >= 8 ? 3 : 4)) quantize_short_rows_kernel(const T* x, int M, int K, int pitch, int8_t* q,
                                                                                float* scale) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that may follow
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
@@ -104,12 +104,17 @@ template <typename T>
 cudaError_t launch_typed(const T* x, int M, int K, int pitch, int8_t* q, float* scale, int num_sms, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const bool wide = K % V == 0;
-    const int parts = wide && K / V <= 64 ? (K / V <= 32 ? 1 : 2) : 0;  // vectors a lane keeps of a row
-    const long long rows = (kQuantThreads / 32) * (parts == 1 ? 4 : (parts == 2 ? 2 : 1));
+    int parts = 1;  // vectors a lane keeps of a row
+    while (parts < 16 && 32 * parts < K / V) parts *= 2;
+    const bool in_registers = wide && 32 * parts >= K / V;
+    const long long rows = (kQuantThreads / 32) * (in_registers && parts <= 2 ? 4 / parts : 1);
     const long long need = (static_cast<long long>(M) + rows - 1) / rows;
     const unsigned grid = static_cast<unsigned>(need < 8LL * num_sms ? need : 8LL * num_sms);
-    if (parts == 1) quantize_short_rows_kernel<T, 1, 4><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else if (parts == 2) quantize_short_rows_kernel<T, 2, 2><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
+    if (in_registers && parts == 1) quantize_short_rows_kernel<T, 1, 4><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
+    else if (in_registers && parts == 2) quantize_short_rows_kernel<T, 2, 2><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
+    else if (in_registers && parts == 4) quantize_short_rows_kernel<T, 4, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
+    else if (in_registers && parts == 8) quantize_short_rows_kernel<T, 8, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
+    else if (in_registers) quantize_short_rows_kernel<T, 16, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
     else if (wide) quantize_rows_kernel<T, V><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
     else quantize_rows_kernel<T, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
     return cudaGetLastError();
