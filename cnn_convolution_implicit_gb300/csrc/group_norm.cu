@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_int8_kernel(const Nor
         for (int v = lane; v < vecs; v += 32) {
             f2 f[Affine<VEC>::H];
             value(v, f);
-            quantise_store<VEC>(p.q + row * p.C + v * VEC, f, rs);
+            quantise_store<VEC>(p.q + row * p.C + v * VEC, f, row_factor(rs.inv));
         }
     }
 }
@@ -738,8 +738,8 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
     int p0, p1;
     res_range(p, rank, p0, p1);
     const int mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;  // this thread's items
-    const long long step = static_cast<long long>(rows) * p.C;
-    const long long base = (static_cast<long long>(n) * p.P + p0 + r) * p.C + c0 + v * VEC;
+    const int step = rows * (p.C / VEC);     // in vectors; an image has fewer than 2^31 of them
+    const long long base = ((static_cast<long long>(n) * p.P + p0 + r) * p.C + c0) / VEC + v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int batch = (p.items + kResBatches - 1) / kResBatches;
     if (p.splits > 1) res_cluster_arrive();  // this CTA runs: its peers may write to it after their wait below
@@ -747,8 +747,8 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
     const uint4* items_dy = sm.dy + threadIdx.x;
 
     {
-        const T* x = static_cast<const T*>(p.x) + base;
-        const T* dy = static_cast<const T*>(p.dy) + base;
+        const uint4* x = static_cast<const uint4*>(p.x) + base;
+        const uint4* dy = static_cast<const uint4*>(p.dy) + base;
         const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(items));
         const uint32_t dst2 = static_cast<uint32_t>(__cvta_generic_to_shared(items_dy));
 #pragma unroll
@@ -869,18 +869,18 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
     const auto result = [&](int c) { return sm.result[(c - c0) / p.cpg]; };
     if constexpr (MODE == kNormForward) {
         af.set(my_c, p.cpg, result);
-        T* y = static_cast<T*>(p.y) + base;
+        uint4* y = static_cast<uint4*>(p.y) + base;
 #pragma unroll 4
         for (int i = 0; i < mine; ++i) {
             f2 f[H];
             Io::unpack(items[i * kThreads], f);
             af.template apply<ACT>(f);
-            *reinterpret_cast<uint4*>(y + i * step) = Io::pack(f);
+            y[i * step] = Io::pack(f);
         }
     } else if constexpr (MODE == kNormBackward) {
         GroupMeans<VEC> gm;
         gm.set(my_c, p.cpg, result);
-        T* dx = static_cast<T*>(p.y) + base;
+        uint4* dx = static_cast<uint4*>(p.y) + base;
 #pragma unroll 2
         for (int i = 0; i < mine; ++i) {
             f2 f[H], d[H];
@@ -888,14 +888,14 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
             Io::unpack(items_dy[i * kThreads], d);
             grad.template apply<ACT>(f, d);
             gm.dx(f, d, grad);
-            *reinterpret_cast<uint4*>(dx + i * step) = Io::pack(f);
+            dx[i * step] = Io::pack(f);
         }
     } else {
         // 8-bit output (chunk = C: whole pixels here).  A pixel on 1, 2, 4, ... 32 neighbouring lanes
         // finds its largest magnitude by shuffles; any other width through shared memory.
         af.set(my_c, p.cpg, result);
         float* scales = p.scale + static_cast<long long>(n) * p.P + p0 + r;
-        int8_t* q = p.q + base;
+        int8_t* q = p.q + base * VEC;
         const auto value = [&](int i, f2 (&f)[H]) {
             Io::unpack(items[i * kThreads], f);
             af.template apply<ACT>(f);
@@ -920,19 +920,21 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
 #pragma unroll
                         for (int u = 0; u < U; ++u) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
                 }
-                RowScale rs[U];
+                RowFactor rf[U];
                 if (vpr >= U) {
-                    row_scales<U>(a, v, vpr, rs);
+                    const float own = row_factors<U>(a, v, vpr, rf);
+                    if (v < U && i0 + v < mine) scales[(i0 + v) * rows] = own;
                 } else {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+                    for (int u = 0; u < U; ++u) {
+                        const RowScale rs = row_scale(a[u]);
+                        rf[u] = row_factor(rs.inv);
+                        if (v == 0 && i0 + u < mine) scales[(i0 + u) * rows] = rs.scale;
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (i0 + u < mine) {
-                        quantise_store<VEC>(q + (i0 + u) * step, f[u], rs[u]);
-                        if (v == 0) scales[(i0 + u) * rows] = rs[u].scale;
-                    }
+                    if (i0 + u < mine) quantise_store<VEC>(q + static_cast<long long>((i0 + u) * step) * VEC, f[u], rf[u]);
             }
         } else {
             for (int i = 0; i < mine; ++i) {
@@ -944,7 +946,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
                 f2 f[H];
                 value(i, f);
                 const RowScale rs = row_scale(sm.top[r + i * rows]);
-                quantise_store<VEC>(q + i * step, f, rs);
+                quantise_store<VEC>(q + static_cast<long long>(i * step) * VEC, f, row_factor(rs.inv));
                 if (v == 0) scales[i * rows] = rs.scale;
             }
         }
@@ -963,7 +965,8 @@ __device__ __forceinline__ void store_past(uint4* p, uint4 v) { __stcs(p, v); }
 // Where a CTA of either pass stands: pixel range `s` of image n, all channels.
 struct TwoRange {
     int n, s, vpr, rows, r, v, p0, p1, mine;
-    long long base, step;  // in vectors
+    long long base;  // in vectors; an image has fewer than 2^31 of them
+    int step;
     __device__ __forceinline__ TwoRange(const NormParams& p, int block, int VEC) {
         n = block / p.splits;
         s = block - n * p.splits;
@@ -974,7 +977,7 @@ struct TwoRange {
         res_range(p, s, p0, p1);
         mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;
         base = (static_cast<long long>(n) * p.P + p0 + r) * vpr + v;
-        step = static_cast<long long>(rows) * vpr;
+        step = rows * vpr;
     }
 };
 
@@ -990,6 +993,7 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint4* x = static_cast<const uint4*>(p.x) + t.base;
     launch_dependents();
+    const long long step = t.step;  // 64 bits: the addresses of a batch are one running sum (32 measured 10% slower here)
     if constexpr (MODE != kNormBackward) {
         Moments<VEC> mo;
         f2 f[H];
@@ -997,12 +1001,12 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
             Io::unpack(__ldg(x), f);
             mo.start(f);
         }
-        constexpr int B = 2 * kTwoBatch;
+        constexpr int B = kTwoBatch;  // eight spill at four CTAs an SM
         for (int i = 0; i < t.mine; i += B) {
             uint4 raw[B];
 #pragma unroll
             for (int k = 0; k < B; ++k)
-                if (i + k < t.mine) raw[k] = __ldg(x + (i + k) * t.step);
+                if (i + k < t.mine) raw[k] = __ldg(x + (i + k) * step);
 #pragma unroll
             for (int k = 0; k < B; ++k)
                 if (i + k < t.mine) {
@@ -1040,8 +1044,8 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
 #pragma unroll
             for (int k = 0; k < B; ++k)
                 if (i + k < t.mine) {
-                    a[k] = __ldg(x + (i + k) * t.step);
-                    b[k] = __ldg(dy + (i + k) * t.step);
+                    a[k] = __ldg(x + static_cast<unsigned>((i + k) * t.step));
+                    b[k] = __ldg(dy + static_cast<unsigned>((i + k) * t.step));
                 }
 #pragma unroll
             for (int k = 0; k < B; ++k)
@@ -1112,7 +1116,7 @@ __global__ void __launch_bounds__(128) norm_range_join_kernel(const NormParams p
 // Second pass.  Joins the ranges of the image's groups, then writes the range backwards.  Backward:
 // the first `extra` CTAs write dgamma and dbeta instead, 32 channels each.
 template <typename T, int MODE, int ACT>
-__global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) norm_range_apply_kernel(const NormParams p, int extra) {
+__global__ void __launch_bounds__(kNormThreads, MODE == kNormForward ? 4 : 3) norm_range_apply_kernel(const NormParams p, int extra) {
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
     using Io = VecIo<T, VEC>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -1173,18 +1177,19 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
     if constexpr (MODE == kNormForward) {
         af.set(my_c, p.cpg, result);
         uint4* y = static_cast<uint4*>(p.y) + t.base;
+        const long long step = t.step;
         const auto put = [&](const uint4& raw, int i) {
             f2 f[H];
             Io::unpack(raw, f);
             af.template apply<ACT>(f);
-            store_past(y + i * t.step, Io::pack(f));
+            store_past(y + i * step, Io::pack(f));
         };
         constexpr int B = kTwoBatch;
         for (int i = t.mine; i > 0; i -= B) {
             uint4 raw[B];
 #pragma unroll
             for (int k = 0; k < B; ++k)
-                if (i > k) raw[k] = load_last(x + (i - 1 - k) * t.step);
+                if (i > k) raw[k] = load_last(x + (i - 1 - k) * step);
 #pragma unroll
             for (int k = 0; k < B; ++k)
                 if (i > k) put(raw[k], i - 1 - k);
@@ -1200,7 +1205,7 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
             Io::unpack(b, d);
             grad.template apply<ACT>(f, d);
             gm.dx(f, d, grad);
-            store_past(dx + i * t.step, Io::pack(f));
+            store_past(dx + static_cast<unsigned>(i * t.step), Io::pack(f));
         };
         constexpr int B = kTwoBatch / 2;
         for (int i = t.mine; i > 0; i -= B) {
@@ -1208,8 +1213,8 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
 #pragma unroll
             for (int k = 0; k < B; ++k)
                 if (i > k) {
-                    a[k] = load_last(x + (i - 1 - k) * t.step);
-                    b[k] = load_last(dy + (i - 1 - k) * t.step);
+                    a[k] = load_last(x + static_cast<unsigned>((i - 1 - k) * t.step));
+                    b[k] = load_last(dy + static_cast<unsigned>((i - 1 - k) * t.step));
                 }
 #pragma unroll
             for (int k = 0; k < B; ++k)
@@ -1217,9 +1222,9 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
         }
     } else {
         // A pixel on 1, 2, 4, ... 32 neighbouring lanes finds its largest magnitude by shuffles, any
-        // other width through shared memory; two pixels under way at a time.
+        // other width through shared memory; four pixels under way at a time.
         af.set(my_c, p.cpg, result);
-        constexpr int U = 2;
+        constexpr int U = 4;
         float* scales = p.scale + static_cast<long long>(t.n) * p.P + t.p0 + t.r;
         const bool by_lanes = (t.vpr & (t.vpr - 1)) == 0 && t.vpr <= 32;
         uint32_t* top = reinterpret_cast<uint32_t*>(joined + p.G);  // [2][U][rows]
@@ -1235,7 +1240,7 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
             uint32_t a[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (i0 + u < t.mine) raw[u] = load_last(x + (i0 + u) * t.step);
+                if (i0 + u < t.mine) raw[u] = load_last(x + static_cast<unsigned>((i0 + u) * t.step));
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 a[u] = 0;
@@ -1267,19 +1272,22 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
 #pragma unroll
                     for (int u = 0; u < U; ++u) a[u] = max(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
             }
-            RowScale rs[U];
+            RowFactor rf[U];
             if (by_lanes && t.vpr >= U) {
-                row_scales<U>(a, t.v, t.vpr, rs);
+                const float own = row_factors<U>(a, t.v, t.vpr, rf);
+                if (t.v < U && i0 + t.v < t.mine) scales[(i0 + t.v) * t.rows] = own;
             } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u) rs[u] = row_scale(a[u]);
+                for (int u = 0; u < U; ++u) {
+                    const RowScale rs = row_scale(a[u]);
+                    rf[u] = row_factor(rs.inv);
+                    if (t.v == 0 && i0 + u < t.mine) scales[(i0 + u) * t.rows] = rs.scale;
+                }
             }
+            int8_t* q = p.q + t.base * VEC;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (i0 + u < t.mine) {
-                    quantise_store<VEC>(p.q + (t.base + (i0 + u) * t.step) * VEC, f[u], rs[u]);
-                    if (t.v == 0) scales[(i0 + u) * t.rows] = rs[u].scale;
-                }
+                if (i0 + u < t.mine) quantise_store<VEC>(q + static_cast<long long>((i0 + u) * t.step) * VEC, f[u], rf[u]);
         }
     }
 }
@@ -1378,7 +1386,7 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
     p.chunk = 0;
-    if (p.vec == 1) return;
+    if (p.vec == 1 || static_cast<long long>(p.P) * (p.C / p.vec) >= (1LL << 31)) return;
     int chunk = 0;
     if (mode == kNormInt8) {
         chunk = p.C;
@@ -1411,6 +1419,8 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
         if (best != 0) break;
     }
     if (best == 0 || units * best > 0x7fffffffLL) return;
+    // Backward on clusters of more than eight: 32 x 112 x 112 x 128 BF16 123 us, in two passes 111.
+    if (mode == kNormBackward && best > 8) return;
     // 8-bit output in more than one round of CTAs: the pixel-wide units make large clusters and long
     // CTAs (64 x 56 x 56 x 256 BF16: 92 us, in two passes 79; 2 x 16 x 16 x 128: 10 us against 13).
     if (mode == kNormInt8 && units * best > 2LL * num_sms) return;
@@ -1421,12 +1431,12 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     p = t;
 }
 
-// Two passes: pixel ranges that fill the SMs once, four CTAs to each (three backward).
+// Two passes: pixel ranges that fill the SMs once, four CTAs to each (three backward or to 8 bits).
 void norm_pick_two_pass(NormParams& p, int mode, int num_sms) {
     const int vecs = p.C / p.vec;
-    if (p.vec == 1 || vecs > kNormThreads) return;
+    if (p.vec == 1 || vecs > kNormThreads || static_cast<long long>(p.P) * vecs >= (1LL << 31)) return;
     const int rows = kNormThreads / vecs;
-    long long splits = static_cast<long long>(num_sms) * (mode == kNormBackward ? 3 : 4) / p.N;
+    long long splits = static_cast<long long>(num_sms) * (mode == kNormForward ? 4 : 3) / p.N;
     const long long most = p.P / (2LL * rows);  // two pixels a thread at least
     if (splits > most) splits = most;
     p.two_pass = 1;
@@ -1479,7 +1489,7 @@ cudaError_t launch_two_pass(const NormParams& p, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>(p.N) * p.splits;
     const int extra = MODE == kNormBackward && p.dgamma != nullptr ? (p.C + 31) / 32 : 0;
     const int vpr = p.C / p.vec, rows = kNormThreads / vpr;
-    const int joined = p.G * 8 + (MODE == kNormInt8 ? 2 * 2 * rows * 4 : 0);
+    const int joined = p.G * 8 + (MODE == kNormInt8 ? 2 * 4 * rows * 4 : 0);
     const int apply_smem = joined > kNormThreads * 8 ? joined : kNormThreads * 8;
     const auto run = [&](auto* sums, auto* apply) {
         sums<<<grid, kNormThreads, range_sums_smem<MODE>(p), stream>>>(p);

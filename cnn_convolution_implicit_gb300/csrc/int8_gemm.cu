@@ -69,11 +69,12 @@ struct Shape {
     static constexpr int kStage = kTileA + kRowsB * kRowBytes;
     static constexpr int kStages = kGroups;              // one for each converter group
     static constexpr int kRaw = (128 + kRowsB) * kStepK;  // one slot of the raw ring
-    static constexpr int kRawSlots = kRowsB >= 128 ? 6 : 8;  // in 227 KB beside the stages
+    static constexpr int kRawSlots = kRowsB >= 128 ? 4 : 8;  // in 227 KB beside the stages and the outputs
+    static constexpr int kOut = 2048;                    // an epilogue warp's block of BF16 outputs, two of them
     static constexpr int kPartRow = BN + 8;              // floats of a row of partial sums (K split over a cluster)
     static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 256;
+    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 2 * kEpilogueWarps * kOut + 256;
 };
 
 struct Bars {
@@ -291,10 +292,18 @@ struct Drain {
     uint8_t* y;      // its first row and column
     long long row8;  // bytes of 8 rows of y
     float xs[4];
+    // BF16 blocks through the TMA: the warp's two buffers, which one is next, and the block's place in y
+    const CUtensorMap* map;
+    uint8_t* out;
+    int turn, block_n, block_m;
 };
 
 // G: 16-row groups of the quarter that this warp drains.
-template <int ACT, bool BF16, bool WHOLE, int G>
+// TMA: the block goes through shared memory (64-byte rows, 64-byte swizzle: the eight lanes of two
+// rows write 128 bytes) and out in one or two bulk stores of 16 rows, which clip what lies past
+// M and N; straight from registers a store touches 8 lines of which it fills half
+// (200704 x 256 -> 512, 8-bit input: 86 us, FIGURE through the TMA).
+template <int ACT, bool BF16, bool WHOLE, bool TMA, int G>
 __device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d) {
     uint32_t v[G][16];
 #pragma unroll
@@ -307,9 +316,32 @@ __device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         finish_block<ACT>(v[g], d.xs[2 * g], d.xs[2 * g + 1], ws, bias);
+        if constexpr (TMA) {
+            if (g == 0) {  // the buffer's last store has read it
+                if ((threadIdx.x & 31) == 0) bulk_wait_read_le1();
+                __syncwarp();
+            }
+            const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (d.rows >> (2 * g + h) & 1) store_row<BF16, WHOLE>(d.y + (2 * g + h) * d.row8, v[g], h, p.N - d.n);
+            for (int h = 0; h < 2; ++h) {
+                const int row = (lane >> 2) + 8 * h;
+                store_row<true, true>(d.out + d.turn * 2048 + g * 1024 + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), v[g], h, 8);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (d.rows >> (2 * g + h) & 1) store_row<BF16, WHOLE>(d.y + (2 * g + h) * d.row8, v[g], h, p.N - d.n);
+        }
+    }
+    if constexpr (TMA) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (d.block_m + 16 * g < p.M) tma_store_2d(d.map, d.out + d.turn * 2048 + g * 1024, d.block_n, d.block_m + 16 * g);
+            bulk_commit();
+        }
     }
 }
 
@@ -378,15 +410,31 @@ __device__ __forceinline__ void join_parts(const Int8Params& p, const float* par
     }
 }
 
-// The columns of a warp, `whole` of its blocks of 32 in wide accesses.
-template <int ACT, bool BF16, int G>
-__device__ __forceinline__ void drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
+// The columns of a warp: `whole` of its blocks of 32 read scales in wide accesses (and, FP32, store
+// so); BF16 rows that start on 16 bytes go through the TMA.
+template <int ACT, bool BF16, bool TMA, int G>
+__device__ __forceinline__ int drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
     constexpr int es = BF16 ? 2 : 4;
+    const auto next = [&] {
+        d.at += 32;
+        d.n += 32;
+        d.y += 32 * es;
+        d.block_n += 32;
+        d.turn ^= 1;
+    };
     int i = 0;
 #pragma unroll 1
-    for (; i < whole; ++i, d.at += 32, d.n += 32, d.y += 32 * es) drain_block<ACT, BF16, true, G>(p, d);
+    for (; i < whole; ++i, next()) drain_block<ACT, BF16, true, TMA, G>(p, d);
 #pragma unroll 1
-    for (; i < blocks; ++i, d.at += 32, d.n += 32, d.y += 32 * es) drain_block<ACT, BF16, false, G>(p, d);
+    for (; i < blocks; ++i, next()) drain_block<ACT, BF16, false, TMA, G>(p, d);
+    return d.turn;
+}
+
+template <bool BF16, bool TMA, int G>
+__device__ __forceinline__ int drain_act(const Int8Params& p, const Drain& d, int blocks, int whole) {
+    if (p.act == CONV_ACT_RELU) return drain_columns<CONV_ACT_RELU, BF16, TMA, G>(p, d, blocks, whole);
+    if (p.act == CONV_ACT_SILU) return drain_columns<CONV_ACT_SILU, BF16, TMA, G>(p, d, blocks, whole);
+    return drain_columns<CONV_ACT_NONE, BF16, TMA, G>(p, d, blocks, whole);
 }
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as idesc_bf16_f32 with FP16 operands (type 0)
@@ -396,7 +444,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as ides
 template <bool PAIR, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     int8_gemm_kernel(const Int8Params p, const __grid_constant__ CUtensorMap map_x,
-                     const __grid_constant__ CUtensorMap map_w) {
+                     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_y) {
     using S = Shape<PAIR, BN>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_addr(smem) & 1023u) {  // the swizzle's atoms; uniform, so no CTA waits for another
@@ -405,7 +453,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     Bars b;
     uint8_t* raw = smem + S::kStages * S::kStage;
-    b.rfull = reinterpret_cast<uint64_t*>(raw + S::kRawSlots * S::kRaw);
+    uint8_t* outputs = raw + S::kRawSlots * S::kRaw;
+    b.rfull = reinterpret_cast<uint64_t*>(outputs + 2 * kEpilogueWarps * S::kOut);
     b.rempty = b.rfull + S::kRawSlots;
     b.full = b.rempty + S::kRawSlots;
     b.empty = b.full + S::kStages;
@@ -514,7 +563,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.rempty[rs]);
                 if (!publish(item)) break;
-                if ((rs += kGroups) >= S::kRawSlots) {  // more slots than groups: one wrap a turn at most
+                if ((rs += kGroups) >= S::kRawSlots) {  // at least as many slots as groups: one wrap a turn at most
                     rs -= S::kRawSlots;
                     rph ^= 1u;
                 }
@@ -528,7 +577,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int es = p.out_bf16 ? 2 : 4;
         const long long row_bytes = static_cast<long long>(p.N) * es;
         const bool wide = row_bytes % 16 == 0;  // y itself starts on 16 bytes
-        int local = 0;
+        int local = 0, turn = 0;
         // A warp drains half of the columns of its quarter's 32 rows; of a tile of 32 columns, 16 rows.
         constexpr int kCols = BN >= 64 ? BN / 2 : BN;
         const int col0 = BN >= 64 ? half * kCols : 0;
@@ -544,6 +593,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             d.n = first + (lane & 3) * 8;
             d.y = static_cast<uint8_t*>(p.y) + row0 * row_bytes + static_cast<long long>(d.n) * es;
             d.row8 = 8 * row_bytes;
+            d.map = &map_y;
+            d.out = outputs + (warp - kConverterWarps) * 2 * S::kOut;
+            d.turn = turn;
+            d.block_n = first;
+            d.block_m = static_cast<int>(row0) - (lane >> 2);
             d.rows = 0;
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i) {
@@ -562,14 +616,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 float* part = reinterpret_cast<float*>(smem) + static_cast<size_t>(lane0 + (lane >> 2)) * S::kPartRow + (lane & 3) * 8;
                 for (int c = col0; c < col0 + kCols; c += 32)
                     leave_block<G>(d.at + (c - col0), part + c, S::kPartRow);
+            } else if (p.out_bf16 && wide) {
+                turn = drain_act<true, true, G>(p, d, blocks, whole);
             } else if (p.out_bf16) {
-                if (p.act == CONV_ACT_RELU) drain_columns<CONV_ACT_RELU, true, G>(p, d, blocks, whole);
-                else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, true, G>(p, d, blocks, whole);
-                else drain_columns<CONV_ACT_NONE, true, G>(p, d, blocks, whole);
+                drain_act<true, false, G>(p, d, blocks, 0);
             } else {
-                if (p.act == CONV_ACT_RELU) drain_columns<CONV_ACT_RELU, false, G>(p, d, blocks, whole);
-                else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, false, G>(p, d, blocks, whole);
-                else drain_columns<CONV_ACT_NONE, false, G>(p, d, blocks, whole);
+                drain_act<false, false, G>(p, d, blocks, whole);
             }
             tc_fence_before();
             __syncwarp();
@@ -578,6 +630,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 else mbar_arrive(&b.tempty[buf]);
             }
         }
+        if (lane == 0) bulk_wait_all();  // none in flight when the CTA leaves
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ raw ring
         Walk w = walk_from<PAIR, BN>(tiles, unit0);
@@ -715,10 +768,20 @@ cudaError_t launch_variant(const Int8Params& p, int num_sms, bool after_layout, 
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    CUtensorMap map_x, map_w;
+    CUtensorMap map_x, map_w, map_y;
+    if (p.out_bf16 && p.N % 8 == 0) {  // rows of y on 16 bytes
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.N) * 2};
+        const cuuint32_t box[2] = {32, 16};
+        if (!tensor_map_encoder_ready() || encode_tiled(&map_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, dims, strides, box,
+                                                        CU_TENSOR_MAP_SWIZZLE_64B) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    } else {
+        map_y = CUtensorMap();
+    }
     if (!encode_rows(&map_x, p.x, p.M, p.K, p.x_pitch, 128) || !encode_rows(&map_w, p.w, p.N, p.K, p.w_pitch, S::kRowsB))
         return cudaErrorInvalidValue;
-    return cudaLaunchKernelEx(&cfg, fn, p, map_x, map_w);
+    return cudaLaunchKernelEx(&cfg, fn, p, map_x, map_w, map_y);
 }
 
 // Rows of K bytes to rows `pitch` apart (pitch a multiple of 16, at least K), 16 bytes a thread; the

@@ -64,7 +64,7 @@ __device__ __forceinline__ void few_amax(const Int8Params& p, const T* x, uint32
                 for (int j = 0; j < V / 2; ++j) a = magnitude(a, f[j]);
             }
         } else {
-            for (int i = seg * 32 + lane; i < p.K; i += 32 * kSegs) a = max_nan(a, fabsf(few_load(row, i)));
+            for (int i = seg * 32 + lane; i < p.K; i += 32 * kSegs) a = max_magnitude(a, few_load(row, i));
         }
     }
     const uint32_t bits = warp_max(magnitude_bits(a));
@@ -100,12 +100,12 @@ __device__ __forceinline__ void few_stage(const Int8Params& p, const T* x, int k
                     if (i >= len / V) break;
                     f2 f[V / 2];
                     Io::unpack(__ldg(reinterpret_cast<const uint4*>(row) + i), f);
-                    quantise_store<V>(reinterpret_cast<int8_t*>(dst) + i * V, f, rs[m]);
+                    quantise_store<V>(reinterpret_cast<int8_t*>(dst) + i * V, f, row_factor(rs[m].inv));
                 }
                 if (threadIdx.x < 16 && (len & 15) > 0 && threadIdx.x >= (len & 15)) dst[(len & ~15) + threadIdx.x] = 0;
             } else {
                 for (int i = threadIdx.x; i < ((len + 15) & ~15); i += kFewThreads)
-                    dst[i] = i < len ? static_cast<uint8_t>(quantise1(few_load(row, i), rs[m])) : 0;
+                    dst[i] = i < len ? static_cast<uint8_t>(quantise1(few_load(row, i), row_factor(rs[m].inv))) : 0;
             }
         }
     }
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         if constexpr (sizeof(T) == 1) {
-            rs[m] = {m < p.M ? __ldg(p.x_scale + m) : 0.0f, 0.0f, 0u};
+            rs[m] = {m < p.M ? __ldg(p.x_scale + m) : 0.0f, 0.0f};
         } else {
             uint32_t a = 0;
 #pragma unroll

@@ -162,15 +162,19 @@ __device__ __forceinline__ f2 activate_grad2(f2 z, f2 up) {
 // A row's largest magnitude travels as the bits of |x|: as unsigned integers they order as the
 // values do, Inf above every number and NaN above Inf, so one maximum finds both the scale and
 // a row that is not finite.
+__device__ __forceinline__ float max_magnitude(float a, float b) {  // |.| of the larger, its sign of no account
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float magnitude(float top, f2 v) {
-    return max_nan(top, max_nan(fabsf(f2_lo(v)), fabsf(f2_hi(v))));
+    return max_magnitude(max_magnitude(top, f2_lo(v)), f2_hi(v));
 }
 __device__ __forceinline__ uint32_t magnitude_bits(float top) { return __float_as_uint(top) & 0x7fffffffu; }
 
 struct RowScale {
-    float scale;    // what one step of q stands for
-    float inv;      // q = rint(x * inv)
-    uint32_t keep;  // all ones, or 0 where every q of the row is 0
+    float scale;  // what one step of q stands for
+    float inv;    // q = rint(x * inv); 0 where every q of the row is 0
 };
 
 // scale = amax / 127, inv = 127 / amax, both rounded once.  Rows below 2^-100 count as zero
@@ -178,31 +182,35 @@ struct RowScale {
 // that every product of it is NaN.
 __device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
     const float amax = __uint_as_float(amax_bits);
-    if (amax_bits >= 0x7f800000u) return {__uint_as_float(0x7fc00000u), 0.0f, 0u};
-    if (amax < 7.888609052e-31f) return {0.0f, 0.0f, 0u};  // 2^-100
-    return {__fdiv_rn(amax, 127.0f), __fdiv_rn(127.0f, amax), ~0u};
+    if (amax_bits >= 0x7f800000u) return {__uint_as_float(0x7fc00000u), 0.0f};
+    if (amax < 7.888609052e-31f) return {0.0f, 0.0f};  // 2^-100
+    return {__fdiv_rn(amax, 127.0f), __fdiv_rn(127.0f, amax)};
 }
 
-// Scales of R rows whose magnitudes every lane of a segment holds: lane r of it works out row r's (the
-// two divisions once for all rows) and hands it round.  lane: within the segment, of `width` lanes
-// (a power of two, R at least).
+struct RowFactor {
+    float inv;
+    uint32_t keep;  // all ones, or 0 where every q of the row is 0 (its values may be NaN)
+};
+
+__device__ __forceinline__ RowFactor row_factor(float inv) { return {inv, inv != 0.0f ? ~0u : 0u}; }
+
+// Factors of R rows whose magnitudes every lane of a segment holds: lane r of it works out row r's
+// (the two divisions once for all rows) and hands the factor round; it returns its own row's
+// scale.  lane: within the segment, of `width` lanes (a power of two, R at least).
 template <int R>
-__device__ __forceinline__ void row_scales(const uint32_t (&top)[R], int lane, int width, RowScale (&rs)[R]) {
+__device__ __forceinline__ float row_factors(const uint32_t (&top)[R], int lane, int width, RowFactor (&f)[R]) {
     uint32_t mine = top[0];
 #pragma unroll
     for (int r = 1; r < R; ++r) mine = lane == r ? top[r] : mine;
     const RowScale own = row_scale(mine);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rs[r].scale = __shfl_sync(0xffffffffu, own.scale, r, width);
-        rs[r].inv = __shfl_sync(0xffffffffu, own.inv, r, width);
-        rs[r].keep = __shfl_sync(0xffffffffu, own.keep, r, width);
-    }
+    for (int r = 0; r < R; ++r) f[r] = row_factor(__shfl_sync(0xffffffffu, own.inv, r, width));
+    return own.scale;
 }
 
 // Four values to four bytes, the first in the low one.  |x * inv| <= 127 up to one rounding; adding
 // 1.5 * 2^23 rounds it to an integer (ties to even), whose low byte is then the sum's.
-__device__ __forceinline__ uint32_t quantise4(f2 a, f2 b, const RowScale& r) {
+__device__ __forceinline__ uint32_t quantise4(f2 a, f2 b, const RowFactor& r) {
     const f2 inv = f2_dup(r.inv), magic = f2_dup(12582912.0f);
     a = f2_add_rounded(f2_mul(a, inv), magic);
     b = f2_add_rounded(f2_mul(b, inv), magic);
@@ -211,13 +219,13 @@ __device__ __forceinline__ uint32_t quantise4(f2 a, f2 b, const RowScale& r) {
     return __byte_perm(lo, hi, 0x5410) & r.keep;
 }
 
-__device__ __forceinline__ int8_t quantise1(float x, const RowScale& r) {
+__device__ __forceinline__ int8_t quantise1(float x, const RowFactor& r) {
     return static_cast<int8_t>(__float2int_rn(__fmul_rn(x, r.inv)) & r.keep);
 }
 
 // A vector's 8-bit values to q.
 template <int VEC>
-__device__ __forceinline__ void quantise_store(int8_t* q, const f2 (&v)[(VEC + 1) / 2], const RowScale& r) {
+__device__ __forceinline__ void quantise_store(int8_t* q, const f2 (&v)[(VEC + 1) / 2], const RowFactor& r) {
     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = make_uint2(quantise4(v[0], v[1], r), quantise4(v[2], v[3], r));
     else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(q) = quantise4(v[0], v[1], r);
     else *q = quantise1(f2_lo(v[0]), r);

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* x
         for (int v = lane; v < vecs; v += 32) {
             f2 f[H];
             Io::unpack(src[v], f);
-            quantise_store<VEC>(dst + v * VEC, f, rs);
+            quantise_store<VEC>(dst + v * VEC, f, row_factor(rs.inv));
         }
     }
 }
@@ -82,19 +82,19 @@ __global__ void __launch_bounds__(kQuantThreads, P >= 16 ? 2 : (P >= 8 ? 3 : 4))
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) top[r] = warp_max(top[r]);
-        RowScale rs[R];
-        row_scales<R>(top, lane, 32, rs);
+        RowFactor rf[R];
+        const float own = row_factors<R>(top, lane, 32, rf);
+        if (lane < R && row0 + lane < M) scale[row0 + lane] = own;
         int8_t* dst = q + row0 * pitch + lane * VEC;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row0 + r >= M) break;
-            if (lane == 0) scale[row0 + r] = rs[r].scale;
 #pragma unroll
             for (int h = 0; h < P; ++h)
                 if (lane + 32 * h < vecs) {
                     f2 f[H];
                     Io::unpack(raw[r][h], f);
-                    quantise_store<VEC>(dst + r * pitch + 32 * h * VEC, f, rs[r]);
+                    quantise_store<VEC>(dst + r * pitch + 32 * h * VEC, f, rf[r]);
                 }
         }
     }
