@@ -14,11 +14,13 @@
 //   packed subtractions for four values.
 //
 // Warp roles (832 threads, one CTA per SM, persistent over tiles):
-//   warps 0..15   converters, four groups that take turns by stage, so one loads, converts,
+//   warps 0..7    converters, four groups that take turns by stage, so one loads, converts,
 //                 publishes or waits while the others do: 8-bit rows from the raw ring to FP16
 //                 values in the 128-byte-swizzle operand tiles of a stage
-//   warps 16..23  epilogue: two warps per 32-row quarter of tensor memory, half of the columns
-//                 each: scales, bias, activation, rounding, stores from registers
+//   warps 8..23   epilogue: four warps per 32-row quarter of tensor memory, a quarter of the
+//                 columns each: scales, bias, activation, rounding, output.  (Eight warps took
+//                 ~7,000 clocks a 256 x 256 tile, which at K = 256 is 1.6 times its MMAs; the
+//                 converters had warps to spare.)
 //   warp 24       tensor memory; one lane issues tcgen05.mma and commits
 //   warp 25       one lane fills the raw ring by TMA: K = 64 of both operands, 8-bit, per slot
 // Rows that do not start on 16 bytes (K % 16) are beyond the TMA: a kernel of its own copies
@@ -53,9 +55,9 @@ namespace convgb {
 namespace {
 
 constexpr int kGroups = 4;       // converter groups
-constexpr int kGroupWarps = 4;
+constexpr int kGroupWarps = 2;
 constexpr int kConverterWarps = kGroups * kGroupWarps;
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 16;
 constexpr int kMmaWarp = kConverterWarps + kEpilogueWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
 constexpr int kGemmThreads = 32 * (kLoadWarp + 1);
@@ -70,11 +72,11 @@ struct Shape {
     static constexpr int kStages = kGroups;              // one for each converter group
     static constexpr int kRaw = (128 + kRowsB) * kStepK;  // one slot of the raw ring
     static constexpr int kRawSlots = kRowsB >= 128 ? 4 : 8;  // in 227 KB beside the stages and the outputs
-    static constexpr int kOut = 2048;                    // an epilogue warp's block of BF16 outputs, two of them
+    static constexpr int kOut = 2048;                    // an epilogue warp's block of BF16 outputs
     static constexpr int kPartRow = BN + 8;              // floats of a row of partial sums (K split over a cluster)
-    static constexpr int kItems = (128 + kRowsB) / 32;   // 16-byte items a converter thread moves per stage
+    static constexpr int kItemsB = kRowsB / 16;          // 16-byte items of w a converter thread moves per stage (of x: 8)
     static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + 2 * kEpilogueWarps * kOut + 256;
+    static constexpr int kSmem = kStages * kStage + kRawSlots * kRaw + kEpilogueWarps * kOut + 256;
 };
 
 struct Bars {
@@ -173,17 +175,16 @@ __device__ __forceinline__ void advance(const Tiles& t, Walk& w, int steps) {
 // 8 j + 2 q + e.
 __device__ __forceinline__ int column_of(int n) { return (n & ~31) | ((n & 6) << 2) | ((n & 24) >> 2) | (n & 1); }
 
-template <bool PAIR, int BN>
-__device__ __forceinline__ void store_stage(const Int8Params& p, const Walk& w, int r0, int c,
-                                            const uint4 (&item)[Shape<PAIR, BN>::kItems], uint8_t* stage) {
-    using S = Shape<PAIR, BN>;
+// COUNT items of one operand (rows r0, r0 + 16, ...) to its FP16 tile.
+template <int COUNT, bool WEIGHTS>
+__device__ __forceinline__ void store_items(int rows_left, int r0, int c, const uint4 (&item)[COUNT], uint8_t* tile) {
 #pragma unroll
-    for (int i = 0; i < S::kItems; ++i) {
-        int row = r0 + 32 * (i < 4 ? i : i - 4);
-        if (i < 4 ? w.m0 + row >= p.M : w.n0 + row >= p.N) continue;
+    for (int i = 0; i < COUNT; ++i) {
+        int row = r0 + 16 * i;
+        if (row >= rows_left) continue;
         const uint2 a = to_half4(item[i].x), b = to_half4(item[i].y), d = to_half4(item[i].z), e = to_half4(item[i].w);
-        if (i >= 4) row = column_of(row);
-        uint8_t* dst = stage + (i < 4 ? 0 : S::kTileA) + row * kRowBytes;
+        if (WEIGHTS) row = column_of(row);
+        uint8_t* dst = tile + row * kRowBytes;
         const int sw = row & 7;  // eight lanes: four chunks of two rows, eight bank groups
         *reinterpret_cast<uint4*>(dst + (((2 * c) ^ sw) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
         *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ sw) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
@@ -292,10 +293,10 @@ struct Drain {
     uint8_t* y;      // its first row and column
     long long row8;  // bytes of 8 rows of y
     float xs[4];
-    // BF16 blocks through the TMA: the warp's two buffers, which one is next, and the block's place in y
+    // BF16 blocks through the TMA: the warp's buffer and the block's place in y
     const CUtensorMap* map;
     uint8_t* out;
-    int turn, block_n, block_m;
+    int block_n, block_m;
 };
 
 // G: 16-row groups of the quarter that this warp drains.
@@ -317,15 +318,15 @@ __device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d)
     for (int g = 0; g < G; ++g) {
         finish_block<ACT>(v[g], d.xs[2 * g], d.xs[2 * g + 1], ws, bias);
         if constexpr (TMA) {
-            if (g == 0) {  // the buffer's last store has read it
-                if ((threadIdx.x & 31) == 0) bulk_wait_read_le1();
+            if (g == 0) {  // the last block's store has read the buffer
+                if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
                 __syncwarp();
             }
             const int lane = threadIdx.x & 31;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = (lane >> 2) + 8 * h;
-                store_row<true, true>(d.out + d.turn * 2048 + g * 1024 + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), v[g], h, 8);
+                store_row<true, true>(d.out + g * 1024 + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), v[g], h, 8);
             }
         } else {
 #pragma unroll
@@ -339,7 +340,7 @@ __device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d)
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                if (d.block_m + 16 * g < p.M) tma_store_2d(d.map, d.out + d.turn * 2048 + g * 1024, d.block_n, d.block_m + 16 * g);
+                if (d.block_m + 16 * g < p.M) tma_store_2d(d.map, d.out + g * 1024, d.block_n, d.block_m + 16 * g);
             bulk_commit();
         }
     }
@@ -413,28 +414,26 @@ __device__ __forceinline__ void join_parts(const Int8Params& p, const float* par
 // The columns of a warp: `whole` of its blocks of 32 read scales in wide accesses (and, FP32, store
 // so); BF16 rows that start on 16 bytes go through the TMA.
 template <int ACT, bool BF16, bool TMA, int G>
-__device__ __forceinline__ int drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
+__device__ __forceinline__ void drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
     constexpr int es = BF16 ? 2 : 4;
     const auto next = [&] {
         d.at += 32;
         d.n += 32;
         d.y += 32 * es;
         d.block_n += 32;
-        d.turn ^= 1;
     };
     int i = 0;
 #pragma unroll 1
     for (; i < whole; ++i, next()) drain_block<ACT, BF16, true, TMA, G>(p, d);
 #pragma unroll 1
     for (; i < blocks; ++i, next()) drain_block<ACT, BF16, false, TMA, G>(p, d);
-    return d.turn;
 }
 
 template <bool BF16, bool TMA, int G>
-__device__ __forceinline__ int drain_act(const Int8Params& p, const Drain& d, int blocks, int whole) {
-    if (p.act == CONV_ACT_RELU) return drain_columns<CONV_ACT_RELU, BF16, TMA, G>(p, d, blocks, whole);
-    if (p.act == CONV_ACT_SILU) return drain_columns<CONV_ACT_SILU, BF16, TMA, G>(p, d, blocks, whole);
-    return drain_columns<CONV_ACT_NONE, BF16, TMA, G>(p, d, blocks, whole);
+__device__ __forceinline__ void drain_act(const Int8Params& p, const Drain& d, int blocks, int whole) {
+    if (p.act == CONV_ACT_RELU) drain_columns<CONV_ACT_RELU, BF16, TMA, G>(p, d, blocks, whole);
+    else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, BF16, TMA, G>(p, d, blocks, whole);
+    else drain_columns<CONV_ACT_NONE, BF16, TMA, G>(p, d, blocks, whole);
 }
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as idesc_bf16_f32 with FP16 operands (type 0)
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     Bars b;
     uint8_t* raw = smem + S::kStages * S::kStage;
     uint8_t* outputs = raw + S::kRawSlots * S::kRaw;
-    b.rfull = reinterpret_cast<uint64_t*>(outputs + 2 * kEpilogueWarps * S::kOut);
+    b.rfull = reinterpret_cast<uint64_t*>(outputs + kEpilogueWarps * S::kOut);
     b.rempty = b.rfull + S::kRawSlots;
     b.full = b.rempty + S::kRawSlots;
     b.empty = b.full + S::kStages;
@@ -534,21 +533,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (w.u < units) {
             uint32_t ph = 0;
             uint8_t* stage = smem + group * S::kStage;
-            const auto publish = [&](uint4(&item)[S::kItems]) {
-                if (!warp_wait(&b.empty[group], ph ^ 1u, abort)) {
-                    record_status(p.status, kStatusTimeoutTransform, abort);
-                    return false;
-                }
-                store_stage<PAIR, BN>(p, w, r0, c, item, stage);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) arrive_leader(&b.full[group]);
-                    else mbar_arrive(&b.full[group]);
-                }
-                ph ^= 1u;
-                return true;
-            };
             int rs = group;
             uint32_t rph = 0;
             while (w.u < units) {
@@ -556,13 +540,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     record_status(p.status, kStatusTimeoutTransform, abort);
                     break;
                 }
-                uint4 item[S::kItems];
                 const uint4* src = reinterpret_cast<const uint4*>(raw + rs * S::kRaw) + t;
+                uint4 x[8], wt[S::kItemsB];
 #pragma unroll
-                for (int i = 0; i < S::kItems; ++i) item[i] = src[i * 128];  // rows r0 + 32 i of x, then of w
+                for (int i = 0; i < 8; ++i) x[i] = src[i * 64];  // rows r0 + 16 i of x, then of w
+                if (!warp_wait(&b.empty[group], ph ^ 1u, abort)) {
+                    record_status(p.status, kStatusTimeoutTransform, abort);
+                    break;
+                }
+                store_items<8, false>(p.M - w.m0, r0, c, x, stage);
+#pragma unroll
+                for (int i = 0; i < S::kItemsB; ++i) wt[i] = src[(8 + i) * 64];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.rempty[rs]);
-                if (!publish(item)) break;
+                store_items<S::kItemsB, true>(p.N - w.n0, r0, c, wt, stage + S::kTileA);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) arrive_leader(&b.full[group]);
+                    else mbar_arrive(&b.full[group]);
+                }
+                ph ^= 1u;
                 if ((rs += kGroups) >= S::kRawSlots) {  // at least as many slots as groups: one wrap a turn at most
                     rs -= S::kRawSlots;
                     rph ^= 1u;
@@ -573,29 +571,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3;
-        const int half = (warp - kConverterWarps) >> 2;
+        const int part = (warp - kConverterWarps) >> 2;
         const int es = p.out_bf16 ? 2 : 4;
         const long long row_bytes = static_cast<long long>(p.N) * es;
         const bool wide = row_bytes % 16 == 0;  // y itself starts on 16 bytes
-        int local = 0, turn = 0;
-        // A warp drains half of the columns of its quarter's 32 rows; of a tile of 32 columns, 16 rows.
-        constexpr int kCols = BN >= 64 ? BN / 2 : BN;
-        const int col0 = BN >= 64 ? half * kCols : 0;
-        constexpr int G = BN >= 64 ? 2 : 1;
-        const int lane0 = quarter * 32 + (BN >= 64 ? 0 : 16 * half);  // its first row of the tile
+        int local = 0;
+        // A warp drains a quarter of the columns of 32 rows; of 64 columns half, of 32 all (two of the four
+        // warps), 16 rows.
+        constexpr int kCols = BN >= 128 ? BN / 4 : 32;
+        const int col0 = BN >= 128 ? part * kCols : (BN == 64 ? (part & 1) * 32 : 0);
+        constexpr int G = BN >= 128 ? 2 : 1;
+        const int lane0 = quarter * 32 + (BN >= 128 ? 0 : 16 * (BN == 64 ? part >> 1 : part & 1));  // its first row of the tile
+        const bool idle = BN == 32 && part >= 2;
         for (Walk w = walk_from<PAIR, BN>(tiles, unit0); w.u < units; next_unit(tiles, w), ++local) {
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
             const long long row0 = static_cast<long long>(w.mu) * 128 * kCtas + rank * 128 + lane0 + (lane >> 2);
-            const int first = w.nt * BN + col0, left = p.N - first;
+            const int first = w.nt * BN + col0, left = idle ? 0 : p.N - first;
             Drain d;
             d.at = tmem + (static_cast<uint32_t>(lane0) << 16) + buf * BN + col0;
             d.n = first + (lane & 3) * 8;
             d.y = static_cast<uint8_t*>(p.y) + row0 * row_bytes + static_cast<long long>(d.n) * es;
             d.row8 = 8 * row_bytes;
             d.map = &map_y;
-            d.out = outputs + (warp - kConverterWarps) * 2 * S::kOut;
-            d.turn = turn;
+            d.out = outputs + (warp - kConverterWarps) * S::kOut;
             d.block_n = first;
             d.block_m = static_cast<int>(row0) - (lane >> 2);
             d.rows = 0;
@@ -612,12 +611,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 break;
             }
             tc_fence_after();
-            if (splits > 1) {
+            if (splits > 1 && !idle) {
                 float* part = reinterpret_cast<float*>(smem) + static_cast<size_t>(lane0 + (lane >> 2)) * S::kPartRow + (lane & 3) * 8;
                 for (int c = col0; c < col0 + kCols; c += 32)
                     leave_block<G>(d.at + (c - col0), part + c, S::kPartRow);
             } else if (p.out_bf16 && wide) {
-                turn = drain_act<true, true, G>(p, d, blocks, whole);
+                drain_act<true, true, G>(p, d, blocks, whole);
             } else if (p.out_bf16) {
                 drain_act<true, false, G>(p, d, blocks, 0);
             } else {
