@@ -1297,9 +1297,12 @@ template <typename F>
 void with_types(const NormParams& p, F&& f) {
     if (p.bf16) {
         if (p.vec == 8) f(__nv_bfloat16(), std::integral_constant<int, 8>());
+        else if (p.vec == 4) f(__nv_bfloat16(), std::integral_constant<int, 4>());
+        else if (p.vec == 2) f(__nv_bfloat16(), std::integral_constant<int, 2>());
         else f(__nv_bfloat16(), std::integral_constant<int, 1>());
     } else {
         if (p.vec == 4) f(float(), std::integral_constant<int, 4>());
+        else if (p.vec == 2) f(float(), std::integral_constant<int, 2>());
         else f(float(), std::integral_constant<int, 1>());
     }
 }
@@ -1386,7 +1389,7 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
     p.chunk = 0;
-    if (p.vec == 1 || static_cast<long long>(p.P) * (p.C / p.vec) >= (1LL << 31)) return;
+    if (p.vec * es != 16 || static_cast<long long>(p.P) * (p.C / p.vec) >= (1LL << 31)) return;
     int chunk = 0;
     if (mode == kNormInt8) {
         chunk = p.C;
@@ -1434,7 +1437,7 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
 // Two passes: pixel ranges that fill the SMs once, four CTAs to each (three backward or to 8 bits).
 void norm_pick_two_pass(NormParams& p, int mode, int num_sms) {
     const int vecs = p.C / p.vec;
-    if (p.vec == 1 || vecs > kNormThreads || static_cast<long long>(p.P) * vecs >= (1LL << 31)) return;
+    if (p.vec * (p.bf16 ? 2 : 4) != 16 || vecs > kNormThreads || static_cast<long long>(p.P) * vecs >= (1LL << 31)) return;
     const int rows = kNormThreads / vecs;
     long long splits = static_cast<long long>(num_sms) * (mode == kNormForward ? 4 : 3) / p.N;
     const long long most = p.P / (2LL * rows);  // two pixels a thread at least

@@ -111,8 +111,8 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
     p.eps = eps;
     p.act = act;
     p.bf16 = dtype == CONV_BF16;
-    const int wide = p.bf16 ? 8 : 4;
-    p.vec = C % wide == 0 ? wide : 1;
+    p.vec = p.bf16 ? 8 : 4;
+    while (C % p.vec != 0) p.vec /= 2;
     // Pixel ranges: about eight CTAs an SM, at least four pixels a thread.
     const int vecs = C / p.vec, cv = vecs < kNormThreads ? vecs : kNormThreads;
     const long long blocks = static_cast<long long>(N) * ((vecs + cv - 1) / cv);

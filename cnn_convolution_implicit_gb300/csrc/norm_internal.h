@@ -18,7 +18,7 @@ struct NormParams {
     float eps;
     int act;      // conv_act
     int bf16;     // element type of x, y, dy, dx (else FP32)
-    int vec;      // elements per access: 16 bytes where every pixel starts on 16 bytes, else 1
+    int vec;      // elements per access: the most, up to 16 bytes, that divide the channels
     int splits;   // pixel ranges per image, or the CTAs of a resident cluster
     int two_pass; // two passes over pixel ranges (else, without a chunk, by channel)
     int joined;   // two passes: a kernel between them joins the ranges

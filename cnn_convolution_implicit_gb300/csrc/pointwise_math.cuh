@@ -56,8 +56,8 @@ __device__ __forceinline__ f2 f2_add_rounded(f2 a, f2 b) {
     return f2_make(__fadd_rn(f2_lo(a), f2_lo(b)), __fadd_rn(f2_hi(a), f2_hi(b)));
 }
 
-// VEC consecutive elements as pairs of FP32.  VEC = 16 bytes of T (one 128-bit access) or 1 (one
-// pair, its second lane 0).
+// VEC consecutive elements as pairs of FP32, one access of 2 to 16 bytes; VEC = 1: one pair, its
+// second lane 0.
 template <typename T, int VEC>
 struct VecIo;
 
@@ -92,6 +92,36 @@ struct VecIo<float, 4> {
     static __device__ __forceinline__ uint4 pack(const f2 (&v)[2]) {
         return make_uint4(__float_as_uint(f2_lo(v[0])), __float_as_uint(f2_hi(v[0])), __float_as_uint(f2_lo(v[1])),
                           __float_as_uint(f2_hi(v[1])));
+    }
+};
+
+template <>
+struct VecIo<__nv_bfloat16, 4> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(const uint2& r, f2 (&v)[2]) {
+        v[0] = VecIo<__nv_bfloat16, 8>::pair(r.x);
+        v[1] = VecIo<__nv_bfloat16, 8>::pair(r.y);
+    }
+    static __device__ __forceinline__ uint2 pack(const f2 (&v)[2]) {
+        return make_uint2(VecIo<__nv_bfloat16, 8>::round(v[0]), VecIo<__nv_bfloat16, 8>::round(v[1]));
+    }
+};
+
+template <>
+struct VecIo<__nv_bfloat16, 2> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ void unpack(const uint32_t& r, f2 (&v)[1]) { v[0] = VecIo<__nv_bfloat16, 8>::pair(r); }
+    static __device__ __forceinline__ uint32_t pack(const f2 (&v)[1]) { return VecIo<__nv_bfloat16, 8>::round(v[0]); }
+};
+
+template <>
+struct VecIo<float, 2> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(const uint2& r, f2 (&v)[1]) {
+        v[0] = f2_make(__uint_as_float(r.x), __uint_as_float(r.y));
+    }
+    static __device__ __forceinline__ uint2 pack(const f2 (&v)[1]) {
+        return make_uint2(__float_as_uint(f2_lo(v[0])), __float_as_uint(f2_hi(v[0])));
     }
 };
 
@@ -228,6 +258,7 @@ template <int VEC>
 __device__ __forceinline__ void quantise_store(int8_t* q, const f2 (&v)[(VEC + 1) / 2], const RowFactor& r) {
     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = make_uint2(quantise4(v[0], v[1], r), quantise4(v[2], v[3], r));
     else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(q) = quantise4(v[0], v[1], r);
+    else if constexpr (VEC == 2) *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(quantise4(v[0], v[0], r));
     else *q = quantise1(f2_lo(v[0]), r);
 }
 

@@ -63,6 +63,38 @@ def test_forward(shape, act, dtype):
     ref.check(_np(stats[1]), rstd, 1e-5 * rstd, False, "rstd")
 
 
+# Maps that no cluster holds: two passes over pixel ranges, joined in the second (twelve images) or
+# by a kernel between them (one image, hundreds of ranges); 40 vectors a pixel: 8-bit rows find
+# their magnitude through shared memory.
+LARGE = [(1, 200, 210, 64, 8), (12, 190, 200, 32, 4), (2, 250, 130, 320, 32)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", LARGE)
+def test_maps_beyond_a_cluster(shape, dtype):
+    import cnn_convolution_implicit_gb300 as cg
+    N, H, W, C, G = shape
+    x, gamma, beta = _make(N, H, W, C, dtype, 13, offset=3.0)
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(2)).to(DT[dtype])
+    xd, gd, bd = x.cuda(), gamma.cuda(), beta.cuda()
+    stats = torch.empty(2, N, G, device="cuda")
+    y = cg.group_norm(xd, G, gd, bd, act="silu", stats=stats)
+    want, tol = ref.norm_forward(_flat(x), G, _np(gamma), _np(beta), 1e-5, "silu")
+    ref.check(_flat(y), want, tol, dtype == "bf16", "y")
+    mean, rstd = ref.norm_stats(_flat(x), G, 1e-5)
+    ref.check(_np(stats[0]), mean, 1e-6 * (1.0 + np.abs(mean)), False, "mean")
+    ref.check(_np(stats[1]), rstd, 1e-5 * rstd, False, "rstd")
+    q, scale = cg.group_norm_int8(xd, G, gd, bd, act="silu")
+    flat, s = want.reshape(-1, C), _np(scale)
+    err = np.abs(_np(q).reshape(-1, C) * s[:, None] - flat)
+    assert np.all(err <= 0.5 * s[:, None] * (1 + 128 * ref.U32 * 2) + tol.reshape(-1, C))
+    got = cg.group_norm_backward(dy.cuda(), xd, stats, G, gd, bd, act="silu")
+    want, tol = ref.norm_backward(_flat(dy), _flat(x), stats.cpu().numpy(), G, _np(gamma), _np(beta), "silu")
+    ref.check(_flat(got[0]), want[0], tol[0], dtype == "bf16", "dx")
+    ref.check(_np(got[1]), want[1], tol[1], False, "dgamma")
+    ref.check(_np(got[2]), want[2], tol[2], False, "dbeta")
+
+
 @pytest.mark.parametrize("gamma_on,beta_on", [(True, False), (False, True), (False, False)])
 def test_forward_without_affine(gamma_on, beta_on):
     import cnn_convolution_implicit_gb300 as cg

@@ -44,6 +44,21 @@ def test_product(size, out):
     assert cg.device_status() == 0
 
 
+# Every tile shape and split of K: pairs of SMs over several rounds, 128, 64 and 32 columns, two, four
+# and eight CTAs to a tile, a K that the split does not divide, and each with rows off 16 bytes.
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(5000, 1000, 528), (5000, 1001, 520), (9000, 512, 256), (16, 4096, 4096), (300, 2048, 1040),
+                                  (128, 100, 2000), (40, 33, 1999), (1000, 704, 304), (2000, 96, 3000), (20, 5000, 70)])
+def test_tile_shapes(size, out):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, xs, w, ws, bias = _inputs(M, N, K, M + N + 5 * K)
+    y = cg.int8_matmul(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), bias.cuda(), act="relu", out=out)
+    want, tol = ref.int8_product(x.numpy(), xs.numpy(), w.numpy(), ws.numpy(), bias.numpy(), "relu")
+    ref.check(_np(y), want, tol, out == "bf16", "y")
+    assert cg.device_status() == 0
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu"])
 @pytest.mark.parametrize("bias_on", [True, False])
 @pytest.mark.parametrize("size", [(1, 96, 160), (5, 96, 100), (140, 200, 130)])
