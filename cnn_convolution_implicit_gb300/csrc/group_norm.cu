@@ -37,6 +37,15 @@ namespace convgb {
 
 namespace {
 
+// Sum over segments of `width` lanes (a power of two), every lane of the warp calling it.
+__device__ __forceinline__ float segment_sum(float v, int width) {
+    for (int o = width >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The smallest power of two that is at least n, at most a warp.
+__device__ __forceinline__ int segment_width(int n) { return n >= 32 ? 32 : (n <= 1 ? 1 : 1 << (32 - __clz(n - 1))); }
+
 // A CTA's threads over [pixels][vectors of channels]: cv vectors side by side, as many pixels as fit.
 struct Lanes {
     int cv, rows;  // vectors side by side, pixel rows
@@ -55,9 +64,10 @@ __device__ __forceinline__ Lanes lanes_of(int vecs, int block) {
     return l;
 }
 
-__device__ __forceinline__ void split_range(int P, int splits, int s, int& p0, int& p1) {
-    p0 = static_cast<int>(static_cast<long long>(P) * s / splits);
-    p1 = static_cast<int>(static_cast<long long>(P) * (s + 1) / splits);
+// Pixels of range (or cluster CTA) k of an image: pix_base, one more in the first pix_more.
+__device__ __forceinline__ void pixel_range(const NormParams& p, int k, int& p0, int& p1) {
+    p0 = k * p.pix_base + min(k, p.pix_more);
+    p1 = p0 + p.pix_base + (k < p.pix_more);
 }
 
 // Sum over the CTA's pixel rows of one value per (row, channel of the block), the same
@@ -125,7 +135,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_moments_kernel(const NormPa
     const int vecs = p.C / VEC;
     const Lanes l = lanes_of(vecs, blockIdx.y);
     int p0, p1;
-    split_range(p.P, p.splits, s, p0, p1);
+    pixel_range(p, s, p0, p1);
     using Io = VecIo<T, VEC>;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + static_cast<long long>(n) * p.P * vecs + l.v;
     Moments<VEC> mo;
@@ -172,30 +182,34 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
     return s;
 }
 
+constexpr int kJoinThreads = 512;
+
+// Calls f(range, channel) for the ranges and channels of a group, spread over the CTA: a segment of
+// lanes to a range, no division per entry.
+template <typename F>
+__device__ __forceinline__ void for_ranges_and_channels(const NormParams& p, F&& f) {
+    const int wide = segment_width(p.cpg), lane = threadIdx.x & 31;
+    for (int sp = (threadIdx.x >> 5) * (32 / wide) + lane / wide; sp < p.splits; sp += kJoinThreads / wide)
+        for (int c = lane & (wide - 1); c < p.cpg; c += wide) f(sp, c);
+}
+
 // One CTA per (image, group): joins the ranges and channels of the group.
-__global__ void __launch_bounds__(128) norm_join_kernel(const NormParams p) {
-    __shared__ float scratch[4];
+__global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const NormParams p) {
+    __shared__ float scratch[kJoinThreads / 32];
     const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
-    const int entries = p.splits * p.cpg;
     const float2* part = p.part + static_cast<long long>(n) * p.splits * p.C + g * p.cpg;
     const float total = static_cast<float>(p.P) * static_cast<float>(p.cpg);
     float s = 0.0f;
-    for (int e = threadIdx.x; e < entries; e += blockDim.x) {
-        const int sp = e / p.cpg, c = e - sp * p.cpg;
-        int p0, p1;
-        split_range(p.P, p.splits, sp, p0, p1);
-        s = fmaf(static_cast<float>(p1 - p0), part[static_cast<long long>(sp) * p.C + c].x, s);
-    }
+    for_ranges_and_channels(p, [&](int sp, int c) {
+        s = fmaf(static_cast<float>(p.pix_base + (sp < p.pix_more)), part[static_cast<long long>(sp) * p.C + c].x, s);
+    });
     const float mean = block_sum(s, scratch) / total;
     float m2 = 0.0f;
-    for (int e = threadIdx.x; e < entries; e += blockDim.x) {
-        const int sp = e / p.cpg, c = e - sp * p.cpg;
-        int p0, p1;
-        split_range(p.P, p.splits, sp, p0, p1);
+    for_ranges_and_channels(p, [&](int sp, int c) {
         const float2 v = part[static_cast<long long>(sp) * p.C + c];
         const float d = v.x - mean;
-        m2 += v.y + static_cast<float>(p1 - p0) * d * d;
-    }
+        m2 += v.y + static_cast<float>(p.pix_base + (sp < p.pix_more)) * d * d;
+    });
     const float var = block_sum(m2, scratch) / total;
     if (threadIdx.x == 0) {
         p.mean[blockIdx.x] = mean;
@@ -330,7 +344,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(const NormPara
     const Lanes l = lanes_of(vecs, blockIdx.y);
     if (!l.on) return;
     int p0, p1;
-    split_range(p.P, p.splits, s, p0, p1);
+    pixel_range(p, s, p0, p1);
     using Io = VecIo<T, VEC>;
     const long long base = static_cast<long long>(n) * p.P * vecs + l.v;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
@@ -392,7 +406,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_sums_kernel(const Norm
     const int vecs = p.C / VEC;
     const Lanes l = lanes_of(vecs, blockIdx.y);
     int p0, p1;
-    split_range(p.P, p.splits, s, p0, p1);
+    pixel_range(p, s, p0, p1);
     using Io = VecIo<T, VEC>;
     const long long base = static_cast<long long>(n) * p.P * vecs + l.v;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
@@ -432,19 +446,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_sums_kernel(const Norm
 }
 
 // One CTA per (image, group): a and b.
-__global__ void __launch_bounds__(128) norm_grad_join_kernel(const NormParams p) {
-    __shared__ float scratch[4];
+__global__ void __launch_bounds__(kJoinThreads) norm_grad_join_kernel(const NormParams p) {
+    __shared__ float scratch[kJoinThreads / 32];
     const int n = blockIdx.x / p.G, g = blockIdx.x - n * p.G;
-    const int entries = p.splits * p.cpg;
     const float2* part = p.part + static_cast<long long>(n) * p.splits * p.C + g * p.cpg;
     float a = 0.0f, b = 0.0f;
-    for (int e = threadIdx.x; e < entries; e += blockDim.x) {
-        const int sp = e / p.cpg, c = e - sp * p.cpg;
+    for_ranges_and_channels(p, [&](int sp, int c) {
         const float2 v = part[static_cast<long long>(sp) * p.C + c];
-        const float gm = p.gamma ? p.gamma[g * p.cpg + c] : 1.0f;
+        const float gm = p.gamma ? __ldg(p.gamma + g * p.cpg + c) : 1.0f;
         a = fmaf(gm, v.x, a);
         b = fmaf(gm, v.y, b);
-    }
+    });
     const float total = static_cast<float>(p.P) * static_cast<float>(p.cpg);
     a = block_sum(a, scratch) / total;
     b = block_sum(b, scratch) / total;
@@ -484,7 +496,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_apply_kernel(const Nor
     const Lanes l = lanes_of(vecs, blockIdx.y);
     if (!l.on) return;
     int p0, p1;
-    split_range(p.P, p.splits, s, p0, p1);
+    pixel_range(p, s, p0, p1);
     using Io = VecIo<T, VEC>;
     const long long base = static_cast<long long>(n) * p.P * vecs + l.v;
     const auto* x = reinterpret_cast<const typename Io::Raw*>(p.x) + base;
@@ -528,27 +540,12 @@ __device__ __forceinline__ void res_push(float2* p, uint32_t rank, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Sum over segments of `width` lanes (a power of two), every lane of the warp calling it.
-__device__ __forceinline__ float segment_sum(float v, int width) {
-    for (int o = width >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// The smallest power of two that is at least n, at most a warp.
-__device__ __forceinline__ int segment_width(int n) { return n >= 32 ? 32 : (n <= 1 ? 1 : 1 << (32 - __clz(n - 1))); }
-
 // Lanes of a vector that share a group, always: the largest power of two that divides cpg, at most
 // a vector.  A thread's statistics are joined over them before they leave it.
 __host__ __device__ inline int res_lump(const NormParams& p) {
     int l = 1;
     while (l < p.vec && p.cpg % (2 * l) == 0) l *= 2;
     return l;
-}
-
-// Pixels of CTA k of a cluster: pix_base, one more in the first pix_more.
-__device__ __forceinline__ void res_range(const NormParams& p, int k, int& p0, int& p1) {
-    p0 = k * p.pix_base + min(k, p.pix_more);
-    p1 = p0 + p.pix_base + (k < p.pix_more);
 }
 
 // Rows of backward partials a CTA keeps: one a warp where neighbouring lanes hold several rows of
@@ -736,7 +733,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
     const int rows = kThreads / vpr;
     const int r = threadIdx.x / vpr, v = threadIdx.x - r * vpr;
     int p0, p1;
-    res_range(p, rank, p0, p1);
+    pixel_range(p, rank, p0, p1);
     const int mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;  // this thread's items
     const int step = rows * (p.C / VEC);     // in vectors; an image has fewer than 2^31 of them
     const long long base = ((static_cast<long long>(n) * p.P + p0 + r) * p.C + c0) / VEC + v;
@@ -974,7 +971,7 @@ struct TwoRange {
         rows = kNormThreads / vpr;
         r = threadIdx.x / vpr;
         v = threadIdx.x - r * vpr;
-        res_range(p, s, p0, p1);
+        pixel_range(p, s, p0, p1);
         mine = r < rows && p0 + r < p1 ? (p1 - p0 - r + rows - 1) / rows : 0;
         base = (static_cast<long long>(n) * p.P + p0 + r) * vpr + v;
         step = rows * vpr;
@@ -1535,7 +1532,7 @@ cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t s
     with_types(p, [&](auto t, auto vec) {
         norm_moments_kernel<decltype(t), vec.value><<<grid, kNormThreads, 0, stream>>>(p);
     });
-    norm_join_kernel<<<p.N * p.G, 128, 0, stream>>>(p);
+    norm_join_kernel<<<p.N * p.G, kJoinThreads, 0, stream>>>(p);
     with_types(p, [&](auto t, auto vec) {
         with_act(p.act, [&](auto act) {
             if (p.q != nullptr) {
@@ -1563,7 +1560,7 @@ cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t 
     with_types(p, [&](auto t, auto vec) {
         with_act(p.act, [&](auto act) {
             norm_grad_sums_kernel<decltype(t), vec.value, act.value><<<grid, kNormThreads, 0, stream>>>(p);
-            norm_grad_join_kernel<<<p.N * p.G, 128, 0, stream>>>(p);
+            norm_grad_join_kernel<<<p.N * p.G, kJoinThreads, 0, stream>>>(p);
             if (p.dgamma != nullptr) norm_grad_channels_kernel<<<(p.C + 31) / 32, 512, 0, stream>>>(p);
             norm_grad_apply_kernel<decltype(t), vec.value, act.value><<<grid, kNormThreads, 0, stream>>>(p);
         });

@@ -113,13 +113,15 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
     p.bf16 = dtype == CONV_BF16;
     p.vec = p.bf16 ? 8 : 4;
     while (C % p.vec != 0) p.vec /= 2;
-    // Pixel ranges: about eight CTAs an SM, at least four pixels a thread.
+    // By channel, where no other form fits: about eight CTAs an SM, at least four pixels a thread.
     const int vecs = C / p.vec, cv = vecs < kNormThreads ? vecs : kNormThreads;
     const long long blocks = static_cast<long long>(N) * ((vecs + cv - 1) / cv);
     const long long least = 4LL * (kNormThreads / cv);
     long long splits = (8LL * pl->num_sms + blocks - 1) / blocks;
     if (splits > P / least) splits = P / least;
     p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    p.pix_base = p.P / p.splits;
+    p.pix_more = p.P % p.splits;
     for (int mode = 0; mode < 3; ++mode) {
         NormParams& m = pl->np[mode];
         m = p;
