@@ -19,17 +19,28 @@
 // sum of squares) triples join as
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + n_i (mean_i - mean)^2.
 //
-// Three forms.
-//   Resident (small maps; FORM_RULE): each CTA copies its pixels of `chunk` channels into
-//   shared memory once (cp.async, each thread reads back only what it copied), pushes its
-//   groups' sums into the shared memory of its cluster, and after one cluster barrier
-//   writes the values from there.  One launch.
-//   Two passes (any other map whose pixels start on 16 bytes): one kernel leaves each pixel range's
-//   group sums, the next joins them in its prologue and writes the values, walking its range
-//   backwards and storing past the caches, so that what the first pass left in the 129 MB L2
-//   is read from there.  The second is launched early and waits for the first.
-//   By channel (odd channel counts, over 256 vectors a pixel): as two passes, the sums kept per
-//   channel and joined by a kernel of their own.
+// Bound by memory: x read and y written once (backward: x and dy read, dx written).  Three forms,
+// chosen per plan (norm_pick_resident, norm_pick_two_pass); times with cold caches, launch
+// included, against the bytes at the card's measured copy rate:
+//
+//   Resident: each CTA copies its pixels of `chunk` channels into shared memory once
+//   (cp.async, each thread reads back only what it copied), pushes its groups' sums into the
+//   shared memory of its cluster, and after one cluster barrier writes the values from
+//   there: every byte crosses the memory bus once, in one launch.  Two CTAs an SM, so one loads
+//   while the other stores; with 200 KB an SM in flight the rate is those bytes over a CTA's
+//   life (~11 us: 5.5 loading, 3 from the last load to the first store, 2.5 storing), and clusters
+//   of eight fill 288 of 304 places, of sixteen 224.
+//     1 x 8 x 8 x 256 BF16: 8 us; 64 x 56 x 56 x 256: 55 us (floor 30); 32 x 112 x 112 x 256: 92 (61).
+//   Two passes (maps that no cluster of 16 holds; backward beyond clusters of 8; 8-bit output
+//   beyond one round of CTAs): one kernel leaves each pixel range's group sums, the next joins
+//   them in its prologue and writes the values, walking its range backwards and storing past
+//   the caches, so that part of x is still in L2.  The second is launched early and waits for
+//   the first.  It reads x twice; where a CTA's life would be long or clusters large it wins.
+//     1 x 512 x 512 x 128 BF16: 44 us (floor 20); 64 x 56 x 56 x 256 to 8 bits: 72 (23), resident 92;
+//     backward 32 x 112 x 112 x 128: 111 (45), resident 123, 16 x 64 x 64 x 256 resident 49 (15).
+//   By channel (pixels that do not start on 16 bytes, over 256 vectors a pixel): as two passes, the
+//   sums kept per channel and joined by a kernel of their own; 4- or 8-byte accesses where the
+//   channels allow.  32 x 112 x 112 x 250 BF16: 186 us (floor 59).
 #include "norm_internal.h"
 #include "pointwise_math.cuh"
 

@@ -8,6 +8,10 @@
 // the products four at a time in 32-bit integers (dp4a), so the sum is exact for every K.
 // Two rows of w share each read of x from shared memory.
 //
+// One token, 4096 -> 4096: 10 us with cold caches and the launch (3.9 us a call in a graph, the
+// weights then in L2), floor 2.5; eight tokens 17: each row of x adds 16 bytes of shared memory
+// read for every 32 of w.
+//
 // Rows of x that arrive as BF16 or FP32 are brought to 8 bits by every CTA for itself (amax,
 // scale, q), between the issue of its first loads of w and their arrival: for a single row that
 // costs less than a launch and a trip through memory.
