@@ -1390,56 +1390,91 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
 
 }  // namespace
 
-// Channels a unit takes and CTAs that share it: the widest chunk of whole groups up to 64 bytes
-// a pixel (the 8-bit output needs whole pixels; 128 bytes make clusters of 16, of which a GPC
-// holds fewer: 32 x 112 x 112 x 256 BF16 113 us against 97, 32 bytes 122), then the fewest CTAs that hold it two
-// to an SM, then one to an SM; more CTAs while there are fewer than SMs.
+// Channels a unit takes and CTAs that share it (the 8-bit output needs whole pixels).  A map of few
+// pixels takes as many channels as one CTA holds, two to an SM (backward: 64 KB of x and dy, since
+// its sums a channel grow with them), while that leaves half a unit an SM: 128 x 14 x 14 x 1024
+// BF16 33 us, 84 at 64 bytes a pixel; 256 x 8 x 8 x 512 17 and 68, backward 29 and 63.  A larger one
+// takes up to 64 bytes a pixel (128 make clusters of 16, of which a GPC holds fewer:
+// 32 x 112 x 112 x 256 BF16 113 us against 97, 32 bytes 122) and the fewest CTAs that hold it
+// two to an SM, then one to an SM.  More CTAs while there are fewer than SMs.
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
     p.chunk = 0;
     if (p.vec * es != 16 || static_cast<long long>(p.P) * (p.C / p.vec) >= (1LL << 31)) return;
-    int chunk = 0;
-    if (mode == kNormInt8) {
-        chunk = p.C;
-    } else {
-        for (int g = 1; g <= p.G; ++g) {  // whole groups that divide the channels and make whole vectors
-            const int c = g * p.cpg;
-            if (p.G % g != 0 || c % p.vec != 0) continue;
-            if (chunk == 0 || c * es <= 64) chunk = c;
-            if (c * es >= 64) break;
-        }
-    }
     const int threads = res_threads(mode);
-    if (chunk == 0 || chunk / p.vec > threads) return;
-    const int rows = threads / (chunk / p.vec);
-    const long long units = static_cast<long long>(p.N) * (p.C / chunk);
     NormParams t = p;
-    t.chunk = chunk;
-    const auto fits = [&](int cluster, int limit) {
+    const auto rows_of = [&](int chunk) { return threads / (chunk / p.vec); };
+    const auto fits = [&](int chunk, int cluster, int limit) {
+        t.chunk = chunk;
         t.splits = cluster;
         const int pixels = res_pixels(t);
-        t.items = (pixels + rows - 1) / rows;
+        t.items = (pixels + rows_of(chunk) - 1) / rows_of(chunk);
         if (static_cast<double>(t.items) * tensors * threads * 16 > limit) return false;
         t.smem_bytes = static_cast<int>(resident_smem(t, mode));
         return t.smem_bytes <= limit;
     };
+    const int half = smem_optin / 2 - 1024;  // of an SM, less what a CTA needs besides
+    int chunk = 0;
+    if (mode == kNormInt8) {
+        chunk = p.C;
+    } else {
+        const long long room = mode == kNormBackward ? 64 * 1024 : half;
+        for (int g = 1; g <= p.G; ++g) {  // whole groups that divide the channels and make whole vectors
+            const int c = g * p.cpg;
+            if (p.G % g != 0 || c % p.vec != 0) continue;
+            if (chunk != 0 && c / p.vec > threads) break;
+            if (chunk == 0 || c * es <= 64 ||
+                (2LL * p.N * (p.C / c) >= num_sms && fits(c, 1, half) && 16LL * tensors * t.items * threads <= room))
+                chunk = c;
+        }
+    }
+    if (chunk == 0 || chunk / p.vec > threads) return;
+    const int rows = rows_of(chunk);
+    const long long units = static_cast<long long>(p.N) * (p.C / chunk);
     int best = 0;
-    for (int limit : {smem_optin / 2 - 1024, smem_optin}) {
+    for (int limit : {half, smem_optin}) {
         for (int cluster = 1; cluster <= kResMaxCluster && best == 0; ++cluster)
-            if (fits(cluster, limit)) best = cluster;
+            if (fits(chunk, cluster, limit)) best = cluster;
         if (best != 0) break;
     }
     if (best == 0 || units * best > 0x7fffffffLL) return;
-    // Backward on clusters of more than eight: 32 x 112 x 112 x 128 BF16 123 us, in two passes 111.
-    if (mode == kNormBackward && best > 8) return;
-    // 8-bit output in more than one round of CTAs: the pixel-wide units make large clusters and long
-    // CTAs (64 x 56 x 56 x 256 BF16: 92 us, in two passes 79; 2 x 16 x 16 x 128: 10 us against 13).
-    if (mode == kNormInt8 && units * best > 2LL * num_sms) return;
     while (2 * best <= kResMaxCluster && units * best * 2 <= num_sms && p.P >= 2 * best * rows) best *= 2;
-    fits(best, smem_optin);
+    fits(chunk, best, smem_optin);
     t.pix_base = t.P / best;
     t.pix_more = t.P % best;
     p = t;
+}
+
+// Whether the resident form (at_a_time clusters on the device) beats two passes, where both can run.
+// A GPC holds few large clusters, so the last of two or three rounds of them leaves much idle,
+// and two CTAs an SM of 100 KB each take long when the SMs are not full of them; two passes pay a second
+// read of x, a launch and their joins.  Pairs: resident, two passes, cold caches, BF16.
+bool norm_resident_pays(const NormParams& p, int mode, int at_a_time, int num_sms) {
+    const long long units = static_cast<long long>(p.N) * (p.C / p.chunk);
+    const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
+    const long long held = 16LL * tensors * p.items * res_threads(mode);  // bytes a CTA holds
+    const bool one_round = units <= at_a_time;
+    if (mode == kNormForward) {
+        // 4 x 160 x 160 x 128 (15 CTAs, 16 units) 31 and 26 us, 12 x 160 x 160 x 128 61 and 46,
+        // 8 x 200 x 200 x 128 74 and 50; of one round, 2 x 160 x 160 x 64 15 and 16.
+        if (p.splits > 8 && !one_round) return false;
+        // 16 x 96 x 96 x 128 (6 CTAs, 64 units of which 46 at a time) 33 and 27 us; at 3.6 rounds of eight
+        // 32 x 112 x 112 x 128 61 and 57, at seven 32 x 112 x 112 x 256 94 and 107.
+        return p.splits <= 4 || one_round || units > 2LL * at_a_time;
+    }
+    if (mode == kNormInt8) {
+        // Pixel-wide units.  Up to 48 KB a CTA: 2 x 16 x 16 x 128 10 and 13 us, 4 x 32 x 32 x 128 12 and 13;
+        // 64 KB of 16 CTAs: 1 x 32 x 32 x 512 21 and 13; 125 KB: 4 x 56 x 56 x 320 33 and 23, 64 x 56 x 56 x 256
+        // 89 and 72.  Many units of at most eight CTAs: 256 x 56 x 56 x 64 71 and 109, 128 x 28 x 28 x 512
+        // 94 and 107; too few of them for the SMs: 16 x 32 x 32 x 320 29 and 24.
+        return held <= 48 * 1024 || (p.splits <= 8 && units * p.splits > num_sms);
+    }
+    // 4 x 96 x 96 x 128 (12 CTAs, 16 units) 23 and 28 us, 4 x 96 x 96 x 512 53 and 59; with four units,
+    // 1 x 96 x 96 x 128 19 and 18; 16 CTAs in nine rounds: 32 x 112 x 112 x 128 124 and 111.
+    if (p.splits > 8) return units >= 8 && (one_round || (p.splits <= 12 && 2 * held <= 224 * 1024));
+    // Small maps of few channels, where the joins are short: 4 x 56 x 56 x 64 16 and 14 us, 1 x 16 x 16 x 64
+    // 13 and 11; of more channels, 4 x 32 x 32 x 512 18 and 24, 2 x 56 x 56 x 320 18 and 24.
+    return p.C > 128 || static_cast<double>(p.N) * p.P * p.C * es > 4e6;
 }
 
 // Two passes: pixel ranges that fill the SMs once, four CTAs to each (three backward or to 8 bits).
@@ -1457,7 +1492,7 @@ void norm_pick_two_pass(NormParams& p, int mode, int num_sms) {
     p.pix_more = p.P % p.splits;
 }
 
-bool norm_resident_runs(const NormParams& p, int mode) {
+int norm_resident_at_a_time(const NormParams& p, int mode, int num_sms) {
     int clusters = 0;
     with_resident(p, mode, [&](auto* fn, SmemLimitCache& limits) {
         cudaLaunchConfig_t cfg;
@@ -1468,10 +1503,10 @@ bool norm_resident_runs(const NormParams& p, int mode) {
             cudaGetLastError();
             clusters = 0;
         } else if (p.splits == 1) {
-            clusters = 1;
+            clusters = 2 * num_sms;
         }
     });
-    return clusters > 0;
+    return clusters;
 }
 
 // Partials of channels (or, forward in two passes, of groups), then per group and range, then the

@@ -125,9 +125,13 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
     for (int mode = 0; mode < 3; ++mode) {
         NormParams& m = pl->np[mode];
         m = p;
+        NormParams two = p;
         norm_pick_resident(m, mode, pl->num_sms, smem_optin);
-        if (m.chunk != 0 && pl->device >= 0 && !norm_resident_runs(m, mode)) m = p;
-        if (m.chunk == 0) norm_pick_two_pass(m, mode, pl->num_sms);
+        norm_pick_two_pass(two, mode, pl->num_sms);
+        int at_a_time = 0;
+        if (m.chunk != 0)
+            at_a_time = pl->device >= 0 ? norm_resident_at_a_time(m, mode, pl->num_sms) : 2 * pl->num_sms / m.splits;
+        if (at_a_time == 0 || (two.two_pass && !norm_resident_pays(m, mode, at_a_time, pl->num_sms))) m = two;
     }
     *out = pl;
     return CONV_OK;

@@ -55,8 +55,10 @@ size_t norm_ab_entries(const NormParams& p);
 void norm_pick_two_pass(NormParams& p, int mode, int num_sms);
 // Fills the resident form's fields for a mode, or leaves chunk 0 where it does not fit.
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin);
-// Whether the device runs a cluster of that shape (called once per plan, with its device current).
-bool norm_resident_runs(const NormParams& p, int mode);
+// Clusters of that shape that the device runs at a time, 0 where it runs none (called once per plan,
+// with its device current).
+int norm_resident_at_a_time(const NormParams& p, int mode, int num_sms);
+bool norm_resident_pays(const NormParams& p, int mode, int at_a_time, int num_sms);
 cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream);
 

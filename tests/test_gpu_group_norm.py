@@ -68,9 +68,14 @@ def test_forward(shape, act, dtype):
 # their magnitude through shared memory.
 LARGE = [(1, 200, 210, 64, 8), (12, 190, 200, 32, 4), (2, 250, 130, 320, 32)]
 
+# Small maps of which one CTA holds many groups, and clusters of a dozen CTAs; more clusters than
+# the device runs at a time.
+HELD = [(40, 7, 7, 320, 20), (160, 5, 3, 104, 13), (20, 14, 14, 512, 32), (4, 96, 96, 64, 4), (160, 28, 28, 96, 8),
+        (3, 150, 160, 32, 2), (80, 9, 9, 2048, 64)]
+
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("shape", LARGE)
+@pytest.mark.parametrize("shape", LARGE + HELD)
 def test_maps_beyond_a_cluster(shape, dtype):
     import cnn_convolution_implicit_gb300 as cg
     N, H, W, C, G = shape
