@@ -268,87 +268,105 @@ __device__ __forceinline__ void finish_block(uint32_t (&v)[16], float xs_lo, flo
     }
 }
 
-// 8 neighbouring outputs of row h of a lane's two to y.  Whole blocks go in 16-byte stores (every
-// row of y starts on 16 bytes then); others one by one, `left` of them.
-template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void store_row(uint8_t* y, const uint32_t (&v)[16], int h, int left) {
-    const auto at = [&](int i) { return v[4 * (i >> 1) + 2 * h + (i & 1)]; };  // column n + i
-    if constexpr (WHOLE && BF16) {
-        uint32_t q[4];
+// 8 neighbouring outputs of row h of a lane's two (columns 8 q .. of row `row` of the block) to the
+// warp's buffer: 64-byte rows with 64-byte swizzle (BF16) or 128 with 128 (FP32), so the eight lanes
+// of a wavefront write 128 bytes.
+template <bool BF16>
+__device__ __forceinline__ uint8_t* block_byte(uint8_t* block, int row, int byte) {
+    if constexpr (BF16) return block + row * 64 + (((byte >> 4) ^ ((row >> 1) & 3)) << 4) + (byte & 15);
+    else return block + row * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void stage_row(uint8_t* block, int row, int q, const uint32_t (&v)[16], int h) {
+    const auto at = [&](int i) { return v[4 * (i >> 1) + 2 * h + (i & 1)]; };  // column 8 q + i
+    if constexpr (BF16) {
+        uint32_t u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(__uint_as_float(at(2 * i)), __uint_as_float(at(2 * i + 1)));
-        *reinterpret_cast<uint4*>(y) = make_uint4(q[0], q[1], q[2], q[3]);
-    } else if constexpr (WHOLE) {
-        reinterpret_cast<uint4*>(y)[0] = make_uint4(at(0), at(1), at(2), at(3));
-        reinterpret_cast<uint4*>(y)[1] = make_uint4(at(4), at(5), at(6), at(7));
+        for (int i = 0; i < 4; ++i) u[i] = pack_bf16x2(__uint_as_float(at(2 * i)), __uint_as_float(at(2 * i + 1)));
+        *reinterpret_cast<uint4*>(block_byte<BF16>(block, row, 16 * q)) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= left) break;
-            if constexpr (BF16) reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(__uint_as_float(at(i)));
-            else reinterpret_cast<uint32_t*>(y)[i] = at(i);
-        }
+        *reinterpret_cast<uint4*>(block_byte<BF16>(block, row, 32 * q)) = make_uint4(at(0), at(1), at(2), at(3));
+        *reinterpret_cast<uint4*>(block_byte<BF16>(block, row, 32 * q + 16)) = make_uint4(at(4), at(5), at(6), at(7));
     }
+}
+
+// The block's 16 rows to rows of y that start on a multiple of T's size, neighbouring lanes at
+// neighbouring places.  columns: of y from the block's first on (a whole number of Ts).
+template <bool BF16, typename T>
+__device__ __forceinline__ void store_rows(uint8_t* y, long long row_bytes, int rows, int columns, uint8_t* block) {
+    constexpr int kRow = BF16 ? 64 : 128, kLanes = kRow / static_cast<int>(sizeof(T)), kRows = kLanes >= 32 ? 1 : 32 / kLanes;
+    const int lane = threadIdx.x & 31, first = lane / kLanes, byte = (lane % kLanes) * static_cast<int>(sizeof(T));
+    if (byte >= columns * (BF16 ? 2 : 4)) return;
+    y += first * row_bytes + byte;
+#pragma unroll 2
+    for (int i = first; i < 16; i += kRows, y += kRows * row_bytes)
+        if (i < rows) *reinterpret_cast<T*>(y) = *reinterpret_cast<const T*>(block_byte<BF16>(block, i, byte));
 }
 
 // What an epilogue warp drains of a tile: its columns in blocks of 32, 16 or 32 rows of them.
 struct Drain {
-    uint32_t at;     // tensor memory of its first row and column
-    int n;           // this lane's first column
-    int rows;        // which of the lane's rows, 8 apart, exist (bits)
-    uint8_t* y;      // its first row and column
-    long long row8;  // bytes of 8 rows of y
-    float xs[4];
-    // BF16 blocks through the TMA: the warp's buffer and the block's place in y
+    uint32_t at;  // tensor memory of its first row and column
+    int n;        // this lane's first column
+    float xs[4];  // scales of this lane's rows, 8 apart
+    uint8_t* out;  // the warp's buffer
     const CUtensorMap* map;
-    uint8_t* out;
-    int block_n, block_m;
+    int block_n, block_m;  // the block's place in y
 };
 
-// G: 16-row groups of the quarter that this warp drains.
-// TMA: the block goes through shared memory (64-byte rows, 64-byte swizzle: the eight lanes of two
-// rows write 128 bytes) and out in one or two bulk stores of 16 rows, which clip what lies past
-// M and N; straight from registers a store touches 8 lines of which it fills half, and ragged N
-// takes single elements (200704 x 256 -> 512, 8-bit input, eight epilogue warps: 86 us straight, 85
-// through the TMA).
+// G: 16-row groups of the quarter that this warp drains.  A block goes through shared memory: out in
+// one or two bulk stores of 16 rows, which clip what lies past M and N (TMA), or, where rows
+// of y do not all start on 16 bytes, in coalesced stores of as many bytes as they start on.
+// Straight from registers a store touches 8 lines, of which it fills half at best (200704 x 256 -> 512,
+// 8-bit input, eight epilogue warps: 86 us straight, 85 through the TMA), and in single elements an
+// eighth (20763 x 170 -> 1035, 8-bit input, BF16: 104 us, 43 from the buffer).
 template <int ACT, bool BF16, bool WHOLE, bool TMA, int G>
 __device__ __forceinline__ void drain_block(const Int8Params& p, const Drain& d) {
-    uint32_t v[G][16];
-#pragma unroll
-    for (int g = 0; g < G; ++g) tmem_ld_16x32(d.at + (static_cast<uint32_t>(16 * g) << 16), v[g]);
+    constexpr int kTurn = BF16 ? G : 1;  // groups that the buffer holds at a time
+    const int lane = threadIdx.x & 31;
     uint64_t ws[4], bias[4];
-    load_pairs<WHOLE>(p.w_scale, d.n, p.N, ws);
-    load_pairs<WHOLE>(p.bias, d.n, p.N, bias);
 #pragma unroll
-    for (int g = 0; g < G; ++g) tmem_ld_wait16(v[g]);
+    for (int t = 0; t < G; t += kTurn) {
+        uint32_t v[kTurn][16];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        finish_block<ACT>(v[g], d.xs[2 * g], d.xs[2 * g + 1], ws, bias);
-        if constexpr (TMA) {
-            if (g == 0) {  // the last block's store has read the buffer
-                if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
+        for (int g = 0; g < kTurn; ++g) tmem_ld_16x32(d.at + (static_cast<uint32_t>(16 * (t + g)) << 16), v[g]);
+        if (t == 0) {
+            load_pairs<WHOLE>(p.w_scale, d.n, p.N, ws);
+            load_pairs<WHOLE>(p.bias, d.n, p.N, bias);
+        }
+#pragma unroll
+        for (int g = 0; g < kTurn; ++g) tmem_ld_wait16(v[g]);
+#pragma unroll
+        for (int g = 0; g < kTurn; ++g) {
+            finish_block<ACT>(v[g], d.xs[2 * (t + g)], d.xs[2 * (t + g) + 1], ws, bias);
+            if (g == 0) {  // what went through the buffer before has been read
+                if (TMA && lane == 0) bulk_wait_read_all();
                 __syncwarp();
             }
-            const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = (lane >> 2) + 8 * h;
-                store_row<true, true>(d.out + g * 1024 + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), v[g], h, 8);
+            for (int h = 0; h < 2; ++h) stage_row<BF16>(d.out + g * 1024, (lane >> 2) + 8 * h, lane & 3, v[g], h);
+        }
+        if constexpr (TMA) fence_proxy_async_smem();
+        __syncwarp();
+        if constexpr (TMA) {
+            if (lane == 0) {
+#pragma unroll
+                for (int g = 0; g < kTurn; ++g)
+                    if (d.block_m + 16 * (t + g) < p.M) tma_store_2d(d.map, d.out + g * 1024, d.block_n, d.block_m + 16 * (t + g));
+                bulk_commit();
             }
         } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (d.rows >> (2 * g + h) & 1) store_row<BF16, WHOLE>(d.y + (2 * g + h) * d.row8, v[g], h, p.N - d.n);
-        }
-    }
-    if constexpr (TMA) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (d.block_m + 16 * g < p.M) tma_store_2d(d.map, d.out + g * 1024, d.block_n, d.block_m + 16 * g);
-            bulk_commit();
+            constexpr int es = BF16 ? 2 : 4;
+            const long long row_bytes = static_cast<long long>(p.N) * es;
+#pragma unroll 1
+            for (int g = 0; g < kTurn; ++g) {
+                const int m = d.block_m + 16 * (t + g);
+                uint8_t* y = static_cast<uint8_t*>(p.y) + m * row_bytes + static_cast<long long>(d.block_n) * es;
+                const int rows = p.M - m, columns = p.N - d.block_n;
+                if (row_bytes % 8 == 0) store_rows<BF16, uint2>(y, row_bytes, rows, columns, d.out + g * 1024);
+                else if (row_bytes % 4 == 0) store_rows<BF16, uint32_t>(y, row_bytes, rows, columns, d.out + g * 1024);
+                else if constexpr (BF16) store_rows<BF16, uint16_t>(y, row_bytes, rows, columns, d.out + g * 1024);
+            }
         }
     }
 }
@@ -418,15 +436,12 @@ __device__ __forceinline__ void join_parts(const Int8Params& p, const float* par
     }
 }
 
-// The columns of a warp: `whole` of its blocks of 32 read scales in wide accesses (and, FP32, store
-// so); BF16 rows that start on 16 bytes go through the TMA.
+// The columns of a warp: `whole` of its blocks of 32 read scales in wide accesses.
 template <int ACT, bool BF16, bool TMA, int G>
 __device__ __forceinline__ void drain_columns(const Int8Params& p, Drain d, int blocks, int whole) {
-    constexpr int es = BF16 ? 2 : 4;
     const auto next = [&] {
         d.at += 32;
         d.n += 32;
-        d.y += 32 * es;
         d.block_n += 32;
     };
     int i = 0;
@@ -442,6 +457,9 @@ __device__ __forceinline__ void drain_act(const Int8Params& p, const Drain& d, i
     else if (p.act == CONV_ACT_SILU) drain_columns<CONV_ACT_SILU, BF16, TMA, G>(p, d, blocks, whole);
     else drain_columns<CONV_ACT_NONE, BF16, TMA, G>(p, d, blocks, whole);
 }
+
+// Whether every row of y starts on 16 bytes (y itself does).
+__host__ __device__ inline bool rows_on_16(const Int8Params& p) { return p.N % (p.out_bf16 ? 8 : 4) == 0; }
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {  // as idesc_bf16_f32 with FP16 operands (type 0)
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -579,9 +597,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3;
         const int part = (warp - kConverterWarps) >> 2;
-        const int es = p.out_bf16 ? 2 : 4;
-        const long long row_bytes = static_cast<long long>(p.N) * es;
-        const bool wide = row_bytes % 16 == 0;  // y itself starts on 16 bytes
+        const bool wide = rows_on_16(p);
         int local = 0;
         // A warp drains a quarter of the columns of 32 rows; of 64 columns half, of 32 all (two of the four
         // warps), 16 rows.
@@ -598,21 +614,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             Drain d;
             d.at = tmem + (static_cast<uint32_t>(lane0) << 16) + buf * BN + col0;
             d.n = first + (lane & 3) * 8;
-            d.y = static_cast<uint8_t*>(p.y) + row0 * row_bytes + static_cast<long long>(d.n) * es;
-            d.row8 = 8 * row_bytes;
             d.map = &map_y;
             d.out = outputs + (warp - kConverterWarps) * S::kOut;
             d.block_n = first;
             d.block_m = static_cast<int>(row0) - (lane >> 2);
-            d.rows = 0;
 #pragma unroll
-            for (int i = 0; i < 2 * G; ++i) {
-                const bool on = row0 + 8 * i < p.M;
-                d.rows |= on ? 1 << i : 0;
-                d.xs[i] = on ? __ldg(p.x_scale + row0 + 8 * i) : 0.0f;
-            }
+            for (int i = 0; i < 2 * G; ++i) d.xs[i] = row0 + 8 * i < p.M ? __ldg(p.x_scale + row0 + 8 * i) : 0.0f;
             const int blocks = left <= 0 ? 0 : (left >= kCols ? kCols / 32 : (left + 31) / 32);
-            const int whole = wide && left > 0 ? (left >= kCols ? kCols / 32 : left / 32) : 0;
+            const int whole = left <= 0 ? 0 : (left >= kCols ? kCols / 32 : left / 32);
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 break;
@@ -625,7 +634,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             } else if (p.out_bf16 && wide) {
                 drain_act<true, true, G>(p, d, blocks, whole);
             } else if (p.out_bf16) {
-                drain_act<true, false, G>(p, d, blocks, 0);
+                drain_act<true, false, G>(p, d, blocks, whole);
+            } else if (wide) {
+                drain_act<false, true, G>(p, d, blocks, whole);
             } else {
                 drain_act<false, false, G>(p, d, blocks, whole);
             }
@@ -775,12 +786,13 @@ cudaError_t launch_variant(const Int8Params& p, int num_sms, bool after_layout, 
     cfg.attrs = attr;
     cfg.numAttrs = n;
     CUtensorMap map_x, map_w, map_y;
-    if (p.out_bf16 && p.N % 8 == 0) {  // rows of y on 16 bytes
+    if (rows_on_16(p)) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
-        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.N) * 2};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.N) * (p.out_bf16 ? 2 : 4)};
         const cuuint32_t box[2] = {32, 16};
-        if (!tensor_map_encoder_ready() || encode_tiled(&map_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, dims, strides, box,
-                                                        CU_TENSOR_MAP_SWIZZLE_64B) != CUDA_SUCCESS)
+        if (!tensor_map_encoder_ready() ||
+            encode_tiled(&map_y, p.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.y, dims,
+                         strides, box, p.out_bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     } else {
         map_y = CUtensorMap();
@@ -800,7 +812,7 @@ __global__ void __launch_bounds__(256) int8_layout_kernel(const int8_t* x, int8_
     for (long long i = blockIdx.x * 256LL + threadIdx.x; i < items; i += gridDim.x * 256LL) {
         const bool is_x = i < x_items;
         const long long at = is_x ? i : i - x_items;
-        const long long row = at / chunks;
+        const long long row = items >> 32 ? at / chunks : static_cast<uint32_t>(at) / static_cast<uint32_t>(chunks);
         const int k = static_cast<int>(at - row * chunks) * 16;
         const int len = K - k < 16 ? K - k : 16;
         const uint4 v = load_item(is_x ? x : w, row * K + k, len, (is_x ? x_rows : w_rows) * K);

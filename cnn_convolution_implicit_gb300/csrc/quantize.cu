@@ -7,6 +7,7 @@
 // a time, 27 us four; the divisions of a row's scale are shared out too).  Longer rows take two sweeps, the largest magnitude, then the
 // values; the second finds a row of ordinary length in L1.
 #include "int8_internal.h"
+#include "int8_rows.cuh"
 #include "pointwise_math.cuh"
 
 namespace convgb {
@@ -15,23 +16,55 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 
-// VEC = 16 bytes of T (rows that all start on 16 bytes) or 1.
-template <typename T, int VEC>
+// Vector v (16 bytes) of a row of K elements, zero past the row; rows may start on any element
+// (ALIGNED: every one starts on 16 bytes and holds whole vectors).
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 row_vector(const T* x, long long row, int M, int K, int v) {
+    constexpr int VEC = 16 / sizeof(T);
+    if constexpr (ALIGNED) {
+        return __ldcs(reinterpret_cast<const uint4*>(x) + row * (K / VEC) + v);
+    } else {
+        const int left = K - v * VEC;
+        return load_item(reinterpret_cast<const int8_t*>(x), (row * K + static_cast<long long>(v) * VEC) * static_cast<int>(sizeof(T)),
+                         (left < VEC ? left : VEC) * static_cast<int>(sizeof(T)), static_cast<long long>(M) * K * static_cast<int>(sizeof(T)));
+    }
+}
+
+// Its 8-bit values to a row of q; pitch: bytes from row to row.  Rows on whole vectors have room for
+// one that runs past K.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void row_store(int8_t* row, int K, int pitch, int v, uint4 raw, const RowFactor& r) {
+    constexpr int VEC = 16 / sizeof(T);
+    f2 f[VEC / 2];
+    VecIo<T, VEC>::unpack(raw, f);
+    int8_t* to = row + v * VEC;
+    if (ALIGNED || pitch % VEC == 0) {
+        quantise_store<VEC>(to, f, r);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+        const uint32_t u = quantise4(f[i / 2], f[i / 2 + 1], r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (v * VEC + i + j < K) to[i + j] = static_cast<int8_t>(u >> (8 * j));
+    }
+}
+
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* x, int M, int K, int pitch,
                                                                       int8_t* q, float* scale) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that may follow
+    constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
     const int lane = threadIdx.x & 31;
-    const int vecs = K / VEC;
-    using Io = VecIo<T, VEC>;
+    const int vecs = (K + VEC - 1) / VEC;
     for (long long row = static_cast<long long>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5); row < M;
          row += static_cast<long long>(gridDim.x) * (kQuantThreads / 32)) {
-        const auto* src = reinterpret_cast<const typename Io::Raw*>(x) + row * vecs;
-        constexpr int H = (VEC + 1) / 2;
         float top = 0.0f;
 #pragma unroll 4
         for (int v = lane; v < vecs; v += 32) {
             f2 f[H];
-            Io::unpack(src[v], f);
+            VecIo<T, VEC>::unpack(row_vector<T, ALIGNED>(x, row, M, K, v), f);
 #pragma unroll
             for (int i = 0; i < H; ++i) top = magnitude(top, f[i]);
         }
@@ -39,34 +72,40 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const T* x
         if (lane == 0) scale[row] = rs.scale;
         int8_t* dst = q + row * pitch;
 #pragma unroll 4
-        for (int v = lane; v < vecs; v += 32) {
-            f2 f[H];
-            Io::unpack(src[v], f);
-            quantise_store<VEC>(dst + v * VEC, f, row_factor(rs.inv));
-        }
+        for (int v = lane; v < vecs; v += 32)
+            row_store<T, ALIGNED>(dst, K, pitch, v, row_vector<T, ALIGNED>(x, row, M, K, v), row_factor(rs.inv));
     }
 }
 
 // Rows of at most 32 P vectors, in registers, R at a time.
-template <typename T, int P, int R>
-__global__ void __launch_bounds__(kQuantThreads, P >= 16 ? 2 : (P >= 8 ? 3 : 4)) quantize_short_rows_kernel(const T* x, int M, int K, int pitch, int8_t* q,
-                                                                               float* scale) {
+template <typename T, int P, int R, bool ALIGNED>
+__global__ void __launch_bounds__(kQuantThreads, P >= 16 ? 2 : (P >= 8 ? 3 : 4))
+    quantize_short_rows_kernel(const T* x, int M, int K, int pitch, int8_t* q, float* scale) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that may follow
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
-    using Io = VecIo<T, VEC>;
     const int lane = threadIdx.x & 31;
-    const int vecs = K / VEC;
+    const int vecs = (K + VEC - 1) / VEC;
     for (long long row0 = (static_cast<long long>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5)) * R; row0 < M;
          row0 += static_cast<long long>(gridDim.x) * (kQuantThreads / 32) * R) {
         uint4 raw[R][P];
-        const uint4* src = reinterpret_cast<const uint4*>(x) + row0 * vecs + lane;
+        if constexpr (ALIGNED) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int h = 0; h < P; ++h) {
-                raw[r][h] = make_uint4(0, 0, 0, 0);
-                if (row0 + r < M && lane + 32 * h < vecs) raw[r][h] = __ldcs(src + r * vecs + 32 * h);
-            }
+                for (int h = 0; h < P; ++h) {
+                    raw[r][h] = make_uint4(0, 0, 0, 0);
+                    if (row0 + r < M && lane + 32 * h < vecs) raw[r][h] = row_vector<T, true>(x, row0 + r, M, K, lane + 32 * h);
+                }
+        } else {
+            constexpr int es = sizeof(T);
+            StraddlingRow<P> rows[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)  // a row past the last has no bytes
+                rows[r].load(reinterpret_cast<const int8_t*>(x), (row0 + r) * K * es, row0 + r < M ? K * es : 0,
+                             static_cast<long long>(M) * K * es, lane, raw[r]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) rows[r].shift(lane, raw[r]);
+        }
         uint32_t top[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -74,7 +113,7 @@ __global__ void __launch_bounds__(kQuantThreads, P >= 16 ? 2 : (P >= 8 ? 3 : 4))
 #pragma unroll
             for (int h = 0; h < P; ++h) {
                 f2 f[H];
-                Io::unpack(raw[r][h], f);
+                VecIo<T, VEC>::unpack(raw[r][h], f);
 #pragma unroll
                 for (int i = 0; i < H; ++i) m = magnitude(m, f[i]);
             }
@@ -85,47 +124,48 @@ __global__ void __launch_bounds__(kQuantThreads, P >= 16 ? 2 : (P >= 8 ? 3 : 4))
         RowFactor rf[R];
         const float own = row_factors<R>(top, lane, 32, rf);
         if (lane < R && row0 + lane < M) scale[row0 + lane] = own;
-        int8_t* dst = q + row0 * pitch + lane * VEC;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row0 + r >= M) break;
 #pragma unroll
             for (int h = 0; h < P; ++h)
-                if (lane + 32 * h < vecs) {
-                    f2 f[H];
-                    Io::unpack(raw[r][h], f);
-                    quantise_store<VEC>(dst + r * pitch + 32 * h * VEC, f, rf[r]);
-                }
+                if (lane + 32 * h < vecs) row_store<T, ALIGNED>(q + (row0 + r) * pitch, K, pitch, lane + 32 * h, raw[r][h], rf[r]);
         }
     }
 }
 
-template <typename T>
+template <typename T, bool ALIGNED>
 cudaError_t launch_typed(const T* x, int M, int K, int pitch, int8_t* q, float* scale, int num_sms, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    const bool wide = K % V == 0;
+    const int vecs = (K + V - 1) / V;
     int parts = 1;  // vectors a lane keeps of a row
-    while (parts < 16 && 32 * parts < K / V) parts *= 2;
-    const bool in_registers = wide && 32 * parts >= K / V;
+    while (parts < 16 && 32 * parts < vecs) parts *= 2;
+    const bool in_registers = 32 * parts >= vecs;
     const long long rows = (kQuantThreads / 32) * (in_registers && parts <= 2 ? 4 / parts : 1);
     const long long need = (static_cast<long long>(M) + rows - 1) / rows;
     const unsigned grid = static_cast<unsigned>(need < 8LL * num_sms ? need : 8LL * num_sms);
-    if (in_registers && parts == 1) quantize_short_rows_kernel<T, 1, 4><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else if (in_registers && parts == 2) quantize_short_rows_kernel<T, 2, 2><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else if (in_registers && parts == 4) quantize_short_rows_kernel<T, 4, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else if (in_registers && parts == 8) quantize_short_rows_kernel<T, 8, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else if (in_registers) quantize_short_rows_kernel<T, 16, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else if (wide) quantize_rows_kernel<T, V><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
-    else quantize_rows_kernel<T, 1><<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale);
+    const auto run = [&](auto* kernel) { kernel<<<grid, kQuantThreads, 0, stream>>>(x, M, K, pitch, q, scale); };
+    if (!in_registers) run(quantize_rows_kernel<T, ALIGNED>);
+    else if (parts == 1) run(quantize_short_rows_kernel<T, 1, 4, ALIGNED>);
+    else if (parts == 2) run(quantize_short_rows_kernel<T, 2, 2, ALIGNED>);
+    else if (parts == 4) run(quantize_short_rows_kernel<T, 4, 1, ALIGNED>);
+    else if (parts == 8) run(quantize_short_rows_kernel<T, 8, 1, ALIGNED>);
+    else run(quantize_short_rows_kernel<T, 16, 1, ALIGNED>);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_rows(const T* x, int M, int K, int pitch, int8_t* q, float* scale, int num_sms, cudaStream_t stream) {
+    if (K % (16 / sizeof(T)) == 0) return launch_typed<T, true>(x, M, K, pitch, q, scale, num_sms, stream);
+    return launch_typed<T, false>(x, M, K, pitch, q, scale, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_rows(const void* x, bool bf16, int M, int K, int pitch, int8_t* q, float* scale, int num_sms,
                                  cudaStream_t stream) {
-    if (bf16) return launch_typed(static_cast<const __nv_bfloat16*>(x), M, K, pitch, q, scale, num_sms, stream);
-    return launch_typed(static_cast<const float*>(x), M, K, pitch, q, scale, num_sms, stream);
+    if (bf16) return launch_rows(static_cast<const __nv_bfloat16*>(x), M, K, pitch, q, scale, num_sms, stream);
+    return launch_rows(static_cast<const float*>(x), M, K, pitch, q, scale, num_sms, stream);
 }
 
 }  // namespace convgb

@@ -44,6 +44,38 @@ def test_product(size, out):
     assert cg.device_status() == 0
 
 
+# Rows of y that start on 2, 4, 8 bytes in every tile shape; rows of x of every length class whose
+# vectors straddle 16 bytes.
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(5000, 1002, 144), (5000, 1004, 64), (5001, 1003, 80), (2000, 90, 112), (2000, 92, 96), (333, 42, 64),
+                                  (40, 31, 48)])
+def test_rows_of_y_off_16_bytes(size, out):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, xs, w, ws, bias = _inputs(M, N, K, 5 * M + N + K)
+    canvas = torch.full((M * N + 64,), 7.0, device="cuda", dtype=torch.bfloat16 if out == "bf16" else torch.float32)
+    y = canvas[:M * N].view(M, N)
+    plan = cg.Int8MatmulPlan(M, N, K, out=out, act="silu")
+    plan.forward(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), bias.cuda(), y=y)
+    want, tol = ref.int8_product(x.numpy(), xs.numpy(), w.numpy(), ws.numpy(), bias.numpy(), "silu")
+    ref.check(_np(y), want, tol, out == "bf16", "y")
+    assert torch.all(canvas[M * N:] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(9, 250), (50, 257), (33, 500), (21, 1022), (17, 2047), (5, 4090), (3, 5001), (700, 36)])
+def test_quantize_rows_that_straddle_vectors(M, K, dtype):
+    import cnn_convolution_implicit_gb300 as cg
+    x = (torch.randn(M, K, generator=torch.Generator().manual_seed(M + K)) * 3).to(dtype)
+    q, s = cg.quantize_rows(x.cuda())
+    wq, ws = ref.quantize_rows(x.float().numpy())
+    assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
+    _, _, w, wsc, bias = _inputs(M, 48, K, 8)
+    y = cg.int8_linear(x.cuda(), w.cuda(), wsc.cuda(), bias.cuda(), out="f32")
+    want, tol = ref.int8_product(wq, ws, w.numpy(), wsc.numpy(), bias.numpy(), "none")
+    ref.check(_np(y), want, tol, False, "y")
+
+
 # Every tile shape and split of K: pairs of SMs over several rounds, 128, 64 and 32 columns, two, four
 # and eight CTAs to a tile, a K that the split does not divide, and each with rows off 16 bytes.
 @pytest.mark.parametrize("out", ["bf16", "f32"])
