@@ -39,7 +39,7 @@
 // 69 % of the card's measured BF16 matrix rate: with the converters' stores left out the same
 // kernel takes 174 us, so a fifth is shared memory's share (per K = 64 and SM of a pair: 16 KB
 // raw in, 16 KB out, 32 KB FP16 in, 32 KB to the MMA, 768 clocks at 128 bytes against 512 of MMA).
-// 200704 x 256 -> 512: 72 us, 62 % of the memory's rate.  16 x 4096 -> 4096: 14 us in a graph.
+// 200704 x 256 -> 512: 68 us, 56 % of the memory's rate over its 257 MB.  16 x 4096 -> 4096: 14 us in a graph.
 //
 // PAIR: two SMs share a 256 x BN tile (tcgen05.mma.cta_group::2): each converts its own
 // 128 rows of x and BN / 2 rows of w.  Shared memory bounds this kernel (written by the
@@ -299,9 +299,18 @@ __device__ __forceinline__ void store_rows(uint8_t* y, long long row_bytes, int 
     const int lane = threadIdx.x & 31, first = lane / kLanes, byte = (lane % kLanes) * static_cast<int>(sizeof(T));
     if (byte >= columns * (BF16 ? 2 : 4)) return;
     y += first * row_bytes + byte;
-#pragma unroll 2
-    for (int i = first; i < 16; i += kRows, y += kRows * row_bytes)
-        if (i < rows) *reinterpret_cast<T*>(y) = *reinterpret_cast<const T*>(block_byte<BF16>(block, i, byte));
+    // Reads under way: of 128 columns, 2-byte stores, two 3.1 us a tile and eight 2.8; 4-byte ones of FP32 on a
+    // pair 6.0 and 7.4.
+    constexpr int kBatch = BF16 ? (16 / kRows < 8 ? 16 / kRows : 8) : 2;
+#pragma unroll 1
+    for (int i = first; i < 16; i += kBatch * kRows) {
+        T v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] = *reinterpret_cast<const T*>(block_byte<BF16>(block, i + k * kRows, byte));
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k, y += kRows * row_bytes)
+            if (i + k * kRows < rows) *reinterpret_cast<T*>(y) = v[k];
+    }
 }
 
 // What an epilogue warp drains of a tile: its columns in blocks of 32, 16 or 32 rows of them.
@@ -837,16 +846,21 @@ cudaError_t launch_int8_layout(const int8_t* x, int8_t* xr, long long x_rows, co
 namespace {
 
 // Tile shapes and what they cost, in microseconds on a 152-SM part at ~1.9 GHz (repeated launches
-// in a graph, 8-bit input, BF16 output): a K = 64 step, the least a tile takes (its epilogue), and
-// what joining the parts adds where a cluster splits K.  From 16 x 4096 x 4096 (64 steps): 29.4 us as
-// 128 tiles of 32 columns, 18.8 as 64 tiles of 64 split in two, 14.2 as 32 tiles of 128 split
-// in four; from 1000 x 4096 x 4096: 66 us in tiles of 128 x 128 and 37 on pairs; from
-// 100 x 512 x 512 in two steps: 7.2 / 7.5 / 9.3 us with 32 / 64 / 128 columns.
+// in a graph, 8-bit input, whole rounds of tiles): a K = 64 step and what a tile takes besides, the
+// least it takes (its epilogue), both again where rows of y start off 16 bytes, the launch, and what
+// joining the parts adds where a cluster splits K.  From K = 64 / 256 / 1024, BF16 output:
+// 1.1 / 2.0 / 6.9 us a tile of 32 columns, 1.3 / 2.2 / 7.3 of 64, 1.8 / 2.8 / 8.2 of 128, 3.1 / 3.8 / 8.8 on a pair.
+// 16 x 4096 x 4096 (64 steps): 29.4 us as 128 tiles of 32 columns, 18.8 as 64 tiles of 64 split
+// in two, 14.2 as 32 tiles of 128 split in four; 1000 x 4096 x 4096: 66 us in tiles of
+// 128 x 128 and 37 on pairs.
 struct Tile {
     int rows, columns;
-    double step, least, join;
+    double step, besides, least, off_besides, off_least, launch, join;
 };
-constexpr Tile kTiles[4] = {{128, 32, 0.38, 0.6, 1.9}, {128, 64, 0.42, 1.0, 2.4}, {128, 128, 0.55, 2.0, 3.8}, {256, 256, 0.50, 4.0, 0.0}};
+constexpr Tile kTiles[4] = {{128, 32, 0.415, 0.25, 1.15, 0.40, 1.45, 4.4, 1.9},
+                            {128, 64, 0.42, 0.45, 1.35, 0.70, 1.80, 4.7, 2.4},
+                            {128, 128, 0.46, 0.90, 1.85, 1.8, 3.0, 5.0, 3.8},
+                            {256, 256, 0.45, 1.60, 3.05, 3.0, 5.5, 5.8, 0.0}};
 
 // Clusters of this kernel's CTAs (one an SM) that the part holds at a time, by CTAs in a cluster: a
 // 152-SM part holds 76 of 2, 36 of 4 and 15 of 8.
@@ -860,6 +874,7 @@ int clusters_at_a_time(int num_sms, int ctas) {
 cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_layout, cudaStream_t stream) {
     Int8Params p = given;
     const long long steps = (p.K + kStepK - 1) / kStepK;
+    const bool on_16 = rows_on_16(p);
     double best = 0.0;
     int tile = -1;
     for (int i = 0; i < 4; ++i) {
@@ -868,8 +883,9 @@ cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_la
         for (int splits = 1; splits <= (i < 3 ? 8 : 1); splits *= 2) {
             const long long at_a_time = clusters_at_a_time(num_sms, i == 3 ? 2 : splits);
             if (splits > 1 && (units > at_a_time || steps < 2 * splits)) break;
-            const double each = static_cast<double>((steps + splits - 1) / splits) * t.step;
-            const double cost = static_cast<double>((units + at_a_time - 1) / at_a_time) * (each > t.least ? each : t.least) +
+            const double each = static_cast<double>((steps + splits - 1) / splits) * t.step + (on_16 ? t.besides : t.off_besides);
+            const double least = on_16 ? t.least : t.off_least;
+            const double cost = t.launch + static_cast<double>((units + at_a_time - 1) / at_a_time) * (each > least ? each : least) +
                                 (splits > 1 ? t.join : 0.0);
             if (tile < 0 || cost < best) {
                 best = cost;
