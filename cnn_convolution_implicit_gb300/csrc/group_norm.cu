@@ -989,6 +989,48 @@ struct TwoRange {
     }
 };
 
+// A thread's vectors of one or two tensors, in order, through slots of shared memory that only it
+// writes and reads: kSlots - 1 of each are on their way at any time, whatever the arithmetic does
+// (four at a time in registers, waited for together, kept half of that in flight on average).
+constexpr int kSlots = 8;  // a power of two
+
+template <int TENSORS>
+struct RangeStream {
+    const uint4* from[TENSORS];
+    uint4* slots;  // [kSlots][TENSORS][threads], from this thread's on
+    long long step;
+    int count;
+
+    __device__ __forceinline__ void fetch(int i) {
+        if (i < count) {
+#pragma unroll
+            for (int t = 0; t < TENSORS; ++t) {
+                copy_async16(static_cast<uint32_t>(__cvta_generic_to_shared(&slots[((i & (kSlots - 1)) * TENSORS + t) * kNormThreads])), from[t]);
+                from[t] += step;
+            }
+        }
+        copy_commit();
+    }
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int i = 0; i < kSlots - 1; ++i) fetch(i);
+    }
+    // take(vectors, first) for each; a slot is filled again one turn after it was read.
+    template <typename F>
+    __device__ __forceinline__ void run(F&& take) {
+#pragma unroll 2
+        for (int i = 0; i < count; ++i) {
+            copy_wait<kSlots - 2>();
+            uint4 raw[TENSORS];
+#pragma unroll
+            for (int t = 0; t < TENSORS; ++t) raw[t] = slots[((i & (kSlots - 1)) * TENSORS + t) * kNormThreads];
+            fetch(i + kSlots - 1);
+            take(raw, i == 0);
+        }
+        copy_wait<0>();
+    }
+};
+
 // First pass.  Forward: (mean, M2) of the range's groups; backward: (sum u gamma, sum u h gamma) of
 // them and the channels' (sum u, sum u h).
 template <typename T, int MODE, int ACT>
@@ -999,66 +1041,48 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
     float2* part = reinterpret_cast<float2*>(smem_raw);
     const TwoRange t(p, blockIdx.x, VEC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint4* x = static_cast<const uint4*>(p.x) + t.base;
+    constexpr int kTensors = MODE == kNormBackward ? 2 : 1;
+    RangeStream<kTensors> stream;
+    stream.from[0] = static_cast<const uint4*>(p.x) + t.base;
+    if constexpr (MODE == kNormBackward) stream.from[1] = static_cast<const uint4*>(p.dy) + t.base;
+    stream.step = t.step;
+    stream.count = t.mine;
+    stream.slots = reinterpret_cast<uint4*>(smem_raw) + threadIdx.x;
+    stream.start();
     launch_dependents();
-    const long long step = t.step;  // 64 bits: the addresses of a batch are one running sum (32 measured 10% slower here)
     if constexpr (MODE != kNormBackward) {
         Moments<VEC> mo;
         f2 f[H];
-        if (t.mine) {
-            Io::unpack(__ldg(x), f);
-            mo.start(f);
-        }
-        constexpr int B = kTwoBatch;  // eight spill at four CTAs an SM
-        for (int i = 0; i < t.mine; i += B) {
-            uint4 raw[B];
-#pragma unroll
-            for (int k = 0; k < B; ++k)
-                if (i + k < t.mine) raw[k] = __ldg(x + (i + k) * step);
-#pragma unroll
-            for (int k = 0; k < B; ++k)
-                if (i + k < t.mine) {
-                    Io::unpack(raw[k], f);
-                    mo.add(f);
-                }
-        }
+        stream.run([&](const uint4 (&raw)[1], bool first) {
+            Io::unpack(raw[0], f);
+            if (first) mo.start(f);
+            mo.add(f);
+        });
         float mean[VEC], m2[VEC];
         mo.finish(t.mine, mean, m2);
+        __syncthreads();  // the slots are the partial sums' place from here
         const auto store = [&](int g, float2 val, int wide) {
             if ((lane & (wide - 1)) == 0) p.part[(static_cast<long long>(t.n) * p.G + g) * p.splits + t.s] = val;
         };
         cta_group_moments<VEC>(p, t.p1 - t.p0, t.vpr, t.rows, t.r, t.v, t.mine, mean, m2, p.G, part, [] {}, store);
     } else {
-        const uint4* dy = static_cast<const uint4*>(p.dy) + t.base;
         Grad<VEC> grad;
         grad.set(p, (t.r < t.rows ? t.v : 0) * VEC, [&](int c) { return stats_of(p, t.n, c); });
         f2 s1[H], s2[H];
 #pragma unroll
         for (int j = 0; j < H; ++j) s1[j] = s2[j] = 0;
-        const auto take = [&](const uint4& a, const uint4& b) {
+        stream.run([&](const uint4 (&raw)[2], bool) {
             f2 f[H], d[H];
-            Io::unpack(a, f);
-            Io::unpack(b, d);
+            Io::unpack(raw[0], f);
+            Io::unpack(raw[1], d);
             grad.template apply<ACT>(f, d);
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 s1[j] = f2_add(s1[j], d[j]);
                 s2[j] = f2_fma(d[j], f[j], s2[j]);
             }
-        };
-        constexpr int B = kTwoBatch;
-        for (int i = 0; i < t.mine; i += B) {
-            uint4 a[B], b[B];
-#pragma unroll
-            for (int k = 0; k < B; ++k)
-                if (i + k < t.mine) {
-                    a[k] = __ldg(x + static_cast<unsigned>((i + k) * t.step));
-                    b[k] = __ldg(dy + static_cast<unsigned>((i + k) * t.step));
-                }
-#pragma unroll
-            for (int k = 0; k < B; ++k)
-                if (i + k < t.mine) take(a[k], b[k]);
-        }
+        });
+        __syncthreads();  // the slots are the partial sums' place from here
         float2* out = p.part + (static_cast<long long>(t.n) * p.splits + t.s) * p.C;
         const auto store = [&](int g, float2 val, int wide) {
             if ((lane & (wide - 1)) == 0) p.ab[(static_cast<long long>(t.n) * p.G + g) * p.splits + t.s] = val;
@@ -1526,7 +1550,14 @@ int range_sums_smem(const NormParams& p) {
     const int vpr = p.C / p.vec, rows = kNormThreads / vpr;
     const int entries = MODE == kNormBackward ? (res_warp_rows(vpr) ? kNormThreads / 32 : rows) * p.C
                                               : rows * vpr * (p.vec / res_lump(p));
-    return entries * 8;  // 16 KB at most
+    const int slots = kSlots * (MODE == kNormBackward ? 2 : 1) * kNormThreads * 16;
+    return entries * 8 > slots ? entries * 8 : slots;  // the partial sums, 16 KB at most, take the slots' place
+}
+
+template <typename T, int MODE, int ACT>
+SmemLimitCache& sums_limits() {
+    static SmemLimitCache limits;
+    return limits;
 }
 
 template <int MODE>
@@ -1537,7 +1568,9 @@ cudaError_t launch_two_pass(const NormParams& p, cudaStream_t stream) {
     const int vpr = p.C / p.vec, rows = kNormThreads / vpr;
     const int joined = p.G * 8 + (MODE == kNormInt8 ? 2 * 4 * rows * 4 : 0);
     const int apply_smem = joined > kNormThreads * 8 ? joined : kNormThreads * 8;
-    const auto run = [&](auto* sums, auto* apply) {
+    const auto run = [&](auto* sums, SmemLimitCache& limits, auto* apply) {
+        e = ensure_smem_limit(reinterpret_cast<const void*>(sums), range_sums_smem<MODE>(p), limits);
+        if (e != cudaSuccess) return;
         sums<<<grid, kNormThreads, range_sums_smem<MODE>(p), stream>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return;
@@ -1563,8 +1596,10 @@ cudaError_t launch_two_pass(const NormParams& p, cudaStream_t stream) {
         constexpr int A = decltype(act)::value;
         constexpr int SA = MODE == kNormBackward ? A : static_cast<int>(CONV_ACT_NONE);  // forward sums need no activation
         constexpr int SM = MODE == kNormBackward ? kNormBackward : kNormForward;
-        if (p.bf16) run(norm_range_sums_kernel<__nv_bfloat16, SM, SA>, norm_range_apply_kernel<__nv_bfloat16, MODE, A>);
-        else run(norm_range_sums_kernel<float, SM, SA>, norm_range_apply_kernel<float, MODE, A>);
+        if (p.bf16)
+            run(norm_range_sums_kernel<__nv_bfloat16, SM, SA>, sums_limits<__nv_bfloat16, SM, SA>(), norm_range_apply_kernel<__nv_bfloat16, MODE, A>);
+        else
+            run(norm_range_sums_kernel<float, SM, SA>, sums_limits<float, SM, SA>(), norm_range_apply_kernel<float, MODE, A>);
     });
     return e;
 }
