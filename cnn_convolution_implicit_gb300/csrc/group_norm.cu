@@ -20,7 +20,7 @@
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + n_i (mean_i - mean)^2.
 //
 // Bound by memory: x read and y written once (backward: x and dy read, dx written).  Three forms,
-// chosen per plan (norm_pick_resident, norm_pick_two_pass); times with cold caches, launch
+// chosen per plan (norm_resident_pays); times with cold caches, launch
 // included, against the bytes at the card's measured copy rate:
 //
 //   Resident: each CTA copies its pixels of `chunk` channels into shared memory once
@@ -31,13 +31,12 @@
 //   life (~11 us: 5.5 loading, 3 from the last load to the first store, 2.5 storing), and clusters
 //   of eight fill 288 of 304 places, of sixteen 224.
 //     1 x 8 x 8 x 256 BF16: 8 us; 64 x 56 x 56 x 256: 55 us (floor 30); 32 x 112 x 112 x 256: 92 (61).
-//   Two passes (maps that no cluster of 16 holds; backward beyond clusters of 8; 8-bit output
-//   beyond one round of CTAs): one kernel leaves each pixel range's group sums, the next joins
+//   Two passes (maps that no cluster of 16 holds, and where clusters fill the SMs badly): one kernel leaves each pixel range's group sums, the next joins
 //   them in its prologue and writes the values, walking its range backwards and storing past
 //   the caches, so that part of x is still in L2.  The second is launched early and waits for
 //   the first.  It reads x twice; where a CTA's life would be long or clusters large it wins.
-//     1 x 512 x 512 x 128 BF16: 44 us (floor 20); 64 x 56 x 56 x 256 to 8 bits: 72 (23), resident 92;
-//     backward 32 x 112 x 112 x 128: 111 (45), resident 123, 16 x 64 x 64 x 256 resident 49 (15).
+//     1 x 512 x 512 x 128 BF16: 43 us (floor 20); 64 x 56 x 56 x 256 to 8 bits: 70 (23), resident 92;
+//     backward 32 x 112 x 112 x 128: 97 (45), resident 123; 16 x 64 x 64 x 256 42 (15), resident 49.
 //   By channel (pixels that do not start on 16 bytes, over 256 vectors a pixel): as two passes, the
 //   sums kept per channel and joined by a kernel of their own; 4- or 8-byte accesses where the
 //   channels allow.  32 x 112 x 112 x 250 BF16: 186 us (floor 59).
@@ -1493,12 +1492,14 @@ bool norm_resident_pays(const NormParams& p, int mode, int at_a_time, int num_sm
         // 94 and 107; too few of them for the SMs: 16 x 32 x 32 x 320 29 and 24.
         return held <= 48 * 1024 || (p.splits <= 8 && units * p.splits > num_sms);
     }
-    // 4 x 96 x 96 x 128 (12 CTAs, 16 units) 23 and 28 us, 4 x 96 x 96 x 512 53 and 59; with four units,
-    // 1 x 96 x 96 x 128 19 and 18; 16 CTAs in nine rounds: 32 x 112 x 112 x 128 124 and 111.
-    if (p.splits > 8) return units >= 8 && (one_round || (p.splits <= 12 && 2 * held <= 224 * 1024));
-    // Small maps of few channels, where the joins are short: 4 x 56 x 56 x 64 16 and 14 us, 1 x 16 x 16 x 64
-    // 13 and 11; of more channels, 4 x 32 x 32 x 512 18 and 24, 2 x 56 x 56 x 320 18 and 24.
-    return p.C > 128 || static_cast<double>(p.N) * p.P * p.C * es > 4e6;
+    // Maps of few channels, where the joins are short: 4 x 56 x 56 x 64 16 and 13 us, 16 x 56 x 56 x 64 21 and 17; of
+    // more channels, 4 x 32 x 32 x 512 18 and 22, 16 x 16 x 16 x 512 16 and 23.
+    if (p.C <= 128 && static_cast<double>(p.N) * p.P * p.C * es <= 1e7) return false;
+    // Clusters of a dozen in one round that fills the SMs, 1 x 96 x 96 x 512 23 and 28 us; in 1.4 rounds 8 x 96 x 96 x 128
+    // 35 and 32, of 200 KB a CTA 4 x 128 x 128 x 128 43 and 32, of sixteen 32 x 112 x 112 x 128 134 and 111.
+    if (p.splits > 8) return one_round && 3 * units >= at_a_time && held > 64 * 1024 && held <= 112 * 1024;
+    // 16 x 64 x 64 x 256 (2.2 rounds) 50 and 44 us; seven rounds, 64 x 56 x 56 x 256, 107 and 111.
+    return units <= 2LL * at_a_time || units > 3LL * at_a_time;
 }
 
 // Two passes: pixel ranges that fill the SMs once, four CTAs to each (three backward or to 8 bits).
