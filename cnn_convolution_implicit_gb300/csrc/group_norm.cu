@@ -20,8 +20,8 @@
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + n_i (mean_i - mean)^2.
 //
 // Bound by memory: x read and y written once (backward: x and dy read, dx written).  Three forms,
-// chosen per plan (norm_resident_pays); times with cold caches, launch
-// included, against the bytes at the card's measured copy rate:
+// chosen per plan (norm_resident_pays); times with cold caches, launch included, against the
+// bytes at the card's measured copy rate:
 //
 //   Resident: each CTA copies its pixels of `chunk` channels into shared memory once
 //   (cp.async, each thread reads back only what it copied), pushes its groups' sums into the
@@ -31,12 +31,13 @@
 //   life (~11 us: 5.5 loading, 3 from the last load to the first store, 2.5 storing), and clusters
 //   of eight fill 288 of 304 places, of sixteen 224.
 //     1 x 8 x 8 x 256 BF16: 8 us; 64 x 56 x 56 x 256: 55 us (floor 30); 32 x 112 x 112 x 256: 92 (61).
-//   Two passes (maps that no cluster of 16 holds, and where clusters fill the SMs badly): one kernel leaves each pixel range's group sums, the next joins
+//   Two passes (maps that no cluster of 16 holds, and where clusters fill the SMs badly): one
+//   kernel leaves each pixel range's group sums, streaming it through shared memory; the next joins
 //   them in its prologue and writes the values, walking its range backwards and storing past
 //   the caches, so that part of x is still in L2.  The second is launched early and waits for
 //   the first.  It reads x twice; where a CTA's life would be long or clusters large it wins.
 //     1 x 512 x 512 x 128 BF16: 43 us (floor 20); 64 x 56 x 56 x 256 to 8 bits: 70 (23), resident 92;
-//     backward 32 x 112 x 112 x 128: 97 (45), resident 123; 16 x 64 x 64 x 256 42 (15), resident 49.
+//     backward 32 x 112 x 112 x 128: 97 (45), resident 123; 16 x 64 x 64 x 256 43 (15), resident 50.
 //   By channel (pixels that do not start on 16 bytes, over 256 vectors a pixel): as two passes, the
 //   sums kept per channel and joined by a kernel of their own; 4- or 8-byte accesses where the
 //   channels allow.  32 x 112 x 112 x 250 BF16: 186 us (floor 59).
@@ -990,7 +991,7 @@ struct TwoRange {
 
 // A thread's vectors of one or two tensors, in order, through slots of shared memory that only it
 // writes and reads: kSlots - 1 of each are on their way at any time, whatever the arithmetic does
-// (four at a time in registers, waited for together, kept half of that in flight on average).
+// (four at a time in registers, waited for together: backward 32 x 112 x 112 x 128 111 us, 97 so).
 constexpr int kSlots = 8;  // a power of two
 
 template <int TENSORS>
@@ -1492,9 +1493,9 @@ bool norm_resident_pays(const NormParams& p, int mode, int at_a_time, int num_sm
         // 94 and 107; too few of them for the SMs: 16 x 32 x 32 x 320 29 and 24.
         return held <= 48 * 1024 || (p.splits <= 8 && units * p.splits > num_sms);
     }
-    // Maps of few channels, where the joins are short: 4 x 56 x 56 x 64 16 and 13 us, 16 x 56 x 56 x 64 21 and 17; of
-    // more channels, 4 x 32 x 32 x 512 18 and 22, 16 x 16 x 16 x 512 16 and 23.
-    if (p.C <= 128 && static_cast<double>(p.N) * p.P * p.C * es <= 1e7) return false;
+    // Small maps of few channels, where the joins are short: 4 x 56 x 56 x 64 16 and 13 us (with x and dy in L2 9.3
+    // and 8.6); larger, 8 x 56 x 56 x 64 FP32, 17 and 17 (8.2 and 11); of more channels 4 x 32 x 32 x 512 18 and 22.
+    if (p.C <= 128 && static_cast<double>(p.N) * p.P * p.C * es <= 4e6) return false;
     // Clusters of a dozen in one round that fills the SMs, 1 x 96 x 96 x 512 23 and 28 us; in 1.4 rounds 8 x 96 x 96 x 128
     // 35 and 32, of 200 KB a CTA 4 x 128 x 128 x 128 43 and 32, of sixteen 32 x 112 x 112 x 128 134 and 111.
     if (p.splits > 8) return one_round && 3 * units >= at_a_time && held > 64 * 1024 && held <= 112 * 1024;
