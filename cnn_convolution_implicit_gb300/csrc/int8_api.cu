@@ -34,8 +34,8 @@ conv_status check_device(const conv_int8_plan* pl) {
 
 size_t up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-// Workspace of the tensor-core form: rows of x that it quantises, or that do not start on 16 bytes
-// as they are; rows of w that do not; the scales of quantised rows.
+// Workspace of the tensor-core forms: rows of x that they quantise, with their scales; for many rows also
+// those of x and w that do not start on 16 bytes.
 struct Workspace {
     int pitch;                // bytes between rows
     size_t x, w, scales;      // offsets
@@ -44,10 +44,10 @@ struct Workspace {
 
 Workspace workspace_of(const Int8Params& p) {
     Workspace ws = {};
-    if (!int8_use_gemm(p)) return ws;
+    if (!int8_use_gemm(p) && !int8_use_mid(p)) return ws;
     ws.pitch = static_cast<int>(up(p.K, 16));
     const size_t x = up(static_cast<size_t>(p.M) * ws.pitch, 256);
-    const size_t w = p.K % 16 != 0 ? up(static_cast<size_t>(p.N) * ws.pitch, 256) : 0;
+    const size_t w = p.K % 16 != 0 && int8_use_gemm(p) ? up(static_cast<size_t>(p.N) * ws.pitch, 256) : 0;
     ws.w = x;
     ws.scales = x + w;
     ws.forward = w != 0 ? x + w : 0;
@@ -126,6 +126,7 @@ conv_status conv_int8_forward(conv_int8_plan* pl, const void* x, const float* x_
     p.y = y;
     p.x_pitch = p.w_pitch = p.K;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (int8_use_mid(p)) return launched(launch_int8_mid(p, false, st));
     if (!int8_use_gemm(p)) return launched(launch_int8_few(p, st));
     if (ws.forward != 0) {
         int8_t* base = static_cast<int8_t*>(workspace);
@@ -150,7 +151,7 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
                                        const float* w_scale, const float* bias, void* y, void* workspace,
                                        void* stream) {
     if (pl == nullptr || x == nullptr || w == nullptr || w_scale == nullptr || y == nullptr ||
-        (workspace == nullptr && int8_use_gemm(pl->ip)))
+        (workspace == nullptr && workspace_of(pl->ip).quantize != 0))
         return CONV_ERR_INVALID_ARG;
     if (x_dtype != CONV_F32 && x_dtype != CONV_BF16) return CONV_ERR_INVALID_ARG;
     for (const void* ptr : {x, w, static_cast<const void*>(w_scale), static_cast<const void*>(bias),
@@ -163,7 +164,7 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     p.w_scale = w_scale;
     p.bias = bias;
     p.y = y;
-    if (!int8_use_gemm(p))
+    if (!int8_use_gemm(p) && !int8_use_mid(p))
         return launched(launch_int8_few_quantize(p, x, x_dtype == CONV_BF16, static_cast<cudaStream_t>(stream)));
     const Workspace ws = workspace_of(p);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -171,7 +172,7 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     float* scale = reinterpret_cast<float*>(base + ws.scales);
     p.w_pitch = p.K;
     cudaError_t e = cudaSuccess;
-    if (p.K % 16 != 0) {
+    if (p.K % 16 != 0 && int8_use_gemm(p)) {
         e = launch_int8_layout(nullptr, nullptr, 0, p.w, base + ws.w, p.N, p.K, ws.pitch, pl->num_sms, st);
         p.w = base + ws.w;
         p.w_pitch = ws.pitch;
@@ -182,6 +183,7 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     p.x = base + ws.x;
     p.x_pitch = ws.pitch;
     p.x_scale = scale;
+    if (int8_use_mid(p)) return launched(launch_int8_mid(p, true, st));
     return launched(launch_int8_gemm(p, pl->num_sms, true, st));
 }
 

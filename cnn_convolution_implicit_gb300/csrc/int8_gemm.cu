@@ -97,16 +97,6 @@ struct Bars {
     int* abort;
 };
 
-// Four 8-bit integers to FP16.
-__device__ __forceinline__ uint2 to_half4(uint32_t v) {
-    const uint32_t u = v ^ 0x80808080u;
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);  // bytes 0, 1 below 0x64
-    uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));  // 1152
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
-    return make_uint2(lo, hi);
-}
-
 // Arrive on the pair leader's barrier.  What it announces is ordered by other means: operand
 // tiles by the proxy fence before it, tensor memory by tcgen05's own fences; it orders no memory
 // of its own.  With release at cluster scope it held its warp for ~1,800 clocks, three and a half

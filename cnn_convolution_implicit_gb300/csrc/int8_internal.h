@@ -24,8 +24,10 @@ struct Int8Params {
     void* y;
     unsigned* status;
 };
-// Whether a product runs on the tensor cores (else, with few rows, on the CUDA cores).
+// Whether a product runs in the tensor-core kernel of many rows, or in that of 9 to 32 (else on the CUDA
+// cores).
 bool int8_use_gemm(const Int8Params& p);
+bool int8_use_mid(const Int8Params& p);
 // Tensor-core kernel (int8_gemm.cu); whether its row and tile counts stay within 32 bits.
 bool int8_gemm_fits(const Int8Params& p);
 // Rows of x and w start on 16 bytes; after_layout: the kernel before it on the stream laid them out.
@@ -35,6 +37,8 @@ cudaError_t launch_int8_layout(const int8_t* x, int8_t* xr, long long x_rows, co
                                int K, int pitch, int num_sms, cudaStream_t stream);
 // Few rows (dense), from 8-bit x or straight from BF16 or FP32 x.
 cudaError_t launch_int8_few(const Int8Params& p, cudaStream_t stream);
+// 9 to 32 rows of x; after_quantise: x and its scales come from launch_quantize_rows just before.
+cudaError_t launch_int8_mid(const Int8Params& p, bool after_quantise, cudaStream_t stream);
 cudaError_t launch_int8_few_quantize(const Int8Params& p, const void* x, bool bf16, cudaStream_t stream);
 
 // Rows of x (BF16 or FP32) to 8 bits with one scale each; rows of q `pitch` bytes apart.

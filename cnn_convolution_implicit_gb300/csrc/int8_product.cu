@@ -1,4 +1,4 @@
-// int8_product.cu -- the 8-bit product with few rows (tokens):
+// int8_product.cu -- the 8-bit product with few rows (tokens), up to 8 and up to 32:
 //
 //   y[m][n] = act( x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k] + bias[n] )
 //
@@ -206,9 +206,118 @@ cudaError_t launch_few(const Int8Params& p, const T* x, cudaStream_t stream) {
     return launch_few<T, 8>(p, x, stream);
 }
 
+// ---------------------------------------------------------------- 9 to 32 rows
+// Still bound by reading w once, but too many products for the CUDA cores: FP16 MMAs of 16 x 8 x 16
+// on operands that go from memory to registers and from there to FP16, exact as in the
+// tensor-core kernel of many rows, whose 128-row tiles, shared-memory stages and launch cost more
+// than the bytes here (MID_FIGURE).
+//
+// A CTA takes 16 rows of w; its eight warps share K, 64 at a time.  Lane 4 g + q holds k = 16 q ..
+// 16 q + 15 of rows g of w and g, g + 8 of x: the MMA sums over k in any order, so its slots
+// (2 q, 2 q + 1, 2 q + 8, 2 q + 9) take the lane's four values of word j, for both operands alike.
+// The warps' sums meet in shared memory in one order.
+constexpr int kMidColumns = 16;
+
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 mid_item(const int8_t* base, int row, int rows, int pitch, int k, int K) {
+    if (row >= rows || k >= K) return make_uint4(0, 0, 0, 0);
+    const long long at = static_cast<long long>(row) * pitch + k;
+    if constexpr (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(base + at));
+    else return load_item(base, at, K - k < 16 ? K - k : 16, static_cast<long long>(rows) * pitch);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w)); }
+
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint2 a_lo, uint2 a_hi, uint2 b) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a_lo.x), "r"(a_hi.x), "r"(a_lo.y), "r"(a_hi.y), "r"(b.x), "r"(b.y));
+}
+
+// MT: 16-row tiles of x.
+template <int MT, bool ALIGNED>
+__global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int8Params p) {
+    constexpr int B = MT == 1 ? 4 : 2;  // steps of K whose loads are under way
+    __shared__ float2 parts[kFewWarps][MT * 16][kMidColumns / 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int n0 = blockIdx.x * kMidColumns;
+    float acc[MT][2][4] = {};
+    uint4 w[B][2];
+    const auto load_weights = [&](int k0) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                w[b][t] = mid_item<ALIGNED>(p.w, n0 + 8 * t + g, p.N, p.w_pitch, k0 + b * 64 * kFewWarps + 16 * q, p.K);
+    };
+    load_weights(64 * warp);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // x may come from the kernel before
+    for (int k0 = 64 * warp; k0 < p.K; k0 += B * 64 * kFewWarps) {
+        uint4 x[B][MT][2];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    x[b][m][h] = mid_item<ALIGNED>(p.x, 16 * m + 8 * h + g, p.M, p.x_pitch, k0 + b * 64 * kFewWarps + 16 * q, p.K);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint2 w0 = to_half4(word_of(w[b][0], j)), w1 = to_half4(word_of(w[b][1], j));
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint2 lo = to_half4(word_of(x[b][m][0], j)), hi = to_half4(word_of(x[b][m][1], j));
+                    mma_16x8x16(acc[m][0], lo, hi, w0);
+                    mma_16x8x16(acc[m][1], lo, hi, w1);
+                }
+            }
+        if (k0 + B * 64 * kFewWarps < p.K) load_weights(k0 + B * 64 * kFewWarps);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            parts[warp][16 * m + g][4 * t + q] = make_float2(acc[m][t][0], acc[m][t][1]);
+            parts[warp][16 * m + 8 + g][4 * t + q] = make_float2(acc[m][t][2], acc[m][t][3]);
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = threadIdx.x; i < MT * 16 * kMidColumns; i += kFewThreads) {
+        const int m = i / kMidColumns, n = n0 + i % kMidColumns;
+        if (m >= p.M || n >= p.N) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kFewWarps; ++k) sum += reinterpret_cast<const float*>(parts[k][m])[i % kMidColumns];
+        float v = fmaf(sum * __ldg(p.x_scale + m), __ldg(p.w_scale + n), p.bias ? __ldg(p.bias + n) : 0.0f);
+        if (p.act == CONV_ACT_RELU) v = activate<CONV_ACT_RELU>(v);
+        else if (p.act == CONV_ACT_SILU) v = activate<CONV_ACT_SILU>(v);
+        const long long o = static_cast<long long>(m) * p.N + n;
+        if (p.out_bf16) static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+        else static_cast<float*>(p.y)[o] = v;
+    }
+}
+
 }  // namespace
 
-bool int8_use_gemm(const Int8Params& p) { return p.M > 8; }
+bool int8_use_mid(const Int8Params& p) { return p.M > 8 && p.M <= 32; }
+bool int8_use_gemm(const Int8Params& p) { return p.M > 8 && !int8_use_mid(p); }
+
+cudaError_t launch_int8_mid(const Int8Params& p, bool after_quantise, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.N) + kMidColumns - 1) / kMidColumns));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the first loads of w overlap the kernel before
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_quantise ? 1 : 0;
+    const bool aligned = p.K % 16 == 0;  // of both operands, then
+    if (p.M <= 16) return cudaLaunchKernelEx(&cfg, aligned ? int8_mid_rows_kernel<1, true> : int8_mid_rows_kernel<1, false>, p);
+    return cudaLaunchKernelEx(&cfg, aligned ? int8_mid_rows_kernel<2, true> : int8_mid_rows_kernel<2, false>, p);
+}
 
 cudaError_t launch_int8_few(const Int8Params& p, cudaStream_t stream) { return launch_few<int8_t>(p, p.x, stream); }
 

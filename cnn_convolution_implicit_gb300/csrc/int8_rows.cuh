@@ -1,4 +1,4 @@
-// int8_rows.cuh -- loads from 8-bit matrices whose rows may start on any byte.
+// int8_rows.cuh -- loads from 8-bit matrices whose rows may start on any byte, and their values in FP16.
 #pragma once
 
 #include <cstdint>
@@ -102,5 +102,15 @@ private:
         return last_granule(base, g, total);
     }
 };
+
+// Four 8-bit integers to FP16.
+__device__ __forceinline__ uint2 to_half4(uint32_t v) {
+    const uint32_t u = v ^ 0x80808080u;
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);  // bytes 0, 1 below 0x64
+    uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));  // 1152
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+    return make_uint2(lo, hi);
+}
 
 }  // namespace convgb
