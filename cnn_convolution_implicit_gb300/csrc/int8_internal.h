@@ -24,7 +24,7 @@ struct Int8Params {
     void* y;
     unsigned* status;
 };
-// Whether a product runs in the tensor-core kernel of many rows, or in that of 9 to 32 (else on the CUDA
+// Whether a product runs in the tensor-core kernel of many rows, or in that of 5 to 64 (else on the CUDA
 // cores).
 bool int8_use_gemm(const Int8Params& p);
 bool int8_use_mid(const Int8Params& p);
@@ -37,7 +37,7 @@ cudaError_t launch_int8_layout(const int8_t* x, int8_t* xr, long long x_rows, co
                                int K, int pitch, int num_sms, cudaStream_t stream);
 // Few rows (dense), from 8-bit x or straight from BF16 or FP32 x.
 cudaError_t launch_int8_few(const Int8Params& p, cudaStream_t stream);
-// 9 to 32 rows of x; after_quantise: x and its scales come from launch_quantize_rows just before.
+// 5 to 64 rows of x; after_quantise: x and its scales come from launch_quantize_rows just before.
 cudaError_t launch_int8_mid(const Int8Params& p, bool after_quantise, cudaStream_t stream);
 cudaError_t launch_int8_few_quantize(const Int8Params& p, const void* x, bool bf16, cudaStream_t stream);
 

@@ -1,15 +1,15 @@
-// int8_product.cu -- the 8-bit product with few rows (tokens), up to 8 and up to 32:
+// int8_product.cu -- the 8-bit product with few rows (tokens), up to 4 and up to 64:
 //
 //   y[m][n] = act( x_scale[m] * w_scale[n] * sum_k x[m][k] * w[n][k] + bias[n] )
 //
-// Bound by reading w once: N * K bytes.  Every row of x of the call (up to 8) sits in
+// Bound by reading w once: N * K bytes.  Every row of x of the call (up to 4) sits in
 // shared memory, 8-bit; a warp takes two rows of w, each lane 16 bytes of each at a time
 // (both rows' loads for a whole chunk of K under way before the first is used), and adds
 // the products four at a time in 32-bit integers (dp4a), so the sum is exact for every K.
 // Two rows of w share each read of x from shared memory.
 //
 // One token, 4096 -> 4096: 10 us with cold caches and the launch (3.9 us a call in a graph, the
-// weights then in L2), floor 2.5; eight tokens 17: each row of x adds 16 bytes of shared memory
+// weights then in L2), floor 2.5; four tokens 13: each row of x adds 16 bytes of shared memory
 // read for every 32 of w.
 //
 // Rows of x that arrive as BF16 or FP32 are brought to 8 bits by every CTA for itself (amax,
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kFewThreads) int8_few_rows_kernel(const Int8Pa
 template <typename T, int M>
 cudaError_t launch_few(const Int8Params& p, const T* x, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.N) + kFewWarps * kFewRowsW - 1) / (kFewWarps * kFewRowsW));
-    const int smem = M * kFewChunk;  // 32 KB at most
+    const int smem = M * kFewChunk;  // 16 KB at most
     if (p.K % 16 == 0) int8_few_rows_kernel<T, M, true><<<grid, kFewThreads, smem, stream>>>(p, x);
     else int8_few_rows_kernel<T, M, false><<<grid, kFewThreads, smem, stream>>>(p, x);
     return cudaGetLastError();
@@ -202,15 +202,15 @@ template <typename T>
 cudaError_t launch_few(const Int8Params& p, const T* x, cudaStream_t stream) {
     if (p.M == 1) return launch_few<T, 1>(p, x, stream);
     if (p.M == 2) return launch_few<T, 2>(p, x, stream);
-    if (p.M <= 4) return launch_few<T, 4>(p, x, stream);
-    return launch_few<T, 8>(p, x, stream);
+    return launch_few<T, 4>(p, x, stream);
 }
 
-// ---------------------------------------------------------------- 9 to 32 rows
+// ---------------------------------------------------------------- 5 to 64 rows
 // Still bound by reading w once, but too many products for the CUDA cores: FP16 MMAs of 16 x 8 x 16
 // on operands that go from memory to registers and from there to FP16, exact as in the
 // tensor-core kernel of many rows, whose 128-row tiles, shared-memory stages and launch cost more
-// than the bytes here (MID_FIGURE).
+// than the bytes here: 16 x 4096 -> 4096 5.4 us a call in a graph against 14.9, 12 and 21 with cold caches
+// and the launch (floor 2.5); 16 x 16384 -> 4096 15 and 34, 32 x 1024 -> 1024 3.0 and 8.7.
 //
 // A CTA takes 16 rows of w; its eight warps share K, 64 at a time.  Lane 4 g + q holds k = 16 q ..
 // 16 q + 15 of rows g of w and g, g + 8 of x: the MMA sums over k in any order, so its slots
@@ -237,7 +237,8 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint2 a_lo, uint2 a_h
 // MT: 16-row tiles of x.
 template <int MT, bool ALIGNED>
 __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int8Params p) {
-    constexpr int B = MT == 1 ? 4 : 2;  // steps of K whose loads are under way
+    constexpr int B = 4, BX = MT == 1 ? 4 : (MT == 2 ? 2 : 1);  // steps of K whose loads of w and of x are under way
+    constexpr int kStep = 64 * kFewWarps;
     __shared__ float2 parts[kFewWarps][MT * 16][kMidColumns / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int n0 = blockIdx.x * kMidColumns;
@@ -247,33 +248,36 @@ __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int
 #pragma unroll
         for (int b = 0; b < B; ++b)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                w[b][t] = mid_item<ALIGNED>(p.w, n0 + 8 * t + g, p.N, p.w_pitch, k0 + b * 64 * kFewWarps + 16 * q, p.K);
+            for (int t = 0; t < 2; ++t) w[b][t] = mid_item<ALIGNED>(p.w, n0 + 8 * t + g, p.N, p.w_pitch, k0 + b * kStep + 16 * q, p.K);
     };
     load_weights(64 * warp);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // x may come from the kernel before
-    for (int k0 = 64 * warp; k0 < p.K; k0 += B * 64 * kFewWarps) {
-        uint4 x[B][MT][2];
+    for (int k0 = 64 * warp; k0 < p.K; k0 += B * kStep) {
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+        for (int b0 = 0; b0 < B; b0 += BX) {
+            if (b0 > 0 && k0 + b0 * kStep >= p.K) break;
+            uint4 x[BX][MT][2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int b = 0; b < BX; ++b)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    x[b][m][h] = mid_item<ALIGNED>(p.x, 16 * m + 8 * h + g, p.M, p.x_pitch, k0 + b * 64 * kFewWarps + 16 * q, p.K);
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+                    for (int h = 0; h < 2; ++h)
+                        x[b][m][h] = mid_item<ALIGNED>(p.x, 16 * m + 8 * h + g, p.M, p.x_pitch, k0 + (b0 + b) * kStep + 16 * q, p.K);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint2 w0 = to_half4(word_of(w[b][0], j)), w1 = to_half4(word_of(w[b][1], j));
+            for (int b = 0; b < BX; ++b)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const uint2 lo = to_half4(word_of(x[b][m][0], j)), hi = to_half4(word_of(x[b][m][1], j));
-                    mma_16x8x16(acc[m][0], lo, hi, w0);
-                    mma_16x8x16(acc[m][1], lo, hi, w1);
+                for (int j = 0; j < 4; ++j) {
+                    const uint2 w0 = to_half4(word_of(w[b0 + b][0], j)), w1 = to_half4(word_of(w[b0 + b][1], j));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint2 lo = to_half4(word_of(x[b][m][0], j)), hi = to_half4(word_of(x[b][m][1], j));
+                        mma_16x8x16(acc[m][0], lo, hi, w0);
+                        mma_16x8x16(acc[m][1], lo, hi, w1);
+                    }
                 }
-            }
-        if (k0 + B * 64 * kFewWarps < p.K) load_weights(k0 + B * 64 * kFewWarps);
+        }
+        if (k0 + B * kStep < p.K) load_weights(k0 + B * kStep);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -301,8 +305,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int
 
 }  // namespace
 
-bool int8_use_mid(const Int8Params& p) { return p.M > 8 && p.M <= 32; }
-bool int8_use_gemm(const Int8Params& p) { return p.M > 8 && !int8_use_mid(p); }
+// In a graph, 8-bit input, this kernel and the one beside it (CUDA cores up to 8 rows, 128-row tiles from 9): 5 x 4096 ->
+// 4096 5.0 and 6.6 us, 8 x 512 -> 512 2.3 and 5.7; 32 x 8192 -> 8192 24.6 and 34.9; 40 x 4096 -> 4096 9.8 and 15.6;
+// 64 x 1024 -> 1024 4.7 and 8.6, but 64 x 4096 -> 16384 43.5 and 33.0 and with cold caches 56 x 8192 -> 2048 34.8 and 26.6:
+// x is read again by every 16 columns.
+bool int8_use_mid(const Int8Params& p) {
+    const long long weights = static_cast<long long>(p.N) * p.K;
+    return p.M > 4 && (p.M <= 32 || (p.M <= 48 && weights <= 1LL << 24) || (p.M <= 64 && weights <= 1LL << 21));
+}
+bool int8_use_gemm(const Int8Params& p) { return p.M > 4 && !int8_use_mid(p); }
 
 cudaError_t launch_int8_mid(const Int8Params& p, bool after_quantise, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
@@ -315,8 +326,11 @@ cudaError_t launch_int8_mid(const Int8Params& p, bool after_quantise, cudaStream
     cfg.attrs = attr;
     cfg.numAttrs = after_quantise ? 1 : 0;
     const bool aligned = p.K % 16 == 0;  // of both operands, then
-    if (p.M <= 16) return cudaLaunchKernelEx(&cfg, aligned ? int8_mid_rows_kernel<1, true> : int8_mid_rows_kernel<1, false>, p);
-    return cudaLaunchKernelEx(&cfg, aligned ? int8_mid_rows_kernel<2, true> : int8_mid_rows_kernel<2, false>, p);
+    const auto run = [&](auto* whole, auto* any) { return cudaLaunchKernelEx(&cfg, aligned ? whole : any, p); };
+    if (p.M <= 16) return run(int8_mid_rows_kernel<1, true>, int8_mid_rows_kernel<1, false>);
+    if (p.M <= 32) return run(int8_mid_rows_kernel<2, true>, int8_mid_rows_kernel<2, false>);
+    if (p.M <= 48) return run(int8_mid_rows_kernel<3, true>, int8_mid_rows_kernel<3, false>);
+    return run(int8_mid_rows_kernel<4, true>, int8_mid_rows_kernel<4, false>);
 }
 
 cudaError_t launch_int8_few(const Int8Params& p, cudaStream_t stream) { return launch_few<int8_t>(p, p.x, stream); }

@@ -44,6 +44,25 @@ def test_product(size, out):
     assert cg.device_status() == 0
 
 
+# The kernel between few rows and many: each count of 16-row tiles, K shorter than its eight warps
+# share and longer than they hold, rows of either operand off 16 bytes.
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(5, 16, 16), (6, 33, 520), (8, 1000, 2064), (16, 15, 4112), (17, 48, 64), (32, 257, 2048), (33, 100, 530),
+                                  (48, 130, 1000), (49, 64, 96), (64, 129, 515), (64, 512, 512), (50, 2048, 2048)])
+def test_rows_between_few_and_many(size, out):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, xs, w, ws, bias = _inputs(M, N, K, 3 * M + N + 7 * K)
+    y = cg.int8_matmul(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), bias.cuda(), act="silu", out=out)
+    want, tol = ref.int8_product(x.numpy(), xs.numpy(), w.numpy(), ws.numpy(), bias.numpy(), "silu")
+    ref.check(_np(y), want, tol, out == "bf16", "y")
+    xf = torch.randn(M, K, generator=torch.Generator().manual_seed(M + K)).to(torch.bfloat16)
+    y = cg.int8_linear(xf.cuda(), w.cuda(), ws.cuda(), bias.cuda(), out="f32")
+    q, s = ref.quantize_rows(xf.float().numpy())
+    want, tol = ref.int8_product(q, s, w.numpy(), ws.numpy(), bias.numpy(), "none")
+    ref.check(_np(y), want, tol, False, "y")
+
+
 # Rows of y that start on 2, 4, 8 bytes in every tile shape; rows of x of every length class whose
 # vectors straddle 16 bytes.
 @pytest.mark.parametrize("out", ["bf16", "f32"])
