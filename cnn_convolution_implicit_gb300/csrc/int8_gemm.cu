@@ -39,7 +39,7 @@
 // 69 % of the card's measured BF16 matrix rate: with the converters' stores left out the same
 // kernel takes 174 us, so a fifth is shared memory's share (per K = 64 and SM of a pair: 16 KB
 // raw in, 16 KB out, 32 KB FP16 in, 32 KB to the MMA, 768 clocks at 128 bytes against 512 of MMA).
-// 200704 x 256 -> 512: 68 us, 56 % of the memory's rate over its 257 MB.  16 x 4096 -> 4096: 14 us in a graph.
+// 200704 x 256 -> 512: 68 us, 56 % of the memory's rate over its 257 MB.  256 x 4096 -> 4096: 23 us in a graph.
 //
 // PAIR: two SMs share a 256 x BN tile (tcgen05.mma.cta_group::2): each converts its own
 // 128 rows of x and BN / 2 rows of w.  Shared memory bounds this kernel (written by the
