@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const NormParam
 }
 
 // What the channels of a vector need: the forward pass's z = (x - mean) * a + beta.  load() takes
-// gamma and beta, set() the statistics.
+// gamma and beta, set() the statistics.  VEC = 1: the second lane of the pair, which holds no
+// channel, stays 0 through every activation, so that a pixel's largest magnitude does not see it.
 template <int VEC>
 struct Affine {
     static constexpr int H = (VEC + 1) / 2;
@@ -249,7 +250,7 @@ struct Affine {
     }
     template <typename F>
     __device__ __forceinline__ void set(int c, int cpg, F&& stats) {  // stats(channel): (mean, rstd)
-        if (cpg % VEC == 0) {  // the vector lies in one group
+        if (VEC > 1 && cpg % VEC == 0) {  // the vector lies in one group
             const float2 st = stats(c);
 #pragma unroll
             for (int i = 0; i < H; ++i) {

@@ -319,3 +319,23 @@ def test_binding_refusals():
     with pytest.raises(cg.ConvError) as e:
         plan.forward(flat[1:1025].view(2, 4, 4, 32), gamma, beta)  # 2 bytes off 16
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("shift", [10.0, -10.0])
+@pytest.mark.parametrize("shape", [(2, 3, 5, 1, 1), (1, 4, 4, 7, 1), (2, 3, 4, 7, 7), (3, 5, 3, 21, 3), (1, 40, 30, 21, 1)])
+def test_forward_int8_odd_channels_far_from_zero(shape, shift, act, dtype):
+    """Channels in single accesses: a pixel's scale comes from its own values alone, wherever the
+    mean lies (ten spreads from 0 here)."""
+    import cnn_convolution_implicit_gb300 as cg
+    N, H, W, C, G = shape
+    x, gamma, beta = _make(N, H, W, C, "f32", 9 * C + H, offset=0.0)
+    x = (x + shift).to(DT[dtype])
+    q, scale = cg.group_norm_int8(x.cuda(), G, gamma.cuda(), beta.cuda(), act=act)
+    want, tol = ref.norm_forward(_flat(x), G, _np(gamma), _np(beta), 1e-5, act)
+    want, tol = want.reshape(-1, C), tol.reshape(-1, C)
+    top, s, qs = np.abs(want).max(1), _np(scale), _np(q).reshape(-1, C)
+    assert np.all(np.abs(127.0 * s - top) <= tol.max(1) + 4 * ref.U32 * top)
+    assert np.all(np.abs(qs).max(1)[s > 0] == 127)
+    assert np.all(np.abs(qs * s[:, None] - want) <= 0.5 * s[:, None] * (1 + 128 * ref.U32 * 2) + tol)
