@@ -422,7 +422,7 @@ __device__ __forceinline__ void join_parts(const Int8Params& p, const float* par
             sum.z += v.z;
             sum.w += v.w;
         }
-        const float xs = __ldg(p.x_scale + m0 + row);
+        const float xs = load1_late(p.x_scale + m0 + row);
         const float in[4] = {sum.x, sum.y, sum.z, sum.w};
         const long long o = static_cast<long long>(m0 + row) * p.N + n;
 #pragma unroll
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if constexpr (PAIR) cluster_sync_all();  // the peer's barriers exist before anything signals them
     tc_fence_after();
     const uint32_t tmem = *b.tmem_slot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // rows laid out by the kernel before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // x, w or x's scales from the kernel before this one
 
     if (warp < kConverterWarps) {
         // ------------------------------------------------------------ converters
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             d.block_n = first;
             d.block_m = static_cast<int>(row0) - (lane >> 2);
 #pragma unroll
-            for (int i = 0; i < 2 * G; ++i) d.xs[i] = row0 + 8 * i < p.M ? __ldg(p.x_scale + row0 + 8 * i) : 0.0f;
+            for (int i = 0; i < 2 * G; ++i) d.xs[i] = row0 + 8 * i < p.M ? load1_late(p.x_scale + row0 + 8 * i) : 0.0f;
             const int blocks = left <= 0 ? 0 : (left >= kCols ? kCols / 32 : (left + 31) / 32);
             const int whole = left <= 0 ? 0 : (left >= kCols ? kCols / 32 : left / 32);
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {

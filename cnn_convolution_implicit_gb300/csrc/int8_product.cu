@@ -218,12 +218,12 @@ cudaError_t launch_few(const Int8Params& p, const T* x, cudaStream_t stream) {
 // The warps' sums meet in shared memory in one order.
 constexpr int kMidColumns = 16;
 
-template <bool ALIGNED>
+template <bool ALIGNED, bool LATE>
 __device__ __forceinline__ uint4 mid_item(const int8_t* base, int row, int rows, int pitch, int k, int K) {
     if (row >= rows || k >= K) return make_uint4(0, 0, 0, 0);
     const long long at = static_cast<long long>(row) * pitch + k;
-    if constexpr (ALIGNED) return __ldg(reinterpret_cast<const uint4*>(base + at));
-    else return load_item(base, at, K - k < 16 ? K - k : 16, static_cast<long long>(rows) * pitch);
+    if constexpr (ALIGNED) return load16<LATE>(reinterpret_cast<const uint4*>(base + at));
+    else return load_item<LATE>(base, at, K - k < 16 ? K - k : 16, static_cast<long long>(rows) * pitch);
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w)); }
@@ -248,10 +248,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int
 #pragma unroll
         for (int b = 0; b < B; ++b)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) w[b][t] = mid_item<ALIGNED>(p.w, n0 + 8 * t + g, p.N, p.w_pitch, k0 + b * kStep + 16 * q, p.K);
+            for (int t = 0; t < 2; ++t) w[b][t] = mid_item<ALIGNED, false>(p.w, n0 + 8 * t + g, p.N, p.w_pitch, k0 + b * kStep + 16 * q, p.K);
     };
     load_weights(64 * warp);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // x may come from the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // x and its scales may come from the kernel before
     for (int k0 = 64 * warp; k0 < p.K; k0 += B * kStep) {
 #pragma unroll
         for (int b0 = 0; b0 < B; b0 += BX) {
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        x[b][m][h] = mid_item<ALIGNED>(p.x, 16 * m + 8 * h + g, p.M, p.x_pitch, k0 + (b0 + b) * kStep + 16 * q, p.K);
+                        x[b][m][h] = mid_item<ALIGNED, true>(p.x, 16 * m + 8 * h + g, p.M, p.x_pitch, k0 + (b0 + b) * kStep + 16 * q, p.K);
 #pragma unroll
             for (int b = 0; b < BX; ++b)
 #pragma unroll
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < kFewWarps; ++k) sum += reinterpret_cast<const float*>(parts[k][m])[i % kMidColumns];
-        float v = fmaf(sum * __ldg(p.x_scale + m), __ldg(p.w_scale + n), p.bias ? __ldg(p.bias + n) : 0.0f);
+        float v = fmaf(sum * load1_late(p.x_scale + m), __ldg(p.w_scale + n), p.bias ? __ldg(p.bias + n) : 0.0f);
         if (p.act == CONV_ACT_RELU) v = activate<CONV_ACT_RELU>(v);
         else if (p.act == CONV_ACT_SILU) v = activate<CONV_ACT_SILU>(v);
         const long long o = static_cast<long long>(m) * p.N + n;

@@ -6,6 +6,24 @@
 
 namespace convgb {
 
+// Loads of an operand.  LATE: the kernel before this one, still running when this one starts
+// (programmatic launch), writes it.  The non-coherent path is only for memory that nothing writes
+// while the grid runs, and the compiler may move such a load across the wait for that kernel, so
+// LATE data takes ordinary loads that stay behind it.
+template <bool LATE>
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+    if constexpr (!LATE) return __ldg(p);
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float load1_late(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // 16 bytes of a row from byte `at` of a matrix of `total` bytes, zero from `len` on (1..16 bytes
 // are wanted): the one or two aligned granules that hold the bytes, shifted.  A granule that
 // the matrix ends in is read byte by byte, so nothing past its last byte is touched.
@@ -17,8 +35,9 @@ static __device__ __noinline__ uint4 last_granule(const int8_t* base, long long 
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+template <bool LATE>
 __device__ __forceinline__ uint4 granule(const int8_t* base, long long g, long long total) {
-    if ((g << 4) + 16 <= total) return __ldg(reinterpret_cast<const uint4*>(base) + g);
+    if ((g << 4) + 16 <= total) return load16<LATE>(reinterpret_cast<const uint4*>(base) + g);
     return last_granule(base, g, total);
 }
 
@@ -47,17 +66,18 @@ __device__ __forceinline__ uint4 first_bytes(uint4 v, int len) {  // zero from l
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+template <bool LATE = false>
 __device__ __forceinline__ uint4 load_item(const int8_t* base, long long at, int len, long long total) {
     const long long g = at >> 4;
     const int off = static_cast<int>(at & 15);
     uint4 a, b;
     if ((g << 4) + 32 <= total) {  // both lie in the matrix, wanted or not
         const uint4* from = reinterpret_cast<const uint4*>(base) + g;
-        a = __ldg(from);
-        b = __ldg(from + 1);
+        a = load16<LATE>(from);
+        b = load16<LATE>(from + 1);
     } else {
-        a = granule(base, g, total);
-        b = off + len > 16 ? granule(base, g + 1, total) : make_uint4(0, 0, 0, 0);
+        a = granule<LATE>(base, g, total);
+        b = off + len > 16 ? granule<LATE>(base, g + 1, total) : make_uint4(0, 0, 0, 0);
     }
     return first_bytes(shift_granules(a, b, off), len);
 }

@@ -301,3 +301,22 @@ def test_binding_refusals():
         cg.int8_matmul(x, xs, w, ws, out="f16")
     with pytest.raises(ValueError):
         cg.quantize_rows(torch.zeros(0, 5, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [(5, 4096, 4096), (16, 512, 8192), (32, 700, 8200), (48, 96, 1000), (300, 512, 256),
+                                  (65, 256, 16384), (2000, 600, 72), (129, 77, 515)])
+def test_linear_reads_what_its_quantiser_wrote(size, dtype):
+    """The product starts while its rows are still being quantised, into memory that holds those of
+    the call before: every call gives the bits of the two calls one after the other."""
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    _, _, w, ws, bias = (t.cuda() for t in _inputs(1, N, K, 12))
+    plan = cg.Int8MatmulPlan(M, N, K, out="f32")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    rows = [(torch.randn(M, K, device="cuda", generator=g) * 2.0 ** i).to(dtype) for i in range(8)]
+    want = [plan.forward(*cg.quantize_rows(x), w, ws, bias) for x in rows]
+    for _ in range(4):
+        got = [plan.forward_quantize(x, w, ws, bias) for x in rows]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert plan.device_status() == 0
