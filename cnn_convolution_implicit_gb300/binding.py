@@ -132,6 +132,20 @@ def device_status() -> int:
     return code.value
 
 
+def other_device(dev, current):
+    return ValueError("the tensors are on cuda:%d, but cuda:%d is current: make the plan and the call under "
+                      "torch.cuda.device(%d)" % (dev, current, dev))
+
+
+def _need_current(x):
+    """x's device has to be the current one: a plan is made for the current device, and the library
+    launches there (and refuses a plan of another)."""
+    import torch
+    current = torch.cuda.current_device()
+    if x.get_device() != current:
+        raise other_device(x.get_device(), current)
+
+
 def _plan_status(fn, plan, stream, name) -> int:
     import torch
     if stream is None:
@@ -229,6 +243,9 @@ class ConvPlan:
         dt = torch.bfloat16 if self.dtype == "bf16" else torch.float32
         if not (x.is_cuda and w.is_cuda):
             raise ValueError("x and w must be CUDA tensors")
+        if any(t is not None and t.get_device() != x.get_device() for t in (w, bias if self.bias else None, scale, y)):
+            raise ValueError("x, w, bias, scale and y must be on one device")
+        _need_current(x)
         if x.dtype != dt or w.dtype != dt:
             raise ValueError("x and w must be %s" % dt)
         if tuple(x.shape) != (N, H, W, C_in) or not x.is_contiguous():
@@ -321,8 +338,11 @@ class BlockPlan:
         def need(t, name, shape, dtype):
             if t is None or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("%s must be a contiguous CUDA %s tensor of shape %s" % (name, dtype, shape))
+            if t.get_device() != x.get_device():
+                raise ValueError("%s must be on x's device" % name)
 
         need(x, "x", (N, H, W, C), torch.float32)
+        _need_current(x)
         need(w_dw, "w_dw", (C, K, K), torch.float32)
         need(w_pw, "w_pw", (C_out, C), torch.bfloat16)
         for t, name, n in ((dw_scale, "dw_scale", C), (dw_bias, "dw_bias", C), (pw_scale, "pw_scale", C_out),
@@ -363,6 +383,7 @@ def measure_mma_rate(iters: int = 1 << 16, device=None):
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
     cycles = torch.zeros(sms, dtype=torch.int64, device=dev)
+    _need_current(cycles)
     stream = torch.cuda.current_stream(dev)
     st = L.conv_measure_mma_rate(int(iters), ctypes.c_void_p(cycles.data_ptr()), sms,
                                  ctypes.c_void_p(stream.cuda_stream))
@@ -384,6 +405,7 @@ def check_wait_timeout(limit_ns: int, device=None):
     L = lib()
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
     elapsed = torch.zeros(1, dtype=torch.int64, device=dev)
+    _need_current(elapsed)
     stream = torch.cuda.current_stream(dev)
     st = L.conv_check_wait_timeout(int(limit_ns), ctypes.c_void_p(elapsed.data_ptr()),
                                    ctypes.c_void_p(stream.cuda_stream))
@@ -405,6 +427,8 @@ def conv2d(x, w, bias=None, stride=1, padding=0, dilation=1, groups=1, relu=Fals
            bias is not None, relu, out_bf16)
     plan = _plan_cache.get(key)
     if plan is None:
+        if x.is_cuda:
+            _need_current(x)
         plan = ConvPlan(N, C_in, H, W, C_out, Kh, Kw, stride, padding, dilation, groups, dtype,
                         bias is not None, relu, out_bf16)
         _plan_cache[key] = plan

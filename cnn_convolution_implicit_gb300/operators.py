@@ -19,13 +19,15 @@ _DTYPES = {"f32": CONV_F32, "bf16": CONV_BF16}
 # torch), and what every call takes from it.
 _t = None
 _raw_stream = None
+_current_device = None
 
 
 def _torch():
-    global _t, _raw_stream
+    global _t, _raw_stream, _current_device
     if _t is None:
         import torch
         _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch._C._cuda_getDevice
         _t = torch
     return _t
 
@@ -38,6 +40,17 @@ def _choice(value, table, name):
     if value not in table:
         raise ValueError("%s must be one of %s, not %r" % (name, ", ".join(sorted(table)), value))
     return table[value]
+
+
+def _device_of(x):
+    """x's CUDA device, which has to be the current one: a plan is made for the current device, and
+    the library launches there (and refuses a plan of another)."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a CUDA tensor")
+    if dev != _current_device():
+        raise binding.other_device(dev, _current_device())
+    return dev
 
 
 def _need(t, name, shape, dtype, dev):
@@ -100,9 +113,7 @@ class GroupNormPlan:
 
     def _inputs(self, x, gamma, beta, stats):
         """Checks them; returns x's device."""
-        dev = x.get_device()
-        if dev < 0:
-            raise ValueError("x must be a CUDA tensor")
+        dev = _device_of(x)
         _need(x, "x", self.shape, self.torch_dtype, dev)
         if gamma is not None:
             _need(gamma, "gamma", self._channels, _t.float32, dev)
@@ -219,9 +230,7 @@ class Int8MatmulPlan:
 
     def _operands(self, x, w, w_scale, bias, y):
         """Checks all but x's type; returns x's device."""
-        dev = x.get_device()
-        if dev < 0:
-            raise ValueError("x must be a CUDA tensor")
+        dev = _device_of(x)
         _need(x, "x", self._x, x.dtype, dev)
         _need(w, "w", self._w, _t.int8, dev)
         _need(w_scale, "w_scale", self._cols, _t.float32, dev)
@@ -284,6 +293,7 @@ def _norm_plan(x, groups, eps, act):
         _need_any(x, "x", (torch.bfloat16, torch.float32))
         if x.dim() != 4:
             raise ValueError("x must be an NHWC tensor [N][H][W][C]")
+        _device_of(x)
         N, H, W, C = x.shape
         plan = _norm_plans[key] = GroupNormPlan(N, C, H, W, groups, "bf16" if x.dtype == torch.bfloat16 else "f32",
                                                 eps, act)
@@ -292,25 +302,34 @@ def _norm_plan(x, groups, eps, act):
 
 def group_norm(x, groups, gamma=None, beta=None, eps=1e-5, act="none", y=None, stats=None, stream=None):
     """act((x - mean) * rstd * gamma + beta) over each image's groups of channels; x NHWC."""
-    return _norm_plan(x, groups, eps, act).forward(x, gamma, beta, y, stats, stream)
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return group_norm(x, groups, gamma, beta, eps, act, y, stats)
+    return _norm_plan(x, groups, eps, act).forward(x, gamma, beta, y, stats)
 
 
 def group_norm_int8(x, groups, gamma=None, beta=None, eps=1e-5, act="none", stats=None, stream=None):
     """(q, scale): group_norm's result as int8 with one FP32 scale per pixel [N*H*W]."""
-    return _norm_plan(x, groups, eps, act).forward_int8(x, gamma, beta, stats=stats, stream=stream)
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return group_norm_int8(x, groups, gamma, beta, eps, act, stats)
+    return _norm_plan(x, groups, eps, act).forward_int8(x, gamma, beta, stats=stats)
 
 
 def group_norm_backward(dy, x, stats, groups, gamma=None, beta=None, eps=1e-5, act="none", stream=None):
     """(dx, dgamma, dbeta) of group_norm from its input and the stats it wrote."""
-    return _norm_plan(x, groups, eps, act).backward(dy, x, stats, gamma, beta, stream=stream)
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return group_norm_backward(dy, x, stats, groups, gamma, beta, eps, act)
+    return _norm_plan(x, groups, eps, act).backward(dy, x, stats, gamma, beta)
 
 
 def _int8_plan(x, w, act, out):
     key = (x.shape, w.shape, x.get_device(), out, act)
     plan = _int8_plans.get(key)
     if plan is None:
-        if not x.is_cuda:
-            raise ValueError("x must be a CUDA tensor")
+        _torch()
+        _device_of(x)
         if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
             raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
         N, K = w.shape
@@ -321,14 +340,20 @@ def _int8_plan(x, w, act, out):
 def int8_matmul(x, x_scale, w, w_scale, bias=None, act="none", out="bf16", stream=None):
     """x int8 [..., K] (rows or NHWC pixels) with x_scale, one FP32 scale per row in row order,
     times w int8 [N][K] with w_scale [N]: [..., N] in ``out`` ("bf16" or "f32")."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return int8_matmul(x, x_scale, w, w_scale, bias, act, out)
     if x_scale.dim() != 1:
         x_scale = x_scale.reshape(-1)
-    return _int8_plan(x, w, act, out).forward(x, x_scale, w, w_scale, bias, stream=stream)
+    return _int8_plan(x, w, act, out).forward(x, x_scale, w, w_scale, bias)
 
 
 def int8_linear(x, w, w_scale, bias=None, act="none", out="bf16", stream=None):
     """x BF16 or FP32 [..., K], its rows brought to 8 bits in the call, times w int8 [N][K]."""
-    return _int8_plan(x, w, act, out).forward_quantize(x, w, w_scale, bias, stream=stream)
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return int8_linear(x, w, w_scale, bias, act, out)
+    return _int8_plan(x, w, act, out).forward_quantize(x, w, w_scale, bias)
 
 
 def quantize_rows(x, stream=None):
@@ -342,7 +367,7 @@ def quantize_rows(x, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return quantize_rows(x)
-    dev = x.get_device()
+    dev = _device_of(x)
     q = torch.empty(x.shape, dtype=torch.int8, device=dev)
     scale = torch.empty(M, dtype=torch.float32, device=dev)
     _check(lib().conv_quantize_rows(x.data_ptr(), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, M, K,
