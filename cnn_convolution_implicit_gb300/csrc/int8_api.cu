@@ -13,7 +13,7 @@ struct conv_int8_plan {
     Int8Params ip;
     int device;
     int num_sms;
-    int status_slot;  // index of the plan's own status word, -1: the library-wide word
+    int status_slot;  // index of the plan's own status word, -1: the library-wide word, or none
 };
 
 namespace {
@@ -96,7 +96,8 @@ conv_status conv_int8_plan_create(conv_int8_plan** out, int M, int N, int K, con
         pl->num_sms = 152;
     } else if (cudaGetDevice(&pl->device) != cudaSuccess ||
                cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess ||
-               acquire_status_word(pl->device, &p.status, &pl->status_slot) != cudaSuccess) {
+               // the kernels of few rows wait for nothing: no word of the pool for them
+               (int8_use_gemm(p) && acquire_status_word(pl->device, &p.status, &pl->status_slot) != cudaSuccess)) {
         cudaGetLastError();
         delete pl;
         return CONV_ERR_CUDA;
@@ -191,6 +192,11 @@ conv_status conv_int8_plan_device_status(const conv_int8_plan* p, void* stream, 
     if (p == nullptr || code == nullptr) return CONV_ERR_INVALID_ARG;
     *code = 0;
     if (p->device < 0) return CONV_ERR_CUDA;  // host-only plan
+    if (p->ip.status == nullptr) {  // no kernel of the plan writes one: clean, once the stream is done
+        const conv_status s = check_device(p);
+        if (s != CONV_OK) return s;
+        return launched(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+    }
     return read_status_word(p->device, p->ip.status, stream, code);
 }
 

@@ -482,7 +482,8 @@ conv_status conv_int8_forward_quantize(conv_int8_plan *p, const void *x, conv_dt
                                        const float *w_scale, const float *bias, void *y, void *workspace,
                                        void *stream);
 
-/* Status word of the plan (waits that gave up): the contract of conv_plan_device_status. */
+/* Status word of the plan (waits that gave up): the contract of conv_plan_device_status.  Plans of few
+ * rows run kernels without waits: they take no word of the 1,024 and read 0 when the stream is done. */
 conv_status conv_int8_plan_device_status(const conv_int8_plan *p, void *stream, int *code);
 
 /* Free the plan: the contract of conv_plan_destroy.  NULL is accepted. */

@@ -320,3 +320,26 @@ def test_linear_reads_what_its_quantiser_wrote(size, dtype):
         got = [plan.forward_quantize(x, w, ws, bias) for x in rows]
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert plan.device_status() == 0
+
+
+def test_plans_of_few_rows_take_no_status_word():
+    """The kernels of few rows have no waits: however many such plans are alive, a convolution's plan
+    made after them has a word of its own, and theirs read 0 without touching the library's."""
+    import ctypes
+    import gc
+    import cnn_convolution_implicit_gb300 as cg
+    from cnn_convolution_implicit_gb300 import binding, operators
+    binding._plan_cache.clear()  # plans other tests left alive hold words
+    operators._int8_plans.clear()
+    gc.collect()
+    assert cg.device_status() == 0
+    few = [cg.Int8MatmulPlan(m, 8, 16) for m in (1, 4, 5, 32) for _ in range(300)]
+    own, many = cg.ConvPlan(1, 8, 8, 8, 8, 3, 3, 1, 1, 1, 1, "bf16"), cg.Int8MatmulPlan(400, 8, 16)
+    elapsed = torch.zeros(1, dtype=torch.int64, device="cuda")
+    stream = torch.cuda.current_stream()
+    assert cg.lib().conv_check_wait_timeout(1_000_000, ctypes.c_void_p(elapsed.data_ptr()),
+                                            ctypes.c_void_p(stream.cuda_stream)) == 0
+    assert own.device_status() == 0 and many.device_status() == 0
+    assert all(few[i].device_status() == 0 for i in range(0, len(few), 100))
+    assert cg.device_status() == 2 | 4  # the library's word, untouched by the reads above
+    assert cg.device_status() == 0
