@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from collections import OrderedDict
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libconv.so")
@@ -371,7 +372,43 @@ class BlockPlan:
                             "conv_block_plan_device_status")
 
 
-_plan_cache = {}
+class PlanCache:
+    """Plans of the functional forms, by shape: the ``limit`` used last.  A dropped plan is closed when
+    its last user lets go of it.  (Plans hold status words of a pool of 1,024: shapes that vary,
+    token counts above all, must not use it up.)"""
+
+    def __init__(self, limit=256):
+        self.limit = limit
+        self._plans = OrderedDict()
+        self._lock = threading.Lock()
+
+    def get(self, key):
+        with self._lock:
+            plan = self._plans.get(key)
+            if plan is not None:
+                self._plans.move_to_end(key)
+            return plan
+
+    def put(self, key, plan):
+        """Keeps ``plan`` and returns it; the plan used longest ago makes room."""
+        dropped = None
+        with self._lock:
+            self._plans[key] = plan
+            if len(self._plans) > self.limit:
+                dropped = self._plans.popitem(last=False)
+        del dropped  # closed, if at all, outside the lock
+        return plan
+
+    def clear(self):
+        with self._lock:
+            plans, self._plans = self._plans, OrderedDict()
+        plans.clear()
+
+    def __len__(self):
+        return len(self._plans)
+
+
+_plan_cache = PlanCache()
 
 
 def measure_mma_rate(iters: int = 1 << 16, device=None):
@@ -429,7 +466,6 @@ def conv2d(x, w, bias=None, stride=1, padding=0, dilation=1, groups=1, relu=Fals
     if plan is None:
         if x.is_cuda:
             _need_current(x)
-        plan = ConvPlan(N, C_in, H, W, C_out, Kh, Kw, stride, padding, dilation, groups, dtype,
-                        bias is not None, relu, out_bf16)
-        _plan_cache[key] = plan
+        plan = _plan_cache.put(key, ConvPlan(N, C_in, H, W, C_out, Kh, Kw, stride, padding, dilation, groups, dtype,
+                                             bias is not None, relu, out_bf16))
     return plan.forward(x, w, bias, y=y, stream=stream)

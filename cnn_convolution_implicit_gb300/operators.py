@@ -281,8 +281,8 @@ class Int8MatmulPlan:
 
 
 # ---------------------------------------------------------------- functional forms
-_norm_plans = {}
-_int8_plans = {}
+_norm_plans = binding.PlanCache()
+_int8_plans = binding.PlanCache()
 
 
 def _norm_plan(x, groups, eps, act):
@@ -295,8 +295,8 @@ def _norm_plan(x, groups, eps, act):
             raise ValueError("x must be an NHWC tensor [N][H][W][C]")
         _device_of(x)
         N, H, W, C = x.shape
-        plan = _norm_plans[key] = GroupNormPlan(N, C, H, W, groups, "bf16" if x.dtype == torch.bfloat16 else "f32",
-                                                eps, act)
+        plan = _norm_plans.put(key, GroupNormPlan(N, C, H, W, groups, "bf16" if x.dtype == torch.bfloat16 else "f32",
+                                                  eps, act))
     return plan
 
 
@@ -333,7 +333,7 @@ def _int8_plan(x, w, act, out):
         if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
             raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
         N, K = w.shape
-        plan = _int8_plans[key] = Int8MatmulPlan(x.numel() // K if K else 0, N, K, out, act, x.shape)
+        plan = _int8_plans.put(key, Int8MatmulPlan(x.numel() // K if K else 0, N, K, out, act, x.shape))
     return plan
 
 

@@ -343,3 +343,24 @@ def test_plans_of_few_rows_take_no_status_word():
     assert all(few[i].device_status() == 0 for i in range(0, len(few), 100))
     assert cg.device_status() == 2 | 4  # the library's word, untouched by the reads above
     assert cg.device_status() == 0
+
+
+def test_many_row_counts_leave_status_words():
+    """Row counts that vary, as token counts do: the functional forms' plans stay few, a convolution's
+    plan made after them has a status word of its own, and a shape that fell out comes back."""
+    import ctypes
+    import cnn_convolution_implicit_gb300 as cg
+    from cnn_convolution_implicit_gb300 import binding, operators
+    assert cg.device_status() == 0
+    x, xs, w, ws, bias = (t.cuda() for t in _inputs(1400, 8, 16, 3))
+    first = cg.int8_matmul(x[:100], xs[:100], w, ws, bias)
+    for m in range(100, 1400):
+        cg.int8_matmul(x[:m], xs[:m], w, ws, bias)
+    assert len(operators._int8_plans) <= operators._int8_plans.limit
+    own = cg.ConvPlan(1, 8, 8, 8, 8, 3, 3, 1, 1, 1, 1, "bf16")
+    elapsed = torch.zeros(1, dtype=torch.int64, device="cuda")
+    assert cg.lib().conv_check_wait_timeout(1_000_000, ctypes.c_void_p(elapsed.data_ptr()),
+                                            ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    assert own.device_status() == 0 and cg.device_status() == 2 | 4 and cg.device_status() == 0
+    assert torch.equal(cg.int8_matmul(x[:100], xs[:100], w, ws, bias), first)
+    assert len(binding._plan_cache) <= binding._plan_cache.limit
