@@ -41,6 +41,25 @@ namespace convgb {
 namespace {
 std::mutex g_slot_mutex;
 bool g_slot_used[kMaxStatusDevices][kStatusSlots];
+bool g_slot_had_owner[kMaxStatusDevices][kStatusSlots];  // may hold that plan's bits
+
+// Clears a word on a stream of its own and waits for it: the default stream would wait for work on
+// others, and may not be touched while a stream that follows it is being captured.
+cudaError_t clear_status_word(unsigned* word) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // this stream is in no capture
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    cudaStream_t st = nullptr;
+    e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+    if (e == cudaSuccess) {
+        e = cudaMemsetAsync(word, 0, sizeof(unsigned), st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+        const cudaError_t d = cudaStreamDestroy(st);
+        if (e == cudaSuccess) e = d;
+    }
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    return e == cudaSuccess ? back : e;
+}
 }  // namespace
 
 cudaError_t acquire_status_word(int device, unsigned** word, int* slot) {
@@ -48,18 +67,20 @@ cudaError_t acquire_status_word(int device, unsigned** word, int* slot) {
     cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_conv_status_word);
     if (e != cudaSuccess || device < 0 || device >= kMaxStatusDevices) return e;
     int idx = -1;
+    bool had_owner = false;
     {
         std::lock_guard<std::mutex> lock(g_slot_mutex);
         for (int i = 0; i < kStatusSlots && idx < 0; ++i)
             if (!g_slot_used[device][i]) {
                 g_slot_used[device][i] = true;
+                had_owner = g_slot_had_owner[device][i];
                 idx = i;
             }
     }
     if (idx < 0) return cudaSuccess;  // every word is taken: share the library-wide one
     unsigned* base = nullptr;
     e = cudaGetSymbolAddress(reinterpret_cast<void**>(&base), g_conv_status_slots);
-    if (e == cudaSuccess) e = cudaMemset(base + idx, 0, sizeof(unsigned));  // a previous owner's bits
+    if (e == cudaSuccess && had_owner) e = clear_status_word(base + idx);
     if (e != cudaSuccess) {
         release_status_word(device, idx);
         return e;
@@ -73,6 +94,7 @@ void release_status_word(int device, int slot) {
     if (slot < 0 || device < 0 || device >= kMaxStatusDevices) return;
     std::lock_guard<std::mutex> lock(g_slot_mutex);
     g_slot_used[device][slot] = false;
+    g_slot_had_owner[device][slot] = true;
 }
 }  // namespace convgb
 

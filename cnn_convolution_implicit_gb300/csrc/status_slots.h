@@ -13,8 +13,9 @@
 
 namespace convgb {
 
-// Take a free word on `device` and clear it (a device memset on the default
-// stream).  On success *word is its device address and *slot its index; with
+// Take a free word on `device`, cleared of an earlier owner's bits (on a stream of
+// its own: the default stream is not touched, so plans can be made during a stream
+// capture).  On success *word is its device address and *slot its index; with
 // none free, *slot = -1 and *word is the shared word.  Returns the first CUDA
 // error met.
 cudaError_t acquire_status_word(int device, unsigned** word, int* slot);

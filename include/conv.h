@@ -200,8 +200,9 @@ conv_status conv_device_status(int *code);
 
 /*
  * Each plan (conv_plan and conv_block_plan) takes its own device status word at
- * creation, from a fixed array of 1,024 per device (no allocation: creation clears
- * the word with a memset on the default stream); when all are taken it shares the
+ * creation, from a fixed array of 1,024 per device (no allocation; a word that had an
+ * owner before is cleared on a stream of its own, waited for, so creation leaves the
+ * default stream alone and may run during a stream capture); when all are taken it shares the
  * library-wide word.  This reads and clears the plan's word in the order of
  * `stream` (after the work queued on it, then waits for the stream only, not the
  * device): *code receives the bits of the plan's kernels whose waits gave up.

@@ -61,3 +61,37 @@ def test_block_forward_replays_in_a_cuda_graph():
     torch.cuda.synchronize()
     assert device_status() == 0
     assert torch.equal(y, y_eager)
+
+
+@pytest.mark.parametrize("call", ["conv2d", "int8_matmul", "group_norm"])
+def test_first_call_of_a_shape_inside_a_capture(call):
+    """The functional forms make their plan in the call: also while a stream that waits for the
+    default stream (an ordinary cudaStreamCreate stream) is being captured, with a status word that
+    had an owner before."""
+    import ctypes
+    import gc
+    import cnn_convolution_implicit_gb300 as cg
+    from cnn_convolution_implicit_gb300 import binding, operators
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, 9, 21, 64, device="cuda", generator=gen).to(torch.bfloat16)
+    w = torch.randn(32, 3, 3, 64, device="cuda", generator=gen).to(torch.bfloat16)
+    q, s = cg.quantize_rows(x)
+    qw, sw = cg.quantize_rows(w[:, 0, 0].contiguous())
+    run = {"conv2d": lambda: cg.conv2d(x, w), "int8_matmul": lambda: cg.int8_matmul(q, s, qw, sw),
+           "group_norm": lambda: cg.group_norm(x, 8)}[call]
+    want = run()
+    torch.cuda.synchronize()
+    for cache in (binding._plan_cache, operators._norm_plans, operators._int8_plans):
+        cache.clear()  # their words go back to the pool: the next plan takes a used one
+    gc.collect()
+    handle = ctypes.c_void_p()
+    rt = torch.cuda.cudart()
+    assert int(rt.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.ExternalStream(handle.value)):
+        y = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    del graph
+    assert int(rt.cudaStreamDestroy(handle.value)) == 0
