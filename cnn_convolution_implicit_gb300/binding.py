@@ -31,7 +31,7 @@ EXPORTS = ("conv_plan_create", "conv_plan_output_shape", "conv_plan_info", "conv
            "conv_plan_gemm_config", "conv_plan_device_status", "conv_block_plan_device_status",
            "conv_group_norm_plan_create", "conv_group_norm_workspace", "conv_group_norm_forward",
            "conv_group_norm_forward_int8", "conv_group_norm_backward", "conv_group_norm_plan_destroy",
-           "conv_int8_plan_create", "conv_int8_forward", "conv_int8_workspace", "conv_int8_forward_quantize",
+           "conv_int8_plan_create", "conv_int8_plan_info", "conv_int8_forward", "conv_int8_workspace", "conv_int8_forward_quantize",
            "conv_int8_plan_device_status", "conv_int8_plan_destroy", "conv_quantize_rows")
 CONV_BLOCK_DW_RELU, CONV_BLOCK_PW_RELU = 1, 2
 
@@ -111,6 +111,7 @@ def lib():
             L.conv_group_norm_backward.argtypes = [vp] * 11
             L.conv_group_norm_plan_destroy.argtypes = [vp]
             L.conv_int8_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 5
+            L.conv_int8_plan_info.argtypes = [vp] + [ctypes.POINTER(c_int)] * 4
             L.conv_int8_forward.argtypes = [vp] * 9
             L.conv_int8_workspace.argtypes = [vp, ctypes.POINTER(c_ull), ctypes.POINTER(c_ull)]
             L.conv_int8_forward_quantize.argtypes = [vp, vp, c_int] + [vp] * 6

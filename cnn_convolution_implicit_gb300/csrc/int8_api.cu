@@ -188,6 +188,17 @@ conv_status conv_int8_forward_quantize(conv_int8_plan* pl, const void* x, conv_d
     return launched(launch_int8_gemm(p, pl->num_sms, true, st));
 }
 
+conv_status conv_int8_plan_info(const conv_int8_plan* p, int* kernel, int* tile_rows, int* tile_columns, int* splits) {
+    if (p == nullptr) return CONV_ERR_INVALID_ARG;
+    const bool gemm = int8_use_gemm(p->ip);
+    const Int8Tile t = gemm ? int8_pick_tile(p->ip, p->num_sms) : Int8Tile();
+    if (kernel) *kernel = gemm ? CONV_INT8_TILES : (int8_use_mid(p->ip) ? CONV_INT8_MID_ROWS : CONV_INT8_FEW_ROWS);
+    if (tile_rows) *tile_rows = t.rows;
+    if (tile_columns) *tile_columns = t.columns;
+    if (splits) *splits = t.splits;
+    return CONV_OK;
+}
+
 conv_status conv_int8_plan_device_status(const conv_int8_plan* p, void* stream, int* code) {
     if (p == nullptr || code == nullptr) return CONV_ERR_INVALID_ARG;
     *code = 0;

@@ -861,12 +861,11 @@ int clusters_at_a_time(int num_sms, int ctas) {
 }  // namespace
 
 // The tile shape and split of K that cost least by those figures.
-cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_layout, cudaStream_t stream) {
-    Int8Params p = given;
+Int8Tile int8_pick_tile(const Int8Params& p, int num_sms) {
     const long long steps = (p.K + kStepK - 1) / kStepK;
     const bool on_16 = rows_on_16(p);
     double best = 0.0;
-    int tile = -1;
+    Int8Tile pick = {};
     for (int i = 0; i < 4; ++i) {
         const Tile& t = kTiles[i];
         const long long units = (static_cast<long long>(p.M) + t.rows - 1) / t.rows * ((p.N + t.columns - 1) / t.columns);
@@ -877,16 +876,22 @@ cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_la
             const double least = on_16 ? t.least : t.off_least;
             const double cost = t.launch + static_cast<double>((units + at_a_time - 1) / at_a_time) * (each > least ? each : least) +
                                 (splits > 1 ? t.join : 0.0);
-            if (tile < 0 || cost < best) {
+            if (pick.rows == 0 || cost < best) {
                 best = cost;
-                tile = i;
-                p.splits = splits;
+                pick = {t.rows, t.columns, splits};
             }
         }
     }
-    if (tile == 3) return launch_variant<true, 256>(p, num_sms, after_layout, stream);
-    if (tile == 2) return launch_variant<false, 128>(p, num_sms, after_layout, stream);
-    if (tile == 1) return launch_variant<false, 64>(p, num_sms, after_layout, stream);
+    return pick;
+}
+
+cudaError_t launch_int8_gemm(const Int8Params& given, int num_sms, bool after_layout, cudaStream_t stream) {
+    Int8Params p = given;
+    const Int8Tile tile = int8_pick_tile(p, num_sms);
+    p.splits = tile.splits;
+    if (tile.columns == 256) return launch_variant<true, 256>(p, num_sms, after_layout, stream);
+    if (tile.columns == 128) return launch_variant<false, 128>(p, num_sms, after_layout, stream);
+    if (tile.columns == 64) return launch_variant<false, 64>(p, num_sms, after_layout, stream);
     return launch_variant<false, 32>(p, num_sms, after_layout, stream);
 }
 

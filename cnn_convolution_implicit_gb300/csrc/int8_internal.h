@@ -28,6 +28,12 @@ struct Int8Params {
 // cores).
 bool int8_use_gemm(const Int8Params& p);
 bool int8_use_mid(const Int8Params& p);
+// The tile of the many-row kernel: rows of x and columns (256 x 256 on a pair of SMs), and CTAs that
+// share its K.
+struct Int8Tile {
+    int rows, columns, splits;
+};
+Int8Tile int8_pick_tile(const Int8Params& p, int num_sms);
 // Tensor-core kernel (int8_gemm.cu); whether its row and tile counts stay within 32 bits.
 bool int8_gemm_fits(const Int8Params& p);
 // Rows of x and w start on 16 bytes; after_layout: the kernel before it on the stream laid them out.

@@ -13,6 +13,7 @@ from . import binding
 from .binding import CONV_BF16, CONV_F32, ConvError, _plan_status, lib
 
 ACTS = {"none": 0, "relu": 1, "silu": 2}
+INT8_KERNELS = {0: "few_rows", 1: "mid_rows", 2: "tiles"}
 _DTYPES = {"f32": CONV_F32, "bf16": CONV_BF16}
 
 # torch, imported with the first plan or call (as in binding.py, importing the package needs no
@@ -213,6 +214,10 @@ class Int8MatmulPlan:
             raise ValueError("x_shape must hold %d rows of %d" % (M, K))
         self._w, self._y = torch.Size((N, K)), torch.Size(self._x[:-1] + (N,))
         self._rows, self._cols = torch.Size((M,)), torch.Size((N,))
+        info = [ctypes.c_int() for _ in range(4)]
+        _check(L.conv_int8_plan_info(h, *[ctypes.byref(v) for v in info]), "conv_int8_plan_info")
+        self.kernel = INT8_KERNELS[info[0].value]
+        self.tile = tuple(v.value for v in info[1:])  # rows, columns, CTAs that share its K ("tiles" alone)
         a, b = ctypes.c_ulonglong(), ctypes.c_ulonglong()
         _check(L.conv_int8_workspace(h, ctypes.byref(a), ctypes.byref(b)), "conv_int8_workspace")
         self.workspace_bytes = {"forward": a.value, "forward_quantize": b.value}

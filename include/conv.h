@@ -483,6 +483,15 @@ conv_status conv_int8_forward_quantize(conv_int8_plan *p, const void *x, conv_dt
                                        const float *w_scale, const float *bias, void *y, void *workspace,
                                        void *stream);
 
+/* The kernel that the plan's calls run (host-side, as conv_plan_info; any pointer may be NULL). */
+typedef enum {
+    CONV_INT8_FEW_ROWS = 0,  /* up to 4 rows, 32-bit integer sums                          */
+    CONV_INT8_MID_ROWS = 1,  /* w read once for up to 64 rows, FP16 MMA from registers      */
+    CONV_INT8_TILES = 2      /* tcgen05 tiles of tile_rows x tile_columns (256 x 256 on a pair
+                                of SMs), the K of each shared by `splits` CTAs; 0 for the others */
+} conv_int8_kernel;
+conv_status conv_int8_plan_info(const conv_int8_plan *p, int *kernel, int *tile_rows, int *tile_columns, int *splits);
+
 /* Status word of the plan (waits that gave up): the contract of conv_plan_device_status.  Plans of few
  * rows run kernels without waits: they take no word of the 1,024 and read 0 when the stream is done. */
 conv_status conv_int8_plan_device_status(const conv_int8_plan *p, void *stream, int *code);
