@@ -161,11 +161,13 @@ class GroupNormPlan:
                "conv_group_norm_forward_int8")
         return q, scale
 
-    def backward(self, dy, x, stats, gamma=None, beta=None, dx=None, dgamma=None, dbeta=None, stream=None):
-        """(dx, dgamma, dbeta) from the forward pass's x and stats."""
+    def backward(self, dy, x, stats, gamma=None, beta=None, dx=None, dgamma=None, dbeta=None, stream=None,
+                 affine_grads=True):
+        """(dx, dgamma, dbeta) from the forward pass's x and stats; without ``affine_grads`` dx alone,
+        (dx, None, None)."""
         if stream is not None:
             with _t.cuda.stream(stream):
-                return self.backward(dy, x, stats, gamma, beta, dx, dgamma, dbeta)
+                return self.backward(dy, x, stats, gamma, beta, dx, dgamma, dbeta, affine_grads=affine_grads)
         if stats is None:
             raise ValueError("stats must be what forward(stats=...) wrote")
         dev = self._inputs(x, gamma, beta, stats)
@@ -174,17 +176,21 @@ class GroupNormPlan:
             dx = _t.empty_like(x)
         else:
             _need(dx, "dx", self.shape, self.torch_dtype, dev)
-        if dgamma is None:
-            dgamma = _t.empty(self._channels, dtype=_t.float32, device=dev)
+        if not affine_grads:
+            if dgamma is not None or dbeta is not None:
+                raise ValueError("dgamma and dbeta are not written without affine_grads")
         else:
-            _need(dgamma, "dgamma", self._channels, _t.float32, dev)
-        if dbeta is None:
-            dbeta = _t.empty(self._channels, dtype=_t.float32, device=dev)
-        else:
-            _need(dbeta, "dbeta", self._channels, _t.float32, dev)
+            if dgamma is None:
+                dgamma = _t.empty(self._channels, dtype=_t.float32, device=dev)
+            else:
+                _need(dgamma, "dgamma", self._channels, _t.float32, dev)
+            if dbeta is None:
+                dbeta = _t.empty(self._channels, dtype=_t.float32, device=dev)
+            else:
+                _need(dbeta, "dbeta", self._channels, _t.float32, dev)
         ws = _workspace(self.workspace_bytes["backward"], dev)
         _check(self._L.conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(gamma),
-                                                _ptr(beta), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+                                                _ptr(beta), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
                                                 _ptr(ws), _raw_stream(dev)), "conv_group_norm_backward")
         return dx, dgamma, dbeta
 
@@ -305,12 +311,61 @@ def _norm_plan(x, groups, eps, act):
     return plan
 
 
+_norm_fn = None
+
+
+def _norm_function():
+    """The autograd function of group_norm.  It keeps statistics of its own: a caller's buffer may
+    hold another call's by the time of the backward pass."""
+    global _norm_fn
+    if _norm_fn is None:
+        from torch.autograd.function import once_differentiable
+
+        class GroupNorm(_torch().autograd.Function):
+            @staticmethod
+            def forward(ctx, x, gamma, beta, plan):
+                stats = plan.empty_stats(x.device)
+                y = plan.forward(x, gamma, beta, stats=stats)
+                ctx.save_for_backward(x, gamma, beta, stats)
+                ctx.mark_non_differentiable(stats)
+                ctx.plan = plan
+                return y, stats
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy, _):
+                x, gamma, beta, stats = ctx.saved_tensors
+                dy = dy.contiguous()
+                if dy.data_ptr() % 16:  # a slice of a larger tensor
+                    dy = dy.clone()
+                need_x, need_gamma, need_beta, _ = ctx.needs_input_grad
+                dx, dgamma, dbeta = ctx.plan.backward(dy, x, stats, gamma, beta, affine_grads=need_gamma or need_beta)
+                return dx if need_x else None, dgamma if need_gamma else None, dbeta if need_beta else None, None
+
+        _norm_fn = GroupNorm
+    return _norm_fn
+
+
 def group_norm(x, groups, gamma=None, beta=None, eps=1e-5, act="none", y=None, stats=None, stream=None):
-    """act((x - mean) * rstd * gamma + beta) over each image's groups of channels; x NHWC."""
+    """act((x - mean) * rstd * gamma + beta) over each image's groups of channels; x NHWC.
+
+    Differentiable: where torch records gradients and x, gamma or beta requires one, the result has
+    its backward pass (group_norm_backward; once, and not with ``y`` given).  The plans and the
+    8-bit forms record none."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return group_norm(x, groups, gamma, beta, eps, act, y, stats)
-    return _norm_plan(x, groups, eps, act).forward(x, gamma, beta, y, stats)
+    plan = _norm_plan(x, groups, eps, act)
+    if _t.is_grad_enabled() and (x.requires_grad or (gamma is not None and gamma.requires_grad) or
+                                 (beta is not None and beta.requires_grad)):
+        if y is not None:
+            raise ValueError("y cannot be given where the result's gradient is recorded")
+        out, own = _norm_function().apply(x, gamma, beta, plan)
+        if stats is not None:
+            _need(stats, "stats", plan.stats_shape, _t.float32, x.get_device())
+            stats.copy_(own)
+        return out
+    return plan.forward(x, gamma, beta, y, stats)
 
 
 def group_norm_int8(x, groups, gamma=None, beta=None, eps=1e-5, act="none", stats=None, stream=None):

@@ -339,3 +339,86 @@ def test_forward_int8_odd_channels_far_from_zero(shape, shift, act, dtype):
     assert np.all(np.abs(127.0 * s - top) <= tol.max(1) + 4 * ref.U32 * top)
     assert np.all(np.abs(qs).max(1)[s > 0] == 127)
     assert np.all(np.abs(qs * s[:, None] - want) <= 0.5 * s[:, None] * (1 + 128 * ref.U32 * 2) + tol)
+
+
+def _leaf(t, on=True):
+    return t.detach().clone().requires_grad_(on)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 9, 7, 64, 8), (1, 40, 30, 21, 3), (4, 56, 56, 64, 4), (1, 8, 8, 256, 32)])
+def test_gradients_are_recorded(shape, dtype):
+    """group_norm in a graph of operations: the gradients that torch hands back are
+    group_norm_backward's, the other branch's are added, and what needs none gets none."""
+    import cnn_convolution_implicit_gb300 as cg
+    N, H, W, C, G = shape
+    x, gamma, beta = (t.cuda() for t in _make(N, H, W, C, dtype, 31))
+    dy = torch.randn(x.shape, generator=torch.Generator().manual_seed(7)).to(DT[dtype]).cuda()
+    stats = torch.empty(2, N, G, device="cuda")
+    y = cg.group_norm(x, G, gamma, beta, act="silu", stats=stats)
+    want = cg.group_norm_backward(dy, x, stats, G, gamma, beta, act="silu")
+    for need in ((True, True, True), (True, False, False), (False, True, False), (False, False, True)):
+        a, b, c = _leaf(x, need[0]), _leaf(gamma, need[1]), _leaf(beta, need[2])
+        given = torch.empty_like(stats)
+        out = cg.group_norm(a, G, b, c, act="silu", stats=given)
+        assert out.requires_grad and torch.equal(out, y) and torch.equal(given, stats)
+        given.fill_(float("nan"))  # the caller's statistics are the caller's
+        out.backward(dy)
+        for leaf, on, w in zip((a, b, c), need, want):
+            assert (leaf.grad is not None) == on and (not on or torch.equal(leaf.grad, w))
+    a = _leaf(x)
+    (cg.group_norm(a, G, act="relu") + a).sum().backward()  # no affine; an expanded gradient of ones
+    s0 = torch.empty_like(stats)
+    cg.group_norm(x, G, act="relu", stats=s0)
+    dx = cg.group_norm_backward(torch.ones_like(x), x, s0, G, act="relu")[0]
+    assert torch.equal(a.grad, dx + torch.ones_like(x))
+
+
+def test_gradients_of_odd_layouts_and_streams():
+    """A gradient that arrives transposed or off 16 bytes, a call on a given stream, and what cannot
+    be recorded."""
+    import cnn_convolution_implicit_gb300 as cg
+    x, gamma, beta = (t.cuda() for t in _make(2, 6, 6, 32, "bf16", 3))
+    dy = torch.randn_like(x)
+    stats = torch.empty(2, 2, 4, device="cuda")
+    y = cg.group_norm(x, 4, gamma, beta, stats=stats)
+    want = cg.group_norm_backward(dy, x, stats, 4, gamma, beta)[0]
+    a = _leaf(x)
+    cg.group_norm(a, 4, gamma, beta).transpose(1, 2).backward(dy.transpose(1, 2).contiguous())
+    assert torch.equal(a.grad, want)
+    a, flat = _leaf(x), torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")
+    off = flat[1:].view(x.shape)
+    off.copy_(dy)
+    cg.group_norm(a, 4, gamma, beta).backward(off)
+    assert torch.equal(a.grad, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = _leaf(x)
+    out = cg.group_norm(a, 4, gamma, beta, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    out.backward(dy)
+    torch.cuda.synchronize()
+    assert torch.equal(out, y) and torch.equal(a.grad, want)
+    with torch.no_grad():
+        assert not cg.group_norm(_leaf(x), 4, gamma, beta, y=torch.empty_like(x)).requires_grad
+    with pytest.raises(ValueError):
+        cg.group_norm(_leaf(x), 4, gamma, beta, y=torch.empty_like(x))
+    a = _leaf(x.float())
+    g = torch.autograd.grad(cg.group_norm(a, 4, act="silu").sum(), a, create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        g.sum().backward()  # differentiable once
+
+
+@pytest.mark.parametrize("shape", [(2, 9, 7, 64, 8), (1, 40, 30, 21, 3), (16, 64, 64, 64, 8)])
+def test_dx_alone(shape):
+    import cnn_convolution_implicit_gb300 as cg
+    N, H, W, C, G = shape
+    x, gamma, beta = (t.cuda() for t in _make(N, H, W, C, "bf16", 17))
+    plan = cg.GroupNormPlan(N, C, H, W, G, "bf16", act="silu")
+    stats, dy = plan.empty_stats(), torch.randn_like(x)
+    plan.forward(x, gamma, beta, stats=stats)
+    dx, dgamma, dbeta = plan.backward(dy, x, stats, gamma, beta, affine_grads=False)
+    assert dgamma is None and dbeta is None
+    assert torch.equal(dx, plan.backward(dy, x, stats, gamma, beta)[0])
+    with pytest.raises(ValueError):
+        plan.backward(dy, x, stats, gamma, beta, dgamma=torch.empty_like(gamma), affine_grads=False)
