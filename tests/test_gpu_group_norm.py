@@ -422,3 +422,20 @@ def test_dx_alone(shape):
     assert torch.equal(dx, plan.backward(dy, x, stats, gamma, beta)[0])
     with pytest.raises(ValueError):
         plan.backward(dy, x, stats, gamma, beta, dgamma=torch.empty_like(gamma), affine_grads=False)
+
+
+def test_channels_past_65535_blocks():
+    """An odd number of channels, 65,536 blocks of 256: more than a grid's second dimension holds."""
+    import cnn_convolution_implicit_gb300 as cg
+    C = 256 * 65535 + 1
+    g = torch.Generator().manual_seed(5)
+    x, dy = torch.randn(1, 1, 1, C, generator=g), torch.randn(1, 1, 1, C, generator=g)
+    gamma, beta = torch.randn(C, generator=g) * 0.3 + 1.0, torch.randn(C, generator=g) * 0.3
+    stats = torch.empty(2, 1, 1, device="cuda")
+    y = cg.group_norm(x.cuda(), 1, gamma.cuda(), beta.cuda(), act="silu", stats=stats)
+    want, tol = ref.norm_forward(_flat(x), 1, _np(gamma), _np(beta), 1e-5, "silu")
+    ref.check(_flat(y), want, tol, False, "y")
+    got = cg.group_norm_backward(dy.cuda(), x.cuda(), stats, 1, gamma.cuda(), beta.cuda(), act="silu")
+    want, tol = ref.norm_backward(_flat(dy), _flat(x), stats.cpu().numpy(), 1, _np(gamma), _np(beta), "silu")
+    for a, b, t, name in zip((_flat(got[0]), _np(got[1]), _np(got[2])), want, tol, ("dx", "dgamma", "dbeta")):
+        ref.check(a, b, t, False, name)
