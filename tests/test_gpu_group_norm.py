@@ -439,3 +439,20 @@ def test_channels_past_65535_blocks():
     want, tol = ref.norm_backward(_flat(dy), _flat(x), stats.cpu().numpy(), 1, _np(gamma), _np(beta), "silu")
     for a, b, t, name in zip((_flat(got[0]), _np(got[1]), _np(got[2])), want, tol, ("dx", "dgamma", "dbeta")):
         ref.check(a, b, t, False, name)
+
+
+@pytest.mark.parametrize("shape,dtype", [((1 << 19, 1, 1, 32, 4), "f32"), ((1 << 18, 1, 1, 21, 3), "f32"),
+                                         ((1 << 17, 2, 2, 64, 8), "bf16")])
+def test_affine_gradients_of_many_images(shape, dtype):
+    """Rows of tokens, each an image: dgamma and dbeta add up hundreds of thousands of partial sums
+    of one sign, whose rounding must not pile up."""
+    import cnn_convolution_implicit_gb300 as cg
+    N, H, W, C, G = shape
+    x, gamma, beta = _make(N, H, W, C, dtype, 23)
+    dy = torch.full(x.shape, 0.1).to(DT[dtype])
+    stats = torch.empty(2, N, G, device="cuda")
+    cg.group_norm(x.cuda(), G, gamma.cuda(), beta.cuda(), stats=stats)
+    got = cg.group_norm_backward(dy.cuda(), x.cuda(), stats, G, gamma.cuda(), beta.cuda())
+    want, tol = ref.norm_backward(_flat(dy), _flat(x), stats.cpu().numpy(), G, _np(gamma), _np(beta), "none")
+    ref.check(_np(got[1]), want[1], tol[1], False, "dgamma")
+    ref.check(_np(got[2]), want[2], tol[2], False, "dbeta")
