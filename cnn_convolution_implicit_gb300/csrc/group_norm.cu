@@ -497,17 +497,22 @@ struct CarriedSum {
 
 template <int STEP>
 __device__ __forceinline__ float2 channel_sum(const float2* part, long long first, long long entries, int C) {
+    constexpr int kBatch = 8;  // loads under way, of a short chain too
     CarriedSum u, uh;
     const long long step = static_cast<long long>(STEP) * C;
     part += first * C;
     for (long long left = first < entries ? (entries - first + STEP - 1) / STEP : 0; left > 0; left -= 256) {
         const int count = static_cast<int>(left < 256 ? left : 256);
         float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-        for (int i = 0; i < count; ++i, part += step) {
-            const float2 v = *part;
-            s.x += v.x;
-            s.y += v.y;
+        for (int i = 0; i < count; i += kBatch) {
+            float2 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k, part += step) v[k] = i + k < count ? *part : make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                s.x += v[k].x;
+                s.y += v[k].y;
+            }
         }
         u.add(s.x);
         uh.add(s.y);
