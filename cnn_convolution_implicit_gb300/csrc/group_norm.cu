@@ -581,8 +581,15 @@ __device__ __forceinline__ uint32_t res_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void res_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void res_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The aligned forms: a warp's lanes arrive, and wait, together, whatever loops they left before.
+__device__ __forceinline__ void res_cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void res_cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Two floats to the same shared-memory place of cluster CTA `rank`.
 __device__ __forceinline__ void res_push(float2* p, uint32_t rank, float2 v) {
