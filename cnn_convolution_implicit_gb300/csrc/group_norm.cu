@@ -1399,11 +1399,16 @@ dim3 stream_grid(const NormParams& p) {
 
 namespace {
 
-// Each kernel with its own record of the shared memory it was given.
+// Each kernel with its own record of the shared-memory limit.
+template <typename T, int MODE, int ACT>
+SmemLimitCache& resident_limits() {
+    static SmemLimitCache limits;
+    return limits;
+}
+
 template <typename T, int MODE, int ACT, typename F>
 void with_limits(F&& f) {
-    static SmemLimitCache limits;
-    f(norm_resident_kernel<T, MODE, ACT>, limits);
+    f(norm_resident_kernel<T, MODE, ACT>, resident_limits<T, MODE, ACT>());
 }
 
 template <typename F>

@@ -456,3 +456,23 @@ def test_affine_gradients_of_many_images(shape, dtype):
     want, tol = ref.norm_backward(_flat(dy), _flat(x), stats.cpu().numpy(), G, _np(gamma), _np(beta), "none")
     ref.check(_np(got[1]), want[1], tol[1], False, "dgamma")
     ref.check(_np(got[2]), want[2], tol[2], False, "dbeta")
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_a_plan_is_the_same_after_other_calls(act):
+    """The form of a plan comes from its shape and the device, not from the maps that went before:
+    small ones must not leave the kernels less shared memory than a larger one counts on."""
+    import cnn_convolution_implicit_gb300 as cg
+    large = [(64, 256, 56, 56, 32), (8, 64, 56, 56, 16), (20, 512, 14, 14, 32)]
+    small = [(4, 64, 56, 56, 32), (2, 128, 16, 16, 16), (1, 256, 8, 8, 32)]
+    for dtype in ("bf16", "f32"):
+        made = [cg.GroupNormPlan(N, C, H, W, G, dtype, act=act).workspace_bytes for N, C, H, W, G in large]
+        for N, C, H, W, G in small:
+            plan = cg.GroupNormPlan(N, C, H, W, G, dtype, act=act)
+            x, stats = torch.randn(plan.shape, device="cuda").to(DT[dtype]), plan.empty_stats()
+            plan.forward(x, stats=stats)
+            plan.forward_int8(x)
+            plan.backward(x, x, stats)
+        again = [cg.GroupNormPlan(N, C, H, W, G, dtype, act=act).workspace_bytes for N, C, H, W, G in large]
+        assert again == made
+    torch.cuda.synchronize()
