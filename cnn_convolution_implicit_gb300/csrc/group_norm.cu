@@ -30,17 +30,17 @@
 //   while the other stores; with 200 KB an SM in flight the rate is those bytes over a CTA's
 //   life (~11 us: 5.5 loading, 3 from the last load to the first store, 2.5 storing), and clusters
 //   of eight fill 288 of 304 places, of sixteen 224.
-//     1 x 8 x 8 x 256 BF16: 8 us; 64 x 56 x 56 x 256: 55 us (floor 30); 32 x 112 x 112 x 256: 92 (61).
+//     1 x 8 x 8 x 256 BF16: 9 us; 64 x 56 x 56 x 256: 57 us (floor 30); 32 x 112 x 112 x 256, ReLU: 95 (61).
 //   Two passes (maps that no cluster of 16 holds, and where clusters fill the SMs badly): one
 //   kernel leaves each pixel range's group sums, streaming it through shared memory; the next joins
 //   them in its prologue and writes the values, walking its range backwards and storing past
 //   the caches, so that part of x is still in L2.  The second is launched early and waits for
 //   the first.  It reads x twice; where a CTA's life would be long or clusters large it wins.
-//     1 x 512 x 512 x 128 BF16: 43 us (floor 20); 64 x 56 x 56 x 256 to 8 bits: 70 (23), resident 92;
-//     backward 32 x 112 x 112 x 128: 97 (45), resident 123; 16 x 64 x 64 x 256 43 (15), resident 50.
+//     1 x 512 x 512 x 128 BF16: 44 us (floor 20); 64 x 56 x 56 x 256 to 8 bits: 70 (23), resident 93;
+//     backward, SiLU, 32 x 112 x 112 x 128: 109 (45), resident 138 (ReLU 97); 16 x 64 x 64 x 256 44 (15), resident 50.
 //   By channel (pixels that do not start on 16 bytes, over 256 vectors a pixel): as two passes, the
 //   sums kept per channel and joined by a kernel of their own; 4- or 8-byte accesses where the
-//   channels allow.  32 x 112 x 112 x 250 BF16: 186 us (floor 59).
+//   channels allow.  32 x 112 x 112 x 250 BF16: 192 us (floor 59), to 8 bits 564 (45), backward 437 (89).
 #include "norm_internal.h"
 #include "pointwise_math.cuh"
 
@@ -625,14 +625,14 @@ struct ResSmem {
 
 template <int MODE>
 __host__ __device__ inline int res_part_entries(const NormParams& p) {
-    const int vpr = p.chunk / p.vec, rows = res_threads(MODE) / vpr;
-    if (MODE == kNormBackward) return (res_warp_rows(vpr) ? res_threads(MODE) / 32 : rows) * p.chunk;
+    const int vpr = p.chunk / p.vec, rows = kResThreads / vpr;
+    if (MODE == kNormBackward) return (res_warp_rows(vpr) ? kResThreads / 32 : rows) * p.chunk;
     return rows * vpr * (p.vec / res_lump(p));
 }
 
 template <int MODE>
 __host__ __device__ inline size_t res_smem_bytes(const NormParams& p) {
-    return static_cast<size_t>(MODE == kNormBackward ? 2 : 1) * p.items * res_threads(MODE) * 16 +
+    return static_cast<size_t>(MODE == kNormBackward ? 2 : 1) * p.items * kResThreads * 16 +
            static_cast<size_t>(res_part_entries<MODE>(p)) * 8 + static_cast<size_t>(res_groups(p)) * (kResMaxCluster + 1) * 8 +
            (MODE == kNormInt8 ? static_cast<size_t>(res_pixels(p)) * 4 : 0);
 }
@@ -641,8 +641,8 @@ template <int MODE>
 __device__ __forceinline__ ResSmem res_carve(uint8_t* raw, const NormParams& p) {
     ResSmem s;
     s.x = reinterpret_cast<uint4*>(raw);
-    s.dy = s.x + static_cast<size_t>(p.items) * res_threads(MODE);
-    s.part = reinterpret_cast<float2*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * res_threads(MODE) : s.dy);
+    s.dy = s.x + static_cast<size_t>(p.items) * kResThreads;
+    s.part = reinterpret_cast<float2*>(MODE == kNormBackward ? s.dy + static_cast<size_t>(p.items) * kResThreads : s.dy);
     s.recv = s.part + res_part_entries<MODE>(p);
     s.result = s.recv + res_groups(p) * kResMaxCluster;
     s.top = reinterpret_cast<uint32_t*>(s.result + res_groups(p));
@@ -776,9 +776,8 @@ __device__ __forceinline__ void cta_group_grads(const NormParams& p, int vpr, in
 }
 
 template <typename T, int MODE, int ACT>
-__global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kResThreads, 2) norm_resident_kernel(const NormParams p) {
     constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
-    constexpr int kThreads = res_threads(MODE);
     using Io = VecIo<T, VEC>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const ResSmem sm = res_carve<MODE>(smem_raw, p);
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
     const int n = unit / chunks;
     const int c0 = (unit - n * chunks) * p.chunk;
     const int vpr = p.chunk / VEC;           // vectors of a pixel
-    const int rows = kThreads / vpr;
+    const int rows = kResThreads / vpr;
     const int r = threadIdx.x / vpr, v = threadIdx.x - r * vpr;
     int p0, p1;
     pixel_range(p, rank, p0, p1);
@@ -811,8 +810,8 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
             const int end = min((b + 1) * batch, mine);
 #pragma unroll 2
             for (int i = b * batch; i < end; ++i) {
-                copy_async16(dst + i * (kThreads * 16), x + i * step);
-                if constexpr (MODE == kNormBackward) copy_async16(dst2 + i * (kThreads * 16), dy + i * step);
+                copy_async16(dst + i * (kResThreads * 16), x + i * step);
+                if constexpr (MODE == kNormBackward) copy_async16(dst2 + i * (kResThreads * 16), dy + i * step);
             }
             copy_commit();
         }
@@ -858,7 +857,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
             }
 #pragma unroll 4
             for (int i = from; i < to; ++i) {
-                Io::unpack(items[i * kThreads], f);
+                Io::unpack(items[i * kResThreads], f);
                 mo.add(f);
             }
         });
@@ -873,8 +872,8 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
 #pragma unroll 2
             for (int i = from; i < to; ++i) {
                 f2 f[H], d[H];
-                Io::unpack(items[i * kThreads], f);
-                Io::unpack(items_dy[i * kThreads], d);
+                Io::unpack(items[i * kResThreads], f);
+                Io::unpack(items_dy[i * kResThreads], d);
                 grad.template apply<ACT>(f, d);
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
@@ -890,7 +889,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
 
     // The cluster's groups, every CTA for itself in the same order.
     if constexpr (MODE == kNormInt8)
-        for (int i = threadIdx.x; i < p1 - p0; i += kThreads) sm.top[i] = 0;
+        for (int i = threadIdx.x; i < p1 - p0; i += kResThreads) sm.top[i] = 0;
     if (p.splits > 1) {
         res_cluster_arrive();
         res_cluster_wait();
@@ -900,7 +899,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
     const float over_total = __frcp_rn(static_cast<float>(p.P) * static_cast<float>(p.cpg));
     const int wide = segment_width(p.splits), at_once = 32 / wide, k = lane & (wide - 1);
     const float cnt = k < p.splits ? static_cast<float>(p.pix_base + (k < p.pix_more)) * static_cast<float>(p.cpg) : 0.0f;
-    for (int gfirst = warp * at_once; gfirst < groups; gfirst += kThreads / 32 * at_once) {
+    for (int gfirst = warp * at_once; gfirst < groups; gfirst += kResThreads / 32 * at_once) {
         const int g = gfirst + lane / wide;
         const float2 o = g < groups && k < p.splits ? sm.recv[g * kResMaxCluster + k] : make_float2(0.0f, 0.0f);
         float2 res;
@@ -928,7 +927,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
 #pragma unroll 4
         for (int i = 0; i < mine; ++i) {
             f2 f[H];
-            Io::unpack(items[i * kThreads], f);
+            Io::unpack(items[i * kResThreads], f);
             af.template apply<ACT>(f);
             y[i * step] = Io::pack(f);
         }
@@ -939,8 +938,8 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
 #pragma unroll 2
         for (int i = 0; i < mine; ++i) {
             f2 f[H], d[H];
-            Io::unpack(items[i * kThreads], f);
-            Io::unpack(items_dy[i * kThreads], d);
+            Io::unpack(items[i * kResThreads], f);
+            Io::unpack(items_dy[i * kResThreads], d);
             grad.template apply<ACT>(f, d);
             gm.dx(f, d, grad);
             dx[i * step] = Io::pack(f);
@@ -952,7 +951,7 @@ __global__ void __launch_bounds__(res_threads(MODE), 2) norm_resident_kernel(con
         float* scales = p.scale + static_cast<long long>(n) * p.P + p0 + r;
         int8_t* q = p.q + base * VEC;
         const auto value = [&](int i, f2 (&f)[H]) {
-            Io::unpack(items[i * kThreads], f);
+            Io::unpack(items[i * kResThreads], f);
             af.template apply<ACT>(f);
             float top = 0.0f;
 #pragma unroll
@@ -1087,7 +1086,7 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
     extern __shared__ __align__(16) uint8_t smem_raw[];
     float2* part = reinterpret_cast<float2*>(smem_raw);
     const TwoRange t(p, blockIdx.x, VEC);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     constexpr int kTensors = MODE == kNormBackward ? 2 : 1;
     RangeStream<kTensors> stream;
     stream.from[0] = static_cast<const uint4*>(p.x) + t.base;
@@ -1137,7 +1136,6 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kNormBackward ? 3 : 4) n
         cta_group_grads<VEC>(p, t.vpr, t.rows, t.r, t.v, s1, s2, p.G, p.C, p.gamma, p.dgamma != nullptr ? out : nullptr,
                              part, [] {}, store);
     }
-    (void)warp;
 }
 
 // One group of an image from its ranges, by `width` threads of which this is the k-th: (mean, rstd),
@@ -1437,7 +1435,7 @@ cudaError_t resident_config(K* fn, SmemLimitCache& limits, const NormParams& p, 
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), p.smem_bytes, limits);
     cfg = cudaLaunchConfig_t();
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.N) * (p.C / p.chunk) * p.splits));
-    cfg.blockDim = dim3(res_threads(mode));
+    cfg.blockDim = dim3(kResThreads);
     cfg.dynamicSmemBytes = p.smem_bytes;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1466,22 +1464,21 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
 // pixels takes as many channels as one CTA holds, two to an SM (backward: 64 KB of x and dy, since
 // its sums a channel grow with them), while that leaves half a unit an SM: 128 x 14 x 14 x 1024
 // BF16 33 us, 84 at 64 bytes a pixel; 256 x 8 x 8 x 512 17 and 68, backward 29 and 63.  A larger one
-// takes up to 64 bytes a pixel (128 make clusters of 16, of which a GPC holds fewer:
-// 32 x 112 x 112 x 256 BF16 113 us against 97, 32 bytes 122) and the fewest CTAs that hold it
+// takes up to 64 bytes a pixel (128 make clusters of 16, of which a GPC holds fewer: 32 x 112 x 112 x 256
+// BF16, SiLU, took 113 us with 128, 97 with 64, 122 with 32) and the fewest CTAs that hold it
 // two to an SM, then one to an SM.  More CTAs while there are fewer than SMs.
 void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
     p.chunk = 0;
     if (p.vec * es != 16 || static_cast<long long>(p.P) * (p.C / p.vec) >= (1LL << 31)) return;
-    const int threads = res_threads(mode);
     NormParams t = p;
-    const auto rows_of = [&](int chunk) { return threads / (chunk / p.vec); };
+    const auto rows_of = [&](int chunk) { return kResThreads / (chunk / p.vec); };
     const auto fits = [&](int chunk, int cluster, int limit) {
         t.chunk = chunk;
         t.splits = cluster;
         const int pixels = res_pixels(t);
         t.items = (pixels + rows_of(chunk) - 1) / rows_of(chunk);
-        if (static_cast<double>(t.items) * tensors * threads * 16 > limit) return false;
+        if (static_cast<double>(t.items) * tensors * kResThreads * 16 > limit) return false;
         t.smem_bytes = static_cast<int>(resident_smem(t, mode));
         return t.smem_bytes <= limit;
     };
@@ -1494,13 +1491,13 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
         for (int g = 1; g <= p.G; ++g) {  // whole groups that divide the channels and make whole vectors
             const int c = g * p.cpg;
             if (p.G % g != 0 || c % p.vec != 0) continue;
-            if (chunk != 0 && c / p.vec > threads) break;
+            if (chunk != 0 && c / p.vec > kResThreads) break;
             if (chunk == 0 || c * es <= 64 ||
-                (2LL * p.N * (p.C / c) >= num_sms && fits(c, 1, half) && 16LL * tensors * t.items * threads <= room))
+                (2LL * p.N * (p.C / c) >= num_sms && fits(c, 1, half) && 16LL * tensors * t.items * kResThreads <= room))
                 chunk = c;
         }
     }
-    if (chunk == 0 || chunk / p.vec > threads) return;
+    if (chunk == 0 || chunk / p.vec > kResThreads) return;
     const int rows = rows_of(chunk);
     const long long units = static_cast<long long>(p.N) * (p.C / chunk);
     int best = 0;
@@ -1520,34 +1517,40 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
 // Whether the resident form (at_a_time clusters on the device) beats two passes, where both can run.
 // A GPC holds few large clusters, so the last of two or three rounds of them leaves much idle,
 // and two CTAs an SM of 100 KB each take long when the SMs are not full of them; two passes pay a second
-// read of x, a launch and their joins.  Pairs: resident, two passes, cold caches, BF16.
+// read of x, a launch and their joins.  Pairs: resident, two passes, microseconds, cold caches, BF16,
+// SiLU, 32 groups.
 bool norm_resident_pays(const NormParams& p, int mode, int at_a_time, int num_sms) {
     const long long units = static_cast<long long>(p.N) * (p.C / p.chunk);
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
-    const long long held = 16LL * tensors * p.items * res_threads(mode);  // bytes a CTA holds
+    const long long held = 16LL * tensors * p.items * kResThreads;  // bytes a CTA holds
     const bool one_round = units <= at_a_time;
     if (mode == kNormForward) {
-        // 4 x 160 x 160 x 128 (15 CTAs, 16 units) 31 and 26 us, 12 x 160 x 160 x 128 61 and 46,
-        // 8 x 200 x 200 x 128 74 and 50; of one round, 2 x 160 x 160 x 64 15 and 16.
+        // 4 x 160 x 160 x 128 (16 CTAs, 1.1 rounds) 31 and 26, 12 x 160 x 160 x 128 (3.4) 58 and 50,
+        // 8 x 200 x 200 x 128 (12 CTAs, 4.0) 74 and 51; of one round, 2 x 160 x 160 x 64 17 and 22.
         if (p.splits > 8 && !one_round) return false;
-        // 16 x 96 x 96 x 128 (6 CTAs, 64 units of which 46 at a time) 33 and 27 us; at 3.6 rounds of eight
-        // 32 x 112 x 112 x 128 61 and 57, at seven 32 x 112 x 112 x 256 94 and 107.
+        // 16 x 96 x 96 x 128 (6 CTAs, 1.4 rounds) 33 and 32; of eight 32 x 112 x 112 x 128 (3.6) 64 and 62,
+        // 32 x 112 x 112 x 256 (7.1) 106 and 111.
         return p.splits <= 4 || one_round || units > 2LL * at_a_time;
     }
     if (mode == kNormInt8) {
-        // Pixel-wide units.  Up to 48 KB a CTA: 2 x 16 x 16 x 128 10 and 13 us, 4 x 32 x 32 x 128 12 and 13;
-        // 64 KB of 16 CTAs: 1 x 32 x 32 x 512 21 and 13; 125 KB: 4 x 56 x 56 x 320 33 and 23, 64 x 56 x 56 x 256
-        // 89 and 72.  Many units of at most eight CTAs: 256 x 56 x 56 x 64 71 and 109, 128 x 28 x 28 x 512
-        // 94 and 107; too few of them for the SMs: 16 x 32 x 32 x 320 29 and 24.
+        // Pixel-wide units.  Up to 48 KB a CTA: 2 x 16 x 16 x 128 13 and 13, 4 x 32 x 32 x 128 15 and 16;
+        // 105 KB of 10 CTAs: 1 x 32 x 32 x 512 21 and 14; 208 KB: 4 x 56 x 56 x 320 36 and 24; of 16 CTAs
+        // 64 x 56 x 56 x 256 93 and 70.  Many units of at most eight CTAs: 256 x 56 x 56 x 64 91 and 105,
+        // 128 x 28 x 28 x 512 95 and 103; too few of them for the SMs: 16 x 32 x 32 x 320 31 and 27.
         return held <= 48 * 1024 || (p.splits <= 8 && units * p.splits > num_sms);
     }
-    // Small maps of few channels, where the joins are short: 4 x 56 x 56 x 64 16 and 13 us (with x and dy in L2 9.3
-    // and 8.6); larger, 8 x 56 x 56 x 64 FP32, 17 and 17 (8.2 and 11); of more channels 4 x 32 x 32 x 512 18 and 22.
+    // Small maps of few channels, where the joins are short: 4 x 56 x 56 x 64 17 and 17 (in a graph, x and dy in
+    // L2, 10.8 and 11.6); larger, 8 x 56 x 56 x 64 FP32, 19 and 21 (10 and 15); of more channels
+    // 4 x 32 x 32 x 512 19 and 22.
     if (p.C <= 128 && static_cast<double>(p.N) * p.P * p.C * es <= 4e6) return false;
-    // Clusters of a dozen in one round that fills the SMs, 1 x 96 x 96 x 512 23 and 28 us; in 1.4 rounds 8 x 96 x 96 x 128
-    // 35 and 32, of 200 KB a CTA 4 x 128 x 128 x 128 43 and 32, of sixteen 32 x 112 x 112 x 128 134 and 111.
+    // Clusters of a dozen in one round that fills the SMs, 1 x 96 x 96 x 512 25 and 28; in 1.4 rounds 8 x 96 x 96 x 128
+    // 38 and 37, of 200 KB a CTA 4 x 128 x 128 x 128 44 and 32, of sixteen 32 x 112 x 112 x 128 138 and 109.
     if (p.splits > 8) return one_round && 3 * units >= at_a_time && held > 64 * 1024 && held <= 112 * 1024;
-    // 16 x 64 x 64 x 256 (2.2 rounds) 50 and 44 us; seven rounds, 64 x 56 x 56 x 256, 107 and 111.
+    // Between two and three rounds 16 x 64 x 64 x 256 (2.2) 50 and 44, 32 x 64 x 64 x 128 (2.2) 52 and 42,
+    // 24 x 56 x 56 x 256 (2.6) 52 and 50, 20 x 64 x 64 x 256 (2.8) 55 and 51, but 100 x 28 x 28 x 256 (2.6, single CTAs)
+    // 48 and 50.  Up to two: 48 x 28 x 28 x 256 (1.3) 31 and 31 (in a graph 21 and 24), 12 x 64 x 64 x 128 FP32 (1.7)
+    // 33 and 31, 16 x 56 x 56 x 256 (1.7) 40 and 37 (28 and 30).  Past three they are close: 64 x 28 x 28 x 512 (3.4)
+    // 56 and 60, 32 x 56 x 56 x 256 (3.5) 61 and 58, 40 x 56 x 56 x 256 (4.3) 74 and 71, 64 x 56 x 56 x 256 (6.9) 108 and 108.
     return units <= 2LL * at_a_time || units > 3LL * at_a_time;
 }
 
@@ -1678,8 +1681,7 @@ cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t s
     return cudaGetLastError();
 }
 
-cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
+cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t stream) {
     if (p.chunk != 0) {
         const cudaError_t e = launch_resident(p, kNormBackward, stream);
         if (e != cudaSuccess) return e;

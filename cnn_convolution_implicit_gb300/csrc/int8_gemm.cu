@@ -840,9 +840,9 @@ namespace {
 // least it takes (its epilogue), both again where rows of y start off 16 bytes, the launch, and what
 // joining the parts adds where a cluster splits K.  From K = 64 / 256 / 1024, BF16 output:
 // 1.1 / 2.0 / 6.9 us a tile of 32 columns, 1.3 / 2.2 / 7.3 of 64, 1.8 / 2.8 / 8.2 of 128, 3.1 / 3.8 / 8.8 on a pair.
-// 16 x 4096 x 4096 (64 steps): 29.4 us as 128 tiles of 32 columns, 18.8 as 64 tiles of 64 split
-// in two, 14.2 as 32 tiles of 128 split in four; 1000 x 4096 x 4096: 66 us in tiles of
-// 128 x 128 and 37 on pairs.
+// 65 x 4096 -> 4096 (64 steps): 29.2 us as 128 tiles of 32 columns, 20.5 as 64 tiles of 64 split
+// in two, 15.7 as 32 tiles of 128 split in four; 256 rows 31.6 as 128 tiles of 64, 23.4 as 64 of 128
+// split in two; 1000 rows 62 in tiles of 128 x 128 and 35 on pairs.
 struct Tile {
     int rows, columns;
     double step, besides, least, off_besides, off_least, launch, join;

@@ -8,9 +8,10 @@
 // the products four at a time in 32-bit integers (dp4a), so the sum is exact for every K.
 // Two rows of w share each read of x from shared memory.
 //
-// One token, 4096 -> 4096: 10 us with cold caches and the launch (3.9 us a call in a graph, the
-// weights then in L2), floor 2.5; four tokens 13: each row of x adds 16 bytes of shared memory
-// read for every 32 of w.
+// One token, 4096 -> 4096: 11 us with cold caches and the launch (3.4 us a call in a graph, the
+// weights then in L2), floor 2.5; four tokens 13 (5.7): each row of x adds 16 bytes of shared memory
+// read for every 32 of w.  Past one chunk of K the next one's loads wait for the last use of this:
+// 16384 -> 4096 21 us (8.0), floor 9.9.
 //
 // Rows of x that arrive as BF16 or FP32 are brought to 8 bits by every CTA for itself (amax,
 // scale, q), between the issue of its first loads of w and their arrival: for a single row that
@@ -52,7 +53,7 @@ __device__ __forceinline__ float few_load(const __nv_bfloat16* x, long long i) {
 template <typename T, int M>
 __device__ __forceinline__ void few_amax(const Int8Params& p, const T* x, uint32_t* top) {
     constexpr int V = 16 / sizeof(T);
-    constexpr int kSegs = kFewWarps / M;  // M is 1, 2, 4 or 8
+    constexpr int kSegs = kFewWarps / M;  // M is 1, 2 or 4
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m = warp / kSegs, seg = warp - m * kSegs;
     float a = 0.0f;
@@ -209,8 +210,8 @@ cudaError_t launch_few(const Int8Params& p, const T* x, cudaStream_t stream) {
 // Still bound by reading w once, but too many products for the CUDA cores: FP16 MMAs of 16 x 8 x 16
 // on operands that go from memory to registers and from there to FP16, exact as in the
 // tensor-core kernel of many rows, whose 128-row tiles, shared-memory stages and launch cost more
-// than the bytes here: 16 x 4096 -> 4096 5.4 us a call in a graph against 14.9, 12 and 21 with cold caches
-// and the launch (floor 2.5); 16 x 16384 -> 4096 15 and 34, 32 x 1024 -> 1024 3.0 and 8.7.
+// than the bytes here: 16 x 4096 -> 4096 5.4 to 5.8 us a call in a graph against 14.9, 13 and 21 with cold caches
+// and the launch (floor 2.5).
 //
 // A CTA takes 16 rows of w; its eight warps share K, 64 at a time.  Lane 4 g + q holds k = 16 q ..
 // 16 q + 15 of rows g of w and g, g + 8 of x: the MMA sums over k in any order, so its slots
@@ -305,10 +306,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) int8_mid_rows_kernel(const Int
 
 }  // namespace
 
-// In a graph, 8-bit input, this kernel and the one beside it (CUDA cores up to 8 rows, 128-row tiles from 9): 5 x 4096 ->
-// 4096 5.0 and 6.6 us, 8 x 512 -> 512 2.3 and 5.7; 32 x 8192 -> 8192 24.6 and 34.9; 40 x 4096 -> 4096 9.8 and 15.6;
-// 64 x 1024 -> 1024 4.7 and 8.6, but 64 x 4096 -> 16384 43.5 and 33.0 and with cold caches 56 x 8192 -> 2048 34.8 and 26.6:
-// x is read again by every 16 columns.
+// This kernel and the tiles of many rows, 8-bit input, microseconds in a graph (cold caches and the launch):
+//    5 x 4096 -> 4096 5.2 (13) and 15.2 (21)      16 x 512 -> 512 2.6 (7) and 7.2 (13)     32 x 8192 -> 8192 24.0 (40) and 34.7 (46)
+//   48 x 4096 -> 4096 10.1 (17) and 15.5 (23)     48 x 4096 -> 8192 18.2 (28) and 22.1 (29)   48 x 4096 -> 16384 31.6 (47) and 32.4 (42)
+//   64 x 1024 -> 1024 4.6 (11) and 8.6 (13)       64 x 4096 -> 4096 12.8 (21) and 15.6 (23)   64 x 4096 -> 16384 42.7 (62) and 32.6 (43)
+// x is read again by every 16 columns, so with more rows and weights the tiles win, with cold caches first (56 x 8192 ->
+// 2048 35 and 27 cold); the bounds lie on their side of where the two meet.
+// This kernel and the CUDA cores': 1 x 4096 -> 4096 5.1 (13) and 3.4 (11), 2 rows 5.2 (13) and 4.1 (11), 4 rows
+// 5.1 (13) and 5.7 (13), 4 x 16384 -> 4096 14.5 (25) and 14.3 (31); a BF16 row takes a launch more here.
 bool int8_use_mid(const Int8Params& p) {
     const long long weights = static_cast<long long>(p.N) * p.K;
     return p.M > 4 && (p.M <= 32 || (p.M <= 48 && weights <= 1LL << 24) || (p.M <= 64 && weights <= 1LL << 21));

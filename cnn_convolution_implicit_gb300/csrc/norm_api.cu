@@ -186,7 +186,7 @@ conv_status conv_group_norm_backward(conv_group_norm_plan* pl, const void* dy, c
     p.mean = const_cast<float*>(stats);
     p.rstd = p.mean + static_cast<size_t>(p.N) * p.G;
     carve_workspace(p, workspace);
-    if (launch_norm_backward(p, pl->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    if (launch_norm_backward(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return CONV_ERR_CUDA;
     }

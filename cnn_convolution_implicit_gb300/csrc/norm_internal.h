@@ -46,8 +46,8 @@ constexpr int kResMaxCluster = 16;
 
 enum NormMode { kNormForward = 0, kNormInt8 = 1, kNormBackward = 2 };
 
-// Threads of a resident CTA, two to an SM: what 64 or 80 registers leave room for.
-__host__ __device__ constexpr int res_threads(int mode) { return mode == kNormBackward ? 256 : 256; }
+// Threads of a resident CTA: two CTAs an SM leave each thread 128 registers (76 to 127 are used).
+constexpr int kResThreads = 256;
 
 size_t norm_workspace_bytes(const NormParams& p);
 size_t norm_part_entries(const NormParams& p);
@@ -60,6 +60,6 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin);
 int norm_resident_at_a_time(const NormParams& p, int mode, int num_sms);
 bool norm_resident_pays(const NormParams& p, int mode, int at_a_time, int num_sms);
 cudaError_t launch_norm_forward(const NormParams& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormParams& p, cudaStream_t stream);
 
 }  // namespace convgb

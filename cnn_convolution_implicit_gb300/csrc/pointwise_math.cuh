@@ -146,9 +146,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN passes thro
     return r;
 }
 
-// 1 / (1 + exp(-z)), about 2 ulp.  z = -inf gives 0, NaN stays NaN.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
-
+// 1 / (1 + exp(-z)).  z = -inf gives 0, NaN stays NaN.  The rounding of z log2 e grows with |z|, and with
+// it the error where exp(-z) rules: up to 3 * 2^-24 of the value for z > -3, 8 for z > -10, 27 for
+// z > -30, 62 at -85 (activate() alike).  What is lost there is below 1e-11 absolute.
 __device__ __forceinline__ f2 sigmoid2(f2 z) {
     const f2 t = f2_mul(z, f2_dup(-1.4426950408889634f));  // exp(-z) = 2^(-z log2 e)
     float a, b;

@@ -360,9 +360,10 @@ def group_norm(x, groups, gamma=None, beta=None, eps=1e-5, act="none", y=None, s
                                  (beta is not None and beta.requires_grad)):
         if y is not None:
             raise ValueError("y cannot be given where the result's gradient is recorded")
-        out, own = _norm_function().apply(x, gamma, beta, plan)
         if stats is not None:
             _need(stats, "stats", plan.stats_shape, _t.float32, x.get_device())
+        out, own = _norm_function().apply(x, gamma, beta, plan)
+        if stats is not None:
             stats.copy_(own)
         return out
     return plan.forward(x, gamma, beta, y, stats)

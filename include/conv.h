@@ -358,7 +358,7 @@ conv_status conv_block_plan_destroy(conv_block_plan *p);
 typedef enum {
     CONV_ACT_NONE = 0,
     CONV_ACT_RELU = 1,   /* max(z, 0)                                                 */
-    CONV_ACT_SILU = 2    /* z / (1 + exp(-z))                                         */
+    CONV_ACT_SILU = 2    /* z / (1 + exp(-z)), to (|z| + 3) * 2^-24 of its value      */
 } conv_act;
 
 /* ------------------------------------------------------------------------
@@ -424,7 +424,9 @@ conv_status conv_group_norm_forward_int8(conv_group_norm_plan *p, const void *x,
  * h = (x - mean) * rstd,
  *   dbeta[c] = sum u, dgamma[c] = sum u * h   (over n, h, w)
  *   dx = rstd * (u * gamma - mean_S(u * gamma) - h * mean_S(u * gamma * h)).
- * The derivative of ReLU at 0 is 0.  dgamma and dbeta are written, not added to, and
+ * The derivative of ReLU at 0 is 0; its kink lies where z, each operation of the formula rounded
+ * in FP32, puts it.  (The forward pass takes z as (x - mean) * (rstd * gamma) + beta in one fused
+ * step: a value within a rounding of 0 may be on in one and off in the other.)  dgamma and dbeta are written, not added to, and
  * both or neither may be NULL.  Every sum has one fixed order: the same inputs give
  * the same bits.
  */
@@ -449,8 +451,11 @@ conv_status conv_group_norm_plan_destroy(conv_group_norm_plan *p);
  *   w_scale  [N]     FP32
  *   bias     [N]     FP32, may be NULL (0)
  *   y        [M][N]  BF16 or FP32
- * The sum is exact while it stays within 2^24 in magnitude (always for K <= 1024);
- * beyond that it carries FP32 rounding.  Scales, bias and activation are FP32, the
+ * The sum is exact while it stays within 2^24 in magnitude (always for K <= 1024).
+ * Beyond, up to 4 rows still add in 32-bit integers and round once; more rows add in FP32
+ * on the tensor cores, where every 16 products may lose 2^-23 of the magnitudes added so
+ * far (1.5e-4 of a sum of one sign at K = 20000), so that there the last bits of a row
+ * depend on how many rows share the call.  Scales, bias and activation are FP32, the
  * result is rounded once.  A row or channel whose scale is NaN or Inf gives NaN or Inf
  * in its own outputs only.
  * ------------------------------------------------------------------------ */
@@ -459,8 +464,8 @@ typedef struct conv_int8_plan conv_int8_plan; /* opaque, host-owned */
 /*
  * Check the shape and choose the kernel.  *plan gets a new plan, or NULL on error.
  * Returns CONV_ERR_INVALID_ARG for non-positive sizes or an unknown dtype or act,
- * CONV_ERR_UNSUPPORTED for K > 131071 (the sum would pass 32 bits), from 2^30 rows or
- * channels on, or above 2^40 elements of x, w or y, CONV_ERR_CUDA if the device cannot be queried.  Tied to the
+ * CONV_ERR_UNSUPPORTED for K > 131071 (the sum would pass 32 bits), from 2^30 rows on, from
+ * 2^30 channels on with more than 32 rows, or above 2^40 elements of x, w or y, CONV_ERR_CUDA if the device cannot be queried.  Tied to the
  * device current at creation; without a device a host-only plan is made, whose calls
  * return CONV_ERR_CUDA.  out_dtype is y's type.
  */

@@ -476,3 +476,27 @@ def test_a_plan_is_the_same_after_other_calls(act):
         again = [cg.GroupNormPlan(N, C, H, W, G, dtype, act=act).workspace_bytes for N, C, H, W, G in large]
         assert again == made
     torch.cuda.synchronize()
+
+
+def test_silu_over_its_range():
+    """SiLU in FP32, of the norm (flat groups give act(beta)), of its gradient and of the product (no
+    sum: act(bias)).  exp(-z) is 2^(-z log2 e): the product's rounding and the constant's are 1.5 * 2^-24
+    |z| of it, the approximate power 4 * 2^-24, the reciprocal and the sums about it another 4; and
+    1 - sigmoid loses as much again where it cancels."""
+    import cnn_convolution_implicit_gb300 as cg
+    z = torch.linspace(-85.0, 85.0, 4096)
+    y = cg.group_norm(torch.ones(1, 2, 2, 4096, device="cuda"), 32, None, z.cuda(), act="silu")
+    want = ref.activation(_np(z), "silu")
+    bound = (1.5 * np.abs(_np(z)) + 8.0) * ref.U32
+    assert np.all(np.abs(_np(y)[0, 0, 0] - want) <= bound * np.abs(want))
+    for rows in (1, 16, 128):  # the kernels of few rows, of 5 to 64, of many
+        p = cg.int8_matmul(torch.zeros(rows, 16, dtype=torch.int8, device="cuda"), torch.ones(rows, device="cuda"),
+                           torch.ones(4096, 16, dtype=torch.int8, device="cuda"), torch.ones(4096, device="cuda"), z.cuda(),
+                           act="silu", out="f32")
+        assert np.all(np.abs(_np(p)[-1] - want) <= bound * np.abs(want))
+    stats = torch.tensor([[[0.0]], [[1.0]]]).repeat(1, 1, 32).cuda()
+    _, _, dbeta = cg.group_norm_backward(torch.ones(1, 1, 1, 4096, device="cuda"), torch.zeros(1, 1, 1, 4096, device="cuda"),
+                                         stats, 32, None, z.cuda(), act="silu")
+    s = 1.0 / (1.0 + np.exp(-_np(z)))
+    grad, size = s * (1.0 + _np(z) * (1.0 - s)), s * (1.0 + np.abs(_np(z)))
+    assert np.all(np.abs(_np(dbeta) - grad) <= 2 * bound * size)

@@ -85,3 +85,16 @@ def test_few_rows_past_one_chunk_of_k(size):
         ref.check(_np(y), want, tol, out == "bf16", "y")
     assert torch.equal(cg.int8_matmul(x.cuda(), torch.ones(M).cuda(), w.cuda(), torch.ones(N).cuda(), out="f32").cpu().double(),
                        (x.double() @ w.double().t()).float().double())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(1, 3), (8, 1)])
+def test_channels_past_2_30(M, K):
+    N = (1 << 30) + 7
+    x = torch.randint(-127, 128, (M, K), device="cuda", dtype=torch.int32).to(torch.int8)
+    w = torch.empty(N, K, dtype=torch.int8, device="cuda").random_(-127, 128)
+    xs, ws = torch.rand(M, device="cuda") + 0.5, torch.rand(N, device="cuda")
+    y = cg.int8_matmul(x, xs, w, ws)
+    for at in (slice(0, 200), slice(N // 2, N // 2 + 200), slice(N - 200, N)):
+        want, tol = ref.int8_product(x.cpu().numpy(), xs.cpu().numpy(), w[at].cpu().numpy(), ws[at].cpu().numpy(), None, "none")
+        ref.check(_np(y[:, at]), want, tol, True, "y")

@@ -124,3 +124,16 @@ def test_binding_refuses_unknown_words():
         cg.int8_matmul(torch.zeros(2, 8, dtype=torch.int8), torch.ones(2), torch.zeros(4, 8, dtype=torch.int8), torch.ones(4))
     with pytest.raises(ValueError):
         cg.quantize_rows(torch.zeros(2, 8))
+
+
+@pytest.mark.parametrize("args,status", [
+    ((1, 1 << 30, 1, 1, 0), 0), ((32, 1 << 30, 1, 1, 0), 0),     # kernels of few rows: any 31-bit number of channels
+    ((33, 1 << 30, 1, 1, 0), 2), ((400, 1 << 30, 1, 1, 0), 2),   # tiles: below 2^30
+    ((1 << 30, 8, 8, 1, 0), 2), (((1 << 30) - 1, 8, 8, 1, 0), 0),
+])
+def test_int8_create_at_2_30(args, status):
+    L = cg.lib()
+    h = ctypes.c_void_p(1234)
+    assert L.conv_int8_plan_create(ctypes.byref(h), *args) == status
+    if h.value:
+        assert L.conv_int8_plan_destroy(h) == 0
