@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from collections import OrderedDict
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libconv.so")
@@ -139,13 +138,13 @@ def other_device(dev, current):
                       "torch.cuda.device(%d)" % (dev, current, dev))
 
 
-def _need_current(x):
-    """x's device has to be the current one: a plan is made for the current device, and the library
-    launches there (and refuses a plan of another)."""
+def _need_current(dev):
+    """A tensor's device has to be the current one: a plan is made for the current device, and the
+    library launches there (and refuses a plan of another)."""
     import torch
-    current = torch.cuda.current_device()
-    if x.get_device() != current:
-        raise other_device(x.get_device(), current)
+    current = torch._C._cuda_getDevice()
+    if dev != current:
+        raise other_device(dev, current)
 
 
 def _plan_status(fn, plan, stream, name) -> int:
@@ -245,9 +244,11 @@ class ConvPlan:
         dt = torch.bfloat16 if self.dtype == "bf16" else torch.float32
         if not (x.is_cuda and w.is_cuda):
             raise ValueError("x and w must be CUDA tensors")
-        if any(t is not None and t.get_device() != x.get_device() for t in (w, bias if self.bias else None, scale, y)):
+        dev = x.get_device()
+        if w.get_device() != dev or (scale is not None and scale.get_device() != dev) or \
+                (y is not None and y.get_device() != dev) or (self.bias and bias is not None and bias.get_device() != dev):
             raise ValueError("x, w, bias, scale and y must be on one device")
-        _need_current(x)
+        _need_current(dev)
         if x.dtype != dt or w.dtype != dt:
             raise ValueError("x and w must be %s" % dt)
         if tuple(x.shape) != (N, H, W, C_in) or not x.is_contiguous():
@@ -344,7 +345,7 @@ class BlockPlan:
                 raise ValueError("%s must be on x's device" % name)
 
         need(x, "x", (N, H, W, C), torch.float32)
-        _need_current(x)
+        _need_current(x.get_device())
         need(w_dw, "w_dw", (C, K, K), torch.float32)
         need(w_pw, "w_pw", (C_out, C), torch.bfloat16)
         for t, name, n in ((dw_scale, "dw_scale", C), (dw_bias, "dw_bias", C), (pw_scale, "pw_scale", C_out),
@@ -373,40 +374,39 @@ class BlockPlan:
                             "conv_block_plan_device_status")
 
 
-class PlanCache:
-    """Plans of the functional forms, by shape: the ``limit`` used last.  A dropped plan is closed when
-    its last user lets go of it.  (Plans hold status words of a pool of 1,024: shapes that vary,
-    token counts above all, must not use it up.)"""
+class PlanCache(dict):
+    """Plans of the functional forms, by shape, ``limit`` at most.  (Plans hold status words of a pool of
+    1,024: shapes that vary, token counts above all, must not use it up.)  Whoever takes a plan
+    out again marks it (``plan.used = True``); the oldest without a mark makes room, those before it
+    lose theirs and go to the end of the line.  A dropped plan is closed when its last user lets go of it."""
 
     def __init__(self, limit=256):
+        super().__init__()
         self.limit = limit
-        self._plans = OrderedDict()
         self._lock = threading.Lock()
 
-    def get(self, key):
-        with self._lock:
-            plan = self._plans.get(key)
-            if plan is not None:
-                self._plans.move_to_end(key)
-            return plan
-
     def put(self, key, plan):
-        """Keeps ``plan`` and returns it; the plan used longest ago makes room."""
+        """Keeps ``plan`` and returns it."""
         dropped = None
         with self._lock:
-            self._plans[key] = plan
-            if len(self._plans) > self.limit:
-                dropped = self._plans.popitem(last=False)
+            old = list(self)
+            self[key] = plan
+            plan.used = False
+            if len(self) > self.limit:
+                for k in old:
+                    if not self[k].used:
+                        break
+                    self[k].used = False
+                    self[k] = self.pop(k)  # last in line
+                else:
+                    k = old[0]
+                dropped = self.pop(k)
         del dropped  # closed, if at all, outside the lock
         return plan
 
     def clear(self):
         with self._lock:
-            plans, self._plans = self._plans, OrderedDict()
-        plans.clear()
-
-    def __len__(self):
-        return len(self._plans)
+            super().clear()
 
 
 _plan_cache = PlanCache()
@@ -421,7 +421,7 @@ def measure_mma_rate(iters: int = 1 << 16, device=None):
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
     cycles = torch.zeros(sms, dtype=torch.int64, device=dev)
-    _need_current(cycles)
+    _need_current(cycles.get_device())
     stream = torch.cuda.current_stream(dev)
     st = L.conv_measure_mma_rate(int(iters), ctypes.c_void_p(cycles.data_ptr()), sms,
                                  ctypes.c_void_p(stream.cuda_stream))
@@ -443,7 +443,7 @@ def check_wait_timeout(limit_ns: int, device=None):
     L = lib()
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
     elapsed = torch.zeros(1, dtype=torch.int64, device=dev)
-    _need_current(elapsed)
+    _need_current(elapsed.get_device())
     stream = torch.cuda.current_stream(dev)
     st = L.conv_check_wait_timeout(int(limit_ns), ctypes.c_void_p(elapsed.data_ptr()),
                                    ctypes.c_void_p(stream.cuda_stream))
@@ -466,7 +466,9 @@ def conv2d(x, w, bias=None, stride=1, padding=0, dilation=1, groups=1, relu=Fals
     plan = _plan_cache.get(key)
     if plan is None:
         if x.is_cuda:
-            _need_current(x)
+            _need_current(x.get_device())
         plan = _plan_cache.put(key, ConvPlan(N, C_in, H, W, C_out, Kh, Kw, stride, padding, dilation, groups, dtype,
                                              bias is not None, relu, out_bf16))
+    else:
+        plan.used = True
     return plan.forward(x, w, bias, y=y, stream=stream)

@@ -43,15 +43,13 @@ def _choice(value, table, name):
     return table[value]
 
 
-def _device_of(x):
-    """x's CUDA device, which has to be the current one: a plan is made for the current device, and
-    the library launches there (and refuses a plan of another)."""
-    dev = x.get_device()
+def _refuse_device(dev):
+    """Raises unless ``dev``, a tensor's device, is the current one: a plan is made for the current
+    device, and the library launches there (and refuses a plan of another)."""
     if dev < 0:
         raise ValueError("x must be a CUDA tensor")
     if dev != _current_device():
         raise binding.other_device(dev, _current_device())
-    return dev
 
 
 def _need(t, name, shape, dtype, dev):
@@ -114,7 +112,9 @@ class GroupNormPlan:
 
     def _inputs(self, x, gamma, beta, stats):
         """Checks them; returns x's device."""
-        dev = _device_of(x)
+        dev = x.get_device()
+        if dev < 0 or dev != _current_device():
+            _refuse_device(dev)
         _need(x, "x", self.shape, self.torch_dtype, dev)
         if gamma is not None:
             _need(gamma, "gamma", self._channels, _t.float32, dev)
@@ -241,7 +241,9 @@ class Int8MatmulPlan:
 
     def _operands(self, x, w, w_scale, bias, y):
         """Checks all but x's type; returns x's device."""
-        dev = _device_of(x)
+        dev = x.get_device()
+        if dev < 0 or dev != _current_device():
+            _refuse_device(dev)
         _need(x, "x", self._x, x.dtype, dev)
         _need(w, "w", self._w, _t.int8, dev)
         _need(w_scale, "w_scale", self._cols, _t.float32, dev)
@@ -304,10 +306,12 @@ def _norm_plan(x, groups, eps, act):
         _need_any(x, "x", (torch.bfloat16, torch.float32))
         if x.dim() != 4:
             raise ValueError("x must be an NHWC tensor [N][H][W][C]")
-        _device_of(x)
+        _refuse_device(x.get_device())
         N, H, W, C = x.shape
         plan = _norm_plans.put(key, GroupNormPlan(N, C, H, W, groups, "bf16" if x.dtype == torch.bfloat16 else "f32",
                                                   eps, act))
+    else:
+        plan.used = True
     return plan
 
 
@@ -356,8 +360,8 @@ def group_norm(x, groups, gamma=None, beta=None, eps=1e-5, act="none", y=None, s
         with _torch().cuda.stream(stream):
             return group_norm(x, groups, gamma, beta, eps, act, y, stats)
     plan = _norm_plan(x, groups, eps, act)
-    if _t.is_grad_enabled() and (x.requires_grad or (gamma is not None and gamma.requires_grad) or
-                                 (beta is not None and beta.requires_grad)):
+    if (x.requires_grad or (gamma is not None and gamma.requires_grad) or
+            (beta is not None and beta.requires_grad)) and _t.is_grad_enabled():
         if y is not None:
             raise ValueError("y cannot be given where the result's gradient is recorded")
         if stats is not None:
@@ -390,11 +394,13 @@ def _int8_plan(x, w, act, out):
     plan = _int8_plans.get(key)
     if plan is None:
         _torch()
-        _device_of(x)
+        _refuse_device(x.get_device())
         if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
             raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
         N, K = w.shape
         plan = _int8_plans.put(key, Int8MatmulPlan(x.numel() // K if K else 0, N, K, out, act, x.shape))
+    else:
+        plan.used = True
     return plan
 
 
@@ -428,7 +434,8 @@ def quantize_rows(x, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return quantize_rows(x)
-    dev = _device_of(x)
+    dev = x.get_device()
+    _refuse_device(dev)
     q = torch.empty(x.shape, dtype=torch.int8, device=dev)
     scale = torch.empty(M, dtype=torch.float32, device=dev)
     _check(lib().conv_quantize_rows(x.data_ptr(), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, M, K,

@@ -37,7 +37,7 @@ def current(monkeypatch):
     """Device 0 is current; nothing may reach the library's calls."""
     operators._torch()
     monkeypatch.setattr(operators, "_current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)  # as the convolutions ask
     for cache in (operators._norm_plans, operators._int8_plans, binding._plan_cache):
         cache.clear()
     yield

@@ -8,7 +8,7 @@ class Plan:
     pass
 
 
-def test_the_plan_used_longest_ago_makes_room():
+def test_a_plan_that_nobody_took_lately_makes_room():
     cache = binding.PlanCache(limit=3)
     gone = {}
     for k in "abc":
@@ -16,15 +16,30 @@ def test_the_plan_used_longest_ago_makes_room():
         gone[k] = weakref.ref(plan)
         assert cache.get(k) is None and cache.put(k, plan) is plan
     del plan
-    assert cache.get("a") is gone["a"]()          # "b" is now the one used longest ago
-    held = cache.get("b"), cache.get("a"), cache.get("c")
-    cache.put("d", Plan())
-    assert cache.get("b") is None and len(cache) == 3
-    assert gone["b"]() is held[0]                 # a call under way still holds it
+    held = cache.get("a")
+    held.used = True                              # as a call does
+    cache.put("d", Plan())                        # "a" loses its mark and its place, "b" goes
+    assert set(cache) == {"a", "c", "d"} and gone["b"]() is None
+    cache.put("e", Plan())
+    assert set(cache) == {"a", "d", "e"} and gone["c"]() is None
+    for k in "fghij":
+        cache.put(k, Plan())
+        assert len(cache) == 3 and cache.get(k) is not None
+    assert cache.get("a") is None and gone["a"]() is held   # a call under way still holds it
     del held
-    assert gone["b"]() is None and gone["a"]() is not None
+    assert gone["a"]() is None
     cache.clear()
-    assert len(cache) == 0 and gone["a"]() is None
+    assert len(cache) == 0
+
+
+def test_a_plan_in_use_stays():
+    cache = binding.PlanCache(limit=8)
+    hot = cache.put("hot", Plan())
+    for k in range(1000):
+        assert cache.get("hot") is hot
+        hot.used = True
+        cache.put(k, Plan())
+    assert len(cache) == 8
 
 
 def test_every_functional_form_is_bounded():
