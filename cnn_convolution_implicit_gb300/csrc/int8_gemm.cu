@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         cluster_sync_all();  // every part is in place
         const Walk w = walk_from<PAIR, BN>(tiles, unit0);
         join_parts<BN>(p, reinterpret_cast<const float*>(smem), w.m0, w.n0, cta, splits);
+        __syncwarp();  // the aligned barrier takes a warp's lanes together
         cluster_sync_all();  // no CTA leaves while another may still read its part
     }
     if (warp == kMmaWarp) {
