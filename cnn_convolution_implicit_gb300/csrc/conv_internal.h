@@ -10,31 +10,28 @@
 
 namespace convgb {
 
-// Per-device dynamic shared-memory limit of one kernel (zero-initialised when declared
-// static; atomic, so plans driven from different host threads may launch the same kernel
-// concurrently).
+// Per-device dynamic shared-memory limit already set on one kernel (zero-initialised
+// when declared static; atomic, so plans driven from different host threads may
+// launch the same kernel concurrently).
 using SmemLimitCache = std::atomic<int>[64];
 
-// Raise a kernel's dynamic shared-memory limit, a per-function attribute, before its first use on
-// this device: to all that a block may have, so that no later call sets it again.  (Set to
-// what the call at hand needs, a second thread or a second record of the same kernel could
-// lower it below what another launch or occupancy query counts on.)  `limits` remembers that
-// it is done: a plan's later launches cost no extra runtime call.
+// Raise a kernel's dynamic shared-memory limit only when a launch needs more
+// than what was set before on this device (`limits` is the caller's per-kernel
+// cache).  The limit is a per-function attribute, so a plan's later launches
+// cost no extra runtime call.  Concurrent first calls may both set it: harmless,
+// and the cache only ever grows.
 inline cudaError_t ensure_smem_limit(const void* func, int bytes, SmemLimitCache& limits) {
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool remember = dev >= 0 && dev < 64;
-    if (remember && limits[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
-    int most = 0;
-    cudaFuncAttributes attr;
-    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, func);
-    if (e != cudaSuccess) return e;
-    most -= static_cast<int>(attr.sharedSizeBytes);
-    if (bytes > most) return cudaErrorInvalidValue;
-    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess && remember) limits[dev].store(most, std::memory_order_relaxed);
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    }
+    if (limits[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) {
+        int cur = limits[dev].load(std::memory_order_relaxed);
+        while (cur < bytes && !limits[dev].compare_exchange_weak(cur, bytes, std::memory_order_relaxed)) {
+        }
+    }
     return e;
 }
 

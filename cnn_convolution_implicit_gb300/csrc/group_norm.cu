@@ -1397,7 +1397,9 @@ dim3 stream_grid(const NormParams& p) {
 
 namespace {
 
-// Each kernel with its own record of the shared-memory limit.
+// Each kernel with its one record of the shared-memory limit, which is set once, to all that a block may
+// have: a limit set to each map's need, by the launches and by the occupancy query on records of their own, sank
+// below what the query counted on after a smaller map had run, and between two threads below what the other launches.
 template <typename T, int MODE, int ACT>
 SmemLimitCache& resident_limits() {
     static SmemLimitCache limits;
@@ -1432,7 +1434,7 @@ size_t resident_smem(const NormParams& p, int mode) {
 template <typename K>
 cudaError_t resident_config(K* fn, SmemLimitCache& limits, const NormParams& p, int mode, cudaStream_t stream,
                             cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[1]) {
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), p.smem_bytes, limits);
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), p.smem_optin, limits);
     cfg = cudaLaunchConfig_t();
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.N) * (p.C / p.chunk) * p.splits));
     cfg.blockDim = dim3(kResThreads);
@@ -1467,7 +1469,7 @@ cudaError_t launch_resident(const NormParams& p, int mode, cudaStream_t stream) 
 // takes up to 64 bytes a pixel (128 make clusters of 16, of which a GPC holds fewer: 32 x 112 x 112 x 256
 // BF16, SiLU, took 113 us with 128, 97 with 64, 122 with 32) and the fewest CTAs that hold it
 // two to an SM, then one to an SM.  More CTAs while there are fewer than SMs.
-void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
+void norm_pick_resident(NormParams& p, int mode, int num_sms) {
     const int es = p.bf16 ? 2 : 4, tensors = mode == kNormBackward ? 2 : 1;
     p.chunk = 0;
     if (p.vec * es != 16 || static_cast<long long>(p.P) * (p.C / p.vec) >= (1LL << 31)) return;
@@ -1482,7 +1484,7 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
         t.smem_bytes = static_cast<int>(resident_smem(t, mode));
         return t.smem_bytes <= limit;
     };
-    const int half = smem_optin / 2 - 1024;  // of an SM, less what a CTA needs besides
+    const int half = p.smem_optin / 2 - 1024;  // of an SM, less what a CTA needs besides
     int chunk = 0;
     if (mode == kNormInt8) {
         chunk = p.C;
@@ -1501,14 +1503,14 @@ void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin) {
     const int rows = rows_of(chunk);
     const long long units = static_cast<long long>(p.N) * (p.C / chunk);
     int best = 0;
-    for (int limit : {half, smem_optin}) {
+    for (int limit : {half, p.smem_optin}) {
         for (int cluster = 1; cluster <= kResMaxCluster && best == 0; ++cluster)
             if (fits(chunk, cluster, limit)) best = cluster;
         if (best != 0) break;
     }
     if (best == 0 || units * best > 0x7fffffffLL) return;
     while (2 * best <= kResMaxCluster && units * best * 2 <= num_sms && p.P >= 2 * best * rows) best *= 2;
-    fits(chunk, best, smem_optin);
+    fits(chunk, best, p.smem_optin);
     t.pix_base = t.P / best;
     t.pix_more = t.P % best;
     p = t;

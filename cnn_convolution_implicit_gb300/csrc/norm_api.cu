@@ -111,6 +111,7 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
     p.eps = eps;
     p.act = act;
     p.bf16 = dtype == CONV_BF16;
+    p.smem_optin = smem_optin;
     p.vec = p.bf16 ? 8 : 4;
     while (C % p.vec != 0) p.vec /= 2;
     // By channel, where no other form fits: about eight CTAs an SM, at least four pixels a thread.
@@ -126,7 +127,7 @@ conv_status conv_group_norm_plan_create(conv_group_norm_plan** out, int N, int C
         NormParams& m = pl->np[mode];
         m = p;
         NormParams two = p;
-        norm_pick_resident(m, mode, pl->num_sms, smem_optin);
+        norm_pick_resident(m, mode, pl->num_sms);
         norm_pick_two_pass(two, mode, pl->num_sms);
         int at_a_time = 0;
         if (m.chunk != 0)

@@ -26,6 +26,7 @@ struct NormParams {
     int chunk;
     int items;       // 16-byte vectors a thread holds of each tensor
     int smem_bytes;
+    int smem_optin;  // what the device lets a block have
     int pix_base, pix_more;  // pixels of a CTA of the cluster or of a range, and how many have one more
     const void* x;
     const void* dy;
@@ -54,7 +55,7 @@ size_t norm_part_entries(const NormParams& p);
 size_t norm_ab_entries(const NormParams& p);
 void norm_pick_two_pass(NormParams& p, int mode, int num_sms);
 // Fills the resident form's fields for a mode, or leaves chunk 0 where it does not fit.
-void norm_pick_resident(NormParams& p, int mode, int num_sms, int smem_optin);
+void norm_pick_resident(NormParams& p, int mode, int num_sms);
 // Clusters of that shape that the device runs at a time, 0 where it runs none (called once per plan,
 // with its device current).
 int norm_resident_at_a_time(const NormParams& p, int mode, int num_sms);
