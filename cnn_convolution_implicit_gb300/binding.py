@@ -31,7 +31,11 @@ EXPORTS = ("conv_plan_create", "conv_plan_output_shape", "conv_plan_info", "conv
            "conv_group_norm_plan_create", "conv_group_norm_workspace", "conv_group_norm_forward",
            "conv_group_norm_forward_int8", "conv_group_norm_backward", "conv_group_norm_plan_destroy",
            "conv_int8_plan_create", "conv_int8_plan_info", "conv_int8_forward", "conv_int8_workspace", "conv_int8_forward_quantize",
-           "conv_int8_plan_device_status", "conv_int8_plan_destroy", "conv_quantize_rows")
+           "conv_int8_plan_device_status", "conv_int8_plan_destroy", "conv_quantize_rows",
+           "conv_rms_norm_plan_create", "conv_rms_norm_workspace", "conv_rms_norm_forward", "conv_rms_norm_forward_int8",
+           "conv_rms_norm_backward", "conv_rms_norm_plan_destroy", "conv_dropout", "conv_linear_plan_create",
+           "conv_linear_workspace", "conv_linear_forward", "conv_linear_backward", "conv_linear_plan_device_status",
+           "conv_linear_plan_destroy")
 CONV_BLOCK_DW_RELU, CONV_BLOCK_PW_RELU = 1, 2
 
 _lock = threading.Lock()
@@ -117,8 +121,22 @@ def lib():
             L.conv_int8_plan_device_status.argtypes = [vp, vp, ctypes.POINTER(c_int)]
             L.conv_int8_plan_destroy.argtypes = [vp]
             L.conv_quantize_rows.argtypes = [vp, c_int, c_int, c_int, vp, vp, vp]
+            L.conv_rms_norm_plan_create.argtypes = [ctypes.POINTER(vp), c_int, c_int, ctypes.c_float, c_int]
+            L.conv_rms_norm_workspace.argtypes = [vp, ctypes.POINTER(c_ull)]
+            L.conv_rms_norm_forward.argtypes = [vp] * 8
+            L.conv_rms_norm_forward_int8.argtypes = [vp] * 9
+            L.conv_rms_norm_backward.argtypes = [vp] * 10
+            L.conv_rms_norm_plan_destroy.argtypes = [vp]
+            L.conv_dropout.argtypes = [vp, vp, c_int, c_ull, ctypes.c_double, vp, vp, vp]
+            L.conv_linear_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 4
+            L.conv_linear_workspace.argtypes = [vp, ctypes.POINTER(c_ull), ctypes.POINTER(c_ull)]
+            L.conv_linear_forward.argtypes = [vp] * 9
+            L.conv_linear_backward.argtypes = [vp] * 10
+            L.conv_linear_plan_device_status.argtypes = [vp, vp, ctypes.POINTER(c_int)]
+            L.conv_linear_plan_destroy.argtypes = [vp]
             for name in EXPORTS:
-                if name.startswith(("conv_group_norm", "conv_int8", "conv_quantize")):
+                if name.startswith(("conv_group_norm", "conv_int8", "conv_quantize", "conv_rms_norm", "conv_dropout",
+                                    "conv_linear")):
                     getattr(L, name).restype = c_int
             _lib = L
         return _lib

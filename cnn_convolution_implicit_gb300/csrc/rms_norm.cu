@@ -1,0 +1,525 @@
+// rms_norm.cu -- root-mean-square norm of rows with the residual's addition, forward (also to 8 bits)
+// and backward:
+//
+//   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * gamma
+//   n = h * rstd, d = dy * gamma:  dx = rstd * (d - n * mean(d * n)) + dh,  dgamma = sum over rows of dy * n
+//
+// Bound by memory.  A row stays in the registers of the 1, 4, 8 or 16 warps that hold it, so every byte
+// crosses the bus once; rows past what 16 warps hold are swept twice (three times to 8 bits).
+//
+// A row starts at any element.  It is handled as the aligned 16-byte granules that it touches: all tensors
+// of a call have the same shape, so a row begins at the same place of a granule in each of them; the
+// first and last granule, shared with the neighbouring rows, are read and written by elements.
+//
+// dgamma: the register form keeps each thread's columns over all the rows that its CTA takes, where
+// a thread has the same columns in every row (rows on 16 bytes); other rows take a kernel of its own that reads
+// dy and h by column.  Either way parts of it meet in the workspace and are added in one order.
+#include <type_traits>
+
+#include "pointwise_math.cuh"
+#include "rows_internal.h"
+
+namespace convgb {
+
+namespace {
+
+// One row as granules: granule i holds columns first(i) .. first(i) + V - 1.
+template <typename T, bool ALIGNED>
+struct Row {
+    static constexpr int V = 16 / sizeof(T), H = V / 2;
+    long long granule;  // the row's first one
+    int off, C, count;
+
+    __device__ __forceinline__ Row(long long m, int C_) : C(C_) {
+        const long long at = m * C_;
+        granule = at / V;
+        off = ALIGNED ? 0 : static_cast<int>(at % V);
+        count = (off + C + V - 1) / V;
+    }
+    __device__ __forceinline__ int first(int i) const { return i * V - off; }
+    __device__ __forceinline__ bool whole(int i) const { return ALIGNED || (first(i) >= 0 && first(i) + V <= C); }
+
+    __device__ __forceinline__ void load(const void* base, int i, f2 (&f)[H]) const {
+        const T* p = static_cast<const T*>(base) + (granule + i) * V;
+        if (whole(i)) {
+            VecIo<T, V>::unpack(__ldcs(reinterpret_cast<const uint4*>(p)), f);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) f[j] = f2_make(element(p, i, 2 * j), element(p, i, 2 * j + 1));
+    }
+    __device__ __forceinline__ void store(void* base, int i, const f2 (&f)[H]) const {
+        T* p = static_cast<T*>(base) + (granule + i) * V;
+        if (whole(i)) {
+            *reinterpret_cast<uint4*>(p) = VecIo<T, V>::pack(f);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            put(p, i, 2 * j, f2_lo(f[j]));
+            put(p, i, 2 * j + 1, f2_hi(f[j]));
+        }
+    }
+    __device__ __forceinline__ void store8(int8_t* base, int i, const f2 (&f)[H], const RowFactor& r) const {
+        int8_t* p = base + (granule + i) * V;
+        if (whole(i)) {
+            quantise_store<V>(p, f, r);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (inside(i, j)) p[j] = quantise1(j & 1 ? f2_hi(f[j / 2]) : f2_lo(f[j / 2]), r);
+    }
+    // gamma of the granule's columns (1 without gamma), 0 outside the row
+    __device__ __forceinline__ void weights(const float* gamma, int i, f2 (&g)[H]) const {
+        if (gamma == nullptr) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) g[j] = f2_dup(1.0f);
+        } else if constexpr (ALIGNED) {
+#pragma unroll
+            for (int j = 0; j < H; j += 2) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(gamma + first(i) + 2 * j));
+                g[j] = f2_make(v.x, v.y);
+                g[j + 1] = f2_make(v.z, v.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                g[j] = f2_make(inside(i, 2 * j) ? __ldg(gamma + first(i) + 2 * j) : 0.0f,
+                               inside(i, 2 * j + 1) ? __ldg(gamma + first(i) + 2 * j + 1) : 0.0f);
+        }
+    }
+
+private:
+    __device__ __forceinline__ bool inside(int i, int j) const {
+        return static_cast<unsigned>(first(i) + j) < static_cast<unsigned>(C);
+    }
+    __device__ __forceinline__ float element(const T* p, int i, int j) const {
+        return inside(i, j) ? static_cast<float>(p[j]) : 0.0f;
+    }
+    __device__ __forceinline__ void put(T* p, int i, int j, float v) const {
+        if (inside(i, j)) p[j] = static_cast<T>(v);  // rounds to nearest even
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
+    return v;
+}
+
+// Over the WARPS warps of a row (a CTA, or one warp of it); `buf` is used once.
+template <int WARPS>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
+    v = warp_sum(v);
+    if constexpr (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) v += buf[i];
+    }
+    return v;
+}
+
+template <int WARPS>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
+    v = warp_max(v);
+    if constexpr (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) v = max(v, buf[i]);
+    }
+    return v;
+}
+
+__device__ __forceinline__ float reciprocal_root(float sum, int C, float eps) {
+    return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(C)), eps));
+}
+
+constexpr int kRowsOfWarps = 4;  // rows of one warp each that a CTA takes
+template <int WARPS>
+constexpr int kThreadsOf = 32 * (WARPS == 1 ? kRowsOfWarps : WARPS);
+
+// This thread's place: its row, and where it starts among the row's threads.
+template <int WARPS>
+__device__ __forceinline__ int row_thread() { return WARPS == 1 ? threadIdx.x & 31 : threadIdx.x; }
+
+// ---------------------------------------------------------------- forward
+template <typename T, bool ALIGNED, int ITEMS, int WARPS, bool INT8>
+__global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_forward_kernel(const RmsParams p) {
+    using R = Row<T, ALIGNED>;
+    __shared__ float sums[WARPS];
+    __shared__ uint32_t tops[WARPS];
+    const long long m = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kRowsOfWarps + (threadIdx.x >> 5) : blockIdx.x;
+    if (m >= p.M) return;  // whole warps of their own rows
+    const R row(m, p.C);
+    const int t = row_thread<WARPS>();
+    f2 v[ITEMS][R::H], square = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = t + k * 32 * WARPS;
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) v[k][j] = 0;
+        if (i < row.count) row.load(p.x, i, v[k]);
+    }
+    if (p.r != nullptr) {
+        f2 r[ITEMS][R::H];
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = t + k * 32 * WARPS;
+#pragma unroll
+            for (int j = 0; j < R::H; ++j) r[k][j] = 0;
+            if (i < row.count) row.load(p.r, i, r[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = t + k * 32 * WARPS;
+#pragma unroll
+            for (int j = 0; j < R::H; ++j) v[k][j] = f2_add(v[k][j], r[k][j]);
+            if (p.h != nullptr && i < row.count) row.store(p.h, i, v[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) square = f2_fma(v[k][j], v[k][j], square);
+    const float rstd = reciprocal_root(row_sum<WARPS>(f2_lo(square) + f2_hi(square), sums), p.C, p.eps);
+    if (t == 0 && p.rstd != nullptr) p.rstd[m] = rstd;
+    const f2 factor = f2_dup(rstd);
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = t + k * 32 * WARPS;
+        if (i >= row.count) break;
+        f2 g[R::H];
+        row.weights(p.gamma, i, g);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) {
+            v[k][j] = f2_mul(f2_mul(v[k][j], factor), g[j]);
+            if constexpr (INT8) top = magnitude(top, v[k][j]);
+        }
+        if constexpr (!INT8) row.store(p.y, i, v[k]);
+    }
+    if constexpr (INT8) {
+        const RowScale rs = row_scale(row_max<WARPS>(magnitude_bits(top), tops));
+        if (t == 0) p.scale[m] = rs.scale;
+        const RowFactor rf = row_factor(rs.inv);
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = t + k * 32 * WARPS;
+            if (i < row.count) row.store8(p.q, i, v[k], rf);
+        }
+    }
+}
+
+// Rows that no 16 warps hold, swept again for every step.  h is written in the last sweep: it may be the
+// residual.
+constexpr int kLongWarps = 16, kLongThreads = 32 * kLongWarps;
+
+template <typename T, bool ALIGNED, bool INT8>
+__global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(const RmsParams p) {
+    using R = Row<T, ALIGNED>;
+    __shared__ float sums[kLongWarps];
+    __shared__ uint32_t tops[kLongWarps];
+    const long long m = blockIdx.x;
+    const R row(m, p.C);
+    const auto sum_of = [&](int i, f2(&v)[R::H]) {
+        row.load(p.x, i, v);
+        if (p.r == nullptr) return;
+        f2 r[R::H];
+        row.load(p.r, i, r);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) v[j] = f2_add(v[j], r[j]);
+    };
+    f2 square = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < row.count; i += kLongThreads) {
+        f2 v[R::H];
+        sum_of(i, v);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) square = f2_fma(v[j], v[j], square);
+    }
+    const float rstd = reciprocal_root(row_sum<kLongWarps>(f2_lo(square) + f2_hi(square), sums), p.C, p.eps);
+    if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[m] = rstd;
+    const f2 factor = f2_dup(rstd);
+    const auto norm_of = [&](int i, f2(&v)[R::H]) {
+        f2 g[R::H];
+        row.weights(p.gamma, i, g);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) v[j] = f2_mul(f2_mul(v[j], factor), g[j]);
+    };
+    RowScale rs = {};
+    if constexpr (INT8) {
+        float top = 0.0f;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < row.count; i += kLongThreads) {
+            f2 v[R::H];
+            sum_of(i, v);
+            norm_of(i, v);
+#pragma unroll
+            for (int j = 0; j < R::H; ++j) top = magnitude(top, v[j]);
+        }
+        rs = row_scale(row_max<kLongWarps>(magnitude_bits(top), tops));
+        if (threadIdx.x == 0) p.scale[m] = rs.scale;
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < row.count; i += kLongThreads) {
+        f2 v[R::H];
+        sum_of(i, v);
+        if (p.h != nullptr) row.store(p.h, i, v);
+        norm_of(i, v);
+        if constexpr (INT8) row.store8(p.q, i, v, row_factor(rs.inv));
+        else row.store(p.y, i, v);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// Rows in registers, `gridDim.x` CTAs over them.  DGAMMA: this thread's columns of dgamma, over its rows.
+template <typename T, bool ALIGNED, int ITEMS, int WARPS, bool DGAMMA>
+__global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const RmsParams p) {
+    static_assert(ALIGNED || !DGAMMA, "a thread's columns move from row to row");
+    using R = Row<T, ALIGNED>;
+    constexpr int kRows = WARPS == 1 ? kRowsOfWarps : 1;
+    __shared__ float sums[2][WARPS];
+    const int t = row_thread<WARPS>();
+    const int slot = WARPS == 1 ? threadIdx.x >> 5 : 0;
+    f2 total[DGAMMA ? ITEMS : 1][R::H] = {};
+    int turn = 0;
+    for (long long m = static_cast<long long>(blockIdx.x) * kRows + slot; m < p.M;
+         m += static_cast<long long>(gridDim.x) * kRows, turn ^= 1) {
+        const R row(m, p.C);
+        const f2 factor = f2_dup(p.rstd[m]);
+        f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = t + k * 32 * WARPS;
+#pragma unroll
+            for (int j = 0; j < R::H; ++j) d[k][j] = n[k][j] = 0;
+            if (i >= row.count) continue;
+            row.load(p.x, i, d[k]);
+            row.load(p.h_in, i, n[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = t + k * 32 * WARPS;
+            if (i >= row.count) continue;
+            f2 g[R::H];
+            row.weights(p.gamma, i, g);
+#pragma unroll
+            for (int j = 0; j < R::H; ++j) {
+                n[k][j] = f2_mul(n[k][j], factor);
+                if constexpr (DGAMMA) total[k][j] = f2_fma(d[k][j], n[k][j], total[k][j]);
+                d[k][j] = f2_mul(d[k][j], g[j]);
+                dot = f2_fma(d[k][j], n[k][j], dot);
+            }
+        }
+        const float mean = __fdiv_rn(row_sum<WARPS>(f2_lo(dot) + f2_hi(dot), sums[turn]), static_cast<float>(p.C));
+        const f2 minus = f2_dup(-mean);
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int i = t + k * 32 * WARPS;
+            if (i >= row.count) continue;
+            f2 r[R::H] = {};
+            if (p.r != nullptr) row.load(p.r, i, r);
+#pragma unroll
+            for (int j = 0; j < R::H; ++j) d[k][j] = f2_fma(f2_fma(n[k][j], minus, d[k][j]), factor, r[j]);
+            row.store(p.y, i, d[k]);
+        }
+    }
+    if constexpr (DGAMMA) {
+        float* part = p.part + (static_cast<long long>(blockIdx.x) * kRows + slot) * p.C;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int c = (t + k * 32 * WARPS) * R::V;
+            if (c >= p.C) continue;
+#pragma unroll
+            for (int j = 0; j < R::H; j += 2)
+                *reinterpret_cast<float4*>(part + c + 2 * j) =
+                    make_float4(f2_lo(total[k][j]), f2_hi(total[k][j]), f2_lo(total[k][j + 1]), f2_hi(total[k][j + 1]));
+        }
+    }
+}
+
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kLongThreads) rms_backward_long_kernel(const RmsParams p) {
+    using R = Row<T, ALIGNED>;
+    __shared__ float sums[kLongWarps];
+    const long long m = blockIdx.x;
+    const R row(m, p.C);
+    const f2 factor = f2_dup(p.rstd[m]);
+    const auto scaled = [&](int i, f2(&d)[R::H], f2(&n)[R::H]) {
+        row.load(p.x, i, d);
+        row.load(p.h_in, i, n);
+        f2 g[R::H];
+        row.weights(p.gamma, i, g);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) {
+            n[j] = f2_mul(n[j], factor);
+            d[j] = f2_mul(d[j], g[j]);
+        }
+    };
+    f2 dot = 0;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < row.count; i += kLongThreads) {
+        f2 d[R::H], n[R::H];
+        scaled(i, d, n);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) dot = f2_fma(d[j], n[j], dot);
+    }
+    const f2 minus = f2_dup(-__fdiv_rn(row_sum<kLongWarps>(f2_lo(dot) + f2_hi(dot), sums), static_cast<float>(p.C)));
+#pragma unroll 1
+    for (int i = threadIdx.x; i < row.count; i += kLongThreads) {
+        f2 d[R::H], n[R::H], r[R::H] = {};
+        scaled(i, d, n);
+        if (p.r != nullptr) row.load(p.r, i, r);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) d[j] = f2_fma(f2_fma(n[j], minus, d[j]), factor, r[j]);
+        row.store(p.y, i, d);
+    }
+}
+
+// dgamma by column: block (x, y) adds rows y, y + gridDim.y, ... eight at a time of 32 columns.
+constexpr int kColumnRows = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(256) rms_columns_kernel(const RmsParams p) {
+    __shared__ float sums[kColumnRows][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const T* dy = static_cast<const T*>(p.x);
+    const T* h = static_cast<const T*>(p.h_in);
+    float total = 0.0f;
+    if (c < p.C) {
+#pragma unroll 4
+        for (long long m = static_cast<long long>(blockIdx.y) * kColumnRows + warp; m < p.M;
+             m += static_cast<long long>(gridDim.y) * kColumnRows)
+            total = fmaf(static_cast<float>(dy[m * p.C + c]), static_cast<float>(h[m * p.C + c]) * p.rstd[m], total);
+    }
+    sums[warp][lane] = total;
+    __syncthreads();
+    if (warp == 0 && c < p.C) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kColumnRows; ++i) sum += sums[i][lane];
+        p.part[static_cast<long long>(blockIdx.y) * p.C + c] = sum;
+    }
+}
+
+// dgamma from its parts, 32 columns a CTA, in one order.
+__global__ void __launch_bounds__(1024) rms_join_kernel(const float* part, int parts, int C, float* dgamma) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float total = 0.0f;
+    if (c < C) {
+#pragma unroll 4
+        for (int i = warp; i < parts; i += 32) total += part[static_cast<long long>(i) * C + c];
+    }
+    sums[warp][lane] = total;
+    __syncthreads();
+    const float sum = warp_sum(sums[lane][warp]);  // column `warp` of the block
+    if (lane == 0 && blockIdx.x * 32 + warp < C) dgamma[blockIdx.x * 32 + warp] = sum;
+}
+
+// ---------------------------------------------------------------- launches
+struct Form {
+    int items, warps;  // 0: rows too long for registers
+};
+
+// Granules a thread holds of each tensor, and warps to a row.
+Form pick_form(const RmsParams& p) {
+    const int V = p.bf16 ? 8 : 4;
+    const int granules = p.C % V == 0 ? p.C / V : (p.C + V - 2) / V + 1;  // the most that a row touches
+    if (granules <= 32) return {1, 1};
+    if (granules <= 64) return {2, 1};
+    if (granules <= 128) return {4, 1};
+    if (granules <= 256) return {2, 4};
+    if (granules <= 512) return {4, 4};
+    if (granules <= 1024) return {4, 8};
+    if (granules <= 2048) return {4, 16};
+    return {0, 0};
+}
+
+bool aligned_rows(const RmsParams& p) { return p.C % (p.bf16 ? 8 : 4) == 0; }
+
+template <typename F>
+void by_form(const Form& f, F&& run) {
+    if (f.warps == 1 && f.items == 1) run(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    else if (f.warps == 1 && f.items == 2) run(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
+    else if (f.warps == 1) run(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+    else if (f.warps == 4 && f.items == 2) run(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
+    else if (f.warps == 4) run(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
+    else if (f.warps == 8) run(std::integral_constant<int, 4>(), std::integral_constant<int, 8>());
+    else run(std::integral_constant<int, 4>(), std::integral_constant<int, 16>());
+}
+
+template <typename T, bool ALIGNED, bool INT8>
+cudaError_t forward(const RmsParams& p, cudaStream_t stream) {
+    const Form f = pick_form(p);
+    if (f.warps == 0) {
+        rms_forward_long_kernel<T, ALIGNED, INT8><<<p.M, kLongThreads, 0, stream>>>(p);
+    } else {
+        by_form(f, [&](auto items, auto warps) {
+            constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
+            rms_forward_kernel<T, ALIGNED, I, W, INT8><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+        });
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, bool ALIGNED>
+cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
+    const Form f = pick_form(p);
+    const unsigned blocks = (p.C + 31) / 32;
+    const bool by_column = p.dgamma != nullptr && (!ALIGNED || f.warps == 0);
+    if (by_column) rms_columns_kernel<T><<<dim3(blocks, p.parts), 256, 0, stream>>>(p);  // first: dx may be dy
+    if (f.warps == 0) {
+        rms_backward_long_kernel<T, ALIGNED><<<p.M, kLongThreads, 0, stream>>>(p);
+    } else {
+        by_form(f, [&](auto items, auto warps) {
+            constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
+            if constexpr (ALIGNED) {
+                if (p.dgamma != nullptr) {
+                    rms_backward_kernel<T, true, I, W, true><<<p.parts / rows, kThreadsOf<W>, 0, stream>>>(p);
+                    return;
+                }
+            }
+            rms_backward_kernel<T, ALIGNED, I, W, false><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+        });
+    }
+    if (p.dgamma != nullptr) rms_join_kernel<<<blocks, 1024, 0, stream>>>(p.part, p.parts, p.C, p.dgamma);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int rms_backward_parts(const RmsParams& p, int num_sms) {
+    const Form f = pick_form(p);
+    if (aligned_rows(p) && f.warps != 0) {  // CTAs over the rows, times the rows that each takes at a time
+        const int rows = f.warps == 1 ? kRowsOfWarps : 1;
+        const long long need = (static_cast<long long>(p.M) + rows - 1) / rows, most = static_cast<long long>(num_sms) * (f.warps <= 4 ? 4 : 16 / f.warps);
+        return static_cast<int>(need < most ? need : most) * rows;
+    }
+    // by column: about four CTAs an SM
+    const long long columns = (p.C + 31) / 32, need = (static_cast<long long>(p.M) + 4 * kColumnRows - 1) / (4 * kColumnRows);
+    const long long most = (4LL * num_sms + columns - 1) / columns;
+    return static_cast<int>(need < most ? need : most);
+}
+
+cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream) {
+    const bool aligned = aligned_rows(p);
+    const auto run = [&](auto element) {
+        using T = decltype(element);
+        if (p.q != nullptr) return aligned ? forward<T, true, true>(p, stream) : forward<T, false, true>(p, stream);
+        return aligned ? forward<T, true, false>(p, stream) : forward<T, false, false>(p, stream);
+    };
+    return p.bf16 ? run(__nv_bfloat16()) : run(float());
+}
+
+cudaError_t launch_rms_backward(const RmsParams& p, cudaStream_t stream) {
+    if (p.bf16) return aligned_rows(p) ? backward<__nv_bfloat16, true>(p, stream) : backward<__nv_bfloat16, false>(p, stream);
+    return aligned_rows(p) ? backward<float, true>(p, stream) : backward<float, false>(p, stream);
+}
+
+}  // namespace convgb

@@ -1,0 +1,51 @@
+// rows_internal.h -- parameter blocks and launchers shared between the C ABI of the row operators
+// (rows_api.cu) and their kernels (rms_norm.cu, dropout.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "conv_internal.h"
+
+namespace convgb {
+
+// Root-mean-square norm over [M][C].
+struct RmsParams {
+    int M, C;
+    float eps;
+    int bf16;            // element type (else FP32)
+    const void* x;       // forward: x; backward: dy
+    const void* r;       // forward: residual; backward: dh (nullptr: 0)
+    const void* h_in;    // backward: the forward pass's h
+    const float* gamma;  // nullptr: 1
+    void* y;             // forward: y; backward: dx
+    void* h;             // forward: x + residual, rounded (nullptr: not wanted)
+    int8_t* q;           // 8-bit output, instead of y
+    float* scale;        // its row scales
+    float* rstd;         // forward: written where given; backward: read
+    float* dgamma;       // nullptr: not wanted
+    float* part;         // workspace: [parts][C] sums of dy * n
+    int parts;
+};
+
+// Rows of sums that the backward pass leaves in the workspace.
+int rms_backward_parts(const RmsParams& p, int num_sms);
+cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream);
+cudaError_t launch_rms_backward(const RmsParams& p, cudaStream_t stream);
+
+struct DropoutParams {
+    const void* x;
+    const void* r;  // nullptr: 0
+    void* y;
+    unsigned long long n;
+    const unsigned long long* state;  // seed, offset
+    uint32_t threshold;               // words below it drop
+    float scale;                      // 1 / (1 - p)
+    int none_left;                    // p = 1
+    int bf16;
+};
+
+cudaError_t launch_dropout(const DropoutParams& p, int num_sms, cudaStream_t stream);
+
+}  // namespace convgb

@@ -1,0 +1,464 @@
+"""The residual branch of a layer, on rows (tokens, pixels): the BF16 linear layer, the
+root-mean-square norm and dropout; ctypes binding of conv_linear_*, conv_rms_norm_* and conv_dropout
+(include/conv.h).
+
+Argument checks and marshalling only, as in operators.py: every step runs in the library's CUDA
+kernels, on torch's current stream or, with ``stream``, as if that were it.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import binding, operators as _ops
+from .binding import CONV_BF16, CONV_F32, _plan_status, lib
+from .operators import ACTS, _DTYPES, _check, _choice, _need, _need_any, _ptr, _refuse_device, _torch, _torch_dtypes, _workspace
+
+
+def _device_of(x):
+    """x's device, which has to be the current one."""
+    dev = x.get_device()
+    if dev < 0 or dev != _ops._current_device():
+        _refuse_device(dev)
+    return dev
+
+
+def _recorded(*tensors):
+    """Whether torch records a gradient for any of them."""
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return _ops._t.is_grad_enabled()
+    return False
+
+
+def _upstream(dy):
+    """A gradient as autograd hands it over, as the kernels take it."""
+    dy = dy.contiguous()
+    return dy.clone() if dy.data_ptr() % 16 else dy  # a slice of a larger tensor
+
+
+class _Plan:
+    _plan = None
+
+    def close(self):
+        if self._plan is not None and binding._lib is not None:
+            getattr(binding._lib, self._destroy)(self._plan)
+        self._plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LinearPlan(_Plan):
+    """Linear layer of one shape in BF16 (include/conv.h, conv_linear_*):
+    z[m][n] = sum_k x[m][k] * w[n][k] + bias[n], y = act(z) + residual, x [M][K], w [N][K], FP32 bias
+    [N], residual, y and z [M][N].  ``x_shape`` [..., K] with M rows in all: x has that shape instead, and
+    residual, y and z [..., N]."""
+
+    _destroy = "conv_linear_plan_destroy"
+
+    def __init__(self, M, N, K, act="none", x_shape=None):
+        L = lib()
+        h = ctypes.c_void_p()
+        _check(L.conv_linear_plan_create(ctypes.byref(h), M, N, K, _choice(act, ACTS, "act")), "conv_linear_plan_create")
+        self._plan = h
+        self._L = L
+        torch = _torch()
+        self.M, self.N, self.K, self.act = M, N, K, act
+        self._x = torch.Size((M, K) if x_shape is None else x_shape)
+        if self._x.numel() != M * K or self._x[-1] != K:
+            raise ValueError("x_shape must hold %d rows of %d" % (M, K))
+        self._w, self._y, self._cols = torch.Size((N, K)), torch.Size(self._x[:-1] + (N,)), torch.Size((N,))
+        a, b = ctypes.c_ulonglong(), ctypes.c_ulonglong()
+        _check(L.conv_linear_workspace(h, ctypes.byref(a), ctypes.byref(b)), "conv_linear_workspace")
+        self.workspace_bytes = {"forward": a.value, "backward": b.value}
+
+    def forward(self, x, w, bias=None, residual=None, y=None, z=None, stream=None):
+        """act(x w^T + bias) + residual; ``z`` receives the values before the activation, which backward()
+        reads.  ``y`` may be the residual itself."""
+        if stream is not None:
+            with _ops._t.cuda.stream(stream):
+                return self.forward(x, w, bias, residual, y, z)
+        bf16 = _ops._t.bfloat16
+        dev = _device_of(x)
+        _need(x, "x", self._x, bf16, dev)
+        _need(w, "w", self._w, bf16, dev)
+        if bias is not None:
+            _need(bias, "bias", self._cols, _ops._t.float32, dev)
+        if residual is not None:
+            _need(residual, "residual", self._y, bf16, dev)
+        if z is not None:
+            _need(z, "z", self._y, bf16, dev)
+        if y is None:
+            y = _ops._t.empty(self._y, dtype=bf16, device=dev)
+        else:
+            _need(y, "y", self._y, bf16, dev)
+        ws = _workspace(self.workspace_bytes["forward"], dev)
+        _check(self._L.conv_linear_forward(self._plan, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
+                                           _ptr(z), _ptr(ws), _ops._raw_stream(dev)), "conv_linear_forward")
+        return y
+
+    __call__ = forward
+
+    def backward(self, dy, x=None, w=None, z=None, dx=None, dw=None, dbias=None, stream=None, need=(True, True, True)):
+        """(dx, dw, dbias) of forward() from its x, w and, with an activation, z; None for those that
+        ``need`` (dx, dw, dbias) leaves out.  w is read for dx and x for dw.  The residual's
+        gradient is dy itself."""
+        if stream is not None:
+            with _ops._t.cuda.stream(stream):
+                return self.backward(dy, x, w, z, dx, dw, dbias, need=need)
+        t = _ops._t
+        dev = _device_of(dy)
+        _need(dy, "dy", self._y, t.bfloat16, dev)
+        if x is not None or need[1]:
+            _need(x, "x", self._x, t.bfloat16, dev)
+        if w is not None or need[0]:
+            _need(w, "w", self._w, t.bfloat16, dev)
+        if z is not None or self.act != "none":
+            _need(z, "z", self._y, t.bfloat16, dev)
+        out = []
+        for given, name, shape, dtype, wanted in ((dx, "dx", self._x, t.bfloat16, need[0]),
+                                                  (dw, "dw", self._w, t.bfloat16, need[1]),
+                                                  (dbias, "dbias", self._cols, t.float32, need[2])):
+            if given is not None:
+                if not wanted:
+                    raise ValueError("%s is not written without need" % name)
+                _need(given, name, shape, dtype, dev)
+            out.append(given if given is not None or not wanted else t.empty(shape, dtype=dtype, device=dev))
+        ws = _workspace(self.workspace_bytes["backward"], dev)
+        _check(self._L.conv_linear_backward(self._plan, dy.data_ptr(), _ptr(x), _ptr(w), _ptr(z), _ptr(out[0]), _ptr(out[1]),
+                                            _ptr(out[2]), _ptr(ws), _ops._raw_stream(dev)), "conv_linear_backward")
+        return tuple(out)
+
+    def device_status(self, stream=None) -> int:
+        """Read and clear the plan's own status word, as ConvPlan.device_status."""
+        return _plan_status(lib().conv_linear_plan_device_status, self._plan, stream, "conv_linear_plan_device_status")
+
+
+class RmsNormPlan(_Plan):
+    """Root-mean-square norm of M rows of C values (include/conv.h, conv_rms_norm_*) in FP32 ("f32") or
+    BF16 ("bf16"): h = x + residual, y = h / sqrt(mean(h^2) + eps) * gamma, FP32 gamma [C] (None: 1).
+    ``x_shape`` [..., C] with M rows in all: x, residual, y and h have that shape.  rstd is FP32 [M]."""
+
+    _destroy = "conv_rms_norm_plan_destroy"
+
+    def __init__(self, M, C, dtype="bf16", eps=1e-6, x_shape=None):
+        L = lib()
+        h = ctypes.c_void_p()
+        _check(L.conv_rms_norm_plan_create(ctypes.byref(h), M, C, eps, _choice(dtype, _DTYPES, "dtype")),
+               "conv_rms_norm_plan_create")
+        self._plan = h
+        self._L = L
+        torch = _torch()
+        self.M, self.C, self.dtype, self.torch_dtype, self.eps = M, C, dtype, _torch_dtypes()[dtype], eps
+        self.shape = torch.Size((M, C) if x_shape is None else x_shape)
+        if self.shape.numel() != M * C or self.shape[-1] != C:
+            raise ValueError("x_shape must hold %d rows of %d" % (M, C))
+        self._cols, self._rows = torch.Size((C,)), torch.Size((M,))
+        b = ctypes.c_ulonglong()
+        _check(L.conv_rms_norm_workspace(h, ctypes.byref(b)), "conv_rms_norm_workspace")
+        self.workspace_bytes = {"backward": b.value}
+
+    def _inputs(self, x, gamma, residual, h, rstd):
+        """Checks them; returns x's device and h, made where a residual calls for one."""
+        dev = _device_of(x)
+        _need(x, "x", self.shape, self.torch_dtype, dev)
+        if gamma is not None:
+            _need(gamma, "gamma", self._cols, _ops._t.float32, dev)
+        if residual is not None:
+            _need(residual, "residual", self.shape, self.torch_dtype, dev)
+        if h is not None:
+            if residual is None:
+                raise ValueError("h is written with a residual alone: without one it is x")
+            _need(h, "h", self.shape, self.torch_dtype, dev)
+        elif residual is not None:
+            h = _ops._t.empty_like(x)
+        if rstd is not None:
+            _need(rstd, "rstd", self._rows, _ops._t.float32, dev)
+        return dev, h
+
+    def forward(self, x, gamma=None, residual=None, y=None, h=None, rstd=None, stream=None):
+        """y, or (y, h) with a residual; ``rstd`` (empty_rstd()) receives what backward() reads.  ``h`` may be
+        the residual itself."""
+        if stream is not None:
+            with _ops._t.cuda.stream(stream):
+                return self.forward(x, gamma, residual, y, h, rstd)
+        dev, h = self._inputs(x, gamma, residual, h, rstd)
+        if y is None:
+            y = _ops._t.empty_like(x)
+        else:
+            _need(y, "y", self.shape, self.torch_dtype, dev)
+        _check(self._L.conv_rms_norm_forward(self._plan, x.data_ptr(), _ptr(residual), _ptr(gamma), y.data_ptr(), _ptr(h),
+                                             _ptr(rstd), _ops._raw_stream(dev)), "conv_rms_norm_forward")
+        return y if residual is None else (y, h)
+
+    __call__ = forward
+
+    def forward_int8(self, x, gamma=None, residual=None, q=None, scale=None, h=None, rstd=None, stream=None):
+        """(q, scale), or (q, scale, h) with a residual: y as int8 with one FP32 scale per row [M]."""
+        if stream is not None:
+            with _ops._t.cuda.stream(stream):
+                return self.forward_int8(x, gamma, residual, q, scale, h, rstd)
+        dev, h = self._inputs(x, gamma, residual, h, rstd)
+        if q is None:
+            q = _ops._t.empty(self.shape, dtype=_ops._t.int8, device=dev)
+        else:
+            _need(q, "q", self.shape, _ops._t.int8, dev)
+        if scale is None:
+            scale = _ops._t.empty(self._rows, dtype=_ops._t.float32, device=dev)
+        else:
+            _need(scale, "scale", self._rows, _ops._t.float32, dev)
+        _check(self._L.conv_rms_norm_forward_int8(self._plan, x.data_ptr(), _ptr(residual), _ptr(gamma), q.data_ptr(),
+                                                  scale.data_ptr(), _ptr(h), _ptr(rstd), _ops._raw_stream(dev)),
+               "conv_rms_norm_forward_int8")
+        return (q, scale) if residual is None else (q, scale, h)
+
+    def backward(self, dy, h, rstd, gamma=None, dh=None, dx=None, dgamma=None, stream=None, gamma_grad=True):
+        """(dx, dgamma) from forward()'s h (x without a residual) and rstd; ``dh`` is the gradient of its
+        output h, dx that of x and of the residual alike.  Without ``gamma_grad`` (dx, None).  ``dx`` may be dy
+        or dh itself."""
+        if stream is not None:
+            with _ops._t.cuda.stream(stream):
+                return self.backward(dy, h, rstd, gamma, dh, dx, dgamma, gamma_grad=gamma_grad)
+        t = _ops._t
+        dev = _device_of(dy)
+        _need(dy, "dy", self.shape, self.torch_dtype, dev)
+        _need(h, "h", self.shape, self.torch_dtype, dev)
+        _need(rstd, "rstd", self._rows, t.float32, dev)
+        if gamma is not None:
+            _need(gamma, "gamma", self._cols, t.float32, dev)
+        if dh is not None:
+            _need(dh, "dh", self.shape, self.torch_dtype, dev)
+        if dx is None:
+            dx = t.empty_like(dy)
+        else:
+            _need(dx, "dx", self.shape, self.torch_dtype, dev)
+        if dgamma is not None:
+            if not gamma_grad:
+                raise ValueError("dgamma is not written without gamma_grad")
+            _need(dgamma, "dgamma", self._cols, t.float32, dev)
+        elif gamma_grad:
+            dgamma = t.empty(self._cols, dtype=t.float32, device=dev)
+        ws = _workspace(self.workspace_bytes["backward"], dev) if gamma_grad else None
+        _check(self._L.conv_rms_norm_backward(self._plan, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _ptr(gamma), _ptr(dh),
+                                              dx.data_ptr(), _ptr(dgamma), _ptr(ws), _ops._raw_stream(dev)),
+               "conv_rms_norm_backward")
+        return dx, dgamma
+
+    def empty_rstd(self, device="cuda"):
+        return _ops._t.empty(self._rows, dtype=_ops._t.float32, device=device)
+
+
+# ---------------------------------------------------------------- functional forms
+_linear_plans = binding.PlanCache()
+_rms_plans = binding.PlanCache()
+_functions = {}
+
+
+def _linear_plan(x, w, act):
+    key = (x.shape, w.shape, x.get_device(), act)
+    plan = _linear_plans.get(key)
+    if plan is None:
+        _torch()
+        _refuse_device(x.get_device())
+        if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
+            raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
+        N, K = w.shape
+        plan = _linear_plans.put(key, LinearPlan(x.numel() // K if K else 0, N, K, act, x.shape))
+    else:
+        plan.used = True
+    return plan
+
+
+def _rms_plan(x, eps):
+    key = (x.shape, x.dtype, x.get_device(), eps)
+    plan = _rms_plans.get(key)
+    if plan is None:
+        torch = _torch()
+        _need_any(x, "x", (torch.bfloat16, torch.float32))
+        if x.dim() < 2:
+            raise ValueError("x must be [..., C]")
+        _refuse_device(x.get_device())
+        C = x.shape[-1]
+        plan = _rms_plans.put(key, RmsNormPlan(x.numel() // C if C else 0, C, "bf16" if x.dtype is torch.bfloat16 else "f32",
+                                               eps, x.shape))
+    else:
+        plan.used = True
+    return plan
+
+
+def _function(name):
+    """The autograd functions of linear, rms_norm and dropout.  They keep buffers of their own: a caller's
+    may hold another call's by the time of the backward pass."""
+    if not _functions:
+        torch = _torch()
+        from torch.autograd.function import once_differentiable
+
+        class Linear(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, w, bias, residual, plan):
+                z = torch.empty(plan._y, dtype=x.dtype, device=x.device) if plan.act != "none" else None
+                y = plan.forward(x, w, bias, residual, z=z)
+                ctx.save_for_backward(x, w, z)
+                ctx.plan = plan
+                return y
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy):
+                x, w, z = ctx.saved_tensors
+                need = ctx.needs_input_grad
+                dx = dw = dbias = None
+                if any(need[:3]):
+                    dx, dw, dbias = ctx.plan.backward(_upstream(dy), x, w, z, need=need[:3])
+                return dx, dw, dbias, dy if need[3] else None, None
+
+        class RmsNorm(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, gamma, residual, plan):
+                rstd = plan.empty_rstd(x.device)
+                out = plan.forward(x, gamma, residual, rstd=rstd)
+                ctx.save_for_backward(x if residual is None else out[1], gamma, rstd)
+                ctx.mark_non_differentiable(rstd)
+                ctx.plan = plan
+                return (out, rstd) if residual is None else out + (rstd,)
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy, *more):
+                h, gamma, rstd = ctx.saved_tensors
+                need_x, need_gamma, need_r, _ = ctx.needs_input_grad
+                dh = _upstream(more[0]) if len(more) > 1 else None
+                dx, dgamma = ctx.plan.backward(_upstream(dy), h, rstd, gamma, dh, gamma_grad=need_gamma)
+                return dx if need_x else None, dgamma, dx if need_r else None, None
+
+        class Dropout(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, residual, p, state):
+                state = state.clone()  # the caller's may have moved on by the time of the backward pass
+                ctx.save_for_backward(state)
+                ctx.p = p
+                return _dropout(x, p, state, residual)
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy):
+                state, = ctx.saved_tensors
+                need = ctx.needs_input_grad
+                return _dropout(_upstream(dy), ctx.p, state) if need[0] else None, dy if need[1] else None, None, None
+
+        _functions.update(linear=Linear, rms_norm=RmsNorm, dropout=Dropout)
+    return _functions[name]
+
+
+def linear(x, w, bias=None, act="none", residual=None, y=None, z=None, stream=None):
+    """act(x w^T + bias) + residual in BF16: x [..., K], w [N][K], FP32 bias [N], residual [..., N]; act
+    "none", "relu" or "silu".  ``z`` receives the values before the activation, which linear_backward reads; ``y``,
+    the result's buffer, may be the residual itself.
+
+    Differentiable: where torch records gradients and x, w, bias or residual requires one, the result
+    has its backward pass (once, and not with ``y`` or ``z`` given).  The plans record none."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return linear(x, w, bias, act, residual, y, z)
+    plan = _linear_plan(x, w, act)
+    if _recorded(x, w, bias, residual):
+        if y is not None or z is not None:
+            raise ValueError("y and z cannot be given where the result's gradient is recorded")
+        return _function("linear").apply(x, w, bias, residual, plan)
+    return plan.forward(x, w, bias, residual, y, z)
+
+
+def linear_backward(dy, x, w, z=None, act="none", stream=None):
+    """(dx, dw, dbias) of linear from its x and w and, with an activation, the z it wrote; the
+    residual's gradient is dy itself."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return linear_backward(dy, x, w, z, act)
+    return _linear_plan(x, w, act).backward(dy, x, w, z)
+
+
+def rms_norm(x, gamma=None, residual=None, eps=1e-6, h=None, rstd=None, stream=None):
+    """y = h / sqrt(mean(h^2) + eps) * gamma over the last axis of h = x + residual, in x's type; x
+    [..., C] BF16 or FP32, FP32 gamma [C].  Returns y, or (y, h) with a residual.  ``h``, that result's buffer, may be
+    the residual itself; ``rstd`` FP32 [rows] receives what rms_norm_backward reads.
+
+    Differentiable: where torch records gradients and x, gamma or residual requires one, the results
+    have their backward pass (once, and not with ``h`` given).  The plans and the 8-bit form
+    record none."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return rms_norm(x, gamma, residual, eps, h, rstd)
+    plan = _rms_plan(x, eps)
+    if _recorded(x, gamma, residual):
+        if h is not None:
+            raise ValueError("h cannot be given where the result's gradient is recorded")
+        if rstd is not None:
+            _need(rstd, "rstd", plan._rows, _ops._t.float32, x.get_device())
+        *out, own = _function("rms_norm").apply(x, gamma, residual, plan)
+        if rstd is not None:
+            rstd.copy_(own)
+        return out[0] if residual is None else tuple(out)
+    return plan.forward(x, gamma, residual, h=h, rstd=rstd)
+
+
+def rms_norm_int8(x, gamma=None, residual=None, eps=1e-6, h=None, rstd=None, stream=None):
+    """(q, scale), or (q, scale, h) with a residual: rms_norm's result as int8 with one FP32 scale per
+    row [rows], as int8_matmul takes it."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return rms_norm_int8(x, gamma, residual, eps, h, rstd)
+    return _rms_plan(x, eps).forward_int8(x, gamma, residual, h=h, rstd=rstd)
+
+
+def rms_norm_backward(dy, h, rstd, gamma=None, dh=None, stream=None):
+    """(dx, dgamma) of rms_norm from the h (x without a residual) and rstd it wrote; ``dh`` is the gradient of
+    its output h.  dx is the gradient of x and of the residual alike."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return rms_norm_backward(dy, h, rstd, gamma, dh)
+    return _rms_plan(h, 1e-6).backward(dy, h, rstd, gamma, dh)  # eps is in rstd already
+
+
+def _dropout(x, p, state, residual=None, y=None):
+    torch = _torch()
+    _need_any(x, "x", (torch.bfloat16, torch.float32))
+    dev = _device_of(x)
+    if residual is not None:
+        _need(residual, "residual", x.shape, x.dtype, dev)
+    _need(state, "state", torch.Size((2,)), torch.int64, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", x.shape, x.dtype, dev)
+    _check(lib().conv_dropout(x.data_ptr(), _ptr(residual), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, x.numel(), p,
+                              state.data_ptr(), y.data_ptr(), _ops._raw_stream(dev)), "conv_dropout")
+    return y
+
+
+def dropout(x, p, state, residual=None, y=None, stream=None):
+    """x / (1 - p) where the generator keeps an element, 0 where it drops one (with probability p), plus
+    the residual; x BF16 or FP32 of any shape.  ``state`` is an int64 tensor of two on the GPU, seed and offset, read when
+    the kernel runs: the same state gives the same mask, and a program moves the offset (or the seed)
+    on for a new one, in a captured graph too.  ``y``, the result's buffer, may be x or the residual itself.
+
+    Differentiable: where torch records gradients and x or residual requires one, the result has its
+    backward pass (dropout_backward; once, and not with ``y`` given)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return dropout(x, p, state, residual, y)
+    _torch()
+    if _recorded(x, residual):
+        if y is not None:
+            raise ValueError("y cannot be given where the result's gradient is recorded")
+        if state.dtype is not _ops._t.int64 or state.shape != (2,):
+            raise ValueError("state must be an int64 tensor of two")
+        return _function("dropout").apply(x, residual, p, state)
+    return _dropout(x, p, state, residual, y)
+
+
+def dropout_backward(dy, p, state, stream=None):
+    """The gradient of dropout's x: the same mask and factor on dy (the residual's gradient is dy itself)."""
+    return dropout(dy, p, state, stream=stream)

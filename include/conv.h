@@ -516,6 +516,156 @@ conv_status conv_int8_plan_destroy(conv_int8_plan *p);
  */
 conv_status conv_quantize_rows(const void *x, conv_dtype dtype, int M, int K, void *q, float *scale, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows with the residual's addition, forward and backward.
+ *
+ *   h[m][c] = x[m][c] + residual[m][c]            (x itself without a residual)
+ *   rstd[m] = 1 / sqrt( sum_c h[m][c]^2 / C + eps )
+ *   y[m][c] = h[m][c] * rstd[m] * gamma[c]
+ *
+ * Sums, rstd and the arithmetic are FP32; y is taken from the sum before it is rounded, and y
+ * and h are rounded once.  A NaN or Inf in a row stays in that row (an Inf gives it rstd 0: 0 for
+ * its finite values, NaN for the Inf); a row whose squares pass FP32 gets rstd 0, one of
+ * zeros 1 / sqrt(eps).
+ *
+ * Layouts (dense, row-major, caller-owned device memory, 16-byte aligned bases; a row may start
+ * anywhere, C may be odd):
+ *   x, residual, y, h, dy, dh, dx   [M][C]   FP32 (CONV_F32) or BF16 (CONV_BF16)
+ *   gamma, dgamma  [C]      FP32
+ *   rstd, q_scale  [M]      FP32
+ *   q              [M][C]   8-bit integers
+ * ------------------------------------------------------------------------ */
+typedef struct conv_rms_norm_plan conv_rms_norm_plan; /* opaque, host-owned */
+
+/*
+ * Check the shape and choose the kernels.  *plan gets a new plan, or NULL on error.  Returns
+ * CONV_ERR_INVALID_ARG for non-positive sizes, an eps that is negative or not finite, or an
+ * unknown dtype; CONV_ERR_UNSUPPORTED for C > 2^20, from 2^30 rows on or above 2^40 elements;
+ * CONV_ERR_CUDA if the device cannot be queried.  Tied to the device current at creation;
+ * without a device a host-only plan is made, whose calls return CONV_ERR_CUDA.
+ */
+conv_status conv_rms_norm_plan_create(conv_rms_norm_plan **plan, int M, int C, float eps, conv_dtype dtype);
+
+/* Bytes of device workspace that conv_rms_norm_backward takes with dgamma (the forward calls take
+ * none).  Its contents are of no account before and after a call; calls that may run at the same
+ * time take one each. */
+conv_status conv_rms_norm_workspace(const conv_rms_norm_plan *p, unsigned long long *backward);
+
+/*
+ * y, and h where it is given.  residual, gamma (1), h and rstd may each be NULL; h needs a residual
+ * and may be the residual itself, otherwise no output overlaps an input.  rstd is what the
+ * backward pass reads.  Asynchronous on `stream`; CONV_ERR_INVALID_ARG for a NULL plan, x or y, an
+ * h without a residual, or another current device, CONV_ERR_MISALIGNED for a pointer that is not
+ * 16-byte aligned, CONV_ERR_CUDA if a launch fails.
+ */
+conv_status conv_rms_norm_forward(conv_rms_norm_plan *p, const void *x, const void *residual, const float *gamma,
+                                  void *y, void *h, float *rstd, void *stream);
+
+/*
+ * The forward pass with y in 8 bits, one scale for each row: q = rint(y * (127 / amax)),
+ * q_scale = amax / 127 with amax the row's largest |y|, taken from the FP32 values.  The rules
+ * of conv_quantize_rows.
+ */
+conv_status conv_rms_norm_forward_int8(conv_rms_norm_plan *p, const void *x, const void *residual, const float *gamma,
+                                       void *q, float *q_scale, void *h, float *rstd, void *stream);
+
+/*
+ * Gradients, from the forward pass's h (x without a residual) and rstd: with n = h * rstd,
+ *   dx = rstd * (dy * gamma - n * mean_c(dy * gamma * n)) + dh,   dgamma[c] = sum_m dy * n.
+ * dh (may be NULL) is the gradient of the forward pass's other output h; dx is the gradient of x and
+ * of the residual alike.  dgamma may be NULL (then the workspace may be, too); it is written, not
+ * added to.  dx may be dy or dh itself, otherwise it overlaps no input.  Every sum has one fixed
+ * order: the same inputs give the same bits.  Errors as above.
+ */
+conv_status conv_rms_norm_backward(conv_rms_norm_plan *p, const void *dy, const void *h, const float *rstd,
+                                   const float *gamma, const void *dh, void *dx, float *dgamma, void *workspace,
+                                   void *stream);
+
+/* Free the plan.  NULL is accepted. */
+conv_status conv_rms_norm_plan_destroy(conv_rms_norm_plan *p);
+
+/* ------------------------------------------------------------------------
+ * Dropout from a counter-based generator, with the residual's addition:
+ *
+ *   y[i] = (w(i) >= t ? x[i] / (1 - p) : 0) + residual[i],   t = p * 2^32 rounded to an integer
+ *
+ * w(i) is word i % 4 of the block that Philox 4x32 of ten rounds (Salmon, Moraes, Dror and Shaw, "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011) gives for the counter (i / 4 low, i / 4 high, offset low,
+ * offset high) and the key (seed low, seed high).  The mask depends on state, i and p alone: the
+ * backward pass is the same call on dy without a residual, and no mask is stored.
+ * state is two 64-bit words in device memory, seed and offset, read when the kernel runs: a
+ * captured call takes what they hold at each replay.  A dropped NaN or Inf is 0.  Arithmetic in FP32, one
+ * rounding.
+ *
+ * x, residual (may be NULL), y: n elements, FP32 or BF16, 16-byte aligned; y may be x or the residual
+ * itself.  state: 8-byte aligned.  Asynchronous on `stream`.
+ * CONV_ERR_INVALID_ARG for a NULL x, state or y, n = 0, a p outside [0, 1] or an unknown dtype,
+ * CONV_ERR_UNSUPPORTED above 2^40 elements, CONV_ERR_MISALIGNED, CONV_ERR_CUDA if the launch fails.
+ * ------------------------------------------------------------------------ */
+conv_status conv_dropout(const void *x, const void *residual, conv_dtype dtype, unsigned long long n, double p,
+                         const unsigned long long *state, void *y, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Linear layer in BF16: the matrix product of rows (tokens, pixels) and weights with bias,
+ * activation and residual in its epilogue, and its gradients.
+ *
+ *   z[m][n] = sum_k x[m][k] * w[n][k] + bias[n],   y[m][n] = act(z[m][n]) + residual[m][n]
+ *
+ * Layouts (dense, row-major, caller-owned device memory, 16-byte aligned bases; a row may
+ * start anywhere, K and N may be odd):
+ *   x, dx           [M][K]  BF16
+ *   w, dw           [N][K]  BF16
+ *   bias, dbias     [N]     FP32
+ *   residual, y, z, dy  [M][N]  BF16
+ * Products are exact, sums and the epilogue FP32 (the tensor cores may drop 2^-23 of the
+ * magnitudes added so far with every 16 products), y and z are rounded once.  The last bits of a
+ * row depend on how many rows share the call.  A NaN or Inf in a row of x stays in that row of y, one in a row of w in
+ * that column.
+ * ------------------------------------------------------------------------ */
+typedef struct conv_linear_plan conv_linear_plan; /* opaque, host-owned */
+
+/*
+ * Check the shape and choose the kernels.  *plan gets a new plan, or NULL on error.  Returns
+ * CONV_ERR_INVALID_ARG for non-positive sizes or an unknown act, CONV_ERR_UNSUPPORTED for a
+ * size from 2^30 on or above 2^40 elements of x, w or y, CONV_ERR_CUDA if the device cannot be
+ * queried.  Tied to the device current at creation; without a device a host-only plan is made,
+ * whose calls return CONV_ERR_CUDA.
+ */
+conv_status conv_linear_plan_create(conv_linear_plan **plan, int M, int N, int K, conv_act act);
+
+/* Bytes of device workspace that the calls take (either may be 0, then NULL will do; either pointer
+ * may be NULL).  Its contents are of no account before and after a call; calls that may run at the
+ * same time take one each. */
+conv_status conv_linear_workspace(const conv_linear_plan *p, unsigned long long *forward, unsigned long long *backward);
+
+/*
+ * y, and z where it is given (what the backward pass of an activation reads).  bias and residual
+ * may be NULL (0).  y may be the residual itself; otherwise no output overlaps an input or another output.
+ * Asynchronous on `stream`; CONV_ERR_INVALID_ARG for a NULL plan, x, w or y, a NULL workspace where
+ * one is needed, or another current device, CONV_ERR_MISALIGNED for a base that is not 16-byte
+ * aligned, CONV_ERR_CUDA if a launch fails.
+ */
+conv_status conv_linear_forward(conv_linear_plan *p, const void *x, const void *w, const float *bias,
+                                const void *residual, void *y, void *z, void *workspace, void *stream);
+
+/*
+ * Gradients: with u = dy * act'(z),
+ *   dx[m][k] = sum_n u[m][n] * w[n][k],  dw[n][k] = sum_m u[m][n] * x[m][k],  dbias[n] = sum_m u[m][n];
+ * the residual's gradient is dy itself.  z is what the forward pass wrote (may be NULL without an activation;
+ * the derivative of ReLU at 0 is 0).  u is rounded to BF16 for dx and dw, the operands' type, and not for
+ * dbias.  Each of dx, dw, dbias may be NULL, but not all; w is read for dx and x for dw alone (else they may be
+ * NULL).  Outputs are written, not added to, and overlap no input.  Every sum has one fixed order: the same inputs
+ * give the same bits.  Errors as above.
+ */
+conv_status conv_linear_backward(conv_linear_plan *p, const void *dy, const void *x, const void *w, const void *z,
+                                 void *dx, void *dw, float *dbias, void *workspace, void *stream);
+
+/* Status word of the plan (waits that gave up): the contract of conv_plan_device_status. */
+conv_status conv_linear_plan_device_status(const conv_linear_plan *p, void *stream, int *code);
+
+/* Free the plan: the contract of conv_plan_destroy.  NULL is accepted. */
+conv_status conv_linear_plan_destroy(conv_linear_plan *p);
+
 #ifdef __cplusplus
 }
 #endif

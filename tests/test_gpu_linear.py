@@ -1,0 +1,288 @@
+"""Linear layer on the GPU against 64-bit restatements: one row to many, odd sizes, rows off 16 bytes,
+every epilogue, gradients against the formula and against differences, bad values, streams, graphs,
+autograd, and the residual branch as a whole."""
+import numpy as np
+import pytest
+import torch
+
+import operator_refs as oref
+import row_refs as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _inputs(M, N, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    x, r, dy = (torch.randn(M, n, generator=g).to(BF16) for n in (K, N, N))
+    w = (torch.randn(N, K, generator=g) / K ** 0.5).to(BF16)
+    return x, w, torch.randn(N, generator=g), r, dy
+
+
+SIZES = [
+    # M, N, K
+    (1, 1, 1), (1, 17, 5), (1, 4096, 1024), (2, 300, 4096), (3, 1, 64), (4, 1000, 2052), (5, 64, 48), (8, 128, 1000), (9, 40, 16),
+    (16, 512, 512), (17, 200, 4104), (31, 77, 333), (32, 256, 2048), (33, 130, 264), (48, 96, 640), (64, 256, 96), (65, 4096, 512),
+    (127, 128, 64), (128, 128, 128), (129, 257, 127), (200, 320, 320), (256, 2048, 1024), (301, 777, 1000), (513, 512, 256),
+    (1000, 96, 2048), (1000, 1003, 72), (2000, 2050, 520), (3136, 512, 256), (5000, 1000, 200), (40000, 64, 72), (7, 20000, 128),
+]
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_forward(size):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, w, b, r, _ = _inputs(M, N, K, M + 3 * N + K)
+    canvas = torch.full((2, M * N + 64), 7.0, device="cuda", dtype=BF16)
+    y, z = (c[:M * N].view(M, N) for c in (canvas[0], canvas[1]))
+    if canvas[1].data_ptr() % 16:
+        z = torch.empty(M, N, device="cuda", dtype=BF16)
+    plan = cg.LinearPlan(M, N, K, "silu")
+    plan.forward(x.cuda(), w.cuda(), b.cuda(), r.cuda(), y=y, z=z)
+    (want, tol), (want_z, tol_z) = ref.linear(_np(x), _np(w), _np(b), _np(r), "silu")
+    oref.check(_np(y), want, tol, True, "y")
+    oref.check(_np(z), want_z, tol_z, True, "z")
+    assert torch.all(canvas[:, M * N:] == 7.0)
+    y = cg.linear(x.cuda(), w.cuda())
+    (want, tol), _ = ref.linear(_np(x), _np(w), None, None, "none")
+    oref.check(_np(y), want, tol, True, "plain y")
+    assert plan.device_status() == 0 and cg.device_status() == 0
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("size", [(1, 96, 160), (3, 97, 100), (20, 96, 160), (20, 95, 101), (140, 200, 136), (140, 203, 130), (600, 512, 520)])
+def test_every_epilogue(size, act):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, w, b, r, _ = _inputs(M, N, K, 5)
+    for bias in (None, b):
+        for res in (None, r):
+            for with_z in (False, True):
+                z = torch.empty(M, N, device="cuda", dtype=BF16) if with_z else None
+                y = cg.linear(x.cuda(), w.cuda(), None if bias is None else bias.cuda(), act,
+                              None if res is None else res.cuda(), z=z)
+                (want, tol), (want_z, tol_z) = ref.linear(_np(x), _np(w), None if bias is None else _np(bias),
+                                                          None if res is None else _np(res), act)
+                oref.check(_np(y), want, tol, True, "y")
+                if with_z:
+                    oref.check(_np(z), want_z, tol_z, True, "z")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("size", [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 520), (77, 264, 520), (301, 777, 1000),
+                                  (1000, 96, 48), (129, 257, 127), (2000, 512, 256), (5000, 64, 40), (300, 1024, 2048), (20000, 130, 72)])
+def test_backward(size, act):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, w, b, _, dy = _inputs(M, N, K, 7 * M + N + K)
+    z = None if act == "none" else torch.from_numpy(ref.linear(_np(x), _np(w), _np(b), None, act)[1][0]).to(BF16)
+    zc = None if z is None else z.cuda()
+    canvas = torch.full((M * K + 64,), 7.0, device="cuda", dtype=BF16)
+    plan = cg.LinearPlan(M, N, K, act)
+    dx, dw, db = plan.backward(dy.cuda(), x.cuda(), w.cuda(), zc, dx=canvas[:M * K].view(M, K))
+    want = ref.linear_backward(_np(dy), _np(x), _np(w), None if z is None else _np(z), act)
+    for got, (value, tol), bf16, what in zip((dx, dw, db), want, (True, True, False), ("dx", "dw", "dbias")):
+        oref.check(_np(got), value, tol, bf16, what)
+    assert torch.all(canvas[M * K:] == 7.0)
+    # each by itself, and the functional form, give the same bits
+    one = cg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), zc, act)
+    for i, (got, name) in enumerate(zip((dx, dw, db), ("dx", "dw", "dbias"))):
+        assert torch.equal(one[i], got), name
+        need = tuple(j == i for j in range(3))
+        alone = plan.backward(dy.cuda(), x.cuda() if i == 1 else None, w.cuda() if i == 0 else None, zc, need=need)
+        assert torch.equal(alone[i], got) and all(alone[j] is None for j in range(3) if j != i)
+    assert plan.device_status() == 0 and cg.device_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_against_differences(M):
+    """The product is linear in each operand: (f(x + d) - f(x)) . dy is dx . d up to the roundings of the
+    two results to BF16 (2^-8 of them each) and of dx."""
+    import cnn_convolution_implicit_gb300 as cg
+    N, K = 200, 120
+    x, w, b, _, dy = _inputs(M, N, K, 17)
+    d = torch.randn(M, K, generator=torch.Generator().manual_seed(4)).to(BF16)
+    moved = (x.float() + d.float()).to(BF16)
+    step = moved.double() - x.double()
+    y0, y1 = _np(cg.linear(x.cuda(), w.cuda(), b.cuda())), _np(cg.linear(moved.cuda(), w.cuda(), b.cuda()))
+    dx, dw, _ = cg.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    g = _np(dy)
+    tol = 1.1 * 2.0 ** -8 * ((np.abs(y0) + np.abs(y1)) * np.abs(g)).sum() + 2.0 ** -8 * np.abs(_np(dx) * step.numpy()).sum()
+    assert abs(((y1 - y0) * g).sum() - (_np(dx) * step.numpy()).sum()) <= tol
+    dwt = torch.randn(N, K, generator=torch.Generator().manual_seed(5)).mul(0.1).to(BF16)
+    moved = (w.float() + dwt.float()).to(BF16)
+    step = (moved.double() - w.double()).numpy()
+    y1 = _np(cg.linear(x.cuda(), moved.cuda(), b.cuda()))
+    tol = 1.1 * 2.0 ** -8 * ((np.abs(y0) + np.abs(y1)) * np.abs(g)).sum() + 2.0 ** -8 * np.abs(_np(dw) * step).sum()
+    assert abs(((y1 - y0) * g).sum() - (_np(dw) * step).sum()) <= tol
+
+
+@pytest.mark.parametrize("M", [1, 4, 20, 60, 200])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_bad_values_stay_in_their_row_and_column(value, M):
+    import cnn_convolution_implicit_gb300 as cg
+    N, K = 200, 328
+    x, w, b, r, dy = _inputs(M, N, K, 3)
+    clean = cg.linear(x.cuda(), w.cuda(), b.cuda(), "silu", r.cuda())
+    bad = w.clone()
+    bad[77, 5] = value
+    y = cg.linear(x.cuda(), bad.cuda(), b.cuda(), "silu", r.cuda())
+    cols = [n for n in range(N) if n != 77]
+    assert torch.equal(y[:, cols], clean[:, cols])
+    assert not torch.any(torch.isfinite(y[:, 77]) & (x[:, 5].cuda() > 0))
+    if M > 1:
+        bad = x.clone()
+        bad[M // 2, 300] = value
+        y = cg.linear(bad.cuda(), w.cuda(), b.cuda(), "silu", r.cuda())
+        rows = [m for m in range(M) if m != M // 2]
+        assert torch.equal(y[rows], clean[rows])
+    dx, dw, db = cg.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    dy[M // 2, 9] = value
+    dx2, dw2, db2 = cg.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    rows, cols = [m for m in range(M) if m != M // 2], [n for n in range(N) if n != 9]
+    assert torch.equal(dx2[rows], dx[rows]) and torch.equal(dw2[cols], dw[cols]) and torch.equal(db2[cols], db[cols])
+    assert not torch.isfinite(db2[9])
+
+
+@pytest.mark.parametrize("size", [(1, 256, 512), (20, 256, 512), (70, 101, 203), (300, 777, 512), (2000, 512, 256)])
+def test_residual_in_place(size):
+    import cnn_convolution_implicit_gb300 as cg
+    x, w, b, r, _ = (t.cuda() for t in _inputs(*size, 31))
+    y = cg.linear(x, w, b, "relu", r)
+    over = r.clone()
+    assert cg.linear(x, w, b, "relu", over, y=over) is over and torch.equal(over, y)
+
+
+@pytest.mark.parametrize("size", [(1, 256, 512), (20, 256, 512), (70, 101, 203), (300, 777, 512), (2000, 512, 256), (513, 2048, 1024)])
+def test_side_stream_graph_and_repeat(size):
+    import cnn_convolution_implicit_gb300 as cg
+    M, N, K = size
+    x, w, b, r, dy = (t.cuda() for t in _inputs(M, N, K, 41))
+    z = torch.empty(M, N, device="cuda", dtype=BF16)
+    y = cg.linear(x, w, b, "silu", r, z=z)
+    grads = cg.linear_backward(dy, x, w, z, "silu")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2 = cg.linear(x, w, b, "silu", r, stream=side)
+    grads2 = cg.linear_backward(dy, x, w, z, "silu", stream=side)
+    y3 = cg.linear(x, w, b, "silu", r)      # at the same time
+    grads3 = cg.linear_backward(dy, x, w, z, "silu")
+    torch.cuda.synchronize()
+    for got in ([y2, *grads2], [y3, *grads3]):
+        assert all(torch.equal(p, q) for p, q in zip([y, *grads], got))
+    graph, x4 = torch.cuda.CUDAGraph(), torch.empty_like(x)
+    with torch.cuda.graph(graph):
+        y4 = cg.linear(x4, w, b, "silu", r)
+        grads4 = cg.linear_backward(dy, x4, w, z, "silu")
+    x4.copy_(x)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip([y, *grads], [y4, *grads4]))
+    assert cg.device_status() == 0
+
+
+@pytest.mark.parametrize("act,shape", [("none", (2, 5, 24)), ("relu", (3, 40)), ("silu", (2, 3, 7, 33))])
+def test_gradients_are_recorded(act, shape):
+    import cnn_convolution_implicit_gb300 as cg
+    K, N = shape[-1], 50
+    M = int(np.prod(shape[:-1]))
+    x, w, b, r, dy = _inputs(M, N, K, 51)
+    leaves = [t.cuda().requires_grad_(True) for t in (x.view(shape), w, b, r.view(shape[:-1] + (N,)))]
+    y = cg.linear(leaves[0], leaves[1], leaves[2], act, leaves[3])
+    assert y.shape == shape[:-1] + (N,)
+    y.backward(dy.cuda().view(y.shape))
+    z = torch.empty(M, N, device="cuda", dtype=BF16)
+    cg.linear(x.cuda(), w.cuda(), b.cuda(), act, z=z)
+    want = cg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), z, act)
+    for leaf, value in zip(leaves, [*want, dy.cuda()]):
+        assert torch.equal(leaf.grad, value.view(leaf.shape))
+    # a gradient for some of them alone, from a gradient that is not contiguous, on another stream
+    w2 = w.cuda().requires_grad_(True)
+    y = cg.linear(x.cuda().view(shape), w2, b.cuda(), act)
+    wide = torch.zeros(*y.shape[:-1], 2 * N, device="cuda", dtype=BF16)
+    wide[..., ::2] = dy.cuda().view(y.shape)
+    y.backward(wide[..., ::2])
+    assert torch.equal(w2.grad, want[1])
+    with pytest.raises(ValueError):
+        cg.linear(leaves[0], leaves[1], y=torch.empty_like(y))
+    with torch.no_grad():
+        assert not cg.linear(leaves[0], leaves[1]).requires_grad
+
+
+def test_refusals():
+    import cnn_convolution_implicit_gb300 as cg
+    x, w, b, r, dy = (t.cuda() for t in _inputs(6, 8, 16, 61))
+    plan = cg.LinearPlan(6, 8, 16, "relu")
+    for bad in (dict(x=x.float()), dict(x=x[:5]), dict(w=w.t()), dict(w=w.float()), dict(bias=b[:7]), dict(bias=b.to(BF16)),
+                dict(residual=r[:5]), dict(residual=r.float()), dict(y=r.float()), dict(z=r.float()), dict(x=x.cpu()), dict(w=w.cpu())):
+        with pytest.raises(ValueError):
+            plan.forward(**dict(dict(x=x, w=w), **bad))
+    for bad in (dict(dy=dy.float()), dict(x=None), dict(w=None), dict(z=None), dict(dx=x.float()), dict(dw=w.t()), dict(dbias=b[:3]),
+                dict(dx=x, need=(False, True, True))):
+        with pytest.raises(ValueError):
+            plan.backward(**dict(dict(dy=dy, x=x, w=w, z=r), **bad))
+    with pytest.raises(cg.ConvError):
+        plan.backward(dy, z=r, need=(False, False, False))
+    with pytest.raises(ValueError):
+        cg.linear(x, w[:, :8])
+    with pytest.raises(cg.ConvError):
+        cg.linear(x[:0], w)
+    with pytest.raises(cg.ConvError):  # a base off 16 bytes
+        cg.linear(torch.ones(17, device="cuda", dtype=BF16)[1:].view(1, 16), w)
+
+
+def test_residual_branch():
+    """Product, dropout with the residual, norm: a branch in training, its gradients through autograd
+    against the same operators called one by one; and in serving, norm to 8 bits and 8-bit product."""
+    import cnn_convolution_implicit_gb300 as cg
+    M, C, F = 300, 264, 520
+    x, w1, b1, _, _ = _inputs(M, F, C, 71)
+    _, w2, b2, r, dy = _inputs(M, C, F, 72)
+    gamma = torch.randn(C, generator=torch.Generator().manual_seed(73)) * 0.1 + 1
+    state = torch.tensor([5, 6], device="cuda")
+    leaves = [t.cuda().requires_grad_(True) for t in (x, w1, b1, w2, b2, gamma)]
+
+    def branch(x, w1, b1, w2, b2, gamma):
+        n = cg.rms_norm(x, gamma)
+        f = cg.linear(n, w1, b1, "silu")
+        return cg.dropout(cg.linear(f, w2, b2), 0.2, state, residual=x)
+
+    y = branch(*leaves)
+    y.backward(dy.cuda())
+    X, W1, B1, W2, B2, G = (t.detach() for t in leaves)
+    rstd, z = torch.empty(M, device="cuda"), torch.empty(M, F, device="cuda", dtype=BF16)
+    n = cg.rms_norm(X, G, rstd=rstd)
+    f = cg.linear(n, W1, B1, "silu", z=z)
+    assert torch.equal(cg.dropout(cg.linear(f, W2, B2), 0.2, state, residual=X), y)
+    d = cg.dropout_backward(dy.cuda(), 0.2, state)
+    df, dw2, db2 = cg.linear_backward(d, f, W2)
+    dn, dw1, db1 = cg.linear_backward(df, n, W1, z, "silu")
+    dx, dg = cg.rms_norm_backward(dn, X, rstd, G, dh=dy.cuda())
+    for leaf, value in zip(leaves[1:], (dw1, db1, dw2, db2, dg)):
+        assert torch.equal(leaf.grad, value)
+    # autograd adds the two gradients of x after rounding each to BF16; the call with dh rounds once
+    assert torch.all((leaves[0].grad.float() - dx.float()).abs() <= 2.0 ** -7 * (dx.float().abs() + dy.cuda().float().abs()) + 1e-30)
+    # against the definitions in 64 bits: five roundings to BF16 on the way, each 2^-8 at most
+    xd = _np(x)
+    nd = xd / np.sqrt((xd ** 2).mean(1, keepdims=True) + 1e-6) * _np(gamma)
+    zd = nd @ _np(w1).T + _np(b1)
+    od = (zd / (1 + np.exp(-zd))) @ _np(w2).T + _np(b2)
+    keep = ref.dropout_keep(5, 6, 0.2, 0, M * C).reshape(M, C)
+    want = xd + np.where(keep, od / 0.8, 0.0)
+    assert np.linalg.norm(_np(y) - want) <= 5 * 2.0 ** -8 * np.linalg.norm(want)
+    # serving
+    wq, ws = cg.quantize_rows(w1.cuda())
+    q, scale, h = cg.rms_norm_int8(X, G, residual=r.cuda())
+    y8 = cg.int8_matmul(q, scale, wq, ws, b1.cuda())
+    want, tol = oref.int8_product(q.cpu().numpy(), scale.cpu().numpy(), wq.cpu().numpy(), ws.cpu().numpy(), b1.numpy(), "none")
+    oref.check(_np(y8), want, tol, True, "8-bit product")
+    one = cg.linear(h[:1], W1, B1, "silu")
+    (want, tol), _ = ref.linear(_np(h[:1]), _np(w1), _np(b1), None, "silu")
+    oref.check(_np(one), want, tol, True, "one token")
