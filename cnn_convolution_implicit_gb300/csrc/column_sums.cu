@@ -1,0 +1,128 @@
+// column_sums.cu -- gradients of what is broadcast over the rows: the linear layer's u = dy * act'(z) with its sums
+// over the rows (dbias), and the join of such sums' parts.
+//
+// Bound by reading dy and z and writing u.  A CTA takes a strip of columns of a range of rows; a thread keeps its
+// columns' sums over its rows in FP32, the threads' meet in shared memory and the ranges' in the workspace, always
+// in one order.
+#include "linear_internal.h"
+#include "pointwise_math.cuh"
+#include "rows_internal.h"
+
+namespace convgb {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// A strip: `lanes` threads (a power of two) of VEC columns each to a row, kThreads / lanes rows at a time.
+struct Strip {
+    int vec, lanes, strips;
+};
+Strip strip_of(int N) {
+    Strip s;
+    s.vec = N % 8 == 0 ? 8 : 1;
+    const int vecs = N / s.vec;
+    s.lanes = 1;
+    while (s.lanes < 32 && s.lanes < vecs) s.lanes *= 2;
+    s.strips = (vecs + s.lanes - 1) / s.lanes;
+    return s;
+}
+
+template <int VEC, int ACT>
+__global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradParams p, int lanes, float* sums_out) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that may follow
+    constexpr int H = (VEC + 1) / 2, kBatch = 4;
+    using Io = VecIo<__nv_bfloat16, VEC>;
+    using Raw = typename Io::Raw;
+    __shared__ float sums[kThreads * VEC];
+    const int lane = threadIdx.x % lanes, slot = threadIdx.x / lanes, slots = kThreads / lanes;
+    const int n = (blockIdx.x * lanes + lane) * VEC;
+    f2 total[H] = {};
+    if (n < p.N) {
+        const long long step = static_cast<long long>(gridDim.y) * slots;
+        for (long long m0 = static_cast<long long>(blockIdx.y) * slots + slot; m0 < p.M; m0 += kBatch * step) {
+            Raw dy[kBatch] = {}, z[kBatch] = {};
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const long long m = m0 + i * step;
+                if (m >= p.M) break;
+                dy[i] = *reinterpret_cast<const Raw*>(p.dy + m * p.N + n);
+                if constexpr (ACT != CONV_ACT_NONE) z[i] = *reinterpret_cast<const Raw*>(p.z + m * p.N + n);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const long long m = m0 + i * step;
+                if (m >= p.M) break;
+                f2 u[H], v[H];
+                Io::unpack(dy[i], u);
+                if constexpr (ACT != CONV_ACT_NONE) {
+                    Io::unpack(z[i], v);
+#pragma unroll
+                    for (int j = 0; j < H; ++j) u[j] = activate_grad2<ACT>(v[j], u[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < H; ++j) total[j] = f2_add_rounded(total[j], u[j]);  // the same sums with and without u
+                if (p.u != nullptr) *reinterpret_cast<Raw*>(p.u + m * p.u_pitch + n) = Io::pack(u);
+            }
+        }
+    }
+    if (sums_out == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sums[slot * lanes * VEC + lane * VEC + j] = j & 1 ? f2_hi(total[j / 2]) : f2_lo(total[j / 2]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < lanes * VEC; i += kThreads) {
+        const int c = blockIdx.x * lanes * VEC + i;
+        if (c >= p.N) break;
+        float sum = 0.0f;
+        for (int k = 0; k < slots; ++k) sum += sums[k * lanes * VEC + i];
+        sums_out[static_cast<long long>(blockIdx.y) * p.N + c] = sum;
+    }
+}
+
+// 32 columns a CTA.
+__global__ void __launch_bounds__(1024) join_columns_kernel(const float* part, int parts, int C, float* out) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float total = 0.0f;
+    if (c < C) {
+#pragma unroll 4
+        for (int i = warp; i < parts; i += 32) total += part[static_cast<long long>(i) * C + c];
+    }
+    sums[warp][lane] = total;
+    __syncthreads();
+    float sum = sums[lane][warp];  // column `warp` of the block
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    if (lane == 0 && blockIdx.x * 32 + warp < C) out[blockIdx.x * 32 + warp] = sum;
+}
+
+}  // namespace
+
+cudaError_t launch_join_columns(const float* part, int parts, int C, float* out, cudaStream_t stream) {
+    join_columns_kernel<<<(C + 31) / 32, 1024, 0, stream>>>(part, parts, C, out);
+    return cudaGetLastError();
+}
+
+// About four CTAs an SM, four rows a thread at least.
+int linear_grad_parts(int M, int N, int num_sms) {
+    const Strip s = strip_of(N);
+    const int slots = kThreads / s.lanes;
+    const long long need = (static_cast<long long>(M) + 4 * slots - 1) / (4 * slots), most = (4LL * num_sms + s.strips - 1) / s.strips;
+    return static_cast<int>(need < most ? need : most);
+}
+
+cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, cudaStream_t stream) {
+    const Strip s = strip_of(p.N);
+    const int parts = linear_grad_parts(p.M, p.N, num_sms);
+    float* sums = p.dbias == nullptr ? nullptr : (parts > 1 ? p.part : p.dbias);
+    const dim3 grid(s.strips, parts);
+    const auto run = [&](auto* eight, auto* one) { (s.vec == 8 ? eight : one)<<<grid, kThreads, 0, stream>>>(p, s.lanes, sums); };
+    if (p.act == CONV_ACT_RELU) run(linear_grad_kernel<8, CONV_ACT_RELU>, linear_grad_kernel<1, CONV_ACT_RELU>);
+    else if (p.act == CONV_ACT_SILU) run(linear_grad_kernel<8, CONV_ACT_SILU>, linear_grad_kernel<1, CONV_ACT_SILU>);
+    else run(linear_grad_kernel<8, CONV_ACT_NONE>, linear_grad_kernel<1, CONV_ACT_NONE>);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.dbias == nullptr || parts == 1) return e;
+    return launch_join_columns(p.part, parts, p.N, p.dbias, stream);
+}
+
+}  // namespace convgb

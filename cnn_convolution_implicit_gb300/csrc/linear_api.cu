@@ -3,6 +3,7 @@
 #include <new>
 
 #include "../../include/conv.h"
+#include "int8_internal.h"
 #include "linear_internal.h"
 #include "status_slots.h"
 
@@ -10,6 +11,7 @@ using namespace convgb;
 
 struct conv_linear_plan {
     int M, N, K, act;
+    GemmTile forward, dx, dw;  // tiles of the three products
     int device;
     int num_sms;
     unsigned* status;
@@ -41,8 +43,41 @@ conv_status launched(cudaError_t e) {
 
 size_t up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-size_t backward_bytes(const conv_linear_plan* pl) {
-    return pl->act != CONV_ACT_NONE ? up(static_cast<size_t>(pl->M) * pl->N * 2, 256) : 0;
+int pitch_of(int n) { return static_cast<int>(up(n, 8)); }  // elements of a row that starts on 16 bytes
+
+// Workspaces: rows off 16 bytes laid out on them, u, parts of sums.
+struct Workspace {
+    size_t x, w, u, part, sums, bytes;  // offsets, and bytes in all
+};
+
+size_t rows_bytes(long long rows, int n) { return up(static_cast<size_t>(rows) * pitch_of(n) * 2, 256); }
+
+Workspace forward_space(const conv_linear_plan* pl) {
+    Workspace ws = {};
+    const bool lay_out = pl->K % 8 != 0;
+    ws.w = lay_out ? rows_bytes(pl->M, pl->K) : 0;
+    ws.part = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
+    ws.bytes = ws.part + gemm_part_bytes(pl->forward, pl->M, pl->N);
+    return ws;
+}
+
+Workspace backward_space(const conv_linear_plan* pl) {
+    Workspace ws = {};
+    const bool lay_out = pl->K % 8 != 0;
+    ws.w = lay_out ? rows_bytes(pl->M, pl->K) : 0;
+    ws.u = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
+    ws.sums = ws.u + (pl->act != CONV_ACT_NONE || pl->N % 8 != 0 ? rows_bytes(pl->M, pl->N) : 0);
+    ws.part = ws.sums + up(static_cast<size_t>(linear_grad_parts(pl->M, pl->N, pl->num_sms)) * pl->N * sizeof(float), 256);
+    const size_t dx = gemm_part_bytes(pl->dx, pl->M, pl->K), dw = gemm_part_bytes(pl->dw, pl->N, pl->K);
+    ws.bytes = ws.part + (dx > dw ? dx : dw);
+    return ws;
+}
+
+// Rows of a and of b (either may have none) to rows on 16 bytes.
+cudaError_t lay_out(const void* a, void* to_a, long long rows_a, const void* b, void* to_b, long long rows_b, int n, int num_sms,
+                    cudaStream_t stream) {
+    return launch_int8_layout(static_cast<const int8_t*>(a), static_cast<int8_t*>(to_a), rows_a, static_cast<const int8_t*>(b),
+                              static_cast<int8_t*>(to_b), rows_b, 2 * n, 2 * pitch_of(n), num_sms, stream);
 }
 
 }  // namespace
@@ -59,6 +94,7 @@ conv_status conv_linear_plan_create(conv_linear_plan** out, int M, int N, int K,
     if (M >= side || N >= side || K >= side || static_cast<long long>(M) * K > most ||
         static_cast<long long>(N) * K > most || static_cast<long long>(M) * N > most)
         return CONV_ERR_UNSUPPORTED;
+    if (!gemm_fits(M, N) || !gemm_fits(M, K) || !gemm_fits(N, K)) return CONV_ERR_UNSUPPORTED;
     conv_linear_plan* pl = new (std::nothrow) conv_linear_plan();
     if (pl == nullptr) return CONV_ERR_NO_MEMORY;
     pl->M = M;
@@ -72,93 +108,126 @@ conv_status conv_linear_plan_create(conv_linear_plan** out, int M, int N, int K,
         pl->device = -1;
         pl->num_sms = 152;
     } else if (cudaGetDevice(&pl->device) != cudaSuccess ||
-               cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess) {
+               cudaDeviceGetAttribute(&pl->num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess ||
+               acquire_status_word(pl->device, &pl->status, &pl->status_slot) != cudaSuccess) {
         cudaGetLastError();
         delete pl;
         return CONV_ERR_CUDA;
     }
+    pl->forward = gemm_pick_tile(M, N, K, pl->num_sms);
+    pl->dx = gemm_pick_tile(M, K, N, pl->num_sms);
+    pl->dw = gemm_pick_tile(N, K, M, pl->num_sms);
     *out = pl;
     return CONV_OK;
 }
 
 conv_status conv_linear_workspace(const conv_linear_plan* p, unsigned long long* forward, unsigned long long* backward) {
     if (p == nullptr) return CONV_ERR_INVALID_ARG;
-    if (forward != nullptr) *forward = 0;
-    if (backward != nullptr) *backward = backward_bytes(p);
+    if (forward != nullptr) *forward = forward_space(p).bytes;
+    if (backward != nullptr) *backward = backward_space(p).bytes;
     return CONV_OK;
 }
 
 conv_status conv_linear_forward(conv_linear_plan* pl, const void* x, const void* w, const float* bias,
                                 const void* residual, void* y, void* z, void* workspace, void* stream) {
     if (pl == nullptr || x == nullptr || w == nullptr || y == nullptr) return CONV_ERR_INVALID_ARG;
+    const Workspace ws = forward_space(pl);
+    if (workspace == nullptr && ws.bytes != 0) return CONV_ERR_INVALID_ARG;
     if (!all_aligned16(x, w, bias, residual, y, z, workspace)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
-    ProductParams p = {};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    GemmParams p = {};
     p.M = pl->M;
     p.N = pl->N;
     p.K = pl->K;
     p.a = static_cast<const __nv_bfloat16*>(x);
     p.b = static_cast<const __nv_bfloat16*>(w);
-    p.a_m = p.b_n = p.K;
-    p.a_k = p.b_k = 1;
+    p.a_pitch = p.b_pitch = p.K;
+    const bool laid_out = p.K % 8 != 0;
+    if (laid_out) {
+        const cudaError_t e = lay_out(x, base + ws.x, p.M, w, base + ws.w, p.N, p.K, pl->num_sms, st);
+        if (e != cudaSuccess) return launched(e);
+        p.a = reinterpret_cast<const __nv_bfloat16*>(base + ws.x);
+        p.b = reinterpret_cast<const __nv_bfloat16*>(base + ws.w);
+        p.a_pitch = p.b_pitch = pitch_of(p.K);
+    }
+    p.act = pl->act;
     p.bias = bias;
     p.r = static_cast<const __nv_bfloat16*>(residual);
     p.y = static_cast<__nv_bfloat16*>(y);
     p.z = static_cast<__nv_bfloat16*>(z);
-    p.act = pl->act;
-    return launched(launch_product(p, static_cast<cudaStream_t>(stream)));
+    p.part = reinterpret_cast<float*>(base + ws.part);
+    p.status = pl->status;
+    return launched(launch_gemm(p, pl->forward, pl->num_sms, laid_out, st));
 }
 
 conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const void* x, const void* w, const void* z,
                                  void* dx, void* dw, float* dbias, void* workspace, void* stream) {
     if (pl == nullptr || dy == nullptr || (dx == nullptr && dw == nullptr && dbias == nullptr) ||
         (dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) || (pl->act != CONV_ACT_NONE && z == nullptr) ||
-        (workspace == nullptr && backward_bytes(pl) != 0))
+        workspace == nullptr)
         return CONV_ERR_INVALID_ARG;
     if (!all_aligned16(dy, x, w, z, dx, dw, dbias, workspace)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Workspace ws = backward_space(pl);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    const bool products = dx != nullptr || dw != nullptr;
     const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(dy);
+    int u_pitch = pl->N;
+    const bool copy = products && (pl->act != CONV_ACT_NONE || pl->N % 8 != 0);
     cudaError_t e = cudaSuccess;
-    if (pl->act != CONV_ACT_NONE || dbias != nullptr) {
+    if (copy || dbias != nullptr) {
         LinearGradParams g = {};
         g.M = pl->M;
         g.N = pl->N;
         g.dy = u;
         g.z = static_cast<const __nv_bfloat16*>(z);
-        if (pl->act != CONV_ACT_NONE) u = g.u = static_cast<__nv_bfloat16*>(workspace);
+        if (copy) {
+            g.u = reinterpret_cast<__nv_bfloat16*>(base + ws.u);
+            u = g.u;
+            u_pitch = pitch_of(pl->N);
+        }
+        g.u_pitch = u_pitch;
+        g.part = reinterpret_cast<float*>(base + ws.sums);
         g.dbias = dbias;
         g.act = pl->act;
-        e = launch_linear_grad(g, st);
+        e = launch_linear_grad(g, pl->num_sms, st);
     }
-    ProductParams p = {};
+    const __nv_bfloat16* xs = static_cast<const __nv_bfloat16*>(x);
+    const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(w);
+    int k_pitch = pl->K;
+    if (e == cudaSuccess && products && pl->K % 8 != 0) {
+        e = lay_out(x, base + ws.x, dw != nullptr ? pl->M : 0, w, base + ws.w, dx != nullptr ? pl->N : 0, pl->K, pl->num_sms, st);
+        xs = reinterpret_cast<const __nv_bfloat16*>(base + ws.x);
+        wt = reinterpret_cast<const __nv_bfloat16*>(base + ws.w);
+        k_pitch = pitch_of(pl->K);
+    }
+    GemmParams p = {};
+    p.N = pl->K;
+    p.a = u;
+    p.a_pitch = u_pitch;
+    p.b_pitch = k_pitch;
+    p.b_by_k = true;
+    p.part = reinterpret_cast<float*>(base + ws.part);
+    p.status = pl->status;
     if (e == cudaSuccess && dx != nullptr) {
         p.M = pl->M;
-        p.N = pl->K;
         p.K = pl->N;
-        p.a = u;
-        p.a_m = pl->N;
-        p.a_k = 1;
-        p.b = static_cast<const __nv_bfloat16*>(w);
-        p.b_n = 1;
-        p.b_k = pl->K;
+        p.b = wt;
         p.y = static_cast<__nv_bfloat16*>(dx);
-        e = launch_product(p, st);
+        e = launch_gemm(p, pl->dx, pl->num_sms, false, st);
     }
     if (e == cudaSuccess && dw != nullptr) {
         p.M = pl->N;
-        p.N = pl->K;
         p.K = pl->M;
-        p.a = u;
-        p.a_m = 1;
-        p.a_k = pl->N;
-        p.b = static_cast<const __nv_bfloat16*>(x);
-        p.b_n = 1;
-        p.b_k = pl->K;
+        p.a_by_k = true;
+        p.b = xs;
         p.y = static_cast<__nv_bfloat16*>(dw);
-        e = launch_product(p, st);
+        e = launch_gemm(p, pl->dw, pl->num_sms, false, st);
     }
     return launched(e);
 }

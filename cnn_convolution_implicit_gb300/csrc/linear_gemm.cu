@@ -1,0 +1,681 @@
+// linear_gemm.cu -- the linear layer's products on tcgen05 tensor cores:
+//
+//   y[m][n] = act( sum_k a(m, k) * b(n, k) + bias[n] ) + r[m][n]
+//
+// One kernel for the forward product (both operands by row: K-major) and the two gradients, whose
+// operands lie the other way round: dx = u w reads w, and dw = u^T x both operands, as rows along K
+// (MN-major: the TMA brings 64 x 64 boxes, whose 128-byte rows run along m or n).
+//
+// Warp roles (one CTA per SM, persistent over units; a unit is a tile, or a part of its K):
+//   the first 8 or 16   epilogue: a warp drains 32 rows x 32 or 64 columns of tensor memory
+//   next                tensor memory; one lane issues tcgen05.mma and commits
+//   last                one lane fills the ring of (A, B) stages, K = 64 each, by TMA
+// Tensor memory holds two accumulators, so the epilogue of one unit overlaps the next one's MMAs.
+//
+// PAIR: two SMs share a 256 x 256 tile (tcgen05.mma.cta_group::2): each loads its own 128 rows of A and
+// 128 of B.
+//
+// The epilogue keeps the sum in FP32 to the end.  The residual comes by TMA into the warp's output
+// buffer while the MMAs run; every thread adds its row's part and writes the result in the same
+// place, from where the TMA stores it (so y may be the residual).  Rows of y off 16 bytes (N % 8) are
+// beyond the TMA: they are moved between buffer and memory by coalesced accesses.
+//
+// Few tiles: the K of each is shared by `splits` units, which leave FP32 parts in the workspace; a kernel
+// of its own adds them in one order and runs the epilogue.
+#include "linear_internal.h"
+#include "pointwise_math.cuh"
+#include "ptx.cuh"
+
+namespace convgb {
+
+namespace {
+
+constexpr int kStepK = 64;       // K of one stage: 128 bytes of a row
+constexpr int kTileA = 128 * 128;  // bytes of A in a stage: 128 rows
+constexpr int kBox = 64 * 128;   // bytes of an MN-major box: 64 of K, 64 of m or n
+
+template <bool PAIR, int BN>
+struct Shape {
+    static constexpr int kCtas = PAIR ? 2 : 1;
+    static constexpr int kRowsB = BN / kCtas;            // of B in this CTA
+    static constexpr int kStage = kTileA + kRowsB * 128;
+    static constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
+    static constexpr int kCols = BN / (kEpilogueWarps / 4);  // columns that a warp drains
+    static constexpr int kBlocks = kCols / 32;
+    static constexpr int kThreads = 32 * (kEpilogueWarps + 2);
+    static constexpr int kOut = 4096;                    // a warp's two blocks of 32 x 32 outputs
+    static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 6 : 8);
+    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kSmem = kStages * kStage + kEpilogueWarps * kOut + 1024;
+    static_assert(kSmem <= 232448, "shared memory of a block");
+};
+
+struct Bars {
+    uint64_t* full;
+    uint64_t* empty;
+    uint64_t* tfull;
+    uint64_t* tempty;
+    uint64_t* drain;
+    uint64_t* res;  // two for each epilogue warp
+    uint32_t* tmem_slot;
+    int* abort;
+};
+
+// Arrive on the pair leader's barrier; tensor memory's contents are ordered by tcgen05's own fences.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_addr(bar), 0)) : "memory");
+}
+
+// A bounded wait whose answer is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
+}
+
+// What a unit is: its tile, in order of groups of kGroupM tile rows (neighbouring units share rows of A and
+// columns of B, which then come from L2), and its steps of K.
+constexpr int kGroupM = 8;
+
+struct Tiles {
+    int m_tiles, n_tiles, tiles, units, step, ksteps, splits;
+};
+
+struct Unit {
+    int mt, nt, split, k_first, k_count;
+};
+
+__device__ __forceinline__ Unit unit_at(const Tiles& t, int u) {
+    Unit w;
+    w.split = u / t.tiles;
+    const int i = u - w.split * t.tiles;
+    const int per_group = kGroupM * t.n_tiles, g = i / per_group, rest = i - g * per_group;
+    const int rows = min(kGroupM, t.m_tiles - g * kGroupM);
+    w.nt = rest / rows;
+    w.mt = g * kGroupM + rest - w.nt * rows;
+    w.k_first = static_cast<int>(static_cast<long long>(w.split) * t.ksteps / t.splits);
+    w.k_count = static_cast<int>(static_cast<long long>(w.split + 1) * t.ksteps / t.splits) - w.k_first;
+    return w;
+}
+
+// Shared-memory descriptor of an MN-major operand: boxes of 64 (K) rows of 128 bytes in the 128-byte swizzle,
+// 8 rows of K 1,024 bytes apart (stride offset), the next 64 of m or n a box further (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kBox >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// ROWS rows of an operand from row `row`, K = 64 from k, to a stage.
+template <bool PAIR, bool BY_K, int ROWS>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_leader, int row, int k) {
+    if constexpr (BY_K) {
+#pragma unroll
+        for (int i = 0; i < ROWS / 64; ++i) {
+            if constexpr (PAIR) tma_load_2d_pair(dst + i * kBox, map, bar_leader, row + 64 * i, k);
+            else tma_load_2d(dst + i * kBox, map, bar, row + 64 * i, k);
+        }
+    } else {
+        if constexpr (PAIR) tma_load_2d_pair(dst, map, bar_leader, k, row);
+        else tma_load_2d(dst, map, bar, k, row);
+    }
+}
+
+template <bool BY_K>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {  // K = 16 j .. 16 j + 15 of a stage
+    if constexpr (BY_K) return sdesc_mn(base + j * 2048);
+    else return sdesc_sw128(base) + 2 * j;
+}
+
+// ---------------------------------------------------------------- epilogue of a 32 x 32 block
+// A thread has one row of it: 64 bytes, in the 64-byte swizzle that the TMA reads and writes.
+__device__ __forceinline__ uint4* block_chunk(uint8_t* block, int row, int j) {
+    return reinterpret_cast<uint4*>(block + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void add_bias(uint32_t (&v)[32], const float* bias, int n, int N) {
+    if (bias == nullptr) return;
+    if (n + 32 <= N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n) + i);
+            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + b.x);
+            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + b.y);
+            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + b.z);
+            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + b.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + (n + i < N ? __ldg(bias + n + i) : 0.0f));
+    }
+}
+
+__device__ __forceinline__ void stage(uint8_t* block, int row, const uint32_t (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
+        *block_chunk(block, row, j) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
+// act(v) + r, each rounded by itself: the result is the same with and without z.
+template <int ACT>
+__device__ __forceinline__ void finish(uint32_t (&v)[32], const uint4 (&r)[4], bool with_r) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(activate<ACT>(__uint_as_float(v[i])));
+    if (!with_r) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t u[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t &lo = v[8 * j + 2 * i], &hi = v[8 * j + 2 * i + 1];
+            lo = __float_as_uint(__fadd_rn(__uint_as_float(lo), __uint_as_float(u[i] << 16)));
+            hi = __float_as_uint(__fadd_rn(__uint_as_float(hi), __uint_as_float(u[i] & 0xffff0000u)));
+        }
+    }
+}
+
+// Between a block in shared memory and rows of y that start on T's size only, neighbouring lanes at
+// neighbouring places.
+template <typename T, bool OUT>
+__device__ __forceinline__ void move_block(uint8_t* block, __nv_bfloat16* y, long long N, int rows, int columns) {
+    constexpr int kEach = static_cast<int>(sizeof(T)) / 2, kLanes = 32 / kEach, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31, c = (lane % kLanes) * kEach;
+    if (c >= columns) return;
+#pragma unroll 8
+    for (int i = 0; i < 32; i += kRows) {
+        const int row = i + lane / kLanes;
+        if (row >= rows) continue;
+        T* mem = reinterpret_cast<T*>(y + row * N + c);
+        T* own = reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(block_chunk(block, row, c >> 3)) + (c & 7) * 2);
+        if constexpr (OUT) *mem = *own;
+        else *own = *mem;
+    }
+}
+
+template <bool OUT>
+__device__ __forceinline__ void move_rows(uint8_t* block, __nv_bfloat16* y, int N, int m, int n, int M) {
+    __nv_bfloat16* at = y + static_cast<long long>(m) * N + n;
+    const int rows = min(32, M - m), columns = min(32, N - n);
+    if (N % 2 == 0) move_block<uint32_t, OUT>(block, at, N, rows, columns);
+    else move_block<uint16_t, OUT>(block, at, N, rows, columns);
+}
+
+struct EpilogueMaps {
+    const CUtensorMap* y;
+    const CUtensorMap* z;
+    const CUtensorMap* part;
+};
+
+__device__ __forceinline__ void run_act(int act, uint32_t (&v)[32], const uint4 (&r)[4], bool with_r) {
+    if (act == CONV_ACT_RELU) finish<CONV_ACT_RELU>(v, r, with_r);
+    else if (act == CONV_ACT_SILU) finish<CONV_ACT_SILU>(v, r, with_r);
+    else finish<CONV_ACT_NONE>(v, r, with_r);
+}
+
+// One block, sums in v, the residual in `block` where there is one.
+template <bool TMA>
+__device__ __forceinline__ void finish_block(const GemmParams& p, const EpilogueMaps& maps, uint32_t (&v)[32], uint8_t* block, int m, int n) {
+    const int lane = threadIdx.x & 31;
+    add_bias(v, p.bias, n, p.N);
+    uint4 r[4] = {};
+    if (p.r != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = *block_chunk(block, lane, j);
+    }
+    const auto out = [&](const CUtensorMap* map, __nv_bfloat16* y) {
+        stage(block, lane, v);
+        if constexpr (TMA) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(map, block, n, m);
+                bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            move_rows<true>(block, y, p.N, m, n, p.M);
+            __syncwarp();
+        }
+    };
+    if (p.z != nullptr) {
+        if (!TMA) __syncwarp();  // every lane has its row of the residual
+        out(maps.z, p.z);
+        if (TMA && lane == 0) bulk_wait_read_all();
+        __syncwarp();
+    }
+    run_act(p.act, v, r, p.r != nullptr);
+    out(maps.y, p.y);
+}
+
+// The sums of a block as they are to the workspace: 128-byte rows in the 128-byte swizzle.
+__device__ __forceinline__ void leave_block(const CUtensorMap* map, const uint32_t (&v)[32], uint8_t* buffer, int m, int n, int split) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(buffer + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_3d(map, buffer, n, m, split);
+        bulk_commit();
+    }
+}
+
+template <bool PAIR, int BN, bool A_BY_K, bool B_BY_K>
+__global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
+    linear_gemm_kernel(const GemmParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                       const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
+                       const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_part) {
+    using S = Shape<PAIR, BN>;
+    constexpr int kMmaWarp = S::kEpilogueWarps, kLoadWarp = kMmaWarp + 1, kCtas = S::kCtas;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join of parts that may follow
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_addr(smem) & 1023u) {  // the swizzle's atoms; uniform, so no CTA waits for another
+        record_status(p.status, kStatusTimeoutMma, nullptr);
+        return;
+    }
+    Bars b;
+    uint8_t* outputs = smem + S::kStages * S::kStage;
+    b.full = reinterpret_cast<uint64_t*>(outputs + S::kEpilogueWarps * S::kOut);
+    b.empty = b.full + S::kStages;
+    b.tfull = b.empty + S::kStages;
+    b.tempty = b.tfull + 2;
+    b.drain = b.tempty + 2;
+    b.res = b.drain + 1;
+    b.tmem_slot = reinterpret_cast<uint32_t*>(b.res + 2 * S::kEpilogueWarps);
+    b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
+    volatile int* abort = b.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+
+    Tiles tiles;
+    tiles.m_tiles = (p.M + 128 * kCtas - 1) / (128 * kCtas);
+    tiles.n_tiles = (p.N + BN - 1) / BN;
+    tiles.tiles = tiles.m_tiles * tiles.n_tiles;
+    tiles.splits = p.splits;
+    tiles.units = tiles.tiles * p.splits;
+    tiles.step = static_cast<int>(gridDim.x) / kCtas;
+    tiles.ksteps = (p.K + kStepK - 1) / kStepK;
+    const int unit0 = static_cast<int>(blockIdx.x) / kCtas;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&b.full[s], 1);
+            mbar_init(&b.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.tfull[i], 1);
+            mbar_init(&b.tempty[i], kCtas * S::kEpilogueWarps);
+        }
+        mbar_init(b.drain, 1);
+        for (int i = 0; i < 2 * S::kEpilogueWarps; ++i) mbar_init(&b.res[i], 1);
+        *b.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(b.tmem_slot, S::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(b.tmem_slot, S::kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // the peer's barriers exist before anything signals them
+    tc_fence_after();
+    const uint32_t tmem = *b.tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // operands from the kernel before this one
+
+    if (warp < S::kEpilogueWarps) {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3, part = warp >> 2;
+        uint8_t* buffer = outputs + warp * S::kOut;
+        uint64_t* res = b.res + 2 * warp;
+        const bool tma = p.N % 8 == 0;
+        const EpilogueMaps maps = {&map_y, &map_z, &map_part};
+        uint32_t res_phase[2] = {0, 0};
+        int local = 0;
+        bool ok = true;
+        for (int u = unit0; u < tiles.units; u += tiles.step, ++local) {
+            const Unit w = unit_at(tiles, u);
+            const int buf = local & 1;
+            const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
+            const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128 + quarter * 32, n = w.nt * BN + part * S::kCols;
+            const int blocks = m >= p.M ? 0 : min(S::kBlocks, (p.N - n + 31) / 32);  // 0 or less: none
+            const bool by_tma = p.r != nullptr && tma && p.splits == 1;
+            if (by_tma && lane == 0) {
+                bulk_wait_read_all();  // what went through the buffers before has left them
+                for (int i = 0; i < blocks; ++i) {
+                    mbar_arrive_expect_tx(&res[i], 2048);
+                    tma_load_2d(buffer + i * 2048, &map_r, &res[i], n + 32 * i, m);
+                }
+            }
+            __syncwarp();
+            if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
+                record_status(p.status, kStatusTimeoutEpilogue, abort);
+                ok = false;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < S::kBlocks; ++i) {
+                if (i >= blocks) break;
+                uint8_t* block = buffer + i * 2048;
+                uint32_t v[32];
+                if (ok) {
+                    tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + part * S::kCols + 32 * i, v);
+                    tmem_ld_wait(v);
+                }
+                if (by_tma) {  // also after a wait that gave up: no copy may be in flight when the CTA leaves
+                    if (!warp_wait(&res[i], res_phase[i], nullptr)) {
+                        record_status(p.status, kStatusTimeoutEpilogue, abort);
+                        ok = false;
+                    }
+                    res_phase[i] ^= 1u;
+                }
+                if (!ok) continue;
+                if (p.splits > 1) {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+                    leave_block(&map_part, v, buffer, m, n + 32 * i, w.split);
+                } else if (tma) {
+                    if (!by_tma) {
+                        if (lane == 0) bulk_wait_read_all();
+                        __syncwarp();
+                    }
+                    finish_block<true>(p, maps, v, block, m, n + 32 * i);
+                } else {
+                    if (p.r != nullptr) {
+                        move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + 32 * i, p.M);
+                        __syncwarp();
+                    }
+                    finish_block<false>(p, maps, v, block, m, n + 32 * i);
+                }
+            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) arrive_leader(&b.tempty[buf]);
+                else mbar_arrive(&b.tempty[buf]);
+            }
+        }
+        if (lane == 0) bulk_wait_all();  // none in flight when the CTA leaves
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ operands
+        if (lane == 0) {
+            long long issued = 0;
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int u = unit0; u < tiles.units && ok; u += tiles.step) {
+                const Unit w = unit_at(tiles, u);
+                const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128, n = w.nt * BN + static_cast<int>(rank) * S::kRowsB;
+                for (int ks = 0; ks < w.k_count; ++ks) {
+                    if (!mbar_wait(&b.empty[st], ph ^ 1u, abort)) {
+                        record_status(p.status, kStatusTimeoutProducer, abort);
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_arrive_expect_tx(&b.full[st], kCtas * S::kStage);
+                    uint8_t* dst = smem + st * S::kStage;
+                    const uint32_t bar = PAIR ? mapa_shared(smem_addr(&b.full[st]), 0) : 0u;
+                    const int k = (w.k_first + ks) * kStepK;  // past the matrix: zeros
+                    load_operand<PAIR, A_BY_K, 128>(dst, &map_a, &b.full[st], bar, m, k);
+                    load_operand<PAIR, B_BY_K, S::kRowsB>(dst + kTileA, &map_b, &b.full[st], bar, n, k);
+                    ++issued;
+                    if (++st == S::kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < S::kStages; ++s) {  // no copy in flight when the CTA leaves
+                const long long fills = issued / S::kStages + (s < issued % S::kStages ? 1 : 0);
+                if (fills == 0) continue;
+                const uint32_t par = static_cast<uint32_t>((fills - 1) & 1);
+                // the peer of a pair sees the MMAs release each slot, which needs its copies landed
+                if (!(leader ? mbar_wait(&b.full[s], par, nullptr) : mbar_wait(&b.empty[s], par, nullptr)))
+                    record_status(p.status, kStatusTimeoutDrain, abort);
+            }
+        }
+    } else if (lane == 0 && leader) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t idesc = idesc_bf16_f32(128 * kCtas, BN) | (A_BY_K ? 1u << 15 : 0u) | (B_BY_K ? 1u << 16 : 0u);
+        int st = 0, local = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = unit0; u < tiles.units && ok; u += tiles.step, ++local) {
+            const Unit w = unit_at(tiles, u);
+            const int buf = local & 1;
+            const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
+            if (!mbar_wait_cluster(&b.tempty[buf], use ^ 1u, abort)) {
+                record_status(p.status, kStatusTimeoutMma, abort);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + buf * BN;
+            for (int ks = 0; ks < w.k_count; ++ks) {
+                if (!mbar_wait_cluster(&b.full[st], ph, abort)) {
+                    record_status(p.status, kStatusTimeoutMma, abort);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = smem_addr(smem + st * S::kStage);
+                const int mmas = min(4, (p.K - (w.k_first + ks) * kStepK + 15) >> 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= mmas) break;
+                    const uint64_t da = operand_desc<A_BY_K>(base, j), db = operand_desc<B_BY_K>(base + kTileA, j);
+                    const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
+                    if constexpr (PAIR) mma_bf16_pair(d, da, db, idesc, acc);
+                    else mma_bf16(d, da, db, idesc, acc);
+                }
+                if constexpr (PAIR) mma_commit_pair(&b.empty[st], 3);
+                else mma_commit(&b.empty[st]);
+                if (++st == S::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if constexpr (PAIR) mma_commit_pair(&b.tfull[buf], 3);
+            else mma_commit(&b.tfull[buf]);
+        }
+        if constexpr (PAIR) mma_commit_pair(b.drain, 1);
+        else mma_commit(b.drain);
+        if (!mbar_wait_cluster(b.drain, 0, nullptr)) record_status(p.status, kStatusTimeoutDrain, abort);
+    }
+    __syncwarp();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // no CTA leaves while its peer may still signal it
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, S::kTmemCols);
+        else tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- parts of K
+// Four neighbouring outputs a thread: their parts in order, then the epilogue.
+__global__ void __launch_bounds__(256) linear_join_kernel(const GemmParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int quads = (p.N + 3) / 4;
+    const long long i = blockIdx.x * 256LL + threadIdx.x, m = i / quads;
+    if (m >= p.M) return;
+    const int n = static_cast<int>(i - m * quads) * 4;
+    const float4* from = reinterpret_cast<const float4*>(p.part) + i;
+    const long long step = static_cast<long long>(p.M) * quads;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+        const float4 v = from[k * step];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    float z[4] = {s.x, s.y, s.z, s.w}, y[4];
+    const long long o = m * p.N + n;
+    const int count = min(4, p.N - n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (p.bias != nullptr && j < count) z[j] += __ldg(p.bias + n + j);
+        y[j] = p.act == CONV_ACT_RELU ? activate<CONV_ACT_RELU>(z[j]) : (p.act == CONV_ACT_SILU ? activate<CONV_ACT_SILU>(z[j]) : z[j]);
+    }
+    if (p.N % 4 == 0) {
+        if (p.z != nullptr) *reinterpret_cast<uint2*>(p.z + o) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+        if (p.r != nullptr) {  // ordinary loads: y may be the residual
+            const uint2 r = *reinterpret_cast<const uint2*>(p.r + o);
+            y[0] = __fadd_rn(y[0], __uint_as_float(r.x << 16));
+            y[1] = __fadd_rn(y[1], __uint_as_float(r.x & 0xffff0000u));
+            y[2] = __fadd_rn(y[2], __uint_as_float(r.y << 16));
+            y[3] = __fadd_rn(y[3], __uint_as_float(r.y & 0xffff0000u));
+        }
+        *reinterpret_cast<uint2*>(p.y + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j >= count) break;
+        if (p.z != nullptr) p.z[o + j] = __float2bfloat16_rn(z[j]);
+        p.y[o + j] = __float2bfloat16_rn(p.r != nullptr ? __fadd_rn(y[j], __bfloat162float(p.r[o + j])) : y[j]);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+constexpr int part_pitch(int N) { return (N + 3) / 4 * 4; }
+
+// [rows][inner] BF16 matrix in boxes of box_rows x box_inner.
+bool encode_matrix(CUtensorMap* map, const void* base, long long rows, long long inner, long long pitch, int box_rows, int box_inner,
+                   CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows)};
+    return tensor_map_encoder_ready() && encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+                                                      swizzle) == CUDA_SUCCESS;
+}
+
+bool encode_operand(CUtensorMap* map, const __nv_bfloat16* base, bool by_k, int rows, int K, int pitch, int box_rows) {
+    return by_k ? encode_matrix(map, base, K, rows, pitch, kStepK, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                : encode_matrix(map, base, rows, K, pitch, box_rows, kStepK, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool PAIR, int BN, bool A_BY_K, bool B_BY_K>
+cudaError_t launch_variant(const GemmParams& p, int num_sms, bool after_other, cudaStream_t stream) {
+    using S = Shape<PAIR, BN>;
+    static SmemLimitCache limits;
+    auto* fn = linear_gemm_kernel<PAIR, BN, A_BY_K, B_BY_K>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), S::kSmem, limits);
+    if (e != cudaSuccess) return e;
+    const long long units = (static_cast<long long>(p.M) + 128 * S::kCtas - 1) / (128 * S::kCtas) * ((p.N + BN - 1) / BN) * p.splits;
+    const int slots = num_sms / S::kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((units < slots ? units : slots) * S::kCtas));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    if (PAIR) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (after_other) {  // its set-up overlaps the kernel before it
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = attr;
+    CUtensorMap a, b, y = CUtensorMap(), z = CUtensorMap(), r = CUtensorMap(), part = CUtensorMap();
+    bool made = encode_operand(&a, p.a, A_BY_K, p.M, p.K, p.a_pitch, 128) && encode_operand(&b, p.b, B_BY_K, p.N, p.K, p.b_pitch, S::kRowsB);
+    if (p.splits > 1) {
+        const cuuint64_t pitch = static_cast<cuuint64_t>(part_pitch(p.N)) * 4;
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(p.splits)};
+        const cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(p.M)};
+        const cuuint32_t box[3] = {32, 32, 1};
+        made = made && encode_tiled(&part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.part, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+    } else if (p.N % 8 == 0) {
+        const auto rows = [&](CUtensorMap* map, const void* base) {
+            return base == nullptr || encode_matrix(map, base, p.M, p.N, p.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+        };
+        made = made && rows(&y, p.y) && rows(&z, p.z) && rows(&r, p.r);
+    }
+    if (!made) return cudaErrorInvalidValue;
+    if ((e = cudaLaunchKernelEx(&cfg, fn, p, a, b, y, z, r, part)) != cudaSuccess || p.splits == 1) return e;
+    cudaLaunchConfig_t join = {};
+    const long long quads = static_cast<long long>(p.M) * ((p.N + 3) / 4);
+    join.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
+    join.blockDim = dim3(256);
+    join.stream = stream;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    join.attrs = early;
+    join.numAttrs = 1;
+    return cudaLaunchKernelEx(&join, linear_join_kernel, p);
+}
+
+template <bool A_BY_K, bool B_BY_K>
+cudaError_t launch_operands(const GemmParams& p, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream) {
+    if (t.columns == 256) return launch_variant<true, 256, A_BY_K, B_BY_K>(p, num_sms, after_other, stream);
+    if (t.columns == 128) return launch_variant<false, 128, A_BY_K, B_BY_K>(p, num_sms, after_other, stream);
+    return launch_variant<false, 64, A_BY_K, B_BY_K>(p, num_sms, after_other, stream);
+}
+
+}  // namespace
+
+bool gemm_fits(int M, int N) { return (static_cast<long long>(M) + 127) / 128 * ((N + 63) / 64) < (1LL << 30); }
+
+size_t gemm_part_bytes(const GemmTile& t, int M, int N) {
+    return t.splits > 1 ? static_cast<size_t>(t.splits) * M * part_pitch(N) * sizeof(float) : 0;
+}
+
+// The tile shape and split of K that cost least by these figures, in microseconds: a K = 64 step, what a tile takes
+// besides, the launch; a split adds its parts' way through memory and the join.
+GemmTile gemm_pick_tile(int M, int N, int K, int num_sms) {
+    struct Cost {
+        int rows, columns;
+        double step, besides;
+    };
+    constexpr Cost kCosts[3] = {{256, 256, 0.29, 2.0}, {128, 128, 0.17, 1.3}, {128, 64, 0.13, 1.0}};
+    const long long steps = (K + kStepK - 1) / kStepK;
+    double best = 0.0;
+    GemmTile pick = {};
+    for (const Cost& c : kCosts) {
+        const long long tiles = (static_cast<long long>(M) + c.rows - 1) / c.rows * ((N + c.columns - 1) / c.columns);
+        const long long slots = c.rows == 256 ? num_sms / 2 : num_sms;
+        for (int splits = 1; splits <= 64 && splits <= steps; ++splits) {
+            if (splits > 1 && tiles * splits > slots) break;
+            const long long rounds = (tiles * splits + slots - 1) / slots;
+            const double each = static_cast<double>((steps + splits - 1) / splits) * c.step + c.besides;
+            const double join = splits > 1 ? 2.0 + static_cast<double>(M) * N * splits * 8.0 / 4e6 : 0.0;
+            const double cost = static_cast<double>(rounds) * each + join;
+            if (pick.rows == 0 || cost < best) {
+                best = cost;
+                pick = {c.rows, c.columns, splits};
+            }
+        }
+    }
+    return pick;
+}
+
+cudaError_t launch_gemm(const GemmParams& given, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream) {
+    GemmParams p = given;
+    p.splits = t.splits;
+    if (p.a_by_k && p.b_by_k) return launch_operands<true, true>(p, t, num_sms, after_other, stream);
+    if (p.b_by_k) return launch_operands<false, true>(p, t, num_sms, after_other, stream);
+    return launch_operands<false, false>(p, t, num_sms, after_other, stream);
+}
+
+}  // namespace convgb

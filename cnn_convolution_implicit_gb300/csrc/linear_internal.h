@@ -1,5 +1,5 @@
-// linear_internal.h -- parameter block and launchers shared between the linear layer's plan code
-// (linear_api.cu) and its kernels.
+// linear_internal.h -- parameter blocks and launchers shared between the linear layer's plan code
+// (linear_api.cu) and its kernels (linear_gemm.cu, linear_few.cu, linear_grad.cu).
 #pragma once
 
 #include <cstdint>
@@ -10,29 +10,48 @@
 
 namespace convgb {
 
-// out[m][n] = act(sum_k a(m, k) * b(n, k) + bias[n]) + residual[m][n]
-struct ProductParams {
+// y[m][n] = act(sum_k a(m, k) * b(n, k) + bias[n]) + r[m][n].  An operand is a matrix of rows `pitch` elements
+// apart: [m][k], or with *_by_k [k][m].
+struct GemmParams {
     int M, N, K;
-    const __nv_bfloat16* a;  // a(m, k) = a[m * a_m + k * a_k]
+    const __nv_bfloat16* a;
     const __nv_bfloat16* b;
-    long long a_m, a_k, b_n, b_k;
-    const float* bias;            // nullptr: 0
-    const __nv_bfloat16* r;       // nullptr: 0
+    int a_pitch, b_pitch;
+    bool a_by_k, b_by_k;
+    int act;              // conv_act
+    const float* bias;    // nullptr: 0
+    const __nv_bfloat16* r;  // nullptr: 0
     __nv_bfloat16* y;
-    __nv_bfloat16* z;             // nullptr: not wanted
-    int act;
+    __nv_bfloat16* z;     // nullptr: not wanted
+    float* part;          // workspace of parts of K: [splits][M][N rounded up to 4]
+    int splits;           // units that share the K of a tile
+    unsigned* status;
 };
-cudaError_t launch_product(const ProductParams& p, cudaStream_t stream);
+
+// The tile of the tensor-core kernel: rows and columns (256 x 256 on a pair of SMs), and how many units share
+// its K.
+struct GemmTile {
+    int rows, columns, splits;
+};
+GemmTile gemm_pick_tile(int M, int N, int K, int num_sms);
+size_t gemm_part_bytes(const GemmTile& t, int M, int N);
+bool gemm_fits(int M, int N);  // tile counts within 32 bits
+// Rows of both operands start on 16 bytes.  after_other: the kernel before it on the stream wrote an
+// operand and lets this one start early.
+cudaError_t launch_gemm(const GemmParams& p, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream);
 
 // u = dy * act'(z) in BF16, and its sums over the rows
 struct LinearGradParams {
     int M, N;
     const __nv_bfloat16* dy;
     const __nv_bfloat16* z;
-    __nv_bfloat16* u;  // nullptr: not wanted
+    __nv_bfloat16* u;  // rows u_pitch elements apart; nullptr: not wanted
+    int u_pitch;
     float* dbias;      // nullptr: not wanted
+    float* part;       // workspace: [parts][N], where there is more than one
     int act;
 };
-cudaError_t launch_linear_grad(const LinearGradParams& p, cudaStream_t stream);
+int linear_grad_parts(int M, int N, int num_sms);
+cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace convgb

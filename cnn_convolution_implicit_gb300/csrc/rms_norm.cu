@@ -407,21 +407,6 @@ __global__ void __launch_bounds__(256) rms_columns_kernel(const RmsParams p) {
     }
 }
 
-// dgamma from its parts, 32 columns a CTA, in one order.
-__global__ void __launch_bounds__(1024) rms_join_kernel(const float* part, int parts, int C, float* dgamma) {
-    __shared__ float sums[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float total = 0.0f;
-    if (c < C) {
-#pragma unroll 4
-        for (int i = warp; i < parts; i += 32) total += part[static_cast<long long>(i) * C + c];
-    }
-    sums[warp][lane] = total;
-    __syncthreads();
-    const float sum = warp_sum(sums[lane][warp]);  // column `warp` of the block
-    if (lane == 0 && blockIdx.x * 32 + warp < C) dgamma[blockIdx.x * 32 + warp] = sum;
-}
-
 // ---------------------------------------------------------------- launches
 struct Form {
     int items, warps;  // 0: rows too long for registers
@@ -488,7 +473,7 @@ cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
             rms_backward_kernel<T, ALIGNED, I, W, false><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
         });
     }
-    if (p.dgamma != nullptr) rms_join_kernel<<<blocks, 1024, 0, stream>>>(p.part, p.parts, p.C, p.dgamma);
+    if (p.dgamma != nullptr) return launch_join_columns(p.part, p.parts, p.C, p.dgamma, stream);
     return cudaGetLastError();
 }
 

@@ -34,6 +34,9 @@ int rms_backward_parts(const RmsParams& p, int num_sms);
 cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream);
 cudaError_t launch_rms_backward(const RmsParams& p, cudaStream_t stream);
 
+// Sums of `parts` rows of C values each, in one order (column_sums.cu).
+cudaError_t launch_join_columns(const float* part, int parts, int C, float* out, cudaStream_t stream);
+
 struct DropoutParams {
     const void* x;
     const void* r;  // nullptr: 0
