@@ -11,6 +11,7 @@ using namespace convgb;
 
 struct conv_linear_plan {
     int M, N, K, act;
+    bool few;                  // the forward product runs in the kernel of few rows
     GemmTile forward, dx, dw;  // tiles of the three products
     int device;
     int num_sms;
@@ -54,6 +55,7 @@ size_t rows_bytes(long long rows, int n) { return up(static_cast<size_t>(rows) *
 
 Workspace forward_space(const conv_linear_plan* pl) {
     Workspace ws = {};
+    if (pl->few) return ws;
     const bool lay_out = pl->K % 8 != 0;
     ws.w = lay_out ? rows_bytes(pl->M, pl->K) : 0;
     ws.part = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
@@ -114,6 +116,7 @@ conv_status conv_linear_plan_create(conv_linear_plan** out, int M, int N, int K,
         delete pl;
         return CONV_ERR_CUDA;
     }
+    pl->few = linear_use_few(M, N, K);
     pl->forward = gemm_pick_tile(M, N, K, pl->num_sms);
     pl->dx = gemm_pick_tile(M, K, N, pl->num_sms);
     pl->dw = gemm_pick_tile(N, K, M, pl->num_sms);
@@ -137,6 +140,12 @@ conv_status conv_linear_forward(conv_linear_plan* pl, const void* x, const void*
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pl->few) {
+        const FewParams f = {pl->M, pl->N, pl->K, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w), bias,
+                             static_cast<const __nv_bfloat16*>(residual), static_cast<__nv_bfloat16*>(y),
+                             static_cast<__nv_bfloat16*>(z), pl->act};
+        return launched(launch_linear_few(f, st));
+    }
     uint8_t* base = static_cast<uint8_t*>(workspace);
     GemmParams p = {};
     p.M = pl->M;

@@ -7,9 +7,14 @@
 // (MN-major: the TMA brings 64 x 64 boxes, whose 128-byte rows run along m or n).
 //
 // Warp roles (one CTA per SM, persistent over units; a unit is a tile, or a part of its K):
-//   the first 8 or 16   epilogue: a warp drains 32 rows x 32 or 64 columns of tensor memory
-//   next                tensor memory; one lane issues tcgen05.mma and commits
-//   last                one lane fills the ring of (A, B) stages, K = 64 each, by TMA
+//   the first 8 or 16   epilogue: a warp drains 32 rows of tensor memory, 64 columns at a time; in two groups that
+//                       take the units in turn where a CTA has several, so that one's residuals and sums arrive
+//                       while the other works
+//   next                tensor memory; the whole warp walks the stages and one elected lane issues tcgen05.mma
+//                       and commits.  (A loop of one lane only, its operands in the registers of a divergent
+//                       thread, took 95 clocks an MMA and 700 a stage of 512 clocks of MMAs: 19456 x 4096 x 4096
+//                       376 us, and 328 as it is, 1,988 TFLOP/s.)
+//   last                fills the ring of (A, B) stages, K = 64 each, by TMA
 // Tensor memory holds two accumulators, so the epilogue of one unit overlaps the next one's MMAs.
 //
 // PAIR: two SMs share a 256 x 256 tile (tcgen05.mma.cta_group::2): each loads its own 128 rows of A and
@@ -30,8 +35,16 @@ namespace convgb {
 
 namespace {
 
+constexpr int kBlockCols = 64, kBlockBytes = 32 * 128;  // 32 rows x 64 columns of outputs
 constexpr int kStepK = 64;       // K of one stage: 128 bytes of a row
 constexpr int kTileA = 128 * 128;  // bytes of A in a stage: 128 rows
+// What a launch fixes besides the operands.
+struct Ring {
+    int stages;  // of operands
+    int warps;   // of the epilogue that work
+    int groups;  // of them: 1, or 2 that take the units in turn
+};
+
 constexpr int kBox = 64 * 128;   // bytes of an MN-major box: 64 of K, 64 of m or n
 
 template <bool PAIR, int BN>
@@ -40,14 +53,13 @@ struct Shape {
     static constexpr int kRowsB = BN / kCtas;            // of B in this CTA
     static constexpr int kStage = kTileA + kRowsB * 128;
     static constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
-    static constexpr int kCols = BN / (kEpilogueWarps / 4);  // columns that a warp drains
-    static constexpr int kBlocks = kCols / 32;
     static constexpr int kThreads = 32 * (kEpilogueWarps + 2);
-    static constexpr int kOut = 4096;                    // a warp's two blocks of 32 x 32 outputs
-    static constexpr int kStages = BN == 256 ? 5 : (BN == 128 ? 6 : 8);
     static constexpr int kTmemCols = 2 * BN;
-    static constexpr int kSmem = kStages * kStage + kEpilogueWarps * kOut + 1024;
-    static_assert(kSmem <= 232448, "shared memory of a block");
+    // Each epilogue warp that works has room for a block of outputs; the ring takes the rest.
+    static constexpr int kBarBytes = 512 + kEpilogueWarps * 128;  // barriers, the warps' biases
+    static constexpr int stages(int warps) { return (232448 - kBarBytes - warps * kBlockBytes) / kStage; }
+    static constexpr int kMaxStages = stages(8);
+    static_assert((2 * kMaxStages + 5 + kEpilogueWarps) * 8 + 8 <= 512, "barriers");
 };
 
 struct Bars {
@@ -56,7 +68,8 @@ struct Bars {
     uint64_t* tfull;
     uint64_t* tempty;
     uint64_t* drain;
-    uint64_t* res;  // two for each epilogue warp
+    uint64_t* res;  // one for each epilogue warp
+    float* bias;    // 32 values for each of them
     uint32_t* tmem_slot;
     int* abort;
 };
@@ -72,6 +85,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
+}
+
+// The same one lane of a converged warp at every call: MMAs and their commits are one thread's.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (PAIR) mma_commit_pair(bar, 3);
+    else mma_commit(bar);
 }
 
 // What a unit is: its tile, in order of groups of kGroupM tile rows (neighbouring units share rows of A and
@@ -127,147 +153,166 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {  // K =
     else return sdesc_sw128(base) + 2 * j;
 }
 
-// ---------------------------------------------------------------- epilogue of a 32 x 32 block
-// A thread has one row of it: 64 bytes, in the 64-byte swizzle that the TMA reads and writes.
+// ---------------------------------------------------------------- epilogue of a block: 32 rows x 64 columns
+// A thread has one row of it: 128 bytes, in the 128-byte swizzle that the TMA reads and writes.
 __device__ __forceinline__ uint4* block_chunk(uint8_t* block, int row, int j) {
-    return reinterpret_cast<uint4*>(block + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
+    return reinterpret_cast<uint4*>(block + row * 128 + ((j ^ (row & 7)) << 4));
 }
 
-__device__ __forceinline__ void add_bias(uint32_t (&v)[32], const float* bias, int n, int N) {
-    if (bias == nullptr) return;
-    if (n + 32 <= N) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n) + i);
-            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + b.x);
-            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + b.y);
-            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + b.z);
-            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + b.w);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + (n + i < N ? __ldg(bias + n + i) : 0.0f));
-    }
-}
-
-__device__ __forceinline__ void stage(uint8_t* block, int row, const uint32_t (&v)[32]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
-        *block_chunk(block, row, j) = make_uint4(u[0], u[1], u[2], u[3]);
-    }
-}
-
-// act(v) + r, each rounded by itself: the result is the same with and without z.
+// Eight columns of a row: act(v + bias) + r, each operation rounded by itself.  bias: the columns' in shared memory,
+// the same for every lane.
 template <int ACT>
-__device__ __forceinline__ void finish(uint32_t (&v)[32], const uint4 (&r)[4], bool with_r) {
+__device__ __forceinline__ uint4 finish_chunk(const uint32_t* v, const float4* bias, const uint4* r) {
+    float f[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(activate<ACT>(__uint_as_float(v[i])));
-    if (!with_r) return;
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+    if (bias != nullptr) {
+        const float4 lo = bias[0], hi = bias[1];
+        const float add[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t u[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+        for (int i = 0; i < 8; ++i) f[i] = __fadd_rn(f[i], add[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = activate<ACT>(f[i]);
+    if (r != nullptr) {
+        const uint4 q = *r;
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t &lo = v[8 * j + 2 * i], &hi = v[8 * j + 2 * i + 1];
-            lo = __float_as_uint(__fadd_rn(__uint_as_float(lo), __uint_as_float(u[i] << 16)));
-            hi = __float_as_uint(__fadd_rn(__uint_as_float(hi), __uint_as_float(u[i] & 0xffff0000u)));
+            f[2 * i] = __fadd_rn(f[2 * i], __uint_as_float(u[i] << 16));
+            f[2 * i + 1] = __fadd_rn(f[2 * i + 1], __uint_as_float(u[i] & 0xffff0000u));
         }
     }
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
 // Between a block in shared memory and rows of y that start on T's size only, neighbouring lanes at
 // neighbouring places.
 template <typename T, bool OUT>
 __device__ __forceinline__ void move_block(uint8_t* block, __nv_bfloat16* y, long long N, int rows, int columns) {
-    constexpr int kEach = static_cast<int>(sizeof(T)) / 2, kLanes = 32 / kEach, kRows = 32 / kLanes;
-    const int lane = threadIdx.x & 31, c = (lane % kLanes) * kEach;
-    if (c >= columns) return;
-#pragma unroll 8
-    for (int i = 0; i < 32; i += kRows) {
-        const int row = i + lane / kLanes;
-        if (row >= rows) continue;
-        T* mem = reinterpret_cast<T*>(y + row * N + c);
-        T* own = reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(block_chunk(block, row, c >> 3)) + (c & 7) * 2);
-        if constexpr (OUT) *mem = *own;
-        else *own = *mem;
+    constexpr int kEach = static_cast<int>(sizeof(T)) / 2, kBatch = 16;  // accesses under way
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int part = 0; part < kBlockCols; part += 32 * kEach) {
+        const int c = part + lane * kEach;
+        if (c >= columns) return;
+#pragma unroll 1
+        for (int row0 = 0; row0 < rows; row0 += kBatch) {
+            T v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int row = row0 + i;
+                if constexpr (OUT) v[i] = *reinterpret_cast<const T*>(reinterpret_cast<uint8_t*>(block_chunk(block, row, c >> 3)) + (c & 7) * 2);
+                else if (row < rows) v[i] = *reinterpret_cast<const T*>(y + row * N + c);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int row = row0 + i;
+                if (row >= rows) break;
+                if constexpr (OUT) *reinterpret_cast<T*>(y + row * N + c) = v[i];
+                else *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(block_chunk(block, row, c >> 3)) + (c & 7) * 2) = v[i];
+            }
+        }
     }
 }
 
 template <bool OUT>
 __device__ __forceinline__ void move_rows(uint8_t* block, __nv_bfloat16* y, int N, int m, int n, int M) {
     __nv_bfloat16* at = y + static_cast<long long>(m) * N + n;
-    const int rows = min(32, M - m), columns = min(32, N - n);
+    const int rows = min(32, M - m), columns = min(kBlockCols, N - n);
     if (N % 2 == 0) move_block<uint32_t, OUT>(block, at, N, rows, columns);
     else move_block<uint16_t, OUT>(block, at, N, rows, columns);
 }
 
-struct EpilogueMaps {
-    const CUtensorMap* y;
-    const CUtensorMap* z;
-    const CUtensorMap* part;
+// A lane's share of the bias of a block: columns lane and 32 + lane.
+struct LaneBias {
+    float* row;  // the warp's 32 values in shared memory; nullptr: no bias
+    float v[2];
+    __device__ __forceinline__ void load(const float* bias, int n, int N) {
+        if (row == nullptr) return;
+        const int c = n + static_cast<int>(threadIdx.x & 31);
+        v[0] = c < N ? __ldg(bias + c) : 0.0f;
+        v[1] = c + 32 < N ? __ldg(bias + c + 32) : 0.0f;
+    }
 };
 
-__device__ __forceinline__ void run_act(int act, uint32_t (&v)[32], const uint4 (&r)[4], bool with_r) {
-    if (act == CONV_ACT_RELU) finish<CONV_ACT_RELU>(v, r, with_r);
-    else if (act == CONV_ACT_SILU) finish<CONV_ACT_SILU>(v, r, with_r);
-    else finish<CONV_ACT_NONE>(v, r, with_r);
-}
-
-// One block, sums in v, the residual in `block` where there is one.
-template <bool TMA>
-__device__ __forceinline__ void finish_block(const GemmParams& p, const EpilogueMaps& maps, uint32_t (&v)[32], uint8_t* block, int m, int n) {
+// One pass over a block's sums: y (with the residual that lies in `block`), or z, takes its place there and goes out.
+// The bias reaches the lanes through shared memory: read from global memory by every lane, 16 bytes at a time, it
+// was what the epilogue waited for (200704 x 256 -> 512 with ReLU 73 us, 55 without a bias).
+template <int ACT, bool TMA>
+__device__ __forceinline__ void block_pass(const GemmParams& p, const CUtensorMap* map, __nv_bfloat16* to, bool with_r, uint32_t at,
+                                           uint8_t* block, const LaneBias& bias, int m, int n) {
     const int lane = threadIdx.x & 31;
-    add_bias(v, p.bias, n, p.N);
-    uint4 r[4] = {};
-    if (p.r != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = *block_chunk(block, lane, j);
-    }
-    const auto out = [&](const CUtensorMap* map, __nv_bfloat16* y) {
-        stage(block, lane, v);
-        if constexpr (TMA) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_2d(map, block, n, m);
-                bulk_commit();
-            }
-        } else {
-            __syncwarp();
-            move_rows<true>(block, y, p.N, m, n, p.M);
+    for (int half = 0; half < 2; ++half) {
+        uint32_t v[32];
+        tmem_ld32(at + 32 * half, v);
+        if (bias.row != nullptr) {
+            __syncwarp();  // every lane has read what was there
+            bias.row[lane] = bias.v[half];
             __syncwarp();
         }
-    };
-    if (p.z != nullptr) {
-        if (!TMA) __syncwarp();  // every lane has its row of the residual
-        out(maps.z, p.z);
-        if (TMA && lane == 0) bulk_wait_read_all();
+        tmem_ld_wait(v);
+        const float4* row = reinterpret_cast<const float4*>(bias.row);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4* chunk = block_chunk(block, lane, 4 * half + j);
+            *chunk = finish_chunk<ACT>(v + 8 * j, row != nullptr ? row + 2 * j : nullptr, with_r ? chunk : nullptr);
+        }
+    }
+    if constexpr (TMA) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, block, n, m);
+            bulk_commit();
+        }
+    } else {
+        __syncwarp();
+        move_rows<true>(block, to, p.N, m, n, p.M);
         __syncwarp();
     }
-    run_act(p.act, v, r, p.r != nullptr);
-    out(maps.y, p.y);
 }
 
-// The sums of a block as they are to the workspace: 128-byte rows in the 128-byte swizzle.
-__device__ __forceinline__ void leave_block(const CUtensorMap* map, const uint32_t (&v)[32], uint8_t* buffer, int m, int n, int split) {
+template <bool TMA>
+__device__ __forceinline__ void finish_block(const GemmParams& p, const CUtensorMap* map_y, const CUtensorMap* map_z, uint32_t at,
+                                             uint8_t* block, const LaneBias& bias, int m, int n) {
+    const bool with_r = p.r != nullptr;
+    if (p.act == CONV_ACT_RELU) block_pass<CONV_ACT_RELU, TMA>(p, map_y, p.y, with_r, at, block, bias, m, n);
+    else if (p.act == CONV_ACT_SILU) block_pass<CONV_ACT_SILU, TMA>(p, map_y, p.y, with_r, at, block, bias, m, n);
+    else block_pass<CONV_ACT_NONE, TMA>(p, map_y, p.y, with_r, at, block, bias, m, n);
+    if (p.z != nullptr) {  // a second pass: tensor memory still has the sums
+        if (TMA && (threadIdx.x & 31) == 0) bulk_wait_read_all();
+        __syncwarp();
+        block_pass<CONV_ACT_NONE, TMA>(p, map_z, p.z, false, at, block, bias, m, n);
+    }
+}
+
+// The sums of a block as they are to the workspace, half a block at a time: 128-byte rows in the 128-byte swizzle.
+__device__ __forceinline__ void leave_block(const CUtensorMap* map, uint32_t at, uint8_t* buffer, int m, int n, int N, int split) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(buffer + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        tma_store_3d(map, buffer, n, m, split);
-        bulk_commit();
+    for (int half = 0; half < 2; ++half) {
+        if (n + 32 * half >= N) break;
+        uint32_t v[32];
+        tmem_ld32(at + 32 * half, v);
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *block_chunk(buffer, lane, j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, buffer, n + 32 * half, m, split);
+            bulk_commit();
+        }
     }
 }
 
 template <bool PAIR, int BN, bool A_BY_K, bool B_BY_K>
 __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
-    linear_gemm_kernel(const GemmParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+    linear_gemm_kernel(const GemmParams p, const Ring ring, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
                        const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_part) {
     using S = Shape<PAIR, BN>;
@@ -279,14 +324,15 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
         return;
     }
     Bars b;
-    uint8_t* outputs = smem + S::kStages * S::kStage;
-    b.full = reinterpret_cast<uint64_t*>(outputs + S::kEpilogueWarps * S::kOut);
-    b.empty = b.full + S::kStages;
-    b.tfull = b.empty + S::kStages;
+    uint8_t* outputs = smem + ring.stages * S::kStage;
+    b.full = reinterpret_cast<uint64_t*>(outputs + ring.warps * kBlockBytes);
+    b.empty = b.full + S::kMaxStages;
+    b.tfull = b.empty + S::kMaxStages;
     b.tempty = b.tfull + 2;
     b.drain = b.tempty + 2;
     b.res = b.drain + 1;
-    b.tmem_slot = reinterpret_cast<uint32_t*>(b.res + 2 * S::kEpilogueWarps);
+    b.bias = reinterpret_cast<float*>(outputs + ring.warps * kBlockBytes + 512);
+    b.tmem_slot = reinterpret_cast<uint32_t*>(b.res + S::kEpilogueWarps);
     b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
     volatile int* abort = b.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,16 +350,16 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
     const int unit0 = static_cast<int>(blockIdx.x) / kCtas;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < ring.stages; ++s) {
             mbar_init(&b.full[s], 1);
             mbar_init(&b.empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.tfull[i], 1);
-            mbar_init(&b.tempty[i], kCtas * S::kEpilogueWarps);
+            mbar_init(&b.tempty[i], kCtas * ring.warps / ring.groups);
         }
         mbar_init(b.drain, 1);
-        for (int i = 0; i < 2 * S::kEpilogueWarps; ++i) mbar_init(&b.res[i], 1);
+        for (int i = 0; i < S::kEpilogueWarps; ++i) mbar_init(&b.res[i], 1);
         *b.abort = 0;
         fence_barrier_init();
     }
@@ -333,70 +379,62 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
     const uint32_t tmem = *b.tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // operands from the kernel before this one
 
-    if (warp < S::kEpilogueWarps) {
+    if (warp < ring.warps) {
         // ------------------------------------------------------------ epilogue
-        const int quarter = warp & 3, part = warp >> 2;
-        uint8_t* buffer = outputs + warp * S::kOut;
-        uint64_t* res = b.res + 2 * warp;
-        const bool tma = p.N % 8 == 0;
-        const EpilogueMaps maps = {&map_y, &map_z, &map_part};
-        uint32_t res_phase[2] = {0, 0};
-        int local = 0;
+        const int per_group = ring.warps / ring.groups, group = warp / per_group;
+        const int quarter = warp & 3, cols = BN * 4 / per_group, part = (warp - group * per_group) >> 2;
+        uint8_t* block = outputs + warp * kBlockBytes;
+        uint64_t* res = b.res + warp;
+        float* bias_row = b.bias + 32 * warp;
+        const bool tma = p.N % 8 == 0, by_tma = p.r != nullptr && tma && p.splits == 1;
+        uint32_t res_phase = 0;
+        int local = group;
         bool ok = true;
-        for (int u = unit0; u < tiles.units; u += tiles.step, ++local) {
+        for (int u = unit0 + group * tiles.step; u < tiles.units && ok; u += ring.groups * tiles.step, local += ring.groups) {
             const Unit w = unit_at(tiles, u);
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
-            const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128 + quarter * 32, n = w.nt * BN + part * S::kCols;
-            const int blocks = m >= p.M ? 0 : min(S::kBlocks, (p.N - n + 31) / 32);  // 0 or less: none
-            const bool by_tma = p.r != nullptr && tma && p.splits == 1;
-            if (by_tma && lane == 0) {
-                bulk_wait_read_all();  // what went through the buffers before has left them
-                for (int i = 0; i < blocks; ++i) {
-                    mbar_arrive_expect_tx(&res[i], 2048);
-                    tma_load_2d(buffer + i * 2048, &map_r, &res[i], n + 32 * i, m);
+            const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128 + quarter * 32, n = w.nt * BN + part * cols;
+            const int blocks = m >= p.M ? 0 : min(cols / kBlockCols, (p.N - n + kBlockCols - 1) / kBlockCols);  // 0 or less: none
+            const auto fetch = [&](int i) {  // block i of the residual, once what was in the buffer has left
+                if (lane == 0) {
+                    bulk_wait_read_all();
+                    mbar_arrive_expect_tx(res, kBlockBytes);
+                    tma_load_2d(block, &map_r, res, n + kBlockCols * i, m);
                 }
-            }
-            __syncwarp();
+                __syncwarp();
+            };
+            LaneBias bias;
+            bias.row = p.bias != nullptr ? bias_row : nullptr;
+            bias.load(p.bias, n, p.N);
+            if (by_tma && blocks > 0) fetch(0);
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 ok = false;
             }
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < S::kBlocks; ++i) {
-                if (i >= blocks) break;
-                uint8_t* block = buffer + i * 2048;
-                uint32_t v[32];
-                if (ok) {
-                    tmem_ld32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + part * S::kCols + 32 * i, v);
-                    tmem_ld_wait(v);
-                }
-                if (by_tma) {  // also after a wait that gave up: no copy may be in flight when the CTA leaves
-                    if (!warp_wait(&res[i], res_phase[i], nullptr)) {
+#pragma unroll 1
+            for (int i = 0; i < blocks && (ok || i == 0); ++i) {
+                if (by_tma) {  // the first also after a wait that gave up: no copy may be in flight when the CTA leaves
+                    if (i > 0) fetch(i);
+                    if (!warp_wait(res, res_phase, nullptr)) {
                         record_status(p.status, kStatusTimeoutEpilogue, abort);
                         ok = false;
                     }
-                    res_phase[i] ^= 1u;
-                }
-                if (!ok) continue;
-                if (p.splits > 1) {
+                    res_phase ^= 1u;
+                } else if (p.splits == 1 && tma) {
                     if (lane == 0) bulk_wait_read_all();
                     __syncwarp();
-                    leave_block(&map_part, v, buffer, m, n + 32 * i, w.split);
-                } else if (tma) {
-                    if (!by_tma) {
-                        if (lane == 0) bulk_wait_read_all();
-                        __syncwarp();
-                    }
-                    finish_block<true>(p, maps, v, block, m, n + 32 * i);
-                } else {
-                    if (p.r != nullptr) {
-                        move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + 32 * i, p.M);
-                        __syncwarp();
-                    }
-                    finish_block<false>(p, maps, v, block, m, n + 32 * i);
+                } else if (p.splits == 1 && p.r != nullptr && ok) {
+                    move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + kBlockCols * i, p.M);
+                    __syncwarp();
                 }
+                if (!ok) continue;
+                if (i > 0) bias.load(p.bias, n + kBlockCols * i, p.N);
+                const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + part * cols + kBlockCols * i;
+                if (p.splits > 1) leave_block(&map_part, at, block, m, n + kBlockCols * i, p.N, w.split);
+                else if (tma) finish_block<true>(p, &map_y, &map_z, at, block, bias, m, n + kBlockCols * i);
+                else finish_block<false>(p, &map_y, &map_z, at, block, bias, m, n + kBlockCols * i);
             }
             if (!ok) break;
             tc_fence_before();
@@ -409,35 +447,38 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
         if (lane == 0) bulk_wait_all();  // none in flight when the CTA leaves
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ operands
-        if (lane == 0) {
-            long long issued = 0;
-            int st = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int u = unit0; u < tiles.units && ok; u += tiles.step) {
-                const Unit w = unit_at(tiles, u);
-                const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128, n = w.nt * BN + static_cast<int>(rank) * S::kRowsB;
-                for (int ks = 0; ks < w.k_count; ++ks) {
-                    if (!mbar_wait(&b.empty[st], ph ^ 1u, abort)) {
-                        record_status(p.status, kStatusTimeoutProducer, abort);
-                        ok = false;
-                        break;
-                    }
+        long long issued = 0;
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = unit0; u < tiles.units && ok; u += tiles.step) {
+            const Unit w = unit_at(tiles, u);
+            const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128, n = w.nt * BN + static_cast<int>(rank) * S::kRowsB;
+            for (int ks = 0; ks < w.k_count; ++ks) {
+                if (!warp_wait(&b.empty[st], ph ^ 1u, abort)) {
+                    record_status(p.status, kStatusTimeoutProducer, abort);
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(&b.full[st], kCtas * S::kStage);
                     uint8_t* dst = smem + st * S::kStage;
                     const uint32_t bar = PAIR ? mapa_shared(smem_addr(&b.full[st]), 0) : 0u;
                     const int k = (w.k_first + ks) * kStepK;  // past the matrix: zeros
                     load_operand<PAIR, A_BY_K, 128>(dst, &map_a, &b.full[st], bar, m, k);
                     load_operand<PAIR, B_BY_K, S::kRowsB>(dst + kTileA, &map_b, &b.full[st], bar, n, k);
-                    ++issued;
-                    if (++st == S::kStages) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == ring.stages) {
+                    st = 0;
+                    ph ^= 1u;
                 }
             }
-            for (int s = 0; s < S::kStages; ++s) {  // no copy in flight when the CTA leaves
-                const long long fills = issued / S::kStages + (s < issued % S::kStages ? 1 : 0);
+        }
+        if (lane == 0) {
+            for (int s = 0; s < ring.stages; ++s) {  // no copy in flight when the CTA leaves
+                const long long fills = issued / ring.stages + (s < issued % ring.stages ? 1 : 0);
                 if (fills == 0) continue;
                 const uint32_t par = static_cast<uint32_t>((fills - 1) & 1);
                 // the peer of a pair sees the MMAs release each slot, which needs its copies landed
@@ -445,9 +486,10 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
                     record_status(p.status, kStatusTimeoutDrain, abort);
             }
         }
-    } else if (lane == 0 && leader) {
+    } else if (warp == kMmaWarp && leader) {
         // ------------------------------------------------------------ MMA
         constexpr uint32_t idesc = idesc_bf16_f32(128 * kCtas, BN) | (A_BY_K ? 1u << 15 : 0u) | (B_BY_K ? 1u << 16 : 0u);
+        const uint32_t base0 = smem_addr(smem);
         int st = 0, local = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -455,43 +497,46 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
             const Unit w = unit_at(tiles, u);
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
-            if (!mbar_wait_cluster(&b.tempty[buf], use ^ 1u, abort)) {
+            if (!warp_wait_cluster(&b.tempty[buf], use ^ 1u, abort)) {
                 record_status(p.status, kStatusTimeoutMma, abort);
                 break;
             }
             tc_fence_after();
-            const uint32_t d = tmem + buf * BN;
             for (int ks = 0; ks < w.k_count; ++ks) {
-                if (!mbar_wait_cluster(&b.full[st], ph, abort)) {
+                if (!warp_wait_cluster(&b.full[st], ph, abort)) {
                     record_status(p.status, kStatusTimeoutMma, abort);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t base = smem_addr(smem + st * S::kStage);
-                const int mmas = min(4, (p.K - (w.k_first + ks) * kStepK + 15) >> 4);
+                const uint32_t base = base0 + st * S::kStage;
+                if (elect_one()) {
+                    const int mmas = min(4, (p.K - (w.k_first + ks) * kStepK + 15) >> 4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j >= mmas) break;
-                    const uint64_t da = operand_desc<A_BY_K>(base, j), db = operand_desc<B_BY_K>(base + kTileA, j);
-                    const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
-                    if constexpr (PAIR) mma_bf16_pair(d, da, db, idesc, acc);
-                    else mma_bf16(d, da, db, idesc, acc);
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= mmas) break;
+                        const uint64_t da = operand_desc<A_BY_K>(base, j), db = operand_desc<B_BY_K>(base + kTileA, j);
+                        const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
+                        if constexpr (PAIR) mma_bf16_pair(tmem + buf * BN, da, db, idesc, acc);
+                        else mma_bf16(tmem + buf * BN, da, db, idesc, acc);
+                    }
+                    commit<PAIR>(&b.empty[st]);
                 }
-                if constexpr (PAIR) mma_commit_pair(&b.empty[st], 3);
-                else mma_commit(&b.empty[st]);
-                if (++st == S::kStages) {
+                __syncwarp();
+                if (++st == ring.stages) {
                     st = 0;
                     ph ^= 1u;
                 }
             }
             if (!ok) break;
-            if constexpr (PAIR) mma_commit_pair(&b.tfull[buf], 3);
-            else mma_commit(&b.tfull[buf]);
+            if (elect_one()) commit<PAIR>(&b.tfull[buf]);
+            __syncwarp();
         }
-        if constexpr (PAIR) mma_commit_pair(b.drain, 1);
-        else mma_commit(b.drain);
-        if (!mbar_wait_cluster(b.drain, 0, nullptr)) record_status(p.status, kStatusTimeoutDrain, abort);
+        if (elect_one()) {
+            if constexpr (PAIR) mma_commit_pair(b.drain, 1);
+            else mma_commit(b.drain);
+            if (!mbar_wait_cluster(b.drain, 0, nullptr)) record_status(p.status, kStatusTimeoutDrain, abort);
+        }
     }
     __syncwarp();
     __syncthreads();
@@ -574,14 +619,20 @@ cudaError_t launch_variant(const GemmParams& p, int num_sms, bool after_other, c
     using S = Shape<PAIR, BN>;
     static SmemLimitCache limits;
     auto* fn = linear_gemm_kernel<PAIR, BN, A_BY_K, B_BY_K>;
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), S::kSmem, limits);
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 232448, limits);  // all that a block may have, once
     if (e != cudaSuccess) return e;
     const long long units = (static_cast<long long>(p.M) + 128 * S::kCtas - 1) / (128 * S::kCtas) * ((p.N + BN - 1) / BN) * p.splits;
     const int slots = num_sms / S::kCtas;
+    // Sixteen epilogue warps where units are short; their buffers cost a stage, which long ones miss (8192 x 4096 x 4096
+    // 147 us with five stages, 142 with six).  Two groups where CTAs have several units; of 64 columns a group has all.
+    Ring ring;
+    ring.warps = p.K >= 1024 ? 8 : S::kEpilogueWarps;
+    ring.groups = BN == 64 || (units > slots && ring.warps == S::kEpilogueWarps) ? 2 : 1;
+    ring.stages = S::stages(ring.warps);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((units < slots ? units : slots) * S::kCtas));
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = ring.stages * S::kStage + ring.warps * kBlockBytes + S::kBarBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     if (PAIR) {
@@ -607,12 +658,12 @@ cudaError_t launch_variant(const GemmParams& p, int num_sms, bool after_other, c
         made = made && encode_tiled(&part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.part, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
     } else if (p.N % 8 == 0) {
         const auto rows = [&](CUtensorMap* map, const void* base) {
-            return base == nullptr || encode_matrix(map, base, p.M, p.N, p.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+            return base == nullptr || encode_matrix(map, base, p.M, p.N, p.N, 32, kBlockCols, CU_TENSOR_MAP_SWIZZLE_128B);
         };
         made = made && rows(&y, p.y) && rows(&z, p.z) && rows(&r, p.r);
     }
     if (!made) return cudaErrorInvalidValue;
-    if ((e = cudaLaunchKernelEx(&cfg, fn, p, a, b, y, z, r, part)) != cudaSuccess || p.splits == 1) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, fn, p, ring, a, b, y, z, r, part)) != cudaSuccess || p.splits == 1) return e;
     cudaLaunchConfig_t join = {};
     const long long quads = static_cast<long long>(p.M) * ((p.N + 3) / 4);
     join.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
@@ -641,14 +692,17 @@ size_t gemm_part_bytes(const GemmTile& t, int M, int N) {
     return t.splits > 1 ? static_cast<size_t>(t.splits) * M * part_pitch(N) * sizeof(float) : 0;
 }
 
-// The tile shape and split of K that cost least by these figures, in microseconds: a K = 64 step, what a tile takes
-// besides, the launch; a split adds its parts' way through memory and the join.
+// The tile shape and split of K that cost least by these figures, in microseconds on a 152-SM part (repeated launches in a
+// graph): the launch with a short tile, a K = 64 step, what a tile takes besides, and the least it takes (its epilogue).
+// From one tile on every SM, K = 64 / 256 / 1024: 7.2 / 8.4 / 12.1 us of 256 x 256 on pairs, 5.4 / 6.3 / 9.2 of 128 x 128,
+// 5.0 / 5.7 / 8.5 of 128 x 64.  A split adds its parts' way through memory and the join: 2432 x 4096 -> 128 19.6 us in tiles of 128 x 128, 11.8
+// with the K of each shared by eight.
 GemmTile gemm_pick_tile(int M, int N, int K, int num_sms) {
     struct Cost {
         int rows, columns;
-        double step, besides;
+        double launch, step, besides, least;
     };
-    constexpr Cost kCosts[3] = {{256, 256, 0.29, 2.0}, {128, 128, 0.17, 1.3}, {128, 64, 0.13, 1.0}};
+    constexpr Cost kCosts[3] = {{256, 256, 5.9, 0.29, 1.0, 2.6}, {128, 128, 4.5, 0.235, 0.7, 1.3}, {128, 64, 4.2, 0.22, 0.6, 0.8}};
     const long long steps = (K + kStepK - 1) / kStepK;
     double best = 0.0;
     GemmTile pick = {};
@@ -659,8 +713,8 @@ GemmTile gemm_pick_tile(int M, int N, int K, int num_sms) {
             if (splits > 1 && tiles * splits > slots) break;
             const long long rounds = (tiles * splits + slots - 1) / slots;
             const double each = static_cast<double>((steps + splits - 1) / splits) * c.step + c.besides;
-            const double join = splits > 1 ? 2.0 + static_cast<double>(M) * N * splits * 8.0 / 4e6 : 0.0;
-            const double cost = static_cast<double>(rounds) * each + join;
+            const double join = splits > 1 ? 3.0 + static_cast<double>(M) * N * splits * 8.0 / 4e6 : 0.0;
+            const double cost = c.launch + static_cast<double>(rounds) * (each > c.least ? each : c.least) + join;
             if (pick.rows == 0 || cost < best) {
                 best = cost;
                 pick = {c.rows, c.columns, splits};

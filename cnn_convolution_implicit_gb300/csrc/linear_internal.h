@@ -40,6 +40,20 @@ bool gemm_fits(int M, int N);  // tile counts within 32 bits
 // operand and lets this one start early.
 cudaError_t launch_gemm(const GemmParams& p, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream);
 
+// The forward product with few rows: dense operands, rows anywhere.
+struct FewParams {
+    int M, N, K;
+    const __nv_bfloat16* x;
+    const __nv_bfloat16* w;
+    const float* bias;
+    const __nv_bfloat16* r;
+    __nv_bfloat16* y;
+    __nv_bfloat16* z;
+    int act;
+};
+bool linear_use_few(int M, int N, int K);
+cudaError_t launch_linear_few(const FewParams& p, cudaStream_t stream);
+
 // u = dy * act'(z) in BF16, and its sums over the rows
 struct LinearGradParams {
     int M, N;
