@@ -31,7 +31,7 @@ Strip strip_of(int N) {
 template <int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradParams p, int lanes, float* sums_out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that may follow
-    constexpr int H = (VEC + 1) / 2, kBatch = 4;
+    constexpr int H = (VEC + 1) / 2, kBatch = 2;
     using Io = VecIo<__nv_bfloat16, VEC>;
     using Raw = typename Io::Raw;
     __shared__ float sums[kThreads * VEC];
@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradP
 
 // 32 columns a CTA.
 __global__ void __launch_bounds__(1024) join_columns_kernel(const float* part, int parts, int C, float* out) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float total = 0.0f;
@@ -98,16 +99,24 @@ __global__ void __launch_bounds__(1024) join_columns_kernel(const float* part, i
 
 }  // namespace
 
-cudaError_t launch_join_columns(const float* part, int parts, int C, float* out, cudaStream_t stream) {
-    join_columns_kernel<<<(C + 31) / 32, 1024, 0, stream>>>(part, parts, C, out);
-    return cudaGetLastError();
+cudaError_t launch_join_columns(const float* part, int parts, int C, float* out, bool early, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((C + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, join_columns_kernel, part, parts, C, out);
 }
 
-// About four CTAs an SM, four rows a thread at least.
+// About four CTAs an SM, two rows a thread at least.
 int linear_grad_parts(int M, int N, int num_sms) {
     const Strip s = strip_of(N);
     const int slots = kThreads / s.lanes;
-    const long long need = (static_cast<long long>(M) + 4 * slots - 1) / (4 * slots), most = (4LL * num_sms + s.strips - 1) / s.strips;
+    const long long need = (static_cast<long long>(M) + 2 * slots - 1) / (2 * slots), most = (4LL * num_sms + s.strips - 1) / s.strips;
     return static_cast<int>(need < most ? need : most);
 }
 
@@ -122,7 +131,7 @@ cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, cudaStrea
     else run(linear_grad_kernel<8, CONV_ACT_NONE>, linear_grad_kernel<1, CONV_ACT_NONE>);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.dbias == nullptr || parts == 1) return e;
-    return launch_join_columns(p.part, parts, p.N, p.dbias, stream);
+    return launch_join_columns(p.part, parts, p.N, p.dbias, true, stream);
 }
 
 }  // namespace convgb

@@ -11,12 +11,13 @@
 // of a call have the same shape, so a row begins at the same place of a granule in each of them; the
 // first and last granule, shared with the neighbouring rows, are read and written by elements.
 //
-// dgamma: the register form keeps each thread's columns over all the rows that its CTA takes, where
-// a thread has the same columns in every row (rows on 16 bytes); other rows take a kernel of its own that reads
-// dy and h by column.  Either way parts of it meet in the workspace and are added in one order.
+// dgamma: the backward pass of rows on 16 bytes keeps each thread's columns over all the rows that its CTA
+// takes; for other rows, whose threads' columns move from row to row, a kernel of its own reads dy and h by
+// column.  Either way parts of it meet in the workspace and are added in one order.
 #include <type_traits>
 
 #include "pointwise_math.cuh"
+#include "ptx.cuh"
 #include "rows_internal.h"
 
 namespace convgb {
@@ -139,6 +140,7 @@ __device__ __forceinline__ float reciprocal_root(float sum, int C, float eps) {
     return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(C)), eps));
 }
 
+constexpr int kStreamMaxStages = 8;
 constexpr int kRowsOfWarps = 4;  // rows of one warp each that a CTA takes
 template <int WARPS>
 constexpr int kThreadsOf = 32 * (WARPS == 1 ? kRowsOfWarps : WARPS);
@@ -277,68 +279,198 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(const Rm
 }
 
 // ---------------------------------------------------------------- backward
-// Rows in registers, `gridDim.x` CTAs over them.  DGAMMA: this thread's columns of dgamma, over its rows.
-template <typename T, bool ALIGNED, int ITEMS, int WARPS, bool DGAMMA>
+// Rows in registers: those that the ring below does not take.
+template <typename T, bool ALIGNED, int ITEMS, int WARPS>
 __global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const RmsParams p) {
-    static_assert(ALIGNED || !DGAMMA, "a thread's columns move from row to row");
     using R = Row<T, ALIGNED>;
-    constexpr int kRows = WARPS == 1 ? kRowsOfWarps : 1;
-    __shared__ float sums[2][WARPS];
+    __shared__ float sums[WARPS];
+    const long long m = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kRowsOfWarps + (threadIdx.x >> 5) : blockIdx.x;
+    if (m >= p.M) return;  // whole warps of their own rows
     const int t = row_thread<WARPS>();
-    const int slot = WARPS == 1 ? threadIdx.x >> 5 : 0;
-    f2 total[DGAMMA ? ITEMS : 1][R::H] = {};
-    int turn = 0;
-    for (long long m = static_cast<long long>(blockIdx.x) * kRows + slot; m < p.M;
-         m += static_cast<long long>(gridDim.x) * kRows, turn ^= 1) {
-        const R row(m, p.C);
-        const f2 factor = f2_dup(p.rstd[m]);
+    const R row(m, p.C);
+    const f2 factor = f2_dup(p.rstd[m]);
+    f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = t + k * 32 * WARPS;
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) d[k][j] = n[k][j] = 0;
+        if (i >= row.count) continue;
+        row.load(p.x, i, d[k]);
+        row.load(p.h_in, i, n[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = t + k * 32 * WARPS;
+        if (i >= row.count) continue;
+        f2 g[R::H];
+        row.weights(p.gamma, i, g);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) {
+            n[k][j] = f2_mul(n[k][j], factor);
+            d[k][j] = f2_mul(d[k][j], g[j]);
+            dot = f2_fma(d[k][j], n[k][j], dot);
+        }
+    }
+    const f2 minus = f2_dup(-__fdiv_rn(row_sum<WARPS>(f2_lo(dot) + f2_hi(dot), sums), static_cast<float>(p.C)));
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = t + k * 32 * WARPS;
+        if (i >= row.count) continue;
+        f2 r[R::H] = {};
+        if (p.r != nullptr) row.load(p.r, i, r);
+#pragma unroll
+        for (int j = 0; j < R::H; ++j) d[k][j] = f2_fma(f2_fma(n[k][j], minus, d[k][j]), factor, r[j]);
+        row.store(p.y, i, d[k]);
+    }
+}
+
+// Rows on 16 bytes of at most 1,024 granules: a warp of its own brings them (dy, h and dh, whole rows, next to each other in
+// memory) by bulk copies into a ring in shared memory, eight rows of one warp each or one row of eight warps to a
+// stage.  Loads into registers left too few bytes under way between a row's barrier and the next row's first
+// load: 8192 x 4096 BF16 with dh 83 us so, 3.2 TB/s.
+constexpr int kStreamWarps = 8, kStreamThreads = 32 * (kStreamWarps + 1);
+
+struct Stream {
+    int stages, stage_bytes;
+};
+
+__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <typename T, int ITEMS, int WARPS, bool DGAMMA>
+__global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backward_stream_kernel(const RmsParams p, const Stream s) {
+    using R = Row<T, true>;
+    constexpr int kRows = WARPS == 1 ? kStreamWarps : 1, kStride = 32 * WARPS;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ uint64_t full[kStreamMaxStages], empty[kStreamMaxStages];
+    __shared__ float sums[2][kStreamWarps];
+    __shared__ int abort_flag;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join of dgamma's parts
+    volatile int* abort = &abort_flag;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kStreamWarps);
+        }
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const int row_bytes = p.C * static_cast<int>(sizeof(T));
+    const int groups = static_cast<int>((static_cast<long long>(p.M) + kRows - 1) / kRows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kStreamWarps) {
+        if (lane != 0) return;
+        const uint8_t* from[3] = {static_cast<const uint8_t*>(p.x), static_cast<const uint8_t*>(p.h_in), static_cast<const uint8_t*>(p.r)};
+        long long issued = 0;
+        int st = 0;
+        uint32_t ph = 0;
+        for (int g = blockIdx.x; g < groups; g += gridDim.x) {
+            if (!mbar_wait(&empty[st], ph ^ 1u, abort)) {
+                record_status(p.status, kStatusTimeoutProducer, abort);
+                break;
+            }
+            const long long m = static_cast<long long>(g) * kRows;
+            const int bytes = static_cast<int>(p.M - m < kRows ? p.M - m : kRows) * row_bytes, tensors = p.r != nullptr ? 3 : 2;
+            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(tensors * bytes));
+            for (int i = 0; i < tensors; ++i)
+                bulk_load(ring + st * s.stage_bytes + i * kRows * row_bytes, from[i] + m * row_bytes, bytes, &full[st]);
+            ++issued;
+            if (++st == s.stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        for (int i = 0; i < s.stages; ++i) {  // no copy in flight when the CTA leaves
+            const long long fills = issued / s.stages + (i < issued % s.stages ? 1 : 0);
+            if (fills && !mbar_wait(&full[i], static_cast<uint32_t>((fills - 1) & 1), nullptr)) record_status(p.status, kStatusTimeoutDrain, abort);
+        }
+        return;
+    }
+    const int t = row_thread<WARPS>(), slot = WARPS == 1 ? warp : 0, vecs = p.C / R::V;
+    f2 gamma[ITEMS][R::H], total[DGAMMA ? ITEMS : 1][R::H] = {};
+    const R first(0, p.C);
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int i = t + k * kStride;
+        if (i < vecs) first.weights(p.gamma, i, gamma[k]);
+    }
+    int st = 0, turn = 0;
+    uint32_t ph = 0;
+    for (int g = blockIdx.x; g < groups; g += gridDim.x, turn ^= 1) {
+        const long long m = static_cast<long long>(g) * kRows + slot;
+        const bool live = m < p.M;
+        const float rstd = live ? __ldg(p.rstd + m) : 0.0f;
+        if (!mbar_wait(&full[st], ph, abort)) record_status(p.status, kStatusTimeoutTransform, abort);  // and on: every wait ends
+        const uint4* dy = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + slot * row_bytes);
+        const uint4* h = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (kRows + slot) * row_bytes);
+        const uint4* dh = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (2 * kRows + slot) * row_bytes);
+        const f2 factor = f2_dup(rstd);
         f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * 32 * WARPS;
-#pragma unroll
-            for (int j = 0; j < R::H; ++j) d[k][j] = n[k][j] = 0;
-            if (i >= row.count) continue;
-            row.load(p.x, i, d[k]);
-            row.load(p.h_in, i, n[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * 32 * WARPS;
-            if (i >= row.count) continue;
-            f2 g[R::H];
-            row.weights(p.gamma, i, g);
+            const int i = t + k * kStride;
+            if (i >= vecs || !live) continue;
+            VecIo<T, R::V>::unpack(dy[i], d[k]);
+            VecIo<T, R::V>::unpack(h[i], n[k]);
 #pragma unroll
             for (int j = 0; j < R::H; ++j) {
                 n[k][j] = f2_mul(n[k][j], factor);
                 if constexpr (DGAMMA) total[k][j] = f2_fma(d[k][j], n[k][j], total[k][j]);
-                d[k][j] = f2_mul(d[k][j], g[j]);
+                d[k][j] = f2_mul(d[k][j], gamma[k][j]);
                 dot = f2_fma(d[k][j], n[k][j], dot);
             }
         }
-        const float mean = __fdiv_rn(row_sum<WARPS>(f2_lo(dot) + f2_hi(dot), sums[turn]), static_cast<float>(p.C));
-        const f2 minus = f2_dup(-mean);
+        float sum = warp_sum(f2_lo(dot) + f2_hi(dot));
+        if constexpr (WARPS > 1) {
+            if (lane == 0) sums[turn][warp] = sum;
+            sync_consumers();
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) sum += sums[turn][i];
+        }
+        const f2 minus = f2_dup(-__fdiv_rn(sum, static_cast<float>(p.C)));
+        const R row(live ? m : 0, p.C);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * 32 * WARPS;
-            if (i >= row.count) continue;
+            const int i = t + k * kStride;
+            if (i >= vecs || !live) continue;
             f2 r[R::H] = {};
-            if (p.r != nullptr) row.load(p.r, i, r);
+            if (p.r != nullptr) VecIo<T, R::V>::unpack(dh[i], r);
 #pragma unroll
             for (int j = 0; j < R::H; ++j) d[k][j] = f2_fma(f2_fma(n[k][j], minus, d[k][j]), factor, r[j]);
             row.store(p.y, i, d[k]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if (++st == s.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
     }
     if constexpr (DGAMMA) {
-        float* part = p.part + (static_cast<long long>(blockIdx.x) * kRows + slot) * p.C;
+        float* part = p.part + static_cast<long long>(blockIdx.x) * p.C;
+        if constexpr (WARPS == 1) {  // the warps' sums, in the ring: every stage has been read
+            sync_consumers();
+            part = reinterpret_cast<float*>(ring) + warp * p.C;
+        }
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int c = (t + k * 32 * WARPS) * R::V;
-            if (c >= p.C) continue;
+            const int i = t + k * kStride;
+            if (i >= vecs) continue;
 #pragma unroll
             for (int j = 0; j < R::H; j += 2)
-                *reinterpret_cast<float4*>(part + c + 2 * j) =
+                *reinterpret_cast<float4*>(part + i * R::V + 2 * j) =
                     make_float4(f2_lo(total[k][j]), f2_hi(total[k][j]), f2_lo(total[k][j + 1]), f2_hi(total[k][j + 1]));
+        }
+        if constexpr (WARPS == 1) {
+            sync_consumers();
+            for (int c = threadIdx.x; c < p.C; c += 32 * kStreamWarps) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kStreamWarps; ++i) sum += reinterpret_cast<const float*>(ring)[i * p.C + c];
+                p.part[static_cast<long long>(blockIdx.x) * p.C + c] = sum;
+            }
         }
     }
 }
@@ -453,43 +585,90 @@ cudaError_t forward(const RmsParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// The streaming backward form of a plan: granules a thread holds, warps to a row (0: another form), and CTAs that an
+// SM runs at a time.
+struct StreamForm {
+    int items, warps, ctas;
+};
+StreamForm stream_form(const RmsParams& p) {
+    const int granules = p.C / (p.bf16 ? 8 : 4);
+    if (!aligned_rows(p) || granules > 1024) return {0, 0, 0};
+    const int warps = granules <= 128 ? 1 : kStreamWarps, stride = 32 * warps;
+    const int items = granules <= stride ? 1 : (granules <= 2 * stride ? 2 : 4);
+    return {items, warps, items == 4 ? 1 : 2};
+}
+
+int stream_ctas(const RmsParams& p, const StreamForm& f, int num_sms) {
+    const int rows = f.warps == 1 ? kStreamWarps : 1;
+    const long long need = (static_cast<long long>(p.M) + rows - 1) / rows, most = static_cast<long long>(f.ctas) * num_sms;
+    return static_cast<int>(need < most ? need : most);
+}
+
+template <typename T, int ITEMS, int WARPS>
+cudaError_t stream_launch(const RmsParams& p, const StreamForm& f, cudaStream_t stream) {
+    Stream s;
+    s.stage_bytes = 3 * p.C * static_cast<int>(sizeof(T)) * (WARPS == 1 ? kStreamWarps : 1);
+    const int room = (f.ctas == 2 ? 113 : 226) * 1024 - 1024;  // of shared memory, barriers aside
+    s.stages = room / s.stage_bytes < kStreamMaxStages ? room / s.stage_bytes : kStreamMaxStages;
+    int bytes = s.stages * s.stage_bytes;
+    if (WARPS == 1 && bytes < kStreamWarps * p.C * 4) bytes = kStreamWarps * p.C * 4;  // the warps' sums
+    const auto run = [&](auto* kernel, SmemLimitCache& limits) {
+        const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 226 * 1024, limits);
+        if (e != cudaSuccess) return e;
+        kernel<<<p.ctas, kStreamThreads, bytes, stream>>>(p, s);
+        return cudaGetLastError();
+    };
+    static SmemLimitCache with, without;
+    return p.dgamma != nullptr ? run(rms_backward_stream_kernel<T, ITEMS, WARPS, true>, with)
+                               : run(rms_backward_stream_kernel<T, ITEMS, WARPS, false>, without);
+}
+
+template <typename T>
+cudaError_t stream_backward(const RmsParams& p, const StreamForm& f, cudaStream_t stream) {
+    if (f.warps == 1) {
+        if (f.items == 1) return stream_launch<T, 1, 1>(p, f, stream);
+        return f.items == 2 ? stream_launch<T, 2, 1>(p, f, stream) : stream_launch<T, 4, 1>(p, f, stream);
+    }
+    if (f.items == 1) return stream_launch<T, 1, kStreamWarps>(p, f, stream);
+    return f.items == 2 ? stream_launch<T, 2, kStreamWarps>(p, f, stream) : stream_launch<T, 4, kStreamWarps>(p, f, stream);
+}
+
 template <typename T, bool ALIGNED>
 cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
+    const StreamForm sf = stream_form(p);
     const Form f = pick_form(p);
-    const unsigned blocks = (p.C + 31) / 32;
-    const bool by_column = p.dgamma != nullptr && (!ALIGNED || f.warps == 0);
-    if (by_column) rms_columns_kernel<T><<<dim3(blocks, p.parts), 256, 0, stream>>>(p);  // first: dx may be dy
+    if (ALIGNED && sf.warps != 0) {
+        const cudaError_t e = stream_backward<T>(p, sf, stream);
+        if (e != cudaSuccess || p.dgamma == nullptr) return e;
+        return launch_join_columns(p.part, p.parts, p.C, p.dgamma, true, stream);
+    }
+    if (p.dgamma != nullptr)  // first: dx may be dy
+        rms_columns_kernel<T><<<dim3((p.C + 31) / 32, p.parts), 256, 0, stream>>>(p);
     if (f.warps == 0) {
         rms_backward_long_kernel<T, ALIGNED><<<p.M, kLongThreads, 0, stream>>>(p);
     } else {
         by_form(f, [&](auto items, auto warps) {
             constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
-            if constexpr (ALIGNED) {
-                if (p.dgamma != nullptr) {
-                    rms_backward_kernel<T, true, I, W, true><<<p.parts / rows, kThreadsOf<W>, 0, stream>>>(p);
-                    return;
-                }
-            }
-            rms_backward_kernel<T, ALIGNED, I, W, false><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+            if constexpr (!ALIGNED || W == 16) rms_backward_kernel<T, ALIGNED, I, W><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
         });
     }
-    if (p.dgamma != nullptr) return launch_join_columns(p.part, p.parts, p.C, p.dgamma, stream);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.dgamma == nullptr) return e;
+    return launch_join_columns(p.part, p.parts, p.C, p.dgamma, false, stream);
 }
 
 }  // namespace
 
-int rms_backward_parts(const RmsParams& p, int num_sms) {
-    const Form f = pick_form(p);
-    if (aligned_rows(p) && f.warps != 0) {  // CTAs over the rows, times the rows that each takes at a time
-        const int rows = f.warps == 1 ? kRowsOfWarps : 1;
-        const long long need = (static_cast<long long>(p.M) + rows - 1) / rows, most = static_cast<long long>(num_sms) * (f.warps <= 4 ? 4 : 16 / f.warps);
-        return static_cast<int>(need < most ? need : most) * rows;
+void rms_plan_backward(RmsParams& p, int num_sms) {
+    const StreamForm f = stream_form(p);
+    if (f.warps != 0) {
+        p.ctas = p.parts = stream_ctas(p, f, num_sms);
+        return;
     }
-    // by column: about four CTAs an SM
+    // dgamma by column: about four CTAs an SM
     const long long columns = (p.C + 31) / 32, need = (static_cast<long long>(p.M) + 4 * kColumnRows - 1) / (4 * kColumnRows);
     const long long most = (4LL * num_sms + columns - 1) / columns;
-    return static_cast<int>(need < most ? need : most);
+    p.parts = static_cast<int>(need < most ? need : most);
 }
 
 cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream) {

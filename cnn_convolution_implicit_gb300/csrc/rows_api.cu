@@ -1,5 +1,6 @@
 // rows_api.cu -- C ABI of the root-mean-square norm and of dropout (conv_rms_norm_*, conv_dropout in
 // include/conv.h): checks, launch configuration and the calls.
+#include <atomic>
 #include <cmath>
 #include <new>
 
@@ -28,6 +29,22 @@ conv_status check_device(const conv_rms_norm_plan* pl) {
         return CONV_ERR_CUDA;
     }
     return cur == pl->device ? CONV_OK : CONV_ERR_INVALID_ARG;
+}
+
+// Of the current device.
+conv_status sm_count(int& sms) {
+    static std::atomic<int> known[64];
+    int dev = -1;
+    if (cudaGetDevice(&dev) == cudaSuccess) {
+        sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+        if (sms != 0) return CONV_OK;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+            if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+            return CONV_OK;
+        }
+    }
+    cudaGetLastError();
+    return CONV_ERR_CUDA;
 }
 
 conv_status launched(cudaError_t e) {
@@ -67,11 +84,13 @@ conv_status conv_rms_norm_plan_create(conv_rms_norm_plan** out, int M, int C, fl
     conv_rms_norm_plan* pl = new (std::nothrow) conv_rms_norm_plan();
     if (pl == nullptr) return CONV_ERR_NO_MEMORY;
     int ndev = 0, num_sms = 152;
+    unsigned* status = nullptr;
     if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
         cudaGetLastError();
         pl->device = -1;
     } else if (cudaGetDevice(&pl->device) != cudaSuccess ||
-               cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess) {
+               cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, pl->device) != cudaSuccess ||
+               device_status_word(&status) != cudaSuccess) {
         cudaGetLastError();
         delete pl;
         return CONV_ERR_CUDA;
@@ -82,7 +101,8 @@ conv_status conv_rms_norm_plan_create(conv_rms_norm_plan** out, int M, int C, fl
     p.C = C;
     p.eps = eps;
     p.bf16 = dtype == CONV_BF16;
-    p.parts = rms_backward_parts(p, num_sms);
+    p.status = status;
+    rms_plan_backward(p, num_sms);
     *out = pl;
     return CONV_OK;
 }
@@ -137,12 +157,9 @@ conv_status conv_dropout(const void* x, const void* residual, conv_dtype dtype, 
     if (dtype != CONV_F32 && dtype != CONV_BF16) return CONV_ERR_INVALID_ARG;
     if (n > (1ULL << 40)) return CONV_ERR_UNSUPPORTED;
     if (!all_aligned16(x, residual, y) || (reinterpret_cast<uintptr_t>(state) & 7u) != 0) return CONV_ERR_MISALIGNED;
-    int dev = -1, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return CONV_ERR_CUDA;
-    }
+    int sms = 0;
+    const conv_status s = sm_count(sms);
+    if (s != CONV_OK) return s;
     DropoutParams d = {};
     d.x = x;
     d.r = residual;

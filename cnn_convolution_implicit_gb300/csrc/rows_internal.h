@@ -26,16 +26,19 @@ struct RmsParams {
     float* rstd;         // forward: written where given; backward: read
     float* dgamma;       // nullptr: not wanted
     float* part;         // workspace: [parts][C] sums of dy * n
-    int parts;
+    int parts;           // rows of sums that the backward pass leaves there
+    int ctas;            // of its streaming form
+    unsigned* status;
 };
 
-// Rows of sums that the backward pass leaves in the workspace.
-int rms_backward_parts(const RmsParams& p, int num_sms);
+// Fills parts and ctas.
+void rms_plan_backward(RmsParams& p, int num_sms);
 cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream);
 cudaError_t launch_rms_backward(const RmsParams& p, cudaStream_t stream);
 
-// Sums of `parts` rows of C values each, in one order (column_sums.cu).
-cudaError_t launch_join_columns(const float* part, int parts, int C, float* out, cudaStream_t stream);
+// Sums of `parts` rows of C values each, in one order (column_sums.cu).  early: the kernel before it on the stream lets it
+// start early.
+cudaError_t launch_join_columns(const float* part, int parts, int C, float* out, bool early, cudaStream_t stream);
 
 struct DropoutParams {
     const void* x;

@@ -14,20 +14,16 @@ from .binding import CONV_BF16, CONV_F32, _plan_status, lib
 from .operators import ACTS, _DTYPES, _check, _choice, _need, _need_any, _ptr, _refuse_device, _torch, _torch_dtypes, _workspace
 
 
-def _device_of(x):
-    """x's device, which has to be the current one."""
-    dev = x.get_device()
-    if dev < 0 or dev != _ops._current_device():
-        _refuse_device(dev)
-    return dev
+def _start():
+    """torch, and what every call takes from it."""
+    global _t, _empty, _empty_like, _bf16, _f32
+    if _t is None:
+        _t = _torch()
+        _empty, _empty_like, _bf16, _f32 = _t.empty, _t.empty_like, _t.bfloat16, _t.float32
+    return _t
 
 
-def _recorded(*tensors):
-    """Whether torch records a gradient for any of them."""
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            return _ops._t.is_grad_enabled()
-    return False
+_t = _empty = _empty_like = _bf16 = _f32 = None
 
 
 def _upstream(dy):
@@ -64,8 +60,7 @@ class LinearPlan(_Plan):
         h = ctypes.c_void_p()
         _check(L.conv_linear_plan_create(ctypes.byref(h), M, N, K, _choice(act, ACTS, "act")), "conv_linear_plan_create")
         self._plan = h
-        self._L = L
-        torch = _torch()
+        torch = _start()
         self.M, self.N, self.K, self.act = M, N, K, act
         self._x = torch.Size((M, K) if x_shape is None else x_shape)
         if self._x.numel() != M * K or self._x[-1] != K:
@@ -74,30 +69,45 @@ class LinearPlan(_Plan):
         a, b = ctypes.c_ulonglong(), ctypes.c_ulonglong()
         _check(L.conv_linear_workspace(h, ctypes.byref(a), ctypes.byref(b)), "conv_linear_workspace")
         self.workspace_bytes = {"forward": a.value, "backward": b.value}
+        self._forward_bytes, self._backward_bytes = a.value, b.value
+        self._forward, self._backward = L.conv_linear_forward, L.conv_linear_backward
 
     def forward(self, x, w, bias=None, residual=None, y=None, z=None, stream=None):
         """act(x w^T + bias) + residual; ``z`` receives the values before the activation, which backward()
         reads.  ``y`` may be the residual itself."""
         if stream is not None:
-            with _ops._t.cuda.stream(stream):
+            with _t.cuda.stream(stream):
                 return self.forward(x, w, bias, residual, y, z)
-        bf16 = _ops._t.bfloat16
-        dev = _device_of(x)
-        _need(x, "x", self._x, bf16, dev)
-        _need(w, "w", self._w, bf16, dev)
+        # The checks stand in line: a call of _need for each tensor took as long as the launch.  (The arguments stay
+        # bound to their tensors to the end: a caller's temporaries have no other owner.)
+        dev = x.get_device()
+        if dev < 0 or dev != _ops._current_device():
+            _refuse_device(dev)
+        shape = self._y
+        if x.shape != self._x or x.dtype is not _bf16 or not x.is_contiguous():
+            _need(x, "x", self._x, _bf16, dev)
+        if w.shape != self._w or w.dtype is not _bf16 or w.get_device() != dev or not w.is_contiguous():
+            _need(w, "w", self._w, _bf16, dev)
         if bias is not None:
-            _need(bias, "bias", self._cols, _ops._t.float32, dev)
+            if bias.shape != self._cols or bias.dtype is not _f32 or bias.get_device() != dev or not bias.is_contiguous():
+                _need(bias, "bias", self._cols, _f32, dev)
         if residual is not None:
-            _need(residual, "residual", self._y, bf16, dev)
+            if residual.shape != shape or residual.dtype is not _bf16 or residual.get_device() != dev or \
+                    not residual.is_contiguous():
+                _need(residual, "residual", shape, _bf16, dev)
         if z is not None:
-            _need(z, "z", self._y, bf16, dev)
+            _need(z, "z", shape, _bf16, dev)
         if y is None:
-            y = _ops._t.empty(self._y, dtype=bf16, device=dev)
+            y = _empty(shape, dtype=_bf16, device=dev)
         else:
-            _need(y, "y", self._y, bf16, dev)
-        ws = _workspace(self.workspace_bytes["forward"], dev)
-        _check(self._L.conv_linear_forward(self._plan, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
-                                           _ptr(z), _ptr(ws), _ops._raw_stream(dev)), "conv_linear_forward")
+            _need(y, "y", shape, _bf16, dev)
+        ws = _workspace(self._forward_bytes, dev) if self._forward_bytes else None
+        status = self._forward(self._plan, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+                               None if residual is None else residual.data_ptr(), y.data_ptr(),
+                               None if z is None else z.data_ptr(),
+                               None if ws is None else ws.data_ptr(), _ops._raw_stream(dev))
+        if status:
+            _check(status, "conv_linear_forward")
         return y
 
     __call__ = forward
@@ -107,30 +117,47 @@ class LinearPlan(_Plan):
         ``need`` (dx, dw, dbias) leaves out.  w is read for dx and x for dw.  The residual's
         gradient is dy itself."""
         if stream is not None:
-            with _ops._t.cuda.stream(stream):
+            with _t.cuda.stream(stream):
                 return self.backward(dy, x, w, z, dx, dw, dbias, need=need)
-        t = _ops._t
-        dev = _device_of(dy)
-        _need(dy, "dy", self._y, t.bfloat16, dev)
-        if x is not None or need[1]:
-            _need(x, "x", self._x, t.bfloat16, dev)
-        if w is not None or need[0]:
-            _need(w, "w", self._w, t.bfloat16, dev)
-        if z is not None or self.act != "none":
-            _need(z, "z", self._y, t.bfloat16, dev)
-        out = []
-        for given, name, shape, dtype, wanted in ((dx, "dx", self._x, t.bfloat16, need[0]),
-                                                  (dw, "dw", self._w, t.bfloat16, need[1]),
-                                                  (dbias, "dbias", self._cols, t.float32, need[2])):
+        dev = dy.get_device()
+        if dev < 0 or dev != _ops._current_device():
+            _refuse_device(dev)
+        need_x, need_w, need_b = need
+        if dy.shape != self._y or dy.dtype is not _bf16 or not dy.is_contiguous():
+            _need(dy, "dy", self._y, _bf16, dev)
+        if x is None:
+            if need_w:
+                _need(x, "x", self._x, _bf16, dev)
+        elif x.shape != self._x or x.dtype is not _bf16 or x.get_device() != dev or not x.is_contiguous():
+            _need(x, "x", self._x, _bf16, dev)
+        if w is None:
+            if need_x:
+                _need(w, "w", self._w, _bf16, dev)
+        elif w.shape != self._w or w.dtype is not _bf16 or w.get_device() != dev or not w.is_contiguous():
+            _need(w, "w", self._w, _bf16, dev)
+        if z is None:
+            if self.act != "none":
+                _need(z, "z", self._y, _bf16, dev)
+        elif z.shape != self._y or z.dtype is not _bf16 or z.get_device() != dev or not z.is_contiguous():
+            _need(z, "z", self._y, _bf16, dev)
+        for given, name, shape, dtype, wanted in ((dx, "dx", self._x, _bf16, need_x), (dw, "dw", self._w, _bf16, need_w),
+                                                  (dbias, "dbias", self._cols, _f32, need_b)):
             if given is not None:
                 if not wanted:
                     raise ValueError("%s is not written without need" % name)
                 _need(given, name, shape, dtype, dev)
-            out.append(given if given is not None or not wanted else t.empty(shape, dtype=dtype, device=dev))
-        ws = _workspace(self.workspace_bytes["backward"], dev)
-        _check(self._L.conv_linear_backward(self._plan, dy.data_ptr(), _ptr(x), _ptr(w), _ptr(z), _ptr(out[0]), _ptr(out[1]),
-                                            _ptr(out[2]), _ptr(ws), _ops._raw_stream(dev)), "conv_linear_backward")
-        return tuple(out)
+        if dx is None and need_x:
+            dx = _empty(self._x, dtype=_bf16, device=dev)
+        if dw is None and need_w:
+            dw = _empty(self._w, dtype=_bf16, device=dev)
+        if dbias is None and need_b:
+            dbias = _empty(self._cols, dtype=_f32, device=dev)
+        ws = _workspace(self._backward_bytes, dev) if self._backward_bytes else None
+        status = self._backward(self._plan, dy.data_ptr(), _ptr(x), _ptr(w), _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias),
+                                None if ws is None else ws.data_ptr(), _ops._raw_stream(dev))
+        if status:
+            _check(status, "conv_linear_backward")
+        return dx, dw, dbias
 
     def device_status(self, stream=None) -> int:
         """Read and clear the plan's own status word, as ConvPlan.device_status."""
@@ -150,8 +177,7 @@ class RmsNormPlan(_Plan):
         _check(L.conv_rms_norm_plan_create(ctypes.byref(h), M, C, eps, _choice(dtype, _DTYPES, "dtype")),
                "conv_rms_norm_plan_create")
         self._plan = h
-        self._L = L
-        torch = _torch()
+        torch = _start()
         self.M, self.C, self.dtype, self.torch_dtype, self.eps = M, C, dtype, _torch_dtypes()[dtype], eps
         self.shape = torch.Size((M, C) if x_shape is None else x_shape)
         if self.shape.numel() != M * C or self.shape[-1] != C:
@@ -161,37 +187,49 @@ class RmsNormPlan(_Plan):
         _check(L.conv_rms_norm_workspace(h, ctypes.byref(b)), "conv_rms_norm_workspace")
         self.workspace_bytes = {"backward": b.value}
 
+        self._forward, self._forward_int8 = L.conv_rms_norm_forward, L.conv_rms_norm_forward_int8
+        self._backward, self._backward_bytes = L.conv_rms_norm_backward, b.value
+
     def _inputs(self, x, gamma, residual, h, rstd):
         """Checks them; returns x's device and h, made where a residual calls for one."""
-        dev = _device_of(x)
-        _need(x, "x", self.shape, self.torch_dtype, dev)
-        if gamma is not None:
-            _need(gamma, "gamma", self._cols, _ops._t.float32, dev)
+        dev, shape, dtype = x.get_device(), self.shape, self.torch_dtype
+        if dev < 0 or dev != _ops._current_device():
+            _refuse_device(dev)
+        if x.shape != shape or x.dtype is not dtype or not x.is_contiguous():
+            _need(x, "x", shape, dtype, dev)
+        if gamma is not None and (gamma.shape != self._cols or gamma.dtype is not _f32 or gamma.get_device() != dev or
+                                  not gamma.is_contiguous()):
+            _need(gamma, "gamma", self._cols, _f32, dev)
         if residual is not None:
-            _need(residual, "residual", self.shape, self.torch_dtype, dev)
-        if h is not None:
-            if residual is None:
-                raise ValueError("h is written with a residual alone: without one it is x")
-            _need(h, "h", self.shape, self.torch_dtype, dev)
-        elif residual is not None:
-            h = _ops._t.empty_like(x)
+            if residual.shape != shape or residual.dtype is not dtype or residual.get_device() != dev or \
+                    not residual.is_contiguous():
+                _need(residual, "residual", shape, dtype, dev)
+            if h is None:
+                h = _empty_like(x)
+            else:
+                _need(h, "h", shape, dtype, dev)
+        elif h is not None:
+            raise ValueError("h is written with a residual alone: without one it is x")
         if rstd is not None:
-            _need(rstd, "rstd", self._rows, _ops._t.float32, dev)
+            _need(rstd, "rstd", self._rows, _f32, dev)
         return dev, h
 
     def forward(self, x, gamma=None, residual=None, y=None, h=None, rstd=None, stream=None):
         """y, or (y, h) with a residual; ``rstd`` (empty_rstd()) receives what backward() reads.  ``h`` may be
         the residual itself."""
         if stream is not None:
-            with _ops._t.cuda.stream(stream):
+            with _t.cuda.stream(stream):
                 return self.forward(x, gamma, residual, y, h, rstd)
         dev, h = self._inputs(x, gamma, residual, h, rstd)
         if y is None:
-            y = _ops._t.empty_like(x)
+            y = _empty_like(x)
         else:
             _need(y, "y", self.shape, self.torch_dtype, dev)
-        _check(self._L.conv_rms_norm_forward(self._plan, x.data_ptr(), _ptr(residual), _ptr(gamma), y.data_ptr(), _ptr(h),
-                                             _ptr(rstd), _ops._raw_stream(dev)), "conv_rms_norm_forward")
+        status = self._forward(self._plan, x.data_ptr(), None if residual is None else residual.data_ptr(),
+                               None if gamma is None else gamma.data_ptr(), y.data_ptr(), None if h is None else h.data_ptr(),
+                               None if rstd is None else rstd.data_ptr(), _ops._raw_stream(dev))
+        if status:
+            _check(status, "conv_rms_norm_forward")
         return y if residual is None else (y, h)
 
     __call__ = forward
@@ -199,20 +237,21 @@ class RmsNormPlan(_Plan):
     def forward_int8(self, x, gamma=None, residual=None, q=None, scale=None, h=None, rstd=None, stream=None):
         """(q, scale), or (q, scale, h) with a residual: y as int8 with one FP32 scale per row [M]."""
         if stream is not None:
-            with _ops._t.cuda.stream(stream):
+            with _t.cuda.stream(stream):
                 return self.forward_int8(x, gamma, residual, q, scale, h, rstd)
         dev, h = self._inputs(x, gamma, residual, h, rstd)
         if q is None:
-            q = _ops._t.empty(self.shape, dtype=_ops._t.int8, device=dev)
+            q = _empty(self.shape, dtype=_t.int8, device=dev)
         else:
-            _need(q, "q", self.shape, _ops._t.int8, dev)
+            _need(q, "q", self.shape, _t.int8, dev)
         if scale is None:
-            scale = _ops._t.empty(self._rows, dtype=_ops._t.float32, device=dev)
+            scale = _empty(self._rows, dtype=_f32, device=dev)
         else:
-            _need(scale, "scale", self._rows, _ops._t.float32, dev)
-        _check(self._L.conv_rms_norm_forward_int8(self._plan, x.data_ptr(), _ptr(residual), _ptr(gamma), q.data_ptr(),
-                                                  scale.data_ptr(), _ptr(h), _ptr(rstd), _ops._raw_stream(dev)),
-               "conv_rms_norm_forward_int8")
+            _need(scale, "scale", self._rows, _f32, dev)
+        status = self._forward_int8(self._plan, x.data_ptr(), _ptr(residual), _ptr(gamma), q.data_ptr(), scale.data_ptr(),
+                                    _ptr(h), _ptr(rstd), _ops._raw_stream(dev))
+        if status:
+            _check(status, "conv_rms_norm_forward_int8")
         return (q, scale) if residual is None else (q, scale, h)
 
     def backward(self, dy, h, rstd, gamma=None, dh=None, dx=None, dgamma=None, stream=None, gamma_grad=True):
@@ -220,48 +259,55 @@ class RmsNormPlan(_Plan):
         output h, dx that of x and of the residual alike.  Without ``gamma_grad`` (dx, None).  ``dx`` may be dy
         or dh itself."""
         if stream is not None:
-            with _ops._t.cuda.stream(stream):
+            with _t.cuda.stream(stream):
                 return self.backward(dy, h, rstd, gamma, dh, dx, dgamma, gamma_grad=gamma_grad)
-        t = _ops._t
-        dev = _device_of(dy)
-        _need(dy, "dy", self.shape, self.torch_dtype, dev)
-        _need(h, "h", self.shape, self.torch_dtype, dev)
-        _need(rstd, "rstd", self._rows, t.float32, dev)
+        dev, shape, dtype = dy.get_device(), self.shape, self.torch_dtype
+        if dev < 0 or dev != _ops._current_device():
+            _refuse_device(dev)
+        if dy.shape != shape or dy.dtype is not dtype or not dy.is_contiguous():
+            _need(dy, "dy", shape, dtype, dev)
+        if h.shape != shape or h.dtype is not dtype or h.get_device() != dev or not h.is_contiguous():
+            _need(h, "h", shape, dtype, dev)
+        _need(rstd, "rstd", self._rows, _f32, dev)
         if gamma is not None:
-            _need(gamma, "gamma", self._cols, t.float32, dev)
+            _need(gamma, "gamma", self._cols, _f32, dev)
         if dh is not None:
-            _need(dh, "dh", self.shape, self.torch_dtype, dev)
+            _need(dh, "dh", shape, dtype, dev)
         if dx is None:
-            dx = t.empty_like(dy)
+            dx = _empty_like(dy)
         else:
-            _need(dx, "dx", self.shape, self.torch_dtype, dev)
-        if dgamma is not None:
-            if not gamma_grad:
-                raise ValueError("dgamma is not written without gamma_grad")
-            _need(dgamma, "dgamma", self._cols, t.float32, dev)
-        elif gamma_grad:
-            dgamma = t.empty(self._cols, dtype=t.float32, device=dev)
-        ws = _workspace(self.workspace_bytes["backward"], dev) if gamma_grad else None
-        _check(self._L.conv_rms_norm_backward(self._plan, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _ptr(gamma), _ptr(dh),
-                                              dx.data_ptr(), _ptr(dgamma), _ptr(ws), _ops._raw_stream(dev)),
-               "conv_rms_norm_backward")
+            _need(dx, "dx", shape, dtype, dev)
+        ws = None
+        if gamma_grad:
+            if dgamma is None:
+                dgamma = _empty(self._cols, dtype=_f32, device=dev)
+            else:
+                _need(dgamma, "dgamma", self._cols, _f32, dev)
+            ws = _workspace(self._backward_bytes, dev)
+        elif dgamma is not None:
+            raise ValueError("dgamma is not written without gamma_grad")
+        status = self._backward(self._plan, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _ptr(gamma), _ptr(dh), dx.data_ptr(),
+                                _ptr(dgamma), _ptr(ws), _ops._raw_stream(dev))
+        if status:
+            _check(status, "conv_rms_norm_backward")
         return dx, dgamma
 
     def empty_rstd(self, device="cuda"):
-        return _ops._t.empty(self._rows, dtype=_ops._t.float32, device=device)
+        return _empty(self._rows, dtype=_f32, device=device)
 
 
 # ---------------------------------------------------------------- functional forms
 _linear_plans = binding.PlanCache()
 _rms_plans = binding.PlanCache()
 _functions = {}
+_TWO = (2,)
 
 
 def _linear_plan(x, w, act):
     key = (x.shape, w.shape, x.get_device(), act)
     plan = _linear_plans.get(key)
     if plan is None:
-        _torch()
+        _start()
         _refuse_device(x.get_device())
         if w.dim() != 2 or x.dim() < 2 or x.shape[-1] != w.shape[1]:
             raise ValueError("x must be [..., K] and w [N][K]: got %s and %s" % (tuple(x.shape), tuple(w.shape)))
@@ -276,7 +322,7 @@ def _rms_plan(x, eps):
     key = (x.shape, x.dtype, x.get_device(), eps)
     plan = _rms_plans.get(key)
     if plan is None:
-        torch = _torch()
+        torch = _start()
         _need_any(x, "x", (torch.bfloat16, torch.float32))
         if x.dim() < 2:
             raise ValueError("x must be [..., C]")
@@ -293,7 +339,7 @@ def _function(name):
     """The autograd functions of linear, rms_norm and dropout.  They keep buffers of their own: a caller's
     may hold another call's by the time of the backward pass."""
     if not _functions:
-        torch = _torch()
+        torch = _start()
         from torch.autograd.function import once_differentiable
 
         class Linear(torch.autograd.Function):
@@ -364,7 +410,8 @@ def linear(x, w, bias=None, act="none", residual=None, y=None, z=None, stream=No
         with _torch().cuda.stream(stream):
             return linear(x, w, bias, act, residual, y, z)
     plan = _linear_plan(x, w, act)
-    if _recorded(x, w, bias, residual):
+    if (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
+            (residual is not None and residual.requires_grad)) and _t.is_grad_enabled():
         if y is not None or z is not None:
             raise ValueError("y and z cannot be given where the result's gradient is recorded")
         return _function("linear").apply(x, w, bias, residual, plan)
@@ -392,11 +439,12 @@ def rms_norm(x, gamma=None, residual=None, eps=1e-6, h=None, rstd=None, stream=N
         with _torch().cuda.stream(stream):
             return rms_norm(x, gamma, residual, eps, h, rstd)
     plan = _rms_plan(x, eps)
-    if _recorded(x, gamma, residual):
+    if (x.requires_grad or (gamma is not None and gamma.requires_grad) or
+            (residual is not None and residual.requires_grad)) and _t.is_grad_enabled():
         if h is not None:
             raise ValueError("h cannot be given where the result's gradient is recorded")
         if rstd is not None:
-            _need(rstd, "rstd", plan._rows, _ops._t.float32, x.get_device())
+            _need(rstd, "rstd", plan._rows, _f32, x.get_device())
         *out, own = _function("rms_norm").apply(x, gamma, residual, plan)
         if rstd is not None:
             rstd.copy_(own)
@@ -423,18 +471,26 @@ def rms_norm_backward(dy, h, rstd, gamma=None, dh=None, stream=None):
 
 
 def _dropout(x, p, state, residual=None, y=None):
-    torch = _torch()
-    _need_any(x, "x", (torch.bfloat16, torch.float32))
-    dev = _device_of(x)
+    dtype, shape, dev = x.dtype, x.shape, x.get_device()
+    if (dtype is not _bf16 and dtype is not _f32) or dev < 0 or not x.is_contiguous():
+        _need_any(x, "x", (_bf16, _f32))
+    if dev != _ops._current_device():
+        _refuse_device(dev)
     if residual is not None:
-        _need(residual, "residual", x.shape, x.dtype, dev)
-    _need(state, "state", torch.Size((2,)), torch.int64, dev)
+        if residual.shape != shape or residual.dtype is not dtype or residual.get_device() != dev or \
+                not residual.is_contiguous():
+            _need(residual, "residual", shape, dtype, dev)
+    if state.dtype is not _t.int64 or state.shape != _TWO or state.get_device() != dev or not state.is_contiguous():
+        _need(state, "state", _TWO, _t.int64, dev)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty_like(x)
     else:
-        _need(y, "y", x.shape, x.dtype, dev)
-    _check(lib().conv_dropout(x.data_ptr(), _ptr(residual), CONV_BF16 if x.dtype is torch.bfloat16 else CONV_F32, x.numel(), p,
-                              state.data_ptr(), y.data_ptr(), _ops._raw_stream(dev)), "conv_dropout")
+        _need(y, "y", shape, dtype, dev)
+    status = (binding._lib or lib()).conv_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                                                  CONV_BF16 if dtype is _bf16 else CONV_F32, x.numel(), p, state.data_ptr(),
+                                                  y.data_ptr(), _ops._raw_stream(dev))
+    if status:
+        _check(status, "conv_dropout")
     return y
 
 
@@ -449,11 +505,12 @@ def dropout(x, p, state, residual=None, y=None, stream=None):
     if stream is not None:
         with _torch().cuda.stream(stream):
             return dropout(x, p, state, residual, y)
-    _torch()
-    if _recorded(x, residual):
+    if _t is None:
+        _start()
+    if (x.requires_grad or (residual is not None and residual.requires_grad)) and _t.is_grad_enabled():
         if y is not None:
             raise ValueError("y cannot be given where the result's gradient is recorded")
-        if state.dtype is not _ops._t.int64 or state.shape != (2,):
+        if state.dtype is not _t.int64 or state.shape != _TWO:
             raise ValueError("state must be an int64 tensor of two")
         return _function("dropout").apply(x, residual, p, state)
     return _dropout(x, p, state, residual, y)

@@ -286,3 +286,20 @@ def test_residual_branch():
     one = cg.linear(h[:1], W1, B1, "silu")
     (want, tol), _ = ref.linear(_np(h[:1]), _np(w1), _np(b1), None, "silu")
     oref.check(_np(one), want, tol, True, "one token")
+
+
+def test_arguments_that_nobody_else_holds():
+    """A caller's temporaries live until the launch: their memory is not given to the call's own buffers (rows to
+    lay out, parts of K, results)."""
+    import cnn_convolution_implicit_gb300 as cg
+    for M, N, K in ((129, 257, 127), (70, 512, 4096), (5, 100, 60)):
+        x, w, b, r, dy = _inputs(M, N, K, 91)
+        want = cg.linear(x.cuda(), w.cuda(), b.cuda(), "silu", r.cuda())
+        keep = [t.cuda() for t in (x, w, b, r, dy)]
+        assert torch.equal(cg.linear(*keep[:3], "silu", keep[3]), want)
+        for _ in range(3):
+            assert torch.equal(cg.linear(*(t.clone() for t in keep[:3]), "silu", keep[3].clone()), want)
+            torch.cuda.empty_cache()
+        grads = cg.linear_backward(keep[4], keep[0], keep[1], want, "silu")
+        again = cg.linear_backward(keep[4].clone(), keep[0].clone(), keep[1].clone(), want.clone(), "silu")
+        assert all(torch.equal(p, q) for p, q in zip(grads, again))
