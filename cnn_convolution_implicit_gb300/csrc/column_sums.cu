@@ -120,7 +120,7 @@ int linear_grad_parts(int M, int N, int num_sms) {
     return static_cast<int>(need < most ? need : most);
 }
 
-cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, bool join, cudaStream_t stream) {
     const Strip s = strip_of(p.N);
     const int parts = linear_grad_parts(p.M, p.N, num_sms);
     float* sums = p.dbias == nullptr ? nullptr : (parts > 1 ? p.part : p.dbias);
@@ -130,7 +130,7 @@ cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, cudaStrea
     else if (p.act == CONV_ACT_SILU) run(linear_grad_kernel<8, CONV_ACT_SILU>, linear_grad_kernel<1, CONV_ACT_SILU>);
     else run(linear_grad_kernel<8, CONV_ACT_NONE>, linear_grad_kernel<1, CONV_ACT_NONE>);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.dbias == nullptr || parts == 1) return e;
+    if (e != cudaSuccess || p.dbias == nullptr || parts == 1 || !join) return e;
     return launch_join_columns(p.part, parts, p.N, p.dbias, true, stream);
 }
 

@@ -12,7 +12,9 @@ using namespace convgb;
 struct conv_linear_plan {
     int M, N, K, act;
     bool few;                  // the forward product runs in the kernel of few rows
-    GemmTile forward, dx, dw;  // tiles of the three products
+    GemmTile forward, backward;  // tiles of the product, and of the gradients' (the longer sums first; alone they keep the same
+                                 // tiles and splits, so that what else a call asks for does not change their bits)
+    bool dw_first;
     int device;
     int num_sms;
     unsigned* status;
@@ -48,7 +50,7 @@ int pitch_of(int n) { return static_cast<int>(up(n, 8)); }  // elements of a row
 
 // Workspaces: rows off 16 bytes laid out on them, u, parts of sums.
 struct Workspace {
-    size_t x, w, u, part, sums, bytes;  // offsets, and bytes in all
+    size_t x, w, u, part, part2, sums, bytes;  // offsets, and bytes in all
 };
 
 size_t rows_bytes(long long rows, int n) { return up(static_cast<size_t>(rows) * pitch_of(n) * 2, 256); }
@@ -59,7 +61,7 @@ Workspace forward_space(const conv_linear_plan* pl) {
     const bool lay_out = pl->K % 8 != 0;
     ws.w = lay_out ? rows_bytes(pl->M, pl->K) : 0;
     ws.part = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
-    ws.bytes = ws.part + gemm_part_bytes(pl->forward, pl->M, pl->N);
+    ws.bytes = ws.part + gemm_part_bytes(pl->forward.splits[0], pl->M, pl->N);
     return ws;
 }
 
@@ -70,8 +72,8 @@ Workspace backward_space(const conv_linear_plan* pl) {
     ws.u = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
     ws.sums = ws.u + (pl->act != CONV_ACT_NONE || pl->N % 8 != 0 ? rows_bytes(pl->M, pl->N) : 0);
     ws.part = ws.sums + up(static_cast<size_t>(linear_grad_parts(pl->M, pl->N, pl->num_sms)) * pl->N * sizeof(float), 256);
-    const size_t dx = gemm_part_bytes(pl->dx, pl->M, pl->K), dw = gemm_part_bytes(pl->dw, pl->N, pl->K);
-    ws.bytes = ws.part + (dx > dw ? dx : dw);
+    ws.part2 = ws.part + up(gemm_part_bytes(pl->backward.splits[pl->dw_first ? 1 : 0], pl->M, pl->K), 256);  // dw's, behind dx's
+    ws.bytes = ws.part2 + gemm_part_bytes(pl->backward.splits[pl->dw_first ? 0 : 1], pl->N, pl->K);
     return ws;
 }
 
@@ -117,9 +119,11 @@ conv_status conv_linear_plan_create(conv_linear_plan** out, int M, int N, int K,
         return CONV_ERR_CUDA;
     }
     pl->few = linear_use_few(M, N, K);
-    pl->forward = gemm_pick_tile(M, N, K, pl->num_sms);
-    pl->dx = gemm_pick_tile(M, K, N, pl->num_sms);
-    pl->dw = gemm_pick_tile(N, K, M, pl->num_sms);
+    const GemmSize forward = {M, N, K}, dx = {M, K, N}, dw = {N, K, M};
+    pl->forward = gemm_pick_tile(&forward, 1, pl->num_sms);
+    pl->dw_first = M > N;
+    const GemmSize both[2] = {pl->dw_first ? dw : dx, pl->dw_first ? dx : dw};
+    pl->backward = gemm_pick_tile(both, 2, pl->num_sms);
     *out = pl;
     return CONV_OK;
 }
@@ -169,7 +173,7 @@ conv_status conv_linear_forward(conv_linear_plan* pl, const void* x, const void*
     p.z = static_cast<__nv_bfloat16*>(z);
     p.part = reinterpret_cast<float*>(base + ws.part);
     p.status = pl->status;
-    return launched(launch_gemm(p, pl->forward, pl->num_sms, laid_out, st));
+    return launched(launch_gemm(&p, 1, pl->forward, ColumnJoin(), pl->num_sms, laid_out, st));
 }
 
 conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const void* x, const void* w, const void* z,
@@ -187,9 +191,12 @@ conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const voi
     const bool products = dx != nullptr || dw != nullptr;
     const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(dy);
     int u_pitch = pl->N;
+    ColumnJoin join = {};  // dbias's parts, left to the products' launch
     const bool copy = products && (pl->act != CONV_ACT_NONE || pl->N % 8 != 0);
     cudaError_t e = cudaSuccess;
+    bool early = false;  // the kernel before the products lets them start early
     if (copy || dbias != nullptr) {
+        early = products;
         LinearGradParams g = {};
         g.M = pl->M;
         g.N = pl->N;
@@ -204,41 +211,48 @@ conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const voi
         g.part = reinterpret_cast<float*>(base + ws.sums);
         g.dbias = dbias;
         g.act = pl->act;
-        e = launch_linear_grad(g, pl->num_sms, st);
+        e = launch_linear_grad(g, pl->num_sms, !products, st);
+        const int parts = linear_grad_parts(pl->M, pl->N, pl->num_sms);
+        if (products && dbias != nullptr && parts > 1) join = {g.part, dbias, parts, pl->N};
     }
     const __nv_bfloat16* xs = static_cast<const __nv_bfloat16*>(x);
     const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(w);
     int k_pitch = pl->K;
     if (e == cudaSuccess && products && pl->K % 8 != 0) {
+        early = true;
         e = lay_out(x, base + ws.x, dw != nullptr ? pl->M : 0, w, base + ws.w, dx != nullptr ? pl->N : 0, pl->K, pl->num_sms, st);
         xs = reinterpret_cast<const __nv_bfloat16*>(base + ws.x);
         wt = reinterpret_cast<const __nv_bfloat16*>(base + ws.w);
         k_pitch = pitch_of(pl->K);
     }
-    GemmParams p = {};
-    p.N = pl->K;
-    p.a = u;
-    p.a_pitch = u_pitch;
-    p.b_pitch = k_pitch;
-    p.b_by_k = true;
-    p.part = reinterpret_cast<float*>(base + ws.part);
-    p.status = pl->status;
-    if (e == cudaSuccess && dx != nullptr) {
-        p.M = pl->M;
-        p.K = pl->N;
-        p.b = wt;
-        p.y = static_cast<__nv_bfloat16*>(dx);
-        e = launch_gemm(p, pl->dx, pl->num_sms, false, st);
+    if (e != cudaSuccess || !products) return launched(e);
+    GemmParams p[2] = {};
+    GemmTile tile = pl->backward;
+    const auto product = [&](GemmParams& g, int M, int K, const __nv_bfloat16* b, void* y, size_t part) {
+        g.M = M;
+        g.N = pl->K;
+        g.K = K;
+        g.a = u;
+        g.a_pitch = u_pitch;
+        g.b = b;
+        g.b_pitch = k_pitch;
+        g.b_by_k = true;
+        g.y = static_cast<__nv_bfloat16*>(y);
+        g.part = reinterpret_cast<float*>(base + part);
+        g.status = pl->status;
+    };
+    const int at_dx = pl->dw_first ? 1 : 0, at_dw = 1 - at_dx;  // in tile's order
+    if (dx != nullptr) product(p[at_dx], pl->M, pl->N, wt, dx, ws.part);
+    if (dw != nullptr) {
+        product(p[at_dw], pl->N, pl->M, xs, dw, ws.part2);
+        p[at_dw].a_by_k = true;
     }
-    if (e == cudaSuccess && dw != nullptr) {
-        p.M = pl->N;
-        p.K = pl->M;
-        p.a_by_k = true;
-        p.b = xs;
-        p.y = static_cast<__nv_bfloat16*>(dw);
-        e = launch_gemm(p, pl->dw, pl->num_sms, false, st);
+    const int only = dx == nullptr ? at_dw : (dw == nullptr ? at_dx : -1);
+    if (only == 1) {
+        p[0] = p[1];
+        tile.splits[0] = tile.splits[1];
     }
-    return launched(e);
+    return launched(launch_gemm(p, only < 0 ? 2 : 1, tile, join, pl->num_sms, early, st));
 }
 
 conv_status conv_linear_plan_device_status(const conv_linear_plan* p, void* stream, int* code) {

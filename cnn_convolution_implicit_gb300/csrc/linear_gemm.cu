@@ -4,7 +4,8 @@
 //
 // One kernel for the forward product (both operands by row: K-major) and the two gradients, whose
 // operands lie the other way round: dx = u w reads w, and dw = u^T x both operands, as rows along K
-// (MN-major: the TMA brings 64 x 64 boxes, whose 128-byte rows run along m or n).
+// (MN-major: the TMA brings 64 x 64 boxes, whose 128-byte rows run along m or n).  Both gradients go in one launch:
+// their tiles fill the SMs' rounds together.
 //
 // Warp roles (one CTA per SM, persistent over units; a unit is a tile, or a part of its K):
 //   the first 8 or 16   epilogue: a warp drains 32 rows of tensor memory, 64 columns at a time; in two groups that
@@ -104,16 +105,42 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // columns of B, which then come from L2), and its steps of K.
 constexpr int kGroupM = 8;
 
-struct Tiles {
-    int m_tiles, n_tiles, tiles, units, step, ksteps, splits;
+// One product of a launch.
+struct Job {
+    CUtensorMap map_a, map_b, map_y, map_z, map_r, map_part;
+    int M, N, K, splits;
+    int m_tiles, n_tiles, tiles, ksteps;
+    int first;  // its first unit
+    int a_by_k, act;
+    const float* bias;
+    const __nv_bfloat16* r;
+    __nv_bfloat16* y;
+    __nv_bfloat16* z;
+};
+
+struct Launch {
+    Job job[2];
+    int jobs, units;
+    Ring ring;
+    ColumnJoin join;
+    unsigned* status;
 };
 
 struct Unit {
     int mt, nt, split, k_first, k_count;
 };
 
-__device__ __forceinline__ Unit unit_at(const Tiles& t, int u) {
+// The forward product comes alone, the gradients (SEVERAL) in twos.
+template <bool SEVERAL>
+__device__ __forceinline__ const Job& job_of(const Launch& L, int u) {
+    if constexpr (!SEVERAL) return L.job[0];
+    return L.job[L.jobs > 1 && u >= L.job[1].first ? 1 : 0];
+}
+
+template <bool SEVERAL>
+__device__ __forceinline__ Unit unit_at(const Job& t, int u) {
     Unit w;
+    if constexpr (SEVERAL) u -= t.first;
     w.split = u / t.tiles;
     const int i = u - w.split * t.tiles;
     const int per_group = kGroupM * t.n_tiles, g = i / per_group, rest = i - g * per_group;
@@ -133,9 +160,9 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
 }
 
 // ROWS rows of an operand from row `row`, K = 64 from k, to a stage.
-template <bool PAIR, bool BY_K, int ROWS>
-__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_leader, int row, int k) {
-    if constexpr (BY_K) {
+template <bool PAIR, int ROWS>
+__device__ __forceinline__ void load_operand(bool by_k, uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t bar_leader, int row, int k) {
+    if (by_k) {
 #pragma unroll
         for (int i = 0; i < ROWS / 64; ++i) {
             if constexpr (PAIR) tma_load_2d_pair(dst + i * kBox, map, bar_leader, row + 64 * i, k);
@@ -147,10 +174,9 @@ __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* ma
     }
 }
 
-template <bool BY_K>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int j) {  // K = 16 j .. 16 j + 15 of a stage
-    if constexpr (BY_K) return sdesc_mn(base + j * 2048);
-    else return sdesc_sw128(base) + 2 * j;
+// K = 16 j .. 16 j + 15 of a stage: 2,048 bytes, or 32, further for each.
+__device__ __forceinline__ uint64_t operand_desc(bool by_k, uint32_t base, int j) {
+    return by_k ? sdesc_mn(base) + 128 * j : sdesc_sw128(base) + 2 * j;
 }
 
 // ---------------------------------------------------------------- epilogue of a block: 32 rows x 64 columns
@@ -240,7 +266,7 @@ struct LaneBias {
 // The bias reaches the lanes through shared memory: read from global memory by every lane, 16 bytes at a time, it
 // was what the epilogue waited for (200704 x 256 -> 512 with ReLU 73 us, 55 without a bias).
 template <int ACT, bool TMA>
-__device__ __forceinline__ void block_pass(const GemmParams& p, const CUtensorMap* map, __nv_bfloat16* to, bool with_r, uint32_t at,
+__device__ __forceinline__ void block_pass(const Job& p, const CUtensorMap* map, __nv_bfloat16* to, bool with_r, uint32_t at,
                                            uint8_t* block, const LaneBias& bias, int m, int n) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -274,17 +300,22 @@ __device__ __forceinline__ void block_pass(const GemmParams& p, const CUtensorMa
     }
 }
 
-template <bool TMA>
-__device__ __forceinline__ void finish_block(const GemmParams& p, const CUtensorMap* map_y, const CUtensorMap* map_z, uint32_t at,
+// PLAIN: y is the sums, rounded.
+template <bool TMA, bool PLAIN>
+__device__ __forceinline__ void finish_block(const Job& p, uint32_t at,
                                              uint8_t* block, const LaneBias& bias, int m, int n) {
+    if constexpr (PLAIN) {
+        block_pass<CONV_ACT_NONE, TMA>(p, &p.map_y, p.y, false, at, block, LaneBias(), m, n);
+        return;
+    }
     const bool with_r = p.r != nullptr;
-    if (p.act == CONV_ACT_RELU) block_pass<CONV_ACT_RELU, TMA>(p, map_y, p.y, with_r, at, block, bias, m, n);
-    else if (p.act == CONV_ACT_SILU) block_pass<CONV_ACT_SILU, TMA>(p, map_y, p.y, with_r, at, block, bias, m, n);
-    else block_pass<CONV_ACT_NONE, TMA>(p, map_y, p.y, with_r, at, block, bias, m, n);
+    if (p.act == CONV_ACT_RELU) block_pass<CONV_ACT_RELU, TMA>(p, &p.map_y, p.y, with_r, at, block, bias, m, n);
+    else if (p.act == CONV_ACT_SILU) block_pass<CONV_ACT_SILU, TMA>(p, &p.map_y, p.y, with_r, at, block, bias, m, n);
+    else block_pass<CONV_ACT_NONE, TMA>(p, &p.map_y, p.y, with_r, at, block, bias, m, n);
     if (p.z != nullptr) {  // a second pass: tensor memory still has the sums
         if (TMA && (threadIdx.x & 31) == 0) bulk_wait_read_all();
         __syncwarp();
-        block_pass<CONV_ACT_NONE, TMA>(p, map_z, p.z, false, at, block, bias, m, n);
+        block_pass<CONV_ACT_NONE, TMA>(p, &p.map_z, p.z, false, at, block, bias, m, n);
     }
 }
 
@@ -310,17 +341,30 @@ __device__ __forceinline__ void leave_block(const CUtensorMap* map, uint32_t at,
     }
 }
 
-template <bool PAIR, int BN, bool A_BY_K, bool B_BY_K>
-__global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
-    linear_gemm_kernel(const GemmParams p, const Ring ring, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                       const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
-                       const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_part) {
+// Sums over rows that the kernel before left in parts, a warp to a column: lane i adds parts i, i + 32, ..., as
+// launch_join_columns' warps do, and the lanes' sums meet in its order.
+__device__ __forceinline__ void join_columns(const ColumnJoin& j, int first, int step) {
+    const int lane = threadIdx.x & 31;
+    for (int c = first; c < j.columns; c += step) {
+        float total = 0.0f;
+        for (int i = lane; i < j.parts; i += 32) total += j.part[static_cast<long long>(i) * j.columns + c];
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(0xffffffffu, total, i);
+        if (lane == 0) j.out[c] = total;
+    }
+}
+
+// TMA: rows of y start on 16 bytes (of their own, lest the other path's registers spill this one's: 200704 x 256 -> 512 with
+// a residual 94 us together, 84 apart).
+template <bool PAIR, int BN, bool B_BY_K, bool TMA>
+__global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kernel(const __grid_constant__ Launch L) {
     using S = Shape<PAIR, BN>;
     constexpr int kMmaWarp = S::kEpilogueWarps, kLoadWarp = kMmaWarp + 1, kCtas = S::kCtas;
+    const Ring ring = L.ring;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join of parts that may follow
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_addr(smem) & 1023u) {  // the swizzle's atoms; uniform, so no CTA waits for another
-        record_status(p.status, kStatusTimeoutMma, nullptr);
+        record_status(L.status, kStatusTimeoutMma, nullptr);
         return;
     }
     Bars b;
@@ -339,15 +383,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
 
-    Tiles tiles;
-    tiles.m_tiles = (p.M + 128 * kCtas - 1) / (128 * kCtas);
-    tiles.n_tiles = (p.N + BN - 1) / BN;
-    tiles.tiles = tiles.m_tiles * tiles.n_tiles;
-    tiles.splits = p.splits;
-    tiles.units = tiles.tiles * p.splits;
-    tiles.step = static_cast<int>(gridDim.x) / kCtas;
-    tiles.ksteps = (p.K + kStepK - 1) / kStepK;
-    const int unit0 = static_cast<int>(blockIdx.x) / kCtas;
+    const int unit0 = static_cast<int>(blockIdx.x) / kCtas, unit_step = static_cast<int>(gridDim.x) / kCtas, units = L.units;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) {
@@ -386,12 +422,14 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
         uint8_t* block = outputs + warp * kBlockBytes;
         uint64_t* res = b.res + warp;
         float* bias_row = b.bias + 32 * warp;
-        const bool tma = p.N % 8 == 0, by_tma = p.r != nullptr && tma && p.splits == 1;
+        if (B_BY_K && L.join.out != nullptr) join_columns(L.join, static_cast<int>(blockIdx.x) * ring.warps + warp, static_cast<int>(gridDim.x) * ring.warps);
         uint32_t res_phase = 0;
         int local = group;
         bool ok = true;
-        for (int u = unit0 + group * tiles.step; u < tiles.units && ok; u += ring.groups * tiles.step, local += ring.groups) {
-            const Unit w = unit_at(tiles, u);
+        for (int u = unit0 + group * unit_step; u < units && ok; u += ring.groups * unit_step, local += ring.groups) {
+            const Job& p = job_of<B_BY_K>(L, u);
+            const Unit w = unit_at<B_BY_K>(p, u);
+            const bool by_tma = TMA && !B_BY_K && p.r != nullptr && p.splits == 1;
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
             const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128 + quarter * 32, n = w.nt * BN + part * cols;
@@ -400,16 +438,18 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
                 if (lane == 0) {
                     bulk_wait_read_all();
                     mbar_arrive_expect_tx(res, kBlockBytes);
-                    tma_load_2d(block, &map_r, res, n + kBlockCols * i, m);
+                    tma_load_2d(block, &p.map_r, res, n + kBlockCols * i, m);
                 }
                 __syncwarp();
             };
-            LaneBias bias;
-            bias.row = p.bias != nullptr ? bias_row : nullptr;
-            bias.load(p.bias, n, p.N);
+            LaneBias bias = {};
+            if constexpr (!B_BY_K) {
+                bias.row = p.bias != nullptr ? bias_row : nullptr;
+                bias.load(p.bias, n, p.N);
+            }
             if (by_tma && blocks > 0) fetch(0);
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
-                record_status(p.status, kStatusTimeoutEpilogue, abort);
+                record_status(L.status, kStatusTimeoutEpilogue, abort);
                 ok = false;
             }
             tc_fence_after();
@@ -418,23 +458,22 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
                 if (by_tma) {  // the first also after a wait that gave up: no copy may be in flight when the CTA leaves
                     if (i > 0) fetch(i);
                     if (!warp_wait(res, res_phase, nullptr)) {
-                        record_status(p.status, kStatusTimeoutEpilogue, abort);
+                        record_status(L.status, kStatusTimeoutEpilogue, abort);
                         ok = false;
                     }
                     res_phase ^= 1u;
-                } else if (p.splits == 1 && tma) {
+                } else if (TMA && p.splits == 1) {
                     if (lane == 0) bulk_wait_read_all();
                     __syncwarp();
-                } else if (p.splits == 1 && p.r != nullptr && ok) {
+                } else if (!TMA && !B_BY_K && p.splits == 1 && p.r != nullptr && ok) {
                     move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + kBlockCols * i, p.M);
                     __syncwarp();
                 }
                 if (!ok) continue;
-                if (i > 0) bias.load(p.bias, n + kBlockCols * i, p.N);
+                if (!B_BY_K && i > 0) bias.load(p.bias, n + kBlockCols * i, p.N);
                 const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + part * cols + kBlockCols * i;
-                if (p.splits > 1) leave_block(&map_part, at, block, m, n + kBlockCols * i, p.N, w.split);
-                else if (tma) finish_block<true>(p, &map_y, &map_z, at, block, bias, m, n + kBlockCols * i);
-                else finish_block<false>(p, &map_y, &map_z, at, block, bias, m, n + kBlockCols * i);
+                if (p.splits > 1) leave_block(&p.map_part, at, block, m, n + kBlockCols * i, p.N, w.split);
+                else finish_block<TMA, B_BY_K>(p, at, block, bias, m, n + kBlockCols * i);
             }
             if (!ok) break;
             tc_fence_before();
@@ -451,12 +490,14 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = unit0; u < tiles.units && ok; u += tiles.step) {
-            const Unit w = unit_at(tiles, u);
+        for (int u = unit0; u < units && ok; u += unit_step) {
+            const Job& p = job_of<B_BY_K>(L, u);
+            const Unit w = unit_at<B_BY_K>(p, u);
             const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128, n = w.nt * BN + static_cast<int>(rank) * S::kRowsB;
+            const bool a_by_k = B_BY_K && p.a_by_k != 0;  // the forward product's operands both lie by row
             for (int ks = 0; ks < w.k_count; ++ks) {
                 if (!warp_wait(&b.empty[st], ph ^ 1u, abort)) {
-                    record_status(p.status, kStatusTimeoutProducer, abort);
+                    record_status(L.status, kStatusTimeoutProducer, abort);
                     ok = false;
                     break;
                 }
@@ -465,8 +506,8 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
                     uint8_t* dst = smem + st * S::kStage;
                     const uint32_t bar = PAIR ? mapa_shared(smem_addr(&b.full[st]), 0) : 0u;
                     const int k = (w.k_first + ks) * kStepK;  // past the matrix: zeros
-                    load_operand<PAIR, A_BY_K, 128>(dst, &map_a, &b.full[st], bar, m, k);
-                    load_operand<PAIR, B_BY_K, S::kRowsB>(dst + kTileA, &map_b, &b.full[st], bar, n, k);
+                    load_operand<PAIR, 128>(a_by_k, dst, &p.map_a, &b.full[st], bar, m, k);
+                    load_operand<PAIR, S::kRowsB>(B_BY_K, dst + kTileA, &p.map_b, &b.full[st], bar, n, k);
                 }
                 __syncwarp();
                 ++issued;
@@ -483,28 +524,30 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
                 const uint32_t par = static_cast<uint32_t>((fills - 1) & 1);
                 // the peer of a pair sees the MMAs release each slot, which needs its copies landed
                 if (!(leader ? mbar_wait(&b.full[s], par, nullptr) : mbar_wait(&b.empty[s], par, nullptr)))
-                    record_status(p.status, kStatusTimeoutDrain, abort);
+                    record_status(L.status, kStatusTimeoutDrain, abort);
             }
         }
     } else if (warp == kMmaWarp && leader) {
         // ------------------------------------------------------------ MMA
-        constexpr uint32_t idesc = idesc_bf16_f32(128 * kCtas, BN) | (A_BY_K ? 1u << 15 : 0u) | (B_BY_K ? 1u << 16 : 0u);
-        const uint32_t base0 = smem_addr(smem);
+                const uint32_t base0 = smem_addr(smem);
         int st = 0, local = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = unit0; u < tiles.units && ok; u += tiles.step, ++local) {
-            const Unit w = unit_at(tiles, u);
+        for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+            const Job& p = job_of<B_BY_K>(L, u);
+            const Unit w = unit_at<B_BY_K>(p, u);
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1) & 1u;
             if (!warp_wait_cluster(&b.tempty[buf], use ^ 1u, abort)) {
-                record_status(p.status, kStatusTimeoutMma, abort);
+                record_status(L.status, kStatusTimeoutMma, abort);
                 break;
             }
             tc_fence_after();
+            const bool a_by_k = B_BY_K && p.a_by_k != 0;
+            const uint32_t idesc = idesc_bf16_f32(128 * kCtas, BN) | (a_by_k ? 1u << 15 : 0u) | (B_BY_K ? 1u << 16 : 0u);
             for (int ks = 0; ks < w.k_count; ++ks) {
                 if (!warp_wait_cluster(&b.full[st], ph, abort)) {
-                    record_status(p.status, kStatusTimeoutMma, abort);
+                    record_status(L.status, kStatusTimeoutMma, abort);
                     ok = false;
                     break;
                 }
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= mmas) break;
-                        const uint64_t da = operand_desc<A_BY_K>(base, j), db = operand_desc<B_BY_K>(base + kTileA, j);
+                        const uint64_t da = operand_desc(a_by_k, base, j), db = operand_desc(B_BY_K, base + kTileA, j);
                         const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
                         if constexpr (PAIR) mma_bf16_pair(tmem + buf * BN, da, db, idesc, acc);
                         else mma_bf16(tmem + buf * BN, da, db, idesc, acc);
@@ -535,7 +578,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
         if (elect_one()) {
             if constexpr (PAIR) mma_commit_pair(b.drain, 1);
             else mma_commit(b.drain);
-            if (!mbar_wait_cluster(b.drain, 0, nullptr)) record_status(p.status, kStatusTimeoutDrain, abort);
+            if (!mbar_wait_cluster(b.drain, 0, nullptr)) record_status(L.status, kStatusTimeoutDrain, abort);
         }
     }
     __syncwarp();
@@ -551,7 +594,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1)
 
 // ---------------------------------------------------------------- parts of K
 // Four neighbouring outputs a thread: their parts in order, then the epilogue.
-__global__ void __launch_bounds__(256) linear_join_kernel(const GemmParams p) {
+__global__ void __launch_bounds__(256) linear_join_kernel(const GemmParams p, int splits) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int quads = (p.N + 3) / 4;
     const long long i = blockIdx.x * 256LL + threadIdx.x, m = i / quads;
@@ -561,7 +604,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const GemmParams p) {
     const long long step = static_cast<long long>(p.M) * quads;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int k = 0; k < p.splits; ++k) {
+    for (int k = 0; k < splits; ++k) {
         const float4 v = from[k * step];
         s.x += v.x;
         s.y += v.y;
@@ -614,25 +657,70 @@ bool encode_operand(CUtensorMap* map, const __nv_bfloat16* base, bool by_k, int 
                 : encode_matrix(map, base, rows, K, pitch, box_rows, kStepK, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool PAIR, int BN, bool A_BY_K, bool B_BY_K>
-cudaError_t launch_variant(const GemmParams& p, int num_sms, bool after_other, cudaStream_t stream) {
+template <bool PAIR, int BN>
+bool make_job(Job& j, const GemmParams& p, int splits, int first) {
+    using S = Shape<PAIR, BN>;
+    j.M = p.M;
+    j.N = p.N;
+    j.K = p.K;
+    j.splits = splits;
+    j.m_tiles = (p.M + 128 * S::kCtas - 1) / (128 * S::kCtas);
+    j.n_tiles = (p.N + BN - 1) / BN;
+    j.tiles = j.m_tiles * j.n_tiles;
+    j.ksteps = (p.K + kStepK - 1) / kStepK;
+    j.first = first;
+    j.a_by_k = p.a_by_k;
+    j.act = p.act;
+    j.bias = p.bias;
+    j.r = p.r;
+    j.y = p.y;
+    j.z = p.z;
+    if (!encode_operand(&j.map_a, p.a, p.a_by_k, p.M, p.K, p.a_pitch, 128) ||
+        !encode_operand(&j.map_b, p.b, p.b_by_k, p.N, p.K, p.b_pitch, S::kRowsB))
+        return false;
+    if (splits > 1) {
+        const cuuint64_t pitch = static_cast<cuuint64_t>(part_pitch(p.N)) * 4;
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(splits)};
+        const cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(p.M)};
+        const cuuint32_t box[3] = {32, 32, 1};
+        return encode_tiled(&j.map_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.part, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+    }
+    if (p.N % 8 != 0) return true;
+    const auto rows = [&](CUtensorMap* map, const void* base) {
+        return base == nullptr || encode_matrix(map, base, p.M, p.N, p.N, 32, kBlockCols, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    return rows(&j.map_y, p.y) && rows(&j.map_z, p.z) && rows(&j.map_r, p.r);
+}
+
+template <bool PAIR, int BN, bool B_BY_K, bool TMA>
+cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, const ColumnJoin& sums, int num_sms, bool after_other,
+                           cudaStream_t stream) {
     using S = Shape<PAIR, BN>;
     static SmemLimitCache limits;
-    auto* fn = linear_gemm_kernel<PAIR, BN, A_BY_K, B_BY_K>;
+    auto* fn = linear_gemm_kernel<PAIR, BN, B_BY_K, TMA>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 232448, limits);  // all that a block may have, once
     if (e != cudaSuccess) return e;
-    const long long units = (static_cast<long long>(p.M) + 128 * S::kCtas - 1) / (128 * S::kCtas) * ((p.N + BN - 1) / BN) * p.splits;
+    Launch L;
+    L.jobs = count;
+    L.units = 0;
+    L.join = sums;
+    L.status = p[0].status;
+    int longest = 0;
+    for (int i = 0; i < count; ++i) {
+        if (!make_job<PAIR, BN>(L.job[i], p[i], t.splits[i], L.units)) return cudaErrorInvalidValue;
+        L.units += L.job[i].tiles * t.splits[i];
+        longest = p[i].K > longest ? p[i].K : longest;
+    }
     const int slots = num_sms / S::kCtas;
     // Sixteen epilogue warps where units are short; their buffers cost a stage, which long ones miss (8192 x 4096 x 4096
     // 147 us with five stages, 142 with six).  Two groups where CTAs have several units; of 64 columns a group has all.
-    Ring ring;
-    ring.warps = p.K >= 1024 ? 8 : S::kEpilogueWarps;
-    ring.groups = BN == 64 || (units > slots && ring.warps == S::kEpilogueWarps) ? 2 : 1;
-    ring.stages = S::stages(ring.warps);
+    L.ring.warps = longest >= 1024 ? 8 : S::kEpilogueWarps;
+    L.ring.groups = BN == 64 || (L.units > slots && L.ring.warps == S::kEpilogueWarps) ? 2 : 1;
+    L.ring.stages = S::stages(L.ring.warps);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((units < slots ? units : slots) * S::kCtas));
+    cfg.gridDim = dim3(static_cast<unsigned>((L.units < slots ? L.units : slots) * S::kCtas));
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = ring.stages * S::kStage + ring.warps * kBlockBytes + S::kBarBytes;
+    cfg.dynamicSmemBytes = L.ring.stages * S::kStage + L.ring.warps * kBlockBytes + S::kBarBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     if (PAIR) {
@@ -648,48 +736,39 @@ cudaError_t launch_variant(const GemmParams& p, int num_sms, bool after_other, c
         ++cfg.numAttrs;
     }
     cfg.attrs = attr;
-    CUtensorMap a, b, y = CUtensorMap(), z = CUtensorMap(), r = CUtensorMap(), part = CUtensorMap();
-    bool made = encode_operand(&a, p.a, A_BY_K, p.M, p.K, p.a_pitch, 128) && encode_operand(&b, p.b, B_BY_K, p.N, p.K, p.b_pitch, S::kRowsB);
-    if (p.splits > 1) {
-        const cuuint64_t pitch = static_cast<cuuint64_t>(part_pitch(p.N)) * 4;
-        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(p.splits)};
-        const cuuint64_t strides[2] = {pitch, pitch * static_cast<cuuint64_t>(p.M)};
-        const cuuint32_t box[3] = {32, 32, 1};
-        made = made && encode_tiled(&part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.part, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
-    } else if (p.N % 8 == 0) {
-        const auto rows = [&](CUtensorMap* map, const void* base) {
-            return base == nullptr || encode_matrix(map, base, p.M, p.N, p.N, 32, kBlockCols, CU_TENSOR_MAP_SWIZZLE_128B);
-        };
-        made = made && rows(&y, p.y) && rows(&z, p.z) && rows(&r, p.r);
+    e = cudaLaunchKernelEx(&cfg, fn, L);
+    bool early = true;  // a second join comes behind the first, which lets nothing start early
+    for (int i = 0; i < count && e == cudaSuccess; ++i) {
+        if (t.splits[i] == 1) continue;
+        cudaLaunchConfig_t join = {};
+        const long long quads = static_cast<long long>(p[i].M) * ((p[i].N + 3) / 4);
+        join.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
+        join.blockDim = dim3(256);
+        join.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        join.attrs = attr;
+        join.numAttrs = early ? 1 : 0;
+        early = false;
+        e = cudaLaunchKernelEx(&join, linear_join_kernel, p[i], t.splits[i]);
     }
-    if (!made) return cudaErrorInvalidValue;
-    if ((e = cudaLaunchKernelEx(&cfg, fn, p, ring, a, b, y, z, r, part)) != cudaSuccess || p.splits == 1) return e;
-    cudaLaunchConfig_t join = {};
-    const long long quads = static_cast<long long>(p.M) * ((p.N + 3) / 4);
-    join.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
-    join.blockDim = dim3(256);
-    join.stream = stream;
-    cudaLaunchAttribute early[1];
-    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early[0].val.programmaticStreamSerializationAllowed = 1;
-    join.attrs = early;
-    join.numAttrs = 1;
-    return cudaLaunchKernelEx(&join, linear_join_kernel, p);
+    return e;
 }
 
-template <bool A_BY_K, bool B_BY_K>
-cudaError_t launch_operands(const GemmParams& p, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream) {
-    if (t.columns == 256) return launch_variant<true, 256, A_BY_K, B_BY_K>(p, num_sms, after_other, stream);
-    if (t.columns == 128) return launch_variant<false, 128, A_BY_K, B_BY_K>(p, num_sms, after_other, stream);
-    return launch_variant<false, 64, A_BY_K, B_BY_K>(p, num_sms, after_other, stream);
+template <bool B_BY_K, bool TMA>
+cudaError_t launch_shape(const GemmParams* p, int count, const GemmTile& t, const ColumnJoin& join, int num_sms, bool after_other,
+                            cudaStream_t stream) {
+    if (t.columns == 256) return launch_variant<true, 256, B_BY_K, TMA>(p, count, t, join, num_sms, after_other, stream);
+    if (t.columns == 128) return launch_variant<false, 128, B_BY_K, TMA>(p, count, t, join, num_sms, after_other, stream);
+    return launch_variant<false, 64, B_BY_K, TMA>(p, count, t, join, num_sms, after_other, stream);
 }
 
 }  // namespace
 
-bool gemm_fits(int M, int N) { return (static_cast<long long>(M) + 127) / 128 * ((N + 63) / 64) < (1LL << 30); }
+bool gemm_fits(int M, int N) { return (static_cast<long long>(M) + 127) / 128 * ((N + 63) / 64) < (1LL << 29); }
 
-size_t gemm_part_bytes(const GemmTile& t, int M, int N) {
-    return t.splits > 1 ? static_cast<size_t>(t.splits) * M * part_pitch(N) * sizeof(float) : 0;
+size_t gemm_part_bytes(int splits, int M, int N) {
+    return splits > 1 ? static_cast<size_t>(splits) * M * part_pitch(N) * sizeof(float) : 0;
 }
 
 // The tile shape and split of K that cost least by these figures, in microseconds on a 152-SM part (repeated launches in a
@@ -697,39 +776,63 @@ size_t gemm_part_bytes(const GemmTile& t, int M, int N) {
 // From one tile on every SM, K = 64 / 256 / 1024: 7.2 / 8.4 / 12.1 us of 256 x 256 on pairs, 5.4 / 6.3 / 9.2 of 128 x 128,
 // 5.0 / 5.7 / 8.5 of 128 x 64.  A split adds its parts' way through memory and the join: 2432 x 4096 -> 128 19.6 us in tiles of 128 x 128, 11.8
 // with the K of each shared by eight.
-GemmTile gemm_pick_tile(int M, int N, int K, int num_sms) {
+GemmTile gemm_pick_tile(const GemmSize* products, int count, int num_sms) {
     struct Cost {
         int rows, columns;
         double launch, step, besides, least;
     };
-    constexpr Cost kCosts[3] = {{256, 256, 5.9, 0.29, 1.0, 2.6}, {128, 128, 4.5, 0.235, 0.7, 1.3}, {128, 64, 4.2, 0.22, 0.6, 0.8}};
-    const long long steps = (K + kStepK - 1) / kStepK;
+    constexpr Cost kCosts[3] = {{256, 256, 5.9, 0.29, 1.0, 3.0}, {128, 128, 4.5, 0.235, 0.7, 2.0}, {128, 64, 4.2, 0.22, 0.6, 1.2}};
+    constexpr int kSplits[14] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64};
     double best = 0.0;
     GemmTile pick = {};
     for (const Cost& c : kCosts) {
-        const long long tiles = (static_cast<long long>(M) + c.rows - 1) / c.rows * ((N + c.columns - 1) / c.columns);
         const long long slots = c.rows == 256 ? num_sms / 2 : num_sms;
-        for (int splits = 1; splits <= 64 && splits <= steps; ++splits) {
-            if (splits > 1 && tiles * splits > slots) break;
-            const long long rounds = (tiles * splits + slots - 1) / slots;
-            const double each = static_cast<double>((steps + splits - 1) / splits) * c.step + c.besides;
-            const double join = splits > 1 ? 3.0 + static_cast<double>(M) * N * splits * 8.0 / 4e6 : 0.0;
-            const double cost = c.launch + static_cast<double>(rounds) * (each > c.least ? each : c.least) + join;
-            if (pick.rows == 0 || cost < best) {
-                best = cost;
-                pick = {c.rows, c.columns, splits};
+        const auto tiles = [&](const GemmSize& p) {
+            return (static_cast<long long>(p.M) + c.rows - 1) / c.rows * ((p.N + c.columns - 1) / c.columns);
+        };
+        const auto each = [&](const GemmSize& p, int splits) {
+            const long long steps = (static_cast<long long>(p.K) + kStepK - 1) / kStepK;
+            const double t = static_cast<double>((steps + splits - 1) / splits) * c.step + c.besides;
+            return t > c.least ? t : c.least;
+        };
+        const auto allowed = [&](const GemmSize& p, int splits) {
+            return splits == 1 || (splits <= (p.K + kStepK - 1) / kStepK && tiles(p) * splits <= slots);
+        };
+        const auto join = [&](const GemmSize& p, int splits) {
+            return splits > 1 ? 3.0 + static_cast<double>(p.M) * p.N * splits * 8.0 / 4e6 : 0.0;
+        };
+        for (int s0 : kSplits) {
+            if (!allowed(products[0], s0)) continue;
+            for (int s1 : kSplits) {
+                if (count == 1 ? s1 != 1 : !allowed(products[1], s1)) continue;
+                // units are dealt out in turn, the first product's before the second's: the CTA with most to do
+                const long long u0 = tiles(products[0]) * s0, u1 = count == 1 ? 0 : tiles(products[1]) * s1;
+                const double e0 = each(products[0], s0), e1 = count == 1 ? 0.0 : each(products[1], s1);
+                double longest = 0.0;
+                for (long long i = 0; i < slots; ++i) {
+                    const long long n0 = u0 > i ? (u0 - i - 1) / slots + 1 : 0, all = u0 + u1 > i ? (u0 + u1 - i - 1) / slots + 1 : 0;
+                    const double t = static_cast<double>(n0) * e0 + static_cast<double>(all - n0) * e1;
+                    longest = t > longest ? t : longest;
+                }
+                const double cost = c.launch + longest + join(products[0], s0) + (count == 1 ? 0.0 : join(products[1], s1));
+                if (pick.rows == 0 || cost < best) {
+                    best = cost;
+                    pick = {c.rows, c.columns, {s0, s1}};
+                }
             }
         }
     }
     return pick;
 }
 
-cudaError_t launch_gemm(const GemmParams& given, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream) {
-    GemmParams p = given;
-    p.splits = t.splits;
-    if (p.a_by_k && p.b_by_k) return launch_operands<true, true>(p, t, num_sms, after_other, stream);
-    if (p.b_by_k) return launch_operands<false, true>(p, t, num_sms, after_other, stream);
-    return launch_operands<false, false>(p, t, num_sms, after_other, stream);
+cudaError_t launch_gemm(const GemmParams* p, int count, const GemmTile& t, const ColumnJoin& join, int num_sms, bool after_other,
+                        cudaStream_t stream) {
+    const bool tma = p[0].N % 8 == 0;  // both products of a launch have the same N
+    if (p[0].b_by_k)
+        return tma ? launch_shape<true, true>(p, count, t, join, num_sms, after_other, stream)
+                   : launch_shape<true, false>(p, count, t, join, num_sms, after_other, stream);
+    return tma ? launch_shape<false, true>(p, count, t, join, num_sms, after_other, stream)
+               : launch_shape<false, false>(p, count, t, join, num_sms, after_other, stream);
 }
 
 }  // namespace convgb

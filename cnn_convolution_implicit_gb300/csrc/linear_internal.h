@@ -24,21 +24,31 @@ struct GemmParams {
     __nv_bfloat16* y;
     __nv_bfloat16* z;     // nullptr: not wanted
     float* part;          // workspace of parts of K: [splits][M][N rounded up to 4]
-    int splits;           // units that share the K of a tile
     unsigned* status;
 };
 
 // The tile of the tensor-core kernel: rows and columns (256 x 256 on a pair of SMs), and how many units share
-// its K.
+// its K, for each product of a launch.
 struct GemmTile {
-    int rows, columns, splits;
+    int rows, columns, splits[2];
 };
-GemmTile gemm_pick_tile(int M, int N, int K, int num_sms);
-size_t gemm_part_bytes(const GemmTile& t, int M, int N);
+struct GemmSize {
+    int M, N, K;
+};
+GemmTile gemm_pick_tile(const GemmSize* products, int count, int num_sms);  // count: 1 or 2
+size_t gemm_part_bytes(int splits, int M, int N);
 bool gemm_fits(int M, int N);  // tile counts within 32 bits
-// Rows of both operands start on 16 bytes.  after_other: the kernel before it on the stream wrote an
-// operand and lets this one start early.
-cudaError_t launch_gemm(const GemmParams& p, const GemmTile& t, int num_sms, bool after_other, cudaStream_t stream);
+
+// Sums over the rows that the kernel before a launch left in parts: added on the side (launch_join_columns' order).
+struct ColumnJoin {
+    const float* part;
+    float* out;  // nullptr: none
+    int parts, columns;
+};
+// One or two products of the same N in a launch.  Rows of their operands start on 16 bytes.  after_other: the kernel before it on the
+// stream wrote an operand and lets this one start early.
+cudaError_t launch_gemm(const GemmParams* p, int count, const GemmTile& t, const ColumnJoin& join, int num_sms, bool after_other,
+                        cudaStream_t stream);
 
 // The forward product with few rows: dense operands, rows anywhere.
 struct FewParams {
@@ -66,6 +76,7 @@ struct LinearGradParams {
     int act;
 };
 int linear_grad_parts(int M, int N, int num_sms);
-cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, cudaStream_t stream);
+// join: the parts too; else dbias is complete only where linear_grad_parts is 1.
+cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, bool join, cudaStream_t stream);
 
 }  // namespace convgb
