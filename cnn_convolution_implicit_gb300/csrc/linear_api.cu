@@ -71,7 +71,8 @@ Workspace backward_space(const conv_linear_plan* pl) {
     ws.w = lay_out ? rows_bytes(pl->M, pl->K) : 0;
     ws.u = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
     ws.sums = ws.u + (pl->act != CONV_ACT_NONE || pl->N % 8 != 0 ? rows_bytes(pl->M, pl->N) : 0);
-    ws.part = ws.sums + up(static_cast<size_t>(linear_grad_parts(pl->M, pl->N, pl->num_sms)) * pl->N * sizeof(float), 256);
+    const int sums = linear_grad_parts(pl->M, pl->N, pl->num_sms);
+    ws.part = ws.sums + (sums > 1 ? up(static_cast<size_t>(sums) * pl->N * sizeof(float), 256) : 0);
     ws.part2 = ws.part + up(gemm_part_bytes(pl->backward.splits[pl->dw_first ? 1 : 0], pl->M, pl->K), 256);  // dw's, behind dx's
     ws.bytes = ws.part2 + gemm_part_bytes(pl->backward.splits[pl->dw_first ? 0 : 1], pl->N, pl->K);
     return ws;
@@ -179,14 +180,14 @@ conv_status conv_linear_forward(conv_linear_plan* pl, const void* x, const void*
 conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const void* x, const void* w, const void* z,
                                  void* dx, void* dw, float* dbias, void* workspace, void* stream) {
     if (pl == nullptr || dy == nullptr || (dx == nullptr && dw == nullptr && dbias == nullptr) ||
-        (dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) || (pl->act != CONV_ACT_NONE && z == nullptr) ||
-        workspace == nullptr)
+        (dx != nullptr && w == nullptr) || (dw != nullptr && x == nullptr) || (pl->act != CONV_ACT_NONE && z == nullptr))
         return CONV_ERR_INVALID_ARG;
+    const Workspace ws = backward_space(pl);
+    if (workspace == nullptr && ws.bytes != 0) return CONV_ERR_INVALID_ARG;
     if (!all_aligned16(dy, x, w, z, dx, dw, dbias, workspace)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Workspace ws = backward_space(pl);
     uint8_t* base = static_cast<uint8_t*>(workspace);
     const bool products = dx != nullptr || dw != nullptr;
     const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(dy);

@@ -1,0 +1,39 @@
+// rms_math.cuh -- what the kernels of the root-mean-square norm share.
+#pragma once
+
+#include "pointwise_math.cuh"
+#include "ptx.cuh"
+
+namespace convgb {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
+    return v;
+}
+
+__device__ __forceinline__ float reciprocal_root(float sum, int C, float eps) {
+    return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(C)), eps));
+}
+
+// Streaming forms: kStreamWarps warps take rows from a ring in shared memory, eight rows of one warp each or one row
+// of all of them at a time.
+constexpr int kStreamWarps = 8, kStreamMaxStages = 8;
+
+struct Stream {
+    int stages, stage_bytes;
+    int rows;  // of a stage
+};
+
+// Rows of a stage: one where all warps share it, else as many for each warp as 24 KB hold, while the CTAs (`ctas`) have two
+// turns at least.
+inline int stream_rows(int M, int warps, int tensors, long long row_bytes, int ctas) {
+    if (warps > 1) return 1;
+    long long each = 24 * 1024 / (kStreamWarps * tensors * row_bytes), most = M / (2LL * kStreamWarps * ctas);
+    if (each > most) each = most;
+    return kStreamWarps * static_cast<int>(each < 1 ? 1 : (each > 16 ? 16 : each));
+}
+
+__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+}  // namespace convgb

@@ -7,17 +7,17 @@
 // Bound by memory.  A row stays in the registers of the 1, 4, 8 or 16 warps that hold it, so every byte
 // crosses the bus once; rows past what 16 warps hold are swept twice (three times to 8 bits).
 //
-// A row starts at any element.  It is handled as the aligned 16-byte granules that it touches: all tensors
-// of a call have the same shape, so a row begins at the same place of a granule in each of them; the
-// first and last granule, shared with the neighbouring rows, are read and written by elements.
+// A row starts at any element.  Rows off 16 bytes of up to 8,192 values have kernels of their own (rms_elements.cu); longer
+// ones are handled here as the aligned 16-byte granules that they touch: all tensors of a call have the same shape, so
+// a row begins at the same place of a granule in each of them; the first and last granule, shared with the
+// neighbouring rows, are read and written by elements.
 //
-// dgamma: the backward pass of rows on 16 bytes keeps each thread's columns over all the rows that its CTA
-// takes; for other rows, whose threads' columns move from row to row, a kernel of its own reads dy and h by
-// column.  Either way parts of it meet in the workspace and are added in one order.
+// dgamma: a backward pass that streams rows through shared memory keeps each thread's columns over all the rows that its
+// CTA takes; for longer rows a kernel of its own reads dy and h by column.  Either way parts of it meet in the
+// workspace and are added in one order.
 #include <type_traits>
 
-#include "pointwise_math.cuh"
-#include "ptx.cuh"
+#include "rms_math.cuh"
 #include "rows_internal.h"
 
 namespace convgb {
@@ -103,12 +103,6 @@ private:
     }
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
-    return v;
-}
-
 // Over the WARPS warps of a row (a CTA, or one warp of it); `buf` is used once.
 template <int WARPS>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
@@ -136,11 +130,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
     return v;
 }
 
-__device__ __forceinline__ float reciprocal_root(float sum, int C, float eps) {
-    return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(C)), eps));
-}
-
-constexpr int kStreamMaxStages = 8;
 constexpr int kRowsOfWarps = 4;  // rows of one warp each that a CTA takes
 template <int WARPS>
 constexpr int kThreadsOf = 32 * (WARPS == 1 ? kRowsOfWarps : WARPS);
@@ -326,21 +315,16 @@ __global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const R
 }
 
 // Rows on 16 bytes of at most 1,024 granules: a warp of its own brings them (dy, h and dh, whole rows, next to each other in
-// memory) by bulk copies into a ring in shared memory, eight rows of one warp each or one row of eight warps to a
-// stage.  Loads into registers left too few bytes under way between a row's barrier and the next row's first
+// memory) by bulk copies into a ring in shared memory, eight rows of one warp each (or a multiple) or one row of eight
+// warps to a stage.  Loads into registers left too few bytes under way between a row's barrier and the next row's first
 // load: 8192 x 4096 BF16 with dh 83 us so, 3.2 TB/s.
-constexpr int kStreamWarps = 8, kStreamThreads = 32 * (kStreamWarps + 1);
-
-struct Stream {
-    int stages, stage_bytes;
-};
-
-__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+constexpr int kStreamThreads = 32 * (kStreamWarps + 1);
 
 template <typename T, int ITEMS, int WARPS, bool DGAMMA>
 __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backward_stream_kernel(const RmsParams p, const Stream s) {
     using R = Row<T, true>;
-    constexpr int kRows = WARPS == 1 ? kStreamWarps : 1, kStride = 32 * WARPS;
+    constexpr int kStride = 32 * WARPS;
+    const int rows = WARPS > 1 ? 1 : s.rows;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t full[kStreamMaxStages], empty[kStreamMaxStages];
     __shared__ float sums[2][kStreamWarps];
@@ -357,7 +341,7 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
     }
     __syncthreads();
     const int row_bytes = p.C * static_cast<int>(sizeof(T));
-    const int groups = static_cast<int>((static_cast<long long>(p.M) + kRows - 1) / kRows);
+    const int groups = static_cast<int>((static_cast<long long>(p.M) + rows - 1) / rows);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == kStreamWarps) {
         if (lane != 0) return;
@@ -370,11 +354,11 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
                 record_status(p.status, kStatusTimeoutProducer, abort);
                 break;
             }
-            const long long m = static_cast<long long>(g) * kRows;
-            const int bytes = static_cast<int>(p.M - m < kRows ? p.M - m : kRows) * row_bytes, tensors = p.r != nullptr ? 3 : 2;
+            const long long m = static_cast<long long>(g) * rows;
+            const int bytes = static_cast<int>(p.M - m < rows ? p.M - m : rows) * row_bytes, tensors = p.r != nullptr ? 3 : 2;
             mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(tensors * bytes));
             for (int i = 0; i < tensors; ++i)
-                bulk_load(ring + st * s.stage_bytes + i * kRows * row_bytes, from[i] + m * row_bytes, bytes, &full[st]);
+                bulk_load(ring + st * s.stage_bytes + i * rows * row_bytes, from[i] + m * row_bytes, bytes, &full[st]);
             ++issued;
             if (++st == s.stages) {
                 st = 0;
@@ -398,48 +382,51 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
     int st = 0, turn = 0;
     uint32_t ph = 0;
     for (int g = blockIdx.x; g < groups; g += gridDim.x, turn ^= 1) {
-        const long long m = static_cast<long long>(g) * kRows + slot;
-        const bool live = m < p.M;
-        const float rstd = live ? __ldg(p.rstd + m) : 0.0f;
         if (!mbar_wait(&full[st], ph, abort)) record_status(p.status, kStatusTimeoutTransform, abort);  // and on: every wait ends
-        const uint4* dy = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + slot * row_bytes);
-        const uint4* h = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (kRows + slot) * row_bytes);
-        const uint4* dh = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (2 * kRows + slot) * row_bytes);
-        const f2 factor = f2_dup(rstd);
-        f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
+#pragma unroll 1
+        for (int at = slot; at < rows; at += kStreamWarps) {  // once, where all warps share a row
+            const long long m = static_cast<long long>(g) * rows + at;
+            if (m >= p.M) break;
+            const float rstd = __ldg(p.rstd + m);
+            const uint4* dy = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + at * row_bytes);
+            const uint4* h = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (rows + at) * row_bytes);
+            const uint4* dh = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (2 * rows + at) * row_bytes);
+            const f2 factor = f2_dup(rstd);
+            f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * kStride;
-            if (i >= vecs || !live) continue;
-            VecIo<T, R::V>::unpack(dy[i], d[k]);
-            VecIo<T, R::V>::unpack(h[i], n[k]);
+            for (int k = 0; k < ITEMS; ++k) {
+                const int i = t + k * kStride;
+                if (i >= vecs) continue;
+                VecIo<T, R::V>::unpack(dy[i], d[k]);
+                VecIo<T, R::V>::unpack(h[i], n[k]);
 #pragma unroll
-            for (int j = 0; j < R::H; ++j) {
-                n[k][j] = f2_mul(n[k][j], factor);
-                if constexpr (DGAMMA) total[k][j] = f2_fma(d[k][j], n[k][j], total[k][j]);
-                d[k][j] = f2_mul(d[k][j], gamma[k][j]);
-                dot = f2_fma(d[k][j], n[k][j], dot);
+                for (int j = 0; j < R::H; ++j) {
+                    n[k][j] = f2_mul(n[k][j], factor);
+                    if constexpr (DGAMMA) total[k][j] = f2_fma(d[k][j], n[k][j], total[k][j]);
+                    d[k][j] = f2_mul(d[k][j], gamma[k][j]);
+                    dot = f2_fma(d[k][j], n[k][j], dot);
+                }
             }
-        }
-        float sum = warp_sum(f2_lo(dot) + f2_hi(dot));
-        if constexpr (WARPS > 1) {
-            if (lane == 0) sums[turn][warp] = sum;
-            sync_consumers();
-            sum = 0.0f;
+            float sum = warp_sum(f2_lo(dot) + f2_hi(dot));
+            if constexpr (WARPS > 1) {
+                if (lane == 0) sums[turn][warp] = sum;
+                sync_consumers();
+                sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < WARPS; ++i) sum += sums[turn][i];
-        }
-        const f2 minus = f2_dup(-__fdiv_rn(sum, static_cast<float>(p.C)));
-        const R row(live ? m : 0, p.C);
+                for (int i = 0; i < WARPS; ++i) sum += sums[turn][i];
+            }
+            const f2 minus = f2_dup(-__fdiv_rn(sum, static_cast<float>(p.C)));
+            const R row(m, p.C);
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * kStride;
-            if (i >= vecs || !live) continue;
-            f2 r[R::H] = {};
-            if (p.r != nullptr) VecIo<T, R::V>::unpack(dh[i], r);
+            for (int k = 0; k < ITEMS; ++k) {
+                const int i = t + k * kStride;
+                if (i >= vecs) continue;
+                f2 r[R::H] = {};
+                if (p.r != nullptr) VecIo<T, R::V>::unpack(dh[i], r);
 #pragma unroll
-            for (int j = 0; j < R::H; ++j) d[k][j] = f2_fma(f2_fma(n[k][j], minus, d[k][j]), factor, r[j]);
-            row.store(p.y, i, d[k]);
+                for (int j = 0; j < R::H; ++j) d[k][j] = f2_fma(f2_fma(n[k][j], minus, d[k][j]), factor, r[j]);
+                row.store(p.y, i, d[k]);
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
@@ -579,7 +566,8 @@ cudaError_t forward(const RmsParams& p, cudaStream_t stream) {
     } else {
         by_form(f, [&](auto items, auto warps) {
             constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
-            rms_forward_kernel<T, ALIGNED, I, W, INT8><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+            if constexpr (ALIGNED || (W == 16 && sizeof(T) == 2))  // other rows off 16 bytes go by elements or are longer
+                rms_forward_kernel<T, ALIGNED, I, W, INT8><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
         });
     }
     return cudaGetLastError();
@@ -598,16 +586,22 @@ StreamForm stream_form(const RmsParams& p) {
     return {items, warps, items == 4 ? 1 : 2};
 }
 
+int stream_rows_of(const RmsParams& p, const StreamForm& f, int num_sms) {
+    return stream_rows(p.M, f.warps, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), f.ctas * num_sms);
+}
+
 int stream_ctas(const RmsParams& p, const StreamForm& f, int num_sms) {
-    const int rows = f.warps == 1 ? kStreamWarps : 1;
+    const int rows = stream_rows_of(p, f, num_sms);
     const long long need = (static_cast<long long>(p.M) + rows - 1) / rows, most = static_cast<long long>(f.ctas) * num_sms;
+    if (need <= 4) return 1;  // a turn takes a microsecond, a join of parts and its launch four
     return static_cast<int>(need < most ? need : most);
 }
 
 template <typename T, int ITEMS, int WARPS>
 cudaError_t stream_launch(const RmsParams& p, const StreamForm& f, cudaStream_t stream) {
     Stream s;
-    s.stage_bytes = 3 * p.C * static_cast<int>(sizeof(T)) * (WARPS == 1 ? kStreamWarps : 1);
+    s.rows = p.rows;
+    s.stage_bytes = 3 * p.C * static_cast<int>(sizeof(T)) * s.rows;
     const int room = (f.ctas == 2 ? 113 : 226) * 1024 - 1024;  // of shared memory, barriers aside
     s.stages = room / s.stage_bytes < kStreamMaxStages ? room / s.stage_bytes : kStreamMaxStages;
     int bytes = s.stages * s.stage_bytes;
@@ -635,11 +629,12 @@ cudaError_t stream_backward(const RmsParams& p, const StreamForm& f, cudaStream_
 
 template <typename T, bool ALIGNED>
 cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
+    const bool join = p.dgamma != nullptr && p.parts > 1;
     const StreamForm sf = stream_form(p);
     const Form f = pick_form(p);
     if (ALIGNED && sf.warps != 0) {
         const cudaError_t e = stream_backward<T>(p, sf, stream);
-        if (e != cudaSuccess || p.dgamma == nullptr) return e;
+        if (e != cudaSuccess || !join) return e;
         return launch_join_columns(p.part, p.parts, p.C, p.dgamma, true, stream);
     }
     if (p.dgamma != nullptr)  // first: dx may be dy
@@ -649,19 +644,25 @@ cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
     } else {
         by_form(f, [&](auto items, auto warps) {
             constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
-            if constexpr (!ALIGNED || W == 16) rms_backward_kernel<T, ALIGNED, I, W><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+            if constexpr (W == 16 && (ALIGNED || sizeof(T) == 2)) rms_backward_kernel<T, ALIGNED, I, W><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
         });
     }
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.dgamma == nullptr) return e;
+    if (e != cudaSuccess || !join) return e;
     return launch_join_columns(p.part, p.parts, p.C, p.dgamma, false, stream);
 }
 
 }  // namespace
 
 void rms_plan_backward(RmsParams& p, int num_sms) {
+    if (rms_by_elements(p)) {
+        p.ctas = 2 * num_sms;
+        p.parts = rms_element_parts(p);
+        return;
+    }
     const StreamForm f = stream_form(p);
     if (f.warps != 0) {
+        p.rows = stream_rows_of(p, f, num_sms);
         p.ctas = p.parts = stream_ctas(p, f, num_sms);
         return;
     }
@@ -672,6 +673,7 @@ void rms_plan_backward(RmsParams& p, int num_sms) {
 }
 
 cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream) {
+    if (rms_by_elements(p)) return launch_rms_elements(p, false, stream);
     const bool aligned = aligned_rows(p);
     const auto run = [&](auto element) {
         using T = decltype(element);
@@ -681,7 +683,14 @@ cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream) {
     return p.bf16 ? run(__nv_bfloat16()) : run(float());
 }
 
-cudaError_t launch_rms_backward(const RmsParams& p, cudaStream_t stream) {
+cudaError_t launch_rms_backward(const RmsParams& given, cudaStream_t stream) {
+    RmsParams p = given;
+    if (p.parts == 1) p.part = p.dgamma;
+    if (rms_by_elements(p)) {
+        const cudaError_t e = launch_rms_elements(p, true, stream);
+        if (e != cudaSuccess || p.dgamma == nullptr || p.parts == 1) return e;
+        return launch_join_columns(p.part, p.parts, p.C, p.dgamma, true, stream);
+    }
     if (p.bf16) return aligned_rows(p) ? backward<__nv_bfloat16, true>(p, stream) : backward<__nv_bfloat16, false>(p, stream);
     return aligned_rows(p) ? backward<float, true>(p, stream) : backward<float, false>(p, stream);
 }

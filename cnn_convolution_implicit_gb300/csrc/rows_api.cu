@@ -47,6 +47,10 @@ conv_status sm_count(int& sms) {
     return CONV_ERR_CUDA;
 }
 
+unsigned long long part_bytes(const conv_rms_norm_plan* pl) {
+    return pl->rp.parts > 1 ? static_cast<unsigned long long>(pl->rp.parts) * pl->rp.C * sizeof(float) : 0;
+}
+
 conv_status launched(cudaError_t e) {
     if (e == cudaSuccess) return CONV_OK;
     cudaGetLastError();
@@ -109,7 +113,7 @@ conv_status conv_rms_norm_plan_create(conv_rms_norm_plan** out, int M, int C, fl
 
 conv_status conv_rms_norm_workspace(const conv_rms_norm_plan* p, unsigned long long* backward) {
     if (p == nullptr) return CONV_ERR_INVALID_ARG;
-    if (backward != nullptr) *backward = static_cast<unsigned long long>(p->rp.parts) * p->rp.C * sizeof(float);
+    if (backward != nullptr) *backward = part_bytes(p);
     return CONV_OK;
 }
 
@@ -129,7 +133,7 @@ conv_status conv_rms_norm_backward(conv_rms_norm_plan* pl, const void* dy, const
                                    const float* gamma, const void* dh, void* dx, float* dgamma, void* workspace,
                                    void* stream) {
     if (pl == nullptr || dy == nullptr || h == nullptr || rstd == nullptr || dx == nullptr ||
-        (dgamma != nullptr && workspace == nullptr))
+        (dgamma != nullptr && workspace == nullptr && part_bytes(pl) != 0))
         return CONV_ERR_INVALID_ARG;
     if (!all_aligned16(dy, h, rstd, gamma, dh, dx, dgamma, workspace)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);

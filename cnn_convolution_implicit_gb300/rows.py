@@ -98,7 +98,7 @@ class LinearPlan(_Plan):
         if z is not None:
             _need(z, "z", shape, _bf16, dev)
         if y is None:
-            y = _empty(shape, dtype=_bf16, device=dev)
+            y = _empty(shape, dtype=_bf16, device=dev) if residual is None else _empty_like(residual)
         else:
             _need(y, "y", shape, _bf16, dev)
         ws = _workspace(self._forward_bytes, dev) if self._forward_bytes else None
@@ -147,9 +147,9 @@ class LinearPlan(_Plan):
                     raise ValueError("%s is not written without need" % name)
                 _need(given, name, shape, dtype, dev)
         if dx is None and need_x:
-            dx = _empty(self._x, dtype=_bf16, device=dev)
+            dx = _empty(self._x, dtype=_bf16, device=dev) if x is None else _empty_like(x)
         if dw is None and need_w:
-            dw = _empty(self._w, dtype=_bf16, device=dev)
+            dw = _empty(self._w, dtype=_bf16, device=dev) if w is None else _empty_like(w)
         if dbias is None and need_b:
             dbias = _empty(self._cols, dtype=_f32, device=dev)
         ws = _workspace(self._backward_bytes, dev) if self._backward_bytes else None
@@ -283,7 +283,7 @@ class RmsNormPlan(_Plan):
                 dgamma = _empty(self._cols, dtype=_f32, device=dev)
             else:
                 _need(dgamma, "dgamma", self._cols, _f32, dev)
-            ws = _workspace(self._backward_bytes, dev)
+            ws = _workspace(self._backward_bytes, dev) if self._backward_bytes else None
         elif dgamma is not None:
             raise ValueError("dgamma is not written without gamma_grad")
         status = self._backward(self._plan, dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), _ptr(gamma), _ptr(dh), dx.data_ptr(),

@@ -63,7 +63,9 @@ def test_null_and_misaligned_pointers():
     assert q8(n._plan, A, None, None, None, A, None, None, None) == 1
     assert q8(n._plan, A, None, None, A + 8, A, None, None, None) == 3
     assert bwd(n._plan, A, A, None, None, None, A, None, A, None) == 1            # no rstd
-    assert bwd(n._plan, A, A, A, None, None, A, A, None, None) == 1               # dgamma without a workspace
+    many = cg.RmsNormPlan(4000, 32)
+    assert n.workspace_bytes["backward"] == 0 and many.workspace_bytes["backward"] > 0
+    assert bwd(many._plan, A, A, A, None, None, A, A, None, None) == 1            # dgamma without a workspace
     assert bwd(n._plan, A, A, A, None, None, A + 2, A, A, None) == 3
     p, a = cg.LinearPlan(400, 16, 32, "none"), cg.LinearPlan(400, 16, 32, "silu")
     f, b = L.conv_linear_forward, L.conv_linear_backward
