@@ -34,7 +34,7 @@ EXPORTS = ("conv_plan_create", "conv_plan_output_shape", "conv_plan_info", "conv
            "conv_int8_plan_device_status", "conv_int8_plan_destroy", "conv_quantize_rows",
            "conv_rms_norm_plan_create", "conv_rms_norm_workspace", "conv_rms_norm_forward", "conv_rms_norm_forward_int8",
            "conv_rms_norm_backward", "conv_rms_norm_plan_destroy", "conv_dropout", "conv_linear_plan_create",
-           "conv_linear_workspace", "conv_linear_forward", "conv_linear_backward", "conv_linear_plan_device_status",
+           "conv_linear_workspace", "conv_linear_plan_info", "conv_linear_forward", "conv_linear_backward", "conv_linear_plan_device_status",
            "conv_linear_plan_destroy")
 CONV_BLOCK_DW_RELU, CONV_BLOCK_PW_RELU = 1, 2
 
@@ -130,6 +130,7 @@ def lib():
             L.conv_dropout.argtypes = [vp, vp, c_int, c_ull, ctypes.c_double, vp, vp, vp]
             L.conv_linear_plan_create.argtypes = [ctypes.POINTER(vp)] + [c_int] * 4
             L.conv_linear_workspace.argtypes = [vp, ctypes.POINTER(c_ull), ctypes.POINTER(c_ull)]
+            L.conv_linear_plan_info.argtypes = [vp, vp]
             L.conv_linear_forward.argtypes = [vp] * 9
             L.conv_linear_backward.argtypes = [vp] * 10
             L.conv_linear_plan_device_status.argtypes = [vp, vp, ctypes.POINTER(c_int)]

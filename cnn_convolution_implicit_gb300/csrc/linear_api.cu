@@ -95,7 +95,7 @@ conv_status conv_linear_plan_create(conv_linear_plan** out, int M, int N, int K,
     if (M <= 0 || N <= 0 || K <= 0) return CONV_ERR_INVALID_ARG;
     if (act != CONV_ACT_NONE && act != CONV_ACT_RELU && act != CONV_ACT_SILU) return CONV_ERR_INVALID_ARG;
     const long long most = 1LL << 40;
-    const int side = 1 << 30;
+    const int side = 1 << 29;
     if (M >= side || N >= side || K >= side || static_cast<long long>(M) * K > most ||
         static_cast<long long>(N) * K > most || static_cast<long long>(M) * N > most)
         return CONV_ERR_UNSUPPORTED;
@@ -254,6 +254,22 @@ conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const voi
         tile.splits[0] = tile.splits[1];
     }
     return launched(launch_gemm(p, only < 0 ? 2 : 1, tile, join, pl->num_sms, early, st));
+}
+
+conv_status conv_linear_plan_info(const conv_linear_plan* p, conv_linear_info* info) {
+    if (p == nullptr || info == nullptr) return CONV_ERR_INVALID_ARG;
+    *info = conv_linear_info();
+    info->kernel = p->few ? CONV_LINEAR_FEW_ROWS : CONV_LINEAR_TILES;
+    if (!p->few) {
+        info->rows = p->forward.rows;
+        info->columns = p->forward.columns;
+        info->splits = p->forward.splits[0];
+    }
+    info->grad_rows = p->backward.rows;
+    info->grad_columns = p->backward.columns;
+    info->dx_splits = p->backward.splits[p->dw_first ? 1 : 0];
+    info->dw_splits = p->backward.splits[p->dw_first ? 0 : 1];
+    return CONV_OK;
 }
 
 conv_status conv_linear_plan_device_status(const conv_linear_plan* p, void* stream, int* code) {

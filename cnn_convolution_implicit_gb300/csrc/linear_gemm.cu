@@ -448,6 +448,12 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kern
                 bias.load(p.bias, n, p.N);
             }
             if (by_tma && blocks > 0) fetch(0);
+            const auto fetch_rows = [&](int i) {
+                move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + kBlockCols * i, p.M);
+                __syncwarp();
+            };
+            const bool by_rows = !TMA && !B_BY_K && p.splits == 1 && p.r != nullptr;
+            if (by_rows && blocks > 0) fetch_rows(0);
             if (!warp_wait_cluster(&b.tfull[buf], use, abort)) {
                 record_status(L.status, kStatusTimeoutEpilogue, abort);
                 ok = false;
@@ -462,12 +468,11 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kern
                         ok = false;
                     }
                     res_phase ^= 1u;
-                } else if (TMA && p.splits == 1) {
+                } else if (TMA ? p.splits == 1 : B_BY_K) {  // off 16 bytes too: the unit before may have left parts of the other product
                     if (lane == 0) bulk_wait_read_all();
                     __syncwarp();
-                } else if (!TMA && !B_BY_K && p.splits == 1 && p.r != nullptr && ok) {
-                    move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + kBlockCols * i, p.M);
-                    __syncwarp();
+                } else if (by_rows && i > 0 && ok) {
+                    fetch_rows(i);
                 }
                 if (!ok) continue;
                 if (!B_BY_K && i > 0) bias.load(p.bias, n + kBlockCols * i, p.N);

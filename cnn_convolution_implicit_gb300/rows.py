@@ -14,6 +14,9 @@ from .binding import CONV_BF16, CONV_F32, _plan_status, lib
 from .operators import ACTS, _DTYPES, _check, _choice, _need, _need_any, _ptr, _refuse_device, _torch, _torch_dtypes, _workspace
 
 
+LINEAR_KERNELS = {0: "few_rows", 1: "tiles"}
+
+
 def _start():
     """torch, and what every call takes from it."""
     global _t, _empty, _empty_like, _bf16, _f32
@@ -66,6 +69,11 @@ class LinearPlan(_Plan):
         if self._x.numel() != M * K or self._x[-1] != K:
             raise ValueError("x_shape must hold %d rows of %d" % (M, K))
         self._w, self._y, self._cols = torch.Size((N, K)), torch.Size(self._x[:-1] + (N,)), torch.Size((N,))
+        info = (ctypes.c_int * 8)()
+        _check(L.conv_linear_plan_info(h, info), "conv_linear_plan_info")
+        self.kernel = LINEAR_KERNELS[info[0]]
+        self.tile = tuple(info[1:4])       # rows, columns, units that share its K ("tiles" alone)
+        self.grad_tile = tuple(info[4:8])  # of the gradients: rows, columns, dx's and dw's units to a tile
         a, b = ctypes.c_ulonglong(), ctypes.c_ulonglong()
         _check(L.conv_linear_workspace(h, ctypes.byref(a), ctypes.byref(b)), "conv_linear_workspace")
         self.workspace_bytes = {"forward": a.value, "backward": b.value}

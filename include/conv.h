@@ -581,7 +581,7 @@ conv_status conv_rms_norm_backward(conv_rms_norm_plan *p, const void *dy, const 
                                    const float *gamma, const void *dh, void *dx, float *dgamma, void *workspace,
                                    void *stream);
 
-/* Free the plan.  NULL is accepted. */
+/* Free the plan.  NULL is accepted.  (Waits of its kernels that gave up show up in conv_device_status.) */
 conv_status conv_rms_norm_plan_destroy(conv_rms_norm_plan *p);
 
 /* ------------------------------------------------------------------------
@@ -627,7 +627,7 @@ typedef struct conv_linear_plan conv_linear_plan; /* opaque, host-owned */
 /*
  * Check the shape and choose the kernels.  *plan gets a new plan, or NULL on error.  Returns
  * CONV_ERR_INVALID_ARG for non-positive sizes or an unknown act, CONV_ERR_UNSUPPORTED for a
- * size from 2^30 on or above 2^40 elements of x, w or y, CONV_ERR_CUDA if the device cannot be
+ * size from 2^29 on or above 2^40 elements of x, w or y, CONV_ERR_CUDA if the device cannot be
  * queried.  Tied to the device current at creation; without a device a host-only plan is made,
  * whose calls return CONV_ERR_CUDA.
  */
@@ -659,6 +659,18 @@ conv_status conv_linear_forward(conv_linear_plan *p, const void *x, const void *
  */
 conv_status conv_linear_backward(conv_linear_plan *p, const void *dy, const void *x, const void *w, const void *z,
                                  void *dx, void *dw, float *dbias, void *workspace, void *stream);
+
+/* The kernels that the plan's calls run (host-side, as conv_plan_info; any pointer may be NULL). */
+typedef enum {
+    CONV_LINEAR_FEW_ROWS = 0,  /* w read once, BF16 MMA from registers                            */
+    CONV_LINEAR_TILES = 1      /* tcgen05 tiles of rows x columns (256 x 256 on a pair of SMs), the K of each
+                                  shared by `splits` units; 0 for the other kernel                */
+} conv_linear_kernel;
+typedef struct {
+    int kernel, rows, columns, splits;                       /* the forward product          */
+    int grad_rows, grad_columns, dx_splits, dw_splits;       /* the gradients' products: tiles */
+} conv_linear_info;
+conv_status conv_linear_plan_info(const conv_linear_plan *p, conv_linear_info *info);
 
 /* Status word of the plan (waits that gave up): the contract of conv_plan_device_status. */
 conv_status conv_linear_plan_device_status(const conv_linear_plan *p, void *stream, int *code);

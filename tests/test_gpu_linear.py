@@ -30,7 +30,16 @@ SIZES = [
     (16, 512, 512), (17, 200, 4104), (31, 77, 333), (32, 256, 2048), (33, 130, 264), (48, 96, 640), (64, 256, 96), (65, 4096, 512),
     (127, 128, 64), (128, 128, 128), (129, 257, 127), (200, 320, 320), (256, 2048, 1024), (301, 777, 1000), (513, 512, 256),
     (1000, 96, 2048), (1000, 1003, 72), (2000, 2050, 520), (3136, 512, 256), (5000, 1000, 200), (40000, 64, 72), (7, 20000, 128),
+    # each tile, whole and with its K shared, rows of y on and off 16 bytes
+    (443, 2728, 36), (4603, 271, 32), (42, 432, 10952), (37, 3206, 1835), (4785, 1624, 40), (4639, 1956, 32), (130, 3504, 7040),
+    (3652, 129, 5960), (34, 34, 1089), (62, 32, 1072),
 ]
+
+GRAD_SIZES = [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 520), (77, 264, 520), (301, 777, 1000),
+              (1000, 96, 48), (129, 257, 127), (2000, 512, 256), (5000, 64, 40), (300, 1024, 2048), (20000, 130, 72),
+              # each tile, whole, with the K of dx, of dw or of both shared
+              (49, 48, 5304), (39, 32, 6635), (4210, 32, 226), (34, 1984, 518), (705, 33, 8624), (758, 33, 8748),
+              (2246, 57, 2792), (58, 3120, 1922), (1198, 36, 32), (34, 1216, 36), (2549, 3552, 39), (1397, 52, 42)]
 
 
 @pytest.mark.parametrize("size", SIZES)
@@ -74,8 +83,7 @@ def test_every_epilogue(size, act):
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu"])
-@pytest.mark.parametrize("size", [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 520), (77, 264, 520), (301, 777, 1000),
-                                  (1000, 96, 48), (129, 257, 127), (2000, 512, 256), (5000, 64, 40), (300, 1024, 2048), (20000, 130, 72)])
+@pytest.mark.parametrize("size", GRAD_SIZES)
 def test_backward(size, act):
     import cnn_convolution_implicit_gb300 as cg
     M, N, K = size
@@ -303,3 +311,89 @@ def test_arguments_that_nobody_else_holds():
         grads = cg.linear_backward(keep[4], keep[0], keep[1], want, "silu")
         again = cg.linear_backward(keep[4].clone(), keep[0].clone(), keep[1].clone(), want.clone(), "silu")
         assert all(torch.equal(p, q) for p, q in zip(grads, again))
+
+
+def test_output_past_2_31_elements():
+    import cnn_convolution_implicit_gb300 as cg
+    for N in (8192, 8191):          # by bulk stores and by elements
+        M = (1 << 31) // N + 300
+        x, w, b, _, _ = _inputs(300, N, 64, 101)
+        xs = torch.zeros(M, 64, device="cuda", dtype=BF16)
+        xs[-300:] = x.cuda()
+        y = cg.linear(xs, w.cuda(), b.cuda(), "relu")
+        (want, tol), _ = ref.linear(_np(x), _np(w), _np(b), None, "relu")
+        oref.check(_np(y[-300:]), want, tol, True, "y")
+        assert torch.equal(y[0], torch.relu(b.cuda()).to(BF16)) and torch.equal(y[M // 2], y[0])
+        # gradients of as many values: rows of zeros but for the last 300
+        y.zero_()
+        y[-300:] = torch.randn(300, N, generator=torch.Generator().manual_seed(7)).to(BF16).cuda()
+        dy = y[-300:].cpu()
+        dx, dw, db = cg.linear_backward(y, xs, w.cuda())
+        (wx, tx), (ww, tw), (wb, tb) = ref.linear_backward(_np(dy), _np(x), _np(w), None, "none")
+        oref.check(_np(dx[-300:]), wx, tx, True, "dx")
+        oref.check(_np(dw), ww, tw, True, "dw")
+        oref.check(_np(db), wb, tb, False, "dbias")
+        assert not torch.any(dx[:1000])
+        del y, dx
+
+
+def test_a_captured_training_step():
+    """Forward and backward of a whole branch in one graph, its plans made inside the capture, replayed on new inputs:
+    the same as eager steps."""
+    import cnn_convolution_implicit_gb300 as cg
+    M, C, F = 150, 136, 264
+    x0, w1, b1, _, _ = _inputs(M, F, C, 111)
+    _, w2, b2, _, dy0 = _inputs(M, C, F, 112)
+    params = [t.cuda().requires_grad_(True) for t in (w1, b1, w2, b2, torch.ones(C))]
+    x, dy = x0.cuda().requires_grad_(True), dy0.cuda()
+    state = torch.tensor([1, 0], device="cuda")
+
+    def step(x, dy):
+        n = cg.rms_norm(x, params[4])
+        y = cg.dropout(cg.linear(cg.linear(n, params[0], params[1], "silu"), params[2], params[3]), 0.1, state, residual=x)
+        return torch.autograd.grad(y, [x, *params], dy)
+
+    side = torch.cuda.Stream()          # torch's warm-up; other shapes, so that the capture makes its own plans
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x[:40].detach().requires_grad_(True), dy[:40])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = step(x, dy)
+        state[1] += 1
+    for offset in range(2):
+        fresh = torch.randn(M, C, generator=torch.Generator().manual_seed(offset)).to(BF16).cuda()
+        with torch.no_grad():
+            x.copy_(fresh)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [g.clone() for g in grads]
+        state.copy_(torch.tensor([1, offset]))
+        want = step(fresh.requires_grad_(True), dy)
+        state[1] += 1
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert cg.device_status() == 0
+
+
+def test_two_streams_at_once():
+    """Products that share a K and norms that join parts, on two streams at the same time, many times over."""
+    import cnn_convolution_implicit_gb300 as cg
+    x, w, b, r, dy = (t.cuda() for t in _inputs(130, 250, 5000, 121))
+    h, gamma = torch.randn(3000, 1003, device="cuda").to(BF16), torch.ones(1003, device="cuda")
+    rstd = torch.rand(3000, device="cuda") + 0.5
+
+    def work():
+        return [cg.linear(x, w, b, "silu", r), *cg.linear_backward(dy, x, w), *cg.rms_norm_backward(h, h, rstd, gamma),
+                cg.rms_norm(h, gamma, h)[0]]
+
+    want = work()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(20):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(work())
+    torch.cuda.synchronize()
+    for one in got:
+        assert all(torch.equal(p, q) for p, q in zip(want, one))

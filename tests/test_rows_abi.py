@@ -31,9 +31,9 @@ def test_rms_norm_create(args, status):
 
 
 @pytest.mark.parametrize("args,status", [
-    ((0, 8, 8, 0), 1), ((8, 0, 8, 0), 1), ((8, 8, -1, 0), 1), ((8, 8, 8, 3), 1), ((1 << 30, 8, 8, 0), 2), ((8, 1 << 30, 8, 0), 2),
-    ((8, 8, 1 << 30, 0), 2), (((1 << 30) - 1, 8, 2048, 0), 2), (((1 << 30) - 1, 2048, 8, 0), 2), ((1, 1, 1, 2), 0),
-    ((1, 1 << 20, 1 << 20, 1), 0),
+    ((0, 8, 8, 0), 1), ((8, 0, 8, 0), 1), ((8, 8, -1, 0), 1), ((8, 8, 8, 3), 1), ((1 << 29, 8, 8, 0), 2), ((8, 1 << 29, 8, 0), 2),
+    ((8, 8, 1 << 29, 0), 2), (((1 << 29) - 1, 8, 4096, 0), 2), (((1 << 29) - 1, 4096, 8, 0), 2), ((1, 1, 1, 2), 0),
+    ((1, 1 << 20, 1 << 20, 1), 0), (((1 << 29) - 1, 1, 1, 0), 0), ((1, (1 << 29) - 1, 1, 0), 0), ((1, 1, (1 << 29) - 1, 0), 0),
 ])
 def test_linear_create(args, status):
     L = cg.lib()
@@ -68,6 +68,7 @@ def test_null_and_misaligned_pointers():
     assert bwd(many._plan, A, A, A, None, None, A, A, None, None) == 1            # dgamma without a workspace
     assert bwd(n._plan, A, A, A, None, None, A + 2, A, A, None) == 3
     p, a = cg.LinearPlan(400, 16, 32, "none"), cg.LinearPlan(400, 16, 32, "silu")
+    assert L.conv_linear_plan_info(None, A) == 1 and L.conv_linear_plan_info(p._plan, None) == 1
     f, b = L.conv_linear_forward, L.conv_linear_backward
     ws = A if p.workspace_bytes["forward"] else None
     assert f(None, A, A, None, None, A, None, A, None) == 1
@@ -161,3 +162,30 @@ def test_tensors_of_another_device_are_refused(name, monkeypatch):
 ])
 def test_the_oracles_generator(counter, key, want):
     assert [int(v) for v in ref.philox([np.array(c) for c in counter], key)] == list(want)
+
+
+def _variants():
+    """The kernels and tiles that the GPU tests' sizes run (the plans choose alike without a device)."""
+    from test_gpu_linear import GRAD_SIZES, SIZES
+    forward, grads = set(), set()
+    for M, N, K in SIZES:
+        p = cg.LinearPlan(M, N, K)
+        forward.add((p.kernel, p.tile[1], p.tile[2] > 1, N % 8 == 0, K % 8 == 0))
+    for M, N, K in GRAD_SIZES:
+        rows_, cols, dx, dw = cg.LinearPlan(M, N, K).grad_tile
+        grads.add((cols, dx > 1, dw > 1, K % 8 == 0))
+    return forward, grads
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="counted for 152 SMs")
+def test_the_gpu_tests_reach_every_kernel():
+    forward, grads = _variants()
+    for aligned in (True, False):
+        assert any(f[0] == "few_rows" and f[4] == aligned for f in forward)
+        for columns in (64, 128, 256):
+            for split in (True, False):
+                if (columns, split) != (256, True):      # pairs share a K rarely: once is enough
+                    assert any(f[0] == "tiles" and f[1:4] == (columns, split, aligned) for f in forward), (columns, split, aligned)
+            assert any(g[0] == columns and g[3] == aligned for g in grads), (columns, aligned)
+    assert any(f[1:3] == (256, True) for f in forward)
+    assert any(g[1] and not g[2] for g in grads) and any(g[2] and not g[1] for g in grads) and any(g[1] and g[2] for g in grads)
