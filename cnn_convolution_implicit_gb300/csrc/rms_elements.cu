@@ -284,7 +284,7 @@ cudaError_t launch(const RmsParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int tensors = (kBack ? 2 : 1) + (p.r != nullptr ? 1 : 0);
     Stream s;
-    s.rows = stream_rows(p.M, WARPS, kBack ? 3 : 2, static_cast<long long>(p.C) * sizeof(T), p.ctas);
+    s.rows = stream_rows(p.M, WARPS == 1 ? kStreamWarps : 1, kBack ? 3 : 2, static_cast<long long>(p.C) * sizeof(T), p.ctas);
     s.stage_bytes = tensors * ((s.rows * p.C * static_cast<int>(sizeof(T)) + 14 + 15) & ~15);
     s.stages = 112 * 1024 / s.stage_bytes;  // two CTAs an SM
     if (s.stages == 0) s.stages = 225 * 1024 / s.stage_bytes;
@@ -319,7 +319,7 @@ cudaError_t by_mode(const RmsParams& p, bool backward, cudaStream_t stream) {
 bool rms_by_elements(const RmsParams& p) { return p.C % (p.bf16 ? 8 : 4) != 0 && p.C <= 8192; }
 
 int rms_element_parts(const RmsParams& p) {
-    const int rows = stream_rows(p.M, form_of(p.C).warps, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), p.ctas);
+    const int rows = stream_rows(p.M, form_of(p.C).warps == 1 ? kStreamWarps : 1, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), p.ctas);
     const long long need = (static_cast<long long>(p.M) + rows - 1) / rows;
     if (need <= 4) return 1;  // as rms_plan_backward
     return static_cast<int>(need < p.ctas ? need : p.ctas);

@@ -16,8 +16,8 @@ __device__ __forceinline__ float reciprocal_root(float sum, int C, float eps) {
     return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(C)), eps));
 }
 
-// Streaming forms: kStreamWarps warps take rows from a ring in shared memory, eight rows of one warp each or one row
-// of all of them at a time.
+// Streaming forms: kStreamWarps warps take rows from a ring in shared memory, several rows or one row of all of them at a
+// time.
 constexpr int kStreamWarps = 8, kStreamMaxStages = 8;
 
 struct Stream {
@@ -25,13 +25,14 @@ struct Stream {
     int rows;  // of a stage
 };
 
-// Rows of a stage: one where all warps share it, else as many for each warp as 24 KB hold, while the CTAs (`ctas`) have two
-// turns at least.
-inline int stream_rows(int M, int warps, int tensors, long long row_bytes, int ctas) {
-    if (warps > 1) return 1;
-    long long each = 24 * 1024 / (kStreamWarps * tensors * row_bytes), most = M / (2LL * kStreamWarps * ctas);
-    if (each > most) each = most;
-    return kStreamWarps * static_cast<int>(each < 1 ? 1 : (each > 16 ? 16 : each));
+// Rows of a stage: one where all warps share it, else a multiple of those that they work on together (`at_once`), as many
+// as 24 KB hold while the CTAs have two turns at least.
+inline int stream_rows(int M, int at_once, int tensors, long long row_bytes, int ctas) {
+    if (at_once == 1) return 1;
+    long long times = 24 * 1024 / (at_once * tensors * row_bytes);
+    const long long most = M / (2LL * at_once * ctas);
+    if (times > most) times = most;
+    return at_once * static_cast<int>(times < 1 ? 1 : (times > 16 ? 16 : times));
 }
 
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }

@@ -4,8 +4,8 @@
 //   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * gamma
 //   n = h * rstd, d = dy * gamma:  dx = rstd * (d - n * mean(d * n)) + dh,  dgamma = sum over rows of dy * n
 //
-// Bound by memory.  A row stays in the registers of the 1, 4, 8 or 16 warps that hold it, so every byte
-// crosses the bus once; rows past what 16 warps hold are swept twice (three times to 8 bits).
+// Bound by memory.  A row stays in the registers of the 8 to 512 threads that hold it, so every byte
+// crosses the bus once; rows past what they hold are swept twice (three times to 8 bits).
 //
 // A row starts at any element.  Rows off 16 bytes of up to 8,192 values have kernels of their own (rms_elements.cu); longer
 // ones are handled here as the aligned 16-byte granules that they touch: all tensors of a call have the same shape, so
@@ -103,88 +103,99 @@ private:
     }
 };
 
-// Over the WARPS warps of a row (a CTA, or one warp of it); `buf` is used once.
-template <int WARPS>
+// Over the LANES threads of a row: a part of a warp, a warp, or a CTA; `buf` is used once.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int i = (LANES < 32 ? LANES : 32) / 2; i > 0; i >>= 1) v += __shfl_xor_sync(0xffffffffu, v, i);
+    return v;
+}
+
+template <int LANES>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
-    v = warp_sum(v);
-    if constexpr (WARPS > 1) {
+    v = lanes_sum<LANES>(v);
+    if constexpr (LANES > 32) {
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) v += buf[i];
+        for (int i = 0; i < LANES / 32; ++i) v += buf[i];
     }
     return v;
 }
 
-template <int WARPS>
+template <int LANES>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
-    v = warp_max(v);
-    if constexpr (WARPS > 1) {
+    if constexpr (LANES >= 32) {
+        v = warp_max(v);
+    } else {
+#pragma unroll
+        for (int i = LANES / 2; i > 0; i >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, i));
+    }
+    if constexpr (LANES > 32) {
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0;
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) v = max(v, buf[i]);
+        for (int i = 0; i < LANES / 32; ++i) v = max(v, buf[i]);
     }
     return v;
 }
 
-constexpr int kRowsOfWarps = 4;  // rows of one warp each that a CTA takes
-template <int WARPS>
-constexpr int kThreadsOf = 32 * (WARPS == 1 ? kRowsOfWarps : WARPS);
-
-// This thread's place: its row, and where it starts among the row's threads.
-template <int WARPS>
-__device__ __forceinline__ int row_thread() { return WARPS == 1 ? threadIdx.x & 31 : threadIdx.x; }
+// A CTA: 128 threads where a warp or a part of one has a row, else a row's threads.
+template <int LANES>
+constexpr int kThreadsOf = LANES <= 32 ? 128 : LANES;
+template <int LANES>
+constexpr int kRowsOf = kThreadsOf<LANES> / LANES;
 
 // ---------------------------------------------------------------- forward
-template <typename T, bool ALIGNED, int ITEMS, int WARPS, bool INT8>
-__global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_forward_kernel(const RmsParams p) {
+template <typename T, bool ALIGNED, int ITEMS, int LANES, bool INT8>
+__global__ void __launch_bounds__(kThreadsOf<LANES>) rms_forward_kernel(const RmsParams p) {
     using R = Row<T, ALIGNED>;
-    __shared__ float sums[WARPS];
-    __shared__ uint32_t tops[WARPS];
-    const long long m = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kRowsOfWarps + (threadIdx.x >> 5) : blockIdx.x;
-    if (m >= p.M) return;  // whole warps of their own rows
-    const R row(m, p.C);
-    const int t = row_thread<WARPS>();
+    __shared__ float sums[LANES > 32 ? LANES / 32 : 1];
+    __shared__ uint32_t tops[LANES > 32 ? LANES / 32 : 1];
+    const long long m = static_cast<long long>(blockIdx.x) * kRowsOf<LANES> + threadIdx.x / LANES;
+    const bool live = m < p.M;
+    if (LANES >= 32 && !live) return;  // whole warps; a part of one stays for the others' shuffles
+    const R row(live ? m : 0, p.C);
+    const int t = threadIdx.x % LANES, count = live ? row.count : 0;
     f2 v[ITEMS][R::H], square = 0;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = t + k * 32 * WARPS;
+        const int i = t + k * LANES;
 #pragma unroll
         for (int j = 0; j < R::H; ++j) v[k][j] = 0;
-        if (i < row.count) row.load(p.x, i, v[k]);
+        if (i < count) row.load(p.x, i, v[k]);
     }
     if (p.r != nullptr) {
         f2 r[ITEMS][R::H];
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * 32 * WARPS;
+            const int i = t + k * LANES;
 #pragma unroll
             for (int j = 0; j < R::H; ++j) r[k][j] = 0;
-            if (i < row.count) row.load(p.r, i, r[k]);
+            if (i < count) row.load(p.r, i, r[k]);
         }
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * 32 * WARPS;
+            const int i = t + k * LANES;
 #pragma unroll
             for (int j = 0; j < R::H; ++j) v[k][j] = f2_add(v[k][j], r[k][j]);
-            if (p.h != nullptr && i < row.count) row.store(p.h, i, v[k]);
+            if (p.h != nullptr && i < count) row.store(p.h, i, v[k]);
         }
     }
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
 #pragma unroll
         for (int j = 0; j < R::H; ++j) square = f2_fma(v[k][j], v[k][j], square);
-    const float rstd = reciprocal_root(row_sum<WARPS>(f2_lo(square) + f2_hi(square), sums), p.C, p.eps);
-    if (t == 0 && p.rstd != nullptr) p.rstd[m] = rstd;
+    const float rstd = reciprocal_root(row_sum<LANES>(f2_lo(square) + f2_hi(square), sums), p.C, p.eps);
+    if (t == 0 && live && p.rstd != nullptr) p.rstd[m] = rstd;
     const f2 factor = f2_dup(rstd);
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = t + k * 32 * WARPS;
-        if (i >= row.count) break;
+        const int i = t + k * LANES;
+        if (i >= count) break;
         f2 g[R::H];
         row.weights(p.gamma, i, g);
 #pragma unroll
@@ -195,18 +206,18 @@ __global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_forward_kernel(const Rm
         if constexpr (!INT8) row.store(p.y, i, v[k]);
     }
     if constexpr (INT8) {
-        const RowScale rs = row_scale(row_max<WARPS>(magnitude_bits(top), tops));
-        if (t == 0) p.scale[m] = rs.scale;
+        const RowScale rs = row_scale(row_max<LANES>(magnitude_bits(top), tops));
+        if (t == 0 && live) p.scale[m] = rs.scale;
         const RowFactor rf = row_factor(rs.inv);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * 32 * WARPS;
-            if (i < row.count) row.store8(p.q, i, v[k], rf);
+            const int i = t + k * LANES;
+            if (i < count) row.store8(p.q, i, v[k], rf);
         }
     }
 }
 
-// Rows that no 16 warps hold, swept again for every step.  h is written in the last sweep: it may be the
+// Rows that no 512 threads hold, swept again for every step.  h is written in the last sweep: it may be the
 // residual.
 constexpr int kLongWarps = 16, kLongThreads = 32 * kLongWarps;
 
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(const Rm
 #pragma unroll
         for (int j = 0; j < R::H; ++j) square = f2_fma(v[j], v[j], square);
     }
-    const float rstd = reciprocal_root(row_sum<kLongWarps>(f2_lo(square) + f2_hi(square), sums), p.C, p.eps);
+    const float rstd = reciprocal_root(row_sum<kLongThreads>(f2_lo(square) + f2_hi(square), sums), p.C, p.eps);
     if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[m] = rstd;
     const f2 factor = f2_dup(rstd);
     const auto norm_of = [&](int i, f2(&v)[R::H]) {
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(const Rm
 #pragma unroll
             for (int j = 0; j < R::H; ++j) top = magnitude(top, v[j]);
         }
-        rs = row_scale(row_max<kLongWarps>(magnitude_bits(top), tops));
+        rs = row_scale(row_max<kLongThreads>(magnitude_bits(top), tops));
         if (threadIdx.x == 0) p.scale[m] = rs.scale;
     }
 #pragma unroll 1
@@ -269,19 +280,19 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(const Rm
 
 // ---------------------------------------------------------------- backward
 // Rows in registers: those that the ring below does not take.
-template <typename T, bool ALIGNED, int ITEMS, int WARPS>
-__global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const RmsParams p) {
+template <typename T, bool ALIGNED, int ITEMS, int LANES>
+__global__ void __launch_bounds__(LANES) rms_backward_kernel(const RmsParams p) {
     using R = Row<T, ALIGNED>;
-    __shared__ float sums[WARPS];
-    const long long m = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kRowsOfWarps + (threadIdx.x >> 5) : blockIdx.x;
-    if (m >= p.M) return;  // whole warps of their own rows
-    const int t = row_thread<WARPS>();
+    static_assert(LANES > 32, "a CTA to a row");
+    __shared__ float sums[LANES / 32];
+    const long long m = blockIdx.x;
+    const int t = threadIdx.x;
     const R row(m, p.C);
     const f2 factor = f2_dup(p.rstd[m]);
     f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = t + k * 32 * WARPS;
+        const int i = t + k * LANES;
 #pragma unroll
         for (int j = 0; j < R::H; ++j) d[k][j] = n[k][j] = 0;
         if (i >= row.count) continue;
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const R
     }
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = t + k * 32 * WARPS;
+        const int i = t + k * LANES;
         if (i >= row.count) continue;
         f2 g[R::H];
         row.weights(p.gamma, i, g);
@@ -301,10 +312,10 @@ __global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const R
             dot = f2_fma(d[k][j], n[k][j], dot);
         }
     }
-    const f2 minus = f2_dup(-__fdiv_rn(row_sum<WARPS>(f2_lo(dot) + f2_hi(dot), sums), static_cast<float>(p.C)));
+    const f2 minus = f2_dup(-__fdiv_rn(row_sum<LANES>(f2_lo(dot) + f2_hi(dot), sums), static_cast<float>(p.C)));
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = t + k * 32 * WARPS;
+        const int i = t + k * LANES;
         if (i >= row.count) continue;
         f2 r[R::H] = {};
         if (p.r != nullptr) row.load(p.r, i, r);
@@ -315,16 +326,16 @@ __global__ void __launch_bounds__(kThreadsOf<WARPS>) rms_backward_kernel(const R
 }
 
 // Rows on 16 bytes of at most 1,024 granules: a warp of its own brings them (dy, h and dh, whole rows, next to each other in
-// memory) by bulk copies into a ring in shared memory, eight rows of one warp each (or a multiple) or one row of eight
-// warps to a stage.  Loads into registers left too few bytes under way between a row's barrier and the next row's first
+// memory) by bulk copies into a ring in shared memory, rows of 8, 16 or 32 lanes each, several to a stage, or one
+// row of all warps.  Loads into registers left too few bytes under way between a row's barrier and the next row's first
 // load: 8192 x 4096 BF16 with dh 83 us so, 3.2 TB/s.
 constexpr int kStreamThreads = 32 * (kStreamWarps + 1);
 
-template <typename T, int ITEMS, int WARPS, bool DGAMMA>
+template <typename T, int ITEMS, int LANES, bool DGAMMA>
 __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backward_stream_kernel(const RmsParams p, const Stream s) {
     using R = Row<T, true>;
-    constexpr int kStride = 32 * WARPS;
-    const int rows = WARPS > 1 ? 1 : s.rows;
+    constexpr int kAtOnce = 32 * kStreamWarps / LANES;  // rows that the warps work on together
+    const int rows = kAtOnce > 1 ? s.rows : 1;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ uint64_t full[kStreamMaxStages], empty[kStreamMaxStages];
     __shared__ float sums[2][kStreamWarps];
@@ -371,12 +382,12 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
         }
         return;
     }
-    const int t = row_thread<WARPS>(), slot = WARPS == 1 ? warp : 0, vecs = p.C / R::V;
+    const int t = threadIdx.x % LANES, slot = threadIdx.x / LANES, vecs = p.C / R::V;
     f2 gamma[ITEMS][R::H], total[DGAMMA ? ITEMS : 1][R::H] = {};
     const R first(0, p.C);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int i = t + k * kStride;
+        const int i = t + k * LANES;
         if (i < vecs) first.weights(p.gamma, i, gamma[k]);
     }
     int st = 0, turn = 0;
@@ -384,10 +395,10 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
     for (int g = blockIdx.x; g < groups; g += gridDim.x, turn ^= 1) {
         if (!mbar_wait(&full[st], ph, abort)) record_status(p.status, kStatusTimeoutTransform, abort);  // and on: every wait ends
 #pragma unroll 1
-        for (int at = slot; at < rows; at += kStreamWarps) {  // once, where all warps share a row
+        for (int at = slot; at < rows; at += kAtOnce) {  // rows is a multiple, 1 where all warps share a row
             const long long m = static_cast<long long>(g) * rows + at;
-            if (m >= p.M) break;
-            const float rstd = __ldg(p.rstd + m);
+            const bool live = m < p.M;  // a dead row's lanes stay for the shuffles of others in their warp
+            const float rstd = live ? __ldg(p.rstd + m) : 0.0f;
             const uint4* dy = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + at * row_bytes);
             const uint4* h = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (rows + at) * row_bytes);
             const uint4* dh = reinterpret_cast<const uint4*>(ring + st * s.stage_bytes + (2 * rows + at) * row_bytes);
@@ -395,8 +406,8 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
             f2 d[ITEMS][R::H], n[ITEMS][R::H], dot = 0;
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
-                const int i = t + k * kStride;
-                if (i >= vecs) continue;
+                const int i = t + k * LANES;
+                if (i >= vecs || !live) continue;
                 VecIo<T, R::V>::unpack(dy[i], d[k]);
                 VecIo<T, R::V>::unpack(h[i], n[k]);
 #pragma unroll
@@ -407,20 +418,20 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
                     dot = f2_fma(d[k][j], n[k][j], dot);
                 }
             }
-            float sum = warp_sum(f2_lo(dot) + f2_hi(dot));
-            if constexpr (WARPS > 1) {
+            float sum = lanes_sum<LANES>(f2_lo(dot) + f2_hi(dot));
+            if constexpr (LANES > 32) {
                 if (lane == 0) sums[turn][warp] = sum;
                 sync_consumers();
                 sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < WARPS; ++i) sum += sums[turn][i];
+                for (int i = 0; i < kStreamWarps; ++i) sum += sums[turn][i];
             }
             const f2 minus = f2_dup(-__fdiv_rn(sum, static_cast<float>(p.C)));
-            const R row(m, p.C);
+            const R row(live ? m : 0, p.C);
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
-                const int i = t + k * kStride;
-                if (i >= vecs) continue;
+                const int i = t + k * LANES;
+                if (i >= vecs || !live) continue;
                 f2 r[R::H] = {};
                 if (p.r != nullptr) VecIo<T, R::V>::unpack(dh[i], r);
 #pragma unroll
@@ -437,25 +448,25 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
     }
     if constexpr (DGAMMA) {
         float* part = p.part + static_cast<long long>(blockIdx.x) * p.C;
-        if constexpr (WARPS == 1) {  // the warps' sums, in the ring: every stage has been read
+        if constexpr (kAtOnce > 1) {  // the rows' sums, in the ring: every stage has been read
             sync_consumers();
-            part = reinterpret_cast<float*>(ring) + warp * p.C;
+            part = reinterpret_cast<float*>(ring) + slot * p.C;
         }
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int i = t + k * kStride;
+            const int i = t + k * LANES;
             if (i >= vecs) continue;
 #pragma unroll
             for (int j = 0; j < R::H; j += 2)
                 *reinterpret_cast<float4*>(part + i * R::V + 2 * j) =
                     make_float4(f2_lo(total[k][j]), f2_hi(total[k][j]), f2_lo(total[k][j + 1]), f2_hi(total[k][j + 1]));
         }
-        if constexpr (WARPS == 1) {
+        if constexpr (kAtOnce > 1) {
             sync_consumers();
             for (int c = threadIdx.x; c < p.C; c += 32 * kStreamWarps) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kStreamWarps; ++i) sum += reinterpret_cast<const float*>(ring)[i * p.C + c];
+                for (int i = 0; i < kAtOnce; ++i) sum += reinterpret_cast<const float*>(ring)[i * p.C + c];
                 p.part[static_cast<long long>(blockIdx.x) * p.C + c] = sum;
             }
         }
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(kLongThreads) rms_backward_long_kernel(const R
 #pragma unroll
         for (int j = 0; j < R::H; ++j) dot = f2_fma(d[j], n[j], dot);
     }
-    const f2 minus = f2_dup(-__fdiv_rn(row_sum<kLongWarps>(f2_lo(dot) + f2_hi(dot), sums), static_cast<float>(p.C)));
+    const f2 minus = f2_dup(-__fdiv_rn(row_sum<kLongThreads>(f2_lo(dot) + f2_hi(dot), sums), static_cast<float>(p.C)));
 #pragma unroll 1
     for (int i = threadIdx.x; i < row.count; i += kLongThreads) {
         f2 d[R::H], n[R::H], r[R::H] = {};
@@ -511,7 +522,7 @@ __global__ void __launch_bounds__(256) rms_columns_kernel(const RmsParams p) {
     const T* h = static_cast<const T*>(p.h_in);
     float total = 0.0f;
     if (c < p.C) {
-#pragma unroll 4
+#pragma unroll 16
         for (long long m = static_cast<long long>(blockIdx.y) * kColumnRows + warp; m < p.M;
              m += static_cast<long long>(gridDim.y) * kColumnRows)
             total = fmaf(static_cast<float>(dy[m * p.C + c]), static_cast<float>(h[m * p.C + c]) * p.rstd[m], total);
@@ -528,66 +539,72 @@ __global__ void __launch_bounds__(256) rms_columns_kernel(const RmsParams p) {
 
 // ---------------------------------------------------------------- launches
 struct Form {
-    int items, warps;  // 0: rows too long for registers
+    int items, lanes;  // granules a thread holds of each tensor, and threads to a row (0: rows too long for registers)
 };
 
-// Granules a thread holds of each tensor, and warps to a row.
 Form pick_form(const RmsParams& p) {
     const int V = p.bf16 ? 8 : 4;
     const int granules = p.C % V == 0 ? p.C / V : (p.C + V - 2) / V + 1;  // the most that a row touches
-    if (granules <= 32) return {1, 1};
-    if (granules <= 64) return {2, 1};
-    if (granules <= 128) return {4, 1};
-    if (granules <= 256) return {2, 4};
-    if (granules <= 512) return {4, 4};
-    if (granules <= 1024) return {4, 8};
-    if (granules <= 2048) return {4, 16};
+    if (granules <= 8) return {1, 8};
+    if (granules <= 16) return {1, 16};
+    if (granules <= 32) return {1, 32};
+    if (granules <= 64) return {2, 32};
+    if (granules <= 128) return {4, 32};
+    if (granules <= 256) return {2, 128};
+    if (granules <= 512) return {4, 128};
+    if (granules <= 1024) return {4, 256};
+    if (granules <= 2048) return {4, 512};
     return {0, 0};
 }
 
 bool aligned_rows(const RmsParams& p) { return p.C % (p.bf16 ? 8 : 4) == 0; }
 
+template <int N>
+using Const = std::integral_constant<int, N>;
+
 template <typename F>
 void by_form(const Form& f, F&& run) {
-    if (f.warps == 1 && f.items == 1) run(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    else if (f.warps == 1 && f.items == 2) run(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
-    else if (f.warps == 1) run(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
-    else if (f.warps == 4 && f.items == 2) run(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
-    else if (f.warps == 4) run(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
-    else if (f.warps == 8) run(std::integral_constant<int, 4>(), std::integral_constant<int, 8>());
-    else run(std::integral_constant<int, 4>(), std::integral_constant<int, 16>());
+    if (f.lanes == 8) run(Const<1>(), Const<8>());
+    else if (f.lanes == 16) run(Const<1>(), Const<16>());
+    else if (f.lanes == 32 && f.items == 1) run(Const<1>(), Const<32>());
+    else if (f.lanes == 32 && f.items == 2) run(Const<2>(), Const<32>());
+    else if (f.lanes == 32) run(Const<4>(), Const<32>());
+    else if (f.lanes == 128 && f.items == 2) run(Const<2>(), Const<128>());
+    else if (f.lanes == 128) run(Const<4>(), Const<128>());
+    else if (f.lanes == 256) run(Const<4>(), Const<256>());
+    else run(Const<4>(), Const<512>());
 }
 
 template <typename T, bool ALIGNED, bool INT8>
 cudaError_t forward(const RmsParams& p, cudaStream_t stream) {
     const Form f = pick_form(p);
-    if (f.warps == 0) {
+    if (f.lanes == 0) {
         rms_forward_long_kernel<T, ALIGNED, INT8><<<p.M, kLongThreads, 0, stream>>>(p);
     } else {
-        by_form(f, [&](auto items, auto warps) {
-            constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
-            if constexpr (ALIGNED || (W == 16 && sizeof(T) == 2))  // other rows off 16 bytes go by elements or are longer
-                rms_forward_kernel<T, ALIGNED, I, W, INT8><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+        by_form(f, [&](auto items, auto lanes) {
+            constexpr int I = decltype(items)::value, N = decltype(lanes)::value;
+            if constexpr (ALIGNED || (N == 512 && sizeof(T) == 2))  // other rows off 16 bytes go by elements or are longer
+                rms_forward_kernel<T, ALIGNED, I, N, INT8><<<(p.M + kRowsOf<N> - 1) / kRowsOf<N>, kThreadsOf<N>, 0, stream>>>(p);
         });
     }
     return cudaGetLastError();
 }
 
-// The streaming backward form of a plan: granules a thread holds, warps to a row (0: another form), and CTAs that an
+// The streaming backward form of a plan: granules a thread holds, threads to a row (0: another form), and CTAs that an
 // SM runs at a time.
 struct StreamForm {
-    int items, warps, ctas;
+    int items, lanes, ctas;
 };
 StreamForm stream_form(const RmsParams& p) {
     const int granules = p.C / (p.bf16 ? 8 : 4);
     if (!aligned_rows(p) || granules > 1024) return {0, 0, 0};
-    const int warps = granules <= 128 ? 1 : kStreamWarps, stride = 32 * warps;
-    const int items = granules <= stride ? 1 : (granules <= 2 * stride ? 2 : 4);
-    return {items, warps, items == 4 ? 1 : 2};
+    const int lanes = granules <= 8 ? 8 : (granules <= 16 ? 16 : (granules <= 128 ? 32 : 32 * kStreamWarps));
+    const int items = granules <= lanes ? 1 : (granules <= 2 * lanes ? 2 : 4);
+    return {items, lanes, items == 4 ? 1 : 2};
 }
 
 int stream_rows_of(const RmsParams& p, const StreamForm& f, int num_sms) {
-    return stream_rows(p.M, f.warps, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), f.ctas * num_sms);
+    return stream_rows(p.M, 32 * kStreamWarps / f.lanes, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), f.ctas * num_sms);
 }
 
 int stream_ctas(const RmsParams& p, const StreamForm& f, int num_sms) {
@@ -597,7 +614,7 @@ int stream_ctas(const RmsParams& p, const StreamForm& f, int num_sms) {
     return static_cast<int>(need < most ? need : most);
 }
 
-template <typename T, int ITEMS, int WARPS>
+template <typename T, int ITEMS, int LANES>
 cudaError_t stream_launch(const RmsParams& p, const StreamForm& f, cudaStream_t stream) {
     Stream s;
     s.rows = p.rows;
@@ -605,7 +622,8 @@ cudaError_t stream_launch(const RmsParams& p, const StreamForm& f, cudaStream_t 
     const int room = (f.ctas == 2 ? 113 : 226) * 1024 - 1024;  // of shared memory, barriers aside
     s.stages = room / s.stage_bytes < kStreamMaxStages ? room / s.stage_bytes : kStreamMaxStages;
     int bytes = s.stages * s.stage_bytes;
-    if (WARPS == 1 && bytes < kStreamWarps * p.C * 4) bytes = kStreamWarps * p.C * 4;  // the warps' sums
+    const int sums = LANES <= 32 ? 32 * kStreamWarps / LANES * p.C * 4 : 0;  // of the rows that the warps work on together
+    if (bytes < sums) bytes = sums;
     const auto run = [&](auto* kernel, SmemLimitCache& limits) {
         const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), 226 * 1024, limits);
         if (e != cudaSuccess) return e;
@@ -613,18 +631,21 @@ cudaError_t stream_launch(const RmsParams& p, const StreamForm& f, cudaStream_t 
         return cudaGetLastError();
     };
     static SmemLimitCache with, without;
-    return p.dgamma != nullptr ? run(rms_backward_stream_kernel<T, ITEMS, WARPS, true>, with)
-                               : run(rms_backward_stream_kernel<T, ITEMS, WARPS, false>, without);
+    return p.dgamma != nullptr ? run(rms_backward_stream_kernel<T, ITEMS, LANES, true>, with)
+                               : run(rms_backward_stream_kernel<T, ITEMS, LANES, false>, without);
 }
 
 template <typename T>
 cudaError_t stream_backward(const RmsParams& p, const StreamForm& f, cudaStream_t stream) {
-    if (f.warps == 1) {
-        if (f.items == 1) return stream_launch<T, 1, 1>(p, f, stream);
-        return f.items == 2 ? stream_launch<T, 2, 1>(p, f, stream) : stream_launch<T, 4, 1>(p, f, stream);
+    constexpr int kAll = 32 * kStreamWarps;
+    if (f.lanes == 8) return stream_launch<T, 1, 8>(p, f, stream);
+    if (f.lanes == 16) return stream_launch<T, 1, 16>(p, f, stream);
+    if (f.lanes == 32) {
+        if (f.items == 1) return stream_launch<T, 1, 32>(p, f, stream);
+        return f.items == 2 ? stream_launch<T, 2, 32>(p, f, stream) : stream_launch<T, 4, 32>(p, f, stream);
     }
-    if (f.items == 1) return stream_launch<T, 1, kStreamWarps>(p, f, stream);
-    return f.items == 2 ? stream_launch<T, 2, kStreamWarps>(p, f, stream) : stream_launch<T, 4, kStreamWarps>(p, f, stream);
+    if (f.items == 1) return stream_launch<T, 1, kAll>(p, f, stream);
+    return f.items == 2 ? stream_launch<T, 2, kAll>(p, f, stream) : stream_launch<T, 4, kAll>(p, f, stream);
 }
 
 template <typename T, bool ALIGNED>
@@ -632,19 +653,19 @@ cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
     const bool join = p.dgamma != nullptr && p.parts > 1;
     const StreamForm sf = stream_form(p);
     const Form f = pick_form(p);
-    if (ALIGNED && sf.warps != 0) {
+    if (ALIGNED && sf.lanes != 0) {
         const cudaError_t e = stream_backward<T>(p, sf, stream);
         if (e != cudaSuccess || !join) return e;
         return launch_join_columns(p.part, p.parts, p.C, p.dgamma, true, stream);
     }
     if (p.dgamma != nullptr)  // first: dx may be dy
         rms_columns_kernel<T><<<dim3((p.C + 31) / 32, p.parts), 256, 0, stream>>>(p);
-    if (f.warps == 0) {
+    if (f.lanes == 0) {
         rms_backward_long_kernel<T, ALIGNED><<<p.M, kLongThreads, 0, stream>>>(p);
     } else {
-        by_form(f, [&](auto items, auto warps) {
-            constexpr int I = decltype(items)::value, W = decltype(warps)::value, rows = W == 1 ? kRowsOfWarps : 1;
-            if constexpr (W == 16 && (ALIGNED || sizeof(T) == 2)) rms_backward_kernel<T, ALIGNED, I, W><<<(p.M + rows - 1) / rows, kThreadsOf<W>, 0, stream>>>(p);
+        by_form(f, [&](auto items, auto lanes) {
+            constexpr int I = decltype(items)::value, N = decltype(lanes)::value;
+            if constexpr (N == 512 && (ALIGNED || sizeof(T) == 2)) rms_backward_kernel<T, ALIGNED, I, N><<<p.M, N, 0, stream>>>(p);
         });
     }
     const cudaError_t e = cudaGetLastError();
@@ -661,7 +682,7 @@ void rms_plan_backward(RmsParams& p, int num_sms) {
         return;
     }
     const StreamForm f = stream_form(p);
-    if (f.warps != 0) {
+    if (f.lanes != 0) {
         p.rows = stream_rows_of(p, f, num_sms);
         p.ctas = p.parts = stream_ctas(p, f, num_sms);
         return;

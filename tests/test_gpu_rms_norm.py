@@ -15,7 +15,7 @@ DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 # element; fewer rows than a CTA takes, more than one round of CTAs
 SHAPES = [(1, 1), (3, 2), (5, 8), (2, 7), (9, 256), (4, 255), (33, 500), (7, 512), (5, 1003), (6, 1024), (300, 1000), (3, 1025), (2, 2048),
           (4, 2049), (1, 4096), (9, 4100), (3, 4099), (2, 8192), (3, 8195), (2, 16384), (2, 16383), (2, 16400), (1, 33000), (2, 20001),
-          (5000, 40), (4001, 33)]
+          (5000, 40), (4001, 33), (1001, 64), (777, 128), (301, 72), (3, 120)]
 
 
 def _np(t):
