@@ -2,7 +2,7 @@
 //
 //   z[m][n] = sum_k x[m][k] * w[n][k] + bias[n],   y = act(z) + residual
 //
-// Bound by reading w once: 2 N K bytes.  Both operands go from memory to registers and from there into BF16 MMAs of
+// Bound by reading w once: 2 N K bytes (1 x 4096 -> 16384 23 us, 5.8 TB/s; 1 x 4096 -> 4096 7.8, 4.3, the launch among them).  Both operands go from memory to registers and from there into BF16 MMAs of
 // 16 x 8 x 16 (16 rows of w, 8 of x), whose rate does not matter here; the 128-row tiles of the kernel for many rows
 // and their set-up would.  A CTA takes 16 rows of w; its eight warps share K, 64 at a time.  Lane 4 g + q holds
 // k = 8 q .. 8 q + 7 of each 32 of rows g and g + 8 of w and of row g of x: the MMA sums over k in any order, so its

@@ -5,7 +5,7 @@
 // bytes whose whole 16-byte granules move by bulk copies, both ways, whatever the rows' starts; in shared memory a
 // thread takes single values, neighbouring lanes neighbouring ones, and keeps the same columns in every row (gamma and
 // the sums of dgamma stay in registers).  Handled as granules in registers, with gamma and dgamma's columns read apart,
-// 8192 x 4099 BF16 took 106 us forward and 322 backward.
+// 8192 x 4099 BF16 took 106 us forward and 322 backward; it takes 46 and 68 so, 58 to 8 bits.
 //
 // Warps: eight work on rows (eight rows of one warp each, or one row of all), one brings groups into the ring, one
 // sends results, which replace their inputs there, back.  The first and last granule of a group, shared with the
