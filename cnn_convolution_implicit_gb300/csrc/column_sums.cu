@@ -4,6 +4,8 @@
 // Bound by reading dy and z and writing u: 8192 x 4096 with SiLU 35 us cold, 5.7 TB/s.  A CTA takes a strip of columns of a range of rows; a thread keeps its
 // columns' sums over its rows in FP32, the threads' meet in shared memory and the ranges' in the workspace, always
 // in one order.
+#include <type_traits>
+
 #include "linear_internal.h"
 #include "pointwise_math.cuh"
 #include "rows_internal.h"
@@ -20,7 +22,7 @@ struct Strip {
 };
 Strip strip_of(int N) {
     Strip s;
-    s.vec = N % 8 == 0 ? 8 : 1;
+    s.vec = N % 8 == 0 ? 8 : (N % 4 == 0 ? 4 : (N % 2 == 0 ? 2 : 1));
     const int vecs = N / s.vec;
     s.lanes = 1;
     while (s.lanes < 32 && s.lanes < vecs) s.lanes *= 2;
@@ -28,10 +30,13 @@ Strip strip_of(int N) {
     return s;
 }
 
+// Rows whose loads a thread has under way: more of them where the loads are narrow.
+__host__ __device__ constexpr int batch_of(int vec) { return vec == 8 ? 2 : (vec == 4 ? 4 : 8); }
+
 template <int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradParams p, int lanes, float* sums_out) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product that may follow
-    constexpr int H = (VEC + 1) / 2, kBatch = 2;
+    constexpr int H = (VEC + 1) / 2, kBatch = batch_of(VEC);
     using Io = VecIo<__nv_bfloat16, VEC>;
     using Raw = typename Io::Raw;
     __shared__ float sums[kThreads * VEC];
@@ -112,11 +117,12 @@ cudaError_t launch_join_columns(const float* part, int parts, int C, float* out,
     return cudaLaunchKernelEx(&cfg, join_columns_kernel, part, parts, C, out);
 }
 
-// About four CTAs an SM, two rows a thread at least.
+// About four CTAs an SM (eight where accesses are narrow), a batch of rows a thread at least.
 int linear_grad_parts(int M, int N, int num_sms) {
     const Strip s = strip_of(N);
     const int slots = kThreads / s.lanes;
-    const long long need = (static_cast<long long>(M) + 2 * slots - 1) / (2 * slots), most = (4LL * num_sms + s.strips - 1) / s.strips;
+    const int rows = slots * batch_of(s.vec);
+    const long long need = (static_cast<long long>(M) + rows - 1) / rows, most = ((s.vec >= 4 ? 4LL : 8LL) * num_sms + s.strips - 1) / s.strips;
     return static_cast<int>(need < most ? need : most);
 }
 
@@ -125,10 +131,16 @@ cudaError_t launch_linear_grad(const LinearGradParams& p, int num_sms, bool join
     const int parts = linear_grad_parts(p.M, p.N, num_sms);
     float* sums = p.dbias == nullptr ? nullptr : (parts > 1 ? p.part : p.dbias);
     const dim3 grid(s.strips, parts);
-    const auto run = [&](auto* eight, auto* one) { (s.vec == 8 ? eight : one)<<<grid, kThreads, 0, stream>>>(p, s.lanes, sums); };
-    if (p.act == CONV_ACT_RELU) run(linear_grad_kernel<8, CONV_ACT_RELU>, linear_grad_kernel<1, CONV_ACT_RELU>);
-    else if (p.act == CONV_ACT_SILU) run(linear_grad_kernel<8, CONV_ACT_SILU>, linear_grad_kernel<1, CONV_ACT_SILU>);
-    else run(linear_grad_kernel<8, CONV_ACT_NONE>, linear_grad_kernel<1, CONV_ACT_NONE>);
+    const auto run = [&](auto vec) {
+        constexpr int V = decltype(vec)::value;
+        if (p.act == CONV_ACT_RELU) linear_grad_kernel<V, CONV_ACT_RELU><<<grid, kThreads, 0, stream>>>(p, s.lanes, sums);
+        else if (p.act == CONV_ACT_SILU) linear_grad_kernel<V, CONV_ACT_SILU><<<grid, kThreads, 0, stream>>>(p, s.lanes, sums);
+        else linear_grad_kernel<V, CONV_ACT_NONE><<<grid, kThreads, 0, stream>>>(p, s.lanes, sums);
+    };
+    if (s.vec == 8) run(std::integral_constant<int, 8>());
+    else if (s.vec == 4) run(std::integral_constant<int, 4>());
+    else if (s.vec == 2) run(std::integral_constant<int, 2>());
+    else run(std::integral_constant<int, 1>());
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.dbias == nullptr || parts == 1 || !join) return e;
     return launch_join_columns(p.part, parts, p.N, p.dbias, true, stream);

@@ -24,7 +24,7 @@
 // The epilogue keeps the sum in FP32 to the end.  The residual comes by TMA into the warp's output
 // buffer while the MMAs run; every thread adds its row's part and writes the result in the same
 // place, from where the TMA stores it (so y may be the residual).  Rows of y off 16 bytes (N % 8) are
-// beyond the TMA: they are moved between buffer and memory by coalesced accesses.
+// beyond the TMA: they move between buffer and memory as the aligned granules that they lie in.
 //
 // Measured (repeated launches in a graph): 8192 x 4096 x 4096 142 us, 1,933 TFLOP/s, the rate of the card's library product;
 // bound by the tensor cores (89 % of their cycles) and, in long streams of calls, by power.  200704 x 256 -> 512 with bias,
@@ -32,6 +32,7 @@
 //
 // Few tiles: the K of each is shared by `splits` units, which leave FP32 parts in the workspace; a kernel
 // of its own adds them in one order and runs the epilogue.
+#include "int8_rows.cuh"
 #include "linear_internal.h"
 #include "pointwise_math.cuh"
 #include "ptx.cuh"
@@ -41,6 +42,7 @@ namespace convgb {
 namespace {
 
 constexpr int kBlockCols = 64, kBlockBytes = 32 * 128;  // 32 rows x 64 columns of outputs
+constexpr int kEdgeBytes = 5 * 1024;                       // room for them where rows start off 16 bytes
 constexpr int kStepK = 64;       // K of one stage: 128 bytes of a row
 constexpr int kTileA = 128 * 128;  // bytes of A in a stage: 128 rows
 
@@ -53,7 +55,7 @@ struct Ring {
 
 constexpr int kBox = 64 * 128;   // bytes of an MN-major box: 64 of K, 64 of m or n
 
-template <bool PAIR, int BN>
+template <bool PAIR, int BN, bool TMA>
 struct Shape {
     static constexpr int kCtas = PAIR ? 2 : 1;
     static constexpr int kRowsB = BN / kCtas;            // of B in this CTA
@@ -63,7 +65,8 @@ struct Shape {
     static constexpr int kTmemCols = 2 * BN;
     // Each epilogue warp that works has room for a block of outputs; the ring takes the rest.
     static constexpr int kBarBytes = 512 + kEpilogueWarps * 128;  // barriers, the warps' biases
-    static constexpr int stages(int warps) { return (232448 - kBarBytes - warps * kBlockBytes) / kStage; }
+    static constexpr int kOut = TMA ? kBlockBytes : kEdgeBytes;
+    static constexpr int stages(int warps) { return (232448 - kBarBytes - warps * kOut) / kStage; }
     static constexpr int kMaxStages = stages(8);
     static_assert((2 * kMaxStages + 5 + kEpilogueWarps) * 8 + 8 <= 512, "barriers");
 };
@@ -217,42 +220,79 @@ __device__ __forceinline__ uint4 finish_chunk(const uint32_t* v, const float4* b
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// Between a block in shared memory and rows of y that start on T's size only, neighbouring lanes at
-// neighbouring places.
-template <typename T, bool OUT>
-__device__ __forceinline__ void move_block(uint8_t* block, __nv_bfloat16* y, long long N, int rows, int columns) {
-    constexpr int kEach = static_cast<int>(sizeof(T)) / 2, kBatch = 16;  // accesses under way
-    const int lane = threadIdx.x & 31;
+// Rows of y that start on 2 bytes only: a block's part of a row lies across 9 aligned granules of 16 bytes at most.  A row of
+// the buffer holds them as they lie in memory (144 bytes from row to row: eight lanes' 16-byte accesses fall on 32 banks),
+// so whole granules move in wide accesses of neighbouring lanes, nine loads of the residual under way a lane, and
+// only the ends of a row go by elements.  (Two-byte accesses throughout: 40000 x 515 -> 777 with a residual 139 us.)
+constexpr int kEdgePitch = 144, kGranules = 9;
+
+__device__ __forceinline__ void edge_load(uint8_t* block, const __nv_bfloat16* r, int m, int n, int M, int N) {
+    const int8_t* base = reinterpret_cast<const int8_t*>(r);
+    const long long total = static_cast<long long>(M) * N * 2;
+    const int lane = threadIdx.x & 31, bytes = 2 * min(kBlockCols, N - n);
+    uint4 v[kGranules];
 #pragma unroll
-    for (int part = 0; part < kBlockCols; part += 32 * kEach) {
-        const int c = part + lane * kEach;
-        if (c >= columns) return;
-#pragma unroll 1
-        for (int row0 = 0; row0 < rows; row0 += kBatch) {
-            T v[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int row = row0 + i;
-                if constexpr (OUT) v[i] = *reinterpret_cast<const T*>(reinterpret_cast<uint8_t*>(block_chunk(block, row, c >> 3)) + (c & 7) * 2);
-                else if (row < rows) v[i] = *reinterpret_cast<const T*>(y + row * N + c);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int row = row0 + i;
-                if (row >= rows) break;
-                if constexpr (OUT) *reinterpret_cast<T*>(y + row * N + c) = v[i];
-                else *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(block_chunk(block, row, c >> 3)) + (c & 7) * 2) = v[i];
-            }
-        }
+    for (int i = 0; i < kGranules; ++i) {
+        const int at = i * 32 + lane, row = at / kGranules, g = at - row * kGranules;
+        const long long first = (static_cast<long long>(m + row) * N + n) * 2, from = (first & ~15LL) + 16 * g;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (m + row < M && from < first + bytes) v[i] = granule<true>(base, from >> 4, total);  // ordinary loads: y may be the residual
     }
+#pragma unroll
+    for (int i = 0; i < kGranules; ++i) {
+        const int at = i * 32 + lane, row = at / kGranules, g = at - row * kGranules;
+        *reinterpret_cast<uint4*>(block + row * kEdgePitch + 16 * g) = v[i];
+    }
+    __syncwarp();
 }
 
-template <bool OUT>
-__device__ __forceinline__ void move_rows(uint8_t* block, __nv_bfloat16* y, int N, int m, int n, int M) {
-    __nv_bfloat16* at = y + static_cast<long long>(m) * N + n;
-    const int rows = min(32, M - m), columns = min(kBlockCols, N - n);
-    if (N % 2 == 0) move_block<uint32_t, OUT>(block, at, N, rows, columns);
-    else move_block<uint16_t, OUT>(block, at, N, rows, columns);
+// Byte of the block's part of a row in its first granule (32 bits do).
+__device__ __forceinline__ int edge_offset(int row, int n, int N) {
+    return static_cast<int>((static_cast<uint32_t>(row) * static_cast<uint32_t>(N) + static_cast<uint32_t>(n)) * 2u & 15u);
+}
+
+__device__ __forceinline__ void edge_store(const uint8_t* block, __nv_bfloat16* y, int m, int n, int M, int N) {
+    uint8_t* first = reinterpret_cast<uint8_t*>(y) + (static_cast<long long>(m) * N + n) * 2;  // the block's first byte
+    const long long pitch = 2LL * N;
+    const int lane = threadIdx.x & 31, rows = min(32, M - m), bytes = 2 * min(kBlockCols, N - n);
+    __syncwarp();
+    // Whole granules: the (lane % 8)th of rows lane / 8, lane / 8 + 4, ...
+    {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + (lane >> 3), off = edge_offset(m + row, n, N), g = (lane & 7) + (off != 0);
+            v[i] = *reinterpret_cast<const uint4*>(block + row * kEdgePitch + 16 * g);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + (lane >> 3), off = edge_offset(m + row, n, N), at = 16 * ((lane & 7) + (off != 0)) - off;
+            if (row < rows && at + 16 <= bytes) *reinterpret_cast<uint4*>(first + row * pitch + at) = v[i];
+        }
+    }
+    if (bytes == 2 * kBlockCols) {  // eight elements of a row, or none, lie before the first of them and behind the last
+        uint16_t v[8];
+        int at[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + (lane >> 3), off = edge_offset(m + row, n, N), k = lane & 7;
+            at[i] = off == 0 || row >= rows ? -1 : (2 * k < 16 - off ? 2 * k : 2 * k + 112);
+            v[i] = *reinterpret_cast<const uint16_t*>(block + row * kEdgePitch + off + max(at[i], 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (at[i] >= 0) *reinterpret_cast<uint16_t*>(first + (i * 4 + (lane >> 3)) * pitch + at[i]) = v[i];
+    } else {  // the last columns of y: up to seven before the first whole granule, up to seven behind the last
+#pragma unroll 8
+        for (int i = 0; i < 16; ++i) {
+            const int row = i * 2 + (lane >> 4), off = edge_offset(m + row, n, N), k = lane & 7;
+            const int inner = (16 - off) & 15, outer = bytes - ((bytes + off) & 15);
+            const int at = (lane & 8 ? max(inner, outer) : 0) + 2 * k;
+            if (row < rows && at < (lane & 8 ? bytes : min(inner, bytes)))
+                *reinterpret_cast<uint16_t*>(first + row * pitch + at) = *reinterpret_cast<const uint16_t*>(block + row * kEdgePitch + off + at);
+        }
+    }
+    __syncwarp();
 }
 
 // A lane's share of the bias of a block: columns lane and 32 + lane.
@@ -274,6 +314,10 @@ template <int ACT, bool TMA>
 __device__ __forceinline__ void block_pass(const Job& p, const CUtensorMap* map, __nv_bfloat16* to, bool with_r, uint32_t at,
                                            uint8_t* block, const LaneBias& bias, int m, int n) {
     const int lane = threadIdx.x & 31;
+    uint4* own = reinterpret_cast<uint4*>(block + lane * kEdgePitch);  // off 16 bytes: the row's granules
+    const int off = TMA ? 0 : edge_offset(m + lane, n, p.N);
+    uint4 r = make_uint4(0, 0, 0, 0), before = r;
+    if (!TMA && with_r) r = own[0];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t v[32];
@@ -287,8 +331,21 @@ __device__ __forceinline__ void block_pass(const Job& p, const CUtensorMap* map,
         const float4* row = reinterpret_cast<const float4*>(bias.row);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint4* chunk = block_chunk(block, lane, 4 * half + j);
-            *chunk = finish_chunk<ACT>(v + 8 * j, row != nullptr ? row + 2 * j : nullptr, with_r ? chunk : nullptr);
+            const float4* b = row != nullptr ? row + 2 * j : nullptr;
+            if constexpr (TMA) {
+                uint4* chunk = block_chunk(block, lane, 4 * half + j);
+                *chunk = finish_chunk<ACT>(v + 8 * j, b, with_r ? chunk : nullptr);
+            } else {  // eight columns lie across two granules, for the residual and for what takes its place
+                const int g = 4 * half + j;
+                uint4 add = r;
+                if (with_r) {
+                    r = own[g + 1];
+                    add = shift_granules(add, r, off);
+                }
+                const uint4 now = finish_chunk<ACT>(v + 8 * j, b, with_r ? &add : nullptr);
+                own[g] = off == 0 ? now : shift_granules(before, now, 16 - off);
+                before = now;
+            }
         }
     }
     if constexpr (TMA) {
@@ -299,9 +356,8 @@ __device__ __forceinline__ void block_pass(const Job& p, const CUtensorMap* map,
             bulk_commit();
         }
     } else {
-        __syncwarp();
-        move_rows<true>(block, to, p.N, m, n, p.M);
-        __syncwarp();
+        if (off != 0) own[kGranules - 1] = shift_granules(before, make_uint4(0, 0, 0, 0), 16 - off);
+        edge_store(block, to, m, n, p.M, p.N);
     }
 }
 
@@ -362,8 +418,8 @@ __device__ __forceinline__ void join_columns(const ColumnJoin& j, int first, int
 // TMA: rows of y start on 16 bytes (of their own, lest the other path's registers spill this one's: 200704 x 256 -> 512 with
 // a residual 94 us together, 84 apart).
 template <bool PAIR, int BN, bool B_BY_K, bool TMA>
-__global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kernel(const __grid_constant__ Launch L) {
-    using S = Shape<PAIR, BN>;
+__global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm_kernel(const __grid_constant__ Launch L) {
+    using S = Shape<PAIR, BN, TMA>;
     constexpr int kMmaWarp = S::kEpilogueWarps, kLoadWarp = kMmaWarp + 1, kCtas = S::kCtas;
     const Ring ring = L.ring;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join of parts that may follow
@@ -374,13 +430,13 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kern
     }
     Bars b;
     uint8_t* outputs = smem + ring.stages * S::kStage;
-    b.full = reinterpret_cast<uint64_t*>(outputs + ring.warps * kBlockBytes);
+    b.full = reinterpret_cast<uint64_t*>(outputs + ring.warps * S::kOut);
     b.empty = b.full + S::kMaxStages;
     b.tfull = b.empty + S::kMaxStages;
     b.tempty = b.tfull + 2;
     b.drain = b.tempty + 2;
     b.res = b.drain + 1;
-    b.bias = reinterpret_cast<float*>(outputs + ring.warps * kBlockBytes + 512);
+    b.bias = reinterpret_cast<float*>(outputs + ring.warps * S::kOut + 512);
     b.tmem_slot = reinterpret_cast<uint32_t*>(b.res + S::kEpilogueWarps);
     b.abort = reinterpret_cast<int*>(b.tmem_slot + 1);
     volatile int* abort = b.abort;
@@ -424,7 +480,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kern
         // ------------------------------------------------------------ epilogue
         const int per_group = ring.warps / ring.groups, group = warp / per_group;
         const int quarter = warp & 3, cols = BN * 4 / per_group, part = (warp - group * per_group) >> 2;
-        uint8_t* block = outputs + warp * kBlockBytes;
+        uint8_t* block = outputs + warp * S::kOut;
         uint64_t* res = b.res + warp;
         float* bias_row = b.bias + 32 * warp;
         if (B_BY_K && L.join.out != nullptr) join_columns(L.join, static_cast<int>(blockIdx.x) * ring.warps + warp, static_cast<int>(gridDim.x) * ring.warps);
@@ -454,8 +510,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kern
             }
             if (by_tma && blocks > 0) fetch(0);
             const auto fetch_rows = [&](int i) {
-                move_rows<false>(block, const_cast<__nv_bfloat16*>(p.r), p.N, m, n + kBlockCols * i, p.M);
-                __syncwarp();
+                edge_load(block, p.r, m, n + kBlockCols * i, p.M, p.N);
             };
             const bool by_rows = !TMA && !B_BY_K && p.splits == 1 && p.r != nullptr;
             if (by_rows && blocks > 0) fetch_rows(0);
@@ -603,30 +658,44 @@ __global__ void __launch_bounds__(Shape<PAIR, BN>::kThreads, 1) linear_gemm_kern
 }
 
 // ---------------------------------------------------------------- parts of K
-// Four neighbouring outputs a thread: their parts in order, then the epilogue.
-__global__ void __launch_bounds__(256) linear_join_kernel(const GemmParams p, int splits) {
+// Four neighbouring outputs to L threads, which add the parts l, l + L, ... each; their sums meet in order, then comes the
+// epilogue.  (One thread to them all: 64 parts of 83 x 48 outputs 21 us.)
+constexpr int kJoinThreads = 256;
+
+template <int L>
+__global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const GemmParams p, int splits) {
+    constexpr int kQuads = kJoinThreads / L;
+    __shared__ float4 sums[L][kQuads];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int quads = (p.N + 3) / 4;
-    const long long i = blockIdx.x * 256LL + threadIdx.x, m = i / quads;
-    if (m >= p.M) return;
-    const int n = static_cast<int>(i - m * quads) * 4;
-    const float4* from = reinterpret_cast<const float4*>(p.part) + i;
-    const long long step = static_cast<long long>(p.M) * quads;
+    const int quads = (p.N + 3) / 4, l = threadIdx.x / kQuads, q = threadIdx.x % kQuads;
+    const long long i = static_cast<long long>(blockIdx.x) * kQuads + q, m = i / quads, all = static_cast<long long>(p.M) * quads;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = 0; k < splits; ++k) {
-        const float4 v = from[k * step];
+    const auto add = [&](const float4& v) {
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
         s.w += v.w;
+    };
+    if (i < all) {
+        const float4* from = reinterpret_cast<const float4*>(p.part) + i;
+#pragma unroll 4
+        for (int k = l; k < splits; k += L) add(from[k * all]);
     }
+    if constexpr (L > 1) {
+        sums[l][q] = s;
+        __syncthreads();
+        if (l != 0) return;
+#pragma unroll
+        for (int k = 1; k < L; ++k) add(sums[k][q]);
+    }
+    if (i >= all) return;
+    const int n = static_cast<int>(i - m * quads) * 4;
     float z[4] = {s.x, s.y, s.z, s.w}, y[4];
     const long long o = m * p.N + n;
     const int count = min(4, p.N - n);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (p.bias != nullptr && j < count) z[j] += __ldg(p.bias + n + j);
+        if (p.bias != nullptr && j < count) z[j] = __fadd_rn(z[j], __ldg(p.bias + n + j));
         y[j] = p.act == CONV_ACT_RELU ? activate<CONV_ACT_RELU>(z[j]) : (p.act == CONV_ACT_SILU ? activate<CONV_ACT_SILU>(z[j]) : z[j]);
     }
     if (p.N % 4 == 0) {
@@ -667,9 +736,9 @@ bool encode_operand(CUtensorMap* map, const __nv_bfloat16* base, bool by_k, int 
                 : encode_matrix(map, base, rows, K, pitch, box_rows, kStepK, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool PAIR, int BN>
+template <bool PAIR, int BN, bool TMA>
 bool make_job(Job& j, const GemmParams& p, int splits, int first) {
-    using S = Shape<PAIR, BN>;
+    using S = Shape<PAIR, BN, TMA>;
     j.M = p.M;
     j.N = p.N;
     j.K = p.K;
@@ -705,7 +774,7 @@ bool make_job(Job& j, const GemmParams& p, int splits, int first) {
 template <bool PAIR, int BN, bool B_BY_K, bool TMA>
 cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, const ColumnJoin& sums, int num_sms, bool after_other,
                            cudaStream_t stream) {
-    using S = Shape<PAIR, BN>;
+    using S = Shape<PAIR, BN, TMA>;
     static SmemLimitCache limits;
     auto* fn = linear_gemm_kernel<PAIR, BN, B_BY_K, TMA>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 232448, limits);  // all that a block may have, once
@@ -717,7 +786,7 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     L.status = p[0].status;
     int longest = 0;
     for (int i = 0; i < count; ++i) {
-        if (!make_job<PAIR, BN>(L.job[i], p[i], t.splits[i], L.units)) return cudaErrorInvalidValue;
+        if (!make_job<PAIR, BN, TMA>(L.job[i], p[i], t.splits[i], L.units)) return cudaErrorInvalidValue;
         L.units += L.job[i].tiles * t.splits[i];
         longest = p[i].K > longest ? p[i].K : longest;
     }
@@ -730,7 +799,7 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((L.units < slots ? L.units : slots) * S::kCtas));
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = L.ring.stages * S::kStage + L.ring.warps * kBlockBytes + S::kBarBytes;
+    cfg.dynamicSmemBytes = L.ring.stages * S::kStage + L.ring.warps * S::kOut + S::kBarBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     if (PAIR) {
@@ -752,15 +821,17 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
         if (t.splits[i] == 1) continue;
         cudaLaunchConfig_t join = {};
         const long long quads = static_cast<long long>(p[i].M) * ((p[i].N + 3) / 4);
-        join.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
-        join.blockDim = dim3(256);
+        const int threads = t.splits[i] <= 4 ? 1 : (t.splits[i] <= 16 ? 4 : 16), at_once = kJoinThreads / threads;
+        join.gridDim = dim3(static_cast<unsigned>((quads + at_once - 1) / at_once));
+        join.blockDim = dim3(kJoinThreads);
         join.stream = stream;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         join.attrs = attr;
         join.numAttrs = early ? 1 : 0;
         early = false;
-        e = cudaLaunchKernelEx(&join, linear_join_kernel, p[i], t.splits[i]);
+        auto* kernel = threads == 1 ? linear_join_kernel<1> : (threads == 4 ? linear_join_kernel<4> : linear_join_kernel<16>);
+        e = cudaLaunchKernelEx(&join, kernel, p[i], t.splits[i]);
     }
     return e;
 }
@@ -809,7 +880,7 @@ GemmTile gemm_pick_tile(const GemmSize* products, int count, int num_sms) {
             return splits == 1 || (splits <= (p.K + kStepK - 1) / kStepK && tiles(p) * splits <= slots);
         };
         const auto join = [&](const GemmSize& p, int splits) {
-            return splits > 1 ? 3.0 + static_cast<double>(p.M) * p.N * splits * 8.0 / 4e6 : 0.0;
+            return splits > 1 ? 5.0 + static_cast<double>(p.M) * p.N * splits * 8.0 / 4e6 : 0.0;
         };
         for (int s0 : kSplits) {
             if (!allowed(products[0], s0)) continue;

@@ -32,14 +32,15 @@ SIZES = [
     (1000, 96, 2048), (1000, 1003, 72), (2000, 2050, 520), (3136, 512, 256), (5000, 1000, 200), (40000, 64, 72), (7, 20000, 128),
     # each tile, whole and with its K shared, rows of y on and off 16 bytes
     (443, 2728, 36), (4603, 271, 32), (42, 432, 10952), (37, 3206, 1835), (4785, 1624, 40), (4639, 1956, 32), (130, 3504, 7040),
-    (3652, 129, 5960), (34, 34, 1089), (62, 32, 1072),
+    (3652, 129, 5960), (34, 34, 1089), (62, 32, 1072), (35, 1455, 4623), (37, 37, 1658), (39, 32, 2599), (1300, 325, 105),
 ]
 
 GRAD_SIZES = [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 520), (77, 264, 520), (301, 777, 1000),
               (1000, 96, 48), (129, 257, 127), (2000, 512, 256), (5000, 64, 40), (300, 1024, 2048), (20000, 130, 72),
               # each tile, whole, with the K of dx, of dw or of both shared
               (49, 48, 5304), (39, 32, 6635), (4210, 32, 226), (34, 1984, 518), (705, 33, 8624), (758, 33, 8748),
-              (2246, 57, 2792), (58, 3120, 1922), (1198, 36, 32), (34, 1216, 36), (2549, 3552, 39), (1397, 52, 42)]
+              (2246, 57, 2792), (58, 3120, 1922), (1198, 36, 32), (34, 1216, 36), (2549, 3552, 39), (1397, 52, 42),
+              (37, 2068, 440), (4648, 32, 3238), (3740, 32, 3824), (1925, 40, 43), (41, 2244, 36), (35, 1704, 48), (2256, 34, 32), (5647, 9421, 8)]
 
 
 @pytest.mark.parametrize("size", SIZES)
