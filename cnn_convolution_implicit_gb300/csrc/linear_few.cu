@@ -115,8 +115,11 @@ cudaError_t launch(const FewParams& p, cudaStream_t stream) {
 // This kernel and the tiles of many rows, microseconds in a graph with cold weights:
 //   8 x 4096 -> 4096 8.3 and 13.4    16 x 4096 -> 4096 10.4 and 13.4   24 x 4096 -> 4096 14.0 and 13.4   32 x 1024 -> 1024 5.4 and 8.4
 //   8 x 16384 -> 4096 24.4 and 29.7  16 x 16384 -> 4096 30.3 and 29.7  16 x 4096 -> 16384 33.7 and 26.8
-// x is read again by every 16 columns, so with more rows and weights the tiles win.
+// x is read again by every 16 columns, so with more rows and weights the tiles win.  Rows of K off 16 bytes take two loads and
+// a shift for each item, and a time that goes by K: 8 x 2045 -> 2048 14.2 and 15.8, 8 x 6661 -> 1592 39 and 19 (with two launches
+// more: rows laid out first, parts joined).
 bool linear_use_few(int M, int N, int K) {
+    if (K % 8 != 0 && K > 3000) return false;
     const long long weights = static_cast<long long>(N) * K;
     return M <= 8 || (M <= 16 && weights <= 1LL << 25) || (M <= 32 && weights <= 1LL << 22);
 }
