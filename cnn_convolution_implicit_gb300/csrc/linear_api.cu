@@ -61,7 +61,7 @@ Workspace forward_space(const conv_linear_plan* pl) {
     const bool lay_out = pl->K % 8 != 0;
     ws.w = lay_out ? rows_bytes(pl->M, pl->K) : 0;
     ws.part = ws.w + (lay_out ? rows_bytes(pl->N, pl->K) : 0);
-    ws.bytes = ws.part + gemm_part_bytes(pl->forward.splits[0], pl->M, pl->N);
+    ws.bytes = ws.part + (gemm_joins_in_cluster(pl->forward) ? 0 : gemm_part_bytes(pl->forward.splits[0], pl->M, pl->N));
     return ws;
 }
 
@@ -121,10 +121,10 @@ conv_status conv_linear_plan_create(conv_linear_plan** out, int M, int N, int K,
     }
     pl->few = linear_use_few(M, N, K);
     const GemmSize forward = {M, N, K}, dx = {M, K, N}, dw = {N, K, M};
-    pl->forward = gemm_pick_tile(&forward, 1, pl->num_sms);
+    pl->forward = gemm_pick_tile(&forward, 1, true, pl->num_sms);
     pl->dw_first = M > N;
     const GemmSize both[2] = {pl->dw_first ? dw : dx, pl->dw_first ? dx : dw};
-    pl->backward = gemm_pick_tile(both, 2, pl->num_sms);
+    pl->backward = gemm_pick_tile(both, 2, false, pl->num_sms);
     *out = pl;
     return CONV_OK;
 }

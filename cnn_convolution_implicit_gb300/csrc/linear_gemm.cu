@@ -30,8 +30,9 @@
 // bound by the tensor cores (89 % of their cycles) and, in long streams of calls, by power.  200704 x 256 -> 512 with bias,
 // ReLU and a residual 84 us, 6.1 TB/s; bound by memory.  dx and dw of 8192 x 1024 -> 4096 85 us, 1,620 TFLOP/s.
 //
-// Few tiles: the K of each is shared by `splits` units, which leave FP32 parts in the workspace; a kernel
-// of its own adds them in one order and runs the epilogue.
+// Few tiles: the K of each is shared by `splits` units.  Of the forward product two, four or eight of them are a cluster:
+// each leaves its FP32 sums in its shared memory, and after a cluster barrier each finishes its share of the rows from
+// all of them, added in one order.  Otherwise they leave parts in the workspace, and a kernel of its own adds and finishes them.
 #include "int8_rows.cuh"
 #include "linear_internal.h"
 #include "pointwise_math.cuh"
@@ -51,6 +52,7 @@ struct Ring {
     int stages;  // of operands
     int warps;   // of the epilogue that work
     int groups;  // of them: 1, or 2 that take the units in turn
+    int cluster;  // CTAs that share the K of a tile and join it themselves; 1: none
 };
 
 constexpr int kBox = 64 * 128;   // bytes of an MN-major box: 64 of K, 64 of m or n
@@ -402,6 +404,90 @@ __device__ __forceinline__ void leave_block(const CUtensorMap* map, uint32_t at,
     }
 }
 
+// Four neighbouring outputs from their whole sums.
+template <typename P>
+__device__ __forceinline__ void finish_four(const P& p, const float4& s, long long m, int n) {
+    float z[4] = {s.x, s.y, s.z, s.w}, y[4];
+    const long long o = m * p.N + n;
+    const int count = min(4, p.N - n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (p.bias != nullptr && j < count) z[j] = __fadd_rn(z[j], __ldg(p.bias + n + j));
+        y[j] = p.act == CONV_ACT_RELU ? activate<CONV_ACT_RELU>(z[j]) : (p.act == CONV_ACT_SILU ? activate<CONV_ACT_SILU>(z[j]) : z[j]);
+    }
+    if (p.N % 4 == 0) {
+        if (p.z != nullptr) *reinterpret_cast<uint2*>(p.z + o) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+        if (p.r != nullptr) {  // ordinary loads: y may be the residual
+            const uint2 r = *reinterpret_cast<const uint2*>(p.r + o);
+            y[0] = __fadd_rn(y[0], __uint_as_float(r.x << 16));
+            y[1] = __fadd_rn(y[1], __uint_as_float(r.x & 0xffff0000u));
+            y[2] = __fadd_rn(y[2], __uint_as_float(r.y << 16));
+            y[3] = __fadd_rn(y[3], __uint_as_float(r.y & 0xffff0000u));
+        }
+        *reinterpret_cast<uint2*>(p.y + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j >= count) break;
+        if (p.z != nullptr) p.z[o + j] = __float2bfloat16_rn(z[j]);
+        p.y[o + j] = __float2bfloat16_rn(p.r != nullptr ? __fadd_rn(y[j], __bfloat162float(p.r[o + j])) : y[j]);
+    }
+}
+
+// ---------------------------------------------------------------- a K shared by a cluster
+// The sums of 32 rows x 64 columns to shared memory: rows BN + 4 floats apart (16-byte accesses of eight rows fall on 32 banks).
+__device__ __forceinline__ void keep_block(uint32_t at, float* part, int pitch) {
+    float* row = part + static_cast<int>(threadIdx.x & 31) * pitch;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t v[32];
+        tmem_ld32(at + 32 * half, v);
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) reinterpret_cast<uint4*>(row + 32 * half)[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+}
+
+__device__ __forceinline__ float4 peer_float4(const float* p, uint32_t cta) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(mapa_shared(smem_addr(p), cta))
+                 : "memory");
+    return v;
+}
+
+// This CTA's rows of the cluster's tile from the parts of all its CTAs, eight accesses of a thread in flight.
+template <int BN, int SPLITS>
+__device__ __forceinline__ void join_cluster(const Job& p, const float* part, int m0, int n0, uint32_t cta) {
+    constexpr int kPitch = BN + 4, kQuads = BN / 4, kRows = 128 / SPLITS, kAtOnce = 8 / SPLITS;
+    const int first = static_cast<int>(cta) * kRows, threads = static_cast<int>(blockDim.x);
+    for (int i = threadIdx.x; i < kRows * kQuads; i += threads * kAtOnce) {
+        float4 v[kAtOnce][SPLITS];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int q = min(i + j * threads, kRows * kQuads - 1);
+#pragma unroll
+            for (int k = 0; k < SPLITS; ++k) v[j][k] = peer_float4(part + (first + q / kQuads) * kPitch + q % kQuads * 4, k);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int q = i + j * threads, m = m0 + first + q / kQuads, n = n0 + q % kQuads * 4;
+            if (q >= kRows * kQuads || m >= p.M || n >= p.N) continue;
+            float4 s = v[j][0];
+#pragma unroll
+            for (int k = 1; k < SPLITS; ++k) {
+                s.x += v[j][k].x;
+                s.y += v[j][k].y;
+                s.z += v[j][k].z;
+                s.w += v[j][k].w;
+            }
+            finish_four(p, s, m, n);
+        }
+    }
+}
+
 // Sums over rows that the kernel before left in parts, a warp to a column: lane i adds parts i, i + 32, ..., as
 // launch_join_columns' warps do, and the lanes' sums meet in its order.
 __device__ __forceinline__ void join_columns(const ColumnJoin& j, int first, int step) {
@@ -444,7 +530,12 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
 
-    const int unit0 = static_cast<int>(blockIdx.x) / kCtas, unit_step = static_cast<int>(gridDim.x) / kCtas, units = L.units;
+    const int units = L.units;
+    constexpr bool kClusters = !PAIR && !B_BY_K;
+    const bool joins = kClusters && ring.cluster > 1;  // then a CTA has one unit: its part of the cluster's tile
+    const uint32_t cta = joins ? cluster_ctarank() : 0u;
+    const int unit0 = joins ? static_cast<int>(cta) * L.job[0].tiles + static_cast<int>(blockIdx.x) / ring.cluster : static_cast<int>(blockIdx.x) / kCtas;
+    const int unit_step = joins ? units : static_cast<int>(gridDim.x) / kCtas;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) {
@@ -537,7 +628,8 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
                 if (!ok) continue;
                 if (!B_BY_K && i > 0) bias.load(p.bias, n + kBlockCols * i, p.N);
                 const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + part * cols + kBlockCols * i;
-                if (p.splits > 1) leave_block(&p.map_part, at, block, m, n + kBlockCols * i, p.N, w.split);
+                if (joins) keep_block(at, reinterpret_cast<float*>(smem) + quarter * 32 * (BN + 4) + part * cols + kBlockCols * i, BN + 4);  // operands are done with
+                else if (p.splits > 1) leave_block(&p.map_part, at, block, m, n + kBlockCols * i, p.N, w.split);
                 else finish_block<TMA, B_BY_K>(p, at, block, bias, m, n + kBlockCols * i);
             }
             if (!ok) break;
@@ -649,6 +741,19 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
     __syncwarp();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();  // no CTA leaves while its peer may still signal it
+    if constexpr (kClusters) {
+        if (joins) {
+            cluster_sync_all();  // every part is in place
+            const Job& p = L.job[0];
+            const Unit w = unit_at<false>(p, unit0);
+            const float* part = reinterpret_cast<const float*>(smem);
+            if (ring.cluster == 2) join_cluster<BN, 2>(p, part, w.mt * 128, w.nt * BN, cta);
+            else if (ring.cluster == 4) join_cluster<BN, 4>(p, part, w.mt * 128, w.nt * BN, cta);
+            else join_cluster<BN, 8>(p, part, w.mt * 128, w.nt * BN, cta);
+            __syncwarp();  // the aligned barrier takes a warp's lanes together
+            cluster_sync_all();  // no CTA leaves while another may still read its part
+        }
+    }
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
@@ -688,34 +793,7 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const GemmPar
 #pragma unroll
         for (int k = 1; k < L; ++k) add(sums[k][q]);
     }
-    if (i >= all) return;
-    const int n = static_cast<int>(i - m * quads) * 4;
-    float z[4] = {s.x, s.y, s.z, s.w}, y[4];
-    const long long o = m * p.N + n;
-    const int count = min(4, p.N - n);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (p.bias != nullptr && j < count) z[j] = __fadd_rn(z[j], __ldg(p.bias + n + j));
-        y[j] = p.act == CONV_ACT_RELU ? activate<CONV_ACT_RELU>(z[j]) : (p.act == CONV_ACT_SILU ? activate<CONV_ACT_SILU>(z[j]) : z[j]);
-    }
-    if (p.N % 4 == 0) {
-        if (p.z != nullptr) *reinterpret_cast<uint2*>(p.z + o) = make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
-        if (p.r != nullptr) {  // ordinary loads: y may be the residual
-            const uint2 r = *reinterpret_cast<const uint2*>(p.r + o);
-            y[0] = __fadd_rn(y[0], __uint_as_float(r.x << 16));
-            y[1] = __fadd_rn(y[1], __uint_as_float(r.x & 0xffff0000u));
-            y[2] = __fadd_rn(y[2], __uint_as_float(r.y << 16));
-            y[3] = __fadd_rn(y[3], __uint_as_float(r.y & 0xffff0000u));
-        }
-        *reinterpret_cast<uint2*>(p.y + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j >= count) break;
-        if (p.z != nullptr) p.z[o + j] = __float2bfloat16_rn(z[j]);
-        p.y[o + j] = __float2bfloat16_rn(p.r != nullptr ? __fadd_rn(y[j], __bfloat162float(p.r[o + j])) : y[j]);
-    }
+    if (i < all) finish_four(p, s, m, static_cast<int>(i - m * quads) * 4);
 }
 
 // ---------------------------------------------------------------- launches
@@ -737,7 +815,7 @@ bool encode_operand(CUtensorMap* map, const __nv_bfloat16* base, bool by_k, int 
 }
 
 template <bool PAIR, int BN, bool TMA>
-bool make_job(Job& j, const GemmParams& p, int splits, int first) {
+bool make_job(Job& j, const GemmParams& p, int splits, bool joins, int first) {
     using S = Shape<PAIR, BN, TMA>;
     j.M = p.M;
     j.N = p.N;
@@ -757,6 +835,7 @@ bool make_job(Job& j, const GemmParams& p, int splits, int first) {
     if (!encode_operand(&j.map_a, p.a, p.a_by_k, p.M, p.K, p.a_pitch, 128) ||
         !encode_operand(&j.map_b, p.b, p.b_by_k, p.N, p.K, p.b_pitch, S::kRowsB))
         return false;
+    if (joins) return true;
     if (splits > 1) {
         const cuuint64_t pitch = static_cast<cuuint64_t>(part_pitch(p.N)) * 4;
         const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(splits)};
@@ -779,6 +858,7 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     auto* fn = linear_gemm_kernel<PAIR, BN, B_BY_K, TMA>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), 232448, limits);  // all that a block may have, once
     if (e != cudaSuccess) return e;
+    const bool joins = !PAIR && !B_BY_K && gemm_joins_in_cluster(t);
     Launch L;
     L.jobs = count;
     L.units = 0;
@@ -786,7 +866,7 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     L.status = p[0].status;
     int longest = 0;
     for (int i = 0; i < count; ++i) {
-        if (!make_job<PAIR, BN, TMA>(L.job[i], p[i], t.splits[i], L.units)) return cudaErrorInvalidValue;
+        if (!make_job<PAIR, BN, TMA>(L.job[i], p[i], t.splits[i], joins, L.units)) return cudaErrorInvalidValue;
         L.units += L.job[i].tiles * t.splits[i];
         longest = p[i].K > longest ? p[i].K : longest;
     }
@@ -796,15 +876,16 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     L.ring.warps = longest >= 1024 ? 8 : S::kEpilogueWarps;
     L.ring.groups = BN == 64 || (L.units > slots && L.ring.warps == S::kEpilogueWarps) ? 2 : 1;
     L.ring.stages = S::stages(L.ring.warps);
+    L.ring.cluster = joins ? t.splits[0] : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((L.units < slots ? L.units : slots) * S::kCtas));
+    cfg.gridDim = dim3(static_cast<unsigned>(joins ? L.units : (L.units < slots ? L.units : slots) * S::kCtas));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = L.ring.stages * S::kStage + L.ring.warps * S::kOut + S::kBarBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    if (PAIR) {
+    if (PAIR || joins) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.x = PAIR ? 2 : t.splits[0];
         attr[cfg.numAttrs].val.clusterDim.y = 1;
         attr[cfg.numAttrs].val.clusterDim.z = 1;
         ++cfg.numAttrs;
@@ -818,7 +899,7 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     e = cudaLaunchKernelEx(&cfg, fn, L);
     bool early = true;  // a second join comes behind the first, which lets nothing start early
     for (int i = 0; i < count && e == cudaSuccess; ++i) {
-        if (t.splits[i] == 1) continue;
+        if (t.splits[i] == 1 || joins) continue;
         cudaLaunchConfig_t join = {};
         const long long quads = static_cast<long long>(p[i].M) * ((p[i].N + 3) / 4);
         const int threads = t.splits[i] <= 4 ? 1 : (t.splits[i] <= 16 ? 4 : 16), at_once = kJoinThreads / threads;
@@ -848,16 +929,26 @@ cudaError_t launch_shape(const GemmParams* p, int count, const GemmTile& t, cons
 
 bool gemm_fits(int M, int N) { return (static_cast<long long>(M) + 127) / 128 * ((N + 63) / 64) < (1LL << 29); }
 
+bool gemm_joins_in_cluster(const GemmTile& t) { return t.columns <= 128 && (t.splits[0] == 2 || t.splits[0] == 4 || t.splits[0] == 8); }
+
 size_t gemm_part_bytes(int splits, int M, int N) {
     return splits > 1 ? static_cast<size_t>(splits) * M * part_pitch(N) * sizeof(float) : 0;
+}
+
+// Clusters of this kernel's CTAs (one an SM) that the part holds at a time, by CTAs in a cluster: a 152-SM part holds
+// 76 of 2, 36 of 4 and 15 of 8.
+static int clusters_at_a_time(int num_sms, int ctas) {
+    return ctas == 2 ? num_sms / 2 : (ctas == 4 ? num_sms * 36 / 152 : num_sms * 15 / 152);
 }
 
 // The tile shape and split of K that cost least by these figures, in microseconds on a 152-SM part (repeated launches in a
 // graph): the launch with a short tile, a K = 64 step, what a tile takes besides, and the least it takes (its epilogue).
 // From one tile on every SM, K = 64 / 256 / 1024: 7.2 / 8.4 / 12.1 us of 256 x 256 on pairs, 5.4 / 6.3 / 9.2 of 128 x 128,
-// 5.0 / 5.7 / 8.5 of 128 x 64.  A split adds its parts' way through memory and the join: 2432 x 4096 -> 128 19.6 us in tiles of 128 x 128, 11.8
-// with the K of each shared by eight.
-GemmTile gemm_pick_tile(const GemmSize* products, int count, int num_sms) {
+// 5.0 / 5.7 / 8.5 of 128 x 64.  A join in a cluster takes 4.0 / 2.7 / 1.8 us of 128 columns by 2 / 4 / 8, 2.2 / 1.7 / 1.7 of
+// 64; of parts in the workspace 1.8 and their way through memory, and the second launch 4 of a call where the host is what
+// bounds it, nothing in a graph: half is counted.  1000 x 2048 -> 96: 12.3 us whole in a graph, 14.4 as called; by eight in
+// a cluster 8.0 and 10.4; by six through the workspace 8.0 and 14.3.
+GemmTile gemm_pick_tile(const GemmSize* products, int count, bool forward, int num_sms) {
     struct Cost {
         int rows, columns;
         double launch, step, besides, least;
@@ -876,11 +967,15 @@ GemmTile gemm_pick_tile(const GemmSize* products, int count, int num_sms) {
             const double t = static_cast<double>((steps + splits - 1) / splits) * c.step + c.besides;
             return t > c.least ? t : c.least;
         };
+        const auto in_cluster = [&](int splits) { return forward && gemm_joins_in_cluster({c.rows, c.columns, {splits, 1}}); };
         const auto allowed = [&](const GemmSize& p, int splits) {
-            return splits == 1 || (splits <= (p.K + kStepK - 1) / kStepK && tiles(p) * splits <= slots);
+            return splits == 1 || (splits <= (p.K + kStepK - 1) / kStepK &&
+                                   (in_cluster(splits) ? tiles(p) <= clusters_at_a_time(num_sms, splits) : tiles(p) * splits <= slots));
         };
         const auto join = [&](const GemmSize& p, int splits) {
-            return splits > 1 ? 5.0 + static_cast<double>(p.M) * p.N * splits * 8.0 / 4e6 : 0.0;
+            if (splits == 1) return 0.0;
+            if (in_cluster(splits)) return 1.3 + 0.042 * c.columns / splits;
+            return 3.8 + static_cast<double>(p.M) * p.N * splits * 1e-6;
         };
         for (int s0 : kSplits) {
             if (!allowed(products[0], s0)) continue;

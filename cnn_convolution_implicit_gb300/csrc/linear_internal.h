@@ -35,7 +35,8 @@ struct GemmTile {
 struct GemmSize {
     int M, N, K;
 };
-GemmTile gemm_pick_tile(const GemmSize* products, int count, int num_sms);  // count: 1 or 2
+GemmTile gemm_pick_tile(const GemmSize* products, int count, bool forward, int num_sms);  // count: 1 (forward) or 2
+bool gemm_joins_in_cluster(const GemmTile& t);  // of the forward product: its parts take no workspace
 size_t gemm_part_bytes(int splits, int M, int N);
 bool gemm_fits(int M, int N);  // tile counts within 32 bits
 

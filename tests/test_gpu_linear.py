@@ -33,6 +33,9 @@ SIZES = [
     # each tile, whole and with its K shared, rows of y on and off 16 bytes
     (443, 2728, 36), (4603, 271, 32), (42, 432, 10952), (37, 3206, 1835), (4785, 1624, 40), (4639, 1956, 32), (130, 3504, 7040),
     (3652, 129, 5960), (34, 34, 1089), (62, 32, 1072), (35, 1455, 4623), (37, 37, 1658), (39, 32, 2599), (1300, 325, 105),
+    # the K of a tile shared by two, four, eight CTAs that join it, by three that leave parts; few rows with a long odd K
+    (4714, 50, 1664), (4683, 48, 2688), (2127, 36, 921), (42, 1664, 848), (147, 1380, 1344), (34, 2376, 2096), (267, 3492, 7581),
+    (4662, 32, 7376), (148, 3232, 2840), (3362, 135, 3305), (41, 32, 6584), (4638, 50, 7803), (2, 100, 3005),
 ]
 
 GRAD_SIZES = [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 520), (77, 264, 520), (301, 777, 1000),

@@ -170,7 +170,7 @@ def _variants():
     forward, grads = set(), set()
     for M, N, K in SIZES:
         p = cg.LinearPlan(M, N, K)
-        forward.add((p.kernel, p.tile[1], p.tile[2] > 1, N % 8 == 0, K % 8 == 0))
+        forward.add((p.kernel, p.tile[1], p.tile[2], N % 8 == 0, K % 8 == 0))
     for M, N, K in GRAD_SIZES:
         rows_, cols, dx, dw = cg.LinearPlan(M, N, K).grad_tile
         grads.add((cols, dx > 1, dw > 1, K % 8 == 0))
@@ -183,9 +183,9 @@ def test_the_gpu_tests_reach_every_kernel():
     for aligned in (True, False):
         assert any(f[0] == "few_rows" and f[4] == aligned for f in forward)
         for columns in (64, 128, 256):
-            for split in (True, False):
-                if (columns, split) != (256, True):      # pairs share a K rarely: once is enough
-                    assert any(f[0] == "tiles" and f[1:4] == (columns, split, aligned) for f in forward), (columns, split, aligned)
+            for split in (1, 2, 4, 8) if columns < 256 else (1,):      # pairs share a K rarely: once is enough
+                assert any(f[0] == "tiles" and f[1:4] == (columns, split, aligned) for f in forward), (columns, split, aligned)
             assert any(g[0] == columns and g[3] == aligned for g in grads), (columns, aligned)
-    assert any(f[1:3] == (256, True) for f in forward)
+    assert any(f[1] == 256 and f[2] > 1 for f in forward)
+    assert any(f[1] == 64 and f[2] == 3 for f in forward)        # parts in the workspace, not a cluster
     assert any(g[1] and not g[2] for g in grads) and any(g[2] and not g[1] for g in grads) and any(g[1] and g[2] for g in grads)
