@@ -4,6 +4,10 @@ root-mean-square norm and dropout; ctypes binding of conv_linear_*, conv_rms_nor
 
 Argument checks and marshalling only, as in operators.py: every step runs in the library's CUDA
 kernels, on torch's current stream or, with ``stream``, as if that were it.
+
+A backward pass may be captured into a graph with its forward pass.  As for any operator of torch, no graph recorded
+outside of the capture on the same leaves may still be alive then: torch adds to a leaf's gradient on the stream that recorded it
+first, and that stream is not the captured one.
 """
 from __future__ import annotations
 
@@ -27,6 +31,11 @@ def _start():
 
 
 _t = _empty = _empty_like = _bf16 = _f32 = None
+
+
+def _size(n):
+    """A size as the library's 32 bits hold it; one past them stays past every limit (ctypes keeps the low bits)."""
+    return n if -2 ** 31 <= n < 2 ** 31 else 2 ** 31 - 1
 
 
 def _upstream(dy):
@@ -61,7 +70,7 @@ class LinearPlan(_Plan):
     def __init__(self, M, N, K, act="none", x_shape=None):
         L = lib()
         h = ctypes.c_void_p()
-        _check(L.conv_linear_plan_create(ctypes.byref(h), M, N, K, _choice(act, ACTS, "act")), "conv_linear_plan_create")
+        _check(L.conv_linear_plan_create(ctypes.byref(h), _size(M), _size(N), _size(K), _choice(act, ACTS, "act")), "conv_linear_plan_create")
         self._plan = h
         torch = _start()
         self.M, self.N, self.K, self.act = M, N, K, act
@@ -182,7 +191,7 @@ class RmsNormPlan(_Plan):
     def __init__(self, M, C, dtype="bf16", eps=1e-6, x_shape=None):
         L = lib()
         h = ctypes.c_void_p()
-        _check(L.conv_rms_norm_plan_create(ctypes.byref(h), M, C, eps, _choice(dtype, _DTYPES, "dtype")),
+        _check(L.conv_rms_norm_plan_create(ctypes.byref(h), _size(M), _size(C), eps, _choice(dtype, _DTYPES, "dtype")),
                "conv_rms_norm_plan_create")
         self._plan = h
         torch = _start()

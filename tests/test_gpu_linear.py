@@ -68,7 +68,8 @@ def test_forward(size):
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu"])
-@pytest.mark.parametrize("size", [(1, 96, 160), (3, 97, 100), (20, 96, 160), (20, 95, 101), (140, 200, 136), (140, 203, 130), (600, 512, 520)])
+@pytest.mark.parametrize("size", [(1, 96, 160), (3, 97, 100), (20, 96, 160), (20, 95, 101), (140, 200, 136), (140, 203, 130), (600, 512, 520),
+                                  (140, 200, 2100), (140, 203, 2100)])
 def test_every_epilogue(size, act):
     import cnn_convolution_implicit_gb300 as cg
     M, N, K = size
@@ -161,7 +162,8 @@ def test_bad_values_stay_in_their_row_and_column(value, M):
     assert not torch.isfinite(db2[9])
 
 
-@pytest.mark.parametrize("size", [(1, 256, 512), (20, 256, 512), (70, 101, 203), (300, 777, 512), (2000, 512, 256)])
+@pytest.mark.parametrize("size", [(1, 256, 512), (20, 256, 512), (70, 101, 203), (300, 777, 512), (2000, 512, 256),
+                                  (1000, 96, 2048), (2127, 36, 921), (35, 1455, 4623)])
 def test_residual_in_place(size):
     import cnn_convolution_implicit_gb300 as cg
     x, w, b, r, _ = (t.cuda() for t in _inputs(*size, 31))
@@ -378,6 +380,31 @@ def test_a_captured_training_step():
         state[1] += 1
         assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert cg.device_status() == 0
+
+
+def test_threads():
+    """One cached plan, called from several threads with their own streams: each gets the bits of a call by itself."""
+    import threading
+    import cnn_convolution_implicit_gb300 as cg
+    x, w, b, r, dy = (t.cuda() for t in _inputs(140, 200, 2100, 131))
+    want = (cg.linear(x, w, b, "none", r), *cg.linear_backward(dy, x, w), cg.rms_norm(x), *cg.rms_norm_int8(x))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = (cg.linear(x, w, b, "none", r), *cg.linear_backward(dy, x, w), cg.rms_norm(x), *cg.rms_norm_int8(x))
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(p, q) for p, q in zip(want, got)):
+                    wrong.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and cg.device_status() == 0
 
 
 def test_two_streams_at_once():

@@ -124,6 +124,15 @@ def test_binding_refuses():
             make()
 
 
+@pytest.mark.parametrize("past", [1 << 31, (1 << 32) + 5, (1 << 33) + 8])
+def test_sizes_past_32_bits_are_refused(past):
+    """Not taken for what their low bits hold."""
+    for make in (lambda: cg.LinearPlan(past, 8, 8), lambda: cg.LinearPlan(8, past, 8), lambda: cg.LinearPlan(8, 8, past),
+                 lambda: cg.RmsNormPlan(past, 8), lambda: cg.RmsNormPlan(8, past)):
+        with pytest.raises(cg.ConvError):
+            make()
+
+
 def _calls(i):
     x, w, y = OnDevice((4, 16), BF16, i), OnDevice((8, 16), BF16, i), OnDevice((4, 8), BF16, i)
     rstd, state = OnDevice((4,), F32, i), OnDevice((2,), torch.int64, i)
