@@ -61,14 +61,18 @@ template <bool PAIR, int BN, bool TMA>
 struct Shape {
     static constexpr int kCtas = PAIR ? 2 : 1;
     static constexpr int kRowsB = BN / kCtas;            // of B in this CTA
-    static constexpr int kStage = kTileA + kRowsB * 128;
+    static constexpr int kStage = kTileA + kRowsB * 128;  // of K = 64
+    // Such stages that share a barrier: a turn of the MMA warp costs 365 clocks besides its MMAs, which those of K = 64 hide on a
+    // pair (512 clocks) and not in smaller tiles (a step of K = 64 0.22 us there, 0.13 with two to a turn); where only two
+    // turns would fit, one.
+    static constexpr int kSteps = !PAIR && (BN == 64 || TMA) ? 2 : 1;
     static constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
     static constexpr int kThreads = 32 * (kEpilogueWarps + 2);
     static constexpr int kTmemCols = 2 * BN;
     // Each epilogue warp that works has room for a block of outputs; the ring takes the rest.
     static constexpr int kBarBytes = 512 + kEpilogueWarps * 128;  // barriers, the warps' biases
     static constexpr int kOut = TMA ? kBlockBytes : kEdgeBytes;
-    static constexpr int stages(int warps) { return (232448 - kBarBytes - warps * kOut) / kStage; }
+    static constexpr int stages(int warps) { return (232448 - kBarBytes - warps * kOut) / (kSteps * kStage); }
     static constexpr int kMaxStages = stages(8);
     static_assert((2 * kMaxStages + 5 + kEpilogueWarps) * 8 + 8 <= 512, "barriers");
 };
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
         return;
     }
     Bars b;
-    uint8_t* outputs = smem + ring.stages * S::kStage;
+    uint8_t* outputs = smem + ring.stages * S::kSteps * S::kStage;
     b.full = reinterpret_cast<uint64_t*>(outputs + ring.warps * S::kOut);
     b.empty = b.full + S::kMaxStages;
     b.tfull = b.empty + S::kMaxStages;
@@ -652,19 +656,24 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
             const Unit w = unit_at<B_BY_K>(p, u);
             const int m = w.mt * 128 * kCtas + static_cast<int>(rank) * 128, n = w.nt * BN + static_cast<int>(rank) * S::kRowsB;
             const bool a_by_k = B_BY_K && p.a_by_k != 0;  // the forward product's operands both lie by row
-            for (int ks = 0; ks < w.k_count; ++ks) {
+            for (int ks = 0; ks < w.k_count; ks += S::kSteps) {
                 if (!warp_wait(&b.empty[st], ph ^ 1u, abort)) {
                     record_status(L.status, kStatusTimeoutProducer, abort);
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
-                    if (leader) mbar_arrive_expect_tx(&b.full[st], kCtas * S::kStage);
-                    uint8_t* dst = smem + st * S::kStage;
+                    const int steps = min(S::kSteps, w.k_count - ks);
+                    if (leader) mbar_arrive_expect_tx(&b.full[st], kCtas * S::kStage * steps);
                     const uint32_t bar = PAIR ? mapa_shared(smem_addr(&b.full[st]), 0) : 0u;
-                    const int k = (w.k_first + ks) * kStepK;  // past the matrix: zeros
-                    load_operand<PAIR, 128>(a_by_k, dst, &p.map_a, &b.full[st], bar, m, k);
-                    load_operand<PAIR, S::kRowsB>(B_BY_K, dst + kTileA, &p.map_b, &b.full[st], bar, n, k);
+#pragma unroll
+                    for (int i = 0; i < S::kSteps; ++i) {
+                        if (i >= steps) break;
+                        uint8_t* dst = smem + (st * S::kSteps + i) * S::kStage;
+                        const int k = (w.k_first + ks + i) * kStepK;  // past the matrix: zeros
+                        load_operand<PAIR, 128>(a_by_k, dst, &p.map_a, &b.full[st], bar, m, k);
+                        load_operand<PAIR, S::kRowsB>(B_BY_K, dst + kTileA, &p.map_b, &b.full[st], bar, n, k);
+                    }
                 }
                 __syncwarp();
                 ++issued;
@@ -686,7 +695,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
         }
     } else if (warp == kMmaWarp && leader) {
         // ------------------------------------------------------------ MMA
-                const uint32_t base0 = smem_addr(smem);
+        const uint32_t base0 = smem_addr(smem);
         int st = 0, local = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -702,20 +711,22 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
             tc_fence_after();
             const bool a_by_k = B_BY_K && p.a_by_k != 0;
             const uint32_t idesc = idesc_bf16_f32(128 * kCtas, BN) | (a_by_k ? 1u << 15 : 0u) | (B_BY_K ? 1u << 16 : 0u);
-            for (int ks = 0; ks < w.k_count; ++ks) {
+            const int k16 = (p.K - w.k_first * kStepK + 15) >> 4;  // steps of K = 16 to the end of the matrix
+            for (int ks = 0; ks < w.k_count; ks += S::kSteps) {
                 if (!warp_wait_cluster(&b.full[st], ph, abort)) {
                     record_status(L.status, kStatusTimeoutMma, abort);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t base = base0 + st * S::kStage;
+                const uint32_t base = base0 + st * S::kSteps * S::kStage;
                 if (elect_one()) {
-                    const int mmas = min(4, (p.K - (w.k_first + ks) * kStepK + 15) >> 4);
+                    const int mmas = min(4 * min(S::kSteps, w.k_count - ks), k16 - 4 * ks);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 4 * S::kSteps; ++j) {
                         if (j >= mmas) break;
-                        const uint64_t da = operand_desc(a_by_k, base, j), db = operand_desc(B_BY_K, base + kTileA, j);
+                        const uint32_t at = base + j / 4 * S::kStage;
+                        const uint64_t da = operand_desc(a_by_k, at, j % 4), db = operand_desc(B_BY_K, at + kTileA, j % 4);
                         const uint32_t acc = (ks | j) != 0 ? 1u : 0u;
                         if constexpr (PAIR) mma_bf16_pair(tmem + buf * BN, da, db, idesc, acc);
                         else mma_bf16(tmem + buf * BN, da, db, idesc, acc);
@@ -880,7 +891,7 @@ cudaError_t launch_variant(const GemmParams* p, int count, const GemmTile& t, co
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(joins ? L.units : (L.units < slots ? L.units : slots) * S::kCtas));
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = L.ring.stages * S::kStage + L.ring.warps * S::kOut + S::kBarBytes;
+    cfg.dynamicSmemBytes = L.ring.stages * S::kSteps * S::kStage + L.ring.warps * S::kOut + S::kBarBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     if (PAIR || joins) {
