@@ -46,7 +46,9 @@ conv_status launched(cudaError_t e) {
 
 size_t up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-int pitch_of(int n) { return static_cast<int>(up(n, 8)); }  // elements of a row that starts on 16 bytes
+// Elements of a row laid out: on 128 bytes (a box's 128 bytes of a row are then one line of L2, not two) unless that lengthens
+// a short row.
+int pitch_of(int n) { return static_cast<int>(up(n, n < 256 ? 8 : 64)); }
 
 // Workspaces: rows off 16 bytes laid out on them, u, parts of sums.
 struct Workspace {

@@ -62,8 +62,8 @@ struct Shape {
     static constexpr int kCtas = PAIR ? 2 : 1;
     static constexpr int kRowsB = BN / kCtas;            // of B in this CTA
     static constexpr int kStage = kTileA + kRowsB * 128;  // of K = 64
-    // Such stages that share a barrier: a turn of the MMA warp costs 365 clocks besides its MMAs, which those of K = 64 hide on a
-    // pair (512 clocks) and not in smaller tiles (a step of K = 64 0.22 us there, 0.13 with two to a turn); where only two
+    // Such stages that share a barrier: a turn of the MMA warp costs 300 clocks besides its MMAs, which those of K = 64 hide on a
+    // pair (512 clocks) and not in smaller tiles (a step of K = 64 0.24 us there, 0.15 with two to a turn); where only two
     // turns would fit, one.
     static constexpr int kSteps = !PAIR && (BN == 64 || TMA) ? 2 : 1;
     static constexpr int kEpilogueWarps = BN == 256 ? 16 : 8;
@@ -94,11 +94,13 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_addr(bar), 0)) : "memory");
 }
 
-// A bounded wait whose answer is the same in every lane.
+// A bounded wait whose answer is the same in every lane.  (The first look by itself: the loop behind it is rarely entered.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(smem_addr(bar), parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
 }
 
@@ -648,6 +650,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ operands
         long long issued = 0;
+        const bool issuer = elect_one();
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
                     ok = false;
                     break;
                 }
-                if (elect_one()) {
+                if (issuer) {
                     const int steps = min(S::kSteps, w.k_count - ks);
                     if (leader) mbar_arrive_expect_tx(&b.full[st], kCtas * S::kStage * steps);
                     const uint32_t bar = PAIR ? mapa_shared(smem_addr(&b.full[st]), 0) : 0u;
@@ -696,6 +699,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
     } else if (warp == kMmaWarp && leader) {
         // ------------------------------------------------------------ MMA
         const uint32_t base0 = smem_addr(smem);
+        const bool issuer = elect_one();
         int st = 0, local = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -720,7 +724,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
                 }
                 tc_fence_after();
                 const uint32_t base = base0 + st * S::kSteps * S::kStage;
-                if (elect_one()) {
+                if (issuer) {
                     const int mmas = min(4 * min(S::kSteps, w.k_count - ks), k16 - 4 * ks);
 #pragma unroll
                     for (int j = 0; j < 4 * S::kSteps; ++j) {
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(Shape<PAIR, BN, TMA>::kThreads, 1) linear_gemm
                 }
             }
             if (!ok) break;
-            if (elect_one()) commit<PAIR>(&b.tfull[buf]);
+            if (issuer) commit<PAIR>(&b.tfull[buf]);
             __syncwarp();
         }
         if (elect_one()) {
@@ -954,28 +958,37 @@ static int clusters_at_a_time(int num_sms, int ctas) {
 
 // The tile shape and split of K that cost least by these figures, in microseconds on a 152-SM part (repeated launches in a
 // graph): the launch with a short tile, a K = 64 step, what a tile takes besides, and the least it takes (its epilogue).
-// From one tile on every SM, K = 64 / 256 / 1024: 7.2 / 8.4 / 12.1 us of 256 x 256 on pairs, 5.4 / 6.3 / 9.2 of 128 x 128,
-// 5.0 / 5.7 / 8.5 of 128 x 64.  A join in a cluster takes 4.0 / 2.7 / 1.8 us of 128 columns by 2 / 4 / 8, 2.2 / 1.7 / 1.7 of
-// 64; of parts in the workspace 1.8 and their way through memory, and the second launch 4 of a call where the host is what
-// bounds it, nothing in a graph: half is counted.  1000 x 2048 -> 96: 12.3 us whole in a graph, 14.4 as called; by eight in
-// a cluster 8.0 and 10.4; by six through the workspace 8.0 and 14.3.
+// From one tile on every SM, K = 64 / 256 / 1024 / 4096: 6.5 / 7.4 / 10.8 / 23.4 us of 256 x 256 on pairs, 4.9 / 5.6 / 7.7 / 15.7
+// of 128 x 128, 4.3 / 4.8 / 6.8 / 13.9 of 128 x 64; the least is what the epilogue takes where y goes to memory.  A join in a
+// cluster takes 4.0 / 3.1 / 2.3 us of 128 columns by 2 / 4 / 8, 2.6 / 2.2 / 2.0 of 64; of parts in the workspace 2 and their way
+// through memory, and the second launch 4 of a call where the host is what bounds it, nothing in a graph: half is counted.
+// Rows of y off 16 bytes: the last tile's epilogue takes 2 to 4 longer, a cluster's or the join kernel's shares of it 1 to 3.
+// Rows of K off 128 bytes: a box's part of a row lies in two lines of L2, and a step takes 0.42 / 0.38 / 0.29 instead of 0.27 /
+// 0.20 / 0.155 (4000 x 1000 -> 1000, 1101 x 2504 -> 1544).
+// The gradients' operands come in smaller boxes, and their steps take longer in small tiles when all SMs run: dx and dw of
+// 3935 x 2648 -> 1656 82 us in 256 x 256 and 111 in 128 x 128.
+// 1000 x 2048 -> 96: 9.4 us whole in a graph, by four in a cluster 7.6, by six through the workspace 7.5.
 GemmTile gemm_pick_tile(const GemmSize* products, int count, bool forward, int num_sms) {
     struct Cost {
         int rows, columns;
         double launch, step, besides, least;
     };
-    constexpr Cost kCosts[3] = {{256, 256, 5.9, 0.29, 1.0, 3.0}, {128, 128, 4.5, 0.235, 0.7, 2.0}, {128, 64, 4.2, 0.22, 0.6, 1.2}};
+    constexpr Cost kForward[3] = {{256, 256, 5.6, 0.27, 0.8, 3.0}, {128, 128, 4.35, 0.20, 0.6, 2.0}, {128, 64, 3.7, 0.155, 0.4, 1.2}};
+    constexpr Cost kAcrossLines[3] = {{256, 256, 5.6, 0.42, 0.8, 3.0}, {128, 128, 4.35, 0.38, 0.6, 2.0}, {128, 64, 3.7, 0.29, 0.4, 1.2}};
+    constexpr Cost kGradients[3] = {{256, 256, 5.9, 0.29, 1.0, 3.0}, {128, 128, 4.5, 0.235, 0.7, 2.0}, {128, 64, 4.2, 0.22, 0.6, 1.2}};
     constexpr int kSplits[14] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64};
     double best = 0.0;
     GemmTile pick = {};
-    for (const Cost& c : kCosts) {
+    const bool lines = products[0].K % 64 == 0 || (products[0].K % 8 != 0 && products[0].K >= 256);  // laid out on 128 bytes
+    for (const Cost& c : !forward ? kGradients : (lines ? kForward : kAcrossLines)) {
         const long long slots = c.rows == 256 ? num_sms / 2 : num_sms;
         const auto tiles = [&](const GemmSize& p) {
             return (static_cast<long long>(p.M) + c.rows - 1) / c.rows * ((p.N + c.columns - 1) / c.columns);
         };
         const auto each = [&](const GemmSize& p, int splits) {
             const long long steps = (static_cast<long long>(p.K) + kStepK - 1) / kStepK;
-            const double t = static_cast<double>((steps + splits - 1) / splits) * c.step + c.besides;
+            const double step = c.columns == 128 && p.N % 8 != 0 && c.step < 0.235 ? 0.235 : c.step;  // one to a turn (kSteps)
+            const double t = static_cast<double>((steps + splits - 1) / splits) * step + c.besides;
             return t > c.least ? t : c.least;
         };
         const auto in_cluster = [&](int splits) { return forward && gemm_joins_in_cluster({c.rows, c.columns, {splits, 1}}); };
@@ -983,9 +996,9 @@ GemmTile gemm_pick_tile(const GemmSize* products, int count, bool forward, int n
             return splits == 1 || (splits <= (p.K + kStepK - 1) / kStepK &&
                                    (in_cluster(splits) ? tiles(p) <= clusters_at_a_time(num_sms, splits) : tiles(p) * splits <= slots));
         };
-        const auto join = [&](const GemmSize& p, int splits) {
-            if (splits == 1) return 0.0;
-            if (in_cluster(splits)) return 1.3 + 0.042 * c.columns / splits;
+        const auto finish = [&](const GemmSize& p, int splits) {
+            if (splits == 1) return forward && p.N % 8 != 0 ? 1.2 : 0.0;
+            if (in_cluster(splits)) return 1.7 + 0.036 * c.columns / splits + (p.N % 4 != 0 ? 1.0 : 0.0);
             return 3.8 + static_cast<double>(p.M) * p.N * splits * 1e-6;
         };
         for (int s0 : kSplits) {
@@ -1001,7 +1014,7 @@ GemmTile gemm_pick_tile(const GemmSize* products, int count, bool forward, int n
                     const double t = static_cast<double>(n0) * e0 + static_cast<double>(all - n0) * e1;
                     longest = t > longest ? t : longest;
                 }
-                const double cost = c.launch + longest + join(products[0], s0) + (count == 1 ? 0.0 : join(products[1], s1));
+                const double cost = c.launch + longest + finish(products[0], s0) + (count == 1 ? 0.0 : finish(products[1], s1));
                 if (pick.rows == 0 || cost < best) {
                     best = cost;
                     pick = {c.rows, c.columns, {s0, s1}};

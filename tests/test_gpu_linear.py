@@ -35,7 +35,9 @@ SIZES = [
     (3652, 129, 5960), (34, 34, 1089), (62, 32, 1072), (35, 1455, 4623), (37, 37, 1658), (39, 32, 2599), (1300, 325, 105),
     # the K of a tile shared by two, four, eight CTAs that join it, by three that leave parts; few rows with a long odd K
     (4714, 50, 1664), (4683, 48, 2688), (2127, 36, 921), (42, 1664, 848), (147, 1380, 1344), (34, 2376, 2096), (267, 3492, 7581),
-    (4662, 32, 7376), (148, 3232, 2840), (3362, 135, 3305), (41, 32, 6584), (4638, 50, 7803), (2, 100, 3005),
+    (4662, 32, 7376), (148, 3232, 2840), (3362, 135, 3305), (41, 32, 6584),
+    (931, 1280, 336), (132, 3400, 5392), (38, 2912, 2587), (39, 1392, 3928), (40, 2476, 2166), (276, 3490, 209), (2732, 372, 2488), (264, 2480, 3152),
+    (3664, 68, 1352), (1646, 75, 2488), (4638, 50, 7803), (2, 100, 3005),
 ]
 
 GRAD_SIZES = [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 520), (77, 264, 520), (301, 777, 1000),
@@ -43,7 +45,8 @@ GRAD_SIZES = [(1, 1, 1), (1, 520, 264), (3, 33, 70), (20, 96, 160), (64, 1000, 5
               # each tile, whole, with the K of dx, of dw or of both shared
               (49, 48, 5304), (39, 32, 6635), (4210, 32, 226), (34, 1984, 518), (705, 33, 8624), (758, 33, 8748),
               (2246, 57, 2792), (58, 3120, 1922), (1198, 36, 32), (34, 1216, 36), (2549, 3552, 39), (1397, 52, 42),
-              (37, 2068, 440), (4648, 32, 3238), (3740, 32, 3824), (1925, 40, 43), (41, 2244, 36), (35, 1704, 48), (2256, 34, 32), (5647, 9421, 8)]
+              (37, 2068, 440), (4648, 32, 3238), (3740, 32, 3824), (1925, 40, 43), (41, 2244, 36), (35, 1704, 48), (2256, 34, 32), (5647, 9421, 8),
+              (90, 2040, 16), (35, 399, 2765), (1943, 47, 970), (2887, 36, 1088), (33, 2132, 856), (885, 3524, 466), (988, 3024, 664)]
 
 
 @pytest.mark.parametrize("size", SIZES)
