@@ -15,7 +15,7 @@
 //                       and commits.  (A loop of one lane only, its operands in the registers of a divergent
 //                       thread, took 95 clocks an MMA and 700 a stage of 512 clocks of MMAs: 19456 x 4096 x 4096
 //                       376 us, and 328 as it is, 1,988 TFLOP/s.)
-//   last                fills the ring of (A, B) stages, K = 64 each, by TMA
+//   last                fills the ring of (A, B) stages, K = 64 or 128 each, by TMA
 // Tensor memory holds two accumulators, so the epilogue of one unit overlaps the next one's MMAs.
 //
 // PAIR: two SMs share a 256 x 256 tile (tcgen05.mma.cta_group::2): each loads its own 128 rows of A and
@@ -44,7 +44,7 @@ namespace {
 
 constexpr int kBlockCols = 64, kBlockBytes = 32 * 128;  // 32 rows x 64 columns of outputs
 constexpr int kEdgeBytes = 5 * 1024;                       // room for them where rows start off 16 bytes
-constexpr int kStepK = 64;       // K of one stage: 128 bytes of a row
+constexpr int kStepK = 64;       // K of a step: 128 bytes of a row
 constexpr int kTileA = 128 * 128;  // bytes of A in a stage: 128 rows
 
 // What a launch fixes besides the operands.
@@ -963,8 +963,8 @@ static int clusters_at_a_time(int num_sms, int ctas) {
 // cluster takes 4.0 / 3.1 / 2.3 us of 128 columns by 2 / 4 / 8, 2.6 / 2.2 / 2.0 of 64; of parts in the workspace 2 and their way
 // through memory, and the second launch 4 of a call where the host is what bounds it, nothing in a graph: half is counted.
 // Rows of y off 16 bytes: the last tile's epilogue takes 2 to 4 longer, a cluster's or the join kernel's shares of it 1 to 3.
-// Rows of K off 128 bytes: a box's part of a row lies in two lines of L2, and a step takes 0.42 / 0.38 / 0.29 instead of 0.27 /
-// 0.20 / 0.155 (4000 x 1000 -> 1000, 1101 x 2504 -> 1544).
+// Rows of K off 64 bytes: a box's part of a row lies in two lines of L2, and a step takes 0.42 / 0.38 / 0.29 instead of 0.27 /
+// 0.20 / 0.155 (4000 x 1000 -> 1000, 1101 x 2504 -> 1544; 8192 x 4096 -> 4096 145 us, 4128 150, 4104 195).
 // The gradients' operands come in smaller boxes, and their steps take longer in small tiles when all SMs run: dx and dw of
 // 3935 x 2648 -> 1656 82 us in 256 x 256 and 111 in 128 x 128.
 // 1000 x 2048 -> 96: 9.4 us whole in a graph, by four in a cluster 7.6, by six through the workspace 7.5.
@@ -979,7 +979,7 @@ GemmTile gemm_pick_tile(const GemmSize* products, int count, bool forward, int n
     constexpr int kSplits[14] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 64};
     double best = 0.0;
     GemmTile pick = {};
-    const bool lines = products[0].K % 64 == 0 || (products[0].K % 8 != 0 && products[0].K >= 256);  // laid out on 128 bytes
+    const bool lines = products[0].K % 32 == 0 || (products[0].K % 8 != 0 && products[0].K >= 256);  // laid out on 128 bytes
     for (const Cost& c : !forward ? kGradients : (lines ? kForward : kAcrossLines)) {
         const long long slots = c.rows == 256 ? num_sms / 2 : num_sms;
         const auto tiles = [&](const GemmSize& p) {
