@@ -113,15 +113,18 @@ cudaError_t launch(const FewParams& p, cudaStream_t stream) {
 }  // namespace
 
 // This kernel and the tiles of many rows, microseconds in a graph with cold weights:
-//   8 x 4096 -> 4096 8.3 and 13.4    16 x 4096 -> 4096 10.4 and 13.4   24 x 4096 -> 4096 14.0 and 13.4   32 x 1024 -> 1024 5.4 and 8.4
-//   8 x 16384 -> 4096 24.4 and 29.7  16 x 16384 -> 4096 30.3 and 29.7  16 x 4096 -> 16384 33.7 and 26.8
-// x is read again by every 16 columns, so with more rows and weights the tiles win.  Rows of K off 16 bytes take two loads and
-// a shift for each item, and a time that goes by K: 8 x 2045 -> 2048 14.2 and 15.8, 8 x 6661 -> 1592 39 and 19 (with two launches
-// more: rows laid out first, parts joined).
+//   8 x 4096 -> 4096 8.6 and 14.5    16 x 4096 -> 4096 10.1 and 12.8   24 x 4096 -> 4096 14.0 and 13.4   32 x 1024 -> 1024 4.9 and 7.1
+//   8 x 16384 -> 4096 24.4 and 29.7  16 x 8192 -> 4096 17.5 and 18.5   16 x 4096 -> 16384 33.7 and 26.8  32 x 2048 -> 2048 8.4 and 8.6
+//   8 x 4096 -> 16384 25.5 and 40.4  16 x 16384 -> 1024 18.7 and 12.1  32 x 4096 -> 1024 12.8 and 9.3
+// x is read again by every 16 columns, so with more rows and weights the tiles win, and where K is long, which they share.
+// Rows of K off 16 bytes take two loads and a shift for each item, and a time that goes by K and M; the tiles take a launch
+// more, that lays rows out (4 of a call where the host bounds it):
+//   8 x 2045 -> 2048 13.8 and 12.8   8 x 2500 -> 512 16.6 and 9.4      16 x 1003 -> 1000 8.2 and 8.2     16 x 2045 -> 2048 18.1 and 12.8
+//   8 x 1027 -> 4096 9.0 and 12.9    32 x 501 -> 300 7.0 and 8.2       32 x 1003 -> 1000 11.1 and 8.0
 bool linear_use_few(int M, int N, int K) {
-    if (K % 8 != 0 && K > 3000) return false;
+    if (K % 8 != 0 && K > (M <= 8 ? 2300 : (M <= 16 ? 1500 : 1200))) return false;
     const long long weights = static_cast<long long>(N) * K;
-    return M <= 8 || (M <= 16 && weights <= 1LL << 25) || (M <= 32 && weights <= 1LL << 22);
+    return M <= 8 || (M <= 16 && weights <= 1LL << 25 && K <= 8192) || (M <= 32 && weights <= 1LL << 22 && K <= 3000);
 }
 
 cudaError_t launch_linear_few(const FewParams& p, cudaStream_t stream) {
