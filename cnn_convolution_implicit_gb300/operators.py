@@ -21,12 +21,15 @@ _DTYPES = {"f32": CONV_F32, "bf16": CONV_BF16}
 _t = None
 _raw_stream = None
 _current_device = None
+_forward_ad = None
 
 
 def _torch():
-    global _t, _raw_stream, _current_device
+    global _t, _raw_stream, _current_device, _forward_ad
     if _t is None:
         import torch
+        from torch.autograd import forward_ad
+        _forward_ad = forward_ad
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _current_device = torch._C._cuda_getDevice
         _t = torch
@@ -61,6 +64,16 @@ def _need(t, name, shape, dtype, dev):
 def _need_any(t, name, dtypes):
     if not t.is_cuda or t.dtype not in dtypes or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor of %s" % (name, " or ".join(str(d) for d in dtypes)))
+
+
+def _refuse_tangents(*tensors):
+    """Raises for a tensor with a tangent: the operators have no forward-mode derivative, and their results would
+    silently be without one."""
+    if _forward_ad._current_level < 0:  # no level is open: none has one
+        return
+    for t in tensors:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("the operators have no forward-mode derivative: detach the tensor from its tangent")
 
 
 def _ptr(t):
@@ -339,6 +352,7 @@ def _norm_function():
             @once_differentiable
             def backward(ctx, dy, _):
                 x, gamma, beta, stats = ctx.saved_tensors
+                _refuse_tangents(dy)
                 dy = dy.contiguous()
                 if dy.data_ptr() % 16:  # a slice of a larger tensor
                     dy = dy.clone()
@@ -355,11 +369,12 @@ def group_norm(x, groups, gamma=None, beta=None, eps=1e-5, act="none", y=None, s
 
     Differentiable: where torch records gradients and x, gamma or beta requires one, the result has
     its backward pass (group_norm_backward; once, and not with ``y`` given).  The plans and the
-    8-bit forms record none."""
+    8-bit forms record none.  A tensor with a forward-mode tangent is refused."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return group_norm(x, groups, gamma, beta, eps, act, y, stats)
     plan = _norm_plan(x, groups, eps, act)
+    _refuse_tangents(x, gamma, beta)
     if (x.requires_grad or (gamma is not None and gamma.requires_grad) or
             (beta is not None and beta.requires_grad)) and _t.is_grad_enabled():
         if y is not None:
@@ -386,7 +401,9 @@ def group_norm_backward(dy, x, stats, groups, gamma=None, beta=None, eps=1e-5, a
     if stream is not None:
         with _torch().cuda.stream(stream):
             return group_norm_backward(dy, x, stats, groups, gamma, beta, eps, act)
-    return _norm_plan(x, groups, eps, act).backward(dy, x, stats, gamma, beta)
+    plan = _norm_plan(x, groups, eps, act)
+    _refuse_tangents(dy, x, stats, gamma, beta)
+    return plan.backward(dy, x, stats, gamma, beta)
 
 
 def _int8_plan(x, w, act, out):

@@ -15,7 +15,7 @@ import ctypes
 
 from . import binding, operators as _ops
 from .binding import CONV_BF16, CONV_F32, _plan_status, lib
-from .operators import ACTS, _DTYPES, _check, _choice, _need, _need_any, _ptr, _refuse_device, _torch, _torch_dtypes, _workspace
+from .operators import ACTS, _DTYPES, _check, _choice, _need, _need_any, _ptr, _refuse_device, _refuse_tangents, _torch, _torch_dtypes, _workspace
 
 
 LINEAR_KERNELS = {0: "few_rows", 1: "tiles"}
@@ -40,6 +40,7 @@ def _size(n):
 
 def _upstream(dy):
     """A gradient as autograd hands it over, as the kernels take it."""
+    _refuse_tangents(dy)
     dy = dy.contiguous()
     return dy.clone() if dy.data_ptr() % 16 else dy  # a slice of a larger tensor
 
@@ -422,11 +423,13 @@ def linear(x, w, bias=None, act="none", residual=None, y=None, z=None, stream=No
     the result's buffer, may be the residual itself.
 
     Differentiable: where torch records gradients and x, w, bias or residual requires one, the result
-    has its backward pass (once, and not with ``y`` or ``z`` given).  The plans record none."""
+    has its backward pass (once, and not with ``y`` or ``z`` given).  The plans record none.  A tensor with a
+    forward-mode tangent is refused."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return linear(x, w, bias, act, residual, y, z)
     plan = _linear_plan(x, w, act)
+    _refuse_tangents(x, w, bias, residual)
     if (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
             (residual is not None and residual.requires_grad)) and _t.is_grad_enabled():
         if y is not None or z is not None:
@@ -441,7 +444,9 @@ def linear_backward(dy, x, w, z=None, act="none", stream=None):
     if stream is not None:
         with _torch().cuda.stream(stream):
             return linear_backward(dy, x, w, z, act)
-    return _linear_plan(x, w, act).backward(dy, x, w, z)
+    plan = _linear_plan(x, w, act)
+    _refuse_tangents(dy, x, w, z)
+    return plan.backward(dy, x, w, z)
 
 
 def rms_norm(x, gamma=None, residual=None, eps=1e-6, h=None, rstd=None, stream=None):
@@ -451,11 +456,12 @@ def rms_norm(x, gamma=None, residual=None, eps=1e-6, h=None, rstd=None, stream=N
 
     Differentiable: where torch records gradients and x, gamma or residual requires one, the results
     have their backward pass (once, and not with ``h`` given).  The plans and the 8-bit form
-    record none."""
+    record none.  A tensor with a forward-mode tangent is refused."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return rms_norm(x, gamma, residual, eps, h, rstd)
     plan = _rms_plan(x, eps)
+    _refuse_tangents(x, gamma, residual)
     if (x.requires_grad or (gamma is not None and gamma.requires_grad) or
             (residual is not None and residual.requires_grad)) and _t.is_grad_enabled():
         if h is not None:
@@ -484,7 +490,9 @@ def rms_norm_backward(dy, h, rstd, gamma=None, dh=None, stream=None):
     if stream is not None:
         with _torch().cuda.stream(stream):
             return rms_norm_backward(dy, h, rstd, gamma, dh)
-    return _rms_plan(h, 1e-6).backward(dy, h, rstd, gamma, dh)  # eps is in rstd already
+    plan = _rms_plan(h, 1e-6)  # eps is in rstd already
+    _refuse_tangents(dy, h, rstd, gamma, dh)
+    return plan.backward(dy, h, rstd, gamma, dh)
 
 
 def _dropout(x, p, state, residual=None, y=None):
@@ -518,12 +526,14 @@ def dropout(x, p, state, residual=None, y=None, stream=None):
     on for a new one, in a captured graph too.  ``y``, the result's buffer, may be x or the residual itself.
 
     Differentiable: where torch records gradients and x or residual requires one, the result has its
-    backward pass (dropout_backward; once, and not with ``y`` given)."""
+    backward pass (dropout_backward; once, and not with ``y`` given).  A tensor with a forward-mode
+    tangent is refused."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return dropout(x, p, state, residual, y)
     if _t is None:
         _start()
+    _refuse_tangents(x, residual)
     if (x.requires_grad or (residual is not None and residual.requires_grad)) and _t.is_grad_enabled():
         if y is not None:
             raise ValueError("y cannot be given where the result's gradient is recorded")
