@@ -157,6 +157,14 @@ def other_device(dev, current):
                       "torch.cuda.device(%d)" % (dev, current, dev))
 
 
+def _written(t):
+    """Tells autograd that a call writes ``t``, a buffer of its caller's, as any operation in place does: a backward
+    pass that saved it before raises instead of reading what the call left there."""
+    import torch
+    if not t.is_inference():  # those keep no versions
+        torch._C._increment_version((t,))
+
+
 def _need_current(dev):
     """A tensor's device has to be the current one: a plan is made for the current device, and the
     library launches there (and refuses a plan of another)."""
@@ -283,6 +291,8 @@ class ConvPlan:
         elif tuple(y.shape) != (N, self.H_out, self.W_out, C_out) or y.dtype != self.out_dtype() or \
                 not y.is_contiguous():
             raise ValueError("y has the wrong shape, dtype or layout")
+        else:
+            _written(y)
         if stream is None:
             stream = torch.cuda.current_stream(x.device)
         bptr = bias.data_ptr() if (self.bias and bias is not None) else None
@@ -375,6 +385,7 @@ class BlockPlan:
             y = self.empty_output(x.device)
         else:
             need(y, "y", (N, self.H_out, self.W_out, C_out), torch.bfloat16)
+            _written(y)
         if stream is None:
             stream = torch.cuda.current_stream(x.device)
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731

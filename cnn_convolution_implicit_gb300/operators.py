@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 
 from . import binding
-from .binding import CONV_BF16, CONV_F32, ConvError, _plan_status, lib
+from .binding import CONV_BF16, CONV_F32, ConvError, _plan_status, _written, lib
 
 ACTS = {"none": 0, "relu": 1, "silu": 2}
 INT8_KERNELS = {0: "few_rows", 1: "mid_rows", 2: "tiles"}
@@ -74,6 +74,12 @@ def _refuse_tangents(*tensors):
     for t in tensors:
         if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
             raise ValueError("the operators have no forward-mode derivative: detach the tensor from its tangent")
+
+
+def _buffer(t, name, shape, dtype, dev):
+    """_need of a buffer that the call writes."""
+    _need(t, name, shape, dtype, dev)
+    _written(t)
 
 
 def _ptr(t):
@@ -143,10 +149,12 @@ class GroupNormPlan:
             with _t.cuda.stream(stream):
                 return self.forward(x, gamma, beta, y, stats)
         dev = self._inputs(x, gamma, beta, stats)
+        if stats is not None:
+            _written(stats)
         if y is None:
             y = _t.empty_like(x)
         else:
-            _need(y, "y", self.shape, self.torch_dtype, dev)
+            _buffer(y, "y", self.shape, self.torch_dtype, dev)
         ws = _workspace(self.workspace_bytes["forward"], dev)
         _check(self._L.conv_group_norm_forward(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(),
                                                _ptr(stats), _ptr(ws), _raw_stream(dev)), "conv_group_norm_forward")
@@ -160,14 +168,16 @@ class GroupNormPlan:
             with _t.cuda.stream(stream):
                 return self.forward_int8(x, gamma, beta, q, scale, stats)
         dev = self._inputs(x, gamma, beta, stats)
+        if stats is not None:
+            _written(stats)
         if q is None:
             q = _t.empty(self.shape, dtype=_t.int8, device=dev)
         else:
-            _need(q, "q", self.shape, _t.int8, dev)
+            _buffer(q, "q", self.shape, _t.int8, dev)
         if scale is None:
             scale = _t.empty(self._pixels, dtype=_t.float32, device=dev)
         else:
-            _need(scale, "scale", self._pixels, _t.float32, dev)
+            _buffer(scale, "scale", self._pixels, _t.float32, dev)
         ws = _workspace(self.workspace_bytes["forward_int8"], dev)
         _check(self._L.conv_group_norm_forward_int8(self._plan, x.data_ptr(), _ptr(gamma), _ptr(beta), q.data_ptr(),
                                                     scale.data_ptr(), _ptr(stats), _ptr(ws), _raw_stream(dev)),
@@ -188,7 +198,7 @@ class GroupNormPlan:
         if dx is None:
             dx = _t.empty_like(x)
         else:
-            _need(dx, "dx", self.shape, self.torch_dtype, dev)
+            _buffer(dx, "dx", self.shape, self.torch_dtype, dev)
         if not affine_grads:
             if dgamma is not None or dbeta is not None:
                 raise ValueError("dgamma and dbeta are not written without affine_grads")
@@ -196,11 +206,11 @@ class GroupNormPlan:
             if dgamma is None:
                 dgamma = _t.empty(self._channels, dtype=_t.float32, device=dev)
             else:
-                _need(dgamma, "dgamma", self._channels, _t.float32, dev)
+                _buffer(dgamma, "dgamma", self._channels, _t.float32, dev)
             if dbeta is None:
                 dbeta = _t.empty(self._channels, dtype=_t.float32, device=dev)
             else:
-                _need(dbeta, "dbeta", self._channels, _t.float32, dev)
+                _buffer(dbeta, "dbeta", self._channels, _t.float32, dev)
         ws = _workspace(self.workspace_bytes["backward"], dev)
         _check(self._L.conv_group_norm_backward(self._plan, dy.data_ptr(), x.data_ptr(), stats.data_ptr(), _ptr(gamma),
                                                 _ptr(beta), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta),
@@ -263,7 +273,7 @@ class Int8MatmulPlan:
         if bias is not None:
             _need(bias, "bias", self._cols, _t.float32, dev)
         if y is not None:
-            _need(y, "y", self._y, self.torch_dtype, dev)
+            _buffer(y, "y", self._y, self.torch_dtype, dev)
         return dev
 
     def forward(self, x, x_scale, w, w_scale, bias=None, y=None, stream=None):

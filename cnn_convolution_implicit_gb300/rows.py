@@ -15,7 +15,7 @@ import ctypes
 
 from . import binding, operators as _ops
 from .binding import CONV_BF16, CONV_F32, _plan_status, lib
-from .operators import ACTS, _DTYPES, _check, _choice, _need, _need_any, _ptr, _refuse_device, _refuse_tangents, _torch, _torch_dtypes, _workspace
+from .operators import ACTS, _DTYPES, _buffer, _check, _choice, _need, _need_any, _ptr, _refuse_device, _refuse_tangents, _torch, _torch_dtypes, _workspace
 
 
 LINEAR_KERNELS = {0: "few_rows", 1: "tiles"}
@@ -114,11 +114,11 @@ class LinearPlan(_Plan):
                     not residual.is_contiguous():
                 _need(residual, "residual", shape, _bf16, dev)
         if z is not None:
-            _need(z, "z", shape, _bf16, dev)
+            _buffer(z, "z", shape, _bf16, dev)
         if y is None:
             y = _empty(shape, dtype=_bf16, device=dev) if residual is None else _empty_like(residual)
         else:
-            _need(y, "y", shape, _bf16, dev)
+            _buffer(y, "y", shape, _bf16, dev)
         ws = _workspace(self._forward_bytes, dev) if self._forward_bytes else None
         status = self._forward(self._plan, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
                                None if residual is None else residual.data_ptr(), y.data_ptr(),
@@ -163,7 +163,7 @@ class LinearPlan(_Plan):
             if given is not None:
                 if not wanted:
                     raise ValueError("%s is not written without need" % name)
-                _need(given, name, shape, dtype, dev)
+                _buffer(given, name, shape, dtype, dev)
         if dx is None and need_x:
             dx = _empty(self._x, dtype=_bf16, device=dev) if x is None else _empty_like(x)
         if dw is None and need_w:
@@ -225,11 +225,11 @@ class RmsNormPlan(_Plan):
             if h is None:
                 h = _empty_like(x)
             else:
-                _need(h, "h", shape, dtype, dev)
+                _buffer(h, "h", shape, dtype, dev)
         elif h is not None:
             raise ValueError("h is written with a residual alone: without one it is x")
         if rstd is not None:
-            _need(rstd, "rstd", self._rows, _f32, dev)
+            _buffer(rstd, "rstd", self._rows, _f32, dev)
         return dev, h
 
     def forward(self, x, gamma=None, residual=None, y=None, h=None, rstd=None, stream=None):
@@ -242,7 +242,7 @@ class RmsNormPlan(_Plan):
         if y is None:
             y = _empty_like(x)
         else:
-            _need(y, "y", self.shape, self.torch_dtype, dev)
+            _buffer(y, "y", self.shape, self.torch_dtype, dev)
         status = self._forward(self._plan, x.data_ptr(), None if residual is None else residual.data_ptr(),
                                None if gamma is None else gamma.data_ptr(), y.data_ptr(), None if h is None else h.data_ptr(),
                                None if rstd is None else rstd.data_ptr(), _ops._raw_stream(dev))
@@ -261,11 +261,11 @@ class RmsNormPlan(_Plan):
         if q is None:
             q = _empty(self.shape, dtype=_t.int8, device=dev)
         else:
-            _need(q, "q", self.shape, _t.int8, dev)
+            _buffer(q, "q", self.shape, _t.int8, dev)
         if scale is None:
             scale = _empty(self._rows, dtype=_f32, device=dev)
         else:
-            _need(scale, "scale", self._rows, _f32, dev)
+            _buffer(scale, "scale", self._rows, _f32, dev)
         status = self._forward_int8(self._plan, x.data_ptr(), _ptr(residual), _ptr(gamma), q.data_ptr(), scale.data_ptr(),
                                     _ptr(h), _ptr(rstd), _ops._raw_stream(dev))
         if status:
@@ -294,13 +294,13 @@ class RmsNormPlan(_Plan):
         if dx is None:
             dx = _empty_like(dy)
         else:
-            _need(dx, "dx", shape, dtype, dev)
+            _buffer(dx, "dx", shape, dtype, dev)
         ws = None
         if gamma_grad:
             if dgamma is None:
                 dgamma = _empty(self._cols, dtype=_f32, device=dev)
             else:
-                _need(dgamma, "dgamma", self._cols, _f32, dev)
+                _buffer(dgamma, "dgamma", self._cols, _f32, dev)
             ws = _workspace(self._backward_bytes, dev) if self._backward_bytes else None
         elif dgamma is not None:
             raise ValueError("dgamma is not written without gamma_grad")
@@ -510,7 +510,7 @@ def _dropout(x, p, state, residual=None, y=None):
     if y is None:
         y = _empty_like(x)
     else:
-        _need(y, "y", shape, dtype, dev)
+        _buffer(y, "y", shape, dtype, dev)
     status = (binding._lib or lib()).conv_dropout(x.data_ptr(), None if residual is None else residual.data_ptr(),
                                                   CONV_BF16 if dtype is _bf16 else CONV_F32, x.numel(), p, state.data_ptr(),
                                                   y.data_ptr(), _ops._raw_stream(dev))
