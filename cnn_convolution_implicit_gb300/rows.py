@@ -22,11 +22,12 @@ LINEAR_KERNELS = {0: "few_rows", 1: "tiles"}
 
 
 def _start():
-    """torch, and what every call takes from it."""
+    """torch, and what every call takes from it.  _t is set last: other threads take the rest to be there with it."""
     global _t, _empty, _empty_like, _bf16, _f32
     if _t is None:
-        _t = _torch()
-        _empty, _empty_like, _bf16, _f32 = _t.empty, _t.empty_like, _t.bfloat16, _t.float32
+        torch = _torch()
+        _empty, _empty_like, _bf16, _f32 = torch.empty, torch.empty_like, torch.bfloat16, torch.float32
+        _t = torch
     return _t
 
 
