@@ -387,6 +387,7 @@ def _function(name):
                 out = plan.forward(x, gamma, residual, rstd=rstd)
                 ctx.save_for_backward(x if residual is None else out[1], gamma, rstd)
                 ctx.mark_non_differentiable(rstd)
+                ctx.set_materialize_grads(False)  # an output that nobody used would bring a gradient of zeros to write and read
                 ctx.plan = plan
                 return (out, rstd) if residual is None else out + (rstd,)
 
@@ -395,8 +396,11 @@ def _function(name):
             def backward(ctx, dy, *more):
                 h, gamma, rstd = ctx.saved_tensors
                 need_x, need_gamma, need_r, _ = ctx.needs_input_grad
-                dh = _upstream(more[0]) if len(more) > 1 else None
-                dx, dgamma = ctx.plan.backward(_upstream(dy), h, rstd, gamma, dh, gamma_grad=need_gamma)
+                dh = _upstream(more[0]) if len(more) > 1 and more[0] is not None else None
+                if dy is not None:
+                    dx, dgamma = ctx.plan.backward(_upstream(dy), h, rstd, gamma, dh, gamma_grad=need_gamma)
+                else:  # y played no part
+                    dx, dgamma = dh, torch.zeros_like(gamma) if need_gamma else None
                 return dx if need_x else None, dgamma, dx if need_r else None, None
 
         class Dropout(torch.autograd.Function):
