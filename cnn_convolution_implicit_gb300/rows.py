@@ -364,9 +364,10 @@ def _function(name):
         class Linear(torch.autograd.Function):
             @staticmethod
             def forward(ctx, x, w, bias, residual, plan):
-                z = torch.empty(plan._y, dtype=x.dtype, device=x.device) if plan.act != "none" else None
+                need_x, need_w, need_b = ctx.needs_input_grad[:3]
+                z = torch.empty(plan._y, dtype=x.dtype, device=x.device) if plan.act != "none" and (need_x or need_w or need_b) else None
                 y = plan.forward(x, w, bias, residual, z=z)
-                ctx.save_for_backward(x, w, z)
+                ctx.save_for_backward(x if need_w else None, w if need_x else None, z)  # what the gradients wanted read
                 ctx.plan = plan
                 return y
 

@@ -1,4 +1,5 @@
-"""What a recorded call keeps and what its backward pass reads: a gradient that nobody gave is not made up of zeros."""
+"""What a recorded call keeps and what its backward pass reads: a gradient that nobody gave is not made up of zeros, and no
+tensor stays alive that no wanted gradient reads."""
 import pytest
 import torch
 
@@ -77,3 +78,22 @@ def test_both_outputs_used(upstream):
     y, h = cg.rms_norm(leaf, gamma, r)
     torch.autograd.backward([y, h], [dy, r])
     assert torch.equal(leaf.grad, want[0])
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("wanted", ["x", "w", "bias", "residual"])
+def test_linear_keeps_what_its_gradients_read(act, wanted):
+    import cnn_convolution_implicit_gb300 as cg
+    g = torch.Generator(device="cuda").manual_seed(6)
+    t = {"x": torch.randn(12, 40, device="cuda", generator=g).to(BF16), "w": torch.randn(24, 40, device="cuda", generator=g).to(BF16),
+         "bias": torch.randn(24, device="cuda", generator=g), "residual": torch.randn(12, 24, device="cuda", generator=g).to(BF16)}
+    dy, z = torch.randn(12, 24, device="cuda", generator=g).to(BF16), torch.empty(12, 24, device="cuda", dtype=BF16)
+    cg.linear(t["x"], t["w"], t["bias"], act, t["residual"], z=z)
+    want = dict(zip(("x", "w", "bias"), cg.linear_backward(dy, t["x"], t["w"], z, act)), residual=dy)
+    t[wanted].requires_grad_(True)
+    y = cg.linear(t["x"], t["w"], t["bias"], act, t["residual"])
+    x, w, z = y.grad_fn.saved_tensors
+    assert (x is not None) == (wanted == "w") and (w is not None) == (wanted == "x")
+    assert (z is not None) == (act != "none" and wanted != "residual")
+    y.backward(dy)
+    assert torch.equal(t[wanted].grad, want[wanted])
