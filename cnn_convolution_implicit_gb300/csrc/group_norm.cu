@@ -486,15 +486,6 @@ __global__ void __launch_bounds__(kJoinThreads) norm_grad_join_kernel(const Norm
 // Sums of partials first, first + STEP, ... of a channel, dgamma's and dbeta's.  Every 256 of them join
 // a total that carries its rounding along: one FP32 chain of 2^15 equal terms is off by up to
 // 1.5e-4, 256 terms by 3e-6.
-struct CarriedSum {
-    float total = 0.0f, lost = 0.0f;
-    __device__ __forceinline__ void add(float v) {
-        const float y = v - lost, t = total + y;
-        lost = (t - total) - y;
-        total = t;
-    }
-};
-
 template <int STEP>
 __device__ __forceinline__ float2 channel_sum(const float2* part, long long first, long long entries, int C) {
     constexpr int kBatch = 8;  // loads under way, of a short chain too

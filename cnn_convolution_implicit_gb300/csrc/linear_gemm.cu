@@ -37,6 +37,7 @@
 #include "linear_internal.h"
 #include "pointwise_math.cuh"
 #include "ptx.cuh"
+#include "row_sums.cuh"
 
 namespace convgb {
 
@@ -499,8 +500,7 @@ __device__ __forceinline__ void join_cluster(const Job& p, const float* part, in
 __device__ __forceinline__ void join_columns(const ColumnJoin& j, int first, int step) {
     const int lane = threadIdx.x & 31;
     for (int c = first; c < j.columns; c += step) {
-        float total = 0.0f;
-        for (int i = lane; i < j.parts; i += 32) total += j.part[static_cast<long long>(i) * j.columns + c];
+        float total = sum_of_parts(j.part, lane, j.parts, j.columns, c);
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(0xffffffffu, total, i);
         if (lane == 0) j.out[c] = total;

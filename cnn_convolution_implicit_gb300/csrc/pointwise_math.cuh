@@ -139,6 +139,16 @@ struct VecIo<float, 1> {
     static __device__ __forceinline__ float pack(const f2 (&v)[1]) { return f2_lo(v[0]); }
 };
 
+// A sum of many terms that carries its rounding along.  (What is lost next to an Inf is no number, and not carried.)
+struct CarriedSum {
+    float total = 0.0f, lost = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float y = v - lost, t = total + y;
+        lost = isinf(t) ? 0.0f : (t - total) - y;
+        total = t;
+    }
+};
+
 // ------------------------------------------------------------------ activations
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN passes through
     float r;

@@ -11,6 +11,7 @@
 // sends results, which replace their inputs there, back.  The first and last granule of a group, shared with the
 // neighbouring groups, are written by elements; what of the tensor's last granule is not the tensor's is not read.
 #include "rms_math.cuh"
+#include "row_sums.cuh"
 #include "rows_internal.h"
 
 namespace convgb {
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 2) rms_element_kernel(const RmsParam
     __syncthreads();
     const long long row_bytes = static_cast<long long>(p.C) * es;
     const int tile_bytes = (rows * p.C * es + 14 + 15) & ~15;  // of one tensor, from the granule that holds its first byte
-    const int groups = static_cast<int>((static_cast<long long>(p.M) + rows - 1) / rows);
+    const GroupRange range(static_cast<int>((static_cast<long long>(p.M) + rows - 1) / rows), kBack ? p.rounds : 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const auto run_of = [&](int g) {
         const long long m = static_cast<long long>(g) * rows;
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 2) rms_element_kernel(const RmsParam
         const int tensors = kBack ? (p.r != nullptr ? 3 : 2) : (p.r != nullptr ? 2 : 1);
         const long long last = p.M * row_bytes;
         long long issued = 0;
-        for (int g = blockIdx.x; g < groups; g += gridDim.x) {
+        for (int g = range.first; g < range.end; g += range.step) {
             if (!mbar_wait(&empty[st], ph ^ 1u, abort)) {
                 record_status(p.status, kStatusTimeoutProducer, abort);
                 break;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 2) rms_element_kernel(const RmsParam
             if (at < (lane < 16 ? head : run.end)) *reinterpret_cast<T*>(out + at) = *reinterpret_cast<const T*>(tile + (at - run.base));
             if (lane == 0 && run.outer > run.inner) bulk_store(out + run.inner, tile + (run.inner - run.base), static_cast<uint32_t>(run.outer - run.inner));
         };
-        for (int g = blockIdx.x; g < groups; g += gridDim.x) {
+        for (int g = range.first; g < range.end; g += range.step) {
             if (!__all_sync(0xffffffffu, mbar_wait(&done[st], ph, abort))) {
                 record_status(p.status, kStatusTimeoutEpilogue, abort);
                 break;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2) rms_element_kernel(const RmsParam
         return v;
     };
     const bool with_r = p.r != nullptr;
-    for (int g = blockIdx.x; g < groups; g += gridDim.x, turn ^= 1) {
+    for (int g = range.first; g < range.end; g += range.step, turn ^= 1) {
         if (!mbar_wait(&full[st], ph, abort)) record_status(p.status, kStatusTimeoutTransform, abort);  // and on: every wait ends
         const Run run = run_of(g);
 #pragma unroll 1
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) rms_element_kernel(const RmsParam
         float* part = p.part + static_cast<long long>(blockIdx.x) * p.C;
         float* warps = reinterpret_cast<float*>(ring);
         if constexpr (WARPS == 1) {  // the warps' sums, in the ring once every stage has left it
-            const int mine = static_cast<int>(blockIdx.x) < groups ? (groups - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1 : 0;
+            const int mine = range.count();
             for (int i = 0; i < s.stages; ++i) {
                 const int fills = mine / s.stages + (i < mine % s.stages ? 1 : 0);
                 if (fills && !mbar_wait(&empty[i], static_cast<uint32_t>((fills - 1) & 1), abort)) record_status(p.status, kStatusTimeoutTransform, abort);
@@ -291,7 +292,9 @@ cudaError_t launch(const RmsParams& p, cudaStream_t stream) {
     if (s.stages > kStreamMaxStages) s.stages = kStreamMaxStages;
     const long long need = (static_cast<long long>(p.M) + s.rows - 1) / s.rows;
     const long long ctas = kBack && p.dgamma != nullptr ? p.parts : (need < p.ctas ? need : p.ctas);
-    kernel<<<static_cast<unsigned>(ctas), kThreads, s.stages * s.stage_bytes, stream>>>(p, s);
+    RmsParams q = p;
+    if (p.dgamma == nullptr) q.rounds = 1;
+    kernel<<<static_cast<unsigned>(ctas), kThreads, s.stages * s.stage_bytes, stream>>>(q, s);
     return cudaGetLastError();
 }
 
@@ -318,11 +321,14 @@ cudaError_t by_mode(const RmsParams& p, bool backward, cudaStream_t stream) {
 
 bool rms_by_elements(const RmsParams& p) { return p.C % (p.bf16 ? 8 : 4) != 0 && p.C <= 8192; }
 
-int rms_element_parts(const RmsParams& p) {
-    const int rows = stream_rows(p.M, form_of(p.C).warps == 1 ? kStreamWarps : 1, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), p.ctas);
+void rms_plan_elements(RmsParams& p) {
+    const int at_once = form_of(p.C).warps == 1 ? kStreamWarps : 1;
+    const int rows = stream_rows(p.M, at_once, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), p.ctas);
     const long long need = (static_cast<long long>(p.M) + rows - 1) / rows;
-    if (need <= 4) return 1;  // as rms_plan_backward
-    return static_cast<int>(need < p.ctas ? need : p.ctas);
+    p.rounds = chain_rounds(p.M, at_once, p.ctas);
+    if (need <= 4) p.parts = 1;  // as plan_stream
+    else if (need < p.ctas) p.parts = static_cast<int>(need);
+    else p.parts = p.rounds * p.ctas;
 }
 
 cudaError_t launch_rms_elements(const RmsParams& p, bool backward, cudaStream_t stream) {

@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "rms_math.cuh"
+#include "row_sums.cuh"
 #include "rows_internal.h"
 
 namespace convgb {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
     }
     __syncthreads();
     const int row_bytes = p.C * static_cast<int>(sizeof(T));
-    const int groups = static_cast<int>((static_cast<long long>(p.M) + rows - 1) / rows);
+    const GroupRange range(static_cast<int>((static_cast<long long>(p.M) + rows - 1) / rows), p.rounds);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == kStreamWarps) {
         if (lane != 0) return;
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
         long long issued = 0;
         int st = 0;
         uint32_t ph = 0;
-        for (int g = blockIdx.x; g < groups; g += gridDim.x) {
+        for (int g = range.first; g < range.end; g += range.step) {
             if (!mbar_wait(&empty[st], ph ^ 1u, abort)) {
                 record_status(p.status, kStatusTimeoutProducer, abort);
                 break;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kStreamThreads, ITEMS == 4 ? 1 : 2) rms_backwa
     }
     int st = 0, turn = 0;
     uint32_t ph = 0;
-    for (int g = blockIdx.x; g < groups; g += gridDim.x, turn ^= 1) {
+    for (int g = range.first; g < range.end; g += range.step, turn ^= 1) {
         if (!mbar_wait(&full[st], ph, abort)) record_status(p.status, kStatusTimeoutTransform, abort);  // and on: every wait ends
 #pragma unroll 1
         for (int at = slot; at < rows; at += kAtOnce) {  // rows is a multiple, 1 where all warps share a row
@@ -608,11 +609,15 @@ int stream_rows_of(const RmsParams& p, const StreamForm& f, int num_sms) {
     return stream_rows(p.M, 32 * kStreamWarps / f.lanes, 3, static_cast<long long>(p.C) * (p.bf16 ? 2 : 4), f.ctas * num_sms);
 }
 
-int stream_ctas(const RmsParams& p, const StreamForm& f, int num_sms) {
-    const int rows = stream_rows_of(p, f, num_sms);
-    const long long need = (static_cast<long long>(p.M) + rows - 1) / rows, most = static_cast<long long>(f.ctas) * num_sms;
-    if (need <= 4) return 1;  // a turn takes a microsecond, a join of parts and its launch four
-    return static_cast<int>(need < most ? need : most);
+void plan_stream(RmsParams& p, const StreamForm& f, int num_sms) {
+    p.rows = stream_rows_of(p, f, num_sms);
+    const long long need = (static_cast<long long>(p.M) + p.rows - 1) / p.rows;
+    const int resident = f.ctas * num_sms;
+    p.rounds = chain_rounds(p.M, 32 * kStreamWarps / f.lanes, resident);
+    if (need <= 4) p.ctas = 1;  // a turn takes a microsecond, a join of parts and its launch four
+    else if (need < resident) p.ctas = static_cast<int>(need);
+    else p.ctas = p.rounds * resident;
+    p.parts = p.ctas;
 }
 
 template <typename T, int ITEMS, int LANES>
@@ -679,19 +684,19 @@ cudaError_t backward(const RmsParams& p, cudaStream_t stream) {
 void rms_plan_backward(RmsParams& p, int num_sms) {
     if (rms_by_elements(p)) {
         p.ctas = 2 * num_sms;
-        p.parts = rms_element_parts(p);
+        rms_plan_elements(p);
         return;
     }
     const StreamForm f = stream_form(p);
     if (f.lanes != 0) {
-        p.rows = stream_rows_of(p, f, num_sms);
-        p.ctas = p.parts = stream_ctas(p, f, num_sms);
+        plan_stream(p, f, num_sms);
         return;
     }
-    // dgamma by column: about four CTAs an SM
+    // dgamma by column: about four CTAs an SM, more where chains of rows would pass kChainRows (65536 x 16384 BF16 4.30 ms, 3.88 so)
     const long long columns = (p.C + 31) / 32, need = (static_cast<long long>(p.M) + 4 * kColumnRows - 1) / (4 * kColumnRows);
     const long long most = (4LL * num_sms + columns - 1) / columns;
-    p.parts = static_cast<int>(need < most ? need : most);
+    const long long chains = (static_cast<long long>(p.M) + kColumnRows * kChainRows - 1) / (kColumnRows * kChainRows);
+    p.parts = static_cast<int>(need < most ? need : (most > chains ? most : chains));
 }
 
 cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream) {

@@ -28,17 +28,18 @@ struct RmsParams {
     float* part;         // workspace: [parts][C] sums of dy * n
     int parts;           // rows of sums that the backward pass leaves there
     int ctas, rows;      // of the streaming forms: CTAs, and rows of a stage (backward)
+    int rounds;          // of the backward pass with dgamma: rounds of CTAs
     unsigned* status;
 };
 
-// Fills parts and ctas.
+// Fills parts, ctas, rows and rounds.
 void rms_plan_backward(RmsParams& p, int num_sms);
 cudaError_t launch_rms_forward(const RmsParams& p, cudaStream_t stream);
 cudaError_t launch_rms_backward(const RmsParams& p, cudaStream_t stream);
 
-// Rows off 16 bytes, up to 8,192 values (rms_elements.cu); CTAs of a backward pass with dgamma.
+// Rows off 16 bytes, up to 8,192 values (rms_elements.cu).
 bool rms_by_elements(const RmsParams& p);
-int rms_element_parts(const RmsParams& p);
+void rms_plan_elements(RmsParams& p);  // fills parts and rounds
 cudaError_t launch_rms_elements(const RmsParams& p, bool backward, cudaStream_t stream);
 
 // Sums of `parts` rows of C values each, in one order (column_sums.cu).  early: the kernel before it on the stream lets it
