@@ -21,8 +21,10 @@ inline int chain_rounds(int M, int at_once, int resident) {
 // 262144 x 4096 BF16: 959 us in one round with chains of 862 rows, 962 in two, 1041 where every round went through the whole map.)
 struct GroupRange {
     int first, end, step;
-    __device__ __forceinline__ GroupRange(int groups, int rounds) {
-        step = static_cast<int>(gridDim.x) / rounds;
+    __device__ __forceinline__ GroupRange(int groups, int rounds)
+        : first(static_cast<int>(blockIdx.x)), end(groups), step(static_cast<int>(gridDim.x)) {
+        if (rounds == 1) return;  // no divisions ahead of the first copy
+        step /= rounds;
         const int stretch = (groups + rounds - 1) / rounds, round = static_cast<int>(blockIdx.x) / step;
         first = round * stretch + static_cast<int>(blockIdx.x) - round * step;
         end = min(groups, (round + 1) * stretch);
