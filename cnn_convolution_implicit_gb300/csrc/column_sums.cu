@@ -1,9 +1,9 @@
 // column_sums.cu -- gradients of what is broadcast over the rows: the linear layer's u = dy * act'(z) with its sums
 // over the rows (dbias), and the join of such sums' parts.
 //
-// Bound by reading dy and z and writing u: 8192 x 4096 with SiLU 35 us cold, 5.7 TB/s.  A CTA takes a strip of columns of a range of rows; a thread keeps its
-// columns' sums over its rows in FP32, the threads' meet in shared memory and the ranges' in the workspace, always
-// in one order.
+// Bound by reading dy and z and writing u: 8192 x 4096 with SiLU 30 us with cold caches, 6.7 TB/s (the last of u is still in L2 when it
+// ends).  A CTA takes a strip of columns of a range of rows; a thread keeps its columns' sums over its rows in FP32, the threads' meet
+// in shared memory and the ranges' in the workspace, always in one order.
 #include <type_traits>
 
 #include "linear_internal.h"

@@ -28,7 +28,7 @@
 //
 // Measured (repeated launches in a graph): 8192 x 4096 x 4096 142 us, 1,933 TFLOP/s, the rate of the card's library product;
 // bound by the tensor cores (89 % of their cycles) and, in long streams of calls, by power.  200704 x 256 -> 512 with bias,
-// ReLU and a residual 84 us, 6.1 TB/s; bound by memory.  dx and dw of 8192 x 1024 -> 4096 85 us, 1,620 TFLOP/s.
+// ReLU and a residual 84 us, 6.1 TB/s; bound by memory.  dx and dw of 8192 x 1024 -> 4096 80 us, 1,720 TFLOP/s.
 //
 // Few tiles: the K of each is shared by `splits` units.  Of the forward product two, four or eight of them are a cluster:
 // each leaves its FP32 sums in its shared memory, and after a cluster barrier each finishes its share of the rows from

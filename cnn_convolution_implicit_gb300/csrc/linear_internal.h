@@ -1,5 +1,5 @@
 // linear_internal.h -- parameter blocks and launchers shared between the linear layer's plan code
-// (linear_api.cu) and its kernels (linear_gemm.cu, linear_few.cu, linear_grad.cu).
+// (linear_api.cu) and its kernels (linear_gemm.cu, linear_few.cu, column_sums.cu).
 #pragma once
 
 #include <cstdint>

@@ -4,7 +4,7 @@
 //   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * gamma
 //   n = h * rstd, d = dy * gamma:  dx = rstd * (d - n * mean(d * n)) + dh,  dgamma = sum over rows of dy * n
 //
-// Bound by memory: 8192 x 4096 BF16 with a residual 43 us forward (6.3 TB/s), 47 backward with dh (5.7), 40 to 8 bits
+// Bound by memory: 8192 x 4096 BF16 with a residual 43 us forward (6.2 TB/s), 48 backward with dh (5.6), 40 to 8 bits
 // (5.9).  A row stays in the registers of the 8 to 512 threads that hold it, so every byte
 // crosses the bus once; rows past what they hold are swept twice (three times to 8 bits).
 //

@@ -529,7 +529,8 @@ def dropout(x, p, state, residual=None, y=None, stream=None):
     """x / (1 - p) where the generator keeps an element, 0 where it drops one (with probability p), plus
     the residual; x BF16 or FP32 of any shape.  ``state`` is an int64 tensor of two on the GPU, seed and offset, read when
     the kernel runs: the same state gives the same mask, and a program moves the offset (or the seed)
-    on for a new one, in a captured graph too.  ``y``, the result's buffer, may be x or the residual itself.
+    on for a new one, in a captured graph too.  (Where a forward pass is run a second time for its backward pass, as
+    checkpointing does, it has to find the state of the first.)  ``y``, the result's buffer, may be x or the residual itself.
 
     Differentiable: where torch records gradients and x or residual requires one, the result has its
     backward pass (dropout_backward; once, and not with ``y`` given).  A tensor with a forward-mode

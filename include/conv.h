@@ -660,7 +660,7 @@ conv_status conv_linear_forward(conv_linear_plan *p, const void *x, const void *
 conv_status conv_linear_backward(conv_linear_plan *p, const void *dy, const void *x, const void *w, const void *z,
                                  void *dx, void *dw, float *dbias, void *workspace, void *stream);
 
-/* The kernels that the plan's calls run (host-side, as conv_plan_info; any pointer may be NULL). */
+/* The kernels that the plan's calls run (host-side).  CONV_ERR_INVALID_ARG for a NULL plan or info. */
 typedef enum {
     CONV_LINEAR_FEW_ROWS = 0,  /* w read once, BF16 MMA from registers                            */
     CONV_LINEAR_TILES = 1      /* tcgen05 tiles of rows x columns (256 x 256 on a pair of SMs), the K of each
