@@ -38,6 +38,21 @@ conv_status check_device(const conv_linear_plan* pl) {
     return cur == pl->device ? CONV_OK : CONV_ERR_INVALID_ARG;
 }
 
+// A buffer of a call, to tell whether two share memory (nullptr shares none).
+struct Span {
+    uintptr_t at;
+    size_t bytes;
+    template <typename T>
+    Span(const T* p, size_t n) : at(reinterpret_cast<uintptr_t>(p)), bytes(p == nullptr ? 0 : n) {}
+    bool meets(const Span& o) const { return bytes != 0 && o.bytes != 0 && at < o.at + o.bytes && o.at < at + bytes; }
+    bool is(const Span& o) const { return at == o.at; }
+};
+
+template <typename... S>
+bool meets_any(const Span& a, const S&... others) {
+    return (a.meets(others) || ...);
+}
+
 conv_status launched(cudaError_t e) {
     if (e == cudaSuccess) return CONV_OK;
     cudaGetLastError();
@@ -146,6 +161,9 @@ conv_status conv_linear_forward(conv_linear_plan* pl, const void* x, const void*
     if (!all_aligned16(x, w, bias, residual, y, z, workspace)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
+    const size_t M = pl->M, N = pl->N, K = pl->K;
+    const Span sx(x, 2 * M * K), sw(w, 2 * N * K), sb(bias, 4 * N), sr(residual, 2 * M * N), sy(y, 2 * M * N), sz(z, 2 * M * N);
+    if (meets_any(sy, sx, sw, sb, sz) || meets_any(sz, sx, sw, sb, sr) || (sy.meets(sr) && !sy.is(sr))) return CONV_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pl->few) {
         const FewParams f = {pl->M, pl->N, pl->K, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w), bias,
@@ -189,6 +207,10 @@ conv_status conv_linear_backward(conv_linear_plan* pl, const void* dy, const voi
     if (!all_aligned16(dy, x, w, z, dx, dw, dbias, workspace)) return CONV_ERR_MISALIGNED;
     const conv_status s = check_device(pl);
     if (s != CONV_OK) return s;
+    const size_t M = pl->M, N = pl->N, K = pl->K;
+    const Span sy(dy, 2 * M * N), sx(x, 2 * M * K), sw(w, 2 * N * K), sz(z, 2 * M * N);
+    const Span gx(dx, 2 * M * K), gw(dw, 2 * N * K), gb(dbias, 4 * N);
+    if (meets_any(gx, sy, sx, sw, sz, gw, gb) || meets_any(gw, sy, sx, sw, sz, gb) || meets_any(gb, sy, sx, sw, sz)) return CONV_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* base = static_cast<uint8_t*>(workspace);
     const bool products = dx != nullptr || dw != nullptr;

@@ -93,7 +93,7 @@ class LinearPlan(_Plan):
 
     def forward(self, x, w, bias=None, residual=None, y=None, z=None, stream=None):
         """act(x w^T + bias) + residual; ``z`` receives the values before the activation, which backward()
-        reads.  ``y`` may be the residual itself."""
+        reads.  ``y`` may be the residual itself, where that is not x too; no other buffer may be shared."""
         if stream is not None:
             with _t.cuda.stream(stream):
                 return self.forward(x, w, bias, residual, y, z)
@@ -426,7 +426,7 @@ def _function(name):
 def linear(x, w, bias=None, act="none", residual=None, y=None, z=None, stream=None):
     """act(x w^T + bias) + residual in BF16: x [..., K], w [N][K], FP32 bias [N], residual [..., N]; act
     "none", "relu" or "silu".  ``z`` receives the values before the activation, which linear_backward reads; ``y``,
-    the result's buffer, may be the residual itself.
+    the result's buffer, may be the residual itself, where that is not x too.
 
     Differentiable: where torch records gradients and x, w, bias or residual requires one, the result
     has its backward pass (once, and not with ``y`` or ``z`` given).  The plans record none.  A tensor with a

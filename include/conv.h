@@ -640,9 +640,9 @@ conv_status conv_linear_workspace(const conv_linear_plan *p, unsigned long long 
 
 /*
  * y, and z where it is given (what the backward pass of an activation reads).  bias and residual
- * may be NULL (0).  y may be the residual itself; otherwise no output overlaps an input or another output.
+ * may be NULL (0).  y may be the residual itself, where that is not x; otherwise no output overlaps an input or another output.
  * Asynchronous on `stream`; CONV_ERR_INVALID_ARG for a NULL plan, x, w or y, a NULL workspace where
- * one is needed, or another current device, CONV_ERR_MISALIGNED for a base that is not 16-byte
+ * one is needed, an output that overlaps what it may not, or another current device, CONV_ERR_MISALIGNED for a base that is not 16-byte
  * aligned, CONV_ERR_CUDA if a launch fails.
  */
 conv_status conv_linear_forward(conv_linear_plan *p, const void *x, const void *w, const float *bias,
